@@ -26,6 +26,13 @@
  *    page_table[b * max_pages_per_seq + i / P] at slot i % P (page tables are
  *    int32 [B][max_pages_per_seq], entries past a sequence unused). Queries are
  *    fp32 [B][H][d]. Query head h reads KV head h / (H / H_kv).
+ *  - 4-bit pools (TS_KV_Q4) are bytes [num_pages][H_kv][16 (d/2 + d/32)]. The
+ *    block of a (page, KV head) holds codes [d/64][16 tokens][32 bytes] (byte j:
+ *    element 2j of the 64 in the low half, 2j + 1 in the high half), then scales
+ *    bf16 [d/64][16 tokens]. A code u stands for (u - 8) * scale. A group of 64
+ *    elements is written with scale = bf16(max|x| / 7) and u = 8 + round(x /
+ *    scale), ties to even: at most half a scale from x (and from 7 scales where
+ *    the scale was rounded down). A group with a NaN or an infinity reads as NaN.
  *  - Work is enqueued on `stream` (a cudaStream_t; NULL is the legacy default
  *    stream) and returns before it runs. Argument and shape errors are
  *    reported synchronously by the return value, before anything is enqueued.
@@ -63,7 +70,7 @@ typedef enum {
   TS_ERR_SCRATCH_LIMIT = 10    /* beyond the fixed scratch of the no-alloc call */
 } ts_status;
 
-enum { TS_KV_F32 = 0, TS_KV_BF16 = 1 };
+enum { TS_KV_F32 = 0, TS_KV_BF16 = 1, TS_KV_Q4 = 2 };
 enum { TS_SELECT_TOPK = 0, TS_SELECT_TOPP = 1 };
 /* Selection function whose per-token score the top-k ranks (TokenSelect deep
  * notes, "Evolution of the selection function"; TokenSelect review, section
@@ -83,7 +90,8 @@ typedef struct {
   int head_dim;           /* d (64 or 128)                                      */
   int page_size;          /* P tokens per page: 16, or 1 for a token-granular   */
                           /* pool (one token per page; separate kernels only)   */
-  int kv_dtype;           /* TS_KV_F32 or TS_KV_BF16                            */
+  int kv_dtype;           /* TS_KV_F32, TS_KV_BF16 or TS_KV_Q4 (16-token pages, */
+                          /* d 64 or 128, at most 16 query heads per KV head)   */
   int max_batch;          /* largest B of any call                              */
   int max_pages_per_seq;  /* page-table row stride; max tokens = this * P       */
   int64_t num_pages;      /* pool size in pages; larger page ids are errors     */
@@ -107,6 +115,10 @@ typedef struct {
  * device. Returns TS_ERR_UNSUPPORTED for a head geometry with no kernel. */
 ts_status ts_create(ts_ctx** out, const ts_config* cfg);
 ts_status ts_destroy(ts_ctx* ctx);
+
+/* Bytes of one page of a K pool (or a V pool) of this shape, all KV heads; 0
+ * for a NULL cfg or an unknown kv_dtype. A pool has num_pages times as many. */
+int64_t ts_page_bytes(const ts_config* cfg);
 
 /* Selection Cache for n_layers layers of max_batch sequences: per (sequence,
  * layer) a first-query flag, C_Q (fp32 H*d) and C_T (int32, `capacity`
@@ -171,6 +183,39 @@ ts_status ts_sparse_attend(ts_ctx* ctx, const float* q, const void* k_pool, cons
                            const int32_t* count, int B, float scale, float* out, float* lse,
                            void* stream);
 
+/* Attention over the whole cache: ts_sparse_attend with every token i <
+ * seq_lens[b] attended, without an index list. 4-bit pools (TS_KV_Q4) only,
+ * else TS_ERR_UNSUPPORTED. A sequence of length 0 gives out = 0 and lse = -inf;
+ * a length outside [0, max tokens] records TS_ERR_SEQ_LEN and is taken as 0;
+ * the tokens of a page outside the pool are left out and TS_ERR_PAGE_OOB is
+ * recorded. Repeated calls give the same bits. */
+ts_status ts_attend(ts_ctx* ctx, const float* q, const void* k_pool, const void* v_pool, const int32_t* page_table,
+                    const int32_t* seq_lens, int B, float scale, float* out, float* lse, void* stream);
+
+/* Causal attention of whole prompts, packed one behind another: sequence b is
+ * rows cu_rows[b] .. cu_rows[b + 1] - 1 of every tensor (cu_rows int32 [B + 1]
+ * on the device, from 0, ascending, at most `total`; a length may be 0), and its
+ * row i attends to rows 0 .. i of the same sequence:
+ *   out[r][h] = softmax_j(scale <q[r][h], k[j][h/G]>) v[j][h/G],
+ *   lse[r][h] = log sum_j exp(scale <q[r][h], k[j][h/G]>)   (lse NULL: not wanted).
+ * q bf16 [total][H][d], k and v bf16 [total][H_kv][d], with q_stride, k_stride,
+ * v_stride elements from row to row (dense inside a row), so that the three may
+ * be column ranges of one projection: base pointers 16-byte aligned, strides
+ * multiples of 8 and at least the row. out bf16 [total][H][d] with out_stride
+ * likewise; lse fp32 [total][H]. Rows of out and lse from cu_rows[B] on are left
+ * as they are. Scores, sums and outputs accumulate in fp32; the softmax weights
+ * are rounded to bf16 for their product with v, the outputs once at the end. No
+ * cache is read or written: the context gives the head geometry (d 64 or 128,
+ * G <= 16, bf16 or 4-bit pools, else TS_ERR_UNSUPPORTED), B <= max_batch, and a
+ * prompt may be longer than its max tokens. Boundaries that are not as above
+ * record TS_ERR_SEQ_LEN: nothing is written for a sequence that descends or
+ * ends beyond `total`. A row's result depends on no later row, on no other
+ * sequence and on no row past the last one, whatever those hold (NaN and
+ * infinities too). Repeated calls give the same bits. */
+ts_status ts_prompt_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const int32_t* cu_rows, int B, int total, float scale,
+                           void* out, int64_t out_stride, float* lse, void* stream);
+
 /* Sparse attention for callers that cannot allocate device memory: the same
  * computation and the same kernel as ts_sparse_attend, but with no context.
  * The paper has no counterpart; this exists for callers that run where
@@ -185,7 +230,7 @@ ts_status ts_sparse_attend(ts_ctx* ctx, const float* q, const void* k_pool, cons
  * the array) and B * H_kv * G * (d + 2) <= 2^20 floats (one split per
  * (sequence, KV head) at that size); beyond them the call returns
  * TS_ERR_SCRATCH_LIMIT and enqueues nothing. A NaN scale returns
- * TS_ERR_INVALID_ARG, as in ts_sparse_attend. It calls no cudaMalloc/cudaFree. The first call on a
+ * TS_ERR_INVALID_ARG, as in ts_sparse_attend, and 4-bit pools TS_ERR_UNSUPPORTED. It calls no cudaMalloc/cudaFree. The first call on a
  * device looks up the array's device address (cudaGetSymbolAddress) and the
  * SM count: make that first call before any stream capture on that device.
  * Every call clears the merge counters, then uses the shared array: calls
@@ -211,7 +256,7 @@ ts_status ts_sparse_attend_noalloc(int n_q_heads, int n_kv_heads, int head_dim, 
  * same inputs give bit-identical results. params->score_fn other than the
  * head soft vote (the ablations) runs the multi-kernel path with that
  * selection function (the vote buffer then holds its scores); so does a
- * context with one-token pages. Environment switches, read once by
+ * context with one-token pages or 4-bit pools. Environment switches, read once by
  * ts_create (comparisons and tests): TOKENSELECT_MULTI_KERNEL=1 keeps the
  * multi-kernel path; TOKENSELECT_NO_TC=1 scans on CUDA cores instead of tensor
  * cores; TOKENSELECT_SCAN_CLAIM=1 lets the CTAs claim scan pages from a shared
@@ -235,9 +280,32 @@ ts_status ts_decode_step(ts_ctx* ctx, ts_cache* cache, int layer, const float* q
  * elements, 16-byte aligned) are written to pool[page][g][slot] of position
  * seq_lens[b] - 1, page = page_table[b][(seq_lens[b] - 1) / page_size]. A
  * length outside [1, max tokens] records TS_ERR_SEQ_LEN, a page outside the
- * pool TS_ERR_PAGE_OOB (nothing is written for that sequence). */
+ * pool TS_ERR_PAGE_OOB (nothing is written for that sequence). For a 4-bit pool
+ * k_new / v_new are bf16 and the rows are quantised. */
 ts_status ts_append_kv(ts_ctx* ctx, const void* k_new, const void* v_new, const int32_t* page_table,
                        const int32_t* seq_lens, int B, void* k_pool, void* v_pool, void* stream);
+
+/* Appends the K and V rows of whole prompts (or of several tokens at once) to the
+ * paged pools. Packed row r of sequence b (cu_rows[b] <= r < cu_rows[b + 1], as in
+ * ts_prompt_attend) goes to position starts[b] + r - cu_rows[b] of that sequence
+ * (starts int32 [B] on the device; NULL: 0). k / v [total][H_kv][d] in the pool's
+ * element type (bf16 for a 4-bit pool, whose rows are quantised), k_stride and
+ * v_stride elements from row to row, dense inside a row, rows 16-byte aligned. A
+ * position outside [0, max tokens), or boundaries that are not ascending from 0 to at
+ * most total, records TS_ERR_SEQ_LEN, a page outside the pool TS_ERR_PAGE_OOB; the
+ * rows concerned are not written. Rows from cu_rows[B] on are not written. Two rows
+ * for one position leave one of them or, in a 4-bit pool, a mix of them. */
+ts_status ts_append_prompt(ts_ctx* ctx, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int32_t* cu_rows, const int32_t* starts, int B, int total,
+                           const int32_t* page_table, void* k_pool, void* v_pool, void* stream);
+
+/* Reads cached rows back as values: the inverse of ts_append_prompt, with the same
+ * cu_rows, starts and errors. k_out / v_out fp32 [total][H_kv][d], dense, 16-byte
+ * aligned, hold every pool type's values exactly; rows that are not read are left as
+ * they are. */
+ts_status ts_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* starts, int B, int total,
+                     const int32_t* page_table, const void* k_pool, const void* v_pool, float* k_out,
+                     float* v_out, void* stream);
 
 /* Block-level selection, the granularity the method argues against
  * (TokenSelect review, figure 2(b): InfLLM-style methods keep or drop whole

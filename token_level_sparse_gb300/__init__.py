@@ -17,9 +17,10 @@ from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int64, c_void_
 
 __all__ = [
     "TokenSelectError", "Config", "SelectParams", "library", "library_path",
-    "TS_KV_F32", "TS_KV_BF16", "TS_SELECT_TOPK", "TS_SELECT_TOPP", "STATUS",
+    "TS_KV_F32", "TS_KV_BF16", "TS_KV_Q4", "TS_SELECT_TOPK", "TS_SELECT_TOPP", "STATUS",
     "TS_SCORE_HEAD_SOFT_VOTE", "TS_SCORE_LOGIT_SUM", "TS_SCORE_HEAD_HARD_VOTE", "ts_score_fn",
-    "ts_prefill_chunk", "ts_select_blocks", "ts_append_kv",
+    "ts_prefill_chunk", "ts_select_blocks", "ts_append_kv", "ts_append_prompt", "ts_read_kv", "ts_attend",
+    "ts_prompt_attend", "ts_page_bytes",
     "ts_create", "ts_destroy", "ts_cache_create", "ts_cache_destroy", "ts_cache_reset",
     "ts_cache_check", "ts_score", "ts_select", "ts_sparse_attend", "ts_decode_step",
     "ts_get_status", "ts_status_str", "ts_version", "ts_profile_enable", "ts_profile_read",
@@ -27,7 +28,7 @@ __all__ = [
     "ts_inject_barrier_skip", "Context", "Cache", "Profile", "PROF_FAMILIES",
 ]
 
-TS_KV_F32, TS_KV_BF16 = 0, 1
+TS_KV_F32, TS_KV_BF16, TS_KV_Q4 = 0, 1, 2
 TS_SELECT_TOPK, TS_SELECT_TOPP = 0, 1
 TS_SCORE_HEAD_SOFT_VOTE, TS_SCORE_LOGIT_SUM, TS_SCORE_HEAD_HARD_VOTE = 0, 1, 2
 STATUS = {
@@ -93,6 +94,15 @@ _SIGS = {
     "ts_prefill_chunk": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
                                  POINTER(SelectParams), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
                                  c_void_p, c_void_p]),
+    "ts_append_prompt": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int, c_int,
+                                 c_void_p, c_void_p, c_void_p, c_void_p]),
+    "ts_read_kv": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                           c_void_p, c_void_p]),
+    "ts_attend": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_float, c_void_p,
+                          c_void_p, c_void_p]),
+    "ts_prompt_attend": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int,
+                                 c_int, c_float, c_void_p, c_int64, c_void_p, c_void_p]),
+    "ts_page_bytes": (c_int64, [POINTER(Config)]),
     "ts_set_wait_limit": (c_int, [c_void_p, ctypes.c_uint64]),
     "ts_inject_barrier_skip": (c_int, [c_void_p, c_int, c_int]),
     "ts_profile_enable": (c_int, [c_void_p, c_int]),
@@ -133,6 +143,14 @@ def _p(t):
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _row_stride(t):
+    """Elements from row to row of a packed [total][heads][d] tensor, which must be dense inside a row."""
+    heads, d = t.shape[1:]
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise TokenSelectError(STATUS_CODE["TS_ERR_INVALID_ARG"], "a packed row is not dense")
+    return t.stride(0) if t.shape[0] > 1 else heads * d
 
 
 def _s(stream):
@@ -254,6 +272,33 @@ def ts_append_kv(ctx, k_new, v_new, page_table, seq_lens, B, k_pool, v_pool, str
                                   _p(v_pool), _s(stream)), "ts_append_kv")
 
 
+def ts_append_prompt(ctx, k, k_stride, v, v_stride, cu_rows, starts, B, total, page_table, k_pool, v_pool,
+                     stream=None) -> None:
+    _check(library().ts_append_prompt(ctx, _p(k), k_stride, _p(v), v_stride, _p(cu_rows), _p(starts), B, total,
+                                      _p(page_table), _p(k_pool), _p(v_pool), _s(stream)), "ts_append_prompt")
+
+
+def ts_read_kv(ctx, cu_rows, starts, B, total, page_table, k_pool, v_pool, k_out, v_out, stream=None) -> None:
+    _check(library().ts_read_kv(ctx, _p(cu_rows), _p(starts), B, total, _p(page_table), _p(k_pool), _p(v_pool),
+                                _p(k_out), _p(v_out), _s(stream)), "ts_read_kv")
+
+
+def ts_attend(ctx, q, k_pool, v_pool, page_table, seq_lens, B, scale, out, lse=None, stream=None) -> None:
+    _check(library().ts_attend(ctx, _p(q), _p(k_pool), _p(v_pool), _p(page_table), _p(seq_lens), B, scale, _p(out),
+                               _p(lse), _s(stream)), "ts_attend")
+
+
+def ts_prompt_attend(ctx, q, q_stride, k, k_stride, v, v_stride, cu_rows, B, total, scale, out, out_stride, lse=None,
+                     stream=None) -> None:
+    _check(library().ts_prompt_attend(ctx, _p(q), q_stride, _p(k), k_stride, _p(v), v_stride, _p(cu_rows), B, total,
+                                      scale, _p(out), out_stride, _p(lse), _s(stream)), "ts_prompt_attend")
+
+
+def ts_page_bytes(cfg: Config) -> int:
+    """Bytes of one page of a K pool (or a V pool), all KV heads."""
+    return library().ts_page_bytes(ctypes.byref(cfg))
+
+
 def ts_set_wait_limit(ctx, ns: int) -> None:
     _check(library().ts_set_wait_limit(ctx, int(ns)), "ts_set_wait_limit")
 
@@ -343,6 +388,25 @@ class Context:
     def append_kv(self, k_new, v_new, page_table, seq_lens, k_pool, v_pool, stream=None):
         """k_new / v_new [B][H_kv][d]: the current token's rows into position seq_lens[b] - 1."""
         ts_append_kv(self.handle, k_new, v_new, page_table, seq_lens, seq_lens.shape[0], k_pool, v_pool, stream)
+
+    def append_prompt(self, k, v, cu_rows, page_table, k_pool, v_pool, starts=None, stream=None):
+        """k / v [total][H_kv][d], packed: row r of sequence b to position starts[b] + r - cu_rows[b]."""
+        ts_append_prompt(self.handle, k, _row_stride(k), v, _row_stride(v), cu_rows, starts, cu_rows.shape[0] - 1,
+                         k.shape[0], page_table, k_pool, v_pool, stream)
+
+    def read_kv(self, cu_rows, page_table, k_pool, v_pool, k_out, v_out, starts=None, stream=None):
+        """k_out / v_out fp32 [total][H_kv][d]: the values of the rows that append_prompt would write."""
+        ts_read_kv(self.handle, cu_rows, starts, cu_rows.shape[0] - 1, k_out.shape[0], page_table, k_pool, v_pool,
+                   k_out, v_out, stream)
+
+    def attend(self, q, k_pool, v_pool, page_table, seq_lens, out, lse=None, scale=0.0, stream=None):
+        """q [B][H][d] attends to every cached token of its sequence (4-bit pools)."""
+        ts_attend(self.handle, q, k_pool, v_pool, page_table, seq_lens, q.shape[0], scale, out, lse, stream)
+
+    def prompt_attend(self, q, k, v, cu_rows, out, lse=None, scale=0.0, stream=None):
+        """q / out [total][H][d], k / v [total][H_kv][d] (bf16, packed): causal attention of every sequence."""
+        ts_prompt_attend(self.handle, q, _row_stride(q), k, _row_stride(k), v, _row_stride(v), cu_rows,
+                         cu_rows.shape[0] - 1, q.shape[0], scale, out, _row_stride(out), lse, stream)
 
     def select_blocks(self, vote, seq_lens, block, budget, idx, count, stream=None):
         ts_select_blocks(self.handle, vote, vote.stride(0), seq_lens, seq_lens.shape[0], block, budget, idx,

@@ -42,6 +42,8 @@ void free_ctx_buffers(ts_ctx* c) {
   cudaFree(c->blk_len);
   cudaFree(c->blk_idx);
   cudaFree(c->sel_rows);
+  cudaFree(c->q4_part_o);
+  cudaFree(c->q4_part_ml);
   cudaFree(c->step_partials);
   cudaFree(c->step_hist);
   cudaFree(c->step_mass);
@@ -71,6 +73,9 @@ bool valid_params(const ts_select_params* p) {
   if (p->score_fn != TS_SCORE_HEAD_SOFT_VOTE && p->mode != TS_SELECT_TOPK) return false;
   return true;
 }
+
+constexpr int kMaxRows = 1 << 30;                     // rows of one packed call
+constexpr int64_t kMaxRowStride = (int64_t)1 << 31;   // elements from one packed row to the next
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
@@ -103,7 +108,7 @@ ts_status ts_create(ts_ctx** out, const ts_config* cfg) {
   const ts_config& c = *cfg;
   if (c.n_q_heads < 1 || c.n_kv_heads < 1 || c.n_q_heads % c.n_kv_heads != 0) return TS_ERR_INVALID_ARG;
   if (c.max_batch < 1 || c.max_pages_per_seq < 1 || c.num_pages < 1 || c.head_dim < 1) return TS_ERR_INVALID_ARG;
-  if (c.kv_dtype != TS_KV_F32 && c.kv_dtype != TS_KV_BF16) return TS_ERR_INVALID_ARG;
+  if (c.kv_dtype != TS_KV_F32 && c.kv_dtype != TS_KV_BF16 && c.kv_dtype != TS_KV_Q4) return TS_ERR_INVALID_ARG;
   if (c.page_size != kPage && c.page_size != 1) return TS_ERR_UNSUPPORTED;
   if (c.n_kv_heads > kCounterSlots - 2 || c.n_q_heads > 256) return TS_ERR_UNSUPPORTED;
   if ((int64_t)c.max_pages_per_seq * c.page_size > (int64_t)1 << 30) return TS_ERR_SHAPE;
@@ -184,6 +189,11 @@ ts_status ts_create(ts_ctx** out, const ts_config* cfg) {
   chk(alloc(&ctx->blk_len, B));
   chk(alloc(&ctx->blk_idx, B * T + B));
   chk(alloc(&ctx->sel_rows, NS * kStepFlagCap));
+  if (c.kv_dtype == TS_KV_Q4) {
+    const size_t slots = (size_t)q4_part_slots(c, ctx->num_sms);
+    chk(alloc(&ctx->q4_part_o, slots * H * D));
+    chk(alloc(&ctx->q4_part_ml, slots * H));
+  }
   if (e == cudaSuccess) chk(cudaMemset(ctx->status, 0, sizeof(int)));
   if (e == cudaSuccess) chk(cudaMemset(ctx->counters, 0, B * kCounterSlots * sizeof(unsigned)));
   if (e == cudaSuccess) chk(cudaMemset(ctx->hist, 0, B * 2048 * sizeof(unsigned)));
@@ -206,6 +216,17 @@ ts_status ts_destroy(ts_ctx* ctx) {
   free_ctx_buffers(ctx);
   delete ctx;
   return TS_OK;
+}
+
+int64_t ts_page_bytes(const ts_config* c) {
+  if (!c) return 0;
+  const int64_t rows = (int64_t)c->n_kv_heads * c->page_size, d = c->head_dim;
+  switch (c->kv_dtype) {
+    case TS_KV_F32: return rows * d * 4;
+    case TS_KV_BF16: return rows * d * 2;
+    case TS_KV_Q4: return rows * (d / 2 + d / 32);
+  }
+  return 0;
 }
 
 ts_status ts_cache_create(ts_ctx* ctx, ts_cache** out, int n_layers, int capacity) {
@@ -453,6 +474,63 @@ ts_status ts_append_kv(ts_ctx* ctx, const void* k_new, const void* v_new, const 
   for (const void* p : {k_new, v_new, static_cast<const void*>(k_pool), static_cast<const void*>(v_pool)})
     if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return TS_ERR_INVALID_ARG;
   return launch_append_kv(ctx, k_new, v_new, page_table, seq_lens, B, k_pool, v_pool, as_stream(stream));
+}
+
+ts_status ts_append_prompt(ts_ctx* ctx, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int32_t* cu_rows, const int32_t* starts, int B, int total,
+                           const int32_t* page_table, void* k_pool, void* v_pool, void* stream) {
+  if (!ctx || !k || !v || !cu_rows || !page_table || !k_pool || !v_pool) return TS_ERR_INVALID_ARG;
+  const ts_config& c = ctx->cfg;
+  const int64_t row = (int64_t)c.n_kv_heads * c.head_dim, per16 = c.kv_dtype == TS_KV_F32 ? 4 : 8;
+  if (B < 1 || B > c.max_batch || total < 0 || total > kMaxRows) return TS_ERR_SHAPE;
+  if (k_stride < row || v_stride < row || k_stride > kMaxRowStride || v_stride > kMaxRowStride) return TS_ERR_SHAPE;
+  if (k_stride % per16 != 0 || v_stride % per16 != 0) return TS_ERR_INVALID_ARG;
+  for (const void* p : {k, v, static_cast<const void*>(k_pool), static_cast<const void*>(v_pool)})
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return TS_ERR_INVALID_ARG;
+  AppendPromptCall a{k, k_stride, v, v_stride, cu_rows, starts, B, total, page_table, k_pool, v_pool};
+  return launch_append_prompt(ctx, a, as_stream(stream));
+}
+
+ts_status ts_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* starts, int B, int total,
+                     const int32_t* page_table, const void* k_pool, const void* v_pool, float* k_out, float* v_out,
+                     void* stream) {
+  if (!ctx || !cu_rows || !page_table || !k_pool || !v_pool || !k_out || !v_out) return TS_ERR_INVALID_ARG;
+  if (B < 1 || B > ctx->cfg.max_batch || total < 0 || total > kMaxRows) return TS_ERR_SHAPE;
+  for (const void* p : {k_pool, v_pool, static_cast<const void*>(k_out), static_cast<const void*>(v_out)})
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return TS_ERR_INVALID_ARG;
+  return launch_read_kv(ctx, cu_rows, starts, B, total, page_table, k_pool, v_pool, k_out, v_out, as_stream(stream));
+}
+
+ts_status ts_attend(ts_ctx* ctx, const float* q, const void* k_pool, const void* v_pool, const int32_t* page_table,
+                    const int32_t* seq_lens, int B, float scale, float* out, float* lse, void* stream) {
+  if (!ctx || !q || !k_pool || !v_pool || !page_table || !seq_lens || !out) return TS_ERR_INVALID_ARG;
+  if (B < 1 || B > ctx->cfg.max_batch) return TS_ERR_SHAPE;
+  if (std::isnan(scale)) return TS_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(k_pool) % 16 != 0 || reinterpret_cast<uintptr_t>(v_pool) % 16 != 0)
+    return TS_ERR_INVALID_ARG;
+  if (ctx->cfg.kv_dtype != TS_KV_Q4) return TS_ERR_UNSUPPORTED;
+  AttendCall c{q, k_pool, v_pool, page_table, nullptr, 0, nullptr, B, resolve_scale(ctx, scale), out, lse};
+  return launch_attend_q4(ctx, c, seq_lens, as_stream(stream));
+}
+
+ts_status ts_prompt_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const int32_t* cu_rows, int B, int total, float scale,
+                           void* out, int64_t out_stride, float* lse, void* stream) {
+  if (!ctx || !q || !k || !v || !cu_rows || !out) return TS_ERR_INVALID_ARG;
+  const ts_config& c = ctx->cfg;
+  const int64_t qrow = (int64_t)c.n_q_heads * c.head_dim, krow = (int64_t)c.n_kv_heads * c.head_dim;
+  if (B < 1 || B > c.max_batch || total < 0 || total > kMaxRows) return TS_ERR_SHAPE;
+  if (q_stride < qrow || out_stride < qrow || k_stride < krow || v_stride < krow) return TS_ERR_SHAPE;
+  for (int64_t st : {q_stride, k_stride, v_stride, out_stride}) {
+    if (st > kMaxRowStride) return TS_ERR_SHAPE;
+    if (st % 8 != 0) return TS_ERR_INVALID_ARG;
+  }
+  for (const void* p : {q, k, v, static_cast<const void*>(out)})
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return TS_ERR_INVALID_ARG;
+  if (std::isnan(scale)) return TS_ERR_INVALID_ARG;
+  if (!prompt_supported(c)) return TS_ERR_UNSUPPORTED;
+  PromptCall a{q, q_stride, k, k_stride, v, v_stride, cu_rows, B, total, resolve_scale(ctx, scale), out, out_stride, lse};
+  return launch_prompt_attend(ctx, a, as_stream(stream));
 }
 
 ts_status ts_select_blocks(ts_ctx* ctx, const float* vote, int64_t vote_stride, const int32_t* seq_lens, int B,

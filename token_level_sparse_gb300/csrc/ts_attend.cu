@@ -283,6 +283,7 @@ ts_status run_attend(ts_ctx* ctx, const AttendCall& c, cudaStream_t s) {
 
 ts_status launch_attend(ts_ctx* ctx, const AttendCall& a, cudaStream_t s) {
   const ts_config& c = ctx->cfg;
+  if (c.kv_dtype == TS_KV_Q4) return launch_attend_q4(ctx, a, nullptr, s);
   const int G = c.n_q_heads / c.n_kv_heads;
 #define X(DT, T, D_, G_) \
   if (c.kv_dtype == DT && c.head_dim == D_ && G == G_) return run_attend<T, D_, G_>(ctx, a, s);
@@ -337,6 +338,7 @@ __global__ void append_kv_kernel(const unsigned char* k_new, const unsigned char
 ts_status launch_append_kv(ts_ctx* ctx, const void* k_new, const void* v_new, const int32_t* page_table,
                            const int32_t* seq_lens, int B, void* k_pool, void* v_pool, cudaStream_t s) {
   const ts_config& c = ctx->cfg;
+  if (c.kv_dtype == TS_KV_Q4) return launch_append_q4(ctx, k_new, v_new, page_table, seq_lens, B, k_pool, v_pool, s);
   const int row_bytes = c.head_dim * (c.kv_dtype == TS_KV_BF16 ? 2 : 4);
   ctx->kernels += 1;
   append_kv_kernel<<<B, 128, 0, s>>>(static_cast<const unsigned char*>(k_new), static_cast<const unsigned char*>(v_new),
@@ -424,6 +426,7 @@ extern "C" ts_status ts_sparse_attend_noalloc(int n_q_heads, int n_kv_heads, int
   if (n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0 || num_pages < 1 ||
       max_pages_per_seq < 1 || idx_stride < 1 || B < 1)
     return TS_ERR_INVALID_ARG;
+  if (kv_dtype == TS_KV_Q4) return TS_ERR_UNSUPPORTED;   // its parts need the context's scratch
   if (kv_dtype != TS_KV_F32 && kv_dtype != TS_KV_BF16) return TS_ERR_INVALID_ARG;
   if (std::isnan(scale)) return TS_ERR_INVALID_ARG;   // the same argument check as ts_sparse_attend
   if (reinterpret_cast<uintptr_t>(k_pool) % 16 != 0 || reinterpret_cast<uintptr_t>(v_pool) % 16 != 0)

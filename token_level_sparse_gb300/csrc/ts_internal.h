@@ -69,6 +69,8 @@ struct ts_ctx {
   int32_t* blk_len = nullptr;            // [max_batch] block counts (block-level selection)
   int32_t* blk_idx = nullptr;            // [max_batch][max_tokens] selected blocks, then [max_batch] counts
   int32_t* sel_rows = nullptr;           // persistent kernel: per CTA, its selected tokens [kStepFlagCap]
+  float* q4_part_o = nullptr;            // 4-bit pools: attention parts [slots][H][d], q4_part_slots
+  float2* q4_part_ml = nullptr;          // ... and their (max, sum), also the score's [slots][H]
   int64_t kernels = 0;           // kernel launches issued
   // persistent decode-step kernel
   int step_grid = 0;                     // CTAs of the cooperative launch (0: not yet sized)
@@ -209,6 +211,34 @@ struct ChunkAttendCall {   // causal attention of a prefill chunk's c queries ov
   float* lse;              // [B][c][H] or null
 };
 
+struct AppendPromptCall {  // packed rows of whole prompts into the pools
+  const void* k;
+  int64_t k_stride;        // elements
+  const void* v;
+  int64_t v_stride;
+  const int32_t* cu_rows;
+  const int32_t* starts;   // or null (0)
+  int B, total;
+  const int32_t* page_table;
+  void* k_pool;
+  void* v_pool;
+};
+
+struct PromptCall {        // causal attention of packed prompts
+  const void* q;
+  int64_t q_stride;        // elements, as the others
+  const void* k;
+  int64_t k_stride;
+  const void* v;
+  int64_t v_stride;
+  const int32_t* cu_rows;
+  int B, total;
+  float scale;
+  void* out;
+  int64_t out_stride;
+  float* lse;
+};
+
 // Head geometries with a compiled kernel: (kv type flag, element type, d, H_kv, G).
 #define TS_STEP_GEOMETRIES(X)             \
   X(TS_KV_F32, float, 64, 4, 1)           \
@@ -229,6 +259,20 @@ ts_status launch_attend(ts_ctx* ctx, const AttendCall& a, cudaStream_t s);
 bool chunk_attend_supported(const ts_config& c);
 ts_status launch_append_kv(ts_ctx* ctx, const void* k_new, const void* v_new, const int32_t* page_table,
                            const int32_t* seq_lens, int B, void* k_pool, void* v_pool, cudaStream_t s);
+bool q4_supported(const ts_config& c);
+int64_t q4_part_slots(const ts_config& c, int num_sms);
+int q4_gather_splits(const ts_config& c, int num_sms, int B);
+// the whole cache (c.idx == null, seq_lens) or the listed tokens of 4-bit pools
+ts_status launch_attend_q4(ts_ctx* ctx, const AttendCall& c, const int32_t* seq_lens, cudaStream_t s);
+ts_status launch_score_q4(ts_ctx* ctx, const ScoreCall& c, cudaStream_t s);   // logits and stats
+ts_status launch_append_q4(ts_ctx* ctx, const void* k_new, const void* v_new, const int32_t* page_table,
+                           const int32_t* seq_lens, int B, void* k_pool, void* v_pool, cudaStream_t s);
+ts_status launch_append_prompt(ts_ctx* ctx, const AppendPromptCall& c, cudaStream_t s);
+ts_status launch_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* starts, int B, int total,
+                         const int32_t* page_table, const void* k_pool, const void* v_pool, float* k_out,
+                         float* v_out, cudaStream_t s);
+bool prompt_supported(const ts_config& c);
+ts_status launch_prompt_attend(ts_ctx* ctx, const PromptCall& c, cudaStream_t s);
 ts_status launch_select_blocks(ts_ctx* ctx, const float* vote, int64_t vote_stride, const int32_t* seq_lens, int B,
                                int block, int budget, int32_t* idx, int64_t idx_stride, int32_t* count,
                                cudaStream_t s);

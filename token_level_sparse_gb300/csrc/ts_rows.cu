@@ -1,0 +1,260 @@
+// Rows into and out of the paged pools: packed K and V rows of whole prompts (ts_append_prompt),
+// one token per sequence into a 4-bit pool (ts_append_kv), and rows read back as fp32 values
+// (ts_read_kv).
+//
+// Packed row r belongs to sequence b with cu[b] <= r < cu[b + 1] and goes to position
+// starts[b] + r - cu[b]. A CTA takes a few neighbouring rows: it looks up their page and slot once,
+// then its threads move 16 bytes (or, into and out of 4-bit blocks, 8 elements) each. Every byte is
+// read and written once, so the copies are bound by memory; eight lanes share one 4-bit group
+// of 64 elements, whose 32 code bytes of neighbouring tokens are contiguous in the block.
+#include "ts_q4.cuh"
+
+namespace ts {
+namespace {
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsPerCta = 16;
+
+struct RowsArgs {
+  const int32_t* cu;           // [B + 1]; null: one row per sequence, at position seq_lens[b] - 1
+  const int32_t* starts;       // [B] or null (0)
+  const int32_t* seq_lens;     // with cu == null
+  int B, total, rows_per_cta;
+  const int32_t* page_table;
+  int pt_stride, page_shift;
+  int64_t num_pages;
+  int max_tokens;
+  int HKV, D;
+  const unsigned char* src[2]; // K and V rows, bytes
+  int64_t src_stride[2];       // bytes between rows
+  unsigned char* pool[2];
+  float* dst[2];               // ts_read_kv: [total][H_kv][d]
+  int* status;
+};
+
+// Place of the CTA's rows: page * page size + slot, or -1 (no such position; recorded).
+__device__ __forceinline__ void place_rows(const RowsArgs& a, int64_t* place) {
+  if (a.cu && blockIdx.x == 0) {
+    // the boundaries: ascending, from 0, within the rows that there are
+    for (int b = threadIdx.x; b <= a.B; b += blockDim.x) {
+      const int v = a.cu[b];
+      if (v > a.total || (b == 0 ? v != 0 : v < a.cu[b - 1])) set_error(a.status, TS_ERR_SEQ_LEN);
+    }
+  }
+  if ((int)threadIdx.x < a.rows_per_cta) {
+    const int64_t r = (int64_t)blockIdx.x * a.rows_per_cta + threadIdx.x;
+    int64_t at = -1;
+    if (r < a.total) {
+      int b = (int)r;
+      int64_t pos = -1;
+      bool inside = true;
+      if (a.cu) {
+        int lo = 0, hi = a.B;              // the last b with cu[b] <= r
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (a.cu[mid] <= r) lo = mid; else hi = mid;
+        }
+        b = lo;
+        inside = r >= a.cu[b] && r < a.cu[b + 1];   // rows behind the last sequence stay as they are
+        pos = (a.starts ? a.starts[b] : 0) + (r - a.cu[b]);
+        if (a.starts && a.starts[b] < 0) pos = -1;
+      } else {
+        pos = (int64_t)a.seq_lens[b] - 1;
+      }
+      if (inside) {
+        if (pos < 0 || pos >= a.max_tokens) {
+          set_error(a.status, TS_ERR_SEQ_LEN);
+        } else {
+          const int page = a.page_table[(size_t)b * a.pt_stride + (pos >> a.page_shift)];
+          if (page < 0 || (int64_t)page >= a.num_pages)
+            set_error(a.status, TS_ERR_PAGE_OOB);
+          else
+            at = ((int64_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+        }
+      }
+    }
+    place[threadIdx.x] = at;
+  }
+  __syncthreads();
+}
+
+// bf16 and fp32 pools: rows copied as they are, 16 bytes per thread.
+__global__ void __launch_bounds__(kRowsThreads) append_rows_kernel(const __grid_constant__ RowsArgs a, int row_bytes) {
+  __shared__ int64_t place[kRowsPerCta];
+  place_rows(a, place);
+  const int cpr = row_bytes / 16, per_row = 2 * a.HKV * cpr;
+  const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
+  const int ps = 1 << a.page_shift;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < per_row * a.rows_per_cta; i += kRowsThreads) {
+    const int row = i / per_row, rem = i % per_row, isv = rem >= a.HKV * cpr;
+    const int c = rem - isv * a.HKV * cpr, g = c / cpr, ch = c % cpr;
+    const int64_t at = place[row];
+    if (at < 0) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(a.src[isv] + (r0 + row) * a.src_stride[isv] + (size_t)c * 16);
+    const int64_t page = at >> a.page_shift, slot = at & (ps - 1);
+    *reinterpret_cast<uint4*>(a.pool[isv] + ((page * a.HKV + g) * ps + slot) * row_bytes + ch * 16) = v;
+  }
+}
+
+// 4-bit pools. Eight lanes quantise one group of 64 elements: scale = bf16(max|x| / 7), code =
+// 8 + round(x / scale) with ties to even (both divisions correctly rounded, so that every
+// implementation of the formula gives the same bits). A scale of zero gives zeros; a group with a
+// NaN or an infinity reads back as NaN: its scale is not finite and its codes stand for zero.
+__global__ void __launch_bounds__(kRowsThreads) append_q4_kernel(const __grid_constant__ RowsArgs a) {
+  __shared__ int64_t place[kRowsPerCta];
+  place_rows(a, place);
+  const int NB = a.D / 64, groups = 2 * a.HKV * NB, blk = q4_block_bytes(a.D), codes = q4_code_bytes(a.D);
+  const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
+  const int lane8 = threadIdx.x & 7;
+  // neighbouring groups of eight lanes take neighbouring rows of the same 64 elements: their codes
+  // are neighbours in the block
+#pragma unroll 2
+  for (int i = threadIdx.x >> 3; i < groups * a.rows_per_cta; i += kRowsThreads / 8) {
+    const int row = i % a.rows_per_cta, gi = i / a.rows_per_cta, isv = gi >= a.HKV * NB;
+    const int c = gi - isv * a.HKV * NB, g = c / NB, nb = c % NB;
+    const int64_t at = place[row];
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (at >= 0)
+      v = *reinterpret_cast<const uint4*>(a.src[isv] + (r0 + row) * a.src_stride[isv] + ((size_t)c * 64 + lane8 * 8) * 2);
+    float x[8];
+    KV<__nv_bfloat16>::unpack(v, x);
+    // the largest magnitude by its bits: ordered like the values, with infinities and NaN on top
+    uint32_t mb = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mb = max(mb, __float_as_uint(x[e]) & 0x7fffffffu);
+    const unsigned peers = 0xffu << (threadIdx.x & 24);
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1) mb = max(mb, __shfl_xor_sync(peers, mb, d));
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(mb), 7.f));
+    const float s = __bfloat162float(sb);
+    const bool live = s > 0.f && s < INFINITY;
+    uint32_t w = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int q = live ? max(-7, min(7, __float2int_rn(__fdiv_rn(x[e], s)))) : 0;
+      w |= (uint32_t)(q + 8) << (4 * e);
+    }
+    if (at >= 0) {
+      unsigned char* base = a.pool[isv] + ((at >> 4) * a.HKV + g) * blk;
+      const int slot = (int)(at & 15);
+      *reinterpret_cast<uint32_t*>(base + nb * 512 + slot * 32 + lane8 * 4) = w;
+      if (lane8 == 0) *reinterpret_cast<__nv_bfloat16*>(base + codes + nb * 32 + slot * 2) = sb;
+    }
+  }
+}
+
+// Rows of a pool as fp32 values: exact for every pool type (a code times a bf16 scale has 12
+// significant bits).
+template <int kType>
+__global__ void __launch_bounds__(kRowsThreads) read_rows_kernel(const __grid_constant__ RowsArgs a) {
+  __shared__ int64_t place[kRowsPerCta];
+  place_rows(a, place);
+  const int c8 = a.HKV * a.D / 8, per_row = 2 * c8, ps = 1 << a.page_shift;   // threads of a row: 8 elements each
+  const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < per_row * a.rows_per_cta; i += kRowsThreads) {
+    const int row = i / per_row, rem = i % per_row, isv = rem >= c8;
+    const int c = rem - isv * c8, g = c / (a.D / 8), e0 = c % (a.D / 8) * 8;
+    const int64_t at = place[row];
+    if (at < 0) continue;
+    const int64_t page = at >> a.page_shift, slot = at & (ps - 1);
+    float x[8];
+    if constexpr (kType == TS_KV_Q4) {
+      const unsigned char* base = a.pool[isv] + (page * a.HKV + g) * q4_block_bytes(a.D);
+      const int nb = e0 / 64;
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(base + nb * 512 + slot * 32 + (e0 % 64) / 2);
+      const float s = bf16_bits_f(*reinterpret_cast<const uint16_t*>(base + q4_code_bytes(a.D) + nb * 32 + slot * 2));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w >> (4 * e)) & 15u) - 8) * s;
+    } else {
+      constexpr int ES = kType == TS_KV_BF16 ? 2 : 4;
+      const uint4* src = reinterpret_cast<const uint4*>(a.pool[isv] + (((page * a.HKV + g) * ps + slot) * a.D + e0) * ES);
+      if constexpr (kType == TS_KV_BF16) {
+        KV<__nv_bfloat16>::unpack(src[0], x);
+      } else {
+        KV<float>::unpack(src[0], x);
+        KV<float>::unpack(src[1], x + 4);
+      }
+    }
+    float4* dst = reinterpret_cast<float4*>(a.dst[isv] + (r0 + row) * a.HKV * a.D + (size_t)c * 8);
+    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+RowsArgs base_args(ts_ctx* ctx, int B, int total, const int32_t* page_table, void* k_pool, void* v_pool) {
+  const ts_config& c = ctx->cfg;
+  RowsArgs a{};
+  a.B = B;
+  a.total = total;
+  // few rows: one per CTA, so that a decode step's rows do not queue behind one another
+  a.rows_per_cta = total >= kRowsPerCta * ctx->num_sms ? kRowsPerCta : (total >= 2 * ctx->num_sms ? 4 : 1);
+  a.page_table = page_table;
+  a.pt_stride = c.max_pages_per_seq;
+  a.page_shift = ctx->page_shift;
+  a.num_pages = c.num_pages;
+  a.max_tokens = ctx->max_tokens;
+  a.HKV = c.n_kv_heads;
+  a.D = c.head_dim;
+  a.pool[0] = static_cast<unsigned char*>(k_pool);
+  a.pool[1] = static_cast<unsigned char*>(v_pool);
+  a.status = ctx->status;
+  return a;
+}
+
+ts_status run_append(ts_ctx* ctx, const RowsArgs& a, cudaStream_t s) {
+  const int grid = (a.total + a.rows_per_cta - 1) / a.rows_per_cta;
+  ctx->kernels += 1;
+  if (ctx->cfg.kv_dtype == TS_KV_Q4)
+    append_q4_kernel<<<grid, kRowsThreads, 0, s>>>(a);
+  else
+    append_rows_kernel<<<grid, kRowsThreads, 0, s>>>(a, a.D * (ctx->cfg.kv_dtype == TS_KV_BF16 ? 2 : 4));
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+ts_status launch_append_q4(ts_ctx* ctx, const void* k_new, const void* v_new, const int32_t* page_table,
+                           const int32_t* seq_lens, int B, void* k_pool, void* v_pool, cudaStream_t s) {
+  RowsArgs a = base_args(ctx, B, B, page_table, k_pool, v_pool);
+  a.seq_lens = seq_lens;
+  a.src[0] = static_cast<const unsigned char*>(k_new);
+  a.src[1] = static_cast<const unsigned char*>(v_new);
+  a.src_stride[0] = a.src_stride[1] = (int64_t)a.HKV * a.D * 2;
+  return run_append(ctx, a, s);
+}
+
+ts_status launch_append_prompt(ts_ctx* ctx, const AppendPromptCall& c, cudaStream_t s) {
+  if (c.total == 0) return TS_OK;
+  RowsArgs a = base_args(ctx, c.B, c.total, c.page_table, c.k_pool, c.v_pool);
+  const int64_t es = ctx->cfg.kv_dtype == TS_KV_F32 ? 4 : 2;
+  a.cu = c.cu_rows;
+  a.starts = c.starts;
+  a.src[0] = static_cast<const unsigned char*>(c.k);
+  a.src[1] = static_cast<const unsigned char*>(c.v);
+  a.src_stride[0] = c.k_stride * es;
+  a.src_stride[1] = c.v_stride * es;
+  return run_append(ctx, a, s);
+}
+
+ts_status launch_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* starts, int B, int total,
+                         const int32_t* page_table, const void* k_pool, const void* v_pool, float* k_out, float* v_out,
+                         cudaStream_t s) {
+  if (total == 0) return TS_OK;
+  RowsArgs a = base_args(ctx, B, total, page_table, const_cast<void*>(k_pool), const_cast<void*>(v_pool));
+  a.cu = cu_rows;
+  a.starts = starts;
+  a.dst[0] = k_out;
+  a.dst[1] = v_out;
+  const int grid = (total + a.rows_per_cta - 1) / a.rows_per_cta;
+  ctx->kernels += 1;
+  switch (ctx->cfg.kv_dtype) {
+    case TS_KV_Q4: read_rows_kernel<TS_KV_Q4><<<grid, kRowsThreads, 0, s>>>(a); break;
+    case TS_KV_BF16: read_rows_kernel<TS_KV_BF16><<<grid, kRowsThreads, 0, s>>>(a); break;
+    default: read_rows_kernel<TS_KV_F32><<<grid, kRowsThreads, 0, s>>>(a); break;
+  }
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace ts

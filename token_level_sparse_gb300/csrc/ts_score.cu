@@ -422,6 +422,24 @@ __global__ void __launch_bounds__(kHardThreads) hard_vote_kernel(HardVoteKArgs a
   }
 }
 
+// The votes (or the ablations' scores) from the logits and the heads' statistics.
+ts_status run_votes(ts_ctx* ctx, const ScoreCall& c, cudaStream_t s) {
+  const int H = ctx->cfg.n_q_heads;
+  ctx->kernels += 1;
+  VoteKArgs v{c.seq_lens, c.skip, H, ctx->logits, ctx->max_tokens, ctx->stats, c.vote, c.vote_stride, c.fn};
+  {
+    ProfScope ps(ctx, TS_PROF_VOTE, s);
+    score_vote_kernel<<<dim3((ctx->max_tokens + kVoteTile - 1) / kVoteTile, c.B), kVoteThreads, 0, s>>>(v);
+    if (c.fn == TS_SCORE_HEAD_HARD_VOTE) {
+      HardVoteKArgs hv{c.seq_lens, c.skip, H, ctx->logits, ctx->max_tokens, c.k, c.n_sink, c.n_local,
+                       c.vote, c.vote_stride};
+      hard_vote_kernel<<<dim3(H, c.B), kHardThreads, 0, s>>>(hv);
+      ctx->kernels += 1;
+    }
+  }
+  return cuda_status(cudaGetLastError());
+}
+
 template <typename KT, int D, int HKV, int G>
 ts_status run_score(ts_ctx* ctx, const ScoreCall& c, cudaStream_t s) {
   using S = ScoreShape<KT, D, HKV, G>;
@@ -452,19 +470,8 @@ ts_status run_score(ts_ctx* ctx, const ScoreCall& c, cudaStream_t s) {
     ProfScope ps(ctx, TS_PROF_SCORE, s);
     kern<<<dim3(ctx->score_max_chunks, c.B), S::THREADS, smem, s>>>(a);
   }
-  ctx->kernels += 2;
-  VoteKArgs v{c.seq_lens, c.skip, H, ctx->logits, ctx->max_tokens, ctx->stats, c.vote, c.vote_stride, c.fn};
-  {
-    ProfScope ps(ctx, TS_PROF_VOTE, s);
-    score_vote_kernel<<<dim3((ctx->max_tokens + kVoteTile - 1) / kVoteTile, c.B), kVoteThreads, 0, s>>>(v);
-    if (c.fn == TS_SCORE_HEAD_HARD_VOTE) {
-      HardVoteKArgs hv{c.seq_lens, c.skip, H, ctx->logits, ctx->max_tokens, c.k, c.n_sink, c.n_local,
-                       c.vote, c.vote_stride};
-      hard_vote_kernel<<<dim3(H, c.B), kHardThreads, 0, s>>>(hv);
-      ctx->kernels += 1;
-    }
-  }
-  return cuda_status(cudaGetLastError());
+  ctx->kernels += 1;
+  return run_votes(ctx, c, s);
 }
 
 }  // namespace
@@ -482,6 +489,7 @@ ts_status run_score(ts_ctx* ctx, const ScoreCall& c, cudaStream_t s) {
 
 bool score_supported(const ts_config& c) {
   const int G = c.n_kv_heads > 0 ? c.n_q_heads / c.n_kv_heads : 0;
+  if (q4_supported(c)) return true;
 #define X(DT, T, D_, HKV_, G_) \
   if (c.kv_dtype == DT && c.head_dim == D_ && c.n_kv_heads == HKV_ && G == G_) return true;
   TS_SCORE_GEOMETRIES(X)
@@ -492,6 +500,10 @@ bool score_supported(const ts_config& c) {
 ts_status launch_score(ts_ctx* ctx, const ScoreCall& a, cudaStream_t s) {
   const ts_config& c = ctx->cfg;
   const int G = c.n_q_heads / c.n_kv_heads;
+  if (c.kv_dtype == TS_KV_Q4) {
+    const ts_status st = launch_score_q4(ctx, a, s);
+    return st == TS_OK ? run_votes(ctx, a, s) : st;
+  }
 #define X(DT, T, D_, HKV_, G_) \
   if (c.kv_dtype == DT && c.head_dim == D_ && c.n_kv_heads == HKV_ && G == G_) return run_score<T, D_, HKV_, G_>(ctx, a, s);
   TS_SCORE_GEOMETRIES(X)
