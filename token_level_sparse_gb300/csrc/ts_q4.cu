@@ -7,12 +7,13 @@
 // stream of 4-bit blocks (68 bytes per row of 128) as long as the arithmetic keeps up: the codes
 // are unpacked in registers (9 instructions for 8 codes) and multiplied on the tensor cores.
 //
-// scan_kernel (whole sequences): a CTA owns a group of up to 4 head sets (a head set: up to 8 query
-// heads of one KV head) and an even share of all pages of the batch, as one contiguous range. A
-// producer warp streams its pages' blocks through a ring in shared memory with bulk copies; 12
-// consumer warps, 12 / sets of them per head set, take the pages in turn. At the end of a
-// sequence's part of the range the warps of a head set join their states, and q4_merge_kernel
-// joins the parts of a sequence in CTA order. Every sum has a fixed order.
+// scan_kernel (whole sequences): a CTA owns a group of up to 4 head sets (a head set: up to 4 query
+// heads of one KV head, or up to 8 where there are more than 4 to a KV head) and an even share of all pages of the batch, as one contiguous range. Its 16
+// warps are shared out over the head sets and take the pages in turn, each with a ring of blocks of
+// its own in shared memory that it fills with bulk copies several pages ahead: no warp waits for
+// another one inside a sequence. At the end of a sequence's part of the range the warps of a head
+// set join their states, and q4_merge_kernel joins the parts of a sequence in CTA order. Every sum
+// has a fixed order.
 //
 // gather_kernel (a list of tokens): 16 listed tokens per step straight from global memory; the list
 // is split over CTAs and joined by the same merge.
@@ -20,15 +21,14 @@
 #include <cmath>
 
 #include "ts_q4.cuh"
+#include "ts_tc.cuh"
 
 namespace ts {
 namespace {
 
-constexpr int kQ4Warps = 12;                    // consumer warps: a multiple of 1, 2, 3 and 4 head sets
-constexpr int kQ4Threads = (kQ4Warps + 1) * 32;
+constexpr int kQ4Warps = 16;                    // of a scan CTA, one CTA per SM
+constexpr int kQ4Threads = kQ4Warps * 32;
 constexpr int kQ4Sets = 4;                      // head sets of a CTA, at most
-constexpr int kQ4MaxStages = 32;
-constexpr int kQ4RingBytes = 144 * 1024;
 constexpr int kGatherWarps = 4;
 
 struct Q4Args {
@@ -42,7 +42,8 @@ struct Q4Args {
   const uint8_t* skip;           // score only: sequences left out
   int max_tokens;
   int B, H, HKV, G;
-  int sets_per_kv;               // head sets of one KV head: ceil(G / 8)
+  int sets_per_kv;               // head sets of one KV head: ceil(G / set_heads)
+  int set_heads;                 // 4 or 8
   int n_groups;                  // groups of kQ4Sets head sets
   int ctas;                      // CTAs per group
   float scale;
@@ -58,10 +59,10 @@ __device__ __forceinline__ int seq_pages(const Q4Args& a, int b) {
   return (n < 0 || n > a.max_tokens) ? 0 : (n + kPage - 1) / kPage;
 }
 
-// CTAs of a group that get pages: a share is at least one page for every warp of a head set, so a
+// CTAs of a group that get pages: a share is about one page for every warp of a head set, so a
 // short batch does not spread over CTAs whose merge would cost more than their pages.
 __device__ __forceinline__ int live_ctas(int64_t total, int ctas) {
-  const int64_t want = (total + 2) / 3;
+  const int64_t want = (total + 3) / 4;
   return (int)(want < 1 ? 1 : (want < ctas ? want : ctas));
 }
 
@@ -112,28 +113,36 @@ __device__ __forceinline__ bool next_part(const Q4Args& a, Q4Range& r, int& b, i
   return false;
 }
 
+// Ring of one warp: blocks of K (and V) of this many pages. 16 warps x 6 x 2176 bytes in flight at
+// d = 128 are four times what one SM's share of HBM bandwidth needs to cover a microsecond.
+template <int NB, int NT, bool kAttend>
+struct Q4Ring {
+  static constexpr int BLK = q4_block_bytes(NB * 64);
+  static constexpr int STAGE = (kAttend ? 2 : 1) * BLK;
+  static constexpr int STAGES = 6;
+  static constexpr int BYTES = STAGES * STAGE;                     // also holds [4 NT][d] floats at a join
+  static constexpr int SMEM = kQ4Warps * BYTES;
+  static_assert(!kAttend || BYTES >= 4 * NT * NB * 64 * 4, "the join's area");
+  static_assert(STAGE % 16 == 0, "bulk copies");
+};
+
 // kAttend: attention partials; otherwise logits and (max, sum exp) partials.
-template <int NB, bool kAttend>
+template <int NB, int NT, bool kAttend>
 __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_constant__ Q4Args a) {
-  constexpr int D = NB * 64;
-  constexpr int BLK = q4_block_bytes(D), CODES = q4_code_bytes(D);
+  using R = Q4Ring<NB, NT, kAttend>;
+  constexpr int D = NB * 64, CODES = q4_code_bytes(D);
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ __align__(8) uint64_t full[kQ4MaxStages], empty[kQ4MaxStages];
-  __shared__ int s_valid[kQ4MaxStages];
-  __shared__ float2 s_ml[kQ4Warps][8];
+  __shared__ __align__(8) uint64_t full[kQ4Warps][R::STAGES];
+  __shared__ float2 s_ml[kQ4Warps][4 * NT];
   __shared__ Q4Range s_range;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = blockIdx.x % a.n_groups, cta = blockIdx.x / a.n_groups;
   const int set0 = group * kQ4Sets, nsets = min(kQ4Sets, a.HKV * a.sets_per_kv - set0);
-  const int kv0 = set0 / a.sets_per_kv, nkv = (set0 + nsets - 1) / a.sets_per_kv - kv0 + 1;
-  const int per_set = kQ4Warps / nsets;
-  const int operand = nkv * BLK;                                   // bytes of one page's K (or V) of this group
-  const int stage_bytes = (kAttend ? 2 : 1) * operand;
-  const int nst = min(kQ4MaxStages, kQ4RingBytes / stage_bytes);
+  const int per_set = kQ4Warps / nsets;                            // 3 head sets: one warp is left over
 
   if (warp == 0) {
-    // this CTA's pages of the batch and the sequence they begin in
+    // this CTA's pages of the batch
     int64_t total, before;
     count_pages(a, 0, lane, total, before);
     if (lane == 0) {
@@ -144,11 +153,6 @@ __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_consta
       r.b = 0;
       r.b0 = 0;
       s_range = r;
-      for (int s = 0; s < nst; ++s) {
-        mbar_init(&full[s], 1);
-        mbar_init(&empty[s], nsets);
-      }
-      mbar_fence_init();
     }
     if (cta == 0 && group == 0)
       for (int b = lane; b < a.B; b += 32) {
@@ -156,186 +160,190 @@ __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_consta
         if (!(a.skip && a.skip[b]) && (n < 0 || n > a.max_tokens)) set_error(a.status, TS_ERR_SEQ_LEN);
       }
   }
+  if (lane == 0) {
+    for (int s = 0; s < R::STAGES; ++s) mbar_init(&full[warp][s], 1);
+    mbar_fence_init();
+  }
   __syncthreads();
   Q4Range r = s_range;
-  int b, p0, p1, it = 0;                                           // it: pages of this CTA so far
 
-  if (warp == kQ4Warps) {
-    // ---- producer: 32 page ids at a time, then one bulk copy per page and operand
-    bool ok = true;
-    while (ok && next_part(a, r, b, p0, p1)) {
-      for (int c0 = p0; c0 < p1 && ok; c0 += 32) {
-        const int mine = c0 + lane < p1 ? a.page_table[(size_t)b * a.pt_stride + c0 + lane] : 0;
-        for (int j = 0; j < min(32, p1 - c0); ++j, ++it) {
-          const int page = __shfl_sync(kFull, mine, j);
-          const int s = it % nst;
-          int fine = 1;
-          if (lane == 0) {
-            if (it >= nst) fine = mbar_wait(&empty[s], ((it / nst) - 1) & 1);
-            if (fine) {
-              const bool in = page >= 0 && (int64_t)page < a.num_pages;
-              s_valid[s] = in;
-              if (in) {
-                unsigned char* dst = smem + (size_t)s * stage_bytes;
-                const size_t off = ((size_t)page * a.HKV + kv0) * BLK;
-                mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes);
-                bulk_g2s(dst, a.k_pool + off, (uint32_t)operand, &full[s]);
-                if (kAttend) bulk_g2s(dst + operand, a.v_pool + off, (uint32_t)operand, &full[s]);
-              } else {
-                set_error(a.status, TS_ERR_PAGE_OOB);
-                mbar_arrive(&full[s]);
-              }
-            }
-          }
-          if (!__shfl_sync(kFull, fine, 0)) {
-            if (lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
-            ok = false;
-            break;
-          }
-        }
-      }
-    }
-    // no copy may still be landing when the CTA exits
-    if (lane == 0)
-      for (int i = max(0, it - nst); i < it; ++i)
-        if (!mbar_wait(&full[i % nst], (i / nst) & 1)) set_error(a.status, TS_ERR_TIMEOUT);
-    return;
-  }
-
-  // ---- consumers: warp -> (head set, pages it = j mod per_set)
   const int hs = warp / per_set, j = warp % per_set;
   const bool works = hs < nsets;
   const int set = set0 + (works ? hs : 0);
-  const int kv = set / a.sets_per_kv, head0 = kv * a.G + (set % a.sets_per_kv) * 8;
-  const int nh = min(8, a.G - (set % a.sets_per_kv) * 8);          // heads of this set
-  float* merge = reinterpret_cast<float*>(smem + kQ4RingBytes);    // [warps][8][D]
+  const int kv = set / a.sets_per_kv, head0 = kv * a.G + (set % a.sets_per_kv) * (4 * NT);
+  const int nh = min(4 * NT, a.G - (set % a.sets_per_kv) * (4 * NT));   // heads of this set
+  unsigned char* ring = smem + (size_t)warp * R::BYTES;
+  uint64_t* bars = full[warp];
+  uint32_t phases = 0u;                                            // bit s: parity of the stage's next wait
   bool ok = works;
+  int b, p0, p1;
   while (next_part(a, r, b, p0, p1)) {
     const int n = a.seq_lens[b];
-    Q4Query<NB> f;
-    q4_load_query<NB>(f, a.q + ((size_t)b * a.H + head0 + (g < nh ? g : 0)) * D, g < nh, t);
-    const float mul = a.scale * f.inv * (kAttend ? 1.4426950408889634f : 1.f);
-    Q4State<NB> st;
+    Q4Query<NB, NT> f;
+    q4_load_query<NB, NT>(f, a.q + ((size_t)b * a.H + head0) * D, nh, lane);
+    float mul[NT];
+    Q4State<NB, NT> st;                                            // (the score uses its m and l alone)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mul[nt] = a.scale * f.inv[nt] * (kAttend ? 1.4426950408889634f : 1.f);
     st.reset();
-    float m = -INFINITY, l = 0.f;                                  // the score's running (max, sum exp) of this lane
-    for (int p = p0; p < p1; ++p, ++it) {
-      if (it % per_set != j || !ok) continue;
-      const int s = it % nst;
-      if (!mbar_wait(&full[s], (it / nst) & 1)) {
-        set_error(a.status, TS_ERR_TIMEOUT);
-        ok = false;
-        continue;
+    // this warp's pages: p0 + j, p0 + j + per_set, ...; lane i holds the id of the next 32 to copy
+    const int32_t* pt = a.page_table + (size_t)b * a.pt_stride;
+    const int mine = ok && p0 + j < p1 ? (p1 - p0 - j + per_set - 1) / per_set : 0;
+    int ids = 0, copied = 0, cs = 0;                               // pages copied so far, the next one's stage
+    uint32_t lost = 0u;                                            // bit s: stage s has no page
+    auto copy_next = [&]() {
+      if (copied >= mine) return;
+      if ((copied & 31) == 0) {
+        const int i = copied + lane;
+        ids = i < mine ? pt[p0 + j + i * per_set] : 0;
       }
-      const unsigned char* kb = smem + (size_t)s * stage_bytes + (kv - kv0) * BLK;
-      const bool valid = s_valid[s] != 0;
-      uint2 kw[2][NB];
-      float ks[NB][4];
-      // token (tile u, column c) of the 16: the attention wants lane t's four tokens to be t + 4 i
-      // (its V rows then fall in different banks), the score wants neighbours for its stores
-      auto token = [&](int u, int c) { return kAttend ? 8 * u + 4 * (c & 1) + (c >> 1) : 8 * u + c; };
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          kw[u][nb] = *reinterpret_cast<const uint2*>(kb + nb * 512 + token(u, g) * 32 + t * 8);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          ks[nb][i] = bf16_bits_f(
-              *reinterpret_cast<const uint16_t*>(kb + CODES + nb * 32 + token(i >> 1, 2 * t + (i & 1)) * 2));
-      }
-      float x[4];
-      q4_scores<NB>(f, kw, ks, x);
-      const int left = valid ? n - p * kPage : 0;                  // tokens of the sequence in this page
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = token(i >> 1, 2 * t + (i & 1)) < left ? x[i] * mul : -INFINITY;
-      if constexpr (kAttend) {
-        const unsigned char* vb = kb + operand;
-        uint32_t vw[4][NB];
-        float vs[NB][4];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tk = token(i >> 1, 2 * t + (i & 1));
-            vw[i][nb] = *reinterpret_cast<const uint32_t*>(vb + nb * 512 + tk * 32 + g * 4);
-            vs[nb][i] = bf16_bits_f(*reinterpret_cast<const uint16_t*>(vb + CODES + nb * 32 + tk * 2));
-          }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
-        q4_accumulate<NB>(st, x, vw, vs);
-      } else {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
-        const float mn = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-        l *= m == mn ? 1.f : expf(m - mn);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) l += x[i] == -INFINITY ? 0.f : expf(x[i] - mn);
-        m = mn;
-        if (g < nh) {
-          float* row = a.logits + ((size_t)b * a.H + head0 + g) * a.max_tokens + p * kPage + 2 * t;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) *reinterpret_cast<float2*>(row + 8 * u) = make_float2(x[2 * u], x[2 * u + 1]);
+      const int page = __shfl_sync(kFull, ids, copied & 31);
+      const bool in = page >= 0 && (int64_t)page < a.num_pages;
+      lost = in ? lost & ~(1u << cs) : lost | (1u << cs);
+      if (lane == 0) {
+        if (in) {
+          unsigned char* dst = ring + cs * R::STAGE;
+          const size_t off = ((size_t)page * a.HKV + kv) * R::BLK;
+          mbar_arrive_expect_tx(&bars[cs], R::STAGE);
+          bulk_g2s(dst, a.k_pool + off, R::BLK, &bars[cs]);
+          if (kAttend) bulk_g2s(dst + R::BLK, a.v_pool + off, R::BLK, &bars[cs]);
+        } else {
+          set_error(a.status, TS_ERR_PAGE_OOB);
+          mbar_arrive(&bars[cs]);
         }
       }
+      ++copied;
+      cs = cs + 1 == R::STAGES ? 0 : cs + 1;
+    };
+    for (int i = 0; i < R::STAGES; ++i) copy_next();
+    int s = 0, left = n - (p0 + j) * kPage;                        // tokens of the sequence from this page on
+    int done = 0;
+    for (; done < mine; ++done) {
+      ok = mbar_wait(&bars[s], (phases >> s) & 1u);
+      ok = __all_sync(kFull, ok);
+      if (!ok) {
+        set_error(a.status, TS_ERR_TIMEOUT);
+        break;
+      }
+      phases ^= 1u << s;
+      const unsigned char* kb = ring + s * R::STAGE;
+      // the place in the page of token (u, c): the attention wants lane t's value rows, tokens (u, 2t)
+      // and (u, 2t + 1), in different banks; the score wants neighbours for its stores
+      auto token = [&](int u, int c) { return kAttend ? 8 * u + 4 * (c & 1) + (c >> 1) : 8 * u + c; };
+      uint2 kw[2][NB];
+      float ks[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          kw[u][nb] = *reinterpret_cast<const uint2*>(kb + nb * 512 + token(u, g) * 32 + t * 8);
+          ks[nb][u] = bf16_bits_f(*reinterpret_cast<const uint16_t*>(kb + CODES + nb * 32 + token(u, g) * 2));
+        }
+      float x[NT][2];
+      q4_scores<NB, NT>(f, kw, ks, x);
+      const int limit = (lost >> s) & 1u ? 0 : left;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) x[nt][u] *= mul[nt];
+      if (limit < kPage) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) x[nt][u] = token(u, g) < limit ? x[nt][u] : -INFINITY;
+      }
+      if constexpr (kAttend) {
+        const unsigned char* vb = kb + R::BLK;
+        uint32_t vw[4][NB];
+        float vs[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            vw[e][nb] = *reinterpret_cast<const uint32_t*>(vb + nb * 512 + token(e >> 1, 2 * t + (e & 1)) * 32 + g * 4);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            vs[nb][u] = bf16_bits_f(*reinterpret_cast<const uint16_t*>(vb + CODES + nb * 32 + token(u, g) * 2));
+        }
+        __syncwarp();                                              // every lane has read the stage
+        copy_next();
+        if (limit < kPage)
+          q4_accumulate<NB, NT, true>(st, x, vw, vs);
+        else
+          q4_accumulate<NB, NT, false>(st, x, vw, vs);
+      } else {
+        __syncwarp();
+        copy_next();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float mn = fmaxf(st.m[nt], fmaxf(x[nt][0], x[nt][1]));
+          st.l[nt] *= st.m[nt] == mn ? 1.f : expf(st.m[nt] - mn);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) st.l[nt] += x[nt][u] == -INFINITY ? 0.f : expf(x[nt][u] - mn);
+          st.m[nt] = mn;
+          if (4 * nt + t < nh) {
+            float* row = a.logits + ((size_t)b * a.H + head0 + 4 * nt + t) * a.max_tokens + (n - left) + g;
+            row[0] = x[nt][0];
+            row[8] = x[nt][1];
+          }
+        }
+      }
+      left -= per_set * kPage;
+      s = s + 1 == R::STAGES ? 0 : s + 1;
     }
-    // ---- the warps of a head set join their states (named barrier of the consumers)
-    if constexpr (kAttend) {
-      l = st.l;
-      m = st.m;
-    } else {
-      const float m1 = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-      const float mn = fmaxf(m1, __shfl_xor_sync(kFull, m1, 2));
-      l *= m == mn ? 1.f : expf(m - mn);
-      m = mn;
+    if (!ok && works) {
+      // a wait ran out: what was copied ahead lands before the ring is used for anything else
+      for (; done < copied; ++done) {
+        mbar_wait(&bars[s], (phases >> s) & 1u);
+        s = s + 1 == R::STAGES ? 0 : s + 1;
+      }
     }
-    l += __shfl_xor_sync(kFull, l, 1);
-    l += __shfl_xor_sync(kFull, l, 2);
-    if (t == 0) s_ml[warp][g] = make_float2(m, l);
-    asm volatile("bar.sync 1, %0;" ::"n"(kQ4Warps * 32) : "memory");
-    float M = -INFINITY, L = 0.f;
-    if (works) {
-      for (int w = 0; w < per_set; ++w) M = fmaxf(M, s_ml[hs * per_set + w][g].x);
-      for (int w = 0; w < per_set; ++w) {
-        const float2 ml = s_ml[hs * per_set + w][g];
+    // the next sequence's copies begin at stage 0 again
+    // ---- the warps of a head set join their states
+    if constexpr (!kAttend) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mn = fmaxf(st.m[nt], __shfl_xor_sync(kFull, st.m[nt], 4));
+        mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 8));
+        mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 16));
+        st.l[nt] *= part_weight<false>(st.m[nt], mn);
+        st.m[nt] = mn;
+      }
+    }
+    st.join_lanes();
+    if (g == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s_ml[warp][4 * nt + t] = make_float2(st.m[nt], st.l[nt]);
+    }
+    __syncthreads();
+    float fac[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float M = -INFINITY, L = 0.f;
+      for (int w = 0; w < (works ? per_set : 0); ++w) M = fmaxf(M, s_ml[hs * per_set + w][4 * nt + t].x);
+      for (int w = 0; w < (works ? per_set : 0); ++w) {
+        const float2 ml = s_ml[hs * per_set + w][4 * nt + t];
         L += ml.y * part_weight<kAttend>(ml.x, M);
       }
-      const int64_t slot = cta + b;
-      if (j == 0 && t == 0 && g < nh) a.part_ml[slot * a.H + head0 + g] = make_float2(M, L);
+      fac[nt] = part_weight<kAttend>(st.m[nt], M);
+      if (works && j == 0 && g == 0 && 4 * nt + t < nh)
+        a.part_ml[(int64_t)(cta + b) * a.H + head0 + 4 * nt + t] = make_float2(M, L);
     }
     if constexpr (kAttend) {
-      if (works) {
-        const float fac = part_weight<true>(st.m, M);
-        float* mg = merge + ((size_t)warp * 8 + g) * D;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float4 lo, hi;
-            lo.x = (st.o[nb][0][q] + st.o[nb][0][q + 2]) * fac;
-            lo.y = (st.o[nb][1][q] + st.o[nb][1][q + 2]) * fac;
-            lo.z = (st.o[nb][2][q] + st.o[nb][2][q + 2]) * fac;
-            lo.w = (st.o[nb][3][q] + st.o[nb][3][q + 2]) * fac;
-            hi.x = (st.o[nb][4][q] + st.o[nb][4][q + 2]) * fac;
-            hi.y = (st.o[nb][5][q] + st.o[nb][5][q + 2]) * fac;
-            hi.z = (st.o[nb][6][q] + st.o[nb][6][q + 2]) * fac;
-            hi.w = (st.o[nb][7][q] + st.o[nb][7][q + 2]) * fac;
-            float4* dst = reinterpret_cast<float4*>(mg + nb * 64 + 8 * (2 * t + q));
-            dst[0] = lo;
-            dst[1] = hi;
-          }
-      }
-      asm volatile("bar.sync 1, %0;" ::"n"(kQ4Warps * 32) : "memory");
+      if (works) st.store(reinterpret_cast<float*>(ring), fac, lane);
+      __syncthreads();
       if (works) {
         float* po = a.part_o + ((int64_t)(cta + b) * a.H + head0) * D;
-        const float* mg = merge + (size_t)hs * per_set * 8 * D;
+        const unsigned char* mg = smem + (size_t)hs * per_set * R::BYTES;
         for (int i = j * 32 + lane; i < nh * D; i += per_set * 32) {
           float acc = 0.f;
-          for (int w = 0; w < per_set; ++w) acc += mg[(size_t)w * 8 * D + i];
+          for (int w = 0; w < per_set; ++w) acc += reinterpret_cast<const float*>(mg + (size_t)w * R::BYTES)[i];
           po[i] = acc;
         }
       }
+      fence_proxy_async();                                         // these areas are copied into again
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(kQ4Warps * 32) : "memory");   // joined: the areas may be reused
+    __syncthreads();
   }
 }
 
@@ -419,30 +427,34 @@ struct Q4GatherArgs {
 };
 
 // CTA (split, head set, sequence): a contiguous part of the index list, 16 tokens per warp and step.
-template <int NB>
+template <int NB, int NT>
 __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_constant__ Q4Args a,
                                                                    const __grid_constant__ Q4GatherArgs ga) {
-  constexpr int D = NB * 64;
-  constexpr int BLK = q4_block_bytes(D), CODES = q4_code_bytes(D);
-  __shared__ __align__(16) float merge[kGatherWarps][8][D];
-  __shared__ float2 s_ml[kGatherWarps][8];
+  constexpr int D = NB * 64, BLK = q4_block_bytes(D), CODES = q4_code_bytes(D);
+  __shared__ __align__(16) float merge[kGatherWarps][4 * NT][D];
+  __shared__ float2 s_ml[kGatherWarps][4 * NT];
   const int split = blockIdx.x, set = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int kv = set / a.sets_per_kv, head0 = kv * a.G + (set % a.sets_per_kv) * 8;
-  const int nh = min(8, a.G - (set % a.sets_per_kv) * 8);
+  const int kv = set / a.sets_per_kv, head0 = kv * a.G + (set % a.sets_per_kv) * (4 * NT);
+  const int nh = min(4 * NT, a.G - (set % a.sets_per_kv) * (4 * NT));
   const int cnt = (int)min((int64_t)max(ga.count[b], 0), ga.idx_stride);
   const int units = (cnt + 15) / 16;
   const int u0 = (int)((int64_t)units * split / ga.splits), u1 = (int)((int64_t)units * (split + 1) / ga.splits);
   const int32_t* ib = ga.idx + (size_t)b * ga.idx_stride;
   const int32_t* pt = a.page_table + (size_t)b * a.pt_stride;
 
-  Q4Query<NB> f;
-  q4_load_query<NB>(f, a.q + ((size_t)b * a.H + head0 + (g < nh ? g : 0)) * D, g < nh, t);
-  const float mul = a.scale * f.inv * 1.4426950408889634f;
-  Q4State<NB> st;
+  Q4Query<NB, NT> f;
+  q4_load_query<NB, NT>(f, a.q + ((size_t)b * a.H + head0) * D, nh, lane);
+  float mul[NT], one[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    mul[nt] = a.scale * f.inv[nt] * 1.4426950408889634f;
+    one[nt] = 1.f;
+  }
+  Q4State<NB, NT> st;
   st.reset();
   for (int u = u0 + warp; u < u1; u += kGatherWarps) {
-    // lane i holds list entry i (of 16) as its block offset and slot; -1 where there is none
+    // lane i holds list entry i (of 16) as its row in the pool; -1 where there is none
     int64_t mine = -1;
     const int at = u * 16 + (lane & 15);
     if (at < cnt) {
@@ -450,51 +462,50 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
       int page = -1;
       if (tk >= 0 && tk < a.max_tokens) page = pt[tk / kPage];
       if (page >= 0 && (int64_t)page < a.num_pages)
-        mine = ((int64_t)page * a.HKV + kv) * kPage + tk % kPage;      // row number in the pool
+        mine = ((int64_t)page * a.HKV + kv) * kPage + tk % kPage;
       else
         set_error(a.status, TS_ERR_PAGE_OOB);
     }
     uint2 kw[2][NB];
-    float ks[NB][4], vs[NB][4], x[4];
+    float ks[NB][2], vs[NB][2], x[NT][2];
     uint32_t vw[4][NB];
-    int64_t own[4];
+    bool in[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t row = __shfl_sync(kFull, mine, 8 * i + g);
-      const unsigned char* kb = a.k_pool + (row < 0 ? 0 : (row / kPage) * BLK + (row % kPage) * 32);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        kw[i][nb] = row < 0 ? make_uint2(0u, 0u) : *reinterpret_cast<const uint2*>(kb + nb * 512 + t * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      own[i] = __shfl_sync(kFull, mine, 8 * (i >> 1) + 2 * t + (i & 1));
-      const size_t blk = own[i] < 0 ? 0 : (size_t)(own[i] / kPage) * BLK;
-      const int slot = own[i] < 0 ? 0 : (int)(own[i] % kPage);
+      in[i] = row >= 0;
+      const size_t blk = in[i] ? (size_t)(row / kPage) * BLK : 0;
+      const int slot = in[i] ? (int)(row % kPage) : 0;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const size_t so = blk + CODES + nb * 32 + slot * 2;
-        ks[nb][i] = own[i] < 0 ? 0.f : bf16_bits_f(*reinterpret_cast<const uint16_t*>(a.k_pool + so));
-        vs[nb][i] = own[i] < 0 ? 0.f : bf16_bits_f(*reinterpret_cast<const uint16_t*>(a.v_pool + so));
-        vw[i][nb] = own[i] < 0 ? 0u : *reinterpret_cast<const uint32_t*>(a.v_pool + blk + nb * 512 + slot * 32 + g * 4);
+        kw[i][nb] = in[i] ? *reinterpret_cast<const uint2*>(a.k_pool + blk + nb * 512 + slot * 32 + t * 8) : make_uint2(0u, 0u);
+        ks[nb][i] = in[i] ? bf16_bits_f(*reinterpret_cast<const uint16_t*>(a.k_pool + so)) : 0.f;
+        vs[nb][i] = in[i] ? bf16_bits_f(*reinterpret_cast<const uint16_t*>(a.v_pool + so)) : 0.f;
       }
     }
-    q4_scores<NB>(f, kw, ks, x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = own[i] < 0 ? -INFINITY : x[i] * mul;
-    q4_accumulate<NB>(st, x, vw, vs);
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = __shfl_sync(kFull, mine, 8 * (i >> 1) + 2 * t + (i & 1));
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        vw[i][nb] = row < 0 ? 0u
+                            : *reinterpret_cast<const uint32_t*>(a.v_pool + (size_t)(row / kPage) * BLK + nb * 512 +
+                                                                 (row % kPage) * 32 + g * 4);
+    }
+    q4_scores<NB, NT>(f, kw, ks, x);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) x[nt][i] = in[i] ? x[nt][i] * mul[nt] : -INFINITY;
+    q4_accumulate<NB, NT, true>(st, x, vw, vs);
   }
-  float l = st.l;
-  l += __shfl_xor_sync(kFull, l, 1);
-  l += __shfl_xor_sync(kFull, l, 2);
-  if (t == 0) s_ml[warp][g] = make_float2(st.m, l);
+  st.join_lanes();
+  if (g == 0) {
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int jj = 0; jj < 8; ++jj)
-        merge[warp][g][nb * 64 + 8 * (2 * t + q) + jj] = st.o[nb][jj][q] + st.o[nb][jj][q + 2];
+    for (int nt = 0; nt < NT; ++nt) s_ml[warp][4 * nt + t] = make_float2(st.m[nt], st.l[nt]);
+  }
+  st.store(&merge[warp][0][0], one, lane);
   __syncthreads();
   const int64_t slot = (int64_t)b * ga.splits + split;
   for (int i = tid; i < nh * D; i += kGatherWarps * 32) {
@@ -529,7 +540,8 @@ Q4Args make_args(ts_ctx* ctx, const float* q, const void* k_pool, const void* v_
   a.H = c.n_q_heads;
   a.HKV = c.n_kv_heads;
   a.G = a.H / a.HKV;
-  a.sets_per_kv = (a.G + 7) / 8;
+  a.set_heads = a.G <= 4 ? 4 : 8;
+  a.sets_per_kv = (a.G + a.set_heads - 1) / a.set_heads;
   a.n_groups = (a.HKV * a.sets_per_kv + kQ4Sets - 1) / kQ4Sets;
   a.ctas = ctx->num_sms / a.n_groups;
   a.ctas = std::max(1, std::min(a.ctas, kMaxParts));
@@ -541,37 +553,43 @@ Q4Args make_args(ts_ctx* ctx, const float* q, const void* k_pool, const void* v_
   return a;
 }
 
-template <int NB>
+template <int NB, int NT>
 ts_status run_attend(ts_ctx* ctx, const Q4Args& a, float* out, float* lse, cudaStream_t s) {
-  constexpr size_t smem = kQ4RingBytes + (size_t)kQ4Warps * 8 * NB * 64 * sizeof(float);
-  if (!ensure_smem<scan_kernel<NB, true>>(smem, ctx->device)) return TS_ERR_CUDA;
+  constexpr size_t smem = Q4Ring<NB, NT, true>::SMEM;
+  if (!ensure_smem<scan_kernel<NB, NT, true>>(smem, ctx->device)) return TS_ERR_CUDA;
   ProfScope ps(ctx, TS_PROF_ATTEND, s);
   ctx->kernels += 2;
-  scan_kernel<NB, true><<<a.ctas * a.n_groups, kQ4Threads, smem, s>>>(a);
+  scan_kernel<NB, NT, true><<<a.ctas * a.n_groups, kQ4Threads, smem, s>>>(a);
   q4_merge_kernel<NB * 64><<<dim3(a.H, a.B), 1024, 0, s>>>(a, 0, out, lse);
   return cuda_status(cudaGetLastError());
 }
 
-template <int NB>
+template <int NB, int NT>
 ts_status run_scan(ts_ctx* ctx, const Q4Args& a, cudaStream_t s) {
-  if (!ensure_smem<scan_kernel<NB, false>>((size_t)kQ4RingBytes, ctx->device)) return TS_ERR_CUDA;
+  constexpr size_t smem = Q4Ring<NB, NT, false>::SMEM;
+  if (!ensure_smem<scan_kernel<NB, NT, false>>(smem, ctx->device)) return TS_ERR_CUDA;
   ProfScope ps(ctx, TS_PROF_SCORE, s);
   ctx->kernels += 2;
-  scan_kernel<NB, false><<<a.ctas * a.n_groups, kQ4Threads, kQ4RingBytes, s>>>(a);
+  scan_kernel<NB, NT, false><<<a.ctas * a.n_groups, kQ4Threads, smem, s>>>(a);
   q4_stats_kernel<<<a.B, 256, 0, s>>>(a, ctx->stats);
   return cuda_status(cudaGetLastError());
 }
 
-template <int NB>
+template <int NB, int NT>
 ts_status run_gather(ts_ctx* ctx, const Q4Args& a, const Q4GatherArgs& ga, float* out, float* lse, cudaStream_t s) {
   ProfScope ps(ctx, TS_PROF_ATTEND, s);
   ctx->kernels += 2;
-  gather_kernel<NB><<<dim3(ga.splits, a.HKV * a.sets_per_kv, a.B), kGatherWarps * 32, 0, s>>>(a, ga);
+  gather_kernel<NB, NT><<<dim3(ga.splits, a.HKV * a.sets_per_kv, a.B), kGatherWarps * 32, 0, s>>>(a, ga);
   q4_merge_kernel<NB * 64><<<dim3(a.H, a.B), 1024, 0, s>>>(a, ga.splits, out, lse);
   return cuda_status(cudaGetLastError());
 }
 
 }  // namespace
+
+// (64-element blocks of a head, column tiles of a head set)
+#define TS_Q4_DISPATCH(FN, ...)                                                                   \
+  (ctx->cfg.head_dim == 64 ? (a.set_heads == 4 ? FN<1, 1>(__VA_ARGS__) : FN<1, 2>(__VA_ARGS__)) \
+                           : (a.set_heads == 4 ? FN<2, 1>(__VA_ARGS__) : FN<2, 2>(__VA_ARGS__)))
 
 bool q4_supported(const ts_config& c) {
   return c.kv_dtype == TS_KV_Q4 && c.page_size == kPage && (c.head_dim == 64 || c.head_dim == 128) &&
@@ -579,27 +597,22 @@ bool q4_supported(const ts_config& c) {
 }
 
 // Parts of any call: a scan has at most one per CTA and one more per sequence, a gather at most
-// 2 num_sms + B (splits below rounds up once per sequence).
+// 2 num_sms + B (its splits round up once per sequence).
 int64_t q4_part_slots(const ts_config& c, int num_sms) { return 2 * (int64_t)num_sms + c.max_batch; }
-
-int q4_gather_splits(const ts_config& c, int num_sms, int B) {
-  const int sets = c.n_kv_heads * ((c.n_q_heads / c.n_kv_heads + 7) / 8);
-  const int s = (2 * num_sms + sets * B - 1) / (sets * B);
-  return s < 1 ? 1 : (s > kAttnMaxSplits ? kAttnMaxSplits : s);
-}
 
 ts_status launch_attend_q4(ts_ctx* ctx, const AttendCall& c, const int32_t* seq_lens, cudaStream_t s) {
   Q4Args a = make_args(ctx, c.q, c.k_pool, c.v_pool, c.page_table, seq_lens, c.B, c.scale);
-  if (!c.idx) return ctx->cfg.head_dim == 64 ? run_attend<1>(ctx, a, c.out, c.lse, s) : run_attend<2>(ctx, a, c.out, c.lse, s);
-  Q4GatherArgs ga{c.idx, c.idx_stride, c.count, q4_gather_splits(ctx->cfg, ctx->num_sms, c.B)};
-  return ctx->cfg.head_dim == 64 ? run_gather<1>(ctx, a, ga, c.out, c.lse, s)
-                                 : run_gather<2>(ctx, a, ga, c.out, c.lse, s);
+  if (!c.idx) return TS_Q4_DISPATCH(run_attend, ctx, a, c.out, c.lse, s);
+  const int sets = a.HKV * a.sets_per_kv * a.B;
+  const int splits = std::max(1, std::min((2 * ctx->num_sms + sets - 1) / sets, kAttnMaxSplits));
+  Q4GatherArgs ga{c.idx, c.idx_stride, c.count, splits};
+  return TS_Q4_DISPATCH(run_gather, ctx, a, ga, c.out, c.lse, s);
 }
 
 ts_status launch_score_q4(ts_ctx* ctx, const ScoreCall& c, cudaStream_t s) {
   Q4Args a = make_args(ctx, c.q, c.k_pool, nullptr, c.page_table, c.seq_lens, c.B, c.scale);
   a.skip = c.skip;
-  return ctx->cfg.head_dim == 64 ? run_scan<1>(ctx, a, s) : run_scan<2>(ctx, a, s);
+  return TS_Q4_DISPATCH(run_scan, ctx, a, s);
 }
 
 }  // namespace ts

@@ -10,10 +10,12 @@
 //    contiguous bytes;
 //  * outputs: lane (g, t) takes word g of token t, so 4 tokens x 8 lanes are 128 contiguous bytes.
 //
-// Both products run as m16n8k16 with the query heads as the 16 rows: rows 0..7 hold the high part
-// of 8 heads' queries (or weights) and rows 8..15 the low part of the same heads, so one
-// instruction takes both parts of a split fp32 operand and a lane adds the two results it already
-// holds. Codes are exact in fp16 and bf16, their products with either part are exact in fp32.
+// Both products run as m16n8k16 with the unpacked codes as the 16-row operand (16 tokens, or 16
+// elements of the values) and the heads as its 8 columns: column 2h holds the high part of head h's
+// query (or weight), column 2h + 1 the low part. One instruction so takes both parts of a split fp32
+// operand for four heads, and the two results of a head lie in one lane: lane (g, t) holds head t's
+// scores of tokens g and g + 8, its maximum, its sum and its outputs. Codes are exact in fp16 and
+// bf16 and their products with either part exact in fp32.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -27,17 +29,18 @@ constexpr int kQ4Group = 64;   // elements that share a scale
 __host__ __device__ constexpr int q4_code_bytes(int d) { return kPage * d / 2; }
 __host__ __device__ constexpr int q4_block_bytes(int d) { return kPage * (d / 2 + d / 32); }
 
-// D (16x8, fp32) += A (16x16) B (16x8): lane (g = lane / 4, t = lane % 4) holds A rows g, g + 8 and
-// D rows g, g + 8 at columns 2t, 2t + 1, and column g of B.
+// D (16x8, fp32) += A (16x16) B (16x8): lane (g = lane / 4, t = lane % 4) holds rows g, g + 8 of A,
+// column g of B and rows g, g + 8 of D at columns 2t, 2t + 1. (Not volatile: products of different
+// accumulators may be interleaved.)
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -82,140 +85,192 @@ __device__ __forceinline__ uint32_t q4_pair_bf16(uint32_t ab, int j) {
   return b2_bits(__hadd2(bits_b2(and_or(ab >> (4 * j), 0x000f000fu, 0x43004300u)), m136));
 }
 
-// The queries of up to 8 heads as the A operand of the scores: element pairs in the order that
+// Transposes an 8x8 matrix of 16-bit elements held as (row g, columns 2t, 2t + 1).
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// The queries of up to 4 NT heads as the column operand of the scores: element pairs in the order that
 // q4_pairs_f16 gives the codes. A head's queries are scaled by a power of two so that the largest
-// lies in [2^14, 2^15), then split into two fp16 terms (hi + lo within 2^-22 of the largest
-// relative to it); inv undoes the scaling.
-template <int NB>
+// lies in [2^14, 2^15), then split into two fp16 terms (hi + lo within 2^-22 of the element, or
+// 2^-39 of the largest); inv undoes the scaling for the head whose scores this lane holds.
+template <int NB, int NT>
 struct Q4Query {
-  uint32_t a[NB][4][4];
-  float inv;
+  uint32_t b[NT][NB][4][2];
+  float inv[NT];
 };
 
-template <int NB>
-__device__ __forceinline__ void q4_load_query(Q4Query<NB>& f, const float* q, bool live, int t) {
-  float x[NB][16];
-  float mx = 0.f;
+// q: the first head's row; head h of nh at q + h d.
+template <int NB, int NT>
+__device__ __forceinline__ void q4_load_query(Q4Query<NB, NT>& f, const float* q, int nh, int lane) {
+  const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
+  for (int nt = 0; nt < NT; ++nt) {
+    const int h = 4 * nt + (g >> 1);
+    float x[NB][16];
+    float mx = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      x[nb][i] = live ? q[nb * 64 + 16 * t + i] : 0.f;
-      mx = fmaxf(mx, fabsf(x[nb][i]));
-    }
-  mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-  const int ex = (int)(__float_as_uint(mx) >> 23) - 127;                   // mx < 2^(ex + 1)
-  const int sh = max(-126, min(126, 14 - ex));
-  const float mul = __uint_as_float((uint32_t)(127 + sh) << 23);
-  f.inv = __uint_as_float((uint32_t)(127 - sh) << 23);
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = 8 * (ks >> 1) + 2 * (ks & 1) + h;
-        const float x0 = x[nb][i] * mul, x1 = x[nb][i + 4] * mul;
-        const __half2 hi = __floats2half2_rn(x0, x1);
-        const float2 hf = __half22float2(hi);
-        f.a[nb][ks][2 * h] = h2_bits(hi);
-        f.a[nb][ks][2 * h + 1] = h2_bits(__floats2half2_rn(x0 - hf.x, x1 - hf.y));
+      for (int i = 0; i < 16; ++i) {
+        x[nb][i] = h < nh ? q[(size_t)h * (NB * 64) + nb * 64 + 16 * t + i] : 0.f;
+        mx = fmaxf(mx, fabsf(x[nb][i]));
       }
-}
-
-// Raw products of 16 tokens with the heads: kw[u][nb] are this lane's 8 bytes of token (u, g).
-// dot[2u + x] is head g against this lane's token x of tile u; ks[nb][2u + x] its scales.
-template <int NB>
-__device__ __forceinline__ void q4_scores(const Q4Query<NB>& f, const uint2 (&kw)[2][NB], const float (&ks)[NB][4],
-                                          float (&dot)[4]) {
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t p0[4], p1[4];
-      q4_pairs_f16(kw[u][nb].x, p0);
-      q4_pairs_f16(kw[u][nb].y, p1);
-      mma_f16(c, f.a[nb][0], p0[0], p0[1]);
-      mma_f16(c, f.a[nb][1], p0[2], p0[3]);
-      mma_f16(c, f.a[nb][2], p1[0], p1[1]);
-      mma_f16(c, f.a[nb][3], p1[2], p1[3]);
-      d0 = fmaf(c[0] + c[2], ks[nb][2 * u], d0);
-      d1 = fmaf(c[1] + c[3], ks[nb][2 * u + 1], d1);
-    }
-    dot[2 * u] = d0;
-    dot[2 * u + 1] = d1;
-  }
-}
-
-// Running softmax state of up to 8 heads in one warp: m is head g's maximum (the same in the four
-// lanes of a head), l this lane's own part of the sum, o the outputs (high-part rows in elements 0,
-// 1 of each tile, low-part rows in 2, 3); column n of tile j is element 64 nb + 8 n + j.
-template <int NB>
-struct Q4State {
-  float m, l;
-  float o[NB][8][4];
-  __device__ __forceinline__ void reset() {
-    m = -INFINITY;
-    l = 0.f;
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+    const int ex = (int)(__float_as_uint(mx) >> 23) - 127;                 // mx < 2^(ex + 1)
+    const int sh = max(-126, min(126, 14 - ex));
+    const float mul = __uint_as_float((uint32_t)(127 + sh) << 23);
+    f.inv[nt] = __shfl_sync(kFull, __uint_as_float((uint32_t)(127 - sh) << 23), 8 * t);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[nb][j][e] = 0.f;
+        for (int i2 = 0; i2 < 2; ++i2) {
+          const int i = 8 * (ks >> 1) + 2 * (ks & 1) + i2;
+          const float x0 = x[nb][i] * mul, x1 = x[nb][i + 4] * mul;
+          const __half2 hi = __floats2half2_rn(x0, x1);
+          const float2 hf = __half22float2(hi);
+          f.b[nt][nb][ks][i2] = h2_bits((g & 1) ? __floats2half2_rn(x0 - hf.x, x1 - hf.y) : hi);
+        }
   }
-};
+}
 
-// Adds 16 tokens: x[i] are base-2 logits of this lane's tokens (-inf: not attended), vw[i][nb] word
-// g of token i's codes, vs[nb][i] its scales. The maximum moves only when a logit passes it by more
-// than 2^8, so most units cost no shuffle and no rescaling; weights stay below 2^8.
-template <int NB>
-__device__ __forceinline__ void q4_accumulate(Q4State<NB>& s, const float (&x)[4], const uint32_t (&vw)[4][NB],
-                                              const float (&vs)[NB][4]) {
-  const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-  if (__any_sync(kFull, mx > s.m + 8.f)) {
-    float mn = fmaxf(s.m, mx);
-    mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 1));
-    mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 2));
-    const float f = s.m == mn ? 1.f : ex2(s.m - mn);
-    s.m = mn;
-    s.l *= f;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s.o[nb][j][e] *= f;
-  }
-  float p[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    p[i] = x[i] == -INFINITY ? 0.f : ex2(x[i] - s.m);
-    s.l += p[i];
-  }
+// Products of 16 tokens with the heads: kw[u][nb] are this lane's 8 bytes of token (u, g), ks[nb][u]
+// that token's scale. dot[nt][u] is head 4 nt + t against token (u, g).
+template <int NB, int NT>
+__device__ __forceinline__ void q4_scores(const Q4Query<NB, NT>& f, const uint2 (&kw)[2][NB], const float (&ks)[NB][2],
+                                          float (&dot)[NT][2]) {
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    // a token that is not attended may lie in a slot never written: its scale is not used
-    float w[4];
+    uint32_t p[2][2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = x[i] == -INFINITY ? 0.f : p[i] * vs[nb][i];
-    uint32_t a[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(w[2 * h], w[2 * h + 1]);
-      const float2 hf = __bfloat1622float2(hi);
-      a[2 * h] = b2_bits(hi);
-      a[2 * h + 1] = b2_bits(__floats2bfloat162_rn(w[2 * h] - hf.x, w[2 * h + 1] - hf.y));
+    for (int u = 0; u < 2; ++u) {
+      q4_pairs_f16(kw[u][nb].x, p[u][0]);
+      q4_pairs_f16(kw[u][nb].y, p[u][1]);
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k4 = 0; k4 < 4; ++k4) {
+        const int x = k4 >> 1, i = 2 * (k4 & 1);
+        const uint32_t a[4] = {p[0][x][i], p[1][x][i], p[0][x][i + 1], p[1][x][i + 1]};
+        mma_f16(c, a, f.b[nt][nb][k4][0], f.b[nt][nb][k4][1]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float d = c[2 * u] + c[2 * u + 1];
+        dot[nt][u] = nb == 0 ? d * ks[nb][u] : fmaf(d, ks[nb][u], dot[nt][u]);
+      }
+    }
+  }
+}
+
+// Running softmax state of 4 NT heads in one warp, for head 4 nt + t: m its maximum (the same in the
+// eight lanes of a head), l this lane's own part of its sum, o its outputs (high parts in elements 0
+// and 2, low parts in 1 and 3): tile j, rows g and g + 8, are elements 64 nb + 8 g + j and + 4.
+template <int NB, int NT>
+struct Q4State {
+  float m[NT], l[NT];
+  float o[NT][NB][4][4];
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt] = -INFINITY;
+      l[nt] = 0.f;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][nb][j][e] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void join_lanes() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      l[nt] += __shfl_xor_sync(kFull, l[nt], 4);
+      l[nt] += __shfl_xor_sync(kFull, l[nt], 8);
+      l[nt] += __shfl_xor_sync(kFull, l[nt], 16);
+    }
+  }
+  // outputs times f[nt] as rows [head][64 NB]
+  __device__ __forceinline__ void store(float* rows, const float (&f)[NT], int lane) const {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float4 v;
+          v.x = (o[nt][nb][0][2 * r] + o[nt][nb][0][2 * r + 1]) * f[nt];
+          v.y = (o[nt][nb][1][2 * r] + o[nt][nb][1][2 * r + 1]) * f[nt];
+          v.z = (o[nt][nb][2][2 * r] + o[nt][nb][2][2 * r + 1]) * f[nt];
+          v.w = (o[nt][nb][3][2 * r] + o[nt][nb][3][2 * r + 1]) * f[nt];
+          *reinterpret_cast<float4*>(rows + (4 * nt + t) * (NB * 64) + nb * 64 + 8 * g + 4 * r) = v;
+        }
+  }
+};
+
+// Adds 16 tokens: x[nt][u] are base-2 logits of head 4 nt + t and token (u, g) (-inf: not attended),
+// vs[nb][u] that token's value scales, vw[i][nb] word g of the codes of token (i / 2, 2t + i % 2). The
+// maximum moves only when a logit passes it by more than 2^8, so most units cost no shuffle and no
+// rescaling; weights stay below 2^8. kMasked: some tokens may not be attended.
+template <int NB, int NT, bool kMasked>
+__device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&x)[NT][2], const uint32_t (&vw)[4][NB],
+                                              const float (&vs)[NB][2]) {
+  bool grow = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) grow |= fmaxf(x[nt][0], x[nt][1]) > s.m[nt] + 8.f;
+  if (__any_sync(kFull, grow)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float mn = fmaxf(s.m[nt], fmaxf(x[nt][0], x[nt][1]));
+      mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 4));
+      mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 8));
+      mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 16));
+      const float f = s.m[nt] == mn ? 1.f : ex2(s.m[nt] - mn);
+      s.m[nt] = mn;
+      s.l[nt] *= f;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s.o[nt][nb][j][e] *= f;
+    }
+  }
+  uint32_t b[NT][NB][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool out = kMasked && x[nt][u] == -INFINITY;
+      const float p = out ? 0.f : ex2(x[nt][u] - s.m[nt]);
+      s.l[nt] += p;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        // a token that is not attended may lie in a slot never written: its scale is not used.
+        // high part by truncation to bf16, low part rounded: together within 2^-16
+        const float w = out ? 0.f : p * vs[nb][u];
+        const float hi = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
+        b[nt][nb][u] = movmatrix_trans(b2_bits(__floats2bfloat162_rn(hi, w - hi)));
+      }
+    }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
     const uint32_t ab0 = __byte_perm(vw[0][nb], vw[1][nb], 0x5410), ab1 = __byte_perm(vw[0][nb], vw[1][nb], 0x7632);
     const uint32_t cd0 = __byte_perm(vw[2][nb], vw[3][nb], 0x5410), cd1 = __byte_perm(vw[2][nb], vw[3][nb], 0x7632);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      mma_bf16(s.o[nb][j], a, q4_pair_bf16(ab0, j), q4_pair_bf16(cd0, j));
-      mma_bf16(s.o[nb][4 + j], a, q4_pair_bf16(ab1, j), q4_pair_bf16(cd1, j));
+      const uint32_t a[4] = {q4_pair_bf16(ab0, j), q4_pair_bf16(ab1, j), q4_pair_bf16(cd0, j), q4_pair_bf16(cd1, j)};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_bf16(s.o[nt][nb][j], a, b[nt][nb][0], b[nt][nb][1]);
     }
   }
 }
