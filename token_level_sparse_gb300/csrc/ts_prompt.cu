@@ -40,7 +40,11 @@ namespace {
 constexpr int kPrRows = 128;     // query rows of a tile
 constexpr int kPrKeys = 128;     // tokens of a key tile
 constexpr int kPrSoftmaxWarps = 8;
-constexpr int kPrThreads = (kPrSoftmaxWarps + 2) * 32;
+constexpr int kPrThreads = (kPrSoftmaxWarps + 4) * 32;   // three warpgroups; two warps of the third idle
+// Registers a thread: 168 at launch (65536 / 384); the softmax warpgroups hold a row of 128 scores and
+// take what the third gives up: 2 * 208 + 88 = 3 * 168.
+constexpr int kPrSoftmaxRegs = 208, kPrOtherRegs = 88;
+static_assert(2 * kPrSoftmaxRegs + kPrOtherRegs <= 3 * 168, "register shares");
 constexpr int kPrNone = 0x7fffffff;
 
 struct PromptArgs {
@@ -207,7 +211,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     const int ntiles = max(nt[0], nt[1]);
     const int masked_from = (i0 + 1) / kPrKeys;                   // tile j holds a key past token i0: 128 j + 127 > i0
 
-    if (warp == kPrSoftmaxWarps) {
+    if (warp >= kPrSoftmaxWarps) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrOtherRegs));
+      if (warp == kPrSoftmaxWarps) {
       // ---------------------------------------------------------------- loads
       if (lane == 0) {
         bool ok = true;
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         for (int j = max(0, vn - 2); j < vn; ++j) mbar_wait(&v_full[j & 1], (j >> 1) & 1, a.wait_ns);
       }
       __syncwarp();
-    } else if (warp == kPrSoftmaxWarps + 1) {
+      } else if (warp == kPrSoftmaxWarps + 1) {
       // ------------------------------------------------------------- products
       if (lane == 0) {
         const uint32_t idesc_s = idesc_bf16_f32(kPrRows, kPrKeys) | (a.negate ? 1u << 13 : 0u);   // bit 13: -A
@@ -289,7 +295,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         if (!ok) set_error(a.status, TS_ERR_TIMEOUT);
       }
       __syncwarp();
+      }
     } else if (nt[warp >> 2] > 0) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrSoftmaxRegs));
       // -------------------------------------------------------------- softmax
       const int i = warp >> 2;                                    // tile
       const int share = S::KT / (nt[1] > 0 ? kPrSoftmaxWarps : kPrSoftmaxWarps / 2);   // bytes of a value tile to look through
