@@ -153,10 +153,18 @@ def _row_stride(t):
     return t.stride(0) if t.shape[0] > 1 else heads * d
 
 
+def _current_stream():
+    """The raw handle of torch's current stream (without the Stream object, whose making takes microseconds)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
+
+
 def _s(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -263,7 +263,7 @@ bool q4_supported(const ts_config& c);
 int64_t q4_part_slots(const ts_config& c, int num_sms);
 // the whole cache (c.idx == null, seq_lens) or the listed tokens of 4-bit pools
 ts_status launch_attend_q4(ts_ctx* ctx, const AttendCall& c, const int32_t* seq_lens, cudaStream_t s);
-ts_status launch_score_q4(ts_ctx* ctx, const ScoreCall& c, cudaStream_t s);   // logits and stats
+ts_status launch_score_q4(ts_ctx* ctx, const ScoreCall& c, cudaStream_t s);   // logits; for the soft vote also the votes
 ts_status launch_append_q4(ts_ctx* ctx, const void* k_new, const void* v_new, const int32_t* page_table,
                            const int32_t* seq_lens, int B, void* k_pool, void* v_pool, cudaStream_t s);
 ts_status launch_append_prompt(ts_ctx* ctx, const AppendPromptCall& c, cudaStream_t s);

@@ -30,6 +30,7 @@ constexpr int kQ4Warps = 16;                    // of a scan CTA, one CTA per SM
 constexpr int kQ4Threads = kQ4Warps * 32;
 constexpr int kQ4Sets = 4;                      // head sets of a CTA, at most
 constexpr int kGatherWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct Q4Args {
   const float* q;                // [B][H][d]
@@ -46,10 +47,10 @@ struct Q4Args {
   int set_heads;                 // 4 or 8
   int n_groups;                  // groups of kQ4Sets head sets
   int ctas;                      // CTAs per group
-  float scale;
-  float* logits;                 // score: [B][H][max_tokens]
+  float scale;                   // base 2 (times log2 e), but natural for the scores that no softmax follows
+  float* logits;                 // score: [B][H][max_tokens], in units of scale
   float* part_o;                 // [slot][H][d]
-  float2* part_ml;               // [slot][H]: max and sum (base 2 for attention, natural for the score)
+  float2* part_ml;               // [slot][H]: max and sum of 2^(x - max)
   int* status;
 };
 
@@ -68,10 +69,7 @@ __device__ __forceinline__ int live_ctas(int64_t total, int ctas) {
 
 // Weight of a part with maximum m in a join with maximum M. Equal maxima weigh 1 also where both are
 // -inf: an empty part brings zeros, a part of NaN logits brings its NaN.
-template <bool kBase2>
-__device__ __forceinline__ float part_weight(float m, float M) {
-  return m == M ? 1.f : (kBase2 ? ex2(m - M) : expf(m - M));
-}
+__device__ __forceinline__ float part_weight(float m, float M) { return m == M ? 1.f : ex2(m - M); }
 
 // Total pages of the batch and of the sequences before `upto` (one warp; the same in every lane).
 __device__ __forceinline__ void count_pages(const Q4Args& a, int upto, int lane, int64_t& total, int64_t& before) {
@@ -113,17 +111,20 @@ __device__ __forceinline__ bool next_part(const Q4Args& a, Q4Range& r, int& b, i
   return false;
 }
 
-// Ring of one warp: blocks of K (and V) of this many pages. 16 warps x 6 x 2176 bytes in flight at
-// d = 128 are four times what one SM's share of HBM bandwidth needs to cover a microsecond.
+// Ring of one warp: stages of two pages' blocks of K (and V). 16 warps x 3 x 4352 bytes in flight at
+// d = 128 are four times what one SM's share of HBM bandwidth needs to cover a microsecond; two pages
+// share the cost of a wait and of a round of copies.
 template <int NB, int NT, bool kAttend>
 struct Q4Ring {
   static constexpr int BLK = q4_block_bytes(NB * 64);
-  static constexpr int STAGE = (kAttend ? 2 : 1) * BLK;
-  static constexpr int STAGES = 6;
+  static constexpr int OPS = kAttend ? 2 : 1;                      // blocks of a page
+  static constexpr int PAGES = 2;                                  // pages of a stage
+  static constexpr int STAGE = PAGES * OPS * BLK;                  // [page][K, V][block]
+  static constexpr int STAGES = kAttend ? 3 : 4;
   static constexpr int BYTES = STAGES * STAGE;                     // also holds [4 NT][d] floats at a join
   static constexpr int SMEM = kQ4Warps * BYTES;
   static_assert(!kAttend || BYTES >= 4 * NT * NB * 64 * 4, "the join's area");
-  static_assert(STAGE % 16 == 0, "bulk copies");
+  static_assert(BLK % 16 == 0, "bulk copies");
 };
 
 // kAttend: attention partials; otherwise logits and (max, sum exp) partials.
@@ -184,33 +185,37 @@ __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_consta
     float mul[NT];
     Q4State<NB, NT> st;                                            // (the score uses its m and l alone)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mul[nt] = a.scale * f.inv[nt] * (kAttend ? 1.4426950408889634f : 1.f);
+    for (int nt = 0; nt < NT; ++nt) mul[nt] = a.scale * f.inv[nt];
     st.reset();
     // this warp's pages: p0 + j, p0 + j + per_set, ...; lane i holds the id of the next 32 to copy
     const int32_t* pt = a.page_table + (size_t)b * a.pt_stride;
     const int mine = ok && p0 + j < p1 ? (p1 - p0 - j + per_set - 1) / per_set : 0;
-    int ids = 0, copied = 0, cs = 0;                               // pages copied so far, the next one's stage
-    uint32_t lost = 0u;                                            // bit s: stage s has no page
+    const int stages = (mine + R::PAGES - 1) / R::PAGES;
+    int ids = 0, copied = 0, cs = 0;                               // stages copied so far, the next one's slot
+    uint32_t lost = 0u;                                            // bits 2s, 2s + 1: pages of slot s that are not in the pool
     auto copy_next = [&]() {
-      if (copied >= mine) return;
-      if ((copied & 31) == 0) {
-        const int i = copied + lane;
+      if (copied >= stages) return;
+      const int in_ids = (copied * R::PAGES) & 31;
+      if (in_ids == 0) {
+        const int i = copied * R::PAGES + lane;
         ids = i < mine ? pt[p0 + j + i * per_set] : 0;
       }
-      const int page = __shfl_sync(kFull, ids, copied & 31);
-      const bool in = page >= 0 && (int64_t)page < a.num_pages;
-      lost = in ? lost & ~(1u << cs) : lost | (1u << cs);
-      if (lane == 0) {
-        if (in) {
-          unsigned char* dst = ring + cs * R::STAGE;
-          const size_t off = ((size_t)page * a.HKV + kv) * R::BLK;
-          mbar_arrive_expect_tx(&bars[cs], R::STAGE);
-          bulk_g2s(dst, a.k_pool + off, R::BLK, &bars[cs]);
-          if (kAttend) bulk_g2s(dst + R::BLK, a.v_pool + off, R::BLK, &bars[cs]);
-        } else {
-          set_error(a.status, TS_ERR_PAGE_OOB);
-          mbar_arrive(&bars[cs]);
-        }
+      // lane (page, operand) copies one block
+      const int which = lane / R::OPS;
+      const int page = __shfl_sync(kFull, ids, in_ids + (which & (R::PAGES - 1)));
+      const bool has = lane < R::PAGES * R::OPS && copied * R::PAGES + which < mine;
+      const bool in = has && page >= 0 && (int64_t)page < a.num_pages;
+      const unsigned good = __ballot_sync(kFull, in), bad = __ballot_sync(kFull, has && !in);
+      if (lane == 0) mbar_arrive_expect_tx(&bars[cs], (uint32_t)__popc(good) * R::BLK);
+      __syncwarp();
+      if (in) {
+        const unsigned char* pool = R::OPS == 2 && (lane & 1) ? a.v_pool : a.k_pool;
+        bulk_g2s(ring + cs * R::STAGE + lane * R::BLK, pool + ((size_t)page * a.HKV + kv) * R::BLK, R::BLK, &bars[cs]);
+      }
+      lost &= ~(3u << (2 * cs));
+      if (bad) {
+        lost |= ((bad & 1u) | ((bad >> R::OPS) & 1u) << 1) << (2 * cs);
+        if (lane == 0) set_error(a.status, TS_ERR_PAGE_OOB);
       }
       ++copied;
       cs = cs + 1 == R::STAGES ? 0 : cs + 1;
@@ -218,7 +223,10 @@ __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_consta
     for (int i = 0; i < R::STAGES; ++i) copy_next();
     int s = 0, left = n - (p0 + j) * kPage;                        // tokens of the sequence from this page on
     int done = 0;
-    for (; done < mine; ++done) {
+    // the place in the page of token (u, c): the attention wants lane t's value rows, tokens (u, 2t)
+    // and (u, 2t + 1), in different banks; the score wants neighbours for its stores
+    auto token = [&](int u, int c) { return kAttend ? 8 * u + 4 * (c & 1) + (c >> 1) : 8 * u + c; };
+    for (; done < stages; ++done) {
       ok = mbar_wait(&bars[s], (phases >> s) & 1u);
       ok = __all_sync(kFull, ok);
       if (!ok) {
@@ -226,69 +234,78 @@ __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_consta
         break;
       }
       phases ^= 1u << s;
-      const unsigned char* kb = ring + s * R::STAGE;
-      // the place in the page of token (u, c): the attention wants lane t's value rows, tokens (u, 2t)
-      // and (u, 2t + 1), in different banks; the score wants neighbours for its stores
-      auto token = [&](int u, int c) { return kAttend ? 8 * u + 4 * (c & 1) + (c >> 1) : 8 * u + c; };
-      uint2 kw[2][NB];
-      float ks[NB][2];
+      const int pages = min(R::PAGES, mine - done * R::PAGES);
+#pragma unroll 1
+      for (int pg = 0; pg < pages; ++pg) {
+        const unsigned char* kb = ring + s * R::STAGE + pg * (R::OPS * R::BLK);
+        const int limit = (lost >> (2 * s + pg)) & 1u ? 0 : left;
+        uint2 kw[2][NB];
+        float ks[NB][2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          kw[u][nb] = *reinterpret_cast<const uint2*>(kb + nb * 512 + token(u, g) * 32 + t * 8);
-          ks[nb][u] = bf16_bits_f(*reinterpret_cast<const uint16_t*>(kb + CODES + nb * 32 + token(u, g) * 2));
-        }
-      float x[NT][2];
-      q4_scores<NB, NT>(f, kw, ks, x);
-      const int limit = (lost >> s) & 1u ? 0 : left;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) x[nt][u] *= mul[nt];
-      if (limit < kPage) {
+          for (int u = 0; u < 2; ++u) {
+            kw[u][nb] = *reinterpret_cast<const uint2*>(kb + nb * 512 + token(u, g) * 32 + t * 8);
+            ks[nb][u] = bf16_bits_f(*reinterpret_cast<const uint16_t*>(kb + CODES + nb * 32 + token(u, g) * 2));
+          }
+        float x[NT][2];
+        q4_scores<NB, NT>(f, kw, ks, x);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) x[nt][u] = token(u, g) < limit ? x[nt][u] : -INFINITY;
-      }
-      if constexpr (kAttend) {
-        const unsigned char* vb = kb + R::BLK;
-        uint32_t vw[4][NB];
-        float vs[NB][2];
+          for (int u = 0; u < 2; ++u) x[nt][u] *= mul[nt];
+        if (limit < kPage) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            vw[e][nb] = *reinterpret_cast<const uint32_t*>(vb + nb * 512 + token(e >> 1, 2 * t + (e & 1)) * 32 + g * 4);
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            vs[nb][u] = bf16_bits_f(*reinterpret_cast<const uint16_t*>(vb + CODES + nb * 32 + token(u, g) * 2));
+            for (int u = 0; u < 2; ++u) x[nt][u] = token(u, g) < limit ? x[nt][u] : -INFINITY;
         }
-        __syncwarp();                                              // every lane has read the stage
-        copy_next();
-        if (limit < kPage)
-          q4_accumulate<NB, NT, true>(st, x, vw, vs);
-        else
-          q4_accumulate<NB, NT, false>(st, x, vw, vs);
-      } else {
-        __syncwarp();
-        copy_next();
+        if constexpr (kAttend) {
+          const unsigned char* vb = kb + R::BLK;
+          uint32_t vw[4][NB];
+          float vs[NB][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float mn = fmaxf(st.m[nt], fmaxf(x[nt][0], x[nt][1]));
-          st.l[nt] *= st.m[nt] == mn ? 1.f : expf(st.m[nt] - mn);
+          for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) st.l[nt] += x[nt][u] == -INFINITY ? 0.f : expf(x[nt][u] - mn);
-          st.m[nt] = mn;
-          if (4 * nt + t < nh) {
-            float* row = a.logits + ((size_t)b * a.H + head0 + 4 * nt + t) * a.max_tokens + (n - left) + g;
-            row[0] = x[nt][0];
-            row[8] = x[nt][1];
+            for (int e = 0; e < 4; ++e)
+              vw[e][nb] = *reinterpret_cast<const uint32_t*>(vb + nb * 512 + token(e >> 1, 2 * t + (e & 1)) * 32 + g * 4);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              vs[nb][u] = bf16_bits_f(*reinterpret_cast<const uint16_t*>(vb + CODES + nb * 32 + token(u, g) * 2));
+          }
+          if (pg == pages - 1) {
+            __syncwarp();                                          // every lane has read the stage
+            copy_next();
+          }
+          if (limit < kPage)
+            q4_accumulate<NB, NT, true>(st, x, vw, vs);
+          else
+            q4_accumulate<NB, NT, false>(st, x, vw, vs);
+        } else {
+          if (pg == pages - 1) {
+            __syncwarp();
+            copy_next();
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            // each lane keeps a maximum of its own tokens, moved as in the attention
+            const float mx = fmaxf(x[nt][0], x[nt][1]);
+            if (mx > st.m[nt] + 8.f) {
+              st.l[nt] *= ex2(st.m[nt] - mx);
+              st.m[nt] = mx;
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              st.l[nt] += limit < kPage && x[nt][u] == -INFINITY ? 0.f : ex2(x[nt][u] - st.m[nt]);
+            if (4 * nt + t < nh) {
+              float* row = a.logits + ((size_t)b * a.H + head0 + 4 * nt + t) * a.max_tokens + (n - left) + g;
+              row[0] = x[nt][0];
+              row[8] = x[nt][1];
+            }
           }
         }
+        left -= per_set * kPage;
       }
-      left -= per_set * kPage;
       s = s + 1 == R::STAGES ? 0 : s + 1;
     }
     if (!ok && works) {
@@ -306,7 +323,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_consta
         float mn = fmaxf(st.m[nt], __shfl_xor_sync(kFull, st.m[nt], 4));
         mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 8));
         mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 16));
-        st.l[nt] *= part_weight<false>(st.m[nt], mn);
+        st.l[nt] *= part_weight(st.m[nt], mn);
         st.m[nt] = mn;
       }
     }
@@ -323,9 +340,9 @@ __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_consta
       for (int w = 0; w < (works ? per_set : 0); ++w) M = fmaxf(M, s_ml[hs * per_set + w][4 * nt + t].x);
       for (int w = 0; w < (works ? per_set : 0); ++w) {
         const float2 ml = s_ml[hs * per_set + w][4 * nt + t];
-        L += ml.y * part_weight<kAttend>(ml.x, M);
+        L += ml.y * part_weight(ml.x, M);
       }
-      fac[nt] = part_weight<kAttend>(st.m[nt], M);
+      fac[nt] = part_weight(st.m[nt], M);
       if (works && j == 0 && g == 0 && 4 * nt + t < nh)
         a.part_ml[(int64_t)(cta + b) * a.H + head0 + 4 * nt + t] = make_float2(M, L);
     }
@@ -387,35 +404,61 @@ __global__ void __launch_bounds__(1024) q4_merge_kernel(const __grid_constant__ 
   const float* po = a.part_o + (first * a.H + h) * D + e;
 #pragma unroll 4
   for (int i = row; i < count; i += ROWS)
-    o = fmaf(part_weight<true>(s_ml[i].x, M), __ldcg(po + (size_t)i * a.H * D), o);
+    o = fmaf(part_weight(s_ml[i].x, M), __ldcg(po + (size_t)i * a.H * D), o);
   s_o[row][e] = o;
   __syncthreads();
   if (row != 0) return;
   float O = 0.f, L = 0.f;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) O += s_o[i][e];
-  for (int i = 0; i < count; ++i) L = fmaf(part_weight<true>(s_ml[i].x, M), s_ml[i].y, L);
+  for (int i = 0; i < count; ++i) L = fmaf(part_weight(s_ml[i].x, M), s_ml[i].y, L);
   const bool some = L != 0.f;   // true for NaN: a NaN among the rows is not an empty sequence
   out[((size_t)b * a.H + h) * D + e] = some ? O / L : 0.f;
   if (lse && e == 0) lse[(size_t)b * a.H + h] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
-// (max, 1 / sum) of each head over the whole sequence, from the scan's parts.
-__global__ void q4_stats_kernel(const __grid_constant__ Q4Args a, float2* stats) {
-  const int b = blockIdx.x;
-  int64_t first;
-  int count;
-  scan_slots(a, b, threadIdx.x & 31, first, count);
-  for (int h = threadIdx.x; h < a.H; h += blockDim.x) {
-    const float2* ml = a.part_ml + first * a.H + h;
-    float M = -INFINITY;
-    for (int i = 0; i < count; ++i) M = fmaxf(M, ml[(size_t)i * a.H].x);
-    KahanF z;
-    for (int i = 0; i < count; ++i) {
-      const float2 x = ml[(size_t)i * a.H];
-      z.add(x.y * part_weight<false>(x.x, M));
+// The head soft vote from the scan's base-2 logits and parts: v_i = sum_h 2^(l_hi - M_h) / Z_h. Like the
+// scan, a CTA takes an even, contiguous share of the batch's pages; for each sequence in it its warps
+// first join the heads' parts (the same in every CTA), then a thread sums the heads of a token,
+// compensated. Reads the logits (written by the scan, in L2 up to about 100 MB) once.
+constexpr int kVoteThreads = 512;
+constexpr int kVoteHeads = 256;
+
+__global__ void __launch_bounds__(kVoteThreads) q4_vote_kernel(const __grid_constant__ Q4Args a, float* vote,
+                                                               int64_t vote_stride) {
+  __shared__ float2 s_mz[kVoteHeads];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int64_t total, before;
+  count_pages(a, 0, lane, total, before);
+  Q4Range r{total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x, 0, 0};
+  int b, p0, p1;
+  while (next_part(a, r, b, p0, p1)) {
+    const int n = a.seq_lens[b];
+    int64_t first;
+    int count;
+    scan_slots(a, b, lane, first, count);
+    __syncthreads();                               // the last sequence's statistics are done with
+    for (int h = warp; h < a.H; h += kVoteThreads / 32) {
+      const float2* ml = a.part_ml + first * a.H + h;
+      float M = -INFINITY;
+      for (int i = lane; i < count; i += 32) M = fmaxf(M, __ldcg(&ml[(size_t)i * a.H].x));
+      M = warp_max(M);
+      KahanF z;
+      for (int i = lane; i < count; i += 32) {
+        const float2 x = __ldcg(&ml[(size_t)i * a.H]);
+        z.add(x.y * part_weight(x.x, M));
+      }
+      const float Z = warp_sum_comp(z.s, -z.c);
+      if (lane == 0) s_mz[h] = make_float2(M, 1.f / Z);
     }
-    stats[(size_t)b * a.H + h] = make_float2(M, 1.f / (z.s - z.c));
+    __syncthreads();
+    const float* lb = a.logits + (size_t)b * a.H * a.max_tokens;
+    for (int i = p0 * kPage + tid; i < min(n, p1 * kPage); i += kVoteThreads) {
+      KahanF acc;
+#pragma unroll 8
+      for (int h = 0; h < a.H; ++h) acc.add(ex2(__ldcg(lb + (size_t)h * a.max_tokens + i) - s_mz[h].x) * s_mz[h].y);
+      vote[(size_t)b * vote_stride + i] = acc.s - acc.c;
+    }
   }
 }
 
@@ -448,7 +491,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
   float mul[NT], one[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    mul[nt] = a.scale * f.inv[nt] * 1.4426950408889634f;
+    mul[nt] = a.scale * f.inv[nt];
     one[nt] = 1.f;
   }
   Q4State<NB, NT> st;
@@ -515,7 +558,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
     for (int w = 0; w < kGatherWarps; ++w) M = fmaxf(M, s_ml[w][hg].x);
 #pragma unroll
     for (int w = 0; w < kGatherWarps; ++w) {
-      const float wt = part_weight<true>(s_ml[w][hg].x, M);
+      const float wt = part_weight(s_ml[w][hg].x, M);
       L = fmaf(wt, s_ml[w][hg].y, L);
       O = fmaf(wt, merge[w][hg][i % D], O);
     }
@@ -569,9 +612,8 @@ ts_status run_scan(ts_ctx* ctx, const Q4Args& a, cudaStream_t s) {
   constexpr size_t smem = Q4Ring<NB, NT, false>::SMEM;
   if (!ensure_smem<scan_kernel<NB, NT, false>>(smem, ctx->device)) return TS_ERR_CUDA;
   ProfScope ps(ctx, TS_PROF_SCORE, s);
-  ctx->kernels += 2;
+  ctx->kernels += 1;
   scan_kernel<NB, NT, false><<<a.ctas * a.n_groups, kQ4Threads, smem, s>>>(a);
-  q4_stats_kernel<<<a.B, 256, 0, s>>>(a, ctx->stats);
   return cuda_status(cudaGetLastError());
 }
 
@@ -601,7 +643,7 @@ bool q4_supported(const ts_config& c) {
 int64_t q4_part_slots(const ts_config& c, int num_sms) { return 2 * (int64_t)num_sms + c.max_batch; }
 
 ts_status launch_attend_q4(ts_ctx* ctx, const AttendCall& c, const int32_t* seq_lens, cudaStream_t s) {
-  Q4Args a = make_args(ctx, c.q, c.k_pool, c.v_pool, c.page_table, seq_lens, c.B, c.scale);
+  Q4Args a = make_args(ctx, c.q, c.k_pool, c.v_pool, c.page_table, seq_lens, c.B, c.scale * kLog2e);
   if (!c.idx) return TS_Q4_DISPATCH(run_attend, ctx, a, c.out, c.lse, s);
   const int sets = a.HKV * a.sets_per_kv * a.B;
   const int splits = std::max(1, std::min((2 * ctx->num_sms + sets - 1) / sets, kAttnMaxSplits));
@@ -610,9 +652,15 @@ ts_status launch_attend_q4(ts_ctx* ctx, const AttendCall& c, const int32_t* seq_
 }
 
 ts_status launch_score_q4(ts_ctx* ctx, const ScoreCall& c, cudaStream_t s) {
-  Q4Args a = make_args(ctx, c.q, c.k_pool, nullptr, c.page_table, c.seq_lens, c.B, c.scale);
+  const bool soft = c.fn == TS_SCORE_HEAD_SOFT_VOTE;
+  Q4Args a = make_args(ctx, c.q, c.k_pool, nullptr, c.page_table, c.seq_lens, c.B, soft ? c.scale * kLog2e : c.scale);
   a.skip = c.skip;
-  return TS_Q4_DISPATCH(run_scan, ctx, a, s);
+  const ts_status st = TS_Q4_DISPATCH(run_scan, ctx, a, s);
+  if (st != TS_OK || !soft) return st;   // the other selection functions rank the natural logits themselves
+  ProfScope ps(ctx, TS_PROF_VOTE, s);
+  ctx->kernels += 1;
+  q4_vote_kernel<<<2 * ctx->num_sms, kVoteThreads, 0, s>>>(a, c.vote, c.vote_stride);
+  return cuda_status(cudaGetLastError());
 }
 
 }  // namespace ts

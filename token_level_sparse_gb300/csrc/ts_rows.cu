@@ -98,9 +98,17 @@ __global__ void __launch_bounds__(kRowsThreads) append_rows_kernel(const __grid_
 }
 
 // 4-bit pools. Eight lanes quantise one group of 64 elements: scale = bf16(max|x| / 7), code =
-// 8 + round(x / scale) with ties to even (both divisions correctly rounded, so that every
-// implementation of the formula gives the same bits). A scale of zero gives zeros; a group with a
-// NaN or an infinity reads back as NaN: its scale is not finite and its codes stand for zero.
+// 8 + round(x / scale), ties to even. A scale of zero gives zeros; a group with a NaN or an infinity
+// reads back as NaN: its scale is not finite and its codes stand for zero.
+//
+// The bits are those of exact arithmetic, without a division: x and the scale s have 8 significant bits
+// each, so a quotient that is not halfway between two codes is at least 2^-9 away from it (numerator
+// and denominator of the difference are whole numbers below 2^9 of one unit), and likewise max|x| / 7
+// lies 2^-12 away from any midpoint of bf16. A product with 1/7 that is right to 2^-22 therefore rounds
+// to the right scale. A quotient x r, r near 1/s, is off by a few units in the last place: its residual
+// x - q s is exact in one fused multiply-add, and q + residual r (Markstein's correction) is the exact
+// quotient where that has few bits, as it has halfway between codes. Scales near or below the smallest
+// normal number have fewer bits and take the divisions instead.
 __global__ void __launch_bounds__(kRowsThreads) append_q4_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ int64_t place[kRowsPerCta];
   place_rows(a, place);
@@ -126,14 +134,28 @@ __global__ void __launch_bounds__(kRowsThreads) append_q4_kernel(const __grid_co
     const unsigned peers = 0xffu << (threadIdx.x & 24);
 #pragma unroll
     for (int d = 4; d >= 1; d >>= 1) mb = max(mb, __shfl_xor_sync(peers, mb, d));
-    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(mb), 7.f));
-    const float s = __bfloat162float(sb);
-    const bool live = s > 0.f && s < INFINITY;
+    const float top = __uint_as_float(mb);
+    __nv_bfloat16 sb;
     uint32_t w = 0u;
+    if (top >= 0x1p-100f && top < INFINITY) {
+      sb = __float2bfloat16_rn(top * (1.f / 7.f));
+      const float s = __bfloat162float(sb), r = __frcp_rn(s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int q = live ? max(-7, min(7, __float2int_rn(__fdiv_rn(x[e], s)))) : 0;
-      w |= (uint32_t)(q + 8) << (4 * e);
+      for (int e = 0; e < 8; ++e) {
+        float q = x[e] * r;
+        q = fmaf(fmaf(-q, s, x[e]), r, q);
+        // rounds to a whole number, 8 + code in the low bits: |q| < 7.1, since s >= top / 7 (1 - 2^-8)
+        w |= (__float_as_uint(q + 12582920.f) & 15u) << (4 * e);
+      }
+    } else {
+      sb = __float2bfloat16_rn(__fdiv_rn(top, 7.f));
+      const float s = __bfloat162float(sb);
+      const bool live = s > 0.f && s < INFINITY;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int q = live ? max(-7, min(7, __float2int_rn(__fdiv_rn(x[e], s)))) : 0;
+        w |= (uint32_t)(q + 8) << (4 * e);
+      }
     }
     if (at >= 0) {
       unsigned char* base = a.pool[isv] + ((at >> 4) * a.HKV + g) * blk;

@@ -502,7 +502,7 @@ ts_status launch_score(ts_ctx* ctx, const ScoreCall& a, cudaStream_t s) {
   const int G = c.n_q_heads / c.n_kv_heads;
   if (c.kv_dtype == TS_KV_Q4) {
     const ts_status st = launch_score_q4(ctx, a, s);
-    return st == TS_OK ? run_votes(ctx, a, s) : st;
+    return st == TS_OK && a.fn != TS_SCORE_HEAD_SOFT_VOTE ? run_votes(ctx, a, s) : st;   // the soft vote is done
   }
 #define X(DT, T, D_, HKV_, G_) \
   if (c.kv_dtype == DT && c.head_dim == D_ && c.n_kv_heads == HKV_ && G == G_) return run_score<T, D_, HKV_, G_>(ctx, a, s);
