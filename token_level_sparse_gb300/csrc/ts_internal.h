@@ -70,7 +70,7 @@ struct ts_ctx {
   int32_t* blk_idx = nullptr;            // [max_batch][max_tokens] selected blocks, then [max_batch] counts
   int32_t* sel_rows = nullptr;           // persistent kernel: per CTA, its selected tokens [kStepFlagCap]
   float* q4_part_o = nullptr;            // 4-bit pools: attention parts [slots][H][d], q4_part_slots
-  float2* q4_part_ml = nullptr;          // ... and their (max, sum), also the score's [slots][H]
+  float2* q4_part_ml = nullptr;          // ... and their (max, sum), also the score's [H][slots]
   int64_t kernels = 0;           // kernel launches issued
   // persistent decode-step kernel
   int step_grid = 0;                     // CTAs of the cooperative launch (0: not yet sized)

@@ -8,7 +8,7 @@
 // are unpacked in registers (9 instructions for 8 codes) and multiplied on the tensor cores.
 //
 // scan_kernel (whole sequences): a CTA owns a group of up to 4 head sets (a head set: up to 4 query
-// heads of one KV head, or up to 8 where there are more than 4 to a KV head) and an even share of all pages of the batch, as one contiguous range. Its 16
+// heads of one KV head, or up to 8 where there are more than 4 to a KV head) and an even share of all pages of the batch, as one contiguous range. Its
 // warps are shared out over the head sets and take the pages in turn, each with a ring of blocks of
 // its own in shared memory that it fills with bulk copies several pages ahead: no warp waits for
 // another one inside a sequence. At the end of a sequence's part of the range the warps of a head
@@ -19,6 +19,7 @@
 // is split over CTAs and joined by the same merge.
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "ts_q4.cuh"
 #include "ts_tc.cuh"
@@ -26,8 +27,6 @@
 namespace ts {
 namespace {
 
-constexpr int kQ4Warps = 16;                    // of a scan CTA, one CTA per SM
-constexpr int kQ4Threads = kQ4Warps * 32;
 constexpr int kQ4Sets = 4;                      // head sets of a CTA, at most
 constexpr int kGatherWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -48,11 +47,18 @@ struct Q4Args {
   int n_groups;                  // groups of kQ4Sets head sets
   int ctas;                      // CTAs per group
   float scale;                   // base 2 (times log2 e), but natural for the scores that no softmax follows
-  float* logits;                 // score: [B][H][max_tokens], in units of scale
+  float* logits;                 // score, in units of scale: H max_tokens to a sequence, head h of token i at
+  int64_t head_stride, page_stride;   // h head_stride + i / 16 page_stride + i % 16
   float* part_o;                 // [slot][H][d]
-  float2* part_ml;               // [slot][H]: max and sum of 2^(x - max)
+  float2* part_ml;               // [H][slots]: max and sum of 2^(x - max)
+  int64_t slots;
   int* status;
 };
+
+// Programmatic dependent launch: the scan lets the kernel behind it start its own set-up as SMs become
+// free, and that kernel waits for the scan's results (and all that came before) where it needs them.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ int seq_pages(const Q4Args& a, int b) {
   if (a.skip && a.skip[b]) return 0;
@@ -111,36 +117,43 @@ __device__ __forceinline__ bool next_part(const Q4Args& a, Q4Range& r, int& b, i
   return false;
 }
 
-// Ring of one warp: stages of two pages' blocks of K (and V). 16 warps x 3 x 4352 bytes in flight at
-// d = 128 are four times what one SM's share of HBM bandwidth needs to cover a microsecond; two pages
-// share the cost of a wait and of a round of copies.
+// Shape of a scan CTA (one per SM). As many warps as the registers of one lane's state allow: with 16
+// warps of the score the issue slots were 64% busy. Each warp's ring has stages of two pages' blocks of
+// K (and V), which share the cost of a wait and of a round of copies; a stage in flight per warp is
+// twice what one SM's share of HBM bandwidth needs to cover a microsecond.
 template <int NB, int NT, bool kAttend>
 struct Q4Ring {
+  static constexpr int WARPS = kAttend ? (NT == 1 ? 20 : 16) : 24;
   static constexpr int BLK = q4_block_bytes(NB * 64);
   static constexpr int OPS = kAttend ? 2 : 1;                      // blocks of a page
   static constexpr int PAGES = 2;                                  // pages of a stage
   static constexpr int STAGE = PAGES * OPS * BLK;                  // [page][K, V][block]
-  static constexpr int STAGES = kAttend ? 3 : 4;
+  static constexpr int STAGES = kAttend ? (NT == 1 ? 2 : 3) : 4;
   static constexpr int BYTES = STAGES * STAGE;                     // also holds [4 NT][d] floats at a join
-  static constexpr int SMEM = kQ4Warps * BYTES;
+  static constexpr int QUERY = kQ4Sets * 4 * NT * NB * 64 * 4;     // the CTA's queries, behind the rings
+  static constexpr int SMEM = WARPS * BYTES + QUERY;
+  static_assert(SMEM + 4096 <= 227 * 1024, "shared memory of an SM");
   static_assert(!kAttend || BYTES >= 4 * NT * NB * 64 * 4, "the join's area");
   static_assert(BLK % 16 == 0, "bulk copies");
 };
 
 // kAttend: attention partials; otherwise logits and (max, sum exp) partials.
 template <int NB, int NT, bool kAttend>
-__global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_constant__ Q4Args a) {
+__global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_kernel(const __grid_constant__ Q4Args a) {
   using R = Q4Ring<NB, NT, kAttend>;
   constexpr int D = NB * 64, CODES = q4_code_bytes(D);
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ __align__(8) uint64_t full[kQ4Warps][R::STAGES];
-  __shared__ float2 s_ml[kQ4Warps][4 * NT];
+  __shared__ __align__(8) uint64_t full[R::WARPS][R::STAGES];
+  __shared__ float2 s_ml[R::WARPS][4 * NT];
   __shared__ Q4Range s_range;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  // (values that are the same in a whole warp pass through a shuffle where they steer loops, so that
+  // the compiler knows and needs no divergence handling there)
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = blockIdx.x % a.n_groups, cta = blockIdx.x / a.n_groups;
   const int set0 = group * kQ4Sets, nsets = min(kQ4Sets, a.HKV * a.sets_per_kv - set0);
-  const int per_set = kQ4Warps / nsets;                            // 3 head sets: one warp is left over
+  const int per_set = R::WARPS / nsets;                            // (some warps may be left over)
+  launch_dependents();
 
   if (warp == 0) {
     // this CTA's pages of the batch
@@ -174,61 +187,83 @@ __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_consta
   const int kv = set / a.sets_per_kv, head0 = kv * a.G + (set % a.sets_per_kv) * (4 * NT);
   const int nh = min(4 * NT, a.G - (set % a.sets_per_kv) * (4 * NT));   // heads of this set
   unsigned char* ring = smem + (size_t)warp * R::BYTES;
+  float* sq = reinterpret_cast<float*>(smem + R::WARPS * R::BYTES);   // [sets][4 NT][D]
   uint64_t* bars = full[warp];
   uint32_t phases = 0u;                                            // bit s: parity of the stage's next wait
   bool ok = works;
   int b, p0, p1;
   while (next_part(a, r, b, p0, p1)) {
-    const int n = a.seq_lens[b];
-    Q4Query<NB, NT> f;
-    q4_load_query<NB, NT>(f, a.q + ((size_t)b * a.H + head0) * D, nh, lane);
-    float mul[NT];
-    Q4State<NB, NT> st;                                            // (the score uses its m and l alone)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mul[nt] = a.scale * f.inv[nt];
-    st.reset();
+    b = __shfl_sync(kFull, b, 0);
+    p0 = __shfl_sync(kFull, p0, 0);
+    p1 = __shfl_sync(kFull, p1, 0);
+    const int n = __shfl_sync(kFull, a.seq_lens[b], 0);
     // this warp's pages: p0 + j, p0 + j + per_set, ...; lane i holds the id of the next 32 to copy
     const int32_t* pt = a.page_table + (size_t)b * a.pt_stride;
     const int mine = ok && p0 + j < p1 ? (p1 - p0 - j + per_set - 1) / per_set : 0;
     const int stages = (mine + R::PAGES - 1) / R::PAGES;
     int ids = 0, copied = 0, cs = 0;                               // stages copied so far, the next one's slot
-    uint32_t lost = 0u;                                            // bits 2s, 2s + 1: pages of slot s that are not in the pool
+    uint32_t lost = 0u;                                            // bits 2s, 2s + 1: pages of slot s without a block
+    // lane (page, operand) copies one block. The score's blocks are streamed through L2 (evict first): its
+    // logits are read again by the votes and should stay there
+    const unsigned char* pool = R::OPS == 2 && (lane & 1) ? a.v_pool : a.k_pool;
+    const uint64_t policy = l2_evict_first_policy();
     auto copy_next = [&]() {
       if (copied >= stages) return;
       const int in_ids = (copied * R::PAGES) & 31;
       if (in_ids == 0) {
         const int i = copied * R::PAGES + lane;
-        ids = i < mine ? pt[p0 + j + i * per_set] : 0;
+        ids = -1;
+        if (i < mine) {
+          ids = pt[p0 + j + i * per_set];
+          if (ids < 0 || (int64_t)ids >= a.num_pages) {
+            set_error(a.status, TS_ERR_PAGE_OOB);
+            ids = -1;
+          }
+        }
       }
-      // lane (page, operand) copies one block
-      const int which = lane / R::OPS;
-      const int page = __shfl_sync(kFull, ids, in_ids + (which & (R::PAGES - 1)));
-      const bool has = lane < R::PAGES * R::OPS && copied * R::PAGES + which < mine;
-      const bool in = has && page >= 0 && (int64_t)page < a.num_pages;
-      const unsigned good = __ballot_sync(kFull, in), bad = __ballot_sync(kFull, has && !in);
+      const int page = __shfl_sync(kFull, ids, in_ids + (lane / R::OPS & (R::PAGES - 1)));
+      const bool in = lane < R::PAGES * R::OPS && page >= 0;       // (pages past the last one have no id)
+      const unsigned good = __ballot_sync(kFull, in);
       if (lane == 0) mbar_arrive_expect_tx(&bars[cs], (uint32_t)__popc(good) * R::BLK);
       __syncwarp();
       if (in) {
-        const unsigned char* pool = R::OPS == 2 && (lane & 1) ? a.v_pool : a.k_pool;
-        bulk_g2s(ring + cs * R::STAGE + lane * R::BLK, pool + ((size_t)page * a.HKV + kv) * R::BLK, R::BLK, &bars[cs]);
+        const unsigned char* src = pool + ((size_t)page * a.HKV + kv) * R::BLK;
+        if (kAttend)
+          bulk_g2s(ring + cs * R::STAGE + lane * R::BLK, src, R::BLK, &bars[cs]);
+        else
+          bulk_g2s_hint(ring + cs * R::STAGE + lane * R::BLK, src, R::BLK, &bars[cs], policy);
       }
-      lost &= ~(3u << (2 * cs));
-      if (bad) {
-        lost |= ((bad & 1u) | ((bad >> R::OPS) & 1u) << 1) << (2 * cs);
-        if (lane == 0) set_error(a.status, TS_ERR_PAGE_OOB);
-      }
+      const unsigned pages = R::OPS == 1 ? good : ((good & 1u) | (good >> 1 & 2u));
+      lost = (lost & ~(3u << (2 * cs))) | ((~pages & 3u) << (2 * cs));
       ++copied;
       cs = cs + 1 == R::STAGES ? 0 : cs + 1;
     };
     for (int i = 0; i < R::STAGES; ++i) copy_next();
+    // the queries of all head sets, once for the CTA, while the first blocks are on their way
+    for (int i = tid; i < nsets * 4 * NT * D; i += R::WARPS * 32) {
+      const int e = i % D, h = i / D, in_set = h % (4 * NT), gs = set0 + h / (4 * NT);
+      const int in_kv = gs % a.sets_per_kv * (4 * NT) + in_set;
+      sq[i] = in_kv < a.G ? a.q[((size_t)b * a.H + gs / a.sets_per_kv * a.G + in_kv) * D + e] : 0.f;
+    }
+    __syncthreads();
+    Q4Query<NB, NT> f;
+    q4_load_query<NB, NT>(f, sq + (works ? hs : 0) * (4 * NT * D), lane);
+    float mul[NT];
+    Q4State<NB, NT> st;                                            // (the score uses its m and l alone)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mul[nt] = a.scale * f.inv[nt];
+    st.reset();
     int s = 0, left = n - (p0 + j) * kPage;                        // tokens of the sequence from this page on
     int done = 0;
     // the place in the page of token (u, c): the attention wants lane t's value rows, tokens (u, 2t)
     // and (u, 2t + 1), in different banks; the score wants neighbours for its stores
     auto token = [&](int u, int c) { return kAttend ? 8 * u + 4 * (c & 1) + (c >> 1) : 8 * u + c; };
+    // where this lane's logits go, for head t of the set; 4 heads on for the next tile of heads
+    float* row = a.logits + (size_t)b * a.H * a.max_tokens + (size_t)(head0 + t) * a.head_stride +
+                 (size_t)(p0 + j) * a.page_stride + g;
+    const size_t row_step = (size_t)per_set * a.page_stride, tile_step = (size_t)4 * a.head_stride;
     for (; done < stages; ++done) {
-      ok = mbar_wait(&bars[s], (phases >> s) & 1u);
-      ok = __all_sync(kFull, ok);
+      ok = __all_sync(kFull, mbar_wait(&bars[s], (phases >> s) & 1u));
       if (!ok) {
         set_error(a.status, TS_ERR_TIMEOUT);
         break;
@@ -286,23 +321,32 @@ __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_consta
             __syncwarp();
             copy_next();
           }
+          // each lane keeps a maximum of its own tokens, moved as in the attention
+          bool grow = false;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            // each lane keeps a maximum of its own tokens, moved as in the attention
-            const float mx = fmaxf(x[nt][0], x[nt][1]);
-            if (mx > st.m[nt] + 8.f) {
-              st.l[nt] *= ex2(st.m[nt] - mx);
-              st.m[nt] = mx;
-            }
+          for (int nt = 0; nt < NT; ++nt) grow |= fmaxf(x[nt][0], x[nt][1]) > st.m[nt] + 8.f;
+          if (__any_sync(kFull, grow)) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-              st.l[nt] += limit < kPage && x[nt][u] == -INFINITY ? 0.f : ex2(x[nt][u] - st.m[nt]);
-            if (4 * nt + t < nh) {
-              float* row = a.logits + ((size_t)b * a.H + head0 + 4 * nt + t) * a.max_tokens + (n - left) + g;
-              row[0] = x[nt][0];
-              row[8] = x[nt][1];
+            for (int nt = 0; nt < NT; ++nt) {
+              const float mn = fmaxf(st.m[nt], fmaxf(x[nt][0], x[nt][1]));
+              st.l[nt] *= part_weight(st.m[nt], mn);
+              st.m[nt] = mn;
             }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float e0 = ex2(x[nt][0] - st.m[nt]), e1 = ex2(x[nt][1] - st.m[nt]);
+            if (limit < kPage) {                                   // no token there: no weight (not 2^(-inf + inf))
+              e0 = x[nt][0] == -INFINITY ? 0.f : e0;
+              e1 = x[nt][1] == -INFINITY ? 0.f : e1;
+            }
+            st.l[nt] += e0 + e1;
+            if (4 * nt + t < nh) {
+              row[nt * tile_step] = x[nt][0];
+              row[nt * tile_step + 8] = x[nt][1];
+            }
+          }
+          row += row_step;
         }
         left -= per_set * kPage;
       }
@@ -344,7 +388,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) scan_kernel(const __grid_consta
       }
       fac[nt] = part_weight(st.m[nt], M);
       if (works && j == 0 && g == 0 && 4 * nt + t < nh)
-        a.part_ml[(int64_t)(cta + b) * a.H + head0 + 4 * nt + t] = make_float2(M, L);
+        a.part_ml[(int64_t)(head0 + 4 * nt + t) * a.slots + cta + b] = make_float2(M, L);
     }
     if constexpr (kAttend) {
       if (works) st.store(reinterpret_cast<float*>(ring), fac, lane);
@@ -396,15 +440,21 @@ __global__ void __launch_bounds__(1024) q4_merge_kernel(const __grid_constant__ 
   } else {
     scan_slots(a, b, tid & 31, first, count);
   }
-  for (int i = tid; i < count; i += blockDim.x) s_ml[i] = __ldcg(a.part_ml + (first + i) * a.H + h);
+  wait_for_primary();
+  for (int i = tid; i < count; i += blockDim.x) s_ml[i] = __ldcg(a.part_ml + h * a.slots + first + i);
   __syncthreads();
   float M = -INFINITY;
   for (int i = 0; i < count; ++i) M = fmaxf(M, s_ml[i].x);
   float o = 0.f;
   const float* po = a.part_o + (first * a.H + h) * D + e;
-#pragma unroll 4
-  for (int i = row; i < count; i += ROWS)
-    o = fmaf(part_weight(s_ml[i].x, M), __ldcg(po + (size_t)i * a.H * D), o);
+  for (int i0 = row; i0 < count; i0 += 8 * ROWS) {                 // eight loads under way at once
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = i0 + k * ROWS < count ? __ldcg(po + (size_t)(i0 + k * ROWS) * a.H * D) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k * ROWS < count) o = fmaf(part_weight(s_ml[i0 + k * ROWS].x, M), x[k], o);
+  }
   s_o[row][e] = o;
   __syncthreads();
   if (row != 0) return;
@@ -419,19 +469,23 @@ __global__ void __launch_bounds__(1024) q4_merge_kernel(const __grid_constant__ 
 
 // The head soft vote from the scan's base-2 logits and parts: v_i = sum_h 2^(l_hi - M_h) / Z_h. Like the
 // scan, a CTA takes an even, contiguous share of the batch's pages; for each sequence in it its warps
-// first join the heads' parts (the same in every CTA), then a thread sums the heads of a token,
-// compensated. Reads the logits (written by the scan, in L2 up to about 100 MB) once.
+// first join the heads' parts (the same in every CTA), then a thread sums a quarter of the heads of
+// four tokens, compensated, and the quarters are added. Reads the logits (written by the scan, in L2
+// up to about 100 MB) once, 16 bytes at a time.
 constexpr int kVoteThreads = 512;
 constexpr int kVoteHeads = 256;
+constexpr int kVoteQuarters = 4;
 
 __global__ void __launch_bounds__(kVoteThreads) q4_vote_kernel(const __grid_constant__ Q4Args a, float* vote,
                                                                int64_t vote_stride) {
   __shared__ float2 s_mz[kVoteHeads];
+  __shared__ float4 s_sum[kVoteQuarters][kVoteThreads / kVoteQuarters];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int64_t total, before;
   count_pages(a, 0, lane, total, before);
   Q4Range r{total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x, 0, 0};
   int b, p0, p1;
+  wait_for_primary();
   while (next_part(a, r, b, p0, p1)) {
     const int n = a.seq_lens[b];
     int64_t first;
@@ -439,25 +493,55 @@ __global__ void __launch_bounds__(kVoteThreads) q4_vote_kernel(const __grid_cons
     scan_slots(a, b, lane, first, count);
     __syncthreads();                               // the last sequence's statistics are done with
     for (int h = warp; h < a.H; h += kVoteThreads / 32) {
-      const float2* ml = a.part_ml + first * a.H + h;
+      const float2* ml = a.part_ml + h * a.slots + first;
+      float2 x[8];                                 // the first 256 parts (one per CTA: all of them) at once
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = lane + 32 * k < count ? ml[lane + 32 * k] : make_float2(-INFINITY, 0.f);
       float M = -INFINITY;
-      for (int i = lane; i < count; i += 32) M = fmaxf(M, __ldcg(&ml[(size_t)i * a.H].x));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) M = fmaxf(M, x[k].x);
+      for (int i = lane + 256; i < count; i += 32) M = fmaxf(M, ml[i].x);
       M = warp_max(M);
       KahanF z;
-      for (int i = lane; i < count; i += 32) {
-        const float2 x = __ldcg(&ml[(size_t)i * a.H]);
-        z.add(x.y * part_weight(x.x, M));
-      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) z.add(x[k].y * part_weight(x[k].x, M));
+      for (int i = lane + 256; i < count; i += 32) z.add(ml[i].y * part_weight(ml[i].x, M));
       const float Z = warp_sum_comp(z.s, -z.c);
       if (lane == 0) s_mz[h] = make_float2(M, 1.f / Z);
     }
     __syncthreads();
-    const float* lb = a.logits + (size_t)b * a.H * a.max_tokens;
-    for (int i = p0 * kPage + tid; i < min(n, p1 * kPage); i += kVoteThreads) {
-      KahanF acc;
-#pragma unroll 8
-      for (int h = 0; h < a.H; ++h) acc.add(ex2(__ldcg(lb + (size_t)h * a.max_tokens + i) - s_mz[h].x) * s_mz[h].y);
-      vote[(size_t)b * vote_stride + i] = acc.s - acc.c;
+    const int quarter = tid / (kVoteThreads / kVoteQuarters), quad = tid % (kVoteThreads / kVoteQuarters);
+    const int end = min(n, p1 * kPage);
+    for (int i0 = p0 * kPage; i0 < end; i0 += kVoteThreads / kVoteQuarters * 4) {
+      const int i = i0 + 4 * quad;
+      KahanF acc[4];
+      const float* lb = a.logits + (size_t)b * a.H * a.max_tokens + (size_t)(i / kPage) * a.page_stride + i % kPage;
+      if (i < end) {                               // (the page's last tokens have logits of -inf)
+        for (int h0 = quarter; h0 < a.H; h0 += 8 * kVoteQuarters) {   // eight loads under way at once
+          float4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            x[k] = h0 + k * kVoteQuarters < a.H
+                       ? __ldcg(reinterpret_cast<const float4*>(lb + (size_t)(h0 + k * kVoteQuarters) * a.head_stride))
+                       : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (h0 + k * kVoteQuarters >= a.H) break;
+            const float2 mz = s_mz[h0 + k * kVoteQuarters];
+            acc[0].add(ex2(x[k].x - mz.x) * mz.y);
+            acc[1].add(ex2(x[k].y - mz.x) * mz.y);
+            acc[2].add(ex2(x[k].z - mz.x) * mz.y);
+            acc[3].add(ex2(x[k].w - mz.x) * mz.y);
+          }
+        }
+      }
+      s_sum[quarter][quad] = make_float4(acc[0].s - acc[0].c, acc[1].s - acc[1].c, acc[2].s - acc[2].c, acc[3].s - acc[3].c);
+      __syncthreads();
+      const float* sums = reinterpret_cast<const float*>(s_sum);
+      if (i0 + tid < end)
+        vote[(size_t)b * vote_stride + i0 + tid] =
+            (sums[tid] + sums[kVoteThreads + tid]) + (sums[2 * kVoteThreads + tid] + sums[3 * kVoteThreads + tid]);
+      __syncthreads();
     }
   }
 }
@@ -475,6 +559,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
                                                                    const __grid_constant__ Q4GatherArgs ga) {
   constexpr int D = NB * 64, BLK = q4_block_bytes(D), CODES = q4_code_bytes(D);
   __shared__ __align__(16) float merge[kGatherWarps][4 * NT][D];
+  __shared__ __align__(16) float sq[4 * NT * D];
   __shared__ float2 s_ml[kGatherWarps][4 * NT];
   const int split = blockIdx.x, set = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -486,8 +571,12 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
   const int32_t* ib = ga.idx + (size_t)b * ga.idx_stride;
   const int32_t* pt = a.page_table + (size_t)b * a.pt_stride;
 
+  launch_dependents();
+  for (int i = tid; i < 4 * NT * D; i += kGatherWarps * 32)
+    sq[i] = i / D < nh ? a.q[((size_t)b * a.H + head0) * D + i] : 0.f;
+  __syncthreads();
   Q4Query<NB, NT> f;
-  q4_load_query<NB, NT>(f, a.q + ((size_t)b * a.H + head0) * D, nh, lane);
+  q4_load_query<NB, NT>(f, sq, lane);
   float mul[NT], one[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -563,7 +652,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
       O = fmaf(wt, merge[w][hg][i % D], O);
     }
     a.part_o[(slot * a.H + head0) * D + i] = O;
-    if (i % D == 0) a.part_ml[slot * a.H + head0 + hg] = make_float2(M, L);
+    if (i % D == 0) a.part_ml[(head0 + hg) * a.slots + slot] = make_float2(M, L);
   }
 }
 
@@ -592,8 +681,24 @@ Q4Args make_args(ts_ctx* ctx, const float* q, const void* k_pool, const void* v_
   a.logits = ctx->logits;
   a.part_o = ctx->q4_part_o;
   a.part_ml = ctx->q4_part_ml;
+  a.slots = q4_part_slots(c, ctx->num_sms);
   a.status = ctx->status;
   return a;
+}
+
+// Launches `kernel` as a dependent of the kernel before it in the stream (see launch_dependents).
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, Args&&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads);
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, std::forward<Args>(args)...);
 }
 
 template <int NB, int NT>
@@ -602,9 +707,9 @@ ts_status run_attend(ts_ctx* ctx, const Q4Args& a, float* out, float* lse, cudaS
   if (!ensure_smem<scan_kernel<NB, NT, true>>(smem, ctx->device)) return TS_ERR_CUDA;
   ProfScope ps(ctx, TS_PROF_ATTEND, s);
   ctx->kernels += 2;
-  scan_kernel<NB, NT, true><<<a.ctas * a.n_groups, kQ4Threads, smem, s>>>(a);
-  q4_merge_kernel<NB * 64><<<dim3(a.H, a.B), 1024, 0, s>>>(a, 0, out, lse);
-  return cuda_status(cudaGetLastError());
+  scan_kernel<NB, NT, true><<<a.ctas * a.n_groups, Q4Ring<NB, NT, true>::WARPS * 32, smem, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return cuda_status(e != cudaSuccess ? e : launch_behind(q4_merge_kernel<NB * 64>, dim3(a.H, a.B), 1024, s, a, 0, out, lse));
 }
 
 template <int NB, int NT>
@@ -613,7 +718,7 @@ ts_status run_scan(ts_ctx* ctx, const Q4Args& a, cudaStream_t s) {
   if (!ensure_smem<scan_kernel<NB, NT, false>>(smem, ctx->device)) return TS_ERR_CUDA;
   ProfScope ps(ctx, TS_PROF_SCORE, s);
   ctx->kernels += 1;
-  scan_kernel<NB, NT, false><<<a.ctas * a.n_groups, kQ4Threads, smem, s>>>(a);
+  scan_kernel<NB, NT, false><<<a.ctas * a.n_groups, Q4Ring<NB, NT, false>::WARPS * 32, smem, s>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
@@ -622,8 +727,8 @@ ts_status run_gather(ts_ctx* ctx, const Q4Args& a, const Q4GatherArgs& ga, float
   ProfScope ps(ctx, TS_PROF_ATTEND, s);
   ctx->kernels += 2;
   gather_kernel<NB, NT><<<dim3(ga.splits, a.HKV * a.sets_per_kv, a.B), kGatherWarps * 32, 0, s>>>(a, ga);
-  q4_merge_kernel<NB * 64><<<dim3(a.H, a.B), 1024, 0, s>>>(a, ga.splits, out, lse);
-  return cuda_status(cudaGetLastError());
+  const cudaError_t e = cudaGetLastError();
+  return cuda_status(e != cudaSuccess ? e : launch_behind(q4_merge_kernel<NB * 64>, dim3(a.H, a.B), 1024, s, a, ga.splits, out, lse));
 }
 
 }  // namespace
@@ -655,12 +760,15 @@ ts_status launch_score_q4(ts_ctx* ctx, const ScoreCall& c, cudaStream_t s) {
   const bool soft = c.fn == TS_SCORE_HEAD_SOFT_VOTE;
   Q4Args a = make_args(ctx, c.q, c.k_pool, nullptr, c.page_table, c.seq_lens, c.B, soft ? c.scale * kLog2e : c.scale);
   a.skip = c.skip;
+  // for the votes page by page, so that what is written and read together lies together; the other
+  // selection functions read [B][H][max_tokens]
+  a.head_stride = soft ? kPage : a.max_tokens;
+  a.page_stride = soft ? (int64_t)kPage * a.H : kPage;
   const ts_status st = TS_Q4_DISPATCH(run_scan, ctx, a, s);
   if (st != TS_OK || !soft) return st;   // the other selection functions rank the natural logits themselves
   ProfScope ps(ctx, TS_PROF_VOTE, s);
   ctx->kernels += 1;
-  q4_vote_kernel<<<2 * ctx->num_sms, kVoteThreads, 0, s>>>(a, c.vote, c.vote_stride);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_behind(q4_vote_kernel, dim3(2 * ctx->num_sms), kVoteThreads, s, a, c.vote, c.vote_stride));
 }
 
 }  // namespace ts

@@ -102,21 +102,25 @@ struct Q4Query {
   float inv[NT];
 };
 
-// q: the first head's row; head h of nh at q + h d.
+// q: 4 NT rows of 64 NB floats in shared memory, zeros where there is no head.
 template <int NB, int NT>
-__device__ __forceinline__ void q4_load_query(Q4Query<NB, NT>& f, const float* q, int nh, int lane) {
+__device__ __forceinline__ void q4_load_query(Q4Query<NB, NT>& f, const float* q, int lane) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int h = 4 * nt + (g >> 1);
+    const float* row = q + (4 * nt + (g >> 1)) * (NB * 64);
     float x[NB][16];
     float mx = 0.f;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        x[nb][i] = h < nh ? q[(size_t)h * (NB * 64) + nb * 64 + 16 * t + i] : 0.f;
-        mx = fmaxf(mx, fabsf(x[nb][i]));
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(row + nb * 64 + 16 * t + 4 * i);
+        x[nb][4 * i] = v.x;
+        x[nb][4 * i + 1] = v.y;
+        x[nb][4 * i + 2] = v.z;
+        x[nb][4 * i + 3] = v.w;
+        mx = fmaxf(fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
       }
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));

@@ -13,7 +13,7 @@ namespace ts {
 namespace {
 
 constexpr int kRowsThreads = 256;
-constexpr int kRowsPerCta = 16;
+constexpr int kRowsPerCta = 16;   // at most: 16, 4 or 1
 
 struct RowsArgs {
   const int32_t* cu;           // [B + 1]; null: one row per sequence, at position seq_lens[b] - 1
@@ -109,29 +109,30 @@ __global__ void __launch_bounds__(kRowsThreads) append_rows_kernel(const __grid_
 // x - q s is exact in one fused multiply-add, and q + residual r (Markstein's correction) is the exact
 // quotient where that has few bits, as it has halfway between codes. Scales near or below the smallest
 // normal number have fewer bits and take the divisions instead.
+template <int NB, int ROWS>
 __global__ void __launch_bounds__(kRowsThreads) append_q4_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ int64_t place[kRowsPerCta];
   place_rows(a, place);
-  const int NB = a.D / 64, groups = 2 * a.HKV * NB, blk = q4_block_bytes(a.D), codes = q4_code_bytes(a.D);
-  const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
-  const int lane8 = threadIdx.x & 7;
+  constexpr int D = NB * 64, BLK = q4_block_bytes(D), CODES = q4_code_bytes(D), COLS = kRowsThreads / 8 / ROWS;
+  const int groups = a.HKV * NB, lane8 = threadIdx.x & 7;
   // neighbouring groups of eight lanes take neighbouring rows of the same 64 elements: their codes
   // are neighbours in the block
-#pragma unroll 2
-  for (int i = threadIdx.x >> 3; i < groups * a.rows_per_cta; i += kRowsThreads / 8) {
-    const int row = i % a.rows_per_cta, gi = i / a.rows_per_cta, isv = gi >= a.HKV * NB;
-    const int c = gi - isv * a.HKV * NB, g = c / NB, nb = c % NB;
-    const int64_t at = place[row];
+  const int row = (threadIdx.x >> 3) % ROWS;
+  const int64_t r = (int64_t)blockIdx.x * ROWS + row;
+  const int64_t at = place[row];
+  const int slot = (int)(at & 15);
+  const unsigned peers = 0xffu << (threadIdx.x & 24);
+#pragma unroll 4
+  for (int i = (threadIdx.x >> 3) / ROWS; i < 2 * groups; i += COLS) {
+    const int isv = i >= groups, c = isv ? i - groups : i, g = c / NB, nb = c % NB;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (at >= 0)
-      v = *reinterpret_cast<const uint4*>(a.src[isv] + (r0 + row) * a.src_stride[isv] + ((size_t)c * 64 + lane8 * 8) * 2);
+    if (at >= 0) v = ldg_nc128(a.src[isv] + r * a.src_stride[isv] + c * 128 + lane8 * 16);
     float x[8];
     KV<__nv_bfloat16>::unpack(v, x);
     // the largest magnitude by its bits: ordered like the values, with infinities and NaN on top
     uint32_t mb = 0u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) mb = max(mb, __float_as_uint(x[e]) & 0x7fffffffu);
-    const unsigned peers = 0xffu << (threadIdx.x & 24);
 #pragma unroll
     for (int d = 4; d >= 1; d >>= 1) mb = max(mb, __shfl_xor_sync(peers, mb, d));
     const float top = __uint_as_float(mb);
@@ -158,40 +159,43 @@ __global__ void __launch_bounds__(kRowsThreads) append_q4_kernel(const __grid_co
       }
     }
     if (at >= 0) {
-      unsigned char* base = a.pool[isv] + ((at >> 4) * a.HKV + g) * blk;
-      const int slot = (int)(at & 15);
+      unsigned char* base = a.pool[isv] + ((at >> 4) * a.HKV + g) * BLK;
       *reinterpret_cast<uint32_t*>(base + nb * 512 + slot * 32 + lane8 * 4) = w;
-      if (lane8 == 0) *reinterpret_cast<__nv_bfloat16*>(base + codes + nb * 32 + slot * 2) = sb;
+      if (lane8 == 0) *reinterpret_cast<__nv_bfloat16*>(base + CODES + nb * 32 + slot * 2) = sb;
     }
   }
 }
 
 // Rows of a pool as fp32 values: exact for every pool type (a code times a bf16 scale has 12
-// significant bits).
-template <int kType>
+// significant bits). Eight elements a thread, eight threads to 64 elements of one row, neighbouring
+// rows next to one another as in the append.
+template <int kType, int ROWS>
 __global__ void __launch_bounds__(kRowsThreads) read_rows_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ int64_t place[kRowsPerCta];
   place_rows(a, place);
-  const int c8 = a.HKV * a.D / 8, per_row = 2 * c8, ps = 1 << a.page_shift;   // threads of a row: 8 elements each
-  const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < per_row * a.rows_per_cta; i += kRowsThreads) {
-    const int row = i / per_row, rem = i % per_row, isv = rem >= c8;
-    const int c = rem - isv * c8, g = c / (a.D / 8), e0 = c % (a.D / 8) * 8;
-    const int64_t at = place[row];
-    if (at < 0) continue;
-    const int64_t page = at >> a.page_shift, slot = at & (ps - 1);
+  constexpr int COLS = kRowsThreads / 8 / ROWS;
+  const int NB = a.D / 64, groups = a.HKV * NB, lane8 = threadIdx.x & 7, ps = 1 << a.page_shift;
+  const int row = (threadIdx.x >> 3) % ROWS;
+  const int64_t r = (int64_t)blockIdx.x * ROWS + row;
+  const int64_t at = place[row];
+  if (at < 0) return;
+  const int64_t page = at >> a.page_shift;
+  const int slot = (int)(at & (ps - 1));
+  const int codes = q4_code_bytes(a.D), blk = q4_block_bytes(a.D), half = NB >> 1;   // NB is 1 or 2
+#pragma unroll 4
+  for (int i = (threadIdx.x >> 3) / ROWS; i < 2 * groups; i += COLS) {
+    const int isv = i >= groups, c = isv ? i - groups : i, g = c >> half, nb = c & half;
     float x[8];
     if constexpr (kType == TS_KV_Q4) {
-      const unsigned char* base = a.pool[isv] + (page * a.HKV + g) * q4_block_bytes(a.D);
-      const int nb = e0 / 64;
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(base + nb * 512 + slot * 32 + (e0 % 64) / 2);
-      const float s = bf16_bits_f(*reinterpret_cast<const uint16_t*>(base + q4_code_bytes(a.D) + nb * 32 + slot * 2));
+      const unsigned char* base = a.pool[isv] + (page * a.HKV + g) * blk;
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(base + nb * 512 + slot * 32 + lane8 * 4);
+      const float s = bf16_bits_f(*reinterpret_cast<const uint16_t*>(base + codes + nb * 32 + slot * 2));
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w >> (4 * e)) & 15u) - 8) * s;
     } else {
       constexpr int ES = kType == TS_KV_BF16 ? 2 : 4;
-      const uint4* src = reinterpret_cast<const uint4*>(a.pool[isv] + (((page * a.HKV + g) * ps + slot) * a.D + e0) * ES);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.pool[isv] + (((page * a.HKV + g) * ps + slot) * a.D + nb * 64 + lane8 * 8) * ES);
       if constexpr (kType == TS_KV_BF16) {
         KV<__nv_bfloat16>::unpack(src[0], x);
       } else {
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kRowsThreads) read_rows_kernel(const __grid_co
         KV<float>::unpack(src[1], x + 4);
       }
     }
-    float4* dst = reinterpret_cast<float4*>(a.dst[isv] + (r0 + row) * a.HKV * a.D + (size_t)c * 8);
+    float4* dst = reinterpret_cast<float4*>(a.dst[isv] + r * a.HKV * a.D + c * 64 + lane8 * 8);
     dst[0] = make_float4(x[0], x[1], x[2], x[3]);
     dst[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
@@ -228,9 +232,12 @@ RowsArgs base_args(ts_ctx* ctx, int B, int total, const int32_t* page_table, voi
 ts_status run_append(ts_ctx* ctx, const RowsArgs& a, cudaStream_t s) {
   const int grid = (a.total + a.rows_per_cta - 1) / a.rows_per_cta;
   ctx->kernels += 1;
-  if (ctx->cfg.kv_dtype == TS_KV_Q4)
-    append_q4_kernel<<<grid, kRowsThreads, 0, s>>>(a);
-  else
+#define TS_APPEND_Q4(NB_, ROWS_) \
+  if (a.D == 64 * NB_ && a.rows_per_cta == ROWS_) append_q4_kernel<NB_, ROWS_><<<grid, kRowsThreads, 0, s>>>(a);
+  if (ctx->cfg.kv_dtype == TS_KV_Q4) {
+    TS_APPEND_Q4(1, 1) TS_APPEND_Q4(1, 4) TS_APPEND_Q4(1, 16) TS_APPEND_Q4(2, 1) TS_APPEND_Q4(2, 4) TS_APPEND_Q4(2, 16)
+  } else
+#undef TS_APPEND_Q4
     append_rows_kernel<<<grid, kRowsThreads, 0, s>>>(a, a.D * (ctx->cfg.kv_dtype == TS_KV_BF16 ? 2 : 4));
   return cuda_status(cudaGetLastError());
 }
@@ -271,11 +278,13 @@ ts_status launch_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* sta
   a.dst[1] = v_out;
   const int grid = (total + a.rows_per_cta - 1) / a.rows_per_cta;
   ctx->kernels += 1;
-  switch (ctx->cfg.kv_dtype) {
-    case TS_KV_Q4: read_rows_kernel<TS_KV_Q4><<<grid, kRowsThreads, 0, s>>>(a); break;
-    case TS_KV_BF16: read_rows_kernel<TS_KV_BF16><<<grid, kRowsThreads, 0, s>>>(a); break;
-    default: read_rows_kernel<TS_KV_F32><<<grid, kRowsThreads, 0, s>>>(a); break;
-  }
+#define TS_READ_ROWS(TYPE_, ROWS_)                                      \
+  if (ctx->cfg.kv_dtype == TYPE_ && a.rows_per_cta == ROWS_) \
+    read_rows_kernel<TYPE_, ROWS_><<<grid, kRowsThreads, 0, s>>>(a);
+  TS_READ_ROWS(TS_KV_Q4, 1) TS_READ_ROWS(TS_KV_Q4, 4) TS_READ_ROWS(TS_KV_Q4, 16)
+  TS_READ_ROWS(TS_KV_BF16, 1) TS_READ_ROWS(TS_KV_BF16, 4) TS_READ_ROWS(TS_KV_BF16, 16)
+  TS_READ_ROWS(TS_KV_F32, 1) TS_READ_ROWS(TS_KV_F32, 4) TS_READ_ROWS(TS_KV_F32, 16)
+#undef TS_READ_ROWS
   return cuda_status(cudaGetLastError());
 }
 
