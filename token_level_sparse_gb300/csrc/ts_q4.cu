@@ -123,7 +123,7 @@ __device__ __forceinline__ bool next_part(const Q4Args& a, Q4Range& r, int& b, i
 // twice what one SM's share of HBM bandwidth needs to cover a microsecond.
 template <int NB, int NT, bool kAttend>
 struct Q4Ring {
-  static constexpr int WARPS = kAttend ? (NT == 1 ? 20 : 16) : 24;
+  static constexpr int WARPS = kAttend ? (NT == 1 ? 20 : 12) : 16;
   static constexpr int BLK = q4_block_bytes(NB * 64);
   static constexpr int OPS = kAttend ? 2 : 1;                      // blocks of a page
   static constexpr int PAGES = 2;                                  // pages of a stage
@@ -269,11 +269,15 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
         break;
       }
       phases ^= 1u << s;
-      const int pages = min(R::PAGES, mine - done * R::PAGES);
-#pragma unroll 1
-      for (int pg = 0; pg < pages; ++pg) {
+      // both pages of the stage together; one that does not exist, or has no block, has no tokens
+      float x[R::PAGES][NT][2];
+      int limit[R::PAGES];
+      bool whole = true;
+#pragma unroll
+      for (int pg = 0; pg < R::PAGES; ++pg) {
+        limit[pg] = (lost >> (2 * s + pg)) & 1u ? 0 : left - pg * per_set * kPage;
+        whole &= limit[pg] >= kPage;
         const unsigned char* kb = ring + s * R::STAGE + pg * (R::OPS * R::BLK);
-        const int limit = (lost >> (2 * s + pg)) & 1u ? 0 : left;
         uint2 kw[2][NB];
         float ks[NB][2];
 #pragma unroll
@@ -283,20 +287,25 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
             kw[u][nb] = *reinterpret_cast<const uint2*>(kb + nb * 512 + token(u, g) * 32 + t * 8);
             ks[nb][u] = bf16_bits_f(*reinterpret_cast<const uint16_t*>(kb + CODES + nb * 32 + token(u, g) * 2));
           }
-        float x[NT][2];
-        q4_scores<NB, NT>(f, kw, ks, x);
+        q4_scores<NB, NT>(f, kw, ks, x[pg]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) x[nt][u] *= mul[nt];
-        if (limit < kPage) {
+          for (int u = 0; u < 2; ++u) x[pg][nt][u] *= mul[nt];
+      }
+      if (!whole) {
+#pragma unroll
+        for (int pg = 0; pg < R::PAGES; ++pg)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) x[nt][u] = token(u, g) < limit ? x[nt][u] : -INFINITY;
-        }
-        if constexpr (kAttend) {
-          const unsigned char* vb = kb + R::BLK;
+            for (int u = 0; u < 2; ++u) x[pg][nt][u] = token(u, g) < limit[pg] ? x[pg][nt][u] : -INFINITY;
+      }
+      q4_raise_max<NB, NT, R::PAGES>(st, x);
+      if constexpr (kAttend) {
+#pragma unroll
+        for (int pg = 0; pg < R::PAGES; ++pg) {
+          const unsigned char* vb = ring + s * R::STAGE + pg * (R::OPS * R::BLK) + R::BLK;
           uint32_t vw[4][NB];
           float vs[NB][2];
 #pragma unroll
@@ -308,48 +317,38 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
             for (int u = 0; u < 2; ++u)
               vs[nb][u] = bf16_bits_f(*reinterpret_cast<const uint16_t*>(vb + CODES + nb * 32 + token(u, g) * 2));
           }
-          if (pg == pages - 1) {
+          if (pg == R::PAGES - 1) {
             __syncwarp();                                          // every lane has read the stage
             copy_next();
           }
-          if (limit < kPage)
-            q4_accumulate<NB, NT, true>(st, x, vw, vs);
+          if (whole)
+            q4_accumulate<NB, NT, false>(st, x[pg], vw, vs);
           else
-            q4_accumulate<NB, NT, false>(st, x, vw, vs);
-        } else {
-          if (pg == pages - 1) {
-            __syncwarp();
-            copy_next();
-          }
-          // each lane keeps a maximum of its own tokens, moved as in the attention
-          bool grow = false;
+            q4_accumulate<NB, NT, true>(st, x[pg], vw, vs);
+        }
+      } else {
+        __syncwarp();
+        copy_next();
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) grow |= fmaxf(x[nt][0], x[nt][1]) > st.m[nt] + 8.f;
-          if (__any_sync(kFull, grow)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const float mn = fmaxf(st.m[nt], fmaxf(x[nt][0], x[nt][1]));
-              st.l[nt] *= part_weight(st.m[nt], mn);
-              st.m[nt] = mn;
-            }
-          }
+        for (int pg = 0; pg < R::PAGES; ++pg) {
+          const bool there = done * R::PAGES + pg < mine;          // (a page without a block has logits of -inf)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float e0 = ex2(x[nt][0] - st.m[nt]), e1 = ex2(x[nt][1] - st.m[nt]);
-            if (limit < kPage) {                                   // no token there: no weight (not 2^(-inf + inf))
-              e0 = x[nt][0] == -INFINITY ? 0.f : e0;
-              e1 = x[nt][1] == -INFINITY ? 0.f : e1;
+            float e0 = ex2(x[pg][nt][0] - st.m[nt]), e1 = ex2(x[pg][nt][1] - st.m[nt]);
+            if (!whole) {                                          // no token there: no weight (not 2^(-inf + inf))
+              e0 = x[pg][nt][0] == -INFINITY ? 0.f : e0;
+              e1 = x[pg][nt][1] == -INFINITY ? 0.f : e1;
             }
             st.l[nt] += e0 + e1;
-            if (4 * nt + t < nh) {
-              row[nt * tile_step] = x[nt][0];
-              row[nt * tile_step + 8] = x[nt][1];
+            if (there && 4 * nt + t < nh) {
+              row[nt * tile_step + pg * row_step] = x[pg][nt][0];
+              row[nt * tile_step + pg * row_step + 8] = x[pg][nt][1];
             }
           }
-          row += row_step;
         }
-        left -= per_set * kPage;
+        row += R::PAGES * row_step;
       }
+      left -= R::PAGES * per_set * kPage;
       s = s + 1 == R::STAGES ? 0 : s + 1;
     }
     if (!ok && works) {
@@ -361,16 +360,6 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
     }
     // the next sequence's copies begin at stage 0 again
     // ---- the warps of a head set join their states
-    if constexpr (!kAttend) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float mn = fmaxf(st.m[nt], __shfl_xor_sync(kFull, st.m[nt], 4));
-        mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 8));
-        mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 16));
-        st.l[nt] *= part_weight(st.m[nt], mn);
-        st.m[nt] = mn;
-      }
-    }
     st.join_lanes();
     if (g == 0) {
 #pragma unroll
@@ -599,7 +588,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
         set_error(a.status, TS_ERR_PAGE_OOB);
     }
     uint2 kw[2][NB];
-    float ks[NB][2], vs[NB][2], x[NT][2];
+    float ks[NB][2], vs[NB][2], x[1][NT][2];
     uint32_t vw[4][NB];
     bool in[2];
 #pragma unroll
@@ -625,12 +614,13 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
                             : *reinterpret_cast<const uint32_t*>(a.v_pool + (size_t)(row / kPage) * BLK + nb * 512 +
                                                                  (row % kPage) * 32 + g * 4);
     }
-    q4_scores<NB, NT>(f, kw, ks, x);
+    q4_scores<NB, NT>(f, kw, ks, x[0]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) x[nt][i] = in[i] ? x[nt][i] * mul[nt] : -INFINITY;
-    q4_accumulate<NB, NT, true>(st, x, vw, vs);
+      for (int i = 0; i < 2; ++i) x[0][nt][i] = in[i] ? x[0][nt][i] * mul[nt] : -INFINITY;
+    q4_raise_max<NB, NT, 1>(st, x);
+    q4_accumulate<NB, NT, true>(st, x[0], vw, vs);
   }
   st.join_lanes();
   if (g == 0) {

@@ -30,17 +30,18 @@ __host__ __device__ constexpr int q4_code_bytes(int d) { return kPage * d / 2; }
 __host__ __device__ constexpr int q4_block_bytes(int d) { return kPage * (d / 2 + d / 32); }
 
 // D (16x8, fp32) += A (16x16) B (16x8): lane (g = lane / 4, t = lane % 4) holds rows g, g + 8 of A,
-// column g of B and rows g, g + 8 of D at columns 2t, 2t + 1. (Not volatile: products of different
-// accumulators may be interleaved.)
+// column g of B and rows g, g + 8 of D at columns 2t, 2t + 1. Volatile, as every instruction that a whole
+// warp executes together has to be: the compiler may otherwise move it into a branch that only some
+// lanes take.
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
+  asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
+  asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -88,7 +89,7 @@ __device__ __forceinline__ uint32_t q4_pair_bf16(uint32_t ab, int j) {
 // Transposes an 8x8 matrix of 16-bit elements held as (row g, columns 2t, 2t + 1).
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 
@@ -221,20 +222,24 @@ struct Q4State {
   }
 };
 
-// Adds 16 tokens: x[nt][u] are base-2 logits of head 4 nt + t and token (u, g) (-inf: not attended),
-// vs[nb][u] that token's value scales, vw[i][nb] word g of the codes of token (i / 2, 2t + i % 2). The
-// maximum moves only when a logit passes it by more than 2^8, so most units cost no shuffle and no
-// rescaling; weights stay below 2^8. kMasked: some tokens may not be attended.
-template <int NB, int NT, bool kMasked>
-__device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&x)[NT][2], const uint32_t (&vw)[4][NB],
-                                              const float (&vs)[NB][2]) {
+// Moves the maxima up for 16 P tokens with base-2 logits x[page][nt][u] (-inf: not attended), where a logit
+// passes its head's maximum by more than 2^8: most calls cost one vote and no rescaling, and weights
+// stay below 2^8.
+template <int NB, int NT, int P>
+__device__ __forceinline__ void q4_raise_max(Q4State<NB, NT>& s, const float (&x)[P][NT][2]) {
+  float top[NT];
   bool grow = false;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) grow |= fmaxf(x[nt][0], x[nt][1]) > s.m[nt] + 8.f;
+  for (int nt = 0; nt < NT; ++nt) {
+    top[nt] = fmaxf(x[0][nt][0], x[0][nt][1]);
+#pragma unroll
+    for (int pg = 1; pg < P; ++pg) top[nt] = fmaxf(top[nt], fmaxf(x[pg][nt][0], x[pg][nt][1]));
+    grow |= top[nt] > s.m[nt] + 8.f;
+  }
   if (__any_sync(kFull, grow)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mn = fmaxf(s.m[nt], fmaxf(x[nt][0], x[nt][1]));
+      float mn = fmaxf(s.m[nt], top[nt]);
       mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 4));
       mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 8));
       mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 16));
@@ -249,6 +254,14 @@ __device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&
           for (int e = 0; e < 4; ++e) s.o[nt][nb][j][e] *= f;
     }
   }
+}
+
+// Adds 16 tokens whose logits x[nt][u] (head 4 nt + t, token (u, g)) the maxima already cover: vs[nb][u]
+// are that token's value scales, vw[i][nb] word g of the codes of token (i / 2, 2t + i % 2). kMasked: some
+// tokens may not be attended (x = -inf).
+template <int NB, int NT, bool kMasked>
+__device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&x)[NT][2], const uint32_t (&vw)[4][NB],
+                                              const float (&vs)[NB][2]) {
   uint32_t b[NT][NB][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
