@@ -9,13 +9,16 @@
 //
 // A tile is 128 query rows of one KV head: 128 / G tokens with all G query heads of the group, row
 // = token * G + head, so a key tile in shared memory serves the whole group and a short prompt fills
-// a tile sooner. A CTA works on a block of two neighbouring tiles, which share every key and value
-// tile of 128 tokens:
-//   warp 8     loads: the two query tiles, then K and V tiles (TMA, 128-byte swizzle, two slots each)
-//   warp 9     products: S_i(j+1) = Q_i K(j+1)^T is issued behind O_i += P_i(j) V(j), so the tensor
-//              cores have the other tile's products to do while one tile's softmax runs
-//   warps 0-3  softmax of tile 0, a thread per row: scores from tensor memory, weights back over them
-//   warps 4-7  the same of tile 1
+// a tile sooner. An item of work is a block of two neighbouring tiles, which share every key and value
+// tile of 128 tokens. One CTA per SM goes through its items, the roles each at their own pace:
+//   warp 8      loads: the two query tiles of an item, then its K and V tiles (TMA, 128-byte swizzle, two
+//               slots each, running on across items)
+//   warp 9      products: S_i(j+1) = Q_i K(j+1)^T is issued behind O_i += P_i(j) V(j), so the tensor
+//               cores have the other tile's products to do while one tile's softmax runs
+//   warp 10     finds the next items
+//   warps 0-3   softmax of tile 0, a thread per row: scores from tensor memory, weights back over them; at
+//               the end of an item its outputs, while the next item is loaded and its first scores taken
+//   warps 4-7   the same of tile 1
 // The running maximum moves only when a score passes it by 2^8: weights and sums stay below 2^8 times
 // their number, far inside fp32, and the accumulators are rescaled a handful of times per row. The
 // softmax warps do that themselves, in between two products of their tile.
@@ -26,8 +29,8 @@
 // sequence's rows are) such values are taken out of the tile in shared memory, noted per column with
 // their first row, and put back into the outputs of the rows that see them.
 //
-// Blocks of all sequences are dealt out heaviest first (a block's work grows with its place in its
-// sequence), so the grid drains evenly.
+// Items are numbered heaviest first over all sequences (a block's work grows with its place in its
+// sequence) and dealt out to the CTAs forth and back, so that they end together.
 #include <cmath>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -42,10 +45,10 @@ constexpr int kPrKeys = 128;     // tokens of a key tile
 constexpr int kPrSoftmaxWarps = 8;
 constexpr int kPrThreads = (kPrSoftmaxWarps + 4) * 32;   // three warpgroups; two warps of the third idle
 // Registers a thread: 168 at launch (65536 / 384); the softmax warpgroups hold a row of 128 scores and
-// take what the third gives up: 2 * 208 + 88 = 3 * 168.
+// take what the third gives up: 2 * 208 + 88 = 3 * 168 (at 72 the products' warp spilled).
 constexpr int kPrSoftmaxRegs = 208, kPrOtherRegs = 88;
 static_assert(2 * kPrSoftmaxRegs + kPrOtherRegs <= 3 * 168, "register shares");
-constexpr int kPrNone = 0x7fffffff;
+constexpr uint16_t kPrNone = 0xffff;
 
 struct PromptArgs {
   CUtensorMap q, k, v;           // [rows][heads][d] each
@@ -67,7 +70,9 @@ struct PrShape {
   static constexpr int HALVES = D / 64;
   static constexpr int QT = kPrRows * D * 2;    // bytes of a query tile
   static constexpr int KT = kPrKeys * D * 2;    // bytes of a key or value tile
-  static constexpr int SMEM = 2 * QT + 4 * KT + 1024;
+  static constexpr int STAGE = 32 * 128;        // bytes of a softmax warp's output staging: 32 rows of 64 columns
+  static constexpr int SMEM = 2 * QT + 4 * KT + kPrSoftmaxWarps * STAGE + 1024;
+  static_assert(SMEM + 2048 <= 227 * 1024, "shared memory of an SM");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t S_COL = 0, O_COL = 256;   // tile i: S at 128 i (weights over its first 64), O at 256 + 128 i
 };
@@ -90,51 +95,77 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// Sequence and block of item t (one warp; the same in every lane): items in order of descending
-// block number over all sequences. False past the last one. Sequences whose boundaries are not
-// ascending inside [0, total] have no blocks.
+// Blocks of sequence b; sequences whose boundaries are not ascending inside [0, total] have none.
 __device__ __forceinline__ int seq_blocks(const PromptArgs& a, int b, int block) {
   const int s0 = a.cu[b], s1 = a.cu[b + 1];
   return (s0 < 0 || s1 < s0 || s1 > a.total) ? 0 : (s1 - s0 + block - 1) / block;
 }
 
-__device__ __forceinline__ int64_t blocks_from(const PromptArgs& a, int block, int mine, int level, int lane) {
-  int64_t n = max(0, mine - level);
-  for (int b = lane + 32; b < a.B; b += 32) n += max(0, seq_blocks(a, b, block) - level);
+// Numbers the blocks of all sequences in order of descending place in their sequence (one warp; results the
+// same in every lane). The blocks of the first 128 sequences stay in registers.
+struct BlockOrder {
+  int n[4];
+  int most;       // blocks of the longest sequence
+
+  __device__ __forceinline__ void init(const PromptArgs& a, int block, int lane) {
+    most = 0;
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) n += __shfl_xor_sync(kFull, n, d);
-  return n;
+    for (int k = 0; k < 4; ++k) {
+      n[k] = lane + 32 * k < a.B ? seq_blocks(a, lane + 32 * k, block) : 0;
+      most = max(most, n[k]);
+    }
+    for (int b = lane + 128; b < a.B; b += 32) most = max(most, seq_blocks(a, b, block));
+    most = __reduce_max_sync(kFull, most);
+  }
+  // number of blocks at place `level` of their sequence or behind it
+  __device__ __forceinline__ int from(const PromptArgs& a, int block, int level, int lane) const {
+    int c = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c += max(0, n[k] - level);
+    for (int b = lane + 128; b < a.B; b += 32) c += max(0, seq_blocks(a, b, block) - level);
+    return __reduce_add_sync(kFull, c);
+  }
+  // block t: its sequence and place. False past the last one. `hi`: a level that block t is below
+  // (most at first, afterwards one above an earlier block's place).
+  __device__ __forceinline__ bool find(const PromptArgs& a, int block, int t, int& hi, int lane, int& seq, int& blk) const {
+    int lo = 0;
+    if (hi <= 0 || from(a, block, 0, lane) <= t) return false;
+    while (hi - lo > 1) {            // from(lo) > t >= from(hi)
+      const int mid = (lo + hi) >> 1;
+      if (from(a, block, mid, lane) > t) lo = mid; else hi = mid;
+    }
+    blk = lo;
+    hi = lo + 1;
+    int rank = t - from(a, block, lo + 1, lane);
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int mine = b0 < 128 ? (b0 == 0 ? n[0] : b0 == 32 ? n[1] : b0 == 64 ? n[2] : n[3])
+                                : (b0 + lane < a.B ? seq_blocks(a, b0 + lane, block) : 0);
+      const unsigned m = __ballot_sync(kFull, mine > lo);
+      if (rank < __popc(m)) {
+        seq = b0 + (int)__fns(m, 0, rank + 1);
+        return true;
+      }
+      rank -= __popc(m);
+    }
+    return false;
+  }
+};
+
+// a[i] = min(a[i], v) between threads (shared memory; for the rare values that are not finite).
+__device__ __forceinline__ void min_u16(uint16_t* a, int i, int v) {
+  unsigned* word = reinterpret_cast<unsigned*>(a + (i & ~1));
+  const int sh = 16 * (i & 1);
+  unsigned old = *reinterpret_cast<volatile unsigned*>(word);
+  while ((int)(old >> sh & 0xffffu) > v) {
+    const unsigned seen = atomicCAS(word, old, (old & ~(0xffffu << sh)) | ((unsigned)v << sh));
+    if (seen == old) break;
+    old = seen;
+  }
 }
 
-__device__ __forceinline__ bool find_item(const PromptArgs& a, int64_t t, int block, int lane, int& seq, int& blk) {
-  const int mine = lane < a.B ? seq_blocks(a, lane, block) : 0;
-  int most = mine;
-  for (int b = lane + 32; b < a.B; b += 32) most = max(most, seq_blocks(a, b, block));
-  most = __reduce_max_sync(kFull, most);
-  if (a.B == 1) {
-    seq = 0;
-    blk = most - 1 - (int)t;
-    return t < most;
-  }
-  if (t >= blocks_from(a, block, mine, 0, lane)) return false;
-  int lo = 0, hi = most;             // blocks at level lo or above: more than t; at hi: not
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (blocks_from(a, block, mine, mid, lane) > t) lo = mid; else hi = mid;
-  }
-  int rank = (int)(t - blocks_from(a, block, mine, lo + 1, lane));
-  blk = lo;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const bool has = (b0 == 0 ? mine : (b0 + lane < a.B ? seq_blocks(a, b0 + lane, block) : 0)) > lo;
-    const unsigned m = __ballot_sync(kFull, has);
-    if (rank < __popc(m)) {
-      seq = b0 + (int)__fns(m, 0, rank + 1);
-      return true;
-    }
-    rank -= __popc(m);
-  }
-  return false;
-}
+struct PromptItem {
+  int found, row0, n, i0, kv;   // first packed row and length of the sequence, first token of the block
+};
 
 template <int D>
 __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_constant__ PromptArgs a) {
@@ -144,116 +175,119 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   unsigned char* sQ = base;                // two query tiles
   unsigned char* sK = sQ + 2 * S::QT;      // two key slots
   unsigned char* sV = sK + 2 * S::KT;      // two value slots
-  __shared__ __align__(8) uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], s_full[2],
-      p_ready[2], o_done[2];
+  unsigned char* sO = sV + 2 * S::KT;      // output staging, one area per softmax warp
+  __shared__ __align__(8) uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], s_full[2],
+      p_ready[2], o_done[2], item_full[2], item_empty[2], drained;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_item[3];                // found, sequence, block
-  __shared__ int s_first[3][D];            // first row of a column's NaN, +inf, -inf behind the diagonal's start
-  __shared__ int s_odd;                    // any of them
+  __shared__ PromptItem s_item[2];
+  // what value tiles held that is not finite, per item slot: first row of a column's NaN, +inf, -inf, counted
+  // from the first masked key tile
+  __shared__ __align__(4) uint16_t s_first[2][3][D];
+  __shared__ int s_odd[2];                 // any of them
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int kv = blockIdx.x % a.HKV;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const int block = 2 * a.tokens;
 
-  if (warp == kPrSoftmaxWarps) {
-    int seq = 0, blk = 0;
-    const bool found = find_item(a, blockIdx.x / a.HKV, block, lane, seq, blk);
-    if (lane == 0) {
-      s_item[0] = found;
-      s_item[1] = seq;
-      s_item[2] = blk;
-      // warps that look through the value tiles: those of a tile past the sequence's end wait for no
-      // scores, so nothing would keep them in step with the value slots
-      const bool second = found && blk * block + a.tokens < a.cu[seq + 1] - a.cu[seq];
-      for (int i = 0; i < 2; ++i) mbar_init(&v_clean[i], second ? kPrSoftmaxWarps : kPrSoftmaxWarps / 2);
-      mbar_fence_init();
-    }
-    if (blockIdx.x == 0)
-      for (int b = lane; b <= a.B; b += 32) {
-        const int v = a.cu[b];
-        if (v > a.total || (b == 0 ? v != 0 : v < a.cu[b - 1])) set_error(a.status, TS_ERR_SEQ_LEN);
-      }
-  }
   if (warp == kPrSoftmaxWarps + 1) {
     tmem_alloc(&s_tmem, S::TMEM_COLS);
     tmem_relinquish();
   }
   if (tid == 0) {
     mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&drained, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
+      mbar_init(&v_clean[i], kPrSoftmaxWarps);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], kPrSoftmaxWarps / 2);
       mbar_init(&o_done[i], 1);
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], kPrSoftmaxWarps + 2);
+      s_odd[i] = 0;
     }
     mbar_fence_init();
-    s_odd = 0;
   }
-  for (int i = tid; i < 3 * D; i += kPrThreads) (&s_first[0][0])[i] = kPrNone;
+  for (int i = tid; i < 2 * 3 * D; i += kPrThreads) (&s_first[0][0][0])[i] = kPrNone;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
-  if (s_item[0]) {
-    const int seq = s_item[1], blk = s_item[2];
-    const int row0 = a.cu[seq], n = a.cu[seq + 1] - row0;
-    const int i0 = blk * block;                                   // first token of the block
-    // key tiles of each query tile (0: the tile lies past the sequence), and the first one masked
-    int nt[2];
+  // Item k of this CTA is in slot k % 2. From it every role derives the same: key tiles of the two query
+  // tiles (0: the tile lies past the sequence), the number of key tiles, the first one that holds a key past
+  // the block's first token (128 j + 127 > i0).
+  auto read_item = [&](int k, PromptItem& it, int (&nt)[2], int& ntiles, int& masked_from) -> bool {
+    if (!mbar_wait(&item_full[k & 1], (k >> 1) & 1, a.wait_ns)) return false;
+    it = s_item[k & 1];
+#pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int first = i0 + i * a.tokens;
-      nt[i] = first < n ? (min(first + a.tokens, n) + kPrKeys - 1) / kPrKeys : 0;
+      const int first = it.i0 + i * a.tokens;
+      nt[i] = first < it.n ? (min(first + a.tokens, it.n) + kPrKeys - 1) / kPrKeys : 0;
     }
-    const int ntiles = max(nt[0], nt[1]);
-    const int masked_from = (i0 + 1) / kPrKeys;                   // tile j holds a key past token i0: 128 j + 127 > i0
+    ntiles = max(nt[0], nt[1]);
+    masked_from = (it.i0 + 1) / kPrKeys;
+    return true;
+  };
+  PromptItem it;
+  int nt[2], ntiles, masked_from;
 
-    if (warp >= kPrSoftmaxWarps) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrOtherRegs));
-      if (warp == kPrSoftmaxWarps) {
+  if (warp >= kPrSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrOtherRegs));
+    if (warp == kPrSoftmaxWarps) {
       // ---------------------------------------------------------------- loads
       if (lane == 0) {
         bool ok = true;
-        int kn = 0, vn = 0;
-        mbar_arrive_expect_tx(&q_full, (uint32_t)(2 * S::HALVES * a.G * a.tokens * 128));
-        for (int i = 0; i < 2; ++i)
-          for (int h = 0; h < S::HALVES; ++h)
-            tma_load_3d(sQ + i * S::QT + h * (kPrRows * 128), &a.q, h * 64, kv * a.G, row0 + i0 + i * a.tokens, &q_full);
-        for (int j = 0; j < ntiles && ok; ++j) {
-          const int s = j & 1;
-          if (j >= 2) ok = mbar_wait(&k_empty[s], ((j >> 1) - 1) & 1, a.wait_ns);
-          if (ok) {
+        int items = 0, kn = 0, vn = 0;                            // loaded so far: items' queries, K tiles, V tiles
+        for (;;) {
+          ok = read_item(items, it, nt, ntiles, masked_from);
+          if (!ok) break;
+          mbar_arrive(&item_empty[items & 1]);
+          if (!it.found) break;
+          if (items > 0) ok = mbar_wait(&q_empty, (items - 1) & 1, a.wait_ns);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&q_full, (uint32_t)(2 * S::HALVES * a.G * a.tokens * 128));
+          for (int i = 0; i < 2; ++i)
+            for (int h = 0; h < S::HALVES; ++h)
+              tma_load_3d(sQ + i * S::QT + h * (kPrRows * 128), &a.q, h * 64, it.kv * a.G, it.row0 + it.i0 + i * a.tokens,
+                          &q_full);
+          ++items;
+          for (int j = 0; j < ntiles && ok; ++j) {
+            int s = kn & 1;
+            if (kn >= 2) ok = mbar_wait(&k_empty[s], ((kn >> 1) - 1) & 1, a.wait_ns);
+            if (!ok) break;
             mbar_arrive_expect_tx(&k_full[s], S::KT);
             for (int h = 0; h < S::HALVES; ++h)
-              tma_load_3d(sK + s * S::KT + h * (kPrKeys * 128), &a.k, h * 64, kv, row0 + j * kPrKeys, &k_full[s]);
+              tma_load_3d(sK + s * S::KT + h * (kPrKeys * 128), &a.k, h * 64, it.kv, it.row0 + j * kPrKeys, &k_full[s]);
             ++kn;
-            if (j >= 2) ok = mbar_wait(&v_empty[s], ((j >> 1) - 1) & 1, a.wait_ns);
-          }
-          if (ok) {
+            s = vn & 1;
+            if (vn >= 2) ok = mbar_wait(&v_empty[s], ((vn >> 1) - 1) & 1, a.wait_ns);
+            if (!ok) break;
             mbar_arrive_expect_tx(&v_full[s], S::KT);
             for (int h = 0; h < S::HALVES; ++h)
-              tma_load_3d(sV + s * S::KT + h * (kPrKeys * 128), &a.v, h * 64, kv, row0 + j * kPrKeys, &v_full[s]);
+              tma_load_3d(sV + s * S::KT + h * (kPrKeys * 128), &a.v, h * 64, it.kv, it.row0 + j * kPrKeys, &v_full[s]);
             ++vn;
           }
+          if (!ok) break;
         }
         if (!ok) set_error(a.status, TS_ERR_TIMEOUT);
         // nothing may still be landing when the CTA exits
-        if (!mbar_wait(&q_full, 0, a.wait_ns)) set_error(a.status, TS_ERR_TIMEOUT);
+        if (items > 0) mbar_wait(&q_full, (items - 1) & 1, a.wait_ns);
         for (int j = max(0, kn - 2); j < kn; ++j) mbar_wait(&k_full[j & 1], (j >> 1) & 1, a.wait_ns);
         for (int j = max(0, vn - 2); j < vn; ++j) mbar_wait(&v_full[j & 1], (j >> 1) & 1, a.wait_ns);
       }
       __syncwarp();
-      } else if (warp == kPrSoftmaxWarps + 1) {
+    } else if (warp == kPrSoftmaxWarps + 1) {
       // ------------------------------------------------------------- products
       if (lane == 0) {
         const uint32_t idesc_s = idesc_bf16_f32(kPrRows, kPrKeys) | (a.negate ? 1u << 13 : 0u);   // bit 13: -A
         constexpr uint32_t idesc_o = idesc_bf16_f32_bmn(kPrRows, D);
         const uint32_t q0 = smem_addr(sQ), k0 = smem_addr(sK), v0 = smem_addr(sV);
-        auto scores = [&](int i, int j) {
-          const uint32_t kt = k0 + (j & 1) * S::KT, qt = q0 + i * S::QT;
+        auto scores = [&](int i, int slot) {
+          const uint32_t kt = k0 + slot * S::KT, qt = q0 + i * S::QT;
 #pragma unroll
           for (int h = 0; h < S::HALVES; ++h)
 #pragma unroll
@@ -262,196 +296,302 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
                         sdesc_sw128(kt + h * (kPrKeys * 128) + ks * 32), idesc_s, (h | ks) != 0);
           umma_commit(&s_full[i]);
         };
-        bool ok = mbar_wait(&q_full, 0, a.wait_ns) && mbar_wait(&k_full[0], 0, a.wait_ns);
-        if (ok) {
+        bool ok = true;
+        int kt = 0;                                               // key tiles of the items before
+        uint32_t clean_par = 0u, p_par = 0u;                      // parities of the next waits, by slot and by tile
+        for (int k = 0;; ++k) {
+          ok = read_item(k, it, nt, ntiles, masked_from);
+          if (!ok) break;
+          mbar_arrive(&item_empty[k & 1]);
+          if (!it.found) break;
+          ok = mbar_wait(&q_full, k & 1, a.wait_ns) && mbar_wait(&k_full[kt & 1], (kt >> 1) & 1, a.wait_ns);
+          if (!ok) break;
           tc_fence_after();
-          for (int i = 0; i < 2; ++i)
-            if (nt[i] > 0) scores(i, 0);
-          umma_commit(&k_empty[0]);
-        }
-        for (int j = 0; j < ntiles && ok; ++j) {
-          const int s = j & 1, s1 = (j + 1) & 1;
-          ok = mbar_wait(&v_full[s], (j >> 1) & 1, a.wait_ns);
-          if (ok && j >= masked_from) ok = mbar_wait(&v_clean[s], ((j >> 1) - (masked_from + (s ^ (masked_from & 1))) / 2) & 1, a.wait_ns);
-          if (ok && j + 1 < ntiles) ok = mbar_wait(&k_full[s1], ((j + 1) >> 1) & 1, a.wait_ns);
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (j >= nt[i]) continue;
-            ok = mbar_wait(&p_ready[i], j & 1, a.wait_ns);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t vt = v0 + s * S::KT;
 #pragma unroll
-            for (int ks = 0; ks < kPrKeys / 16; ++ks)
-              umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 8 * ks,
-                           sdesc_sw128_mn(vt + ks * 2048, kPrKeys * 128, 1024), idesc_o, (j | ks) != 0);
-            umma_commit(&o_done[i]);
-            if (j + 1 < nt[i]) scores(i, j + 1);
+          for (int i = 0; i < 2; ++i)
+            if (nt[i] > 0) scores(i, kt & 1);
+          umma_commit(&k_empty[kt & 1]);
+          if (ntiles == 1) umma_commit(&q_empty);
+          for (int j = 0; j < ntiles && ok; ++j) {
+            const int g = kt + j, s = g & 1, s1 = s ^ 1;
+            ok = mbar_wait(&v_full[s], (g >> 1) & 1, a.wait_ns);
+            if (ok && j >= masked_from) {
+              ok = mbar_wait(&v_clean[s], (clean_par >> s) & 1u, a.wait_ns);
+              clean_par ^= 1u << s;
+            }
+            if (ok && j + 1 < ntiles) ok = mbar_wait(&k_full[s1], ((g + 1) >> 1) & 1, a.wait_ns);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!ok || j >= nt[i]) continue;
+              ok = mbar_wait(&p_ready[i], (p_par >> i) & 1u, a.wait_ns);
+              if (!ok) continue;
+              p_par ^= 1u << i;
+              tc_fence_after();
+              const uint32_t vt = v0 + s * S::KT;
+#pragma unroll
+              for (int ks = 0; ks < kPrKeys / 16; ++ks)
+                umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 8 * ks,
+                             sdesc_sw128_mn(vt + ks * 2048, kPrKeys * 128, 1024), idesc_o, (j | ks) != 0);
+              umma_commit(&o_done[i]);
+              if (j + 1 < nt[i]) scores(i, s1);
+            }
+            if (ok) {
+              umma_commit(&v_empty[s]);
+              if (j + 1 < ntiles) umma_commit(&k_empty[s1]);
+              if (j + 2 == ntiles) umma_commit(&q_empty);
+            }
           }
-          if (ok) {
-            umma_commit(&v_empty[s]);
-            if (j + 1 < ntiles) umma_commit(&k_empty[s1]);
-          }
+          if (!ok) break;
+          kt += ntiles;
         }
         if (!ok) set_error(a.status, TS_ERR_TIMEOUT);
+        // no product may be under way when tensor memory is given back
+        umma_commit(&drained);
+        mbar_wait(&drained, 0, a.wait_ns);
       }
       __syncwarp();
+    } else if (warp == kPrSoftmaxWarps + 2) {
+      // ---------------------------------------------------------------- items
+      if (blockIdx.x == 0)
+        for (int b = lane; b <= a.B; b += 32) {
+          const int v = a.cu[b];
+          if (v > a.total || (b == 0 ? v != 0 : v < a.cu[b - 1])) set_error(a.status, TS_ERR_SEQ_LEN);
+        }
+      BlockOrder order;
+      order.init(a, block, lane);
+      int level = order.most;
+      bool found = true;
+      for (int k = 0; found; ++k) {
+        const int64_t t = (int64_t)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        int seq = 0, blk = 0;
+        found = t / a.HKV < 0x7fffffff && order.find(a, block, (int)(t / a.HKV), level, lane, seq, blk);
+        if (k >= 2 && !mbar_wait(&item_empty[k & 1], ((k >> 1) - 1) & 1, a.wait_ns)) {
+          set_error(a.status, TS_ERR_TIMEOUT);
+          break;
+        }
+        if (s_odd[k & 1]) {
+          for (int i = lane; i < 3 * D; i += 32) (&s_first[k & 1][0][0])[i] = kPrNone;
+          __syncwarp();
+          if (lane == 0) s_odd[k & 1] = 0;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          PromptItem& o = s_item[k & 1];
+          o.found = found;
+          o.row0 = found ? a.cu[seq] : 0;
+          o.n = found ? a.cu[seq + 1] - a.cu[seq] : 0;
+          o.i0 = blk * block;
+          o.kv = (int)(t % a.HKV);
+          mbar_arrive(&item_full[k & 1]);
+        }
+        __syncwarp();
       }
-    } else if (nt[warp >> 2] > 0) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrSoftmaxRegs));
-      // -------------------------------------------------------------- softmax
-      const int i = warp >> 2;                                    // tile
-      const int share = S::KT / (nt[1] > 0 ? kPrSoftmaxWarps : kPrSoftmaxWarps / 2);   // bytes of a value tile to look through
-      const int row = 32 * (warp & 3) + lane;
-      const int first = i0 + i * a.tokens;                        // first token of the tile
-      const int tok = first + row / a.G, head = kv * a.G + row % a.G;
-      const bool real = row < a.tokens * a.G && tok < n;
-      const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-      const uint32_t tS = tmem + S::S_COL + 128 * i + lane_off, tO = tmem + S::O_COL + 128 * i + lane_off;
-      float m2 = -INFINITY, la = 0.f, lb = 0.f;                   // running maximum (base 2) and two halves of the sum
-      bool ok = true;
-      for (int j = 0; j < ntiles && ok; ++j) {
-        if (j >= masked_from) {
-          // this warp's part of the value tile: what is not finite from token i0 on comes out
-          ok = mbar_wait(&v_full[j & 1], (j >> 1) & 1, a.wait_ns);
-          if (!__all_sync(kFull, ok)) break;
-          unsigned char* vt = sV + (j & 1) * S::KT + warp * share;
-          uint32_t odd = 0u;
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrSoftmaxRegs));
+    const int i = warp >> 2;                                      // tile
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t inv_g = 65536u / (uint32_t)a.G + 1u;           // r / G = (r inv_g) >> 16 for r < 128, G <= 16
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + S::S_COL + 128 * i + lane_off, tO = tmem + S::O_COL + 128 * i + lane_off;
+    bool ok = true, in_step = true;
+    int kt = 0;                                                   // key tiles of the items before
+    uint32_t clean_par = 0u;                                      // parity of the next use of v_clean, by slot
+    uint32_t s_par = 0u;                                          // parity of the next score tile
+    for (int k = 0; ok; ++k) {
+      ok = __all_sync(kFull, read_item(k, it, nt, ntiles, masked_from));
+      if (!ok || !it.found) break;
+      const int mine = nt[i], slot = k & 1;
+      if (mine == 0) {
+        // Past the sequence's end: nothing to do, and the other tile's warps look through the value tiles
+        // alone. Nothing keeps this warp in step with the value slots meanwhile.
+        for (int j = masked_from; j < ntiles; ++j) clean_par ^= 1u << ((kt + j) & 1);
+        in_step = false;
+      } else {
+        const int first = it.i0 + i * a.tokens;                   // first token of the tile
+        const int row_tok = (int)((uint32_t)row * inv_g >> 16), tok = first + row_tok;
+        const bool real = row_tok < a.tokens && tok < it.n;
+        const int cleaners = nt[1] > 0 ? kPrSoftmaxWarps : kPrSoftmaxWarps / 2;
+        const int share = S::KT / cleaners;                       // bytes of a value tile to look through
+        float m2 = -INFINITY, la = 0.f, lb = 0.f;                 // running maximum (base 2) and two halves of the sum
+        for (int j = 0; j < ntiles && ok; ++j) {
+          const int vs = (kt + j) & 1;
+          bool have_s = false;
+          if (j >= masked_from) {
+            if (!in_step) {
+              // the item's first scores are taken after all products of the items before
+              ok = __all_sync(kFull, mbar_wait(&s_full[i], s_par, a.wait_ns));
+              if (!ok) break;
+              have_s = in_step = true;
+            }
+            // this warp's part of the value tile: what is not finite behind token i0 comes out
+            ok = __all_sync(kFull, mbar_wait(&v_full[vs], ((kt + j) >> 1) & 1, a.wait_ns));
+            if (!ok) break;
+            unsigned char* vt = sV + vs * S::KT + warp * share;
+            uint32_t odd = 0u;
 #pragma unroll 4
-          for (int c = 0; c < share / 512; ++c) {
-            const uint4 w = lds128(vt + c * 512 + lane * 16);
-            odd |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
-                   ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
-          }
-          if (odd & 0x80008000u) {
             for (int c = 0; c < share / 512; ++c) {
-              const int off = warp * share + c * 512 + lane * 16;        // byte in the tile
-              const int r = (off % (kPrKeys * 128)) / 128, key = j * kPrKeys + r;
-              const int col0 = off / (kPrKeys * 128) * 64 + (((off / 16) % 8) ^ (r & 7)) * 8;
-              if (key <= i0) continue;                            // every row of the block sees it
-              uint16_t* e16 = reinterpret_cast<uint16_t*>(sV + (j & 1) * S::KT + off);
-              for (int e = 0; e < 8; ++e) {
-                const uint32_t u = e16[e];
-                if ((u & 0x7f80u) != 0x7f80u) continue;
-                atomicMin(&s_first[(u & 0x7fu) ? 0 : (u >> 15 ? 2 : 1)][col0 + e], key);
-                e16[e] = 0;
-                s_odd = 1;
+              const uint4 w = lds128(vt + c * 512 + lane * 16);
+              odd |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                     ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+            }
+            if (odd & 0x80008000u) {
+              for (int c = 0; c < share / 512; ++c) {
+                const int off = warp * share + c * 512 + lane * 16;              // byte in the tile
+                const int r = (off % (kPrKeys * 128)) / 128, key = j * kPrKeys + r;
+                const int col0 = off / (kPrKeys * 128) * 64 + (((off / 16) % 8) ^ (r & 7)) * 8;
+                if (key <= s_item[slot].i0) continue;             // every row of the block sees it
+                uint16_t* e16 = reinterpret_cast<uint16_t*>(sV + vs * S::KT + off);
+                for (int e = 0; e < 8; ++e) {
+                  const uint32_t u = e16[e];
+                  if ((u & 0x7f80u) != 0x7f80u) continue;
+                  min_u16(s_first[slot][(u & 0x7fu) ? 0 : (u >> 15 ? 2 : 1)], col0 + e, key - masked_from * kPrKeys);
+                  e16[e] = 0;
+                  s_odd[slot] = 1;
+                }
+              }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&v_clean[vs]);
+              if (cleaners < kPrSoftmaxWarps) mbar_arrive(&v_clean[vs]);         // for a warp of the other tile
+            }
+            clean_par ^= 1u << vs;
+          }
+          if (j >= mine) continue;
+          if (!have_s) ok = __all_sync(kFull, mbar_wait(&s_full[i], s_par, a.wait_ns));
+          if (!ok) break;
+          in_step = true;
+          tc_fence_after();
+          uint32_t u[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_x32(tS + 32 * c, u + 32 * c);
+          tmem_wait_ld();
+          float* x = reinterpret_cast<float*>(u);
+          if (j * kPrKeys + kPrKeys - 1 > first) {                // the tile holds keys that a row may not see
+            const int lim = tok - j * kPrKeys;
+#pragma unroll
+            for (int c = 0; c < 128; ++c) x[c] = c <= lim ? x[c] : -INFINITY;
+          }
+          float mx = x[0], my = x[1];
+#pragma unroll
+          for (int c = 2; c < 128; c += 2) {
+            mx = fmaxf(mx, x[c]);
+            my = fmaxf(my, x[c + 1]);
+          }
+          // rows that are no query of the sequence (their operands may be anything) move no maximum
+          const float top = real ? fmaxf(mx, my) * a.scale2 : -INFINITY;
+          if (__any_sync(kFull, top > m2 + 8.f)) {
+            const float mn = fmaxf(m2, top);
+            const float f = mn == m2 ? 1.f : pr_ex2(m2 - mn);
+            m2 = mn;
+            la *= f;
+            lb *= f;
+            if (j > 0) {
+              // the tile's last product must be in before its accumulators are rescaled
+              ok = __all_sync(kFull, mbar_wait(&o_done[i], s_par ^ 1u, a.wait_ns));
+              if (!ok) break;
+              tc_fence_after();
+              // (rare, and the scores hold most registers: eight columns at a time)
+#pragma unroll 1
+              for (int c = 0; c < D; c += 8) {
+                float o[8];
+                tmem_ld_x8(tO + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= f;
+                tmem_st_x8(tO + c, o);
               }
             }
           }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_clean[j & 1]);
-        }
-        if (j >= nt[i]) continue;
-        ok = mbar_wait(&s_full[i], j & 1, a.wait_ns);
-        if (!__all_sync(kFull, ok)) break;
-        tc_fence_after();
-        uint32_t u[128];
+          const float ms = m2 == -INFINITY ? 0.f : -m2;           // nothing seen yet: every weight is zero
+          const uint64_t sc = pack_f2(a.scale2, a.scale2), mm = pack_f2(ms, ms);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_x32(tS + 32 * c, u + 32 * c);
-        tmem_wait_ld();
-        float* x = reinterpret_cast<float*>(u);
-        if (j * kPrKeys + kPrKeys - 1 > first) {                  // the tile holds keys that a row may not see
-          const int lim = tok - j * kPrKeys;
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
 #pragma unroll
-          for (int c = 0; c < 128; ++c) x[c] = c <= lim ? x[c] : -INFINITY;
-        }
-        float mx = x[0], my = x[1];
-#pragma unroll
-        for (int c = 2; c < 128; c += 2) {
-          mx = fmaxf(mx, x[c]);
-          my = fmaxf(my, x[c + 1]);
-        }
-        // rows that are no query of the sequence (their operands may be anything) move no maximum
-        const float top = real ? fmaxf(mx, my) * a.scale2 : -INFINITY;
-        if (__any_sync(kFull, top > m2 + 8.f)) {
-          const float mn = fmaxf(m2, top);
-          const float f = mn == m2 ? 1.f : pr_ex2(m2 - mn);
-          m2 = mn;
-          la *= f;
-          lb *= f;
-          if (j > 0) {
-            // the tile's last product must be in before its accumulators are rescaled
-            ok = mbar_wait(&o_done[i], (j - 1) & 1, a.wait_ns);
-            if (!__all_sync(kFull, ok)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld_x32(tO + 32 * c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st_x32(tO + 32 * c, o);
+            for (int c = 0; c < 32; ++c) {
+              const int e = 64 * h + 2 * c;
+              float y0, y1;
+              unpack_f2(fma_f2(pack_f2(x[e], x[e + 1]), sc, mm), y0, y1);
+              y0 = pr_ex2(y0);
+              y1 = pr_ex2(y1);
+              add2(la, lb, y0, y1);
+              p[c] = pack_bf16(y0, y1);
             }
+            tmem_st_x32(tS + 32 * h, p);
           }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[i]);
+          s_par ^= 1u;
         }
-        const float ms = m2 == -INFINITY ? 0.f : -m2;             // nothing seen yet: every weight is zero
-        const uint64_t sc = pack_f2(a.scale2, a.scale2), mm = pack_f2(ms, ms);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int e = 64 * h + 2 * c;
-            float y0, y1;
-            unpack_f2(fma_f2(pack_f2(x[e], x[e + 1]), sc, mm), y0, y1);
-            y0 = pr_ex2(y0);
-            y1 = pr_ex2(y1);
-            add2(la, lb, y0, y1);
-            p[c] = pack_bf16(y0, y1);
-          }
-          tmem_st_x32(tS + 32 * h, p);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[i]);
-      }
-      // ---- outputs
-      if (__all_sync(kFull, ok)) {
-        ok = mbar_wait(&o_done[i], (nt[i] - 1) & 1, a.wait_ns);
+        // ---- outputs
+        if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[i], s_par ^ 1u, a.wait_ns));
         // what the value tiles held is known once every warp has looked through the last of them
-        for (int j = max(masked_from, ntiles - 2); j < ntiles; ++j)
-          ok = ok && mbar_wait(&v_clean[j & 1], ((j >> 1) - (masked_from + ((j & 1) ^ (masked_from & 1))) / 2) & 1, a.wait_ns);
-        if (__all_sync(kFull, ok)) {
+        for (int j = max(masked_from, ntiles - 2); j < ntiles && ok; ++j)
+          ok = __all_sync(kFull, mbar_wait(&v_clean[(kt + j) & 1], ((clean_par >> ((kt + j) & 1)) & 1u) ^ 1u, a.wait_ns));
+        if (ok) {
           tc_fence_after();
           const float l = la + lb, inv = 1.f / l;
-          __nv_bfloat16* dst = a.out + (int64_t)(row0 + tok) * a.out_stride + (int64_t)head * D;
-          const bool odd = s_odd != 0;
+          const bool odd = s_odd[slot] != 0;
+          const int row0 = s_item[slot].row0, n = s_item[slot].n, head0 = s_item[slot].kv * a.G;
+          if (real && a.lse)
+            a.lse[(int64_t)(row0 + tok) * a.H + head0 + row - row_tok * a.G] = (m2 + log2f(l)) * 0.6931471805599453f;
+          unsigned char* stage = sO + warp * S::STAGE;
+#pragma unroll 1
+          for (int h = 0; h < S::HALVES; ++h) {
+            // 64 columns of 32 rows through this warp's staging area (swizzled like the operands), so that a
+            // store covers whole 128-byte pieces of four rows instead of 16 bytes of 32
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld_x32(tO + 32 * c, o);
-            tmem_wait_ld();
-            if (odd) {
+            for (int c = 0; c < 2; ++c) {
+              uint32_t o[32];
+              tmem_ld_x32(tO + 64 * h + 32 * c, o);
+              tmem_wait_ld();
+              if (odd) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int col = 32 * c + e;
-                const bool pos = tok >= s_first[1][col], neg = tok >= s_first[2][col];
-                float add = pos ? INFINITY : 0.f;
-                if (neg) add += -INFINITY;
-                if (tok >= s_first[0][col]) add = NAN;
-                o[e] = __float_as_uint(__uint_as_float(o[e]) + add);
+                for (int e = 0; e < 32; ++e) {
+                  const int col = 64 * h + 32 * c + e;
+                  const int at = tok - masked_from * kPrKeys;      // (below 4 tiles: kPrNone is never reached)
+                  float add = at >= s_first[slot][1][col] ? INFINITY : 0.f;
+                  if (at >= s_first[slot][2][col]) add += -INFINITY;
+                  if (at >= s_first[slot][0][col]) add = NAN;
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) + add);
+                }
               }
-            }
-            if (real) {
-              uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 uint32_t w[4];
 #pragma unroll
                 for (int z = 0; z < 4; ++z)
                   w[z] = pack_bf16(__uint_as_float(o[8 * e + 2 * z]) * inv, __uint_as_float(o[8 * e + 2 * z + 1]) * inv);
-                d4[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + e) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
               }
             }
+            __syncwarp();
+#pragma unroll
+            for (int r4 = 0; r4 < 8; ++r4) {
+              const int rl = 4 * r4 + (lane >> 3), rr = 32 * (warp & 3) + rl, c16 = lane & 7;
+              const int rt = (int)((uint32_t)rr * inv_g >> 16), rh = rr - rt * a.G;
+              const uint4 v = lds128(stage + rl * 128 + ((c16 ^ (rl & 7)) << 4));
+              if (rt < a.tokens && first + rt < n)
+                *reinterpret_cast<uint4*>(a.out + (int64_t)(row0 + first + rt) * a.out_stride +
+                                          (int64_t)(head0 + rh) * D + 64 * h + c16 * 8) = v;
+            }
+            __syncwarp();
           }
-          if (real && a.lse) a.lse[(int64_t)(row0 + tok) * a.H + head] = (m2 + log2f(l)) * 0.6931471805599453f;
+          // the accumulators have been read before the next item's weights let a product write them
+          tc_fence_before();
         }
       }
-      if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
+      kt += ntiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
     }
+    if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
   }
   tc_fence_before();
   __syncthreads();
@@ -524,9 +664,9 @@ ts_status launch_prompt_attend(ts_ctx* ctx, const PromptCall& c, cudaStream_t s)
       !rows_map(&a.k, c.k, c.total, a.HKV, cfg.head_dim, c.k_stride, 1, kPrKeys) ||
       !rows_map(&a.v, c.v, c.total, a.HKV, cfg.head_dim, c.v_stride, 1, kPrKeys))
     return TS_ERR_CUDA;
-  // a sequence has at most one block that is not full
-  const int64_t grid = ((int64_t)c.total / (2 * a.tokens) + (c.B < c.total ? c.B : c.total)) * a.HKV;
-  if (grid > 0x7fffffff) return TS_ERR_SHAPE;
+  // a sequence has at most one block that is not full; one CTA per SM where there are that many
+  const int64_t items = ((int64_t)c.total / (2 * a.tokens) + (c.B < c.total ? c.B : c.total)) * a.HKV;
+  const int64_t grid = items < ctx->num_sms ? items : ctx->num_sms;
   return cfg.head_dim == 64 ? run_prompt<64>(ctx, a, grid, s) : run_prompt<128>(ctx, a, grid, s);
 }
 
