@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   unsigned char* sV = sK + 2 * S::KT;      // two value slots
   unsigned char* sO = sV + 2 * S::KT;      // output staging, one area per softmax warp
   __shared__ __align__(8) uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], s_full[2],
-      p_ready[2], o_done[2], item_full[2], item_empty[2], drained;
+      p_ready[2][2], o_done[2], item_full[2], item_empty[2], drained;
   __shared__ uint32_t s_tmem;
   __shared__ PromptItem s_item[2];
   // what value tiles held that is not finite, per item slot: first row of a column's NaN, +inf, -inf, counted
@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       mbar_init(&v_empty[i], 1);
       mbar_init(&v_clean[i], kPrSoftmaxWarps);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_ready[i], kPrSoftmaxWarps / 2);
+      mbar_init(&p_ready[i][0], kPrSoftmaxWarps / 2);
+      mbar_init(&p_ready[i][1], kPrSoftmaxWarps / 2);
       mbar_init(&o_done[i], 1);
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], kPrSoftmaxWarps + 2);
@@ -282,73 +283,98 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       __syncwarp();
     } else if (warp == kPrSoftmaxWarps + 1) {
       // ------------------------------------------------------------- products
-      if (lane == 0) {
-        const uint32_t idesc_s = idesc_bf16_f32(kPrRows, kPrKeys) | (a.negate ? 1u << 13 : 0u);   // bit 13: -A
-        constexpr uint32_t idesc_o = idesc_bf16_f32_bmn(kPrRows, D);
-        const uint32_t q0 = smem_addr(sQ), k0 = smem_addr(sK), v0 = smem_addr(sV);
-        auto scores = [&](int i, int slot) {
-          const uint32_t kt = k0 + slot * S::KT, qt = q0 + i * S::QT;
+      // The whole warp goes through the loop and one lane issues: with descriptors built by one diverged
+      // thread an instruction took 115 cycles to issue where the tensor cores need 64.
+      const uint32_t idesc_s = idesc_bf16_f32(kPrRows, kPrKeys) | (a.negate ? 1u << 13 : 0u);   // bit 13: -A
+      constexpr uint32_t idesc_o = idesc_bf16_f32_bmn(kPrRows, D);
+      const uint64_t dq = sdesc_sw128(smem_addr(sQ)), dk = sdesc_sw128(smem_addr(sK));
+      const uint64_t dv = sdesc_sw128_mn(smem_addr(sV), kPrKeys * 128, 1024);
+      const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
+      const uint32_t qk_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32);
+      auto scores = [&](int i, int slot) {
+        const uint32_t ql = q_lo + i * (S::QT >> 4), kl = k_lo + slot * (S::KT >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < S::HALVES; ++h)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + S::S_COL + 128 * i, sdesc_sw128(qt + h * (kPrRows * 128) + ks * 32),
-                        sdesc_sw128(kt + h * (kPrKeys * 128) + ks * 32), idesc_s, (h | ks) != 0);
+              umma_bf16(tmem + S::S_COL + 128 * i, sdesc_from(ql + ((h * (kPrRows * 128) + ks * 32) >> 4), qk_hi),
+                        sdesc_from(kl + ((h * (kPrKeys * 128) + ks * 32) >> 4), qk_hi), idesc_s, (h | ks) != 0);
           umma_commit(&s_full[i]);
-        };
-        bool ok = true;
-        int kt = 0;                                               // key tiles of the items before
-        uint32_t clean_par = 0u, p_par = 0u;                      // parities of the next waits, by slot and by tile
-        for (int k = 0;; ++k) {
-          ok = read_item(k, it, nt, ntiles, masked_from);
-          if (!ok) break;
-          mbar_arrive(&item_empty[k & 1]);
-          if (!it.found) break;
-          ok = mbar_wait(&q_full, k & 1, a.wait_ns) && mbar_wait(&k_full[kt & 1], (kt >> 1) & 1, a.wait_ns);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (nt[i] > 0) scores(i, kt & 1);
-          umma_commit(&k_empty[kt & 1]);
-          if (ntiles == 1) umma_commit(&q_empty);
-          for (int j = 0; j < ntiles && ok; ++j) {
-            const int g = kt + j, s = g & 1, s1 = s ^ 1;
-            ok = mbar_wait(&v_full[s], (g >> 1) & 1, a.wait_ns);
-            if (ok && j >= masked_from) {
-              ok = mbar_wait(&v_clean[s], (clean_par >> s) & 1u, a.wait_ns);
-              clean_par ^= 1u << s;
-            }
-            if (ok && j + 1 < ntiles) ok = mbar_wait(&k_full[s1], ((g + 1) >> 1) & 1, a.wait_ns);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (!ok || j >= nt[i]) continue;
-              ok = mbar_wait(&p_ready[i], (p_par >> i) & 1u, a.wait_ns);
-              if (!ok) continue;
-              p_par ^= 1u << i;
-              tc_fence_after();
-              const uint32_t vt = v0 + s * S::KT;
-#pragma unroll
-              for (int ks = 0; ks < kPrKeys / 16; ++ks)
-                umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 8 * ks,
-                             sdesc_sw128_mn(vt + ks * 2048, kPrKeys * 128, 1024), idesc_o, (j | ks) != 0);
-              umma_commit(&o_done[i]);
-              if (j + 1 < nt[i]) scores(i, s1);
-            }
-            if (ok) {
-              umma_commit(&v_empty[s]);
-              if (j + 1 < ntiles) umma_commit(&k_empty[s1]);
-              if (j + 2 == ntiles) umma_commit(&q_empty);
-            }
-          }
-          if (!ok) break;
-          kt += ntiles;
         }
-        if (!ok) set_error(a.status, TS_ERR_TIMEOUT);
-        // no product may be under way when tensor memory is given back
-        umma_commit(&drained);
-        mbar_wait(&drained, 0, a.wait_ns);
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(kFull, mbar_wait(bar, parity, a.wait_ns)); };
+      bool ok = true;
+      int kt = 0;                                                 // key tiles of the items before
+      uint32_t clean_par = 0u, p_par = 0u;                        // parities of the next waits, by slot and by tile
+      for (int k = 0;; ++k) {
+        ok = __all_sync(kFull, read_item(k, it, nt, ntiles, masked_from));
+        if (!ok) break;
+        const bool found = __shfl_sync(kFull, it.found, 0) != 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) nt[i] = __shfl_sync(kFull, nt[i], 0);
+        ntiles = max(nt[0], nt[1]);
+        masked_from = __shfl_sync(kFull, masked_from, 0);
+        if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+        __syncwarp();
+        if (!found) break;
+        ok = wait(&q_full, k & 1) && wait(&k_full[kt & 1], (kt >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (nt[i] > 0) scores(i, kt & 1);
+        commit(&k_empty[kt & 1]);
+        if (ntiles == 1) commit(&q_empty);
+        for (int j = 0; j < ntiles && ok; ++j) {
+          const int g = kt + j, s = g & 1, s1 = s ^ 1;
+          ok = wait(&v_full[s], (g >> 1) & 1);
+          if (ok && j >= masked_from) {
+            ok = wait(&v_clean[s], (clean_par >> s) & 1u);
+            clean_par ^= 1u << s;
+          }
+          if (ok && j + 1 < ntiles) ok = wait(&k_full[s1], ((g + 1) >> 1) & 1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok || j >= nt[i]) continue;
+            const uint32_t vl = v_lo + s * (S::KT >> 4);
+            // the first 64 keys' product runs while the other 64 weights are formed
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && wait(&p_ready[i][h], (p_par >> i) & 1u);
+              if (!ok) continue;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                  umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 8 * ks,
+                               sdesc_from(vl + ((ks * 2048) >> 4), v_hi), idesc_o, (j | ks) != 0);
+                if (h == 1) umma_commit(&o_done[i]);
+              }
+              __syncwarp();
+            }
+            if (!ok) continue;
+            p_par ^= 1u << i;
+            if (j + 1 < nt[i]) scores(i, s1);
+          }
+          if (ok) {
+            commit(&v_empty[s]);
+            if (j + 1 < ntiles) commit(&k_empty[s1]);
+            if (j + 2 == ntiles) commit(&q_empty);
+          }
+        }
+        if (!ok) break;
+        kt += ntiles;
       }
+      if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
+      // no product may be under way when tensor memory is given back
+      commit(&drained);
+      mbar_wait(&drained, 0, a.wait_ns);
       __syncwarp();
     } else if (warp == kPrSoftmaxWarps + 2) {
       // ---------------------------------------------------------------- items
@@ -522,11 +548,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
               p[c] = pack_bf16(y0, y1);
             }
             tmem_st_x32(tS + 32 * h, p);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready[i][h]);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[i]);
           s_par ^= 1u;
         }
         // ---- outputs
