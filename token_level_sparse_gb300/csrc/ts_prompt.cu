@@ -16,6 +16,7 @@
 //   warp 9      products: S_i(j+1) = Q_i K(j+1)^T is issued behind O_i += P_i(j) V(j), so the tensor
 //               cores have the other tile's products to do while one tile's softmax runs
 //   warp 10     finds the next items
+//   warp 11     looks through the value tiles on the diagonal (below)
 //   warps 0-3   softmax of tile 0, a thread per row: scores from tensor memory, weights back over them; at
 //               the end of an item its outputs, while the next item is loaded and its first scores taken
 //   warps 4-7   the same of tile 1
@@ -43,7 +44,7 @@ namespace {
 constexpr int kPrRows = 128;     // query rows of a tile
 constexpr int kPrKeys = 128;     // tokens of a key tile
 constexpr int kPrSoftmaxWarps = 8;
-constexpr int kPrThreads = (kPrSoftmaxWarps + 4) * 32;   // three warpgroups; two warps of the third idle
+constexpr int kPrThreads = (kPrSoftmaxWarps + 4) * 32;   // three warpgroups
 // Registers a thread: 168 at launch (65536 / 384); the softmax warpgroups hold a row of 128 scores and
 // take what the third gives up: 2 * 208 + 88 = 3 * 168 (at 72 the products' warp spilled).
 constexpr int kPrSoftmaxRegs = 208, kPrOtherRegs = 88;
@@ -104,32 +105,34 @@ __device__ __forceinline__ int seq_blocks(const PromptArgs& a, int b, int block)
 // Numbers the blocks of all sequences in order of descending place in their sequence (one warp; results the
 // same in every lane). The blocks of the first 128 sequences stay in registers.
 struct BlockOrder {
-  int n[4];
+  int n[4], start[4];
   int most;       // blocks of the longest sequence
+  int all;        // blocks
 
   __device__ __forceinline__ void init(const PromptArgs& a, int block, int lane) {
     most = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      n[k] = lane + 32 * k < a.B ? seq_blocks(a, lane + 32 * k, block) : 0;
+      const int b = lane + 32 * k;
+      n[k] = b < a.B ? seq_blocks(a, b, block) : 0;
+      start[k] = b < a.B ? a.cu[b] : 0;
       most = max(most, n[k]);
     }
     for (int b = lane + 128; b < a.B; b += 32) most = max(most, seq_blocks(a, b, block));
     most = __reduce_max_sync(kFull, most);
+    all = from(a, block, 0, lane);
   }
   // number of blocks at place `level` of their sequence or behind it
   __device__ __forceinline__ int from(const PromptArgs& a, int block, int level, int lane) const {
-    int c = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) c += max(0, n[k] - level);
+    int c = max(0, n[0] - level);
+    if (a.B > 32) c += max(0, n[1] - level) + max(0, n[2] - level) + max(0, n[3] - level);
     for (int b = lane + 128; b < a.B; b += 32) c += max(0, seq_blocks(a, b, block) - level);
     return __reduce_add_sync(kFull, c);
   }
-  // block t: its sequence and place. False past the last one. `hi`: a level that block t is below
-  // (most at first, afterwards one above an earlier block's place).
-  __device__ __forceinline__ bool find(const PromptArgs& a, int block, int t, int& hi, int lane, int& seq, int& blk) const {
+  // block t < all: its sequence and place. `hi`: a level that block t is below (most at first,
+  // afterwards one above an earlier block's place).
+  __device__ __forceinline__ void find(const PromptArgs& a, int block, int t, int& hi, int lane, int& seq, int& blk) const {
     int lo = 0;
-    if (hi <= 0 || from(a, block, 0, lane) <= t) return false;
     while (hi - lo > 1) {            // from(lo) > t >= from(hi)
       const int mid = (lo + hi) >> 1;
       if (from(a, block, mid, lane) > t) lo = mid; else hi = mid;
@@ -142,12 +145,13 @@ struct BlockOrder {
                                 : (b0 + lane < a.B ? seq_blocks(a, b0 + lane, block) : 0);
       const unsigned m = __ballot_sync(kFull, mine > lo);
       if (rank < __popc(m)) {
-        seq = b0 + (int)__fns(m, 0, rank + 1);
-        return true;
+        // the lane with `rank` set bits below its own
+        const unsigned at = __ballot_sync(kFull, mine > lo && __popc(m & ((1u << lane) - 1u)) == rank);
+        seq = b0 + __ffs(at) - 1;
+        return;
       }
       rank -= __popc(m);
     }
-    return false;
   }
 };
 
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   unsigned char* sV = sK + 2 * S::KT;      // two value slots
   unsigned char* sO = sV + 2 * S::KT;      // output staging, one area per softmax warp
   __shared__ __align__(8) uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], s_full[2],
-      p_ready[2][2], o_done[2], item_full[2], item_empty[2], drained;
+      p_ready[2][2], o_done[2], item_full[2], item_empty[2], item_clean[2], drained;
   __shared__ uint32_t s_tmem;
   __shared__ PromptItem s_item[2];
   // what value tiles held that is not finite, per item slot: first row of a column's NaN, +inf, -inf, counted
@@ -200,20 +204,28 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-      mbar_init(&v_clean[i], kPrSoftmaxWarps);
+      mbar_init(&v_empty[i], 2);           // the products and the look through
+      mbar_init(&v_clean[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i][0], kPrSoftmaxWarps / 2);
       mbar_init(&p_ready[i][1], kPrSoftmaxWarps / 2);
       mbar_init(&o_done[i], 1);
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], kPrSoftmaxWarps + 2);
+      mbar_init(&item_empty[i], kPrSoftmaxWarps + 3);
+      mbar_init(&item_clean[i], 1);
       s_odd[i] = 0;
     }
     mbar_fence_init();
   }
   for (int i = tid; i < 2 * 3 * D; i += kPrThreads) (&s_first[0][0][0])[i] = kPrNone;
   tc_fence_before();
+  BlockOrder order;                        // (of warp 10, its loads under way before the others are set up)
+  if (warp == kPrSoftmaxWarps + 2) order.init(a, block, lane);
+  if (warp == kPrSoftmaxWarps && lane == 0) {
+    prefetch_tmap(&a.q);
+    prefetch_tmap(&a.k);
+    prefetch_tmap(&a.v);
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
@@ -383,14 +395,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           const int v = a.cu[b];
           if (v > a.total || (b == 0 ? v != 0 : v < a.cu[b - 1])) set_error(a.status, TS_ERR_SEQ_LEN);
         }
-      BlockOrder order;
-      order.init(a, block, lane);
       int level = order.most;
       bool found = true;
       for (int k = 0; found; ++k) {
         const int64_t t = (int64_t)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         int seq = 0, blk = 0;
-        found = t / a.HKV < 0x7fffffff && order.find(a, block, (int)(t / a.HKV), level, lane, seq, blk);
+        found = t < (int64_t)order.all * a.HKV;
+        if (found) order.find(a, block, (int)(t / a.HKV), level, lane, seq, blk);
+        const int row0 = seq < 128 ? __shfl_sync(kFull, seq < 32 ? order.start[0] : seq < 64 ? order.start[1] : seq < 96 ? order.start[2] : order.start[3], seq & 31)
+                                   : a.cu[seq];
+        const int end = a.cu[seq + 1];
         if (k >= 2 && !mbar_wait(&item_empty[k & 1], ((k >> 1) - 1) & 1, a.wait_ns)) {
           set_error(a.status, TS_ERR_TIMEOUT);
           break;
@@ -402,16 +416,64 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         }
         __syncwarp();
         if (lane == 0) {
-          PromptItem& o = s_item[k & 1];
-          o.found = found;
-          o.row0 = found ? a.cu[seq] : 0;
-          o.n = found ? a.cu[seq + 1] - a.cu[seq] : 0;
-          o.i0 = blk * block;
-          o.kv = (int)(t % a.HKV);
+          s_item[k & 1] = PromptItem{found, row0, end - row0, blk * block, (int)(t % a.HKV)};
           mbar_arrive(&item_full[k & 1]);
         }
         __syncwarp();
       }
+    } else {
+      // --------------------------------------------- what is not finite behind the diagonal
+      bool ok = true;
+      int kt = 0;
+      for (int k = 0;; ++k) {
+        ok = __all_sync(kFull, read_item(k, it, nt, ntiles, masked_from));
+        if (!ok || !it.found) break;
+        for (int j = 0; j < ntiles && ok; ++j) {
+          const int vs = (kt + j) & 1;
+          ok = __all_sync(kFull, mbar_wait(&v_full[vs], ((kt + j) >> 1) & 1, a.wait_ns));
+          if (!ok) break;
+          if (j >= masked_from) {
+            // the values of rows behind token i0 that are not finite come out of the tile
+            unsigned char* vt = sV + vs * S::KT;
+            uint32_t odd = 0u;
+#pragma unroll 8
+            for (int c = 0; c < S::KT / 512; ++c) {
+              const uint4 w = lds128(vt + c * 512 + lane * 16);
+              odd |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                     ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+            }
+            if (odd & 0x80008000u) {
+              for (int off = lane * 16; off < S::KT; off += 512) {               // byte in the tile
+                const int r = (off % (kPrKeys * 128)) / 128, key = j * kPrKeys + r;
+                const int col0 = off / (kPrKeys * 128) * 64 + (((off / 16) % 8) ^ (r & 7)) * 8;
+                if (key <= it.i0) continue;                       // every row of the block sees it
+                uint16_t* e16 = reinterpret_cast<uint16_t*>(vt + off);
+                for (int e = 0; e < 8; ++e) {
+                  const uint32_t u = e16[e];
+                  if ((u & 0x7f80u) != 0x7f80u) continue;
+                  min_u16(s_first[k & 1][(u & 0x7fu) ? 0 : (u >> 15 ? 2 : 1)], col0 + e, key - masked_from * kPrKeys);
+                  e16[e] = 0;
+                  s_odd[k & 1] = 1;
+                }
+              }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_clean[vs]);
+          }
+          // (also for the tiles not looked at: so this warp never falls a round behind the value slots)
+          if (lane == 0) mbar_arrive(&v_empty[vs]);
+          __syncwarp();
+        }
+        if (!ok) break;
+        kt += ntiles;
+        if (lane == 0) {
+          mbar_arrive(&item_clean[k & 1]);
+          mbar_arrive(&item_empty[k & 1]);
+        }
+        __syncwarp();
+      }
+      if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -421,75 +483,20 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     const uint32_t inv_g = 65536u / (uint32_t)a.G + 1u;           // r / G = (r inv_g) >> 16 for r < 128, G <= 16
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + S::S_COL + 128 * i + lane_off, tO = tmem + S::O_COL + 128 * i + lane_off;
-    bool ok = true, in_step = true;
-    int kt = 0;                                                   // key tiles of the items before
-    uint32_t clean_par = 0u;                                      // parity of the next use of v_clean, by slot
+    bool ok = true;
     uint32_t s_par = 0u;                                          // parity of the next score tile
     for (int k = 0; ok; ++k) {
       ok = __all_sync(kFull, read_item(k, it, nt, ntiles, masked_from));
       if (!ok || !it.found) break;
-      const int mine = nt[i], slot = k & 1;
-      if (mine == 0) {
-        // Past the sequence's end: nothing to do, and the other tile's warps look through the value tiles
-        // alone. Nothing keeps this warp in step with the value slots meanwhile.
-        for (int j = masked_from; j < ntiles; ++j) clean_par ^= 1u << ((kt + j) & 1);
-        in_step = false;
-      } else {
+      const int mine = __shfl_sync(kFull, i == 0 ? nt[0] : nt[1], 0), slot = k & 1;
+      if (mine > 0) {                                             // (else the tile lies past the sequence's end)
         const int first = it.i0 + i * a.tokens;                   // first token of the tile
         const int row_tok = (int)((uint32_t)row * inv_g >> 16), tok = first + row_tok;
         const bool real = row_tok < a.tokens && tok < it.n;
-        const int cleaners = nt[1] > 0 ? kPrSoftmaxWarps : kPrSoftmaxWarps / 2;
-        const int share = S::KT / cleaners;                       // bytes of a value tile to look through
         float m2 = -INFINITY, la = 0.f, lb = 0.f;                 // running maximum (base 2) and two halves of the sum
-        for (int j = 0; j < ntiles && ok; ++j) {
-          const int vs = (kt + j) & 1;
-          bool have_s = false;
-          if (j >= masked_from) {
-            if (!in_step) {
-              // the item's first scores are taken after all products of the items before
-              ok = __all_sync(kFull, mbar_wait(&s_full[i], s_par, a.wait_ns));
-              if (!ok) break;
-              have_s = in_step = true;
-            }
-            // this warp's part of the value tile: what is not finite behind token i0 comes out
-            ok = __all_sync(kFull, mbar_wait(&v_full[vs], ((kt + j) >> 1) & 1, a.wait_ns));
-            if (!ok) break;
-            unsigned char* vt = sV + vs * S::KT + warp * share;
-            uint32_t odd = 0u;
-#pragma unroll 4
-            for (int c = 0; c < share / 512; ++c) {
-              const uint4 w = lds128(vt + c * 512 + lane * 16);
-              odd |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
-                     ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
-            }
-            if (odd & 0x80008000u) {
-              for (int c = 0; c < share / 512; ++c) {
-                const int off = warp * share + c * 512 + lane * 16;              // byte in the tile
-                const int r = (off % (kPrKeys * 128)) / 128, key = j * kPrKeys + r;
-                const int col0 = off / (kPrKeys * 128) * 64 + (((off / 16) % 8) ^ (r & 7)) * 8;
-                if (key <= s_item[slot].i0) continue;             // every row of the block sees it
-                uint16_t* e16 = reinterpret_cast<uint16_t*>(sV + vs * S::KT + off);
-                for (int e = 0; e < 8; ++e) {
-                  const uint32_t u = e16[e];
-                  if ((u & 0x7f80u) != 0x7f80u) continue;
-                  min_u16(s_first[slot][(u & 0x7fu) ? 0 : (u >> 15 ? 2 : 1)], col0 + e, key - masked_from * kPrKeys);
-                  e16[e] = 0;
-                  s_odd[slot] = 1;
-                }
-              }
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&v_clean[vs]);
-              if (cleaners < kPrSoftmaxWarps) mbar_arrive(&v_clean[vs]);         // for a warp of the other tile
-            }
-            clean_par ^= 1u << vs;
-          }
-          if (j >= mine) continue;
-          if (!have_s) ok = __all_sync(kFull, mbar_wait(&s_full[i], s_par, a.wait_ns));
+        for (int j = 0; j < mine; ++j) {
+          ok = __all_sync(kFull, mbar_wait(&s_full[i], s_par, a.wait_ns));
           if (!ok) break;
-          in_step = true;
           tc_fence_after();
           uint32_t u[128];
 #pragma unroll
@@ -497,9 +504,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           tmem_wait_ld();
           float* x = reinterpret_cast<float*>(u);
           if (j * kPrKeys + kPrKeys - 1 > first) {                // the tile holds keys that a row may not see
-            const int lim = tok - j * kPrKeys;
+            const int lim = tok - j * kPrKeys;                    // ascending with the lanes
+            const int low = __shfl_sync(kFull, lim, 0);
 #pragma unroll
-            for (int c = 0; c < 128; ++c) x[c] = c <= lim ? x[c] : -INFINITY;
+            for (int c0 = 0; c0 < 128; c0 += 32) {
+              if (low < c0 + 31) {                                // (else every row of the warp sees these 32)
+#pragma unroll
+                for (int c = c0; c < c0 + 32; ++c) x[c] = c <= lim ? x[c] : -INFINITY;
+              }
+            }
           }
           float mx = x[0], my = x[1];
 #pragma unroll
@@ -557,16 +570,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         }
         // ---- outputs
         if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[i], s_par ^ 1u, a.wait_ns));
-        // what the value tiles held is known once every warp has looked through the last of them
-        for (int j = max(masked_from, ntiles - 2); j < ntiles && ok; ++j)
-          ok = __all_sync(kFull, mbar_wait(&v_clean[(kt + j) & 1], ((clean_par >> ((kt + j) & 1)) & 1u) ^ 1u, a.wait_ns));
+        if (ok) ok = __all_sync(kFull, mbar_wait(&item_clean[slot], (k >> 1) & 1, a.wait_ns));
         if (ok) {
           tc_fence_after();
           const float l = la + lb, inv = 1.f / l;
           const bool odd = s_odd[slot] != 0;
-          const int row0 = s_item[slot].row0, n = s_item[slot].n, head0 = s_item[slot].kv * a.G;
-          if (real && a.lse)
-            a.lse[(int64_t)(row0 + tok) * a.H + head0 + row - row_tok * a.G] = (m2 + log2f(l)) * 0.6931471805599453f;
+          const int row0 = s_item[slot].row0, head = s_item[slot].kv * a.G + row - row_tok * a.G;
+          if (real && a.lse) a.lse[(int64_t)(row0 + tok) * a.H + head] = (m2 + log2f(l)) * 0.6931471805599453f;
+          // this lane's output row; a null pointer where it is none
+          const uint64_t dst = real ? reinterpret_cast<uint64_t>(a.out + (int64_t)(row0 + tok) * a.out_stride + (int64_t)head * D) : 0u;
           unsigned char* stage = sO + warp * S::STAGE;
 #pragma unroll 1
           for (int h = 0; h < S::HALVES; ++h) {
@@ -600,12 +612,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
             __syncwarp();
 #pragma unroll
             for (int r4 = 0; r4 < 8; ++r4) {
-              const int rl = 4 * r4 + (lane >> 3), rr = 32 * (warp & 3) + rl, c16 = lane & 7;
-              const int rt = (int)((uint32_t)rr * inv_g >> 16), rh = rr - rt * a.G;
+              const int rl = 4 * r4 + (lane >> 3), c16 = lane & 7;
+              const uint64_t to = __shfl_sync(kFull, dst, rl);
               const uint4 v = lds128(stage + rl * 128 + ((c16 ^ (rl & 7)) << 4));
-              if (rt < a.tokens && first + rt < n)
-                *reinterpret_cast<uint4*>(a.out + (int64_t)(row0 + first + rt) * a.out_stride +
-                                          (int64_t)(head0 + rh) * D + 64 * h + c16 * 8) = v;
+              if (to) *reinterpret_cast<uint4*>(to + 128 * h + c16 * 16) = v;
             }
             __syncwarp();
           }
@@ -613,7 +623,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           tc_fence_before();
         }
       }
-      kt += ntiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_empty[slot]);
     }
