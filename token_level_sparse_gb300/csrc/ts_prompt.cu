@@ -20,9 +20,10 @@
 //   warps 0-3   softmax of tile 0, a thread per row: scores from tensor memory, weights back over them; at
 //               the end of an item its outputs, while the next item is loaded and its first scores taken
 //   warps 4-7   the same of tile 1
-// The running maximum moves only when a score passes it by 2^8: weights and sums stay below 2^8 times
-// their number, far inside fp32, and the accumulators are rescaled a handful of times per row. The
-// softmax warps do that themselves, in between two products of their tile.
+// The running maximum is taken anew only in tiles where the sum of the weights against the old one passes
+// 2^14: weights and sums stay far inside fp32 (and bf16 has the same relative error everywhere), most tiles
+// need no pass over the scores for a maximum, and the accumulators are rescaled a handful of times per row.
+// The softmax warps do that themselves, in between two products of their tile.
 //
 // Masked places hold what they hold. A score behind the diagonal is replaced before it is used. A
 // value behind the diagonal meets a weight of zero in the product, which is not enough for a NaN or
@@ -49,6 +50,7 @@ constexpr int kPrThreads = (kPrSoftmaxWarps + 4) * 32;   // three warpgroups
 // take what the third gives up: 2 * 208 + 88 = 3 * 168 (at 72 the products' warp spilled).
 constexpr int kPrSoftmaxRegs = 208, kPrOtherRegs = 88;
 static_assert(2 * kPrSoftmaxRegs + kPrOtherRegs <= 3 * 168, "register shares");
+constexpr float kPrMaxSum = 16384.f;   // of a tile's weights against a maximum taken earlier
 constexpr uint16_t kPrNone = 0xffff;
 
 struct PromptArgs {
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   unsigned char* sV = sK + 2 * S::KT;      // two value slots
   unsigned char* sO = sV + 2 * S::KT;      // output staging, one area per softmax warp
   __shared__ __align__(8) uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], s_full[2],
-      p_ready[2][2], o_done[2], item_full[2], item_empty[2], item_clean[2], drained;
+      p_ready[2], o_done[2], item_full[2], item_empty[2], item_clean[2], drained;
   __shared__ uint32_t s_tmem;
   __shared__ PromptItem s_item[2];
   // what value tiles held that is not finite, per item slot: first row of a column's NaN, +inf, -inf, counted
@@ -207,8 +209,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       mbar_init(&v_empty[i], 2);           // the products and the look through
       mbar_init(&v_clean[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_ready[i][0], kPrSoftmaxWarps / 2);
-      mbar_init(&p_ready[i][1], kPrSoftmaxWarps / 2);
+      mbar_init(&p_ready[i], kPrSoftmaxWarps / 2);
       mbar_init(&o_done[i], 1);
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], kPrSoftmaxWarps + 3);
@@ -355,22 +356,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           for (int i = 0; i < 2; ++i) {
             if (!ok || j >= nt[i]) continue;
             const uint32_t vl = v_lo + s * (S::KT >> 4);
-            // the first 64 keys' product runs while the other 64 weights are formed
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              ok = ok && wait(&p_ready[i][h], (p_par >> i) & 1u);
-              if (!ok) continue;
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                  umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 8 * ks,
-                               sdesc_from(vl + ((ks * 2048) >> 4), v_hi), idesc_o, (j | ks) != 0);
-                if (h == 1) umma_commit(&o_done[i]);
-              }
-              __syncwarp();
-            }
+            ok = wait(&p_ready[i], (p_par >> i) & 1u);
             if (!ok) continue;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 0; ks < kPrKeys / 16; ++ks)
+                umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 8 * ks,
+                             sdesc_from(vl + ((ks * 2048) >> 4), v_hi), idesc_o, (j | ks) != 0);
+              umma_commit(&o_done[i]);
+            }
+            __syncwarp();
             p_par ^= 1u << i;
             if (j + 1 < nt[i]) scores(i, s1);
           }
@@ -498,74 +494,85 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           ok = __all_sync(kFull, mbar_wait(&s_full[i], s_par, a.wait_ns));
           if (!ok) break;
           tc_fence_after();
-          uint32_t u[128];
+          // Weights against the maximum that the row has, which covers most tiles. Where their sum says that
+          // it does not (and in the first tile, which has none), the scores, still in tensor memory, are read
+          // again and the maximum is taken first.
+          uint32_t p[64];
+          float ta, tb;
+          bool over = real;                                       // this row needs its maximum (in a pass that takes it)
+          for (bool raise = j == 0;; raise = true) {
+            uint32_t u[128];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_x32(tS + 32 * c, u + 32 * c);
-          tmem_wait_ld();
-          float* x = reinterpret_cast<float*>(u);
-          if (j * kPrKeys + kPrKeys - 1 > first) {                // the tile holds keys that a row may not see
-            const int lim = tok - j * kPrKeys;                    // ascending with the lanes
-            const int low = __shfl_sync(kFull, lim, 0);
+            for (int c = 0; c < 4; ++c) tmem_ld_x32(tS + 32 * c, u + 32 * c);
+            tmem_wait_ld();
+            float* x = reinterpret_cast<float*>(u);
+            if (j * kPrKeys + kPrKeys - 1 > first) {              // the tile holds keys that a row may not see
+              const int lim = tok - j * kPrKeys;                  // ascending with the lanes
+              const int low = __shfl_sync(kFull, lim, 0);
 #pragma unroll
-            for (int c0 = 0; c0 < 128; c0 += 32) {
-              if (low < c0 + 31) {                                // (else every row of the warp sees these 32)
+              for (int c0 = 0; c0 < 128; c0 += 32) {
+                if (low < c0 + 31) {                              // (else every row of the warp sees these 32)
 #pragma unroll
-                for (int c = c0; c < c0 + 32; ++c) x[c] = c <= lim ? x[c] : -INFINITY;
+                  for (int c = c0; c < c0 + 32; ++c) x[c] = c <= lim ? x[c] : -INFINITY;
+                }
               }
             }
-          }
-          float mx = x[0], my = x[1];
+            if (raise) {
+              float mx = x[0], my = x[1];
 #pragma unroll
-          for (int c = 2; c < 128; c += 2) {
-            mx = fmaxf(mx, x[c]);
-            my = fmaxf(my, x[c + 1]);
-          }
-          // rows that are no query of the sequence (their operands may be anything) move no maximum
-          const float top = real ? fmaxf(mx, my) * a.scale2 : -INFINITY;
-          if (__any_sync(kFull, top > m2 + 8.f)) {
-            const float mn = fmaxf(m2, top);
-            const float f = mn == m2 ? 1.f : pr_ex2(m2 - mn);
-            m2 = mn;
-            la *= f;
-            lb *= f;
-            if (j > 0) {
-              // the tile's last product must be in before its accumulators are rescaled
-              ok = __all_sync(kFull, mbar_wait(&o_done[i], s_par ^ 1u, a.wait_ns));
-              if (!ok) break;
-              tc_fence_after();
-              // (rare, and the scores hold most registers: eight columns at a time)
+              for (int c = 2; c < 128; c += 2) {
+                mx = fmaxf(mx, x[c]);
+                my = fmaxf(my, x[c + 1]);
+              }
+              // each row by itself, so that no row's bits depend on another's: rows that do not need it keep their
+              // maximum, as do rows that are no query of the sequence (their operands may be anything)
+              const float mn = over ? fmaxf(m2, fmaxf(mx, my) * a.scale2) : m2;
+              const float f = mn == m2 ? 1.f : pr_ex2(m2 - mn);
+              m2 = mn;
+              la *= f;
+              lb *= f;
+              if (j > 0) {
+                // the tile's last product must be in before its accumulators are rescaled
+                ok = __all_sync(kFull, mbar_wait(&o_done[i], s_par ^ 1u, a.wait_ns));
+                if (!ok) break;
+                tc_fence_after();
+                // (rare, and the scores hold most registers: eight columns at a time)
 #pragma unroll 1
-              for (int c = 0; c < D; c += 8) {
-                float o[8];
-                tmem_ld_x8(tO + c, o);
-                tmem_wait_ld();
+                for (int c = 0; c < D; c += 8) {
+                  float o[8];
+                  tmem_ld_x8(tO + c, o);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] *= f;
-                tmem_st_x8(tO + c, o);
+                  for (int e = 0; e < 8; ++e) o[e] *= f;
+                  tmem_st_x8(tO + c, o);
+                }
               }
             }
-          }
-          const float ms = m2 == -INFINITY ? 0.f : -m2;           // nothing seen yet: every weight is zero
-          const uint64_t sc = pack_f2(a.scale2, a.scale2), mm = pack_f2(ms, ms);
+            const float ms = m2 == -INFINITY ? 0.f : -m2;         // nothing seen yet: every weight is zero
+            const uint64_t sc = pack_f2(a.scale2, a.scale2), mm = pack_f2(ms, ms);
+            ta = tb = 0.f;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int e = 64 * h + 2 * c;
+            for (int c = 0; c < 64; ++c) {
               float y0, y1;
-              unpack_f2(fma_f2(pack_f2(x[e], x[e + 1]), sc, mm), y0, y1);
+              unpack_f2(fma_f2(pack_f2(x[2 * c], x[2 * c + 1]), sc, mm), y0, y1);
               y0 = pr_ex2(y0);
               y1 = pr_ex2(y1);
-              add2(la, lb, y0, y1);
+              add2(ta, tb, y0, y1);
               p[c] = pack_bf16(y0, y1);
             }
-            tmem_st_x32(tS + 32 * h, p);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[i][h]);
+            if (raise) break;
+            over = real && !(ta + tb <= kPrMaxSum);
+            if (!__any_sync(kFull, over)) break;
           }
+          if (!ok) break;
+          la += ta;
+          lb += tb;
+          tmem_st_x32(tS, p);
+          tmem_st_x32(tS + 32, p + 32);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[i]);
           s_par ^= 1u;
         }
         // ---- outputs
