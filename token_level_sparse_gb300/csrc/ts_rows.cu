@@ -34,11 +34,19 @@ struct RowsArgs {
 
 // Place of the CTA's rows: page * page size + slot, or -1 (no such position; recorded).
 __device__ __forceinline__ void place_rows(const RowsArgs& a, int64_t* place) {
+  // the boundaries of up to 256 sequences in shared memory: one read instead of one per step of the search
+  __shared__ int32_t s_cu[257];
+  const int32_t* cu = a.cu;
+  if (a.cu && a.B <= 256) {
+    for (int b = threadIdx.x; b <= a.B; b += blockDim.x) s_cu[b] = a.cu[b];
+    __syncthreads();
+    cu = s_cu;
+  }
   if (a.cu && blockIdx.x == 0) {
     // the boundaries: ascending, from 0, within the rows that there are
     for (int b = threadIdx.x; b <= a.B; b += blockDim.x) {
-      const int v = a.cu[b];
-      if (v > a.total || (b == 0 ? v != 0 : v < a.cu[b - 1])) set_error(a.status, TS_ERR_SEQ_LEN);
+      const int v = cu[b];
+      if (v > a.total || (b == 0 ? v != 0 : v < cu[b - 1])) set_error(a.status, TS_ERR_SEQ_LEN);
     }
   }
   if ((int)threadIdx.x < a.rows_per_cta) {
@@ -52,12 +60,12 @@ __device__ __forceinline__ void place_rows(const RowsArgs& a, int64_t* place) {
         int lo = 0, hi = a.B;              // the last b with cu[b] <= r
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
-          if (a.cu[mid] <= r) lo = mid; else hi = mid;
+          if (cu[mid] <= r) lo = mid; else hi = mid;
         }
         b = lo;
-        inside = r >= a.cu[b] && r < a.cu[b + 1];   // rows behind the last sequence stay as they are
-        pos = (a.starts ? a.starts[b] : 0) + (r - a.cu[b]);
-        if (a.starts && a.starts[b] < 0) pos = -1;
+        inside = r >= cu[b] && r < cu[b + 1];       // rows behind the last sequence stay as they are
+        const int start = a.starts ? a.starts[b] : 0;
+        pos = start < 0 ? -1 : start + (r - cu[b]);
       } else {
         pos = (int64_t)a.seq_lens[b] - 1;
       }
@@ -112,68 +120,110 @@ __global__ void __launch_bounds__(kRowsThreads) append_rows_kernel(const __grid_
 template <int NB, int ROWS>
 __global__ void __launch_bounds__(kRowsThreads) append_q4_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ int64_t place[kRowsPerCta];
-  place_rows(a, place);
   constexpr int D = NB * 64, BLK = q4_block_bytes(D), CODES = q4_code_bytes(D), COLS = kRowsThreads / 8 / ROWS;
+  constexpr int BATCH = 4;               // loads under way per thread
   const int groups = a.HKV * NB, lane8 = threadIdx.x & 7;
   // neighbouring groups of eight lanes take neighbouring rows of the same 64 elements: their codes
   // are neighbours in the block
   const int row = (threadIdx.x >> 3) % ROWS;
   const int64_t r = (int64_t)blockIdx.x * ROWS + row;
+  const unsigned peers = 0xffu << (threadIdx.x & 24);
+  uint4 raw[BATCH];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int i = i0 + k * COLS, isv = i >= groups, c = isv ? i - groups : i;
+      raw[k] = r < a.total && i < 2 * groups ? ldg_nc128(a.src[isv] + r * a.src_stride[isv] + c * 128 + lane8 * 16)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  const int first = (threadIdx.x >> 3) / ROWS;
+  load(first);                           // on their way while the rows' places are looked up
+  place_rows(a, place);
   const int64_t at = place[row];
   const int slot = (int)(at & 15);
-  const unsigned peers = 0xffu << (threadIdx.x & 24);
-#pragma unroll 4
-  for (int i = (threadIdx.x >> 3) / ROWS; i < 2 * groups; i += COLS) {
-    const int isv = i >= groups, c = isv ? i - groups : i, g = c / NB, nb = c % NB;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (at >= 0) v = ldg_nc128(a.src[isv] + r * a.src_stride[isv] + c * 128 + lane8 * 16);
-    float x[8];
-    KV<__nv_bfloat16>::unpack(v, x);
-    // the largest magnitude by its bits: ordered like the values, with infinities and NaN on top
-    uint32_t mb = 0u;
+  for (int i0 = first; i0 < 2 * groups; i0 += BATCH * COLS) {
+    if (i0 != first) load(i0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mb = max(mb, __float_as_uint(x[e]) & 0x7fffffffu);
+    for (int k = 0; k < BATCH; ++k) {
+      const int i = i0 + k * COLS, isv = i >= groups, c = isv ? i - groups : i, g = c / NB, nb = c % NB;
+      if (i >= 2 * groups) break;        // (the same in all eight lanes)
+      const uint32_t in[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+      // the largest magnitude by its bits, two at a time: ordered like the values, with infinities and NaN on top
+      uint32_t mb = 0u;
 #pragma unroll
-    for (int d = 4; d >= 1; d >>= 1) mb = max(mb, __shfl_xor_sync(peers, mb, d));
-    const float top = __uint_as_float(mb);
-    __nv_bfloat16 sb;
-    uint32_t w = 0u;
-    if (top >= 0x1p-100f && top < INFINITY) {
-      sb = __float2bfloat16_rn(top * (1.f / 7.f));
-      const float s = __bfloat162float(sb), r = __frcp_rn(s);
+      for (int e = 0; e < 4; ++e) mb = __vmaxu2(mb, in[e] & 0x7fff7fffu);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float q = x[e] * r;
-        q = fmaf(fmaf(-q, s, x[e]), r, q);
-        // rounds to a whole number, 8 + code in the low bits: |q| < 7.1, since s >= top / 7 (1 - 2^-8)
-        w |= (__float_as_uint(q + 12582920.f) & 15u) << (4 * e);
+      for (int d = 4; d >= 1; d >>= 1) mb = __vmaxu2(mb, __shfl_xor_sync(peers, mb, d));
+      const float top = bf16_bits_f(max(mb & 0xffffu, mb >> 16));
+      __nv_bfloat16 sb;
+      uint32_t w;
+      if (top >= 0x1p-100f && top < INFINITY) {
+        sb = __float2bfloat16_rn(top * (1.f / 7.f));
+        const float s = __bfloat162float(sb);
+        float rs;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(s));
+        const uint64_t s2 = pack_f2(-s, -s), r2 = pack_f2(rs, rs), zero = pack_f2(0.f, 0.f),
+                       magic = pack_f2(12582920.f, 12582920.f), one = pack_f2(1.f, 1.f);
+        uint32_t u[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t x = pack_f2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u));
+          uint64_t q = fma_f2(x, r2, zero);
+          q = fma_f2(fma_f2(q, s2, x), r2, q);
+          // a whole number behind the sum's point: 8 + code in the low byte, since |q| < 7.1 (s >= top / 7 (1 - 2^-8))
+          float lo, hi;
+          unpack_f2(fma_f2(q, one, magic), lo, hi);
+          u[2 * e] = __float_as_uint(lo);
+          u[2 * e + 1] = __float_as_uint(hi);
+        }
+        const uint32_t even = __byte_perm(__byte_perm(u[0], u[2], 0x0040), __byte_perm(u[4], u[6], 0x0040), 0x5410);
+        const uint32_t odd = __byte_perm(__byte_perm(u[1], u[3], 0x0040), __byte_perm(u[5], u[7], 0x0040), 0x5410);
+        w = even | odd << 4;
+      } else {
+        sb = __float2bfloat16_rn(__fdiv_rn(top, 7.f));
+        const float s = __bfloat162float(sb);
+        const bool live = s > 0.f && s < INFINITY;
+        w = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = __uint_as_float(e & 1 ? in[e >> 1] & 0xffff0000u : in[e >> 1] << 16);
+          const int q = live ? max(-7, min(7, __float2int_rn(__fdiv_rn(x, s)))) : 0;
+          w |= (uint32_t)(q + 8) << (4 * e);
+        }
       }
-    } else {
-      sb = __float2bfloat16_rn(__fdiv_rn(top, 7.f));
-      const float s = __bfloat162float(sb);
-      const bool live = s > 0.f && s < INFINITY;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int q = live ? max(-7, min(7, __float2int_rn(__fdiv_rn(x[e], s)))) : 0;
-        w |= (uint32_t)(q + 8) << (4 * e);
+      if (at >= 0) {
+        unsigned char* base = a.pool[isv] + ((at >> 4) * a.HKV + g) * BLK;
+        *reinterpret_cast<uint32_t*>(base + nb * 512 + slot * 32 + lane8 * 4) = w;
+        if (lane8 == 0) *reinterpret_cast<__nv_bfloat16*>(base + CODES + nb * 32 + slot * 2) = sb;
       }
-    }
-    if (at >= 0) {
-      unsigned char* base = a.pool[isv] + ((at >> 4) * a.HKV + g) * BLK;
-      *reinterpret_cast<uint32_t*>(base + nb * 512 + slot * 32 + lane8 * 4) = w;
-      if (lane8 == 0) *reinterpret_cast<__nv_bfloat16*>(base + CODES + nb * 32 + slot * 2) = sb;
     }
   }
 }
 
 // Rows of a pool as fp32 values: exact for every pool type (a code times a bf16 scale has 12
-// significant bits). Eight elements a thread, eight threads to 64 elements of one row, neighbouring
-// rows next to one another as in the append.
+// significant bits). Eight threads to 64 elements of one row, thread l elements 4l .. 4l + 3 and 32 + 4l .. ,
+// so that each of its two stores fills whole sectors with its neighbours'.
+template <int kType>
+struct RawQuads;                         // the raw elements of one thread
+template <>
+struct RawQuads<TS_KV_Q4> {
+  uint32_t lo, hi, scale;
+};
+template <>
+struct RawQuads<TS_KV_BF16> {
+  uint2 lo, hi;
+};
+template <>
+struct RawQuads<TS_KV_F32> {
+  float4 lo, hi;
+};
+
 template <int kType, int ROWS>
 __global__ void __launch_bounds__(kRowsThreads) read_rows_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ int64_t place[kRowsPerCta];
   place_rows(a, place);
-  constexpr int COLS = kRowsThreads / 8 / ROWS;
+  constexpr int COLS = kRowsThreads / 8 / ROWS, BATCH = 4;
   const int NB = a.D / 64, groups = a.HKV * NB, lane8 = threadIdx.x & 7, ps = 1 << a.page_shift;
   const int row = (threadIdx.x >> 3) % ROWS;
   const int64_t r = (int64_t)blockIdx.x * ROWS + row;
@@ -182,30 +232,51 @@ __global__ void __launch_bounds__(kRowsThreads) read_rows_kernel(const __grid_co
   const int64_t page = at >> a.page_shift;
   const int slot = (int)(at & (ps - 1));
   const int codes = q4_code_bytes(a.D), blk = q4_block_bytes(a.D), half = NB >> 1;   // NB is 1 or 2
-#pragma unroll 4
-  for (int i = (threadIdx.x >> 3) / ROWS; i < 2 * groups; i += COLS) {
-    const int isv = i >= groups, c = isv ? i - groups : i, g = c >> half, nb = c & half;
-    float x[8];
-    if constexpr (kType == TS_KV_Q4) {
-      const unsigned char* base = a.pool[isv] + (page * a.HKV + g) * blk;
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(base + nb * 512 + slot * 32 + lane8 * 4);
-      const float s = bf16_bits_f(*reinterpret_cast<const uint16_t*>(base + codes + nb * 32 + slot * 2));
+  for (int i0 = (threadIdx.x >> 3) / ROWS; i0 < 2 * groups; i0 += BATCH * COLS) {
+    RawQuads<kType> raw[BATCH];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w >> (4 * e)) & 15u) - 8) * s;
-    } else {
-      constexpr int ES = kType == TS_KV_BF16 ? 2 : 4;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.pool[isv] + (((page * a.HKV + g) * ps + slot) * a.D + nb * 64 + lane8 * 8) * ES);
-      if constexpr (kType == TS_KV_BF16) {
-        KV<__nv_bfloat16>::unpack(src[0], x);
+    for (int k = 0; k < BATCH; ++k) {
+      const int i = i0 + k * COLS, isv = i >= groups, c = isv ? i - groups : i, g = c >> half, nb = c & half;
+      if (i >= 2 * groups) break;
+      if constexpr (kType == TS_KV_Q4) {
+        const unsigned char* base = a.pool[isv] + (page * a.HKV + g) * blk;
+        const unsigned char* piece = base + nb * 512 + slot * 32 + lane8 * 2;
+        raw[k].lo = *reinterpret_cast<const uint16_t*>(piece);
+        raw[k].hi = *reinterpret_cast<const uint16_t*>(piece + 16);
+        raw[k].scale = *reinterpret_cast<const uint16_t*>(base + codes + nb * 32 + slot * 2);
       } else {
-        KV<float>::unpack(src[0], x);
-        KV<float>::unpack(src[1], x + 4);
+        using Quad = decltype(raw[k].lo);
+        constexpr int ES = kType == TS_KV_BF16 ? 2 : 4;
+        const unsigned char* src = a.pool[isv] + (((page * a.HKV + g) * ps + slot) * a.D + nb * 64 + lane8 * 4) * ES;
+        raw[k].lo = *reinterpret_cast<const Quad*>(src);
+        raw[k].hi = *reinterpret_cast<const Quad*>(src + 32 * ES);
       }
     }
-    float4* dst = reinterpret_cast<float4*>(a.dst[isv] + r * a.HKV * a.D + c * 64 + lane8 * 8);
-    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int i = i0 + k * COLS, isv = i >= groups, c = isv ? i - groups : i;
+      if (i >= 2 * groups) break;
+      float4 lo, hi;
+      if constexpr (kType == TS_KV_Q4) {
+        const float s = bf16_bits_f(raw[k].scale);
+        auto value = [&](uint32_t w, int e) { return (float)((int)((w >> (4 * e)) & 15u) - 8) * s; };
+        lo = make_float4(value(raw[k].lo, 0), value(raw[k].lo, 1), value(raw[k].lo, 2), value(raw[k].lo, 3));
+        hi = make_float4(value(raw[k].hi, 0), value(raw[k].hi, 1), value(raw[k].hi, 2), value(raw[k].hi, 3));
+      } else if constexpr (kType == TS_KV_BF16) {
+        auto quad = [](uint2 w) {
+          return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                             __uint_as_float(w.y & 0xffff0000u));
+        };
+        lo = quad(raw[k].lo);
+        hi = quad(raw[k].hi);
+      } else {
+        lo = raw[k].lo;
+        hi = raw[k].hi;
+      }
+      float* dst = a.dst[isv] + r * a.HKV * a.D + c * 64 + lane8 * 4;
+      *reinterpret_cast<float4*>(dst) = lo;
+      *reinterpret_cast<float4*>(dst + 32) = hi;
+    }
   }
 }
 
