@@ -27,8 +27,11 @@
 namespace ts {
 namespace {
 
+constexpr int kScanSeqs = 512;                  // sequences whose page counts a scan CTA keeps in shared memory
 constexpr int kQ4Sets = 4;                      // head sets of a CTA, at most
 constexpr int kGatherWarps = 4;
+constexpr int kGatherCtas = 4;                  // gather CTAs per SM
+constexpr int gather_ctas(int nb, int nt) { return nb * nt == 4 ? 3 : kGatherCtas; }   // (3: registers)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Q4Args {
@@ -66,22 +69,36 @@ __device__ __forceinline__ int seq_pages(const Q4Args& a, int b) {
   return (n < 0 || n > a.max_tokens) ? 0 : (n + kPage - 1) / kPage;
 }
 
-// CTAs of a group that get pages: a share is about one page for every warp of a head set, so a
-// short batch does not spread over CTAs whose merge would cost more than their pages.
-__device__ __forceinline__ int live_ctas(int64_t total, int ctas) {
-  const int64_t want = (total + 3) / 4;
-  return (int)(want < 1 ? 1 : (want < ctas ? want : ctas));
-}
-
 // Weight of a part with maximum m in a join with maximum M. Equal maxima weigh 1 also where both are
 // -inf: an empty part brings zeros, a part of NaN logits brings its NaN.
 __device__ __forceinline__ float part_weight(float m, float M) { return m == M ? 1.f : ex2(m - M); }
 
-// Total pages of the batch and of the sequences before `upto` (one warp; the same in every lane).
-__device__ __forceinline__ void count_pages(const Q4Args& a, int upto, int lane, int64_t& total, int64_t& before) {
+// How the pages of the batch are shared out over the CTAs of a group. Two ways:
+//  * each sequence gets CTAs of its own, one for every `chunk` pages (4 at least: about a page for every
+//    warp of a head set), so that no CTA has parts of two sequences;
+//  * the pages of all sequences, one behind another, are cut into equal contiguous ranges.
+// A CTA that ends one sequence and begins another pays for both beginnings and ends, 6 us where a page takes
+// 0.26 us; rounding up to whole CTAs costs up to chunk - total / ctas pages. The first way is taken where
+// that is below 24 pages, and there are more CTAs than sequences.
+constexpr int kScanSlack = 24;
+
+struct Q4Share {
+  int64_t total, before;    // pages of the batch, and of the sequences before the one asked for
+  int ctas, chunk;          // chunk 0: equal ranges
+  int first;                // chunk > 0: first CTA of the sequence asked for
+
+  __device__ __forceinline__ int live() const {
+    const int64_t want = (total + 3) / 4;
+    return (int)(want < 1 ? 1 : (want < ctas ? want : ctas));
+  }
+};
+
+// (one warp; the same in every lane) pages(b): pages of sequence b
+template <typename Pages>
+__device__ __forceinline__ Q4Share share_pages(const Q4Args& a, int upto, int lane, Pages pages) {
   int64_t t = 0, u = 0;
   for (int b = lane; b < a.B; b += 32) {
-    const int n = seq_pages(a, b);
+    const int n = pages(b);
     t += n;
     if (b < upto) u += n;
   }
@@ -90,31 +107,64 @@ __device__ __forceinline__ void count_pages(const Q4Args& a, int upto, int lane,
     t += __shfl_xor_sync(kFull, t, d);
     u += __shfl_xor_sync(kFull, u, d);
   }
-  total = t;
-  before = u;
+  Q4Share sh{t, u, a.ctas, 0, 0};
+  if (a.ctas > a.B) {
+    const int64_t room = a.ctas - a.B, chunk = max((int64_t)4, (t + room - 1) / room);   // sum of ceil(pages / chunk) <= ctas
+    if (chunk * a.ctas < t + (int64_t)kScanSlack * a.ctas) {
+      sh.chunk = (int)chunk;
+      int f = 0;
+      for (int b = lane; b < upto; b += 32) f += (pages(b) + sh.chunk - 1) / sh.chunk;
+      sh.first = __reduce_add_sync(kFull, f);
+    }
+  }
+  return sh;
 }
 
-// The part of one CTA's page range that lies in one sequence.
+// The pages left to a CTA: `left` of them, from page `page` of sequence `b` on.
 struct Q4Range {
-  int64_t at, end;   // pages of the batch left to this CTA
-  int b;             // sequence of `at`
-  int64_t b0;        // first page of sequence b in the batch
+  int b, page, left;
 };
 
-__device__ __forceinline__ bool next_part(const Q4Args& a, Q4Range& r, int& b, int& p0, int& p1) {
-  while (r.at < r.end && r.b < a.B) {
-    const int np = seq_pages(a, r.b);
-    if (r.at < r.b0 + np) {
-      b = r.b;
-      p0 = (int)(r.at - r.b0);
-      p1 = (int)min((int64_t)np, r.end - r.b0);
-      r.at = r.b0 + p1;
+template <typename Pages>
+__device__ __forceinline__ bool next_part(const Q4Args& a, Q4Range& r, Pages pages, int& b, int& p0, int& p1) {
+  while (r.left > 0 && r.b < a.B) {
+    const int np = pages(r.b);
+    b = r.b++;
+    p0 = r.page;
+    r.page = 0;
+    if (p0 < np) {
+      p1 = min(np, p0 + r.left);
+      r.left -= p1 - p0;
       return true;
     }
-    r.b0 += np;
-    ++r.b;
   }
   return false;
+}
+
+// The range of one of `ctas` equal shares.
+template <typename Pages>
+__device__ __forceinline__ Q4Range equal_range(const Q4Args& a, int64_t total, int cta, int ctas, Pages pages) {
+  int64_t at = total * cta / ctas;
+  Q4Range r{0, 0, (int)(total * (cta + 1) / ctas - at)};
+  while (r.b < a.B && at >= pages(r.b)) at -= pages(r.b++);
+  r.page = (int)at;
+  return r;
+}
+
+// The range of CTA `cta` of a scan (every thread of a warp; all the same).
+template <typename Pages>
+__device__ __forceinline__ Q4Range cta_range(const Q4Args& a, const Q4Share& sh, int cta, Pages pages) {
+  if (sh.chunk == 0) return cta < sh.live() ? equal_range(a, sh.total, cta, sh.live(), pages) : Q4Range{0, 0, 0};
+  int c = cta;
+  for (int b = 0; b < a.B; ++b) {
+    const int np = pages(b), f = (np + sh.chunk - 1) / sh.chunk;
+    if (c < f) {
+      const int at = (int)((int64_t)np * c / f);
+      return Q4Range{b, at, (int)((int64_t)np * (c + 1) / f) - at};
+    }
+    c -= f;
+  }
+  return Q4Range{0, 0, 0};
 }
 
 // Shape of a scan CTA (one per SM). As many warps as the registers of one lane's state allow: with 16
@@ -145,7 +195,9 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) uint64_t full[R::WARPS][R::STAGES];
   __shared__ float2 s_ml[R::WARPS][4 * NT];
-  __shared__ Q4Range s_range;
+  __shared__ int s_pages[kScanSeqs];
+  __shared__ Q4Range s_left;           // the CTA's pages that no part has been made of yet
+  __shared__ int s_part[4];            // the part at work: is there one, sequence, first page, end
 
   // (values that are the same in a whole warp pass through a shuffle where they steer loops, so that
   // the compiler knows and needs no divergence handling there)
@@ -155,31 +207,34 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
   const int per_set = R::WARPS / nsets;                            // (some warps may be left over)
   launch_dependents();
 
-  if (warp == 0) {
-    // this CTA's pages of the batch
-    int64_t total, before;
-    count_pages(a, 0, lane, total, before);
-    if (lane == 0) {
-      const int nc = live_ctas(total, a.ctas);
-      Q4Range r;
-      r.at = cta < nc ? total * cta / nc : 0;
-      r.end = cta < nc ? total * (cta + 1) / nc : 0;
-      r.b = 0;
-      r.b0 = 0;
-      s_range = r;
+  for (int b = tid; b < min(a.B, kScanSeqs); b += R::WARPS * 32) s_pages[b] = seq_pages(a, b);
+  if (blockIdx.x == 0)
+    for (int b = tid; b < a.B; b += R::WARPS * 32) {
+      const int n = a.seq_lens[b];
+      if (!(a.skip && a.skip[b]) && (n < 0 || n > a.max_tokens)) set_error(a.status, TS_ERR_SEQ_LEN);
     }
-    if (cta == 0 && group == 0)
-      for (int b = lane; b < a.B; b += 32) {
-        const int n = a.seq_lens[b];
-        if (!(a.skip && a.skip[b]) && (n < 0 || n > a.max_tokens)) set_error(a.status, TS_ERR_SEQ_LEN);
-      }
-  }
   if (lane == 0) {
     for (int s = 0; s < R::STAGES; ++s) mbar_init(&full[warp][s], 1);
     mbar_fence_init();
   }
   __syncthreads();
-  Q4Range r = s_range;
+  // (the share and its parts are kept in shared memory by one thread: registers are short in the loop)
+  auto pages = [&](int b) { return b < kScanSeqs ? s_pages[b] : seq_pages(a, b); };
+  auto make_part = [&]() {
+    int b = 0, p0 = 0, p1 = 0;
+    s_part[0] = next_part(a, s_left, pages, b, p0, p1);
+    s_part[1] = b;
+    s_part[2] = p0;
+    s_part[3] = p1;
+  };
+  if (warp == 0) {
+    const Q4Range r = cta_range(a, share_pages(a, 0, lane, pages), cta, pages);
+    if (lane == 0) {
+      s_left = r;
+      make_part();
+    }
+  }
+  __syncthreads();
 
   const int hs = warp / per_set, j = warp % per_set;
   const bool works = hs < nsets;
@@ -191,12 +246,9 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
   uint64_t* bars = full[warp];
   uint32_t phases = 0u;                                            // bit s: parity of the stage's next wait
   bool ok = works;
-  int b, p0, p1;
-  while (next_part(a, r, b, p0, p1)) {
-    b = __shfl_sync(kFull, b, 0);
-    p0 = __shfl_sync(kFull, p0, 0);
-    p1 = __shfl_sync(kFull, p1, 0);
-    const int n = __shfl_sync(kFull, a.seq_lens[b], 0);
+  while (s_part[0]) {
+    const int b = __shfl_sync(kFull, s_part[1], 0), p0 = __shfl_sync(kFull, s_part[2], 0),
+              p1 = __shfl_sync(kFull, s_part[3], 0), n = __shfl_sync(kFull, a.seq_lens[b], 0);
     // this warp's pages: p0 + j, p0 + j + per_set, ...; lane i holds the id of the next 32 to copy
     const int32_t* pt = a.page_table + (size_t)b * a.pt_stride;
     const int mine = ok && p0 + j < p1 ? (p1 - p0 - j + per_set - 1) / per_set : 0;
@@ -393,20 +445,25 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
       }
       fence_proxy_async();                                         // these areas are copied into again
     }
+    if (tid == 0) make_part();                                     // (every warp has read the old one)
     __syncthreads();
   }
 }
 
 // The parts of a sequence's scan that exist: slots [first, first + count).
 __device__ __forceinline__ void scan_slots(const Q4Args& a, int b, int lane, int64_t& first, int& count) {
-  int64_t total, before;
-  count_pages(a, b, lane, total, before);
+  const Q4Share sh = share_pages(a, b, lane, [&](int i) { return seq_pages(a, i); });
   const int np = seq_pages(a, b);
   count = 0;
   first = 0;
   if (np == 0) return;
-  const int nc = live_ctas(total, a.ctas);
-  const int c0 = (int)(((before + 1) * nc - 1) / total), c1 = (int)(((before + np) * nc - 1) / total);
+  if (sh.chunk > 0) {
+    first = sh.first + b;
+    count = (np + sh.chunk - 1) / sh.chunk;
+    return;
+  }
+  const int nc = sh.live();
+  const int c0 = (int)(((sh.before + 1) * nc - 1) / sh.total), c1 = (int)(((sh.before + np) * nc - 1) / sh.total);
   first = c0 + b;
   count = c1 - c0 + 1;
 }
@@ -470,12 +527,11 @@ __global__ void __launch_bounds__(kVoteThreads) q4_vote_kernel(const __grid_cons
   __shared__ float2 s_mz[kVoteHeads];
   __shared__ float4 s_sum[kVoteQuarters][kVoteThreads / kVoteQuarters];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int64_t total, before;
-  count_pages(a, 0, lane, total, before);
-  Q4Range r{total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x, 0, 0};
+  auto pages = [&](int i) { return seq_pages(a, i); };
+  Q4Range r = equal_range(a, share_pages(a, 0, lane, pages).total, blockIdx.x, gridDim.x, pages);
   int b, p0, p1;
   wait_for_primary();
-  while (next_part(a, r, b, p0, p1)) {
+  while (next_part(a, r, pages, b, p0, p1)) {
     const int n = a.seq_lens[b];
     int64_t first;
     int count;
@@ -544,7 +600,7 @@ struct Q4GatherArgs {
 
 // CTA (split, head set, sequence): a contiguous part of the index list, 16 tokens per warp and step.
 template <int NB, int NT>
-__global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_constant__ Q4Args a,
+__global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas(NB, NT)) gather_kernel(const __grid_constant__ Q4Args a,
                                                                    const __grid_constant__ Q4GatherArgs ga) {
   constexpr int D = NB * 64, BLK = q4_block_bytes(D), CODES = q4_code_bytes(D);
   __shared__ __align__(16) float merge[kGatherWarps][4 * NT][D];
@@ -561,6 +617,19 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
   const int32_t* pt = a.page_table + (size_t)b * a.pt_stride;
 
   launch_dependents();
+  // lane i looks up list entry i (of 16) of a step: its row in the pool, -1 where there is none. The next
+  // step's entries are looked up while one step's rows are on their way.
+  auto listed = [&](int u) -> int64_t {
+    const int at = u * 16 + (lane & 15);
+    if (u >= u1 || at >= cnt) return -1;
+    const int tk = ib[at];
+    int page = -1;
+    if (tk >= 0 && tk < a.max_tokens) page = pt[tk / kPage];
+    if (page >= 0 && (int64_t)page < a.num_pages) return ((int64_t)page * a.HKV + kv) * kPage + tk % kPage;
+    set_error(a.status, TS_ERR_PAGE_OOB);
+    return -1;
+  };
+  int64_t mine = listed(u0 + warp);
   for (int i = tid; i < 4 * NT * D; i += kGatherWarps * 32)
     sq[i] = i / D < nh ? a.q[((size_t)b * a.H + head0) * D + i] : 0.f;
   __syncthreads();
@@ -575,18 +644,6 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
   Q4State<NB, NT> st;
   st.reset();
   for (int u = u0 + warp; u < u1; u += kGatherWarps) {
-    // lane i holds list entry i (of 16) as its row in the pool; -1 where there is none
-    int64_t mine = -1;
-    const int at = u * 16 + (lane & 15);
-    if (at < cnt) {
-      const int tk = ib[at];
-      int page = -1;
-      if (tk >= 0 && tk < a.max_tokens) page = pt[tk / kPage];
-      if (page >= 0 && (int64_t)page < a.num_pages)
-        mine = ((int64_t)page * a.HKV + kv) * kPage + tk % kPage;
-      else
-        set_error(a.status, TS_ERR_PAGE_OOB);
-    }
     uint2 kw[2][NB];
     float ks[NB][2], vs[NB][2], x[1][NT][2];
     uint32_t vw[4][NB];
@@ -614,6 +671,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const __grid_
                             : *reinterpret_cast<const uint32_t*>(a.v_pool + (size_t)(row / kPage) * BLK + nb * 512 +
                                                                  (row % kPage) * 32 + g * 4);
     }
+    mine = listed(u + kGatherWarps);
     q4_scores<NB, NT>(f, kw, ks, x[0]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -734,14 +792,15 @@ bool q4_supported(const ts_config& c) {
 }
 
 // Parts of any call: a scan has at most one per CTA and one more per sequence, a gather at most
-// 2 num_sms + B (its splits round up once per sequence).
-int64_t q4_part_slots(const ts_config& c, int num_sms) { return 2 * (int64_t)num_sms + c.max_batch; }
+// kGatherCtas num_sms, or one per sequence.
+int64_t q4_part_slots(const ts_config& c, int num_sms) { return kGatherCtas * (int64_t)num_sms + c.max_batch; }
 
 ts_status launch_attend_q4(ts_ctx* ctx, const AttendCall& c, const int32_t* seq_lens, cudaStream_t s) {
   Q4Args a = make_args(ctx, c.q, c.k_pool, c.v_pool, c.page_table, seq_lens, c.B, c.scale * kLog2e);
   if (!c.idx) return TS_Q4_DISPATCH(run_attend, ctx, a, c.out, c.lse, s);
-  const int sets = a.HKV * a.sets_per_kv * a.B;
-  const int splits = std::max(1, std::min((2 * ctx->num_sms + sets - 1) / sets, kAttnMaxSplits));
+  // as many CTAs as fit the GPU at once
+  const int sets = a.HKV * a.sets_per_kv * a.B, fit = gather_ctas(ctx->cfg.head_dim / 64, a.set_heads / 4) * ctx->num_sms;
+  const int splits = std::max(1, std::min(fit / sets, kAttnMaxSplits));
   Q4GatherArgs ga{c.idx, c.idx_stride, c.count, splits};
   return TS_Q4_DISPATCH(run_gather, ctx, a, ga, c.out, c.lse, s);
 }
