@@ -4,8 +4,9 @@ cache and over a selection, and a whole decode step, against the fp64 oracle.
 Tolerances (u24 = 2^-24 and so on). A logit is a sum of d products that are exact in fp32, of a query
 held in two fp16 terms (2^-22 of the head's largest element) and scaled: off by at most
 el = alpha sum|q_e k_e| (d + 16) u24 + alpha max|q| sum|k_e| 2^-21. A weight is off by twice that and
-2^-20 for its exponential, relatively; in the output it is held in two bf16 terms (2^-16). Sums of n
-terms in fp32 add at most n 2^-23 of the sum of magnitudes.
+2^-20 for its exponential, relatively; times its scale it enters the output as two fp16 terms (2^-21, or
+2^-31 of the largest such product, 7 of which a code may be). Sums of n terms in fp32 add at most n 2^-23
+of the sum of magnitudes.
 """
 import math
 
@@ -73,7 +74,8 @@ class Cache:
             want, wl, w = O.attention(q, k, v, scale)
             el = abs(scale) * float(np.max(np.abs(k) @ np.abs(q) * (self.d + 16) * 2.0 ** -24
                                            + np.abs(k).sum(1) * np.abs(q).max() * 2.0 ** -21))
-            tol = (w @ np.abs(v)) * (2 * el + 2.0 ** -16 + 2.0 ** -20 + n * 2.0 ** -23) + 1e-30
+            big = 7 * n * float(np.max(w[:, None] * np.abs(v))) * 2.0 ** -31
+            tol = (w @ np.abs(v)) * (2 * el + 2.0 ** -21 + 2.0 ** -20 + n * 2.0 ** -23) + big + 1e-30
             assert np.all(np.abs(out[b, h] - want) <= tol), (b, h, np.max(np.abs(out[b, h] - want) / tol))
             assert abs(lse[b, h] - wl) <= el + n * 2.0 ** -23 + 2.0 ** -20 + abs(wl) * 2.0 ** -22
 
@@ -240,6 +242,46 @@ def test_attend_where_the_maximum_moves_late_and_far():
         out, lse = torch.zeros(1, 16, 128, device=DEV), torch.zeros(1, 16, device=DEV)
         c.ctx.attend(c.q, c.kp, c.vp, c.pt, c.seq, out, lse, scale=scale)
         c.check(out.double().cpu().numpy(), lse.double().cpu().numpy(), 0, np.arange(1500), scale or None)
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 2, 64), (28, 4, 128)])
+def test_attend_over_values_of_very_different_sizes(H, Hkv, d):
+    # scales from 1e-12 to 1e12 along the sequence, both ways, and single rows far above the others
+    n = 700
+    c = Cache(H, Hkv, d, [n, n, n], seed=14)
+    size = torch.logspace(-12, 12, n, device=DEV)
+    outlier = torch.full((n,), 1e-3, device=DEV)
+    outlier[5], outlier[333], outlier[690] = 1e6, 3e9, 0.0
+    v = c.v.float().view(3, n, Hkv, d) * torch.stack([size, size.flip(0), outlier]).view(3, n, 1, 1)
+    c.ctx.append_prompt(c.k, v.view(3 * n, Hkv, d).to(torch.bfloat16), c.cu, c.pt, c.kp, c.vp)
+    c.vval = O.q4_pool_values(c.vp.cpu().numpy(), d)
+    out, lse = torch.zeros(3, H, d, device=DEV), torch.zeros(3, H, device=DEV)
+    idx = torch.arange(n, dtype=torch.int32, device=DEV).repeat(3, 1)
+    for call in (lambda: c.ctx.attend(c.q, c.kp, c.vp, c.pt, c.seq, out, lse),
+                 lambda: c.ctx.sparse_attend(c.q, c.kp, c.vp, c.pt, idx, c.seq, out, lse)):
+        out.zero_()
+        call()
+        for b in range(3):
+            c.check(out.double().cpu().numpy(), lse.double().cpu().numpy(), b, np.arange(n))
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(4, 4, 64), (28, 4, 128)])
+def test_more_sequences_than_a_kernel_keeps_at_hand(H, Hkv, d):
+    # 600 sequences, most of them empty or short
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.choice([0, 0, 0, 1, 5, 16, 17, 40], 600)]
+    lens[599] = 33
+    c = Cache(H, Hkv, d, lens, seed=15)
+    out, lse = torch.zeros(600, H, d, device=DEV), torch.zeros(600, H, device=DEV)
+    c.ctx.attend(c.q, c.kp, c.vp, c.pt, c.seq, out, lse)
+    vote = torch.zeros(600, c.ctx.max_tokens, device=DEV)
+    c.ctx.score(c.q, c.kp, c.pt, c.seq, vote)
+    assert c.ctx.status() == 0
+    o, z = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b in list(range(0, 600, 37)) + [511, 512, 513, 599]:
+        c.check(o, z, b, np.arange(lens[b]))
+    mass = vote.double().sum(1).cpu().numpy()
+    assert np.allclose(mass, [H if n else 0 for n in lens], atol=1e-4)
 
 
 @pytest.mark.parametrize("H,Hkv,d", GEOS)

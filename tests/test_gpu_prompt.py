@@ -197,6 +197,20 @@ def test_the_same_bits_again_and_in_a_graph_and_in_any_packing():
     _check(out40, lse40, q, k, v, many.tolist(), 1 / math.sqrt(d), [0, 27, 28, 500, 39 * 28 - 30, n - 6, n - 5, n - 1])
 
 
+def test_three_hundred_prompts_at_once():
+    H, Hkv, d = 8, 2, 64
+    rng = np.random.default_rng(4)
+    lens = [int(x) for x in rng.choice([0, 1, 3, 20, 63, 64, 65, 140], 300)]
+    q, k, v, cu_dev, cu = _make(H, Hkv, d, lens, seed=31)
+    n = sum(lens)
+    out, lse = torch.zeros(n, H, d, dtype=torch.bfloat16, device=DEV), torch.zeros(n, H, device=DEV)
+    ctx = _ctx(H, Hkv, d, 300)
+    ctx.prompt_attend(q, k, v, cu_dev, out, lse)
+    assert ctx.status() == 0
+    rows = {0, n - 1} | {int(cu[b]) for b in range(0, 300, 13) if lens[b]} | {int(cu[b + 1]) - 1 for b in range(0, 300, 13) if lens[b]}
+    _check(out, lse, q, k, v, cu, 1 / math.sqrt(d), sorted(rows))
+
+
 def test_bad_boundaries_are_reported_and_nothing_else_is_written():
     T = tsl()
     H, Hkv, d = 8, 4, 64

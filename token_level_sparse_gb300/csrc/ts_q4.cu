@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
 #pragma unroll
             for (int u = 0; u < 2; ++u) x[pg][nt][u] = token(u, g) < limit[pg] ? x[pg][nt][u] : -INFINITY;
       }
-      q4_raise_max<NB, NT, R::PAGES>(st, x);
+      const bool raised = q4_raise_max<NB, NT, R::PAGES>(st, x);
       if constexpr (kAttend) {
 #pragma unroll
         for (int pg = 0; pg < R::PAGES; ++pg) {
@@ -374,9 +374,9 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
             copy_next();
           }
           if (whole)
-            q4_accumulate<NB, NT, false>(st, x[pg], vw, vs);
+            q4_accumulate<NB, NT, false>(st, x[pg], vw, vs, raised && pg == 0);
           else
-            q4_accumulate<NB, NT, true>(st, x[pg], vw, vs);
+            q4_accumulate<NB, NT, true>(st, x[pg], vw, vs, raised && pg == 0);
         }
       } else {
         __syncwarp();
@@ -677,8 +677,8 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas(NB, NT)) gather
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) x[0][nt][i] = in[i] ? x[0][nt][i] * mul[nt] : -INFINITY;
-    q4_raise_max<NB, NT, 1>(st, x);
-    q4_accumulate<NB, NT, true>(st, x[0], vw, vs);
+    const bool raised = q4_raise_max<NB, NT, 1>(st, x);
+    q4_accumulate<NB, NT, true>(st, x[0], vw, vs, raised);
   }
   st.join_lanes();
   if (g == 0) {

@@ -14,8 +14,8 @@
 // elements of the values) and the heads as its 8 columns: column 2h holds the high part of head h's
 // query (or weight), column 2h + 1 the low part. One instruction so takes both parts of a split fp32
 // operand for four heads, and the two results of a head lie in one lane: lane (g, t) holds head t's
-// scores of tokens g and g + 8, its maximum, its sum and its outputs. Codes are exact in fp16 and
-// bf16 and their products with either part exact in fp32.
+// scores of tokens g and g + 8, its maximum, its sum and its outputs. Codes are exact in fp16 and their
+// products with either part exact in fp32.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -36,13 +36,6 @@ __host__ __device__ constexpr int q4_block_bytes(int d) { return kPage * (d / 2 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -77,13 +70,6 @@ __device__ __forceinline__ void q4_pairs_f16(uint32_t w, uint32_t (&p)[4]) {
   p[1] = h2_bits(__hfma2(bits_h2(and_or(w, 0x00f000f0u, 0x64006400u)), r16, m72));
   p[2] = h2_bits(__hadd2(bits_h2(and_or(h, 0x000f000fu, 0x64006400u)), m1032));
   p[3] = h2_bits(__hfma2(bits_h2(and_or(h, 0x00f000f0u, 0x64006400u)), r16, m72));
-}
-
-// Codes j of two words of four codes each (one token in the low half, one in the high), minus 8, as
-// a bf16 pair: a code in the low mantissa bits of 128 is 128 + u.
-__device__ __forceinline__ uint32_t q4_pair_bf16(uint32_t ab, int j) {
-  const __nv_bfloat162 m136 = bits_b2(0xc308c308u);                        // -136
-  return b2_bits(__hadd2(bits_b2(and_or(ab >> (4 * j), 0x000f000fu, 0x43004300u)), m136));
 }
 
 // Transposes an 8x8 matrix of 16-bit elements held as (row g, columns 2t, 2t + 1).
@@ -176,17 +162,20 @@ __device__ __forceinline__ void q4_scores(const Q4Query<NB, NT>& f, const uint2 
 }
 
 // Running softmax state of 4 NT heads in one warp, for head 4 nt + t: m its maximum (the same in the
-// eight lanes of a head), l this lane's own part of its sum, o its outputs (high parts in elements 0
-// and 2, low parts in 1 and 3): tile j, rows g and g + 8, are elements 64 nb + 8 g + j and + 4.
+// eight lanes of a head), l this lane's own part of its sum, o its outputs times sc, a power of two (high
+// parts in elements 0 and 2, low parts in 1 and 3): tile j, rows g and g + 8, are elements 64 nb + 8 g + j
+// and + 4. A weight times its value's scale enters its product as two fp16 terms, held with sc between the
+// largest so far at 2^6 and 2^13: within 2^-22 of it, or 2^-31 of the largest.
 template <int NB, int NT>
 struct Q4State {
-  float m[NT], l[NT];
+  float m[NT], l[NT], sc[NT];
   float o[NT][NB][4][4];
   __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt] = -INFINITY;
       l[nt] = 0.f;
+      sc[nt] = 1.f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -203,30 +192,32 @@ struct Q4State {
       l[nt] += __shfl_xor_sync(kFull, l[nt], 16);
     }
   }
-  // outputs times f[nt] as rows [head][64 NB]
+  // outputs (without sc) times f[nt] as rows [head][64 NB]
   __device__ __forceinline__ void store(float* rows, const float (&f)[NT], int lane) const {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const float inv = __uint_as_float((254u << 23) - __float_as_uint(sc[nt]));
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           float4 v;
-          v.x = (o[nt][nb][0][2 * r] + o[nt][nb][0][2 * r + 1]) * f[nt];
-          v.y = (o[nt][nb][1][2 * r] + o[nt][nb][1][2 * r + 1]) * f[nt];
-          v.z = (o[nt][nb][2][2 * r] + o[nt][nb][2][2 * r + 1]) * f[nt];
-          v.w = (o[nt][nb][3][2 * r] + o[nt][nb][3][2 * r + 1]) * f[nt];
+          v.x = (o[nt][nb][0][2 * r] + o[nt][nb][0][2 * r + 1]) * inv * f[nt];
+          v.y = (o[nt][nb][1][2 * r] + o[nt][nb][1][2 * r + 1]) * inv * f[nt];
+          v.z = (o[nt][nb][2][2 * r] + o[nt][nb][2][2 * r + 1]) * inv * f[nt];
+          v.w = (o[nt][nb][3][2 * r] + o[nt][nb][3][2 * r + 1]) * inv * f[nt];
           *reinterpret_cast<float4*>(rows + (4 * nt + t) * (NB * 64) + nb * 64 + 8 * g + 4 * r) = v;
         }
+    }
   }
 };
 
 // Moves the maxima up for 16 P tokens with base-2 logits x[page][nt][u] (-inf: not attended), where a logit
 // passes its head's maximum by more than 2^8: most calls cost one vote and no rescaling, and weights
-// stay below 2^8.
+// stay below 2^8. True (in the whole warp) where a maximum moved.
 template <int NB, int NT, int P>
-__device__ __forceinline__ void q4_raise_max(Q4State<NB, NT>& s, const float (&x)[P][NT][2]) {
+__device__ __forceinline__ bool q4_raise_max(Q4State<NB, NT>& s, const float (&x)[P][NT][2]) {
   float top[NT];
   bool grow = false;
 #pragma unroll
@@ -236,7 +227,8 @@ __device__ __forceinline__ void q4_raise_max(Q4State<NB, NT>& s, const float (&x
     for (int pg = 1; pg < P; ++pg) top[nt] = fmaxf(top[nt], fmaxf(x[pg][nt][0], x[pg][nt][1]));
     grow |= top[nt] > s.m[nt] + 8.f;
   }
-  if (__any_sync(kFull, grow)) {
+  const bool raised = __any_sync(kFull, grow);
+  if (raised) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float mn = fmaxf(s.m[nt], top[nt]);
@@ -254,40 +246,86 @@ __device__ __forceinline__ void q4_raise_max(Q4State<NB, NT>& s, const float (&x
           for (int e = 0; e < 4; ++e) s.o[nt][nb][j][e] *= f;
     }
   }
+  return raised;
 }
 
 // Adds 16 tokens whose logits x[nt][u] (head 4 nt + t, token (u, g)) the maxima already cover: vs[nb][u]
 // are that token's value scales, vw[i][nb] word g of the codes of token (i / 2, 2t + i % 2). kMasked: some
-// tokens may not be attended (x = -inf).
+// tokens may not be attended (x = -inf). refresh: sc is chosen anew from these tokens (after a maximum moved;
+// otherwise only where a term would pass 2^13).
 template <int NB, int NT, bool kMasked>
 __device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&x)[NT][2], const uint32_t (&vw)[4][NB],
-                                              const float (&vs)[NB][2]) {
-  uint32_t b[NT][NB][2];
+                                              const float (&vs)[NB][2], bool refresh) {
+  float w[NT][NB][2], top[NT];
+  bool over = refresh;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt) {
+    top[nt] = 0.f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const bool out = kMasked && x[nt][u] == -INFINITY;
       const float p = out ? 0.f : ex2(x[nt][u] - s.m[nt]);
       s.l[nt] += p;
+      const float ps = p * s.sc[nt];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        // a token that is not attended may lie in a slot never written: its scale is not used.
-        // high part by truncation to bf16, low part rounded: together within 2^-16
-        const float w = out ? 0.f : p * vs[nb][u];
-        const float hi = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
-        b[nt][nb][u] = movmatrix_trans(b2_bits(__floats2bfloat162_rn(hi, w - hi)));
+        // a token that is not attended may lie in a slot never written: its scale is not used
+        w[nt][nb][u] = out ? 0.f : ps * vs[nb][u];
+        top[nt] = fmaxf(top[nt], w[nt][nb][u]);
       }
     }
+    over |= top[nt] > 8192.f;
+  }
+  if (__any_sync(kFull, over)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float t = top[nt];
+      t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
+      t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
+      t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
+      if (t > 0.f && (refresh || t > 8192.f)) {
+        // t to [2^6, 2^7); up by 2^60 at most, where what is summed already counts for nothing below it
+        const int was = (int)(__float_as_uint(s.sc[nt]) >> 23) - 127;
+        int step = 6 - ((int)(__float_as_uint(t) >> 23) - 127);
+        step = max(-120, min(step, 60));
+        step = max(-120 - was, min(step, 120 - was));
+        const float f = __uint_as_float((uint32_t)(127 + step) << 23);
+        s.sc[nt] *= f;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          w[nt][nb][0] *= f;
+          w[nt][nb][1] *= f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s.o[nt][nb][j][e] *= f;
+        }
+      }
+    }
+  }
+  uint32_t b[NT][NB][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        // high and low part of one weight side by side, then across: a lane's tokens become another's columns
+        const float hi = __half2float(__float2half_rn(w[nt][nb][u]));
+        b[nt][nb][u] = movmatrix_trans(h2_bits(__floats2half2_rn(hi, w[nt][nb][u] - hi)));
+      }
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const uint32_t ab0 = __byte_perm(vw[0][nb], vw[1][nb], 0x5410), ab1 = __byte_perm(vw[0][nb], vw[1][nb], 0x7632);
-    const uint32_t cd0 = __byte_perm(vw[2][nb], vw[3][nb], 0x5410), cd1 = __byte_perm(vw[2][nb], vw[3][nb], 0x7632);
+    uint32_t ab0[4], ab1[4], cd0[4], cd1[4];
+    q4_pairs_f16(__byte_perm(vw[0][nb], vw[1][nb], 0x5410), ab0);
+    q4_pairs_f16(__byte_perm(vw[0][nb], vw[1][nb], 0x7632), ab1);
+    q4_pairs_f16(__byte_perm(vw[2][nb], vw[3][nb], 0x5410), cd0);
+    q4_pairs_f16(__byte_perm(vw[2][nb], vw[3][nb], 0x7632), cd1);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t a[4] = {q4_pair_bf16(ab0, j), q4_pair_bf16(ab1, j), q4_pair_bf16(cd0, j), q4_pair_bf16(cd1, j)};
+      const uint32_t a[4] = {ab0[j], ab1[j], cd0[j], cd1[j]};
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_bf16(s.o[nt][nb][j], a, b[nt][nb][0], b[nt][nb][1]);
+      for (int nt = 0; nt < NT; ++nt) mma_f16(s.o[nt][nb][j], a, b[nt][nb][0], b[nt][nb][1]);
     }
   }
 }
