@@ -22,7 +22,6 @@
 #include <utility>
 
 #include "ts_q4.cuh"
-#include "ts_tc.cuh"
 
 namespace ts {
 namespace {
@@ -179,11 +178,11 @@ struct Q4Ring {
   static constexpr int PAGES = 2;                                  // pages of a stage
   static constexpr int STAGE = PAGES * OPS * BLK;                  // [page][K, V][block]
   static constexpr int STAGES = kAttend ? (NT == 1 ? 2 : 3) : 4;
-  static constexpr int BYTES = STAGES * STAGE;                     // also holds [4 NT][d] floats at a join
+  static constexpr int BYTES = STAGES * STAGE;
   static constexpr int QUERY = kQ4Sets * 4 * NT * NB * 64 * 4;     // the CTA's queries, behind the rings
-  static constexpr int SMEM = WARPS * BYTES + QUERY;
+  static constexpr int ROWS = kAttend ? 4 * NT * NB * 64 * 4 : 0;  // one warp's output sums, behind the queries
+  static constexpr int SMEM = WARPS * (BYTES + ROWS) + QUERY;
   static_assert(SMEM + 4096 <= 227 * 1024, "shared memory of an SM");
-  static_assert(!kAttend || BYTES >= 4 * NT * NB * 64 * 4, "the join's area");
   static_assert(BLK % 16 == 0, "bulk copies");
 };
 
@@ -194,7 +193,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
   constexpr int D = NB * 64, CODES = q4_code_bytes(D);
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) uint64_t full[R::WARPS][R::STAGES];
-  __shared__ float2 s_ml[R::WARPS][4 * NT];
+  __shared__ float2 s_ml[R::WARPS][4 * NT], s_units[kAttend ? R::WARPS : 1][4 * NT];
   __shared__ int s_pages[kScanSeqs];
   __shared__ Q4Range s_left;           // the CTA's pages that no part has been made of yet
   __shared__ int s_part[4];            // the part at work: is there one, sequence, first page, end
@@ -243,6 +242,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
   const int nh = min(4 * NT, a.G - (set % a.sets_per_kv) * (4 * NT));   // heads of this set
   unsigned char* ring = smem + (size_t)warp * R::BYTES;
   float* sq = reinterpret_cast<float*>(smem + R::WARPS * R::BYTES);   // [sets][4 NT][D]
+  float* sums = reinterpret_cast<float*>(smem + R::WARPS * R::BYTES + R::QUERY + warp * R::ROWS);   // [4 NT][D]
   uint64_t* bars = full[warp];
   uint32_t phases = 0u;                                            // bit s: parity of the stage's next wait
   bool ok = works;
@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
         }
         row += R::PAGES * row_step;
       }
+      if (kAttend && done % kQ4Flush == kQ4Flush - 1) st.flush(sums, s_units[warp], done < kQ4Flush, lane);
       left -= R::PAGES * per_set * kPage;
       s = s + 1 == R::STAGES ? 0 : s + 1;
     }
@@ -432,18 +433,24 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
         a.part_ml[(int64_t)(head0 + 4 * nt + t) * a.slots + cta + b] = make_float2(M, L);
     }
     if constexpr (kAttend) {
-      if (works) st.store(reinterpret_cast<float*>(ring), fac, lane);
+      st.flush(sums, s_units[warp], done < kQ4Flush, lane);
+      // each warp's own factor: from its maximum to the set's, and out of its power of two
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        if (g == 0) s_units[warp][4 * nt + t] = make_float2(fac[nt], __uint_as_float((254u << 23) - __float_as_uint(st.sc[nt])));
       __syncthreads();
       if (works) {
         float* po = a.part_o + ((int64_t)(cta + b) * a.H + head0) * D;
-        const unsigned char* mg = smem + (size_t)hs * per_set * R::BYTES;
+        const float* rows = reinterpret_cast<const float*>(smem + R::WARPS * R::BYTES + R::QUERY) + hs * per_set * (4 * NT * D);
         for (int i = j * 32 + lane; i < nh * D; i += per_set * 32) {
           float acc = 0.f;
-          for (int w = 0; w < per_set; ++w) acc += reinterpret_cast<const float*>(mg + (size_t)w * R::BYTES)[i];
+          for (int w = 0; w < per_set; ++w) {
+            const float2 f = s_units[hs * per_set + w][i / D];
+            acc = fmaf(rows[w * (4 * NT * D) + i] * f.y, f.x, acc);
+          }
           po[i] = acc;
         }
       }
-      fence_proxy_async();                                         // these areas are copied into again
     }
     if (tid == 0) make_part();                                     // (every warp has read the old one)
     __syncthreads();
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas(NB, NT)) gather
   constexpr int D = NB * 64, BLK = q4_block_bytes(D), CODES = q4_code_bytes(D);
   __shared__ __align__(16) float merge[kGatherWarps][4 * NT][D];
   __shared__ __align__(16) float sq[4 * NT * D];
-  __shared__ float2 s_ml[kGatherWarps][4 * NT];
+  __shared__ float2 s_ml[kGatherWarps][4 * NT], s_units[kGatherWarps][4 * NT];
   const int split = blockIdx.x, set = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int kv = set / a.sets_per_kv, head0 = kv * a.G + (set % a.sets_per_kv) * (4 * NT);
@@ -635,14 +642,13 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas(NB, NT)) gather
   __syncthreads();
   Q4Query<NB, NT> f;
   q4_load_query<NB, NT>(f, sq, lane);
-  float mul[NT], one[NT];
+  float mul[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    mul[nt] = a.scale * f.inv[nt];
-    one[nt] = 1.f;
-  }
+  for (int nt = 0; nt < NT; ++nt) mul[nt] = a.scale * f.inv[nt];
   Q4State<NB, NT> st;
   st.reset();
+  int steps = 0;
+  bool flushed = false;
   for (int u = u0 + warp; u < u1; u += kGatherWarps) {
     uint2 kw[2][NB];
     float ks[NB][2], vs[NB][2], x[1][NT][2];
@@ -679,13 +685,17 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas(NB, NT)) gather
       for (int i = 0; i < 2; ++i) x[0][nt][i] = in[i] ? x[0][nt][i] * mul[nt] : -INFINITY;
     const bool raised = q4_raise_max<NB, NT, 1>(st, x);
     q4_accumulate<NB, NT, true>(st, x[0], vw, vs, raised);
+    if (++steps % (2 * kQ4Flush) == 0) {
+      st.flush(&merge[warp][0][0], s_units[warp], !flushed, lane);
+      flushed = true;
+    }
   }
   st.join_lanes();
   if (g == 0) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) s_ml[warp][4 * nt + t] = make_float2(st.m[nt], st.l[nt]);
   }
-  st.store(&merge[warp][0][0], one, lane);
+  st.flush(&merge[warp][0][0], s_units[warp], !flushed, lane);
   __syncthreads();
   const int64_t slot = (int64_t)b * ga.splits + split;
   for (int i = tid; i < nh * D; i += kGatherWarps * 32) {
@@ -697,7 +707,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas(NB, NT)) gather
     for (int w = 0; w < kGatherWarps; ++w) {
       const float wt = part_weight(s_ml[w][hg].x, M);
       L = fmaf(wt, s_ml[w][hg].y, L);
-      O = fmaf(wt, merge[w][hg][i % D], O);
+      O = fmaf(wt, merge[w][hg][i % D] * __uint_as_float((254u << 23) - __float_as_uint(s_units[w][hg].y)), O);
     }
     a.part_o[(slot * a.H + head0) * D + i] = O;
     if (i % D == 0) a.part_ml[(head0 + hg) * a.slots + slot] = make_float2(M, L);

@@ -165,10 +165,16 @@ __device__ __forceinline__ void q4_scores(const Q4Query<NB, NT>& f, const uint2 
 // eight lanes of a head), l this lane's own part of its sum, o its outputs times sc, a power of two (high
 // parts in elements 0 and 2, low parts in 1 and 3): tile j, rows g and g + 8, are elements 64 nb + 8 g + j
 // and + 4. A weight times its value's scale enters its product as two fp16 terms, held with sc between the
-// largest so far at 2^6 and 2^13: within 2^-22 of it, or 2^-31 of the largest.
+// largest so far at 2^6 and 2^13: within 2^-22 of it, or 2^-31 of the largest. `big` bounds the products
+// summed so far, in units of sc, so that a later sc never takes the sums out of range.
+//
+// The tensor cores cut their sums off rather than round them: over a few hundred steps in one accumulator
+// that is 3e-6 of an output. So the sums go over to rows in shared memory every kQ4Flush stages, added
+// there with rounding, and begin again at zero.
+constexpr int kQ4Flush = 16;
 template <int NB, int NT>
 struct Q4State {
-  float m[NT], l[NT], sc[NT];
+  float m[NT], l[NT], sc[NT], big[NT];
   float o[NT][NB][4][4];
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -176,6 +182,7 @@ struct Q4State {
       m[nt] = -INFINITY;
       l[nt] = 0.f;
       sc[nt] = 1.f;
+      big[nt] = 0.f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -192,24 +199,37 @@ struct Q4State {
       l[nt] += __shfl_xor_sync(kFull, l[nt], 16);
     }
   }
-  // outputs (without sc) times f[nt] as rows [head][64 NB]
-  __device__ __forceinline__ void store(float* rows, const float (&f)[NT], int lane) const {
+  // Moves the sums over to rows [head][64 NB] (in shared memory, this warp's own), whose units are kept in
+  // units[head]: the maximum and sc that they belong to. first: there is nothing in the rows yet.
+  __device__ __forceinline__ void flush(float* rows, float2* units, bool first, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float inv = __uint_as_float((254u << 23) - __float_as_uint(sc[nt]));
+      float f = 0.f;
+      if (!first) {
+        const float2 was = units[4 * nt + t];
+        const int step = (int)(__float_as_uint(sc[nt]) >> 23) - (int)(__float_as_uint(was.y) >> 23);
+        f = (was.x == m[nt] ? 1.f : ex2(was.x - m[nt])) * __uint_as_float((uint32_t)(127 + max(-126, min(step, 126))) << 23);
+      }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float4 v;
-          v.x = (o[nt][nb][0][2 * r] + o[nt][nb][0][2 * r + 1]) * inv * f[nt];
-          v.y = (o[nt][nb][1][2 * r] + o[nt][nb][1][2 * r + 1]) * inv * f[nt];
-          v.z = (o[nt][nb][2][2 * r] + o[nt][nb][2][2 * r + 1]) * inv * f[nt];
-          v.w = (o[nt][nb][3][2 * r] + o[nt][nb][3][2 * r + 1]) * inv * f[nt];
-          *reinterpret_cast<float4*>(rows + (4 * nt + t) * (NB * 64) + nb * 64 + 8 * g + 4 * r) = v;
+          float4* row = reinterpret_cast<float4*>(rows + (4 * nt + t) * (NB * 64) + nb * 64 + 8 * g + 4 * r);
+          float4 v = make_float4(o[nt][nb][0][2 * r] + o[nt][nb][0][2 * r + 1], o[nt][nb][1][2 * r] + o[nt][nb][1][2 * r + 1],
+                                 o[nt][nb][2][2 * r] + o[nt][nb][2][2 * r + 1], o[nt][nb][3][2 * r] + o[nt][nb][3][2 * r + 1]);
+          if (!first) {
+            const float4 w = *row;
+            v = make_float4(fmaf(w.x, f, v.x), fmaf(w.y, f, v.y), fmaf(w.z, f, v.z), fmaf(w.w, f, v.w));
+          }
+          *row = v;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[nt][nb][j][2 * r] = o[nt][nb][j][2 * r + 1] = 0.f;
         }
+      __syncwarp();
+      if (g == 0) units[4 * nt + t] = make_float2(m[nt], sc[nt]);
     }
+    __syncwarp();
   }
 };
 
@@ -238,6 +258,7 @@ __device__ __forceinline__ bool q4_raise_max(Q4State<NB, NT>& s, const float (&x
       const float f = s.m[nt] == mn ? 1.f : ex2(s.m[nt] - mn);
       s.m[nt] = mn;
       s.l[nt] *= f;
+      s.big[nt] *= f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -284,13 +305,14 @@ __device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&
       t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
       t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
       if (t > 0.f && (refresh || t > 8192.f)) {
-        // t to [2^6, 2^7); up by 2^60 at most, where what is summed already counts for nothing below it
+        // t to [2^6, 2^7), but not so far up that products summed before pass 2^40: next to those, these count
+        // for nothing
         const int was = (int)(__float_as_uint(s.sc[nt]) >> 23) - 127;
-        int step = 6 - ((int)(__float_as_uint(t) >> 23) - 127);
-        step = max(-120, min(step, 60));
-        step = max(-120 - was, min(step, 120 - was));
+        int step = min(6 - ((int)(__float_as_uint(t) >> 23) - 127), 40 - ((int)(__float_as_uint(s.big[nt]) >> 23) - 127));
+        step = max(max(-120, -120 - was), min(min(step, 120), 120 - was));
         const float f = __uint_as_float((uint32_t)(127 + step) << 23);
         s.sc[nt] *= f;
+        s.big[nt] = fmaxf(8192.f, s.big[nt] * f);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           w[nt][nb][0] *= f;
