@@ -293,7 +293,8 @@ ts_status ts_append_kv(ts_ctx* ctx, const void* k_new, const void* v_new, const 
  * v_stride elements from row to row, dense inside a row, rows 16-byte aligned. A
  * position outside [0, max tokens), or boundaries that are not ascending from 0 to at
  * most total, records TS_ERR_SEQ_LEN, a page outside the pool TS_ERR_PAGE_OOB; the
- * rows concerned are not written. Rows from cu_rows[B] on are not written. Two rows
+ * rows concerned (of a sequence that ends beyond total: all of its rows) are not
+ * written. Rows from cu_rows[B] on are not written. Two rows
  * for one position leave one of them or, in a 4-bit pool, a mix of them. */
 ts_status ts_append_prompt(ts_ctx* ctx, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                            const int32_t* cu_rows, const int32_t* starts, int B, int total,
@@ -345,7 +346,9 @@ ts_status ts_prefill_chunk(ts_ctx* ctx, const float* q, int c, const void* k_poo
  * nanoseconds (default 1 s): the kernel then records TS_ERR_TIMEOUT, raises an
  * abort word that the other CTAs see at their next barrier, waits (bounded)
  * for its own copies in flight, frees its tensor memory and returns, so the
- * context stays usable. The waits of the separate calls (ts_score,
+ * context stays usable. The waits of ts_prefill_chunk and ts_prompt_attend have
+ * the same bound (each by itself; one of the longest lasts as long as 128 rows of
+ * a prompt take). The waits of the separate calls (ts_score, ts_attend,
  * ts_sparse_attend) keep the 1 s bound. ns == 0 is TS_ERR_INVALID_ARG. */
 ts_status ts_set_wait_limit(ts_ctx* ctx, uint64_t ns);
 

@@ -187,7 +187,12 @@ def test_rows_without_a_place_are_reported_and_left_out():
 
     st, kp, vp = append([0, 30, 50])
     assert st == 0 and torch.equal(kp, c.kp)
-    assert append([0, 30, 51])[0] == SEQ                       # ends beyond the rows
+    st, kp, _ = append([0, 30, 51])                            # ends beyond the rows: none of its rows
+    assert st == SEQ
+    first = torch.zeros_like(kp)
+    for p in range(2):
+        first[c.table[0, p]] = c.kp[c.table[0, p]]
+    assert torch.equal(kp, first)
     assert append([0, 30, 20])[0] == SEQ                       # descends
     assert append([3, 30, 50])[0] == SEQ                       # does not begin at 0
     st, kp, _ = append([0, 30, 50], starts=[c.ctx.max_tokens - 10, -1])
@@ -487,5 +492,13 @@ def test_calls_that_the_context_does_not_serve():
     refused("TS_ERR_SHAPE", T.ts_append_prompt, c.ctx.handle, k, 256, k, 256, c.cu, None, 1, -1, c.pt, c.kp, c.vp)
     refused("TS_ERR_SHAPE", T.ts_append_prompt, c.ctx.handle, k, 256, k, 256, c.cu, None, 2, 20, c.pt, c.kp, c.vp)
     refused("TS_ERR_INVALID_ARG", T.ts_read_kv, c.ctx.handle, c.cu, None, 1, 20, c.pt, c.kp, c.vp, None, out)
+    rows = torch.zeros(20, 4, 64, device=DEV)
+    for call in (lambda: c.ctx.append_prompt(k.float(), k, c.cu, c.pt, c.kp, c.vp),
+                 lambda: c.ctx.append_prompt(k, k[:9], c.cu, c.pt, c.kp, c.vp),
+                 lambda: c.ctx.append_prompt(k, k, c.cu, c.pt, c.kp, c.vp, starts=c.cu),
+                 lambda: c.ctx.read_kv(c.cu, c.pt, c.kp, c.vp, rows, rows[:9]),
+                 lambda: c.ctx.read_kv(c.cu, c.pt, c.kp, c.vp, rows, rows.to(torch.bfloat16))):
+        with pytest.raises(T.TokenSelectError):
+            call()
     T.ts_append_prompt(c.ctx.handle, k, 256, k, 256, c.cu, None, 1, 0, c.pt, c.kp, c.vp)      # no rows: nothing to do
     assert c.ctx.status() == 0

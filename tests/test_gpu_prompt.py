@@ -197,6 +197,26 @@ def test_the_same_bits_again_and_in_a_graph_and_in_any_packing():
     _check(out40, lse40, q, k, v, many.tolist(), 1 / math.sqrt(d), [0, 27, 28, 500, 39 * 28 - 30, n - 6, n - 5, n - 1])
 
 
+def test_scores_of_minus_infinity_in_the_first_tiles():
+    # every key but the last 30 gives -inf for head 0 (its queries point against an infinite key element), so
+    # the rows behind them see their first finite score late; rows that see none are NaN, as a softmax over
+    # nothing but -inf is
+    H, Hkv, d, n, cut = 2, 1, 64, 400, 370
+    q, k, v, cu_dev, cu = _make(H, Hkv, d, [n], seed=37, spread=0.1)
+    q, k = q.clone(), k.clone()
+    q[:, 0, 0], q[:, 1, 0] = -1.0, -2.0
+    k[:cut, 0, 0] = float("inf")
+    out, lse = torch.zeros(n, H, d, dtype=torch.bfloat16, device=DEV), torch.zeros(n, H, device=DEV)
+    ctx = _ctx(H, Hkv, d, 1)
+    ctx.prompt_attend(q, k, v, cu_dev, out, lse)
+    assert torch.isnan(out[:cut]).all()
+    alone, alone_lse = torch.zeros(n - cut, H, d, dtype=torch.bfloat16, device=DEV), torch.zeros(n - cut, H, device=DEV)
+    ctx.prompt_attend(q[cut:], k[cut:], v[cut:], torch.tensor([0, n - cut], dtype=torch.int32, device=DEV), alone, alone_lse)
+    # the same weights over the same rows; sums in another grouping, outputs rounded to bf16
+    assert torch.allclose(lse[cut:], alone_lse, rtol=0, atol=2.0 ** -18)
+    assert torch.allclose(out[cut:].float(), alone.float(), rtol=2.0 ** -7, atol=2.0 ** -7)
+
+
 def test_three_hundred_prompts_at_once():
     H, Hkv, d = 8, 2, 64
     rng = np.random.default_rng(4)
@@ -253,5 +273,11 @@ def test_refusals():
     refused("TS_ERR_SHAPE", ctx, q, st, k, st, v, st, cu, 2, 10, 0.0, out, qs)
     refused("TS_ERR_SHAPE", ctx, q, st, k, st, v, st, cu, 0, 10, 0.0, out, qs)
     refused("TS_ERR_SHAPE", ctx, q, st, k, st, v, st, cu, 1, -1, 0.0, out, qs)
+    for bad in (dict(k=k[:9]), dict(v=v[:, :2]), dict(out=out[:9]), dict(lse=torch.zeros(10, H, dtype=torch.bfloat16, device=DEV)),
+                dict(q=q.float()), dict(out=out.float()), dict(cu=cu.long()), dict(k=k.cpu()),
+                dict(lse=torch.zeros(10, 2 * H, device=DEV)[:, :H])):
+        a = dict(dict(q=q, k=k, v=v, cu=cu, out=out, lse=None), **bad)
+        with pytest.raises(T.TokenSelectError):
+            ctx.prompt_attend(a["q"], a["k"], a["v"], a["cu"], a["out"], a["lse"])
     T.ts_prompt_attend(ctx.handle, q, st, k, st, v, st, cu, 1, 0, 0.0, out, qs)                  # no rows: nothing to do
     assert not out.any() and ctx.status() == 0

@@ -145,6 +145,25 @@ def _p(t):
     return t.data_ptr()
 
 
+def _packed(where, shapes, dtypes, on_device):
+    """Refuses a packed call: shapes and dtypes are (got, wanted) pairs, on_device the tensors (None: absent)."""
+    for got, want in shapes:
+        if got != want:
+            raise TokenSelectError(STATUS_CODE["TS_ERR_SHAPE"], f"{where}: {tuple(got)} instead of {tuple(want)}")
+    for got, want in dtypes:
+        if got is not want:
+            raise TokenSelectError(STATUS_CODE["TS_ERR_INVALID_ARG"], f"{where}: {got} instead of {want}")
+    for t in on_device:
+        if t is not None and not t.is_cuda:
+            raise TokenSelectError(STATUS_CODE["TS_ERR_INVALID_ARG"], f"{where}: a tensor is not on the device")
+
+
+def _dense(where, *tensors):
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise TokenSelectError(STATUS_CODE["TS_ERR_INVALID_ARG"], f"{where}: a tensor is not dense")
+
+
 def _row_stride(t):
     """Elements from row to row of a packed [total][heads][d] tensor, which must be dense inside a row."""
     heads, d = t.shape[1:]
@@ -350,6 +369,11 @@ class Context:
                           max_pages_per_seq, num_pages)
         self.handle = ts_create(self.cfg)
         self.max_tokens = max_pages_per_seq * page_size
+        # what the packed calls compare their tensors with
+        import torch
+        self._q_row, self._kv_row = (n_q_heads, head_dim), (n_kv_heads, head_dim)
+        self._bfloat16, self._float32, self._int32 = torch.bfloat16, torch.float32, torch.int32
+        self._rows_dtype = torch.float32 if kv_dtype == TS_KV_F32 else torch.bfloat16
 
     def close(self):
         if self.handle:
@@ -399,11 +423,27 @@ class Context:
 
     def append_prompt(self, k, v, cu_rows, page_table, k_pool, v_pool, starts=None, stream=None):
         """k / v [total][H_kv][d], packed: row r of sequence b to position starts[b] + r - cu_rows[b]."""
+        ks, B, i32, kind = k.shape, cu_rows.shape[0] - 1, self._int32, self._rows_dtype
+        if not (ks[1:] == self._kv_row and v.shape == ks and k.dtype is kind and v.dtype is kind and cu_rows.dtype is i32
+                and k.is_cuda and v.is_cuda and cu_rows.is_cuda):
+            _packed("append_prompt", ((ks[1:], self._kv_row), (v.shape, ks)), ((k.dtype, kind), (v.dtype, kind), (cu_rows.dtype, i32)),
+                    (k, v, cu_rows))
+        if starts is not None and not (starts.shape == (B,) and starts.dtype is i32 and starts.is_cuda):
+            _packed("append_prompt", ((starts.shape, (B,)),), ((starts.dtype, i32),), (starts,))
+        _dense("append_prompt", cu_rows, starts)
         ts_append_prompt(self.handle, k, _row_stride(k), v, _row_stride(v), cu_rows, starts, cu_rows.shape[0] - 1,
                          k.shape[0], page_table, k_pool, v_pool, stream)
 
     def read_kv(self, cu_rows, page_table, k_pool, v_pool, k_out, v_out, starts=None, stream=None):
         """k_out / v_out fp32 [total][H_kv][d]: the values of the rows that append_prompt would write."""
+        ks, B, i32, f32 = k_out.shape, cu_rows.shape[0] - 1, self._int32, self._float32
+        if not (ks[1:] == self._kv_row and v_out.shape == ks and k_out.dtype is f32 and v_out.dtype is f32
+                and cu_rows.dtype is i32 and k_out.is_cuda and v_out.is_cuda and cu_rows.is_cuda):
+            _packed("read_kv", ((ks[1:], self._kv_row), (v_out.shape, ks)),
+                    ((k_out.dtype, f32), (v_out.dtype, f32), (cu_rows.dtype, i32)), (k_out, v_out, cu_rows))
+        if starts is not None and not (starts.shape == (B,) and starts.dtype is i32 and starts.is_cuda):
+            _packed("read_kv", ((starts.shape, (B,)),), ((starts.dtype, i32),), (starts,))
+        _dense("read_kv", k_out, v_out, cu_rows, starts)
         ts_read_kv(self.handle, cu_rows, starts, cu_rows.shape[0] - 1, k_out.shape[0], page_table, k_pool, v_pool,
                    k_out, v_out, stream)
 
@@ -413,6 +453,15 @@ class Context:
 
     def prompt_attend(self, q, k, v, cu_rows, out, lse=None, scale=0.0, stream=None):
         """q / out [total][H][d], k / v [total][H_kv][d] (bf16, packed): causal attention of every sequence."""
+        qs, ks, bf, i32 = q.shape, k.shape, self._bfloat16, self._int32
+        if not (qs[1:] == self._q_row and ks[1:] == self._kv_row and ks[0] == qs[0] and v.shape == ks and out.shape == qs
+                and q.dtype is bf and k.dtype is bf and v.dtype is bf and out.dtype is bf and cu_rows.dtype is i32
+                and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and cu_rows.is_cuda):
+            _packed("prompt_attend", ((qs[1:], self._q_row), (ks[1:], self._kv_row), (ks[:1], qs[:1]), (v.shape, ks), (out.shape, qs)),
+                    ((q.dtype, bf), (k.dtype, bf), (v.dtype, bf), (out.dtype, bf), (cu_rows.dtype, i32)), (q, k, v, out, cu_rows))
+        if lse is not None and not (lse.shape == qs[:2] and lse.dtype is self._float32 and lse.is_cuda):
+            _packed("prompt_attend", ((lse.shape, qs[:2]),), ((lse.dtype, self._float32),), (lse,))
+        _dense("prompt_attend", cu_rows, lse)
         ts_prompt_attend(self.handle, q, _row_stride(q), k, _row_stride(k), v, _row_stride(v), cu_rows,
                          cu_rows.shape[0] - 1, q.shape[0], scale, out, _row_stride(out), lse, stream)
 

@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
               p[c] = pack_bf16(y0, y1);
             }
             if (raise) break;
-            over = real && !(ta + tb <= kPrMaxSum);
+            over = real && (!(ta + tb <= kPrMaxSum) || m2 == -INFINITY);
             if (!__any_sync(kFull, over)) break;
           }
           if (!ok) break;

@@ -63,7 +63,8 @@ __device__ __forceinline__ void place_rows(const RowsArgs& a, int64_t* place) {
           if (cu[mid] <= r) lo = mid; else hi = mid;
         }
         b = lo;
-        inside = r >= cu[b] && r < cu[b + 1];       // rows behind the last sequence stay as they are
+        // rows behind the last sequence stay as they are, so do those of one that ends beyond the rows
+        inside = cu[b] >= 0 && r >= cu[b] && r < cu[b + 1] && cu[b + 1] <= a.total;
         const int start = a.starts ? a.starts[b] : 0;
         pos = start < 0 ? -1 : start + (r - cu[b]);
       } else {
