@@ -26,6 +26,7 @@
 namespace ts {
 namespace {
 
+constexpr int kScorePages = 4;
 constexpr int kScanSeqs = 512;                  // sequences whose page counts a scan CTA keeps in shared memory
 constexpr int kQ4Sets = 4;                      // head sets of a CTA, at most
 constexpr int kGatherWarps = 4;
@@ -175,9 +176,9 @@ struct Q4Ring {
   static constexpr int WARPS = kAttend ? (NT == 1 ? 20 : 12) : 16;
   static constexpr int BLK = q4_block_bytes(NB * 64);
   static constexpr int OPS = kAttend ? 2 : 1;                      // blocks of a page
-  static constexpr int PAGES = 2;                                  // pages of a stage
+  static constexpr int PAGES = kAttend ? 2 : kScorePages;          // pages of a stage
   static constexpr int STAGE = PAGES * OPS * BLK;                  // [page][K, V][block]
-  static constexpr int STAGES = kAttend ? (NT == 1 ? 2 : 3) : 4;
+  static constexpr int STAGES = kAttend ? (NT == 1 ? 2 : 3) : 8 / kScorePages;
   static constexpr int BYTES = STAGES * STAGE;
   static constexpr int QUERY = kQ4Sets * 4 * NT * NB * 64 * 4;     // the CTA's queries, behind the rings
   static constexpr int ROWS = kAttend ? 4 * NT * NB * 64 * 4 : 0;  // one warp's output sums, behind the queries
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
     const int mine = ok && p0 + j < p1 ? (p1 - p0 - j + per_set - 1) / per_set : 0;
     const int stages = (mine + R::PAGES - 1) / R::PAGES;
     int ids = 0, copied = 0, cs = 0;                               // stages copied so far, the next one's slot
-    uint32_t lost = 0u;                                            // bits 2s, 2s + 1: pages of slot s without a block
+    uint32_t lost = 0u;                                            // bit PAGES s + p: page p of slot s has no block
     // lane (page, operand) copies one block. The score's blocks are streamed through L2 (evict first): its
     // logits are read again by the votes and should stay there
     const unsigned char* pool = R::OPS == 2 && (lane & 1) ? a.v_pool : a.k_pool;
@@ -285,8 +286,10 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
         else
           bulk_g2s_hint(ring + cs * R::STAGE + lane * R::BLK, src, R::BLK, &bars[cs], policy);
       }
-      const unsigned pages = R::OPS == 1 ? good : ((good & 1u) | (good >> 1 & 2u));
-      lost = (lost & ~(3u << (2 * cs))) | ((~pages & 3u) << (2 * cs));
+      static_assert(R::OPS == 1 || R::PAGES == 2, "bits of the pages");
+      constexpr unsigned kAll = (1u << R::PAGES) - 1u;
+      const unsigned there = R::OPS == 1 ? good : ((good & 1u) | (good >> 1 & 2u));
+      lost = (lost & ~(kAll << (R::PAGES * cs))) | ((~there & kAll) << (R::PAGES * cs));
       ++copied;
       cs = cs + 1 == R::STAGES ? 0 : cs + 1;
     };
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
       bool whole = true;
 #pragma unroll
       for (int pg = 0; pg < R::PAGES; ++pg) {
-        limit[pg] = (lost >> (2 * s + pg)) & 1u ? 0 : left - pg * per_set * kPage;
+        limit[pg] = (lost >> (R::PAGES * s + pg)) & 1u ? 0 : left - pg * per_set * kPage;
         whole &= limit[pg] >= kPage;
         const unsigned char* kb = ring + s * R::STAGE + pg * (R::OPS * R::BLK);
         uint2 kw[2][NB];
@@ -458,9 +461,10 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
 }
 
 // The parts of a sequence's scan that exist: slots [first, first + count).
-__device__ __forceinline__ void scan_slots(const Q4Args& a, int b, int lane, int64_t& first, int& count) {
-  const Q4Share sh = share_pages(a, b, lane, [&](int i) { return seq_pages(a, i); });
-  const int np = seq_pages(a, b);
+template <typename Pages>
+__device__ __forceinline__ void scan_slots(const Q4Args& a, int b, int lane, Pages pages, int64_t& first, int& count) {
+  const Q4Share sh = share_pages(a, b, lane, pages);
+  const int np = pages(b);
   count = 0;
   first = 0;
   if (np == 0) return;
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(1024) q4_merge_kernel(const __grid_constant__ 
     first = (int64_t)b * splits;
     count = splits;
   } else {
-    scan_slots(a, b, tid & 31, first, count);
+    scan_slots(a, b, tid & 31, [&](int i) { return seq_pages(a, i); }, first, count);
   }
   wait_for_primary();
   for (int i = tid; i < count; i += blockDim.x) s_ml[i] = __ldcg(a.part_ml + h * a.slots + first + i);
@@ -522,78 +526,91 @@ __global__ void __launch_bounds__(1024) q4_merge_kernel(const __grid_constant__ 
 
 // The head soft vote from the scan's base-2 logits and parts: v_i = sum_h 2^(l_hi - M_h) / Z_h. Like the
 // scan, a CTA takes an even, contiguous share of the batch's pages; for each sequence in it its warps
-// first join the heads' parts (the same in every CTA), then a thread sums a quarter of the heads of
-// four tokens, compensated, and the quarters are added. Reads the logits (written by the scan, in L2
-// up to about 100 MB) once, 16 bytes at a time.
+// first join the heads' parts (the same in every CTA), then a warp sums a page at a time: lane (head, quad)
+// every eighth head of four tokens, and then across the lanes. The logits of a page lie together, so a load
+// of the warp is 512 contiguous bytes, four pages' worth of which are under way per lane and page.
 constexpr int kVoteThreads = 512;
 constexpr int kVoteHeads = 256;
-constexpr int kVoteQuarters = 4;
 
-__global__ void __launch_bounds__(kVoteThreads) q4_vote_kernel(const __grid_constant__ Q4Args a, float* vote,
-                                                               int64_t vote_stride) {
+__global__ void __launch_bounds__(kVoteThreads, 2) q4_vote_kernel(const __grid_constant__ Q4Args a, float* vote,
+                                                                  int64_t vote_stride) {
+  constexpr int WARPS = kVoteThreads / 32, BATCH = 4;
   __shared__ float2 s_mz[kVoteHeads];
-  __shared__ float4 s_sum[kVoteQuarters][kVoteThreads / kVoteQuarters];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto pages = [&](int i) { return seq_pages(a, i); };
+  __shared__ int s_pages[kScanSeqs];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 3, h8 = lane >> 2;
+  for (int b = tid; b < min(a.B, kScanSeqs); b += kVoteThreads) s_pages[b] = seq_pages(a, b);
+  __syncthreads();
+  auto pages = [&](int i) { return i < kScanSeqs ? s_pages[i] : seq_pages(a, i); };
   Q4Range r = equal_range(a, share_pages(a, 0, lane, pages).total, blockIdx.x, gridDim.x, pages);
   int b, p0, p1;
   wait_for_primary();
   while (next_part(a, r, pages, b, p0, p1)) {
     const int n = a.seq_lens[b];
+    const float* logits = a.logits + (size_t)b * a.H * a.max_tokens + 4 * quad;
+    // heads h8 + 8 (k0 .. k0 + 3) of this lane's four tokens of page pg
+    auto load = [&](float4 (&x)[BATCH], int pg, int k0) {
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int h = h8 + 8 * (k0 + k);
+        x[k] = pg < p1 && h < a.H
+                   ? __ldcg(reinterpret_cast<const float4*>(logits + (size_t)pg * a.page_stride + (size_t)h * a.head_stride))
+                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      }
+    };
+    float4 x[BATCH];
+    load(x, p0 + warp, 0);                         // on their way while the statistics are joined
     int64_t first;
     int count;
-    scan_slots(a, b, lane, first, count);
+    scan_slots(a, b, lane, pages, first, count);
     __syncthreads();                               // the last sequence's statistics are done with
-    for (int h = warp; h < a.H; h += kVoteThreads / 32) {
+    for (int h = warp; h < a.H; h += WARPS) {
+      constexpr int FIRST = 5;                     // parts of a lane under way at once
       const float2* ml = a.part_ml + h * a.slots + first;
-      float2 x[8];                                 // the first 256 parts (one per CTA: all of them) at once
+      float2 y[FIRST];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = lane + 32 * k < count ? ml[lane + 32 * k] : make_float2(-INFINITY, 0.f);
+      for (int k = 0; k < FIRST; ++k) y[k] = lane + 32 * k < count ? ml[lane + 32 * k] : make_float2(-INFINITY, 0.f);
       float M = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) M = fmaxf(M, x[k].x);
-      for (int i = lane + 256; i < count; i += 32) M = fmaxf(M, ml[i].x);
+      for (int k = 0; k < FIRST; ++k) M = fmaxf(M, y[k].x);
+      for (int i = lane + 32 * FIRST; i < count; i += 32) M = fmaxf(M, ml[i].x);
       M = warp_max(M);
       KahanF z;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) z.add(x[k].y * part_weight(x[k].x, M));
-      for (int i = lane + 256; i < count; i += 32) z.add(ml[i].y * part_weight(ml[i].x, M));
+      for (int k = 0; k < FIRST; ++k) z.add(y[k].y * part_weight(y[k].x, M));
+      for (int i = lane + 32 * FIRST; i < count; i += 32) z.add(ml[i].y * part_weight(ml[i].x, M));
       const float Z = warp_sum_comp(z.s, -z.c);
       if (lane == 0) s_mz[h] = make_float2(M, 1.f / Z);
     }
     __syncthreads();
-    const int quarter = tid / (kVoteThreads / kVoteQuarters), quad = tid % (kVoteThreads / kVoteQuarters);
-    const int end = min(n, p1 * kPage);
-    for (int i0 = p0 * kPage; i0 < end; i0 += kVoteThreads / kVoteQuarters * 4) {
-      const int i = i0 + 4 * quad;
-      KahanF acc[4];
-      const float* lb = a.logits + (size_t)b * a.H * a.max_tokens + (size_t)(i / kPage) * a.page_stride + i % kPage;
-      if (i < end) {                               // (the page's last tokens have logits of -inf)
-        for (int h0 = quarter; h0 < a.H; h0 += 8 * kVoteQuarters) {   // eight loads under way at once
-          float4 x[8];
+    for (int pg = p0 + warp; pg < p1; pg += WARPS) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      float4 next[BATCH];
+      load(next, pg + WARPS, 0);
+      for (int k0 = 0; 8 * k0 < a.H; k0 += BATCH) {
+        if (k0 > 0) load(x, pg, k0);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            x[k] = h0 + k * kVoteQuarters < a.H
-                       ? __ldcg(reinterpret_cast<const float4*>(lb + (size_t)(h0 + k * kVoteQuarters) * a.head_stride))
-                       : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (h0 + k * kVoteQuarters >= a.H) break;
-            const float2 mz = s_mz[h0 + k * kVoteQuarters];
-            acc[0].add(ex2(x[k].x - mz.x) * mz.y);
-            acc[1].add(ex2(x[k].y - mz.x) * mz.y);
-            acc[2].add(ex2(x[k].z - mz.x) * mz.y);
-            acc[3].add(ex2(x[k].w - mz.x) * mz.y);
-          }
+        for (int k = 0; k < BATCH; ++k) {
+          const int h = h8 + 8 * (k0 + k);
+          if (h >= a.H) continue;
+          const float2 mz = s_mz[h];
+          acc[0] = fmaf(ex2(x[k].x - mz.x), mz.y, acc[0]);
+          acc[1] = fmaf(ex2(x[k].y - mz.x), mz.y, acc[1]);
+          acc[2] = fmaf(ex2(x[k].z - mz.x), mz.y, acc[2]);
+          acc[3] = fmaf(ex2(x[k].w - mz.x), mz.y, acc[3]);
         }
       }
-      s_sum[quarter][quad] = make_float4(acc[0].s - acc[0].c, acc[1].s - acc[1].c, acc[2].s - acc[2].c, acc[3].s - acc[3].c);
-      __syncthreads();
-      const float* sums = reinterpret_cast<const float*>(s_sum);
-      if (i0 + tid < end)
-        vote[(size_t)b * vote_stride + i0 + tid] =
-            (sums[tid] + sums[kVoteThreads + tid]) + (sums[2 * kVoteThreads + tid] + sums[3 * kVoteThreads + tid]);
-      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[e] += __shfl_xor_sync(kFull, acc[e], 4);
+        acc[e] += __shfl_xor_sync(kFull, acc[e], 8);
+        acc[e] += __shfl_xor_sync(kFull, acc[e], 16);
+      }
+      // lane (h8 = e, quad) writes token 4 quad + e
+      const float v = h8 == 0 ? acc[0] : h8 == 1 ? acc[1] : h8 == 2 ? acc[2] : acc[3];
+      const int i = pg * kPage + 4 * quad + h8;
+      if (h8 < 4 && i < n) vote[(size_t)b * vote_stride + i] = v;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) x[k] = next[k];
     }
   }
 }
