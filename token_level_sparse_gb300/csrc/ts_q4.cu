@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
     float mul[NT];
     Q4State<NB, NT> st;                                            // (the score uses its m and l alone)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mul[nt] = a.scale * f.inv[nt];
+    for (int nt = 0; nt < NT; ++nt) mul[nt] = f.unit(a.scale, nt);
     st.reset();
     int s = 0, left = n - (p0 + j) * kPage;                        // tokens of the sequence from this page on
     int done = 0;
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas(NB, NT)) gather
   q4_load_query<NB, NT>(f, sq, lane);
   float mul[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) mul[nt] = a.scale * f.inv[nt];
+  for (int nt = 0; nt < NT; ++nt) mul[nt] = f.unit(a.scale, nt);
   Q4State<NB, NT> st;
   st.reset();
   int steps = 0;
