@@ -123,7 +123,8 @@ def test_null_arguments_are_refused(lib):
 def test_packed_rows_must_be_dense_inside():
     import token_level_sparse_gb300 as T
     x = torch.zeros(5, 4, 64)
-    assert T._row_stride(x) == 256 and T._row_stride(x[:, :2]) == 256
+    stride = lambda t: T._row_stride(t, t.shape[0], t.shape[1:])
+    assert stride(x) == 256 and stride(x[:, :2]) == 256 and stride(x[:1].expand(1, 4, 64)) == 256
     for bad in (x[:, ::2], x[:, :, ::2], x.transpose(0, 1)):
         with pytest.raises(T.TokenSelectError):
-            T._row_stride(bad)
+            stride(bad)

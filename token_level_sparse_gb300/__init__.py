@@ -164,21 +164,28 @@ def _dense(where, *tensors):
             raise TokenSelectError(STATUS_CODE["TS_ERR_INVALID_ARG"], f"{where}: a tensor is not dense")
 
 
-def _row_stride(t):
+def _row_stride(t, total, row):
     """Elements from row to row of a packed [total][heads][d] tensor, which must be dense inside a row."""
-    heads, d = t.shape[1:]
-    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+    heads, d = row
+    rows, head, one = t.stride()        # (one call: each takes as long as all three)
+    if (one != 1 and d > 1) or (head != d and heads > 1):
         raise TokenSelectError(STATUS_CODE["TS_ERR_INVALID_ARG"], "a packed row is not dense")
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    return rows if total > 1 else heads * d
+
+
+_stream_of, _device = None, None
 
 
 def _current_stream():
     """The raw handle of torch's current stream (without the Stream object, whose making takes microseconds)."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+    global _stream_of, _device
+    if _stream_of is None:
+        import torch
+        _device = torch.cuda.current_device
+        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if _stream_of is None:
+            _stream_of = lambda device: torch.cuda.current_stream(device).cuda_stream
+    return _stream_of(_device())
 
 
 def _s(stream):
@@ -431,8 +438,9 @@ class Context:
         if starts is not None and not (starts.shape == (B,) and starts.dtype is i32 and starts.is_cuda):
             _packed("append_prompt", ((starts.shape, (B,)),), ((starts.dtype, i32),), (starts,))
         _dense("append_prompt", cu_rows, starts)
-        ts_append_prompt(self.handle, k, _row_stride(k), v, _row_stride(v), cu_rows, starts, cu_rows.shape[0] - 1,
-                         k.shape[0], page_table, k_pool, v_pool, stream)
+        total, row = ks[0], self._kv_row
+        ts_append_prompt(self.handle, k, _row_stride(k, total, row), v, _row_stride(v, total, row), cu_rows, starts, B, total,
+                         page_table, k_pool, v_pool, stream)
 
     def read_kv(self, cu_rows, page_table, k_pool, v_pool, k_out, v_out, starts=None, stream=None):
         """k_out / v_out fp32 [total][H_kv][d]: the values of the rows that append_prompt would write."""
@@ -444,8 +452,7 @@ class Context:
         if starts is not None and not (starts.shape == (B,) and starts.dtype is i32 and starts.is_cuda):
             _packed("read_kv", ((starts.shape, (B,)),), ((starts.dtype, i32),), (starts,))
         _dense("read_kv", k_out, v_out, cu_rows, starts)
-        ts_read_kv(self.handle, cu_rows, starts, cu_rows.shape[0] - 1, k_out.shape[0], page_table, k_pool, v_pool,
-                   k_out, v_out, stream)
+        ts_read_kv(self.handle, cu_rows, starts, B, ks[0], page_table, k_pool, v_pool, k_out, v_out, stream)
 
     def attend(self, q, k_pool, v_pool, page_table, seq_lens, out, lse=None, scale=0.0, stream=None):
         """q [B][H][d] attends to every cached token of its sequence (4-bit pools)."""
@@ -462,8 +469,10 @@ class Context:
         if lse is not None and not (lse.shape == qs[:2] and lse.dtype is self._float32 and lse.is_cuda):
             _packed("prompt_attend", ((lse.shape, qs[:2]),), ((lse.dtype, self._float32),), (lse,))
         _dense("prompt_attend", cu_rows, lse)
-        ts_prompt_attend(self.handle, q, _row_stride(q), k, _row_stride(k), v, _row_stride(v), cu_rows,
-                         cu_rows.shape[0] - 1, q.shape[0], scale, out, _row_stride(out), lse, stream)
+        total, row = qs[0], self._kv_row
+        ts_prompt_attend(self.handle, q, _row_stride(q, total, self._q_row), k, _row_stride(k, total, row), v,
+                         _row_stride(v, total, row), cu_rows, cu_rows.shape[0] - 1, total, scale, out,
+                         _row_stride(out, total, self._q_row), lse, stream)
 
     def select_blocks(self, vote, seq_lens, block, budget, idx, count, stream=None):
         ts_select_blocks(self.handle, vote, vote.stride(0), seq_lens, seq_lens.shape[0], block, budget, idx,
