@@ -24,8 +24,6 @@
 
 namespace ts {
 
-constexpr int kQ4Group = 64;   // elements that share a scale
-
 __host__ __device__ constexpr int q4_code_bytes(int d) { return kPage * d / 2; }
 __host__ __device__ constexpr int q4_block_bytes(int d) { return kPage * (d / 2 + d / 32); }
 
@@ -47,9 +45,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ uint32_t b2_bits(__nv_bfloat162 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-__device__ __forceinline__ __nv_bfloat162 bits_b2(uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); }
 __device__ __forceinline__ float bf16_bits_f(uint32_t u) { return __uint_as_float(u << 16); }
 
 // (x & m) | k in one instruction

