@@ -5,7 +5,7 @@
 //
 // Both read every block of a sequence once and nothing else of size, so they are bound by the
 // stream of 4-bit blocks (68 bytes per row of 128) as long as the arithmetic keeps up: the codes
-// are unpacked in registers (5 instructions for 8 codes of K, 9 of V) and multiplied on the tensor cores.
+// are unpacked in registers (9 instructions for 8 codes) and multiplied on the tensor cores.
 //
 // scan_kernel (whole sequences): a CTA owns a group of up to 4 head sets (a head set: up to 4 query
 // heads of one KV head, or up to 8 where there are more than 4 to a KV head) and a share of the batch's
@@ -190,7 +190,7 @@ struct Q4Ring {
 
 // kAttend: attention partials; otherwise logits and (max, sum exp) partials.
 //
-// Measured: attention of four sequences, 924K tokens, 32 heads over 8 of 128: 190 us, 5.3 TB/s of blocks;
+// Measured: attention of four sequences, 924K tokens, 32 heads over 8 of 128: 196 us, 5.1 TB/s of blocks;
 // what binds is instruction issue (about 70% of the slots; the tensor pipe a quarter). Scores of eight
 // sequences, 783K tokens, 28 heads over 4: 74 us, 2.9 TB/s of blocks and 1.2 TB/s of logits; issue 55%, the
 // rest waits for the tensor and integer pipes, which the unpacking and the products take in turn.
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
     float mul[NT];
     Q4State<NB, NT> st;                                            // (the score uses its m and l alone)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mul[nt] = f.unit(a.scale, nt);
+    for (int nt = 0; nt < NT; ++nt) mul[nt] = a.scale * f.inv[nt];
     st.reset();
     int s = 0, left = n - (p0 + j) * kPage;                        // tokens of the sequence from this page on
     int done = 0;
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas(NB, NT)) gather
   q4_load_query<NB, NT>(f, sq, lane);
   float mul[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) mul[nt] = f.unit(a.scale, nt);
+  for (int nt = 0; nt < NT; ++nt) mul[nt] = a.scale * f.inv[nt];
   Q4State<NB, NT> st;
   st.reset();
   int steps = 0;

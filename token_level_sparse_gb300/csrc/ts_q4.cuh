@@ -56,7 +56,9 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t k) {
 }
 
 // The eight codes of a word as four fp16 pairs, pair i = codes (i, i + 4), each minus 8, exactly:
-// a code in the low mantissa bits of 1024 is 1024 + u, four bits higher it is 1024 + 16 u.
+// a code in the low mantissa bits of 1024 is 1024 + u, four bits higher it is 1024 + 16 u. (The bits alone, as
+// numbers below 2^-14, with 8 times the queries' sum taken off the products, are 4 instructions fewer and made
+// the attention 3% faster, but the tensor cores cut the larger sums off: scores lost a bit.)
 __device__ __forceinline__ void q4_pairs_f16(uint32_t w, uint32_t (&p)[4]) {
   const __half2 m1032 = __half2half2(__ushort_as_half(0xe408));            // -1032
   const __half2 r16 = __half2half2(__ushort_as_half(0x2c00));              // 1 / 16
@@ -68,18 +70,6 @@ __device__ __forceinline__ void q4_pairs_f16(uint32_t w, uint32_t (&p)[4]) {
   p[3] = h2_bits(__hfma2(bits_h2(and_or(h, 0x00f000f0u, 0x64006400u)), r16, m72));
 }
 
-// The same for the scores: pair i as the fp16 numbers below 2^-14 that have the code (pairs 0 and 2) or 16
-// times the code (1 and 3) in their low bits, 2^-24 u and 2^-20 u. Five instructions where the centred codes
-// take nine; the scores make up for the 16, the 2^24 and the 8 on the queries' side (Q4Query). The outputs
-// cannot: taken over a long sequence their 8 sum_i w_i s_i would be many times what is left of the sum.
-__device__ __forceinline__ void q4_pairs_tiny(uint32_t w, uint32_t (&p)[4]) {
-  const uint32_t h = w >> 8;
-  p[0] = w & 0x000f000fu;
-  p[1] = w & 0x00f000f0u;
-  p[2] = h & 0x000f000fu;
-  p[3] = h & 0x00f000f0u;
-}
-
 // Transposes an 8x8 matrix of 16-bit elements held as (row g, columns 2t, 2t + 1).
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t r;
@@ -88,17 +78,13 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
 }
 
 // The queries of up to 4 NT heads as the column operand of the scores: element pairs in the order that
-// q4_pairs_tiny gives the codes. A head's queries are scaled by a power of two so that the largest
-// lies in [2^14, 2^15), those that meet 16 times a code by 1/16 of that, then split into two fp16 terms
-// (hi + lo within 2^-22 of the element, or 2^-35 of the largest). For the head whose scores this lane holds,
-// centre is -8 times the sum of a 64-element block's queries in the products' units, where the sums begin: the
-// codes' rounding error so is at most three times that of centred codes. inv 2^12 undoes the scaling.
+// q4_pairs_f16 gives the codes. A head's queries are scaled by a power of two so that the largest
+// lies in [2^14, 2^15), then split into two fp16 terms (hi + lo within 2^-22 of the element, or
+// 2^-39 of the largest); inv undoes the scaling for the head whose scores this lane holds.
 template <int NB, int NT>
 struct Q4Query {
   uint32_t b[NT][NB][4][2];
-  float inv[NT], centre[NT][NB];
-  // by which products are multiplied to be scores (in this order finite wherever the result is)
-  __device__ __forceinline__ float unit(float scale, int nt) const { return scale * inv[nt] * 4096.f; }
+  float inv[NT];
 };
 
 // q: 4 NT rows of 64 NB floats in shared memory, zeros where there is no head.
@@ -126,27 +112,19 @@ __device__ __forceinline__ void q4_load_query(Q4Query<NB, NT>& f, const float* q
     const int ex = (int)(__float_as_uint(mx) >> 23) - 127;                 // mx < 2^(ex + 1)
     const int sh = max(-126, min(126, 14 - ex));
     const float mul = __uint_as_float((uint32_t)(127 + sh) << 23);
-    f.inv[nt] = __shfl_sync(kFull, __uint_as_float((uint32_t)(127 + 12 - sh) << 23), 8 * t);
+    f.inv[nt] = __shfl_sync(kFull, __uint_as_float((uint32_t)(127 - sh) << 23), 8 * t);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sum += x[nb][i] * mul;
-      sum += __shfl_xor_sync(kFull, sum, 1);
-      sum += __shfl_xor_sync(kFull, sum, 2);
-      f.centre[nt][nb] = __shfl_sync(kFull, sum * (-8.f / 16777216.f), 8 * t);
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
         for (int i2 = 0; i2 < 2; ++i2) {
           const int i = 8 * (ks >> 1) + 2 * (ks & 1) + i2;
-          const float to = i2 ? mul * 0.0625f : mul;
-          const float x0 = x[nb][i] * to, x1 = x[nb][i + 4] * to;
+          const float x0 = x[nb][i] * mul, x1 = x[nb][i + 4] * mul;
           const __half2 hi = __floats2half2_rn(x0, x1);
           const float2 hf = __half22float2(hi);
           f.b[nt][nb][ks][i2] = h2_bits((g & 1) ? __floats2half2_rn(x0 - hf.x, x1 - hf.y) : hi);
         }
-    }
   }
 }
 
@@ -160,12 +138,12 @@ __device__ __forceinline__ void q4_scores(const Q4Query<NB, NT>& f, const uint2 
     uint32_t p[2][2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      q4_pairs_tiny(kw[u][nb].x, p[u][0]);
-      q4_pairs_tiny(kw[u][nb].y, p[u][1]);
+      q4_pairs_f16(kw[u][nb].x, p[u][0]);
+      q4_pairs_f16(kw[u][nb].y, p[u][1]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float c[4] = {f.centre[nt][nb], 0.f, f.centre[nt][nb], 0.f};
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k4 = 0; k4 < 4; ++k4) {
         const int x = k4 >> 1, i = 2 * (k4 & 1);
