@@ -192,7 +192,7 @@ struct Q4Ring {
 //
 // Measured: attention of four sequences, 924K tokens, 32 heads over 8 of 128: 196 us, 5.1 TB/s of blocks;
 // what binds is instruction issue (about 70% of the slots; the tensor pipe a quarter). Scores of eight
-// sequences, 783K tokens, 28 heads over 4: 74 us, 2.9 TB/s of blocks and 1.2 TB/s of logits; issue 55%, the
+// sequences, 783K tokens, 28 heads over 4: 77 us, 2.8 TB/s of blocks and 1.1 TB/s of logits; issue 58%, the
 // rest waits for the tensor and integer pipes, which the unpacking and the products take in turn.
 template <int NB, int NT, bool kAttend>
 __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_kernel(const __grid_constant__ Q4Args a) {
