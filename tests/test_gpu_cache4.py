@@ -465,6 +465,108 @@ def test_the_operators_together_prompt_to_decode():
     assert torch.isfinite(out).all()
 
 
+def _far_calls(ctx, T, k, v, kn, vn, q, cu, table, kp, vp, n):
+    """Everything that reads or writes pages, over the pages of `table`; what it gives."""
+    H, d = q.shape[1:]
+    Hkv = k.shape[1]
+    q4 = ctx.cfg.kv_dtype == T.TS_KV_Q4
+    seq = torch.tensor([n + 1], dtype=torch.int32, device=DEV)
+    ctx.append_prompt(k, v, cu, table, kp, vp)
+    ctx.append_kv(kn, vn, table, seq, kp, vp)
+    ko, vo = torch.zeros(n + 1, Hkv, d, device=DEV), torch.zeros(n + 1, Hkv, d, device=DEV)
+    ctx.read_kv(torch.tensor([0, n + 1], dtype=torch.int32, device=DEV), table, kp, vp, ko, vo)
+    got = [ko, vo]
+    if q4:
+        vote = torch.zeros(1, ctx.max_tokens, device=DEV)
+        ctx.score(q, kp, table, seq, vote)
+        idx = torch.arange(0, n + 1, 3, dtype=torch.int32, device=DEV).view(1, -1)
+        cnt = torch.tensor([idx.shape[1]], dtype=torch.int32, device=DEV)
+        o = [torch.zeros(1, H, d, device=DEV) for _ in range(2)]
+        ctx.attend(q, kp, vp, table, seq, o[0])
+        ctx.sparse_attend(q, kp, vp, table, idx, cnt, o[1])
+        got += [vote[:, :n + 1], *o]
+    assert ctx.status() == 0
+    return [x.clone() for x in got]
+
+
+@pytest.mark.parametrize("kind,pages", [("TS_KV_Q4", 520_000), ("TS_KV_F32", 70_000)])
+def test_pages_past_four_gigabytes(kind, pages):
+    T = tsl()
+    H, Hkv, d, n = 32, 8, 128, 90
+    kv_dtype = getattr(T, kind)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    rows = [torch.randn(m, Hkv, d, generator=g, device=DEV) for m in (n, n, 1, 1)]
+    if kv_dtype == T.TS_KV_Q4:
+        rows = [x.to(torch.bfloat16) for x in rows]
+    q = torch.randn(1, H, d, generator=g, device=DEV)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    results = []
+    for num, first in ((pages, pages - 6), (6, 0)):
+        ctx = T.Context(H, Hkv, d, kv_dtype, 1, 6, num)
+        size = num * T.ts_page_bytes(ctx.cfg)
+        assert num == 6 or size > 1 << 32
+        kp, vp = (torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(2))
+        table = (first + torch.tensor([[5, 0, 3, 1, 4, 2]], device=DEV)).to(torch.int32)
+        results.append(_far_calls(ctx, T, *rows, q, cu, table, kp, vp, n))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_a_decode_chain_captured_once_and_replayed_over_growing_sequences():
+    # append, decode step and attention of the whole cache as one graph on a stream of its own; lengths, rows and
+    # queries change between replays, and eager calls run in between over the same context
+    T = tsl()
+    H, Hkv, d, lens, steps = 32, 8, 128, [300, 1, 47], 20
+    a, b = (Cache(H, Hkv, d, [n + steps for n in lens], seed=31, poison=False) for _ in range(2))
+    B = len(lens)
+    prm = T.params(k=32, n_sink=4, n_local=16, theta=0.9)
+
+    def state(c):
+        z = dict(idx=torch.zeros(B, 52, dtype=torch.int32, device=DEV), cnt=torch.zeros(B, dtype=torch.int32, device=DEV),
+                 o=torch.zeros(B, H, d, device=DEV), full=torch.zeros(B, H, d, device=DEV), lse=torch.zeros(B, H, device=DEV))
+        z.update(q=torch.zeros(B, H, d, device=DEV), kn=torch.zeros(B, Hkv, d, dtype=torch.bfloat16, device=DEV),
+                 vn=torch.zeros(B, Hkv, d, dtype=torch.bfloat16, device=DEV), seq=torch.ones(B, dtype=torch.int32, device=DEV),
+                 cache=c.ctx.cache(1, 52))
+        return z
+
+    def chain(c, z):
+        c.ctx.append_kv(z["kn"], z["vn"], c.pt, z["seq"], c.kp, c.vp)
+        c.ctx.decode_step(z["q"], c.kp, c.vp, c.pt, z["seq"], prm, z["idx"], z["cnt"], z["o"], cache=z["cache"])
+        c.ctx.attend(z["q"], c.kp, c.vp, c.pt, z["seq"], z["full"], z["lse"])
+
+    warm = Cache(H, Hkv, d, [20] * B, seed=1, poison=False)
+    chain(warm, state(warm))
+    za, zb = state(a), state(b)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            chain(a, za)
+    torch.cuda.synchronize()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    for t in range(steps):
+        new = dict(q=torch.randn(B, H, d, generator=g, device=DEV),
+                   kn=torch.randn(B, Hkv, d, generator=g, device=DEV).to(torch.bfloat16),
+                   vn=torch.randn(B, Hkv, d, generator=g, device=DEV).to(torch.bfloat16),
+                   seq=torch.tensor([n + t + 1 for n in lens], dtype=torch.int32, device=DEV))
+        for z in (za, zb):
+            for name, x in new.items():
+                z[name].copy_(x)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            graph.replay()
+        torch.cuda.current_stream().wait_stream(s)
+        chain(b, zb)
+        if t % 5 == 0:                                 # an eager call in between uses the same scratch
+            a.ctx.attend(za["q"], a.kp, a.vp, a.pt, za["seq"], torch.empty_like(za["full"]))
+        for name in ("idx", "cnt", "o", "full", "lse"):
+            assert torch.equal(za[name], zb[name]), (t, name)
+    assert a.ctx.status() == 0 and b.ctx.status() == 0
+
+
 def test_calls_that_the_context_does_not_serve():
     T = tsl()
     c = Cache(8, 4, 64, [20], seed=2)

@@ -231,6 +231,26 @@ def test_three_hundred_prompts_at_once():
     _check(out, lse, q, k, v, cu, 1 / math.sqrt(d), sorted(rows))
 
 
+def test_rows_past_four_gigabytes():
+    # the last prompt lies behind 2^31 elements of q and out: the same bits as by itself
+    H, Hkv, d, n, many = 32, 8, 128, 333, 530
+    q, k, v, cu1, _ = _make(H, Hkv, d, [n], seed=12)
+    rows = many * 1000 + n
+    cu = torch.tensor([1000 * i for i in range(many + 1)] + [rows], dtype=torch.int32, device=DEV)
+    big = [torch.zeros(rows, x.shape[1], d, dtype=torch.bfloat16, device=DEV) for x in (q, k, v)]
+    assert (rows - n) * H * d > 1 << 31
+    for x, y in zip(big, (q, k, v)):
+        x[-n:] = y
+    out, lse = torch.zeros(rows, H, d, dtype=torch.bfloat16, device=DEV), torch.zeros(rows, H, device=DEV)
+    ctx = _ctx(H, Hkv, d, many + 1)
+    ctx.prompt_attend(*big, cu, out, lse)
+    out1, lse1 = torch.zeros(n, H, d, dtype=torch.bfloat16, device=DEV), torch.zeros(n, H, device=DEV)
+    ctx.prompt_attend(q, k, v, cu1, out1, lse1)
+    assert ctx.status() == 0
+    assert torch.equal(out[-n:], out1) and torch.equal(lse[-n:], lse1)
+    assert not out[:-n].any()
+
+
 def test_bad_boundaries_are_reported_and_nothing_else_is_written():
     T = tsl()
     H, Hkv, d = 8, 4, 64
