@@ -114,10 +114,10 @@ __global__ void __launch_bounds__(kRowsThreads) append_rows_kernel(const __grid_
 // each, so a quotient that is not halfway between two codes is at least 2^-9 away from it (numerator
 // and denominator of the difference are whole numbers below 2^9 of one unit), and likewise max|x| / 7
 // lies 2^-12 away from any midpoint of bf16. A product with 1/7 that is right to 2^-22 therefore rounds
-// to the right scale. A quotient x r, r near 1/s, is off by a few units in the last place: its residual
-// x - q s is exact in one fused multiply-add, and q + residual r (Markstein's correction) is the exact
-// quotient where that has few bits, as it has halfway between codes. Scales near or below the smallest
-// normal number have fewer bits and take the divisions instead.
+// to the right scale. A quotient x r, r near 1/s, is off by less than 2^-19, and is rounded twice: to a
+// multiple of 2^-10 (by a sum with 1.5 2^13), which makes a quotient halfway between codes exact and leaves
+// every other one on its side of halfway, then to a whole number, ties to even (by a sum with 1.5 2^23).
+// Scales near or below the smallest normal number have fewer bits and take the divisions instead.
 //
 // Measured: 33,122 rows of 8 KV heads of 128, K and V: 51 us, 3.4 TB/s, bound by issue and by the blocks'
 // small stores (with the divisions throughout 104 us; four loads under way, more gave nothing).
@@ -167,23 +167,18 @@ __global__ void __launch_bounds__(kRowsThreads) append_q4_kernel(const __grid_co
         const float s = __bfloat162float(sb);
         float rs;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(s));
-        const uint64_t s2 = pack_f2(-s, -s), r2 = pack_f2(rs, rs), zero = pack_f2(0.f, 0.f),
-                       magic = pack_f2(12582920.f, 12582920.f), one = pack_f2(1.f, 1.f);
-        uint32_t u[8];
+        const uint64_t r2 = pack_f2(rs, rs), fine = pack_f2(12288.f, 12288.f),
+                       whole = pack_f2(12582920.f - 12288.f, 12582920.f - 12288.f), one = pack_f2(1.f, 1.f);
+        uint32_t u[4];                   // two codes in the low byte
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint64_t x = pack_f2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u));
-          uint64_t q = fma_f2(x, r2, zero);
-          q = fma_f2(fma_f2(q, s2, x), r2, q);
-          // a whole number behind the sum's point: 8 + code in the low byte, since |q| < 7.1 (s >= top / 7 (1 - 2^-8))
+          // 1.5 2^23 + 8 + the rounded quotient: the code in the low byte, since |q| < 7.1 (s >= top / 7 (1 - 2^-8))
           float lo, hi;
-          unpack_f2(fma_f2(q, one, magic), lo, hi);
-          u[2 * e] = __float_as_uint(lo);
-          u[2 * e + 1] = __float_as_uint(hi);
+          unpack_f2(fma_f2(fma_f2(x, r2, fine), one, whole), lo, hi);
+          u[e] = __float_as_uint(hi) * 16u + __float_as_uint(lo);
         }
-        const uint32_t even = __byte_perm(__byte_perm(u[0], u[2], 0x0040), __byte_perm(u[4], u[6], 0x0040), 0x5410);
-        const uint32_t odd = __byte_perm(__byte_perm(u[1], u[3], 0x0040), __byte_perm(u[5], u[7], 0x0040), 0x5410);
-        w = even | odd << 4;
+        w = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
       } else {
         sb = __float2bfloat16_rn(__fdiv_rn(top, 7.f));
         const float s = __bfloat162float(sb);
