@@ -12,8 +12,12 @@
 namespace ts {
 namespace {
 
-constexpr int kRowsThreads = 256;
-constexpr int kRowsPerCta = 16;   // at most: 16, 4 or 1
+// Rows of a CTA: four, whose codes are 128 contiguous bytes, or one where there are few rows, so that a decode
+// step's rows do not queue behind one another. 33,122 rows written and read back: 89.5 us with four rows
+// and 128 threads, 92.5 with 64 threads, 94.7 with 16 rows and 256 threads, 120 with two rows. Eight rows, one to a
+// CTA, written and read back: 4.6 us with 256 threads, 4.8 with 128.
+constexpr int kRowsPerCta = 4;
+__host__ __device__ constexpr int rows_threads(int rows) { return rows == 1 ? 256 : 128; }
 
 struct RowsArgs {
   const int32_t* cu;           // [B + 1]; null: one row per sequence, at position seq_lens[b] - 1
@@ -88,14 +92,14 @@ __device__ __forceinline__ void place_rows(const RowsArgs& a, int64_t* place) {
 }
 
 // bf16 and fp32 pools: rows copied as they are, 16 bytes per thread, four under way. Bound by memory.
-__global__ void __launch_bounds__(kRowsThreads) append_rows_kernel(const __grid_constant__ RowsArgs a, int row_bytes) {
+__global__ void __launch_bounds__(rows_threads(1)) append_rows_kernel(const __grid_constant__ RowsArgs a, int row_bytes) {
   __shared__ int64_t place[kRowsPerCta];
   place_rows(a, place);
   const int cpr = row_bytes / 16, per_row = 2 * a.HKV * cpr;
   const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
   const int ps = 1 << a.page_shift;
 #pragma unroll 4
-  for (int i = threadIdx.x; i < per_row * a.rows_per_cta; i += kRowsThreads) {
+  for (int i = threadIdx.x; i < per_row * a.rows_per_cta; i += blockDim.x) {
     const int row = i / per_row, rem = i % per_row, isv = rem >= a.HKV * cpr;
     const int c = rem - isv * a.HKV * cpr, g = c / cpr, ch = c % cpr;
     const int64_t at = place[row];
@@ -119,12 +123,12 @@ __global__ void __launch_bounds__(kRowsThreads) append_rows_kernel(const __grid_
 // every other one on its side of halfway, then to a whole number, ties to even (by a sum with 1.5 2^23).
 // Scales near or below the smallest normal number have fewer bits and take the divisions instead.
 //
-// Measured: 33,122 rows of 8 KV heads of 128, K and V: 51 us, 3.4 TB/s, bound by issue and by the blocks'
-// small stores (with the divisions throughout 104 us; four loads under way, more gave nothing).
+// Measured: 33,122 rows of 8 KV heads of 128, K and V: 43 us, 4.0 TB/s, bound by issue (with the divisions
+// throughout 104 us; eight loads under way in place of four 2 us more).
 template <int NB, int ROWS>
-__global__ void __launch_bounds__(kRowsThreads) append_q4_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(rows_threads(ROWS)) append_q4_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ int64_t place[kRowsPerCta];
-  constexpr int D = NB * 64, BLK = q4_block_bytes(D), CODES = q4_code_bytes(D), COLS = kRowsThreads / 8 / ROWS;
+  constexpr int D = NB * 64, BLK = q4_block_bytes(D), CODES = q4_code_bytes(D), COLS = rows_threads(ROWS) / 8 / ROWS;
   constexpr int BATCH = 4;               // loads under way per thread
   const int groups = a.HKV * NB, lane8 = threadIdx.x & 7;
   // neighbouring groups of eight lanes take neighbouring rows of the same 64 elements: their codes
@@ -220,10 +224,10 @@ struct RawQuads<TS_KV_F32> {
 };
 
 template <int kType, int ROWS>
-__global__ void __launch_bounds__(kRowsThreads) read_rows_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(rows_threads(ROWS)) read_rows_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ int64_t place[kRowsPerCta];
   place_rows(a, place);
-  constexpr int COLS = kRowsThreads / 8 / ROWS, BATCH = 4;
+  constexpr int COLS = rows_threads(ROWS) / 8 / ROWS, BATCH = 4;
   const int NB = a.D / 64, groups = a.HKV * NB, lane8 = threadIdx.x & 7, ps = 1 << a.page_shift;
   const int row = (threadIdx.x >> 3) % ROWS;
   const int64_t r = (int64_t)blockIdx.x * ROWS + row;
@@ -285,8 +289,7 @@ RowsArgs base_args(ts_ctx* ctx, int B, int total, const int32_t* page_table, voi
   RowsArgs a{};
   a.B = B;
   a.total = total;
-  // few rows: one per CTA, so that a decode step's rows do not queue behind one another
-  a.rows_per_cta = total >= kRowsPerCta * ctx->num_sms ? kRowsPerCta : (total >= 2 * ctx->num_sms ? 4 : 1);
+  a.rows_per_cta = total >= 2 * ctx->num_sms ? kRowsPerCta : 1;
   a.page_table = page_table;
   a.pt_stride = c.max_pages_per_seq;
   a.page_shift = ctx->page_shift;
@@ -304,12 +307,12 @@ ts_status run_append(ts_ctx* ctx, const RowsArgs& a, cudaStream_t s) {
   const int grid = (a.total + a.rows_per_cta - 1) / a.rows_per_cta;
   ctx->kernels += 1;
 #define TS_APPEND_Q4(NB_, ROWS_) \
-  if (a.D == 64 * NB_ && a.rows_per_cta == ROWS_) append_q4_kernel<NB_, ROWS_><<<grid, kRowsThreads, 0, s>>>(a);
+  if (a.D == 64 * NB_ && a.rows_per_cta == ROWS_) append_q4_kernel<NB_, ROWS_><<<grid, rows_threads(ROWS_), 0, s>>>(a);
   if (ctx->cfg.kv_dtype == TS_KV_Q4) {
-    TS_APPEND_Q4(1, 1) TS_APPEND_Q4(1, 4) TS_APPEND_Q4(1, 16) TS_APPEND_Q4(2, 1) TS_APPEND_Q4(2, 4) TS_APPEND_Q4(2, 16)
+    TS_APPEND_Q4(1, 1) TS_APPEND_Q4(1, kRowsPerCta) TS_APPEND_Q4(2, 1) TS_APPEND_Q4(2, kRowsPerCta)
   } else
 #undef TS_APPEND_Q4
-    append_rows_kernel<<<grid, kRowsThreads, 0, s>>>(a, a.D * (ctx->cfg.kv_dtype == TS_KV_BF16 ? 2 : 4));
+    append_rows_kernel<<<grid, rows_threads(a.rows_per_cta), 0, s>>>(a, a.D * (ctx->cfg.kv_dtype == TS_KV_BF16 ? 2 : 4));
   return cuda_status(cudaGetLastError());
 }
 
@@ -351,10 +354,10 @@ ts_status launch_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* sta
   ctx->kernels += 1;
 #define TS_READ_ROWS(TYPE_, ROWS_)                                      \
   if (ctx->cfg.kv_dtype == TYPE_ && a.rows_per_cta == ROWS_) \
-    read_rows_kernel<TYPE_, ROWS_><<<grid, kRowsThreads, 0, s>>>(a);
-  TS_READ_ROWS(TS_KV_Q4, 1) TS_READ_ROWS(TS_KV_Q4, 4) TS_READ_ROWS(TS_KV_Q4, 16)
-  TS_READ_ROWS(TS_KV_BF16, 1) TS_READ_ROWS(TS_KV_BF16, 4) TS_READ_ROWS(TS_KV_BF16, 16)
-  TS_READ_ROWS(TS_KV_F32, 1) TS_READ_ROWS(TS_KV_F32, 4) TS_READ_ROWS(TS_KV_F32, 16)
+    read_rows_kernel<TYPE_, ROWS_><<<grid, rows_threads(ROWS_), 0, s>>>(a);
+  TS_READ_ROWS(TS_KV_Q4, 1) TS_READ_ROWS(TS_KV_Q4, kRowsPerCta)
+  TS_READ_ROWS(TS_KV_BF16, 1) TS_READ_ROWS(TS_KV_BF16, kRowsPerCta)
+  TS_READ_ROWS(TS_KV_F32, 1) TS_READ_ROWS(TS_KV_F32, kRowsPerCta)
 #undef TS_READ_ROWS
   return cuda_status(cudaGetLastError());
 }
