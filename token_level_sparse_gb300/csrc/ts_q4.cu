@@ -29,9 +29,8 @@ namespace {
 constexpr int kScorePages = 4;                  // pages of a stage of the score (4 against 2: 79 against 85 us, 783K tokens)
 constexpr int kScanSeqs = 512;                  // sequences whose page counts a scan CTA keeps in shared memory
 constexpr int kQ4Sets = 4;                      // head sets of a CTA, at most
-constexpr int kGatherWarps = 4;
-constexpr int kGatherCtas = 4;                  // gather CTAs per SM
-constexpr int gather_ctas(int nb, int nt) { return nb * nt == 4 ? 3 : kGatherCtas; }   // (3: registers)
+constexpr int kGatherWarps = 6;
+constexpr int kGatherCtas = 2;                  // gather CTAs per SM
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Q4Args {
@@ -632,10 +631,13 @@ struct Q4GatherArgs {
 
 // CTA (split, head set, sequence): a contiguous part of the index list, 16 tokens per warp and step. Bound by
 // a chain of latencies (list, page id, row), so the list is spread over as many CTAs as fit at once and
-// the next step's ids are looked up early: 2564 of 131,057 tokens, 32 heads over 8: 9.6 us, then the merge.
+// the next step's ids are looked up early: 2564 of 131,057 tokens, 32 heads over 8: 9.0 us, then the merge. Two
+// CTAs of six warps to an SM: with merge, that list takes 9.2 us and one of 20,000 17.3 (four CTAs of four
+// warps: 10.3 and 18.4; two of eight, as far as the registers allow: 9.6 and 16.8, but eight lists of 10,000
+// with 28 heads over 4 58 in place of 47).
 template <int NB, int NT>
-__global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas(NB, NT)) gather_kernel(const __grid_constant__ Q4Args a,
-                                                                   const __grid_constant__ Q4GatherArgs ga) {
+__global__ void __launch_bounds__(kGatherWarps * 32, kGatherCtas) gather_kernel(const __grid_constant__ Q4Args a,
+                                                                                  const __grid_constant__ Q4GatherArgs ga) {
   constexpr int D = NB * 64, BLK = q4_block_bytes(D), CODES = q4_code_bytes(D);
   __shared__ __align__(16) float merge[kGatherWarps][4 * NT][D];
   __shared__ __align__(16) float sq[4 * NT * D];
@@ -835,9 +837,11 @@ int64_t q4_part_slots(const ts_config& c, int num_sms) { return kGatherCtas * (i
 ts_status launch_attend_q4(ts_ctx* ctx, const AttendCall& c, const int32_t* seq_lens, cudaStream_t s) {
   Q4Args a = make_args(ctx, c.q, c.k_pool, c.v_pool, c.page_table, seq_lens, c.B, c.scale * kLog2e);
   if (!c.idx) return TS_Q4_DISPATCH(run_attend, ctx, a, c.out, c.lse, s);
-  // as many CTAs as fit the GPU at once
-  const int sets = a.HKV * a.sets_per_kv * a.B, fit = gather_ctas(ctx->cfg.head_dim / 64, a.set_heads / 4) * ctx->num_sms;
-  const int splits = std::max(1, std::min(fit / sets, kAttnMaxSplits));
+  // as many CTAs as fit the GPU at once, but no more than have a step for each of their warps: every part
+  // costs the merge
+  const int sets = a.HKV * a.sets_per_kv * a.B, fit = kGatherCtas * ctx->num_sms / sets;
+  const int64_t full = (c.idx_stride + 16 * kGatherWarps - 1) / (16 * kGatherWarps);
+  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(fit, kAttnMaxSplits), full));
   Q4GatherArgs ga{c.idx, c.idx_stride, c.count, splits};
   return TS_Q4_DISPATCH(run_gather, ctx, a, ga, c.out, c.lse, s);
 }
