@@ -1,0 +1,92 @@
+"""Values over a 4-bit cache that differ widely in size, or are not finite: the attention over the whole
+cache and over a list, and a decode step, against the fp64 oracle, each 64 elements of a head by itself.
+
+Tolerance: that of the 4-bit cache's other tests, with what a weight times its scale may lose counted per 64
+elements: two fp16 terms hold it within 2^-22 of itself, or within 2^-31 of the largest such product of the
+same 64 elements, which a code multiplies by 7 at most (so n 2^-31 of the largest weight times the largest
+value of a row's 64 elements).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from parity import tsl
+from test_gpu_cache4 import Cache
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _check(c, out, lse, b, tokens, spoilt=()):
+    """out, lse of sequence b against the oracle; spoilt: (KV head, 64 elements) that have to be NaN throughout."""
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    d, n, scale = c.d, len(tokens), 1 / math.sqrt(c.d)
+    for h in range(c.H):
+        g = h // (c.H // c.Hkv)
+        q = c.q[b, h].double().cpu().numpy()
+        k, v = c.rows(c.kval, b, g, tokens), c.rows(c.vval, b, g, tokens)
+        _, wl, w = O.attention(q, k, np.zeros_like(k), scale)
+        el = scale * float(np.max(np.abs(k) @ np.abs(q) * (d + 16) * 2.0 ** -24
+                                  + np.abs(k).sum(1) * np.abs(q).max() * 2.0 ** -21))
+        assert abs(lse[b, h] - wl) <= el + n * 2.0 ** -23 + 2.0 ** -20 + abs(wl) * 2.0 ** -22
+        for half in range(d // 64):
+            e = slice(64 * half, 64 * half + 64)
+            if (g, half) in spoilt:
+                assert np.isnan(out[b, h, e]).all(), (b, h, half)
+                continue
+            want, mag = w @ v[:, e], w @ np.abs(v[:, e])
+            big = n * float(np.max(w * np.abs(v[:, e]).max(1))) * 2.0 ** -31
+            tol = mag * (2 * el + 2.0 ** -21 + 2.0 ** -20 + n * 2.0 ** -23) + big + 1e-30
+            bad = np.abs(out[b, h, e] - want) / tol
+            assert np.all(bad <= 1), (b, h, half, float(np.max(bad)), want[:2], out[b, h, e][:2])
+
+
+def _write(c, k=None, v=None):
+    c.ctx.append_prompt(c.k if k is None else k, c.v if v is None else v, c.cu, c.pt, c.kp, c.vp)
+    c.kval, c.vval = (O.q4_pool_values(x.cpu().numpy(), c.d) for x in (c.kp, c.vp))
+
+
+def _both(c, n):
+    """Every token of the only sequence, through the whole-cache call and through a list."""
+    out, lse = torch.zeros(1, c.H, c.d, device=DEV), torch.zeros(1, c.H, device=DEV)
+    idx = torch.arange(n, dtype=torch.int32, device=DEV).view(1, n)
+    for call in (lambda: c.ctx.attend(c.q, c.kp, c.vp, c.pt, c.seq, out, lse),
+                 lambda: c.ctx.sparse_attend(c.q, c.kp, c.vp, c.pt, idx, c.seq, out, lse)):
+        out.zero_()
+        lse.zero_()
+        call()
+        assert c.ctx.status() == 0
+        yield out, lse
+
+
+@pytest.mark.parametrize("H,Hkv", [(8, 2), (28, 4)])
+@pytest.mark.parametrize("n", [16, 300, 2049])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_value_that_is_not_finite_spoils_its_own_64_elements_only(H, Hkv, n, bad):
+    c = Cache(H, Hkv, 128, [n], seed=n + H)
+    v = c.v.clone()
+    v[3, 0, 70] = v[n - 1, 1, 5] = bad
+    _write(c, v=v)
+    for out, lse in _both(c, n):
+        _check(c, out, lse, 0, np.arange(n), spoilt=((0, 1), (1, 0)))
+    # a decode step, whose sinks and window hold both rows
+    T = tsl()
+    idx, cnt = torch.zeros(1, 84, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = torch.zeros(1, H, 128, device=DEV), torch.zeros(1, H, device=DEV)
+    c.ctx.decode_step(c.q, c.kp, c.vp, c.pt, c.seq, T.params(k=64, n_sink=4, n_local=16), idx, cnt, out, lse)
+    assert c.ctx.status() == 0
+    _check(c, out, lse, 0, idx[0, :int(cnt[0])].cpu().numpy(), spoilt=((0, 1), (1, 0)))
+
+
+@pytest.mark.parametrize("H,Hkv", [(8, 2), (28, 4)])
+@pytest.mark.parametrize("n,at", [(64, 40), (700, 3), (16000, 8000)])
+def test_a_large_value_costs_the_other_64_elements_nothing(H, Hkv, n, at):
+    c = Cache(H, Hkv, 128, [n], seed=n + 1)
+    v = c.v.clone()
+    v[at, :, 64:] *= 2.0 ** 40
+    _write(c, v=v)
+    for out, lse in _both(c, n):
+        _check(c, out, lse, 0, np.arange(n))

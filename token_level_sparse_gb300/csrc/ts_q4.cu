@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
   constexpr int D = NB * 64, CODES = q4_code_bytes(D);
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) uint64_t full[R::WARPS][R::STAGES];
-  __shared__ float2 s_ml[R::WARPS][4 * NT], s_units[kAttend ? R::WARPS : 1][4 * NT];
+  __shared__ float2 s_ml[R::WARPS][4 * NT];
+  __shared__ Q4Unit<NB> s_units[kAttend ? R::WARPS : 1][4 * NT];
   __shared__ int s_pages[kScanSeqs];
   __shared__ Q4Range s_left;           // the CTA's pages that no part has been made of yet
   __shared__ int s_part[4];            // the part at work: is there one, sequence, first page, end
@@ -442,10 +443,14 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
     }
     if constexpr (kAttend) {
       st.flush(sums, s_units[warp], done < kQ4Flush, lane);
-      // each warp's own factor: from its maximum to the set's, and out of its power of two
+      // each warp's own factors: from its maximum to the set's, and out of its powers of two
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        if (g == 0) s_units[warp][4 * nt + t] = make_float2(fac[nt], __uint_as_float((254u << 23) - __float_as_uint(st.sc[nt])));
+        if (g == 0) {
+          s_units[warp][4 * nt + t].m = fac[nt];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) s_units[warp][4 * nt + t].sc[nb] = __uint_as_float((254u << 23) - __float_as_uint(st.sc[nt][nb]));
+        }
       __syncthreads();
       if (works) {
         float* po = a.part_o + ((int64_t)(cta + b) * a.H + head0) * D;
@@ -453,8 +458,8 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
         for (int i = j * 32 + lane; i < nh * D; i += per_set * 32) {
           float acc = 0.f;
           for (int w = 0; w < per_set; ++w) {
-            const float2 f = s_units[hs * per_set + w][i / D];
-            acc = fmaf(rows[w * (4 * NT * D) + i] * f.y, f.x, acc);
+            const Q4Unit<NB>& f = s_units[hs * per_set + w][i / D];
+            acc = fmaf(rows[w * (4 * NT * D) + i] * f.sc[i % D / 64], f.m, acc);
           }
           po[i] = acc;
         }
@@ -641,7 +646,8 @@ __global__ void __launch_bounds__(kGatherWarps * 32, kGatherCtas) gather_kernel(
   constexpr int D = NB * 64, BLK = q4_block_bytes(D), CODES = q4_code_bytes(D);
   __shared__ __align__(16) float merge[kGatherWarps][4 * NT][D];
   __shared__ __align__(16) float sq[4 * NT * D];
-  __shared__ float2 s_ml[kGatherWarps][4 * NT], s_units[kGatherWarps][4 * NT];
+  __shared__ float2 s_ml[kGatherWarps][4 * NT];
+  __shared__ Q4Unit<NB> s_units[kGatherWarps][4 * NT];
   const int split = blockIdx.x, set = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int kv = set / a.sets_per_kv, head0 = kv * a.G + (set % a.sets_per_kv) * (4 * NT);
@@ -736,7 +742,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32, kGatherCtas) gather_kernel(
     for (int w = 0; w < kGatherWarps; ++w) {
       const float wt = part_weight(s_ml[w][hg].x, M);
       L = fmaf(wt, s_ml[w][hg].y, L);
-      O = fmaf(wt, merge[w][hg][i % D] * __uint_as_float((254u << 23) - __float_as_uint(s_units[w][hg].y)), O);
+      O = fmaf(wt, merge[w][hg][i % D] * __uint_as_float((254u << 23) - __float_as_uint(s_units[w][hg].sc[i % D / 64])), O);
     }
     a.part_o[(slot * a.H + head0) * D + i] = O;
     if (i % D == 0) a.part_ml[(head0 + hg) * a.slots + slot] = make_float2(M, L);

@@ -160,33 +160,42 @@ __device__ __forceinline__ void q4_scores(const Q4Query<NB, NT>& f, const uint2 
 }
 
 // Running softmax state of 4 NT heads in one warp, for head 4 nt + t: m its maximum (the same in the
-// eight lanes of a head), l this lane's own part of its sum, o its outputs times sc, a power of two (high
-// parts in elements 0 and 2, low parts in 1 and 3): tile j, rows g and g + 8, are elements 64 nb + 8 g + j
-// and + 4. A weight times its value's scale enters its product as two fp16 terms, held with sc between the
-// largest so far at 2^6 and 2^13: within 2^-22 of it, or 2^-31 of the largest. `big` bounds the products
-// summed so far, in units of sc, so that a later sc never takes the sums out of range.
+// eight lanes of a head), l this lane's own part of its sum, o its outputs times sc, a power of two of its own
+// for each 64 elements (high parts in elements 0 and 2, low parts in 1 and 3): tile j, rows g and g + 8, are
+// elements 64 nb + 8 g + j and + 4. A weight times its value's scale enters its product as two fp16 terms, held
+// with sc between the largest so far at 2^6 and 2^13: within 2^-22 of it, or 2^-31 of the largest of the same 64
+// elements. Groups do not share sc, so that one whose values are large, or not finite, takes nothing from the
+// others. `big` bounds the products summed so far, in units of sc, so that a later sc never takes the sums out of
+// range.
 //
 // The tensor cores cut their sums off rather than round them: over a few hundred steps in one accumulator
 // that is 3e-6 of an output. So the sums go over to rows in shared memory every kQ4Flush stages, added
 // there with rounding, and begin again at zero.
 constexpr int kQ4Flush = 16;
+// What a head's sums in shared memory count in: the maximum and the powers of two that they belong to.
+template <int NB>
+struct Q4Unit {
+  float m, sc[NB];
+};
+
 template <int NB, int NT>
 struct Q4State {
-  float m[NT], l[NT], sc[NT], big[NT];
+  float m[NT], l[NT], sc[NT][NB], big[NT][NB];
   float o[NT][NB][4][4];
   __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt] = -INFINITY;
       l[nt] = 0.f;
-      sc[nt] = 1.f;
-      big[nt] = 0.f;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb) {
+        sc[nt][nb] = 1.f;
+        big[nt][nb] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[nt][nb][j][e] = 0.f;
+      }
     }
   }
   __device__ __forceinline__ void join_lanes() {
@@ -198,19 +207,19 @@ struct Q4State {
     }
   }
   // Moves the sums over to rows [head][64 NB] (in shared memory, this warp's own), whose units are kept in
-  // units[head]: the maximum and sc that they belong to. first: there is nothing in the rows yet.
-  __device__ __forceinline__ void flush(float* rows, float2* units, bool first, int lane) {
+  // units[head]. first: there is nothing in the rows yet.
+  __device__ __forceinline__ void flush(float* rows, Q4Unit<NB>* units, bool first, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float f = 0.f;
-      if (!first) {
-        const float2 was = units[4 * nt + t];
-        const int step = (int)(__float_as_uint(sc[nt]) >> 23) - (int)(__float_as_uint(was.y) >> 23);
-        f = (was.x == m[nt] ? 1.f : ex2(was.x - m[nt])) * __uint_as_float((uint32_t)(127 + max(-126, min(step, 126))) << 23);
-      }
+      Q4Unit<NB>& unit = units[4 * nt + t];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb) {
+        float f = 0.f;
+        if (!first) {
+          const int step = (int)(__float_as_uint(sc[nt][nb]) >> 23) - (int)(__float_as_uint(unit.sc[nb]) >> 23);
+          f = (unit.m == m[nt] ? 1.f : ex2(unit.m - m[nt])) * __uint_as_float((uint32_t)(127 + max(-126, min(step, 126))) << 23);
+        }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           float4* row = reinterpret_cast<float4*>(rows + (4 * nt + t) * (NB * 64) + nb * 64 + 8 * g + 4 * r);
@@ -224,8 +233,13 @@ struct Q4State {
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[nt][nb][j][2 * r] = o[nt][nb][j][2 * r + 1] = 0.f;
         }
+      }
       __syncwarp();
-      if (g == 0) units[4 * nt + t] = make_float2(m[nt], sc[nt]);
+      if (g == 0) {
+        unit.m = m[nt];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) unit.sc[nb] = sc[nt][nb];
+      }
     }
     __syncwarp();
   }
@@ -256,13 +270,14 @@ __device__ __forceinline__ bool q4_raise_max(Q4State<NB, NT>& s, const float (&x
       const float f = s.m[nt] == mn ? 1.f : ex2(s.m[nt] - mn);
       s.m[nt] = mn;
       s.l[nt] *= f;
-      s.big[nt] *= f;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb) {
+        s.big[nt][nb] *= f;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s.o[nt][nb][j][e] *= f;
+      }
     }
   }
   return raised;
@@ -275,44 +290,45 @@ __device__ __forceinline__ bool q4_raise_max(Q4State<NB, NT>& s, const float (&x
 template <int NB, int NT, bool kMasked>
 __device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&x)[NT][2], const uint32_t (&vw)[4][NB],
                                               const float (&vs)[NB][2], bool refresh) {
-  float w[NT][NB][2], top[NT];
+  float w[NT][NB][2], top[NT][NB];
   bool over = refresh;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    top[nt] = 0.f;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) top[nt][nb] = 0.f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const bool out = kMasked && x[nt][u] == -INFINITY;
       const float p = out ? 0.f : ex2(x[nt][u] - s.m[nt]);
       s.l[nt] += p;
-      const float ps = p * s.sc[nt];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         // a token that is not attended may lie in a slot never written: its scale is not used
-        w[nt][nb][u] = out ? 0.f : ps * vs[nb][u];
-        top[nt] = fmaxf(top[nt], w[nt][nb][u]);
+        w[nt][nb][u] = out ? 0.f : p * s.sc[nt][nb] * vs[nb][u];
+        top[nt][nb] = fmaxf(top[nt][nb], w[nt][nb][u]);
       }
     }
-    over |= top[nt] > 8192.f;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) over |= top[nt][nb] > 8192.f;
   }
   if (__any_sync(kFull, over)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float t = top[nt];
-      t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
-      t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
-      t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
-      if (t > 0.f && (refresh || t > 8192.f)) {
-        // t to [2^6, 2^7), but not so far up that products summed before pass 2^40: next to those, these count
-        // for nothing
-        const int was = (int)(__float_as_uint(s.sc[nt]) >> 23) - 127;
-        int step = min(6 - ((int)(__float_as_uint(t) >> 23) - 127), 40 - ((int)(__float_as_uint(s.big[nt]) >> 23) - 127));
-        step = max(max(-120, -120 - was), min(min(step, 120), 120 - was));
-        const float f = __uint_as_float((uint32_t)(127 + step) << 23);
-        s.sc[nt] *= f;
-        s.big[nt] = fmaxf(8192.f, s.big[nt] * f);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+      for (int nb = 0; nb < NB; ++nb) {
+        float t = top[nt][nb];
+        t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
+        t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
+        t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
+        if (t > 0.f && (refresh || t > 8192.f)) {
+          // t to [2^6, 2^7), but not so far up that products summed before pass 2^40: next to those, these count
+          // for nothing
+          const int was = (int)(__float_as_uint(s.sc[nt][nb]) >> 23) - 127;
+          int step = min(6 - ((int)(__float_as_uint(t) >> 23) - 127), 40 - ((int)(__float_as_uint(s.big[nt][nb]) >> 23) - 127));
+          step = max(max(-120, -120 - was), min(min(step, 120), 120 - was));
+          const float f = __uint_as_float((uint32_t)(127 + step) << 23);
+          s.sc[nt][nb] *= f;
+          s.big[nt][nb] = fmaxf(8192.f, s.big[nt][nb] * f);
           w[nt][nb][0] *= f;
           w[nt][nb][1] *= f;
 #pragma unroll
