@@ -90,3 +90,22 @@ def test_a_large_value_costs_the_other_64_elements_nothing(H, Hkv, n, at):
     _write(c, v=v)
     for out, lse in _both(c, n):
         _check(c, out, lse, 0, np.arange(n))
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 4, 64), (32, 8, 128), (28, 4, 128)])
+@pytest.mark.parametrize("gap,small,large", [(110.0, 1.0, 1e30), (80.0, 1.0, 2000.0), (70.0, 1e-4, 2000.0), (55.0, 1e-9, 1e20),
+                                             (30.0, 1e20, 1e-20)])
+def test_logits_that_jump_far_between_pages(H, Hkv, d, gap, small, large):
+    # the keys of half of the pages give logits `gap` below the others': the softmax has a new maximum in the first or
+    # the second page of a warp's pair, and what came before counts for little or nothing
+    n = 16000
+    c = Cache(H, Hkv, d, [n], seed=5)
+    # the heads share their query, 1.0 throughout; a key is its level in every element, and some noise
+    c.q[:] = 1.0
+    rng = np.random.default_rng(3)
+    low = torch.from_numpy(np.repeat(rng.integers(0, 2, n // 16), 16)).to(DEV).view(n, 1, 1)
+    k = (low * (-gap / math.sqrt(d)) + 0.05 * torch.randn(n, Hkv, d, device=DEV)).to(torch.bfloat16)
+    _write(c, k=k, v=(c.v.float() * torch.where(low > 0, small, large)).to(torch.bfloat16))
+    for out, lse in _both(c, n):
+        assert torch.isfinite(out).all()
+        _check(c, out, lse, 0, np.arange(n))

@@ -283,58 +283,66 @@ __device__ __forceinline__ bool q4_raise_max(Q4State<NB, NT>& s, const float (&x
   return raised;
 }
 
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }   // -127: 0
+
 // Adds 16 tokens whose logits x[nt][u] (head 4 nt + t, token (u, g)) the maxima already cover: vs[nb][u]
 // are that token's value scales, vw[i][nb] word g of the codes of token (i / 2, 2t + i % 2). kMasked: some
 // tokens may not be attended (x = -inf). refresh: sc is chosen anew from these tokens (after a maximum moved;
-// otherwise only where a term would pass 2^13).
+// otherwise only where a term may pass 2^13).
+//
+// A new sc comes from the exponents of weights and scales, and the terms are formed again from both: a term in
+// the old unit may have passed fp32. Terms that are not finite have no say in it.
 template <int NB, int NT, bool kMasked>
 __device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&x)[NT][2], const uint32_t (&vw)[4][NB],
                                               const float (&vs)[NB][2], bool refresh) {
-  float w[NT][NB][2], top[NT][NB];
-  bool over = refresh;
+  float p[NT][2], w[NT][NB][2], top = 0.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) top[nt][nb] = 0.f;
-#pragma unroll
     for (int u = 0; u < 2; ++u) {
       const bool out = kMasked && x[nt][u] == -INFINITY;
-      const float p = out ? 0.f : ex2(x[nt][u] - s.m[nt]);
-      s.l[nt] += p;
+      p[nt][u] = out ? 0.f : ex2(x[nt][u] - s.m[nt]);
+      s.l[nt] += p[nt][u];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         // a token that is not attended may lie in a slot never written: its scale is not used
-        w[nt][nb][u] = out ? 0.f : p * s.sc[nt][nb] * vs[nb][u];
-        top[nt][nb] = fmaxf(top[nt][nb], w[nt][nb][u]);
+        w[nt][nb][u] = out ? 0.f : p[nt][u] * s.sc[nt][nb] * vs[nb][u];
+        top = fmaxf(top, fabsf(w[nt][nb][u]));
       }
     }
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) over |= top[nt][nb] > 8192.f;
   }
-  if (__any_sync(kFull, over)) {
+  if (__any_sync(kFull, refresh || top > 8192.f)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float t = top[nt][nb];
-        t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
-        t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
-        t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
-        if (t > 0.f && (refresh || t > 8192.f)) {
-          // t to [2^6, 2^7), but not so far up that products summed before pass 2^40: next to those, these count
-          // for nothing
-          const int was = (int)(__float_as_uint(s.sc[nt][nb]) >> 23) - 127;
-          int step = min(6 - ((int)(__float_as_uint(t) >> 23) - 127), 40 - ((int)(__float_as_uint(s.big[nt][nb]) >> 23) - 127));
-          step = max(max(-120, -120 - was), min(min(step, 120), 120 - was));
-          const float f = __uint_as_float((uint32_t)(127 + step) << 23);
-          s.sc[nt][nb] *= f;
+        // the largest term lies in [2^e, 2^(e + 2))
+        constexpr int kNone = -1000;
+        int e = kNone;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float v = fabsf(vs[nb][u]);
+          if (p[nt][u] > 0.f && v > 0.f && v < INFINITY) e = max(e, exponent(p[nt][u]) + exponent(v));
+        }
+        e = max(e, __shfl_xor_sync(kFull, e, 4));
+        e = max(e, __shfl_xor_sync(kFull, e, 8));
+        e = max(e, __shfl_xor_sync(kFull, e, 16));
+        const int was = exponent(s.sc[nt][nb]);
+        if (e > kNone && (refresh || e + was > 11)) {
+          // the largest to [2^6, 2^8), but not so far up that products summed before pass 2^40: next to those,
+          // these count for nothing. (Weights are at most 2^8, so that a weight times sc stays below 2^128.)
+          int step = min(min(6 - e - was, 40 - exponent(s.big[nt][nb])), 120);
+          step = max(-126 - was, min(step, 119 - was));
+          const float f = power_of_two(max(step, -127));
+          s.sc[nt][nb] = power_of_two(was + step);
           s.big[nt][nb] = fmaxf(8192.f, s.big[nt][nb] * f);
-          w[nt][nb][0] *= f;
-          w[nt][nb][1] *= f;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) w[nt][nb][u] = kMasked && x[nt][u] == -INFINITY ? 0.f : p[nt][u] * s.sc[nt][nb] * vs[nb][u];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s.o[nt][nb][j][e] *= f;
+            for (int i = 0; i < 4; ++i) s.o[nt][nb][j][i] *= f;
         }
       }
     }
