@@ -109,3 +109,28 @@ def test_logits_that_jump_far_between_pages(H, Hkv, d, gap, small, large):
     for out, lse in _both(c, n):
         assert torch.isfinite(out).all()
         _check(c, out, lse, 0, np.arange(n))
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 4, 64), (32, 8, 128), (28, 4, 128)])
+@pytest.mark.parametrize("size", [1.0, 1e-4, 1e-8, 1e-20, 1e6])
+def test_pages_of_zero_values_among_others(H, Hkv, d, size):
+    # half of the pages have value rows of zeros, the first among them
+    n = 16000
+    c = Cache(H, Hkv, d, [n], seed=6)
+    rng = np.random.default_rng(4)
+    keep = np.repeat(rng.integers(0, 2, n // 16), 16)
+    keep[:16] = 0
+    v = c.v.float() * size * torch.from_numpy(keep).to(DEV).view(n, 1, 1)
+    _write(c, v=v.to(torch.bfloat16))
+    for out, lse in _both(c, n):
+        _check(c, out, lse, 0, np.arange(n))
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 4, 64), (28, 4, 128)])
+def test_a_first_page_of_zero_values_in_a_short_sequence(H, Hkv, d):
+    c = Cache(H, Hkv, d, [64], seed=7)
+    v = c.v.float() * 1e-6
+    v[:16] = 0
+    _write(c, v=v.to(torch.bfloat16))
+    for out, lse in _both(c, 64):
+        _check(c, out, lse, 0, np.arange(64))

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
 #pragma unroll
             for (int u = 0; u < 2; ++u) x[pg][nt][u] = token(u, g) < limit[pg] ? x[pg][nt][u] : -INFINITY;
       }
-      const bool raised = q4_raise_max<NB, NT, R::PAGES>(st, x);
+      q4_raise_max<NB, NT, R::PAGES>(st, x);
       if constexpr (kAttend) {
 #pragma unroll
         for (int pg = 0; pg < R::PAGES; ++pg) {
@@ -383,9 +383,9 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
             copy_next();
           }
           if (whole)
-            q4_accumulate<NB, NT, false>(st, x[pg], vw, vs, raised && pg == 0);
+            q4_accumulate<NB, NT, false>(st, x[pg], vw, vs);
           else
-            q4_accumulate<NB, NT, true>(st, x[pg], vw, vs, raised && pg == 0);
+            q4_accumulate<NB, NT, true>(st, x[pg], vw, vs);
         }
       } else {
         __syncwarp();
@@ -718,8 +718,8 @@ __global__ void __launch_bounds__(kGatherWarps * 32, kGatherCtas) gather_kernel(
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) x[0][nt][i] = in[i] ? x[0][nt][i] * mul[nt] : -INFINITY;
-    const bool raised = q4_raise_max<NB, NT, 1>(st, x);
-    q4_accumulate<NB, NT, true>(st, x[0], vw, vs, raised);
+    q4_raise_max<NB, NT, 1>(st, x);
+    q4_accumulate<NB, NT, true>(st, x[0], vw, vs);
     if (++steps % (2 * kQ4Flush) == 0) {
       st.flush(&merge[warp][0][0], s_units[warp], !flushed, lane);
       flushed = true;

@@ -159,19 +159,27 @@ __device__ __forceinline__ void q4_scores(const Q4Query<NB, NT>& f, const uint2 
   }
 }
 
-// Running softmax state of 4 NT heads in one warp, for head 4 nt + t: m its maximum (the same in the
-// eight lanes of a head), l this lane's own part of its sum, o its outputs times sc, a power of two of its own
-// for each 64 elements (high parts in elements 0 and 2, low parts in 1 and 3): tile j, rows g and g + 8, are
-// elements 64 nb + 8 g + j and + 4. A weight times its value's scale enters its product as two fp16 terms, held
-// with sc between the largest so far at 2^6 and 2^13: within 2^-22 of it, or 2^-31 of the largest of the same 64
-// elements. Groups do not share sc, so that one whose values are large, or not finite, takes nothing from the
-// others. `big` bounds the products summed so far, in units of sc, so that a later sc never takes the sums out of
-// range.
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }   // -127: 0
+
+// Running softmax state of 4 NT heads in one warp, for head 4 nt + t: m what its logits are taken against (their
+// maximum rounded down, raised now and then; the same in the eight lanes of a head), l this lane's own part of its
+// sum, o its outputs times sc, a power of two of its own for each 64 elements (high parts in elements 0 and 2, low
+// parts in 1 and 3): tile j, rows g and g + 8, are elements 64 nb + 8 g + j and + 4.
+//
+// A weight times its value's scale enters its product as two fp16 terms. sc keeps the largest such term so far
+// between 2^6 and 2^13, so that a term is held within 2^-22 of itself, or within 2^-31 of the largest of the same
+// 64 elements. It begins as far up as weights below 2^9 allow and comes down to the first terms that there are
+// (however late: rows of zeros say nothing about the size of the others) and to any that pass 2^13. Where m rises by a
+// whole number, sc rises with it: the sums stay as they are, and the terms behind, which weigh that much more, find
+// the unit right for them or bring it down again. Groups do not share sc, so that one whose values are large, or
+// not finite, takes nothing from the others.
 //
 // The tensor cores cut their sums off rather than round them: over a few hundred steps in one accumulator
 // that is 3e-6 of an output. So the sums go over to rows in shared memory every kQ4Flush stages, added
 // there with rounding, and begin again at zero.
 constexpr int kQ4Flush = 16;
+constexpr int kQ4MaxUnit = 119;   // largest exponent of sc: weights of 2^8 times sc are finite
 // What a head's sums in shared memory count in: the maximum and the powers of two that they belong to.
 template <int NB>
 struct Q4Unit {
@@ -180,7 +188,7 @@ struct Q4Unit {
 
 template <int NB, int NT>
 struct Q4State {
-  float m[NT], l[NT], sc[NT][NB], big[NT][NB];
+  float m[NT], l[NT], sc[NT][NB];
   float o[NT][NB][4][4];
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -189,8 +197,7 @@ struct Q4State {
       l[nt] = 0.f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        sc[nt][nb] = 1.f;
-        big[nt][nb] = 0.f;
+        sc[nt][nb] = power_of_two(kQ4MaxUnit);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -215,10 +222,11 @@ struct Q4State {
       Q4Unit<NB>& unit = units[4 * nt + t];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
+        // (sc rises no further than m, so that f is at most 1)
         float f = 0.f;
         if (!first) {
-          const int step = (int)(__float_as_uint(sc[nt][nb]) >> 23) - (int)(__float_as_uint(unit.sc[nb]) >> 23);
-          f = (unit.m == m[nt] ? 1.f : ex2(unit.m - m[nt])) * __uint_as_float((uint32_t)(127 + max(-126, min(step, 126))) << 23);
+          const int rise = unit.m == m[nt] ? 0 : (int)fminf(m[nt] - unit.m, 1000.f);
+          f = power_of_two(max(-127, exponent(sc[nt][nb]) - exponent(unit.sc[nb]) - rise));
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -246,10 +254,10 @@ struct Q4State {
 };
 
 // Moves the maxima up for 16 P tokens with base-2 logits x[page][nt][u] (-inf: not attended), where a logit
-// passes its head's maximum by more than 2^8: most calls cost one vote and no rescaling, and weights
-// stay below 2^8. True (in the whole warp) where a maximum moved.
+// passes its head's by more than 8: most calls cost one vote and no rescaling, and weights are 2^8 at most.
+// Whole numbers, so that what they change by is a power of two.
 template <int NB, int NT, int P>
-__device__ __forceinline__ bool q4_raise_max(Q4State<NB, NT>& s, const float (&x)[P][NT][2]) {
+__device__ __forceinline__ void q4_raise_max(Q4State<NB, NT>& s, const float (&x)[P][NT][2]) {
   float top[NT];
   bool grow = false;
 #pragma unroll
@@ -259,20 +267,21 @@ __device__ __forceinline__ bool q4_raise_max(Q4State<NB, NT>& s, const float (&x
     for (int pg = 1; pg < P; ++pg) top[nt] = fmaxf(top[nt], fmaxf(x[pg][nt][0], x[pg][nt][1]));
     grow |= top[nt] > s.m[nt] + 8.f;
   }
-  const bool raised = __any_sync(kFull, grow);
-  if (raised) {
+  if (__any_sync(kFull, grow)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mn = fmaxf(s.m[nt], top[nt]);
+      float mn = fmaxf(s.m[nt], floorf(top[nt]));
       mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 4));
       mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 8));
       mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 16));
-      const float f = s.m[nt] == mn ? 1.f : ex2(s.m[nt] - mn);
+      const int rise = s.m[nt] == mn ? 0 : (int)fminf(mn - s.m[nt], 1000.f);
+      s.l[nt] *= power_of_two(max(-127, -rise));
       s.m[nt] = mn;
-      s.l[nt] *= f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        s.big[nt][nb] *= f;
+        const int was = exponent(s.sc[nt][nb]), up = min(rise, kQ4MaxUnit - was);
+        s.sc[nt][nb] = power_of_two(was + up);
+        const float f = power_of_two(max(-127, up - rise));            // (1 but at the end of sc's range)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -280,22 +289,17 @@ __device__ __forceinline__ bool q4_raise_max(Q4State<NB, NT>& s, const float (&x
       }
     }
   }
-  return raised;
 }
-
-__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }   // -127: 0
 
 // Adds 16 tokens whose logits x[nt][u] (head 4 nt + t, token (u, g)) the maxima already cover: vs[nb][u]
 // are that token's value scales, vw[i][nb] word g of the codes of token (i / 2, 2t + i % 2). kMasked: some
-// tokens may not be attended (x = -inf). refresh: sc is chosen anew from these tokens (after a maximum moved;
-// otherwise only where a term may pass 2^13).
+// tokens may not be attended (x = -inf).
 //
-// A new sc comes from the exponents of weights and scales, and the terms are formed again from both: a term in
-// the old unit may have passed fp32. Terms that are not finite have no say in it.
+// Where a term passes 2^13, the new sc comes from the exponents of weights and scales, and the terms are formed
+// again from both: one in the old unit may have passed fp32. Terms that are not finite have no say in it.
 template <int NB, int NT, bool kMasked>
 __device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&x)[NT][2], const uint32_t (&vw)[4][NB],
-                                              const float (&vs)[NB][2], bool refresh) {
+                                              const float (&vs)[NB][2]) {
   float p[NT][2], w[NT][NB][2], top = 0.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -312,14 +316,13 @@ __device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&
       }
     }
   }
-  if (__any_sync(kFull, refresh || top > 8192.f)) {
+  if (__any_sync(kFull, top > 8192.f)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         // the largest term lies in [2^e, 2^(e + 2))
-        constexpr int kNone = -1000;
-        int e = kNone;
+        int e = -1000;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const float v = fabsf(vs[nb][u]);
@@ -329,14 +332,10 @@ __device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&
         e = max(e, __shfl_xor_sync(kFull, e, 8));
         e = max(e, __shfl_xor_sync(kFull, e, 16));
         const int was = exponent(s.sc[nt][nb]);
-        if (e > kNone && (refresh || e + was > 11)) {
-          // the largest to [2^6, 2^8), but not so far up that products summed before pass 2^40: next to those,
-          // these count for nothing. (Weights are at most 2^8, so that a weight times sc stays below 2^128.)
-          int step = min(min(6 - e - was, 40 - exponent(s.big[nt][nb])), 120);
-          step = max(-126 - was, min(step, 119 - was));
-          const float f = power_of_two(max(step, -127));
-          s.sc[nt][nb] = power_of_two(was + step);
-          s.big[nt][nb] = fmaxf(8192.f, s.big[nt][nb] * f);
+        if (e + was > 11) {
+          const int to = max(-126, 6 - e);                           // the largest term to [2^6, 2^8)
+          const float f = power_of_two(max(-127, to - was));
+          s.sc[nt][nb] = power_of_two(to);
 #pragma unroll
           for (int u = 0; u < 2; ++u) w[nt][nb][u] = kMasked && x[nt][u] == -INFINITY ? 0.f : p[nt][u] * s.sc[nt][nb] * vs[nb][u];
 #pragma unroll
