@@ -134,3 +134,28 @@ def test_a_first_page_of_zero_values_in_a_short_sequence(H, Hkv, d):
     _write(c, v=v.to(torch.bfloat16))
     for out, lse in _both(c, 64):
         _check(c, out, lse, 0, np.arange(64))
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 4, 64), (32, 8, 128), (28, 4, 128)])
+@pytest.mark.parametrize("n,cut", [(64, 48), (2000, 1000), (9000, 8990)])
+def test_logits_that_leave_fp32_weigh_nothing_beside_finite_ones(H, Hkv, d, n, cut):
+    # the first `cut` keys give logits near -1e39, which fp32 holds as -inf; the others give 0 throughout, so the
+    # weights are 0 and 1 / (n - cut)
+    c = Cache(H, Hkv, d, [n], seed=8)
+    c.q[:] = 0
+    c.q[:, :, 0] = 1e20
+    k = torch.zeros_like(c.k)
+    k[:cut, :, 0] = -1e20
+    _write(c, k=k)
+    rest = n - cut
+    for out, lse in _both(c, n):
+        for h in range(H):
+            v = c.rows(c.vval, 0, h // (H // Hkv), np.arange(cut, n))
+            tol = np.abs(v).mean(0) * (2.0 ** -21 + 2.0 ** -20 + n * 2.0 ** -23) + np.abs(v).max() * n * 2.0 ** -31
+            assert np.all(np.abs(out[0, h].double().cpu().numpy() - v.mean(0)) <= tol)
+        assert torch.all(torch.abs(lse.double() - math.log(rest)) <= n * 2.0 ** -23 + 2.0 ** -20 + math.log(rest) * 2.0 ** -22)
+    vote = torch.full((1, c.ctx.max_tokens), 7.0, device=DEV)
+    c.ctx.score(c.q, c.kp, c.pt, c.seq, vote)
+    assert c.ctx.status() == 0
+    assert not vote[0, :cut].any()
+    assert torch.all(torch.abs(vote[0, cut:n].double() * rest / H - 1) <= n * 2.0 ** -23 + 2.0 ** -19)

@@ -395,12 +395,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
           const bool there = done * R::PAGES + pg < mine;          // (a page without a block has logits of -inf)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float e0 = ex2(x[pg][nt][0] - st.m[nt]), e1 = ex2(x[pg][nt][1] - st.m[nt]);
-            if (!whole) {                                          // no token there: no weight (not 2^(-inf + inf))
-              e0 = x[pg][nt][0] == -INFINITY ? 0.f : e0;
-              e1 = x[pg][nt][1] == -INFINITY ? 0.f : e1;
-            }
-            st.l[nt] += e0 + e1;
+            st.l[nt] += q4_weight(x[pg][nt][0], st.m[nt]) + q4_weight(x[pg][nt][1], st.m[nt]);
             if (there && 4 * nt + t < nh) {
               row[nt * tile_step + pg * row_step] = x[pg][nt][0];
               row[nt * tile_step + pg * row_step + 8] = x[pg][nt][1];

@@ -18,6 +18,7 @@
 // products with either part exact in fp32.
 #pragma once
 
+#include <cfloat>
 #include <cuda_fp16.h>
 
 #include "ts_common.cuh"
@@ -291,6 +292,9 @@ __device__ __forceinline__ void q4_raise_max(Q4State<NB, NT>& s, const float (&x
   }
 }
 
+// Weight of a base-2 logit x against m (neither -inf against -inf nor a masked place has any: 0, not NaN).
+__device__ __forceinline__ float q4_weight(float x, float m) { return ex2(x - fmaxf(m, -FLT_MAX)); }
+
 // Adds 16 tokens whose logits x[nt][u] (head 4 nt + t, token (u, g)) the maxima already cover: vs[nb][u]
 // are that token's value scales, vw[i][nb] word g of the codes of token (i / 2, 2t + i % 2). kMasked: some
 // tokens may not be attended (x = -inf).
@@ -306,7 +310,7 @@ __device__ __forceinline__ void q4_accumulate(Q4State<NB, NT>& s, const float (&
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const bool out = kMasked && x[nt][u] == -INFINITY;
-      p[nt][u] = out ? 0.f : ex2(x[nt][u] - s.m[nt]);
+      p[nt][u] = q4_weight(x[nt][u], s.m[nt]);
       s.l[nt] += p[nt][u];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
