@@ -159,3 +159,24 @@ def test_logits_that_leave_fp32_weigh_nothing_beside_finite_ones(H, Hkv, d, n, c
     assert c.ctx.status() == 0
     assert not vote[0, :cut].any()
     assert torch.all(torch.abs(vote[0, cut:n].double() * rest / H - 1) <= n * 2.0 ** -23 + 2.0 ** -19)
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 4, 64), (28, 4, 128)])
+def test_a_sequence_without_a_page_in_the_pool_has_votes_of_zero(H, Hkv, d):
+    T = tsl()
+    c = Cache(H, Hkv, d, [100, 300], seed=9)
+    ref, vote = (torch.full((2, c.ctx.max_tokens), 7.0, device=DEV) for _ in range(2))
+    c.ctx.score(c.q, c.kp, c.pt, c.seq, ref)
+    assert c.ctx.status() == 0
+    bad = c.pt.clone()
+    bad[0] = c.pages
+    c.ctx.score(c.q, c.kp, bad, c.seq, vote)
+    assert c.ctx.status() == T.STATUS_CODE["TS_ERR_PAGE_OOB"]
+    assert not vote[0, :100].any() and torch.equal(vote[1], ref[1]) and (vote[0, 100:] == 7).all()
+    # a decode step over it: the lowest candidates (all votes are equal), and no token to attend to
+    idx, cnt = torch.zeros(2, 30, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    out, lse = torch.ones(2, H, d, device=DEV), torch.ones(2, H, device=DEV)
+    c.ctx.decode_step(c.q, c.kp, c.vp, bad, c.seq, T.params(k=10, n_sink=4, n_local=16), idx, cnt, out, lse)
+    assert c.ctx.status() == T.STATUS_CODE["TS_ERR_PAGE_OOB"]
+    assert idx[0].tolist() == list(range(14)) + list(range(84, 100)) and cnt.tolist() == [30, 30]
+    assert not out[0].any() and torch.isinf(lse[0]).all() and torch.isfinite(out[1]).all()

@@ -586,7 +586,8 @@ __global__ void __launch_bounds__(kVoteThreads, 2) q4_vote_kernel(const __grid_c
       for (int k = 0; k < FIRST; ++k) z.add(y[k].y * part_weight(y[k].x, M));
       for (int i = lane + 32 * FIRST; i < count; i += 32) z.add(ml[i].y * part_weight(ml[i].x, M));
       const float Z = warp_sum_comp(z.s, -z.c);
-      if (lane == 0) s_mz[h] = make_float2(M, 1.f / Z);
+      // a sequence none of whose pages is in the pool has logits of -inf alone and a sum of zero: votes of zero
+      if (lane == 0) s_mz[h] = Z == 0.f ? make_float2(0.f, 0.f) : make_float2(M, 1.f / Z);
     }
     __syncthreads();
     for (int pg = p0 + warp; pg < p1; pg += WARPS) {
