@@ -173,18 +173,25 @@ def _row_stride(t, total, row):
     return rows if total > 1 else heads * d
 
 
-_stream_of, _device = None, None
+_stream_of = _device = _bfloat16 = _float32 = _int32 = None
+
+
+def _torch():
+    """What the calls below need of torch, looked up at the first call that needs it (raw calls with raw streams
+    need none of it)."""
+    global _stream_of, _device, _bfloat16, _float32, _int32
+    import torch
+    _bfloat16, _float32, _int32 = torch.bfloat16, torch.float32, torch.int32
+    _device = torch.cuda.current_device
+    _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _stream_of is None:
+        _stream_of = lambda device: torch.cuda.current_stream(device).cuda_stream
 
 
 def _current_stream():
     """The raw handle of torch's current stream (without the Stream object, whose making takes microseconds)."""
-    global _stream_of, _device
-    if _stream_of is None:
-        import torch
-        _device = torch.cuda.current_device
-        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if _stream_of is None:
-            _stream_of = lambda device: torch.cuda.current_stream(device).cuda_stream
+    if _device is None:
+        _torch()
     return _stream_of(_device())
 
 
@@ -377,10 +384,11 @@ class Context:
         self.handle = ts_create(self.cfg)
         self.max_tokens = max_pages_per_seq * page_size
         # what the packed calls compare their tensors with
-        import torch
         self._q_row, self._kv_row = (n_q_heads, head_dim), (n_kv_heads, head_dim)
-        self._bfloat16, self._float32, self._int32 = torch.bfloat16, torch.float32, torch.int32
-        self._rows_dtype = torch.float32 if kv_dtype == TS_KV_F32 else torch.bfloat16
+
+    def _rows_dtype(self):
+        """Element type of the rows that go into the pools."""
+        return _float32 if self.cfg.kv_dtype == TS_KV_F32 else _bfloat16
 
     def close(self):
         if self.handle:
@@ -430,7 +438,9 @@ class Context:
 
     def append_prompt(self, k, v, cu_rows, page_table, k_pool, v_pool, starts=None, stream=None):
         """k / v [total][H_kv][d], packed: row r of sequence b to position starts[b] + r - cu_rows[b]."""
-        ks, B, i32, kind = k.shape, cu_rows.shape[0] - 1, self._int32, self._rows_dtype
+        if _device is None:
+            _torch()
+        ks, B, i32, kind = k.shape, cu_rows.shape[0] - 1, _int32, self._rows_dtype()
         if not (ks[1:] == self._kv_row and v.shape == ks and k.dtype is kind and v.dtype is kind and cu_rows.dtype is i32
                 and k.is_cuda and v.is_cuda and cu_rows.is_cuda):
             _packed("append_prompt", ((ks[1:], self._kv_row), (v.shape, ks)), ((k.dtype, kind), (v.dtype, kind), (cu_rows.dtype, i32)),
@@ -444,7 +454,9 @@ class Context:
 
     def read_kv(self, cu_rows, page_table, k_pool, v_pool, k_out, v_out, starts=None, stream=None):
         """k_out / v_out fp32 [total][H_kv][d]: the values of the rows that append_prompt would write."""
-        ks, B, i32, f32 = k_out.shape, cu_rows.shape[0] - 1, self._int32, self._float32
+        if _device is None:
+            _torch()
+        ks, B, i32, f32 = k_out.shape, cu_rows.shape[0] - 1, _int32, _float32
         if not (ks[1:] == self._kv_row and v_out.shape == ks and k_out.dtype is f32 and v_out.dtype is f32
                 and cu_rows.dtype is i32 and k_out.is_cuda and v_out.is_cuda and cu_rows.is_cuda):
             _packed("read_kv", ((ks[1:], self._kv_row), (v_out.shape, ks)),
@@ -460,14 +472,16 @@ class Context:
 
     def prompt_attend(self, q, k, v, cu_rows, out, lse=None, scale=0.0, stream=None):
         """q / out [total][H][d], k / v [total][H_kv][d] (bf16, packed): causal attention of every sequence."""
-        qs, ks, bf, i32 = q.shape, k.shape, self._bfloat16, self._int32
+        if _device is None:
+            _torch()
+        qs, ks, bf, i32 = q.shape, k.shape, _bfloat16, _int32
         if not (qs[1:] == self._q_row and ks[1:] == self._kv_row and ks[0] == qs[0] and v.shape == ks and out.shape == qs
                 and q.dtype is bf and k.dtype is bf and v.dtype is bf and out.dtype is bf and cu_rows.dtype is i32
                 and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and cu_rows.is_cuda):
             _packed("prompt_attend", ((qs[1:], self._q_row), (ks[1:], self._kv_row), (ks[:1], qs[:1]), (v.shape, ks), (out.shape, qs)),
                     ((q.dtype, bf), (k.dtype, bf), (v.dtype, bf), (out.dtype, bf), (cu_rows.dtype, i32)), (q, k, v, out, cu_rows))
-        if lse is not None and not (lse.shape == qs[:2] and lse.dtype is self._float32 and lse.is_cuda):
-            _packed("prompt_attend", ((lse.shape, qs[:2]),), ((lse.dtype, self._float32),), (lse,))
+        if lse is not None and not (lse.shape == qs[:2] and lse.dtype is _float32 and lse.is_cuda):
+            _packed("prompt_attend", ((lse.shape, qs[:2]),), ((lse.dtype, _float32),), (lse,))
         _dense("prompt_attend", cu_rows, lse)
         total, row = qs[0], self._kv_row
         ts_prompt_attend(self.handle, q, _row_stride(q, total, self._q_row), k, _row_stride(k, total, row), v,
