@@ -180,3 +180,28 @@ def test_a_sequence_without_a_page_in_the_pool_has_votes_of_zero(H, Hkv, d):
     assert c.ctx.status() == T.STATUS_CODE["TS_ERR_PAGE_OOB"]
     assert idx[0].tolist() == list(range(14)) + list(range(84, 100)) and cnt.tolist() == [30, 30]
     assert not out[0].any() and torch.isinf(lse[0]).all() and torch.isfinite(out[1]).all()
+
+
+def test_queries_and_rows_of_another_type_are_refused():
+    T = tsl()
+    c = Cache(8, 2, 128, [100, 30], seed=10)
+    out, lse = torch.full((2, 8, 128), 7.0, device=DEV), torch.full((2, 8), 7.0, device=DEV)
+    idx, cnt = torch.zeros(2, 30, dtype=torch.int32, device=DEV), torch.full((2,), 3, dtype=torch.int32, device=DEV)
+    kn = torch.ones(2, 2, 128, dtype=torch.bfloat16, device=DEV)
+    kp = c.kp.clone()
+    q = c.q.to(torch.bfloat16)
+    for call in (lambda: c.ctx.attend(q, c.kp, c.vp, c.pt, c.seq, out, lse),
+                 lambda: c.ctx.attend(c.q, c.kp, c.vp, c.pt, c.seq.long(), out, lse),
+                 lambda: c.ctx.attend(c.q, c.kp, c.vp, c.pt[:, :-1].contiguous(), c.seq, out, lse),
+                 lambda: c.ctx.attend(c.q, c.kp[:-1], c.vp, c.pt, c.seq, out, lse),
+                 lambda: c.ctx.attend(c.q, c.kp, c.vp, c.pt, c.seq, out.to(torch.bfloat16), lse),
+                 lambda: c.ctx.sparse_attend(q, c.kp, c.vp, c.pt, idx, cnt, out, lse),
+                 lambda: c.ctx.decode_step(q, c.kp, c.vp, c.pt, c.seq, T.params(), idx, cnt, out, lse),
+                 lambda: c.ctx.score(q, c.kp, c.pt, c.seq, torch.zeros(2, c.ctx.max_tokens, device=DEV)),
+                 lambda: c.ctx.append_kv(kn.float(), kn, c.pt, c.seq, c.kp, c.vp),
+                 lambda: c.ctx.append_kv(kn[:1], kn, c.pt, c.seq, c.kp, c.vp),
+                 lambda: c.ctx.append_prompt(c.k, c.v, c.cu, c.pt[:1], c.kp, c.vp),
+                 lambda: c.ctx.read_kv(c.cu, c.pt, c.kp[:-1], c.vp, *(torch.zeros(130, 2, 128, device=DEV) for _ in range(2)))):
+        with pytest.raises(T.TokenSelectError):
+            call()
+    assert (out == 7).all() and (lse == 7).all() and torch.equal(c.kp, kp) and c.ctx.status() == 0

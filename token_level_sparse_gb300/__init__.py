@@ -158,6 +158,38 @@ def _packed(where, shapes, dtypes, on_device):
             raise TokenSelectError(STATUS_CODE["TS_ERR_INVALID_ARG"], f"{where}: a tensor is not on the device")
 
 
+def _refuse(where, status, why):
+    raise TokenSelectError(STATUS_CODE[status], f"{where}: {why}")
+
+
+def _tensors(where, *specs):
+    """Refuses a call unless every (tensor, shape, type) is a dense tensor of these on the device. None and raw
+    addresses are not looked at, here and below: the library sees to the first, nobody can to the second."""
+    for t, shape, dtype in specs:
+        if t is None or isinstance(t, int):
+            continue
+        if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.is_cuda:
+            continue
+        if t.shape != shape:
+            _refuse(where, "TS_ERR_SHAPE", f"{tuple(t.shape)} instead of {tuple(shape)}")
+        if t.dtype is not dtype:
+            _refuse(where, "TS_ERR_INVALID_ARG", f"{t.dtype} instead of {dtype}")
+        _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the device")
+
+
+def _rows_of(where, B, *specs):
+    """The same for (tensor, columns, type), with a row for each sequence at least, dense inside a row."""
+    for t, columns, dtype in specs:
+        if t is None or isinstance(t, int):
+            continue
+        if t.dim() != 2 or t.shape[0] < B or t.shape[1] < columns:
+            _refuse(where, "TS_ERR_SHAPE", f"{tuple(t.shape)} instead of {(B, columns)} or more")
+        if t.dtype is not dtype:
+            _refuse(where, "TS_ERR_INVALID_ARG", f"{t.dtype} instead of {dtype}")
+        if t.stride(1) != 1 or not t.is_cuda:
+            _refuse(where, "TS_ERR_INVALID_ARG", "a tensor's rows are not dense, or not on the device")
+
+
 def _dense(where, *tensors):
     for t in tensors:
         if t is not None and not t.is_contiguous():
@@ -385,10 +417,48 @@ class Context:
         self.max_tokens = max_pages_per_seq * page_size
         # what the packed calls compare their tensors with
         self._q_row, self._kv_row = (n_q_heads, head_dim), (n_kv_heads, head_dim)
+        self._q4 = kv_dtype == TS_KV_Q4
+        self._pool_bytes, self._columns = num_pages * ts_page_bytes(self.cfg), max_pages_per_seq
 
     def _rows_dtype(self):
         """Element type of the rows that go into the pools."""
         return _float32 if self.cfg.kv_dtype == TS_KV_F32 else _bfloat16
+
+    def _paged(self, where, B, page_table, k_pool, v_pool):
+        """Refuses a page table or pools smaller than the context's."""
+        try:
+            shape, need = page_table.shape, self._pool_bytes
+            if (shape[0] >= B and shape[1] == self._columns and page_table.dtype is _int32 and page_table.is_cuda
+                    and page_table.is_contiguous() and k_pool.nbytes >= need and k_pool.is_cuda and k_pool.is_contiguous()
+                    and v_pool.nbytes >= need and v_pool.is_cuda and v_pool.is_contiguous() and len(shape) == 2):
+                return                                             # (one test of all, as most calls pass)
+        except (AttributeError, IndexError):                       # None, raw addresses, other shapes
+            pass
+        if page_table is not None and not isinstance(page_table, int):
+            _tensors(where, (page_table, (max(B, *page_table.shape[:1]), self._columns), _int32))
+        for t in (k_pool, v_pool):
+            if t is None or isinstance(t, int):
+                continue
+            if t.nbytes < self._pool_bytes:
+                _refuse(where, "TS_ERR_SHAPE", f"a pool of less than {self._pool_bytes} bytes")
+            if not (t.is_cuda and t.is_contiguous()):
+                _refuse(where, "TS_ERR_INVALID_ARG", "a pool is not dense or not on the device")
+
+    def _queries(self, where, q, page_table, k_pool, v_pool, seq_lens=None, out=None, lse=None, vote=None, idx=None,
+                 count=None, flags=None):
+        """Refuses what a call over a 4-bit cache would read or write beyond, or take for another type."""
+        if _device is None:
+            _torch()
+        B, shape = q.shape[0], (q.shape[0], *self._q_row)
+        _tensors(where, (q, shape, _float32), (out, shape, _float32), (lse, shape[:2], _float32), (seq_lens, shape[:1], _int32),
+                 (count, shape[:1], _int32))
+        self._paged(where, B, page_table, k_pool, k_pool if v_pool is None else v_pool)
+        _rows_of(where, B, (vote, self.max_tokens, _float32), (idx, 1, _int32))
+        if flags is not None and not isinstance(flags, int):
+            if flags.numel() < B or flags.element_size() != 1:
+                _refuse(where, "TS_ERR_SHAPE", f"{tuple(flags.shape)} of {flags.dtype} instead of {(B,)} bytes")
+            if not (flags.is_cuda and flags.is_contiguous()):
+                _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the device")
 
     def close(self):
         if self.handle:
@@ -405,10 +475,14 @@ class Context:
         return Cache(self, n_layers, capacity)
 
     def score(self, q, k_pool, page_table, seq_lens, vote, skip=None, scale=0.0, stream=None):
+        if self._q4:
+            self._queries("score", q, page_table, k_pool, None, seq_lens, vote=vote, flags=skip)
         ts_score(self.handle, q, k_pool, page_table, seq_lens, q.shape[0], skip, scale, vote,
                  vote.stride(0), stream)
 
     def score_fn(self, params, q, k_pool, page_table, seq_lens, vote, skip=None, stream=None):
+        if self._q4:
+            self._queries("score_fn", q, page_table, k_pool, None, seq_lens, vote=vote, flags=skip)
         ts_score_fn(self.handle, params, q, k_pool, page_table, seq_lens, q.shape[0], skip, vote, vote.stride(0),
                     stream)
 
@@ -417,11 +491,15 @@ class Context:
                   seq_lens.shape[0], hit, params, idx, idx.stride(0), count, stream)
 
     def sparse_attend(self, q, k_pool, v_pool, page_table, idx, count, out, lse=None, scale=0.0, stream=None):
+        if self._q4:
+            self._queries("sparse_attend", q, page_table, k_pool, v_pool, out=out, lse=lse, idx=idx, count=count)
         ts_sparse_attend(self.handle, q, k_pool, v_pool, page_table, idx, idx.stride(0), count, q.shape[0],
                          scale, out, lse, stream)
 
     def decode_step(self, q, k_pool, v_pool, page_table, seq_lens, params, idx, count, out, lse=None,
                     hit=None, vote=None, cache=None, layer=0, stream=None):
+        if self._q4:
+            self._queries("decode_step", q, page_table, k_pool, v_pool, seq_lens, out, lse, vote, idx, count, hit)
         ts_decode_step(self.handle, cache.handle if cache else None, layer, q, k_pool, v_pool, page_table,
                        seq_lens, q.shape[0], params, vote, vote.stride(0) if vote is not None else 0, idx,
                        idx.stride(0), count, out, lse, hit, stream)
@@ -434,6 +512,26 @@ class Context:
 
     def append_kv(self, k_new, v_new, page_table, seq_lens, k_pool, v_pool, stream=None):
         """k_new / v_new [B][H_kv][d]: the current token's rows into position seq_lens[b] - 1."""
+        if _device is None:
+            _torch()
+        B, kind, row = seq_lens.shape[0], self._rows_dtype(), self._kv_row
+        try:
+            ks = k_new.shape
+            good = (ks[1:] == row and ks[0] == B and v_new.shape == ks and k_new.dtype is kind and v_new.dtype is kind
+                    and k_new.is_cuda and v_new.is_cuda and k_new.is_contiguous() and v_new.is_contiguous())
+        except (AttributeError, IndexError):
+            good = False
+        for t in () if good else (k_new, v_new):
+            if t is None or isinstance(t, int):
+                continue
+            # (any view of the rows' bits goes into a pool that holds them as they are)
+            if t.numel() != B * row[0] * row[1] or t.element_size() != kind.itemsize:
+                _refuse("append_kv", "TS_ERR_SHAPE", f"{tuple(t.shape)} of {t.dtype} instead of {(B, *row)} of {kind}")
+            if (self._q4 and t.dtype is not kind) or not (t.is_cuda and t.is_contiguous()):
+                _refuse("append_kv", "TS_ERR_INVALID_ARG", f"dense rows of {kind} on the device are wanted")
+        if self._q4:
+            _tensors("append_kv", (seq_lens, (B,), _int32))
+            self._paged("append_kv", B, page_table, k_pool, v_pool)
         ts_append_kv(self.handle, k_new, v_new, page_table, seq_lens, seq_lens.shape[0], k_pool, v_pool, stream)
 
     def append_prompt(self, k, v, cu_rows, page_table, k_pool, v_pool, starts=None, stream=None):
@@ -448,6 +546,7 @@ class Context:
         if starts is not None and not (starts.shape == (B,) and starts.dtype is i32 and starts.is_cuda):
             _packed("append_prompt", ((starts.shape, (B,)),), ((starts.dtype, i32),), (starts,))
         _dense("append_prompt", cu_rows, starts)
+        self._paged("append_prompt", B, page_table, k_pool, v_pool)
         total, row = ks[0], self._kv_row
         ts_append_prompt(self.handle, k, _row_stride(k, total, row), v, _row_stride(v, total, row), cu_rows, starts, B, total,
                          page_table, k_pool, v_pool, stream)
@@ -464,10 +563,13 @@ class Context:
         if starts is not None and not (starts.shape == (B,) and starts.dtype is i32 and starts.is_cuda):
             _packed("read_kv", ((starts.shape, (B,)),), ((starts.dtype, i32),), (starts,))
         _dense("read_kv", k_out, v_out, cu_rows, starts)
+        self._paged("read_kv", B, page_table, k_pool, v_pool)
         ts_read_kv(self.handle, cu_rows, starts, B, ks[0], page_table, k_pool, v_pool, k_out, v_out, stream)
 
     def attend(self, q, k_pool, v_pool, page_table, seq_lens, out, lse=None, scale=0.0, stream=None):
         """q [B][H][d] attends to every cached token of its sequence (4-bit pools)."""
+        if self._q4:
+            self._queries("attend", q, page_table, k_pool, v_pool, seq_lens, out, lse)
         ts_attend(self.handle, q, k_pool, v_pool, page_table, seq_lens, q.shape[0], scale, out, lse, stream)
 
     def prompt_attend(self, q, k, v, cu_rows, out, lse=None, scale=0.0, stream=None):
