@@ -39,9 +39,11 @@
  *    Errors found on the device (a page id outside the pool, an output that
  *    does not fit, a wait that ran out) are recorded in the context's status
  *    word and read back with ts_get_status. Nothing aborts or traps.
- *  - A context is bound to the device current at ts_create and is not thread
- *    safe: calls on one context must be serialised by the caller, and calls
- *    that share a context's scratch must go to one stream (or be ordered).
+ *  - A context is bound to the device current at ts_create (the packed calls,
+ *    ts_attend and every call over a 4-bit pool return TS_ERR_INVALID_ARG where
+ *    another one is current) and is not thread safe: calls on one context must
+ *    be serialised by the caller, and calls that share a context's scratch must
+ *    go to one stream (or be ordered).
  */
 #ifndef TOKENSELECT_H
 #define TOKENSELECT_H

@@ -12,8 +12,17 @@ class Reached(Exception):
 
 
 class OnDevice(torch.Tensor):
-    """A tensor that says that it is on the device."""
-    is_cuda = property(lambda self: True)
+    """A tensor that says that it is on device 0, the current one here."""
+
+    def get_device(self):
+        return 0
+
+
+class Elsewhere(OnDevice):
+    """One that says that it is on another."""
+
+    def get_device(self):
+        return 1
 
 
 def _on(t):
@@ -36,6 +45,8 @@ def context(monkeypatch):
     monkeypatch.setattr(T, "_check", reached)
     monkeypatch.setattr(T, "_current_stream", lambda: 0)
     monkeypatch.setattr(T, "library", reached)
+    T._torch()
+    monkeypatch.setattr(T, "_device", lambda: 0)
     monkeypatch.setattr(T, "ts_page_bytes", lambda cfg: 2 * 16 * (68 if cfg.kv_dtype == T.TS_KV_Q4 else 512))
     yield make
     for c in made:
@@ -100,23 +111,35 @@ def test_tensors_of_another_shape_or_type_are_refused(context, name):
         call(**good)
     for key, t in good.items():
         smaller = t[:-1] if t.dim() == 1 or key.endswith("pool") or key == "idx" else t[..., :-1].contiguous()
-        wrong = [smaller, t.to(torch.float64), t.as_subclass(torch.Tensor)]
+        wrong = [smaller, t.to(torch.float64), t.as_subclass(torch.Tensor), t.as_subclass(Elsewhere)]
         if t.dtype == torch.float32 and key != "vote":
             wrong.append(t.to(torch.bfloat16))
         if key in ("k_new", "v_new", "k", "v"):
             wrong += [t.float(), t.to(torch.float16)]              # the type of another pool; as wide, but another type
         if key.endswith("pool"):
-            wrong = [smaller, t.as_subclass(torch.Tensor)]         # (a pool is bytes, of any type)
+            wrong = [smaller, t.as_subclass(torch.Tensor), t.as_subclass(Elsewhere)]         # (a pool is bytes, of any type)
         if key in ("skip", "hit"):
-            wrong = [smaller, t.int(), t.as_subclass(torch.Tensor)]
+            wrong = [smaller, t.int(), t.as_subclass(torch.Tensor), t.as_subclass(Elsewhere)]
         if key == "cu_rows":
-            wrong = [t.long(), t.as_subclass(torch.Tensor)]        # (fewer boundaries are fewer sequences)
+            wrong = [t.long(), t.as_subclass(torch.Tensor), t.as_subclass(Elsewhere)]        # (fewer boundaries are fewer sequences)
         if key in ("q", "page_table", "vote", "idx"):
             wrong.append(t.repeat_interleave(2, -1)[..., ::2])     # (not dense)
         for bad in wrong:
             with pytest.raises(T.TokenSelectError) as e:
                 call(**(good | {key: bad}))
             assert e.value.status in (T.STATUS_CODE["TS_ERR_SHAPE"], T.STATUS_CODE["TS_ERR_INVALID_ARG"]), (key, bad.dtype)
+
+
+def test_prompts_on_another_device_are_refused(context):
+    c = context(H, HKV, D, T.TS_KV_Q4, B, 4, 8)
+    q, k = (_on(torch.zeros(5, heads, D, dtype=torch.bfloat16)) for heads in (H, HKV))
+    good = dict(q=q, k=k, v=k, cu_rows=_on(torch.tensor([0, 2, 5], dtype=torch.int32)), out=q, lse=_on(torch.zeros(5, H)))
+    with pytest.raises(Reached):
+        c.prompt_attend(**good)
+    for key, t in good.items():
+        for there in (torch.Tensor, Elsewhere):
+            with pytest.raises(T.TokenSelectError):
+                c.prompt_attend(**(good | {key: t.as_subclass(there)}))
 
 
 def test_rows_for_a_pool_that_holds_them_as_they_are(context):

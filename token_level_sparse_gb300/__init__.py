@@ -154,8 +154,8 @@ def _packed(where, shapes, dtypes, on_device):
         if got is not want:
             raise TokenSelectError(STATUS_CODE["TS_ERR_INVALID_ARG"], f"{where}: {got} instead of {want}")
     for t in on_device:
-        if t is not None and not t.is_cuda:
-            raise TokenSelectError(STATUS_CODE["TS_ERR_INVALID_ARG"], f"{where}: a tensor is not on the device")
+        if t is not None and t.get_device() != _device():
+            raise TokenSelectError(STATUS_CODE["TS_ERR_INVALID_ARG"], f"{where}: a tensor is not on the current device")
 
 
 def _refuse(where, status, why):
@@ -163,22 +163,24 @@ def _refuse(where, status, why):
 
 
 def _tensors(where, *specs):
-    """Refuses a call unless every (tensor, shape, type) is a dense tensor of these on the device. None and raw
+    """Refuses a call unless every (tensor, shape, type) is a dense tensor of these on the current device. None and raw
     addresses are not looked at, here and below: the library sees to the first, nobody can to the second."""
+    here = _device()
     for t, shape, dtype in specs:
         if t is None or isinstance(t, int):
             continue
-        if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.is_cuda:
+        if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == here:
             continue
         if t.shape != shape:
             _refuse(where, "TS_ERR_SHAPE", f"{tuple(t.shape)} instead of {tuple(shape)}")
         if t.dtype is not dtype:
             _refuse(where, "TS_ERR_INVALID_ARG", f"{t.dtype} instead of {dtype}")
-        _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the device")
+        _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the current device")
 
 
 def _rows_of(where, B, *specs):
     """The same for (tensor, columns, type), with a row for each sequence at least, dense inside a row."""
+    here = _device()
     for t, columns, dtype in specs:
         if t is None or isinstance(t, int):
             continue
@@ -186,8 +188,8 @@ def _rows_of(where, B, *specs):
             _refuse(where, "TS_ERR_SHAPE", f"{tuple(t.shape)} instead of {(B, columns)} or more")
         if t.dtype is not dtype:
             _refuse(where, "TS_ERR_INVALID_ARG", f"{t.dtype} instead of {dtype}")
-        if t.stride(1) != 1 or not t.is_cuda:
-            _refuse(where, "TS_ERR_INVALID_ARG", "a tensor's rows are not dense, or not on the device")
+        if t.stride(1) != 1 or t.get_device() != here:
+            _refuse(where, "TS_ERR_INVALID_ARG", "a tensor's rows are not dense, or not on the current device")
 
 
 def _dense(where, *tensors):
@@ -426,11 +428,12 @@ class Context:
 
     def _paged(self, where, B, page_table, k_pool, v_pool):
         """Refuses a page table or pools smaller than the context's."""
+        here = _device()
         try:
             shape, need = page_table.shape, self._pool_bytes
-            if (shape[0] >= B and shape[1] == self._columns and page_table.dtype is _int32 and page_table.is_cuda
-                    and page_table.is_contiguous() and k_pool.nbytes >= need and k_pool.is_cuda and k_pool.is_contiguous()
-                    and v_pool.nbytes >= need and v_pool.is_cuda and v_pool.is_contiguous() and len(shape) == 2):
+            if (shape[0] >= B and shape[1] == self._columns and page_table.dtype is _int32 and page_table.get_device() == here
+                    and page_table.is_contiguous() and k_pool.nbytes >= need and k_pool.get_device() == here and k_pool.is_contiguous()
+                    and v_pool.nbytes >= need and v_pool.get_device() == here and v_pool.is_contiguous() and len(shape) == 2):
                 return                                             # (one test of all, as most calls pass)
         except (AttributeError, IndexError):                       # None, raw addresses, other shapes
             pass
@@ -441,8 +444,8 @@ class Context:
                 continue
             if t.nbytes < self._pool_bytes:
                 _refuse(where, "TS_ERR_SHAPE", f"a pool of less than {self._pool_bytes} bytes")
-            if not (t.is_cuda and t.is_contiguous()):
-                _refuse(where, "TS_ERR_INVALID_ARG", "a pool is not dense or not on the device")
+            if t.get_device() != here or not t.is_contiguous():
+                _refuse(where, "TS_ERR_INVALID_ARG", "a pool is not dense or not on the current device")
 
     def _queries(self, where, q, page_table, k_pool, v_pool, seq_lens=None, out=None, lse=None, vote=None, idx=None,
                  count=None, flags=None):
@@ -454,11 +457,12 @@ class Context:
                  (count, shape[:1], _int32))
         self._paged(where, B, page_table, k_pool, k_pool if v_pool is None else v_pool)
         _rows_of(where, B, (vote, self.max_tokens, _float32), (idx, 1, _int32))
+        here = _device()
         if flags is not None and not isinstance(flags, int):
             if flags.numel() < B or flags.element_size() != 1:
                 _refuse(where, "TS_ERR_SHAPE", f"{tuple(flags.shape)} of {flags.dtype} instead of {(B,)} bytes")
-            if not (flags.is_cuda and flags.is_contiguous()):
-                _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the device")
+            if flags.get_device() != here or not flags.is_contiguous():
+                _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the current device")
 
     def close(self):
         if self.handle:
@@ -514,11 +518,11 @@ class Context:
         """k_new / v_new [B][H_kv][d]: the current token's rows into position seq_lens[b] - 1."""
         if _device is None:
             _torch()
-        B, kind, row = seq_lens.shape[0], self._rows_dtype(), self._kv_row
+        B, kind, row, here = seq_lens.shape[0], self._rows_dtype(), self._kv_row, _device()
         try:
             ks = k_new.shape
             good = (ks[1:] == row and ks[0] == B and v_new.shape == ks and k_new.dtype is kind and v_new.dtype is kind
-                    and k_new.is_cuda and v_new.is_cuda and k_new.is_contiguous() and v_new.is_contiguous())
+                    and k_new.get_device() == here and v_new.get_device() == here and k_new.is_contiguous() and v_new.is_contiguous())
         except (AttributeError, IndexError):
             good = False
         for t in () if good else (k_new, v_new):
@@ -527,8 +531,8 @@ class Context:
             # (any view of the rows' bits goes into a pool that holds them as they are)
             if t.numel() != B * row[0] * row[1] or t.element_size() != kind.itemsize:
                 _refuse("append_kv", "TS_ERR_SHAPE", f"{tuple(t.shape)} of {t.dtype} instead of {(B, *row)} of {kind}")
-            if (self._q4 and t.dtype is not kind) or not (t.is_cuda and t.is_contiguous()):
-                _refuse("append_kv", "TS_ERR_INVALID_ARG", f"dense rows of {kind} on the device are wanted")
+            if (self._q4 and t.dtype is not kind) or t.get_device() != here or not t.is_contiguous():
+                _refuse("append_kv", "TS_ERR_INVALID_ARG", f"dense rows of {kind} on the current device are wanted")
         if self._q4:
             _tensors("append_kv", (seq_lens, (B,), _int32))
             self._paged("append_kv", B, page_table, k_pool, v_pool)
@@ -538,12 +542,12 @@ class Context:
         """k / v [total][H_kv][d], packed: row r of sequence b to position starts[b] + r - cu_rows[b]."""
         if _device is None:
             _torch()
-        ks, B, i32, kind = k.shape, cu_rows.shape[0] - 1, _int32, self._rows_dtype()
+        ks, B, i32, kind, here = k.shape, cu_rows.shape[0] - 1, _int32, self._rows_dtype(), _device()
         if not (ks[1:] == self._kv_row and v.shape == ks and k.dtype is kind and v.dtype is kind and cu_rows.dtype is i32
-                and k.is_cuda and v.is_cuda and cu_rows.is_cuda):
+                and k.get_device() == here and v.get_device() == here and cu_rows.get_device() == here):
             _packed("append_prompt", ((ks[1:], self._kv_row), (v.shape, ks)), ((k.dtype, kind), (v.dtype, kind), (cu_rows.dtype, i32)),
                     (k, v, cu_rows))
-        if starts is not None and not (starts.shape == (B,) and starts.dtype is i32 and starts.is_cuda):
+        if starts is not None and not (starts.shape == (B,) and starts.dtype is i32 and starts.get_device() == here):
             _packed("append_prompt", ((starts.shape, (B,)),), ((starts.dtype, i32),), (starts,))
         _dense("append_prompt", cu_rows, starts)
         self._paged("append_prompt", B, page_table, k_pool, v_pool)
@@ -555,12 +559,12 @@ class Context:
         """k_out / v_out fp32 [total][H_kv][d]: the values of the rows that append_prompt would write."""
         if _device is None:
             _torch()
-        ks, B, i32, f32 = k_out.shape, cu_rows.shape[0] - 1, _int32, _float32
+        ks, B, i32, f32, here = k_out.shape, cu_rows.shape[0] - 1, _int32, _float32, _device()
         if not (ks[1:] == self._kv_row and v_out.shape == ks and k_out.dtype is f32 and v_out.dtype is f32
-                and cu_rows.dtype is i32 and k_out.is_cuda and v_out.is_cuda and cu_rows.is_cuda):
+                and cu_rows.dtype is i32 and k_out.get_device() == here and v_out.get_device() == here and cu_rows.get_device() == here):
             _packed("read_kv", ((ks[1:], self._kv_row), (v_out.shape, ks)),
                     ((k_out.dtype, f32), (v_out.dtype, f32), (cu_rows.dtype, i32)), (k_out, v_out, cu_rows))
-        if starts is not None and not (starts.shape == (B,) and starts.dtype is i32 and starts.is_cuda):
+        if starts is not None and not (starts.shape == (B,) and starts.dtype is i32 and starts.get_device() == here):
             _packed("read_kv", ((starts.shape, (B,)),), ((starts.dtype, i32),), (starts,))
         _dense("read_kv", k_out, v_out, cu_rows, starts)
         self._paged("read_kv", B, page_table, k_pool, v_pool)
@@ -576,13 +580,13 @@ class Context:
         """q / out [total][H][d], k / v [total][H_kv][d] (bf16, packed): causal attention of every sequence."""
         if _device is None:
             _torch()
-        qs, ks, bf, i32 = q.shape, k.shape, _bfloat16, _int32
+        qs, ks, bf, i32, here = q.shape, k.shape, _bfloat16, _int32, _device()
         if not (qs[1:] == self._q_row and ks[1:] == self._kv_row and ks[0] == qs[0] and v.shape == ks and out.shape == qs
                 and q.dtype is bf and k.dtype is bf and v.dtype is bf and out.dtype is bf and cu_rows.dtype is i32
-                and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and cu_rows.is_cuda):
+                and q.get_device() == here and k.get_device() == here and v.get_device() == here and out.get_device() == here and cu_rows.get_device() == here):
             _packed("prompt_attend", ((qs[1:], self._q_row), (ks[1:], self._kv_row), (ks[:1], qs[:1]), (v.shape, ks), (out.shape, qs)),
                     ((q.dtype, bf), (k.dtype, bf), (v.dtype, bf), (out.dtype, bf), (cu_rows.dtype, i32)), (q, k, v, out, cu_rows))
-        if lse is not None and not (lse.shape == qs[:2] and lse.dtype is _float32 and lse.is_cuda):
+        if lse is not None and not (lse.shape == qs[:2] and lse.dtype is _float32 and lse.get_device() == here):
             _packed("prompt_attend", ((lse.shape, qs[:2]),), ((lse.dtype, _float32),), (lse,))
         _dense("prompt_attend", cu_rows, lse)
         total, row = qs[0], self._kv_row

@@ -79,6 +79,13 @@ constexpr int64_t kMaxRowStride = (int64_t)1 << 31;   // elements from one packe
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
+// The current device is not the context's: its kernels would be launched where its memory is not.
+bool elsewhere(const ts_ctx* ctx) {
+  int device = -1;
+  return cudaGetDevice(&device) != cudaSuccess || device != ctx->device;
+}
+bool q4_elsewhere(const ts_ctx* ctx) { return ctx->cfg.kv_dtype == TS_KV_Q4 && elsewhere(ctx); }
+
 }  // namespace
 
 extern "C" {
@@ -286,6 +293,7 @@ ts_status ts_score(ts_ctx* ctx, const float* q, const void* k_pool, const int32_
                    const int32_t* seq_lens, int B, const uint8_t* skip, float scale, float* vote,
                    int64_t vote_stride, void* stream) {
   if (!ctx || !q || !k_pool || !page_table || !seq_lens || !vote) return TS_ERR_INVALID_ARG;
+  if (q4_elsewhere(ctx)) return TS_ERR_INVALID_ARG;
   if (B < 1 || B > ctx->cfg.max_batch || vote_stride < ctx->max_tokens) return TS_ERR_SHAPE;
   if (std::isnan(scale)) return TS_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(k_pool) % 16 != 0) return TS_ERR_INVALID_ARG;
@@ -298,6 +306,7 @@ ts_status ts_score_fn(ts_ctx* ctx, const ts_select_params* params, const float* 
                       float* vote, int64_t vote_stride, void* stream) {
   if (!ctx || !q || !k_pool || !page_table || !seq_lens || !vote || !valid_params(params))
     return TS_ERR_INVALID_ARG;
+  if (q4_elsewhere(ctx)) return TS_ERR_INVALID_ARG;
   if (B < 1 || B > ctx->cfg.max_batch || vote_stride < ctx->max_tokens) return TS_ERR_SHAPE;
   if (reinterpret_cast<uintptr_t>(k_pool) % 16 != 0) return TS_ERR_INVALID_ARG;
   ScoreCall c{q, k_pool, page_table, seq_lens, skip, B, resolve_scale(ctx, params->softmax_scale), vote,
@@ -328,6 +337,7 @@ ts_status ts_sparse_attend(ts_ctx* ctx, const float* q, const void* k_pool, cons
                            const int32_t* page_table, const int32_t* idx, int64_t idx_stride,
                            const int32_t* count, int B, float scale, float* out, float* lse, void* stream) {
   if (!ctx || !q || !k_pool || !v_pool || !page_table || !idx || !count || !out) return TS_ERR_INVALID_ARG;
+  if (q4_elsewhere(ctx)) return TS_ERR_INVALID_ARG;
   if (B < 1 || B > ctx->cfg.max_batch || idx_stride < 1) return TS_ERR_SHAPE;
   if (std::isnan(scale)) return TS_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(k_pool) % 16 != 0 || reinterpret_cast<uintptr_t>(v_pool) % 16 != 0)
@@ -344,6 +354,7 @@ ts_status ts_decode_step(ts_ctx* ctx, ts_cache* cache, int layer, const float* q
   if (!ctx || !q || !k_pool || !v_pool || !page_table || !seq_lens || !idx || !count || !out ||
       !valid_params(params))
     return TS_ERR_INVALID_ARG;
+  if (q4_elsewhere(ctx)) return TS_ERR_INVALID_ARG;
   if (B < 1 || B > ctx->cfg.max_batch || idx_stride < 1) return TS_ERR_SHAPE;
   if (cache && (cache->ctx != ctx || layer < 0 || layer >= cache->n_layers)) return TS_ERR_INVALID_ARG;
   if (!vote) {
@@ -470,6 +481,7 @@ ts_status ts_prefill_chunk(ts_ctx* ctx, const float* q, int c, const void* k_poo
 ts_status ts_append_kv(ts_ctx* ctx, const void* k_new, const void* v_new, const int32_t* page_table,
                        const int32_t* seq_lens, int B, void* k_pool, void* v_pool, void* stream) {
   if (!ctx || !k_new || !v_new || !page_table || !seq_lens || !k_pool || !v_pool) return TS_ERR_INVALID_ARG;
+  if (q4_elsewhere(ctx)) return TS_ERR_INVALID_ARG;
   if (B < 1 || B > ctx->cfg.max_batch) return TS_ERR_SHAPE;
   for (const void* p : {k_new, v_new, static_cast<const void*>(k_pool), static_cast<const void*>(v_pool)})
     if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return TS_ERR_INVALID_ARG;
@@ -480,6 +492,7 @@ ts_status ts_append_prompt(ts_ctx* ctx, const void* k, int64_t k_stride, const v
                            const int32_t* cu_rows, const int32_t* starts, int B, int total,
                            const int32_t* page_table, void* k_pool, void* v_pool, void* stream) {
   if (!ctx || !k || !v || !cu_rows || !page_table || !k_pool || !v_pool) return TS_ERR_INVALID_ARG;
+  if (elsewhere(ctx)) return TS_ERR_INVALID_ARG;
   const ts_config& c = ctx->cfg;
   const int64_t row = (int64_t)c.n_kv_heads * c.head_dim, per16 = c.kv_dtype == TS_KV_F32 ? 4 : 8;
   if (B < 1 || B > c.max_batch || total < 0 || total > kMaxRows) return TS_ERR_SHAPE;
@@ -495,6 +508,7 @@ ts_status ts_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* starts,
                      const int32_t* page_table, const void* k_pool, const void* v_pool, float* k_out, float* v_out,
                      void* stream) {
   if (!ctx || !cu_rows || !page_table || !k_pool || !v_pool || !k_out || !v_out) return TS_ERR_INVALID_ARG;
+  if (elsewhere(ctx)) return TS_ERR_INVALID_ARG;
   if (B < 1 || B > ctx->cfg.max_batch || total < 0 || total > kMaxRows) return TS_ERR_SHAPE;
   for (const void* p : {k_pool, v_pool, static_cast<const void*>(k_out), static_cast<const void*>(v_out)})
     if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return TS_ERR_INVALID_ARG;
@@ -504,6 +518,7 @@ ts_status ts_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* starts,
 ts_status ts_attend(ts_ctx* ctx, const float* q, const void* k_pool, const void* v_pool, const int32_t* page_table,
                     const int32_t* seq_lens, int B, float scale, float* out, float* lse, void* stream) {
   if (!ctx || !q || !k_pool || !v_pool || !page_table || !seq_lens || !out) return TS_ERR_INVALID_ARG;
+  if (elsewhere(ctx)) return TS_ERR_INVALID_ARG;
   if (B < 1 || B > ctx->cfg.max_batch) return TS_ERR_SHAPE;
   if (std::isnan(scale)) return TS_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(k_pool) % 16 != 0 || reinterpret_cast<uintptr_t>(v_pool) % 16 != 0)
@@ -517,6 +532,7 @@ ts_status ts_prompt_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const v
                            const void* v, int64_t v_stride, const int32_t* cu_rows, int B, int total, float scale,
                            void* out, int64_t out_stride, float* lse, void* stream) {
   if (!ctx || !q || !k || !v || !cu_rows || !out) return TS_ERR_INVALID_ARG;
+  if (elsewhere(ctx)) return TS_ERR_INVALID_ARG;
   const ts_config& c = ctx->cfg;
   const int64_t qrow = (int64_t)c.n_q_heads * c.head_dim, krow = (int64_t)c.n_kv_heads * c.head_dim;
   if (B < 1 || B > c.max_batch || total < 0 || total > kMaxRows) return TS_ERR_SHAPE;
