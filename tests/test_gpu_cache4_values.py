@@ -205,3 +205,15 @@ def test_queries_and_rows_of_another_type_are_refused():
         with pytest.raises(T.TokenSelectError):
             call()
     assert (out == 7).all() and (lse == 7).all() and torch.equal(c.kp, kp) and c.ctx.status() == 0
+
+
+def test_a_context_for_many_prompts_holds_no_scratch_of_other_kernels():
+    # 531 sequences of 32 heads over 8: the parts of the kernels that do not serve 4-bit pools would be 1.9 GB
+    T = tsl()
+    T.Context(32, 8, 128, T.TS_KV_Q4, 1, 1, 1).close()
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    ctx = T.Context(32, 8, 128, T.TS_KV_Q4, 531, 1, 1)
+    held = free - torch.cuda.mem_get_info()[0]
+    ctx.close()
+    assert held < 256 << 20, held

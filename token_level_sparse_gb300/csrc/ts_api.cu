@@ -170,37 +170,39 @@ ts_status ts_create(ts_ctx** out, const ts_config* cfg) {
   ctx->logits_floats = (int64_t)(B * H * T + H * NS * 2 * kPage);
   chk(alloc(&ctx->status, 1));
   chk(alloc(&ctx->logits, (size_t)ctx->logits_floats));
-  chk(alloc(&ctx->step_partials, B * NS * 2 * H));   // two partial rows per CTA where a tile holds two pages
-  chk(alloc(&ctx->step_hist, B * kStepHistPerSeq));
-  chk(alloc(&ctx->step_mass, B * kStepHistPerSeq));
-  chk(alloc(&ctx->cand_n, B));
-  chk(alloc(&ctx->cands, B * 2048));
-  chk(alloc(&ctx->cta_cnt, B * NS * 4));
-  chk(alloc(&ctx->apart, B * NS * H * (D + 2) + 2 * B * H));   // (max, sum) rows padded to an even count
-  // per CTA: [sequence][scan warp][head] (max, sum exp) pairs of the CUDA-core scan
-  chk(alloc(&ctx->step_wpart, NS * B * kMaxScanWarps * kMaxScanG * 2));
+  const bool q4 = c.kv_dtype == TS_KV_Q4;
+  if (!q4) {   // the persistent kernel, and the kernels of the other pools
+    chk(alloc(&ctx->step_partials, B * NS * 2 * H));   // two partial rows per CTA where a tile holds two pages
+    chk(alloc(&ctx->step_hist, B * kStepHistPerSeq));
+    chk(alloc(&ctx->step_mass, B * kStepHistPerSeq));
+    chk(alloc(&ctx->cand_n, B));
+    chk(alloc(&ctx->cands, B * 2048));
+    chk(alloc(&ctx->cta_cnt, B * NS * 4));
+    chk(alloc(&ctx->apart, B * NS * H * (D + 2) + 2 * B * H));   // (max, sum) rows padded to an even count
+    // per CTA: [sequence][scan warp][head] (max, sum exp) pairs of the CUDA-core scan
+    chk(alloc(&ctx->step_wpart, NS * B * kMaxScanWarps * kMaxScanG * 2));
+    chk(alloc(&ctx->sel_rows, NS * kStepFlagCap));
+    chk(alloc(&ctx->partials, B * ctx->score_max_chunks * H));
+    chk(alloc(&ctx->attn_part, B * HKV * kAttnMaxSplits * G * (D + 2)));
+    chk(alloc(&ctx->qmean, B * H * D));
+  } else {
+    const size_t slots = (size_t)q4_part_slots(c, ctx->num_sms);
+    chk(alloc(&ctx->q4_part_o, slots * H * D));
+    chk(alloc(&ctx->q4_part_ml, slots * H));
+  }
   chk(alloc(&ctx->gsync, 4));
   if (e == cudaSuccess) chk(cudaMemset(ctx->gsync, 0, 4 * sizeof(unsigned)));   // then kept zero by each launch
   chk(alloc(&ctx->phase_ns, 64));
-  chk(alloc(&ctx->partials, B * ctx->score_max_chunks * H));
   chk(alloc(&ctx->stats, B * H));
   chk(alloc(&ctx->counters, B * kCounterSlots));
   chk(alloc(&ctx->sel_state, B));
   chk(alloc(&ctx->hist, B * 2048));
   chk(alloc(&ctx->mass_hist, B * 2048));
   chk(alloc(&ctx->chunk_counts, B * ctx->sel_max_chunks));
-  chk(alloc(&ctx->attn_part, B * HKV * kAttnMaxSplits * G * (D + 2)));
   chk(alloc(&ctx->vote, B * T));
   chk(alloc(&ctx->hit, B));
-  chk(alloc(&ctx->qmean, B * H * D));
   chk(alloc(&ctx->blk_len, B));
   chk(alloc(&ctx->blk_idx, B * T + B));
-  chk(alloc(&ctx->sel_rows, NS * kStepFlagCap));
-  if (c.kv_dtype == TS_KV_Q4) {
-    const size_t slots = (size_t)q4_part_slots(c, ctx->num_sms);
-    chk(alloc(&ctx->q4_part_o, slots * H * D));
-    chk(alloc(&ctx->q4_part_ml, slots * H));
-  }
   if (e == cudaSuccess) chk(cudaMemset(ctx->status, 0, sizeof(int)));
   if (e == cudaSuccess) chk(cudaMemset(ctx->counters, 0, B * kCounterSlots * sizeof(unsigned)));
   if (e == cudaSuccess) chk(cudaMemset(ctx->hist, 0, B * 2048 * sizeof(unsigned)));
