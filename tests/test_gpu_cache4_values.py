@@ -217,3 +217,53 @@ def test_a_context_for_many_prompts_holds_no_scratch_of_other_kernels():
     held = free - torch.cuda.mem_get_info()[0]
     ctx.close()
     assert held < 256 << 20, held
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 4, 64), (32, 8, 128), (28, 4, 128)])
+def test_from_prompts_to_decode_steps_within_each_operator_s_tolerance(H, Hkv, d):
+    # prompts are attended and written, then decode steps append, select and attend: every output against the oracle
+    # over the values that the cache holds, as near as the operators by themselves
+    from test_gpu_prompt import _check as check_prompt
+    T = tsl()
+    lens, steps = [333, 1, 70], 3
+    B, rows = len(lens), sum(lens)
+    c = Cache(H, Hkv, d, [n + steps for n in lens], seed=22, poison=False)
+    c.kp.fill_(255)                                                # (slots not written yet hold NaN)
+    c.vp.fill_(255)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(9)
+    qkv = torch.randn(rows, (H + 2 * Hkv) * d, generator=g, device=DEV).to(torch.bfloat16)
+    q = qkv[:, :H * d].view(rows, H, d)
+    k, v = (qkv[:, (H + i * Hkv) * d:(H + (i + 1) * Hkv) * d].view(rows, Hkv, d) for i in range(2))
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    cu_dev = torch.from_numpy(cu).to(DEV)
+    out, lse = torch.zeros(rows, H, d, dtype=torch.bfloat16, device=DEV), torch.zeros(rows, H, device=DEV)
+    c.ctx.prompt_attend(q, k, v, cu_dev, out, lse)
+    c.ctx.append_prompt(k, v, cu_dev, c.pt, c.kp, c.vp)
+    assert c.ctx.status() == 0
+    check_prompt(out, lse, q, k, v, cu, 1 / math.sqrt(d), [0, 1, 127, 128, 255, 256, 332, 333, 334, 403])
+    cache, prm = c.ctx.cache(1, 52), T.params(k=32, n_sink=4, n_local=16, theta=0.9)
+    idx, cnt = torch.zeros(B, 52, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    o, z, full, fullz = (torch.zeros(B, H, *x, device=DEV) for x in ((d,), (), (d,), ()))
+    hit = torch.zeros(B, dtype=torch.uint8, device=DEV)
+    states, hits = [O.CacheState() for _ in range(B)], 0
+    for t in range(steps):
+        seq = torch.tensor([n + t + 1 for n in lens], dtype=torch.int32, device=DEV)
+        kn, vn = (torch.randn(B, Hkv, d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+        noise = torch.randn(B, H, d, generator=g, device=DEV)
+        c.q = noise if t != 1 else c.q + 0.1 * noise
+        c.ctx.append_kv(kn, vn, c.pt, seq, c.kp, c.vp)
+        c.ctx.decode_step(c.q, c.kp, c.vp, c.pt, seq, prm, idx, cnt, o, z, hit=hit, cache=cache)
+        c.ctx.attend(c.q, c.kp, c.vp, c.pt, seq, full, fullz)
+        assert c.ctx.status() == 0
+        c.kval, c.vval = (O.q4_pool_values(x.cpu().numpy(), d) for x in (c.kp, c.vp))
+        for b in range(B):
+            n = lens[b] + t + 1
+            ref = O.decode_step(states[b], c.q[b].double().cpu().numpy(), c.kval, c.vval, c.table[b], n, k=32, n_sink=4,
+                                n_local=16, theta=0.9)
+            got = idx[b, :int(cnt[b])].cpu().numpy()
+            assert bool(hit[b]) == ref["hit"] and np.array_equal(got, ref["idx"])
+            hits += ref["hit"]
+            _check(c, o, z, b, got)
+            _check(c, full, fullz, b, np.arange(n))
+    assert hits == B
