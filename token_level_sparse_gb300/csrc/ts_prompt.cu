@@ -105,6 +105,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Base-2 maxima that fp32 holds to no better than 1 (or not at all: infinities): the rounding of the maximum is then
+// a factor of 2 or more in the weights, and of nothing but zeros and infinities from 2^31 on. The weights of such
+// rows are taken from the scores less the unscaled maximum, which is exact for the scores that matter.
+__device__ __forceinline__ bool far(float m2) { return !(fabsf(m2) <= 16777216.f); }
+
 // Blocks of sequence b; sequences whose boundaries are not ascending inside [0, total] have none.
 __device__ __forceinline__ int seq_blocks(const PromptArgs& a, int b, int block) {
   const int s0 = a.cu[b], s1 = a.cu[b + 1];
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         const int first = it.i0 + i * a.tokens;                   // first token of the tile
         const int row_tok = (int)((uint32_t)row * inv_g >> 16), tok = first + row_tok;
         const bool real = row_tok < a.tokens && tok < it.n;
-        float m2 = -INFINITY, la = 0.f, lb = 0.f;                 // running maximum (base 2) and two halves of the sum
+        float mx = -INFINITY, la = 0.f, lb = 0.f;                 // running maximum (unscaled) and two halves of the sum
         for (int j = 0; j < mine; ++j) {
           ok = __all_sync(kFull, mbar_wait(&s_full[i], s_par, a.wait_ns));
           if (!ok) break;
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           // it does not (and in the first tile, which has none), the scores, still in tensor memory, are read
           // again and the maximum is taken first.
           uint32_t p[64];
-          float ta, tb;
+          float ta, tb, m2 = mx * a.scale2;
           bool over = real;                                       // this row needs its maximum (in a pass that takes it)
           for (bool raise = j == 0;; raise = true) {
             uint32_t u[128];
@@ -525,17 +530,21 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
               }
             }
             if (raise) {
-              float mx = x[0], my = x[1];
+              float ma = x[0], mb = x[1];
 #pragma unroll
               for (int c = 2; c < 128; c += 2) {
-                mx = fmaxf(mx, x[c]);
-                my = fmaxf(my, x[c + 1]);
+                ma = fmaxf(ma, x[c]);
+                mb = fmaxf(mb, x[c + 1]);
               }
               // each row by itself, so that no row's bits depend on another's: rows that do not need it keep their
               // maximum, as do rows that are no query of the sequence (their operands may be anything)
-              const float mn = over ? fmaxf(m2, fmaxf(mx, my) * a.scale2) : m2;
-              const float f = mn == m2 ? 1.f : pr_ex2(m2 - mn);
-              m2 = mn;
+              const float mn = over ? fmaxf(mx, fmaxf(ma, mb)) : mx, n2 = mn * a.scale2;
+              // from the reference that the row's weights had to the one that they get (far maxima: the exact product)
+              const float d = far(m2) ? (far(n2) ? (mx - mn) * a.scale2 : fmaf(mx, a.scale2, -n2))
+                                      : (far(n2) ? -fmaf(mn, a.scale2, -m2) : m2 - n2);
+              const float f = mn == mx ? 1.f : pr_ex2(d);
+              mx = mn;
+              m2 = n2;
               la *= f;
               lb *= f;
               if (j > 0) {
@@ -555,7 +564,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
                 }
               }
             }
-            const float ms = m2 == -INFINITY ? 0.f : -m2;         // nothing seen yet: every weight is zero
+            float ms = m2 == -INFINITY ? 0.f : -m2;               // nothing seen yet: every weight is zero
+            if (raise && __any_sync(kFull, far(m2) && m2 != -INFINITY)) {
+              const bool shift = far(m2) && m2 != -INFINITY;
+              const float off = shift ? mx : 0.f;
+              ms = shift ? 0.f : ms;
+#pragma unroll
+              for (int c = 0; c < 128; c += 2) add2(x[c], x[c + 1], -off, -off);
+            }
             const uint64_t sc = pack_f2(a.scale2, a.scale2), mm = pack_f2(ms, ms);
             ta = tb = 0.f;
 #pragma unroll
@@ -568,7 +584,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
               p[c] = pack_bf16(y0, y1);
             }
             if (raise) break;
-            over = real && (!(ta + tb <= kPrMaxSum) || m2 == -INFINITY);
+            over = real && (!(ta + tb <= kPrMaxSum) || far(m2));
             if (!__any_sync(kFull, over)) break;
           }
           if (!ok) break;
@@ -590,7 +606,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           const float l = la + lb, inv = 1.f / l;
           const bool odd = s_odd[slot] != 0;
           const int row0 = s_item[slot].row0, head = s_item[slot].kv * a.G + row - row_tok * a.G;
-          if (real && a.lse) a.lse[(int64_t)(row0 + tok) * a.H + head] = (m2 + log2f(l)) * 0.6931471805599453f;
+          if (real && a.lse) a.lse[(int64_t)(row0 + tok) * a.H + head] = (mx * a.scale2 + log2f(l)) * 0.6931471805599453f;
           // this lane's output row; a null pointer where it is none
           const uint64_t dst = real ? reinterpret_cast<uint64_t>(a.out + (int64_t)(row0 + tok) * a.out_stride + (int64_t)head * D) : 0u;
           unsigned char* stage = sO + warp * S::STAGE;
