@@ -350,8 +350,10 @@ ts_status ts_prefill_chunk(ts_ctx* ctx, const float* q, int c, const void* k_poo
  * for its own copies in flight, frees its tensor memory and returns, so the
  * context stays usable. The waits of ts_prefill_chunk and ts_prompt_attend have
  * the same bound (each by itself; one of the longest lasts as long as 128 rows of
- * a prompt take). The waits of the separate calls (ts_score, ts_attend,
- * ts_sparse_attend) keep the 1 s bound. ns == 0 is TS_ERR_INVALID_ARG. */
+ * a prompt take), but what ts_prompt_attend has in flight when one runs out is
+ * waited for as long as 1 s even where ns is less. The waits of the separate calls
+ * (ts_score, ts_attend, ts_sparse_attend) keep the 1 s bound. ns == 0 is
+ * TS_ERR_INVALID_ARG. */
 ts_status ts_set_wait_limit(ts_ctx* ctx, uint64_t ns);
 
 /* Fault injection for tests of the time-out path: the NEXT persistent

@@ -56,3 +56,25 @@ def test_scores_of_any_size(H, Hkv, e, scale, rise):
                 tol = np.abs(want) * 2.0 ** -8 + (w @ np.abs(vv)) * (2.0 ** -8 + t * 2.0 ** -22) + np.abs(vv).max() * 2.0 ** -38 + 1e-30
                 assert np.all(np.abs(on[r, h] - want) <= tol), (r, h, t, on[r, h][:3], want[:3])
                 assert abs(ln[r, h] - wl) <= abs(wl) * 2.0 ** -22 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 4, 64), (32, 8, 128)])
+def test_a_wait_limit_far_below_any_wait_is_reported_and_leaves_the_context_usable(H, Hkv, d):
+    # every role gives up at its first wait that is not over at once; copies and products in flight are waited for
+    T, n = tsl(), 3000
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    q, k, v = (torch.randn(n, heads, d, generator=g, device=DEV).to(torch.bfloat16) for heads in (H, Hkv, Hkv))
+    cu = torch.tensor([0, 700, n], dtype=torch.int32, device=DEV)
+    ctx = T.Context(H, Hkv, d, T.TS_KV_Q4, 2, 1, 1)
+    ref, out = (torch.zeros(n, H, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ctx.prompt_attend(q, k, v, cu, ref)
+    assert ctx.status() == 0
+    T.ts_set_wait_limit(ctx.handle, 1)
+    for _ in range(3):
+        ctx.prompt_attend(q, k, v, cu, out)
+        assert ctx.status() == T.STATUS_CODE["TS_ERR_TIMEOUT"]
+    T.ts_set_wait_limit(ctx.handle, 1_000_000_000)
+    out.zero_()
+    ctx.prompt_attend(q, k, v, cu, out)
+    assert ctx.status() == 0 and torch.equal(out, ref)

@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const int block = 2 * a.tokens;
+  const uint64_t settle = a.wait_ns > kWaitLimitNs ? a.wait_ns : kWaitLimitNs;   // for what is in flight at the end
 
   if (warp == kPrSoftmaxWarps + 1) {
     tmem_alloc(&s_tmem, S::TMEM_COLS);
@@ -300,10 +301,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           if (!ok) break;
         }
         if (!ok) set_error(a.status, TS_ERR_TIMEOUT);
-        // nothing may still be landing when the CTA exits
-        if (items > 0) mbar_wait(&q_full, (items - 1) & 1, a.wait_ns);
-        for (int j = max(0, kn - 2); j < kn; ++j) mbar_wait(&k_full[j & 1], (j >> 1) & 1, a.wait_ns);
-        for (int j = max(0, vn - 2); j < vn; ++j) mbar_wait(&v_full[j & 1], (j >> 1) & 1, a.wait_ns);
+        // nothing may still be landing when the CTA exits, however short the limit was that a role gave up at
+        if (items > 0) mbar_wait(&q_full, (items - 1) & 1, settle);
+        for (int j = max(0, kn - 2); j < kn; ++j) mbar_wait(&k_full[j & 1], (j >> 1) & 1, settle);
+        for (int j = max(0, vn - 2); j < vn; ++j) mbar_wait(&v_full[j & 1], (j >> 1) & 1, settle);
       }
       __syncwarp();
     } else if (warp == kPrSoftmaxWarps + 1) {
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
       // no product may be under way when tensor memory is given back
       commit(&drained);
-      mbar_wait(&drained, 0, a.wait_ns);
+      mbar_wait(&drained, 0, settle);
       __syncwarp();
     } else if (warp == kPrSoftmaxWarps + 2) {
       // ---------------------------------------------------------------- items
