@@ -109,8 +109,16 @@ def test_tensors_of_another_shape_or_type_are_refused(context, name):
     good = {key: _on(t) for key, t in good.items()}
     with pytest.raises(Reached):
         call(**good)
+    # buffers for more sequences than the call has, and scores in rows of a wider matrix
+    for key in {"seq_lens", "out", "lse", "count", "idx", "vote", "page_table", "hit", "skip", "k_pool"} & set(good):
+        if (name, key) != ("append_kv", "seq_lens"):
+            with pytest.raises(Reached):
+                call(**(good | {key: _on(torch.cat([good[key], good[key][:1]]))}))
+    if "vote" in good:
+        with pytest.raises(Reached):
+            call(**(good | {"vote": _on(torch.zeros(B, 99))[:, :30]}))
     for key, t in good.items():
-        smaller = t[:-1] if t.dim() == 1 or key.endswith("pool") or key == "idx" else t[..., :-1].contiguous()
+        smaller = t[:-1] if t.dim() == 1 or key.endswith("pool") or key in ("idx", "vote") else t[..., :-1].contiguous()
         wrong = [smaller, t.to(torch.float64), t.as_subclass(torch.Tensor), t.as_subclass(Elsewhere)]
         if t.dtype == torch.float32 and key != "vote":
             wrong.append(t.to(torch.bfloat16))
@@ -120,6 +128,8 @@ def test_tensors_of_another_shape_or_type_are_refused(context, name):
             wrong = [smaller, t.as_subclass(torch.Tensor), t.as_subclass(Elsewhere)]         # (a pool is bytes, of any type)
         if key in ("skip", "hit"):
             wrong = [smaller, t.int(), t.as_subclass(torch.Tensor), t.as_subclass(Elsewhere)]
+        if (name, key) == ("append_kv", "seq_lens"):
+            wrong = wrong[1:]                                      # (fewer lengths are fewer sequences)
         if key == "cu_rows":
             wrong = [t.long(), t.as_subclass(torch.Tensor), t.as_subclass(Elsewhere)]        # (fewer boundaries are fewer sequences)
         if key in ("q", "page_table", "vote", "idx"):
@@ -147,9 +157,9 @@ def test_rows_for_a_pool_that_holds_them_as_they_are(context):
     good = dict(k_new=torch.zeros(B, HKV, D), v_new=torch.zeros(B, HKV, D), page_table=torch.zeros(B, 4, dtype=torch.int32),
                 seq_lens=torch.ones(B, dtype=torch.int32), k_pool=torch.zeros(1), v_pool=torch.zeros(1))
     good = {key: _on(t) for key, t in good.items()}
-    for bad in (torch.zeros(B, HKV, D, dtype=torch.bfloat16), torch.zeros(B, HKV, D - 1)):
+    for bad in (torch.zeros(B, HKV, D, dtype=torch.bfloat16), torch.zeros(B, HKV, D - 1), torch.zeros(B - 1, HKV, D)):
         with pytest.raises(T.TokenSelectError):
             c.append_kv(**(good | {"k_new": _on(bad)}))
-    for fine in (torch.zeros(B, HKV, D), torch.zeros(B, HKV * D, dtype=torch.int32)):
+    for fine in (torch.zeros(B, HKV, D), torch.zeros(B + 1, HKV, D), torch.zeros(B, HKV * D, dtype=torch.int32)):
         with pytest.raises(Reached):
             c.append_kv(**(good | {"k_new": _on(fine)}))

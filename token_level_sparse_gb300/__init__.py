@@ -163,29 +163,32 @@ def _refuse(where, status, why):
 
 
 def _tensors(where, *specs):
-    """Refuses a call unless every (tensor, shape, type) is a dense tensor of these on the current device. None and raw
-    addresses are not looked at, here and below: the library sees to the first, nobody can to the second."""
+    """Refuses a call unless every (tensor, shape, type) is a dense tensor of these on the current device, or of more
+    rows. None and raw addresses are not looked at, here and below: the library sees to the first, nobody can to the
+    second."""
     here = _device()
     for t, shape, dtype in specs:
         if t is None or isinstance(t, int):
             continue
-        if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == here:
+        got = t.shape
+        if got == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == here:
             continue
-        if t.shape != shape:
-            _refuse(where, "TS_ERR_SHAPE", f"{tuple(t.shape)} instead of {tuple(shape)}")
+        if len(got) != len(shape) or got[0] < shape[0] or got[1:] != shape[1:]:
+            _refuse(where, "TS_ERR_SHAPE", f"{tuple(got)} instead of {tuple(shape)}")
         if t.dtype is not dtype:
             _refuse(where, "TS_ERR_INVALID_ARG", f"{t.dtype} instead of {dtype}")
-        _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the current device")
+        if t.get_device() != here or not t.is_contiguous():
+            _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the current device")
 
 
 def _rows_of(where, B, *specs):
-    """The same for (tensor, columns, type), with a row for each sequence at least, dense inside a row."""
+    """The same for (tensor, type) with a row for each sequence, rows dense in themselves."""
     here = _device()
-    for t, columns, dtype in specs:
+    for t, dtype in specs:
         if t is None or isinstance(t, int):
             continue
-        if t.dim() != 2 or t.shape[0] < B or t.shape[1] < columns:
-            _refuse(where, "TS_ERR_SHAPE", f"{tuple(t.shape)} instead of {(B, columns)} or more")
+        if t.dim() != 2 or t.shape[0] < B:
+            _refuse(where, "TS_ERR_SHAPE", f"{tuple(t.shape)} instead of {B} rows")
         if t.dtype is not dtype:
             _refuse(where, "TS_ERR_INVALID_ARG", f"{t.dtype} instead of {dtype}")
         if t.stride(1) != 1 or t.get_device() != here:
@@ -428,22 +431,21 @@ class Context:
 
     def _paged(self, where, B, page_table, k_pool, v_pool):
         """Refuses a page table or pools smaller than the context's."""
-        here = _device()
+        here, need = _device(), self._pool_bytes
         try:
-            shape, need = page_table.shape, self._pool_bytes
-            if (shape[0] >= B and shape[1] == self._columns and page_table.dtype is _int32 and page_table.get_device() == here
-                    and page_table.is_contiguous() and k_pool.nbytes >= need and k_pool.get_device() == here and k_pool.is_contiguous()
-                    and v_pool.nbytes >= need and v_pool.get_device() == here and v_pool.is_contiguous() and len(shape) == 2):
-                return                                             # (one test of all, as most calls pass)
-        except (AttributeError, IndexError):                       # None, raw addresses, other shapes
+            rows, columns = page_table.shape                       # (one test of all, as most calls pass it)
+            if (columns == self._columns and rows >= B and page_table.dtype is _int32 and page_table.is_contiguous()
+                    and k_pool.nbytes >= need and v_pool.nbytes >= need and k_pool.is_contiguous() and v_pool.is_contiguous()
+                    and page_table.get_device() == here and k_pool.get_device() == here and v_pool.get_device() == here):
+                return
+        except (AttributeError, TypeError, ValueError):            # None, raw addresses, other shapes
             pass
-        if page_table is not None and not isinstance(page_table, int):
-            _tensors(where, (page_table, (max(B, *page_table.shape[:1]), self._columns), _int32))
+        _tensors(where, (page_table, (B, self._columns), _int32))
         for t in (k_pool, v_pool):
             if t is None or isinstance(t, int):
                 continue
-            if t.nbytes < self._pool_bytes:
-                _refuse(where, "TS_ERR_SHAPE", f"a pool of less than {self._pool_bytes} bytes")
+            if t.nbytes < need:
+                _refuse(where, "TS_ERR_SHAPE", f"a pool of less than {need} bytes")
             if t.get_device() != here or not t.is_contiguous():
                 _refuse(where, "TS_ERR_INVALID_ARG", "a pool is not dense or not on the current device")
 
@@ -452,12 +454,23 @@ class Context:
         """Refuses what a call over a 4-bit cache would read or write beyond, or take for another type."""
         if _device is None:
             _torch()
-        B, shape = q.shape[0], (q.shape[0], *self._q_row)
-        _tensors(where, (q, shape, _float32), (out, shape, _float32), (lse, shape[:2], _float32), (seq_lens, shape[:1], _int32),
-                 (count, shape[:1], _int32))
+        B, H, d = shape = q.shape if q.dim() == 3 else (q.shape[0], *self._q_row)
+        here, row = _device(), self._q_row
+        try:
+            good = (H == row[0] and d == row[1] and q.dtype is _float32 and q.is_contiguous() and q.get_device() == here
+                    and (out is None or out.dtype is _float32 and out.shape == shape and out.is_contiguous()
+                         and out.get_device() == here)
+                    and (seq_lens is None or seq_lens.dtype is _int32 and seq_lens.shape == shape[:1]
+                         and seq_lens.is_contiguous() and seq_lens.get_device() == here))
+        except AttributeError:
+            good = False
+        if not good:
+            _tensors(where, (q, (B, *row), _float32), (out, (B, *row), _float32), (seq_lens, (B,), _int32))
+        if lse is not None or count is not None:
+            _tensors(where, (lse, (B, H), _float32), (count, (B,), _int32))
         self._paged(where, B, page_table, k_pool, k_pool if v_pool is None else v_pool)
-        _rows_of(where, B, (vote, self.max_tokens, _float32), (idx, 1, _int32))
-        here = _device()
+        if vote is not None or idx is not None:
+            _rows_of(where, B, (vote, _float32), (idx, _int32))
         if flags is not None and not isinstance(flags, int):
             if flags.numel() < B or flags.element_size() != 1:
                 _refuse(where, "TS_ERR_SHAPE", f"{tuple(flags.shape)} of {flags.dtype} instead of {(B,)} bytes")
@@ -518,23 +531,19 @@ class Context:
         """k_new / v_new [B][H_kv][d]: the current token's rows into position seq_lens[b] - 1."""
         if _device is None:
             _torch()
-        B, kind, row, here = seq_lens.shape[0], self._rows_dtype(), self._kv_row, _device()
-        try:
-            ks = k_new.shape
-            good = (ks[1:] == row and ks[0] == B and v_new.shape == ks and k_new.dtype is kind and v_new.dtype is kind
-                    and k_new.get_device() == here and v_new.get_device() == here and k_new.is_contiguous() and v_new.is_contiguous())
-        except (AttributeError, IndexError):
-            good = False
-        for t in () if good else (k_new, v_new):
+        B, kind, here = seq_lens.shape[0], self._rows_dtype(), _device()
+        elements = B * self._kv_row[0] * self._kv_row[1]
+        for t in (k_new, v_new):
             if t is None or isinstance(t, int):
                 continue
             # (any view of the rows' bits goes into a pool that holds them as they are)
-            if t.numel() != B * row[0] * row[1] or t.element_size() != kind.itemsize:
-                _refuse("append_kv", "TS_ERR_SHAPE", f"{tuple(t.shape)} of {t.dtype} instead of {(B, *row)} of {kind}")
-            if (self._q4 and t.dtype is not kind) or t.get_device() != here or not t.is_contiguous():
+            if t.numel() < elements or (t.dtype is not kind and t.element_size() != kind.itemsize):
+                _refuse("append_kv", "TS_ERR_SHAPE", f"{tuple(t.shape)} of {t.dtype} instead of {(B, *self._kv_row)} of {kind}")
+            if (t.dtype is not kind and self._q4) or t.get_device() != here or not t.is_contiguous():
                 _refuse("append_kv", "TS_ERR_INVALID_ARG", f"dense rows of {kind} on the current device are wanted")
         if self._q4:
-            _tensors("append_kv", (seq_lens, (B,), _int32))
+            if seq_lens.dtype is not _int32 or seq_lens.get_device() != here or not seq_lens.is_contiguous():
+                _tensors("append_kv", (seq_lens, (B,), _int32))
             self._paged("append_kv", B, page_table, k_pool, v_pool)
         ts_append_kv(self.handle, k_new, v_new, page_table, seq_lens, seq_lens.shape[0], k_pool, v_pool, stream)
 
