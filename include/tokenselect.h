@@ -190,7 +190,8 @@ ts_status ts_sparse_attend(ts_ctx* ctx, const float* q, const void* k_pool, cons
  * else TS_ERR_UNSUPPORTED. A sequence of length 0 gives out = 0 and lse = -inf;
  * a length outside [0, max tokens] records TS_ERR_SEQ_LEN and is taken as 0;
  * the tokens of a page outside the pool are left out and TS_ERR_PAGE_OOB is
- * recorded. Repeated calls give the same bits. */
+ * recorded. 64 elements of a value row that read as NaN make the same elements of
+ * the outputs NaN, and no others. Repeated calls give the same bits. */
 ts_status ts_attend(ts_ctx* ctx, const float* q, const void* k_pool, const void* v_pool, const int32_t* page_table,
                     const int32_t* seq_lens, int B, float scale, float* out, float* lse, void* stream);
 
@@ -213,7 +214,8 @@ ts_status ts_attend(ts_ctx* ctx, const float* q, const void* k_pool, const void*
  * record TS_ERR_SEQ_LEN: nothing is written for a sequence that descends or
  * ends beyond `total`. A row's result depends on no later row, on no other
  * sequence and on no row past the last one, whatever those hold (NaN and
- * infinities too). Repeated calls give the same bits. */
+ * infinities too). An infinite value that a row does see gives it an infinity, or
+ * NaN where its weight is below fp32's range. Repeated calls give the same bits. */
 ts_status ts_prompt_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                            const void* v, int64_t v_stride, const int32_t* cu_rows, int B, int total, float scale,
                            void* out, int64_t out_stride, float* lse, void* stream);

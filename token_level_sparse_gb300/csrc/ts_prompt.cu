@@ -25,6 +25,11 @@
 // need no pass over the scores for a maximum, and the accumulators are rescaled a handful of times per row.
 // The softmax warps do that themselves, in between two products of their tile.
 //
+// A weight enters its product as one bf16 number (the sum takes it unrounded). That is the largest error there is
+// beside the rounding of the outputs: rms 2.0e-3 of the outputs against 1.6e-3 for their rounding alone, with nine
+// ragged prompts. A second bf16 term leaves 1.6e-3, but the tensor cores are what binds: 138 us in place of 98 for
+// those, 7.75 ms in place of 5.40 for 32,771 tokens.
+//
 // Masked places hold what they hold. A score behind the diagonal is replaced before it is used. A
 // value behind the diagonal meets a weight of zero in the product, which is not enough for a NaN or
 // an infinity, so in the tiles on the diagonal (and past the sequence's end, where the next
@@ -35,7 +40,7 @@
 // sequence) and dealt out to the CTAs forth and back, so that they end together.
 //
 // Measured: 32,771 tokens, 32 heads over 8 of 128: 5.3 ms, 1.65 PFLOP/s (the products; power); nine
-// prompts of 7615 tokens together, 28 heads over 4: 97 us, 1.15 PFLOP/s; 48 prompts of 16,437 tokens, 8
+// prompts of 7615 tokens together, 28 heads over 4: 97 us, 1.16 PFLOP/s; 48 prompts of 16,437 tokens, 8
 // heads over 4 of 64: 29 us, where an item has two or three key tiles and what binds is the softmax of a
 // tile (1850 cycles, where one in the middle of a long prompt takes 1100) and an item's outputs (2400
 // cycles). Writing outputs by tiled copies instead of stores, and leaving out weights right

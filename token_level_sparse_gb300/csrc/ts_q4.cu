@@ -26,7 +26,7 @@
 namespace ts {
 namespace {
 
-constexpr int kScorePages = 4;                  // pages of a stage of the score (4 against 2: 79 against 85 us, 783K tokens)
+constexpr int kScorePages = 4;                  // pages of a stage of the score (4 against 2: 79 against 85 us, 898K tokens)
 constexpr int kScanSeqs = 512;                  // sequences whose page counts a scan CTA keeps in shared memory
 constexpr int kQ4Sets = 4;                      // head sets of a CTA, at most
 constexpr int kGatherWarps = 6;
@@ -189,9 +189,10 @@ struct Q4Ring {
 
 // kAttend: attention partials; otherwise logits and (max, sum exp) partials.
 //
-// Measured: attention of four sequences, 924K tokens, 32 heads over 8 of 128: 196 us, 5.1 TB/s of blocks;
-// what binds is instruction issue (about 70% of the slots; the tensor pipe a quarter). Scores of eight
-// sequences, 783K tokens, 28 heads over 4: 77 us, 2.8 TB/s of blocks and 1.1 TB/s of logits; issue 58%, the
+// Measured: attention of four sequences, 954K tokens, 32 heads over 8 of 128: 202 us, 5.1 TB/s of blocks;
+// what binds is instruction issue (72% of the slots; the tensor pipe 27%). 28 heads over 4: 159 us, 3.3 TB/s;
+// a block has twice the products and exponentials, on 12 warps (registers): issue 56%, tensor 35%. Scores of eight
+// sequences, 898K tokens, 28 heads over 4: 74 us, 3.3 TB/s of blocks and 1.4 TB/s of logits; issue 56%, the
 // rest waits for the tensor and integer pipes, which the unpacking and the products take in turn.
 template <int NB, int NT, bool kAttend>
 __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_kernel(const __grid_constant__ Q4Args a) {
@@ -534,8 +535,8 @@ __global__ void __launch_bounds__(1024) q4_merge_kernel(const __grid_constant__ 
 // scan, a CTA takes an even, contiguous share of the batch's pages; for each sequence in it its warps
 // first join the heads' parts (the same in every CTA), then a warp sums a page at a time: lane (head, quad)
 // every eighth head of four tokens, and then across the lanes. The logits of a page lie together, so a load
-// of the warp is 512 contiguous bytes, four of which are under way per page. Measured: 88 MB of logits,
-// 27 us, 3.2 TB/s, half of them out of L2.
+// of the warp is 512 contiguous bytes, four of which are under way per page. Measured: 101 MB of logits,
+// 27 us, 3.7 TB/s, more than half of them out of L2.
 constexpr int kVoteThreads = 512;
 constexpr int kVoteHeads = 256;
 
@@ -632,10 +633,10 @@ struct Q4GatherArgs {
 
 // CTA (split, head set, sequence): a contiguous part of the index list, 16 tokens per warp and step. Bound by
 // a chain of latencies (list, page id, row), so the list is spread over as many CTAs as fit at once and
-// the next step's ids are looked up early: 2564 of 131,057 tokens, 32 heads over 8: 9.0 us, then the merge. Two
-// CTAs of six warps to an SM: with merge, that list takes 9.2 us and one of 20,000 17.3 (four CTAs of four
-// warps: 10.3 and 18.4; two of eight, as far as the registers allow: 9.6 and 16.8, but eight lists of 10,000
-// with 28 heads over 4 58 in place of 47).
+// the next step's ids are looked up early: 2564 of 131,057 tokens, 32 heads over 8: 9.3 us from cold caches, the
+// merge, begun meanwhile, 5.7. Two CTAs of six warps to an SM: over the same inputs again and again, with merge,
+// that list takes 9.2 us and one of 20,000 17.3 (four CTAs of four warps: 10.3 and 18.4; two of eight, as far as
+// the registers allow: 9.6 and 16.8, but eight lists of 10,000 with 28 heads over 4 58 in place of 47).
 template <int NB, int NT>
 __global__ void __launch_bounds__(kGatherWarps * 32, kGatherCtas) gather_kernel(const __grid_constant__ Q4Args a,
                                                                                   const __grid_constant__ Q4GatherArgs ga) {

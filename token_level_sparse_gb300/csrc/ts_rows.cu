@@ -91,7 +91,9 @@ __device__ __forceinline__ void place_rows(const RowsArgs& a, int64_t* place) {
   __syncthreads();
 }
 
-// bf16 and fp32 pools: rows copied as they are, 16 bytes per thread, four under way. Bound by memory.
+// bf16 and fp32 pools: rows copied as they are, 16 bytes per thread, four under way. Bound by memory: 33,122 rows
+// of 8 KV heads of 128, K and V: 50 us, 5.5 TB/s read and written in bf16 (16- and one-token pages alike), 91 us and
+// 6.0 TB/s in fp32.
 __global__ void __launch_bounds__(rows_threads(1)) append_rows_kernel(const __grid_constant__ RowsArgs a, int row_bytes) {
   __shared__ int64_t place[kRowsPerCta];
   place_rows(a, place);
@@ -207,7 +209,8 @@ __global__ void __launch_bounds__(rows_threads(ROWS)) append_q4_kernel(const __g
 // Rows of a pool as fp32 values: exact for every pool type (a code times a bf16 scale has 12
 // significant bits). Eight threads to 64 elements of one row, thread l elements 4l .. 4l + 3 and 32 + 4l .. ,
 // so that each of its two stores fills whole sectors with its neighbours'. Bound by the values written:
-// 33,122 rows of 8 KV heads of 128 from a 4-bit pool, 50 us, 6.1 TB/s.
+// 33,122 rows of 8 KV heads of 128: from a 4-bit pool 48 us, 6.4 TB/s, from a bf16 pool 66 us, 6.2 TB/s, from an
+// fp32 pool 84 us, 6.4 TB/s.
 template <int kType>
 struct RawQuads;                         // the raw elements of one thread
 template <>
