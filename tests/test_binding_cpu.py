@@ -114,6 +114,12 @@ def test_tensors_of_another_shape_or_type_are_refused(context, name):
         if (name, key) != ("append_kv", "seq_lens"):
             with pytest.raises(Reached):
                 call(**(good | {key: _on(torch.cat([good[key], good[key][:1]]))}))
+    if "q" in good:
+        with pytest.raises(Reached):
+            call(**(good | {"q": good["q"].flatten(1)}))
+        for bad in (good["q"].flatten(1)[:, :-1], good["q"].flatten(), good["q"][:, :1], good["q"].transpose(0, 1)):
+            with pytest.raises(T.TokenSelectError):
+                call(**(good | {"q": bad}))
     if "vote" in good:
         with pytest.raises(Reached):
             call(**(good | {"vote": _on(torch.zeros(B, 99))[:, :30]}))

@@ -163,22 +163,20 @@ def _refuse(where, status, why):
 
 
 def _tensors(where, *specs):
-    """Refuses a call unless every (tensor, shape, type) is a dense tensor of these on the current device, or of more
-    rows. None and raw addresses are not looked at, here and below: the library sees to the first, nobody can to the
-    second."""
+    """Refuses a call unless every (tensor, elements, type) is dense, of this type, on the current device and holds as
+    many elements or more. None and raw addresses are not looked at, here and below: the library sees to the first,
+    nobody can to the second."""
     here = _device()
-    for t, shape, dtype in specs:
+    for t, elements, dtype in specs:
         if t is None or isinstance(t, int):
             continue
-        got = t.shape
-        if got == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == here:
+        if t.dtype is dtype and t.numel() >= elements and t.is_contiguous() and t.get_device() == here:
             continue
-        if len(got) != len(shape) or got[0] < shape[0] or got[1:] != shape[1:]:
-            _refuse(where, "TS_ERR_SHAPE", f"{tuple(got)} instead of {tuple(shape)}")
+        if t.numel() < elements:
+            _refuse(where, "TS_ERR_SHAPE", f"{tuple(t.shape)}: less than {elements} elements")
         if t.dtype is not dtype:
             _refuse(where, "TS_ERR_INVALID_ARG", f"{t.dtype} instead of {dtype}")
-        if t.get_device() != here or not t.is_contiguous():
-            _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the current device")
+        _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the current device")
 
 
 def _rows_of(where, B, *specs):
@@ -422,12 +420,12 @@ class Context:
         self.max_tokens = max_pages_per_seq * page_size
         # what the packed calls compare their tensors with
         self._q_row, self._kv_row = (n_q_heads, head_dim), (n_kv_heads, head_dim)
-        self._q4 = kv_dtype == TS_KV_Q4
+        self._q4, self._f32 = kv_dtype == TS_KV_Q4, kv_dtype == TS_KV_F32
         self._pool_bytes, self._columns = num_pages * ts_page_bytes(self.cfg), max_pages_per_seq
 
     def _rows_dtype(self):
         """Element type of the rows that go into the pools."""
-        return _float32 if self.cfg.kv_dtype == TS_KV_F32 else _bfloat16
+        return _float32 if self._f32 else _bfloat16
 
     def _paged(self, where, B, page_table, k_pool, v_pool):
         """Refuses a page table or pools smaller than the context's."""
@@ -440,7 +438,10 @@ class Context:
                 return
         except (AttributeError, TypeError, ValueError):            # None, raw addresses, other shapes
             pass
-        _tensors(where, (page_table, (B, self._columns), _int32))
+        if page_table is not None and not isinstance(page_table, int):
+            if page_table.dim() != 2 or page_table.shape[1] != self._columns:
+                _refuse(where, "TS_ERR_SHAPE", f"{tuple(page_table.shape)} instead of {(B, self._columns)}")
+            _tensors(where, (page_table, B * self._columns, _int32))
         for t in (k_pool, v_pool):
             if t is None or isinstance(t, int):
                 continue
@@ -454,20 +455,12 @@ class Context:
         """Refuses what a call over a 4-bit cache would read or write beyond, or take for another type."""
         if _device is None:
             _torch()
-        B, H, d = shape = q.shape if q.dim() == 3 else (q.shape[0], *self._q_row)
-        here, row = _device(), self._q_row
-        try:
-            good = (H == row[0] and d == row[1] and q.dtype is _float32 and q.is_contiguous() and q.get_device() == here
-                    and (out is None or out.dtype is _float32 and out.shape == shape and out.is_contiguous()
-                         and out.get_device() == here)
-                    and (seq_lens is None or seq_lens.dtype is _int32 and seq_lens.shape == shape[:1]
-                         and seq_lens.is_contiguous() and seq_lens.get_device() == here))
-        except AttributeError:
-            good = False
-        if not good:
-            _tensors(where, (q, (B, *row), _float32), (out, (B, *row), _float32), (seq_lens, (B,), _int32))
-        if lse is not None or count is not None:
-            _tensors(where, (lse, (B, H), _float32), (count, (B,), _int32))
+        B, here = q.shape[0], _device()
+        n = B * self._q_row[0] * self._q_row[1]
+        if q.numel() != n:
+            _refuse(where, "TS_ERR_SHAPE", f"{tuple(q.shape)} instead of {(B, *self._q_row)}")
+        _tensors(where, (q, n, _float32), (out, n, _float32), (seq_lens, B, _int32), (lse, B * self._q_row[0], _float32),
+                 (count, B, _int32))
         self._paged(where, B, page_table, k_pool, k_pool if v_pool is None else v_pool)
         if vote is not None or idx is not None:
             _rows_of(where, B, (vote, _float32), (idx, _int32))
@@ -542,8 +535,7 @@ class Context:
             if (t.dtype is not kind and self._q4) or t.get_device() != here or not t.is_contiguous():
                 _refuse("append_kv", "TS_ERR_INVALID_ARG", f"dense rows of {kind} on the current device are wanted")
         if self._q4:
-            if seq_lens.dtype is not _int32 or seq_lens.get_device() != here or not seq_lens.is_contiguous():
-                _tensors("append_kv", (seq_lens, (B,), _int32))
+            _tensors("append_kv", (seq_lens, B, _int32))
             self._paged("append_kv", B, page_table, k_pool, v_pool)
         ts_append_kv(self.handle, k_new, v_new, page_table, seq_lens, seq_lens.shape[0], k_pool, v_pool, stream)
 
