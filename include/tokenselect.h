@@ -207,7 +207,9 @@ ts_status ts_attend(ts_ctx* ctx, const float* q, const void* k_pool, const void*
  * multiples of 8 and at least the row. out bf16 [total][H][d] with out_stride
  * likewise; lse fp32 [total][H]. Rows of out and lse from cu_rows[B] on are left
  * as they are. Scores, sums and outputs accumulate in fp32; the softmax weights
- * are rounded to bf16 for their product with v, the outputs once at the end. No
+ * are rounded to bf16 for their product with v, the outputs once at the end (a
+ * row's weights sum to 2^37 at most before they are divided, so values below 2^90
+ * never pass fp32). No
  * cache is read or written: the context gives the head geometry (d 64 or 128,
  * G <= 16, bf16 or 4-bit pools, else TS_ERR_UNSUPPORTED), B <= max_batch, and a
  * prompt may be longer than its max tokens. Boundaries that are not as above

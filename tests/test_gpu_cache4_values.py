@@ -267,3 +267,13 @@ def test_from_prompts_to_decode_steps_within_each_operator_s_tolerance(H, Hkv, d
             _check(c, o, z, b, got)
             _check(c, full, fullz, b, np.arange(n))
     assert hits == B
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 4, 64), (28, 4, 128)])
+@pytest.mark.parametrize("n", [1, 40, 3000])
+def test_values_at_the_end_of_fp32_s_range(H, Hkv, d, n):
+    # every value is near 3e38: the outputs are finite, the sums of weights times values are not
+    c = Cache(H, Hkv, d, [n], seed=11)
+    _write(c, v=(3e38 * (1 - 0.1 * torch.rand(n, Hkv, d, device=DEV))).to(torch.bfloat16))
+    for out, lse in _both(c, n):
+        _check(c, out, lse, 0, np.arange(n))

@@ -51,7 +51,7 @@ struct Q4Args {
   float scale;                   // base 2 (times log2 e), but natural for the scores that no softmax follows
   float* logits;                 // score, in units of scale: H max_tokens to a sequence, head h of token i at
   int64_t head_stride, page_stride;   // h head_stride + i / 16 page_stride + i % 16
-  float* part_o;                 // [slot][H][d]
+  float* part_o;                 // [slot][H][d]: a part's own outputs, divided by its sum
   float2* part_ml;               // [H][slots]: max and sum of 2^(x - max)
   int64_t slots;
   int* status;
@@ -67,6 +67,10 @@ __device__ __forceinline__ int seq_pages(const Q4Args& a, int b) {
   const int n = a.seq_lens[b];
   return (n < 0 || n > a.max_tokens) ? 0 : (n + kPage - 1) / kPage;
 }
+
+// Outputs are divided by their sums in every join, before they are added up: sums of weights times values may pass
+// fp32 where the values themselves do not. (No token: a sum and outputs of zero.)
+__device__ __forceinline__ float reciprocal(float sum) { return sum != 0.f ? 1.f / sum : 0.f; }
 
 // Weight of a part with maximum m in a join with maximum M. Equal maxima weigh 1 also where both are
 // -inf: an empty part brings zeros, a part of NaN logits brings its NaN.
@@ -433,13 +437,13 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
         const float2 ml = s_ml[hs * per_set + w][4 * nt + t];
         L += ml.y * part_weight(ml.x, M);
       }
-      fac[nt] = part_weight(st.m[nt], M);
+      fac[nt] = part_weight(st.m[nt], M) * reciprocal(L);
       if (works && j == 0 && g == 0 && 4 * nt + t < nh)
         a.part_ml[(int64_t)(head0 + 4 * nt + t) * a.slots + cta + b] = make_float2(M, L);
     }
     if constexpr (kAttend) {
       st.flush(sums, s_units[warp], done < kQ4Flush, lane);
-      // each warp's own factors: from its maximum to the set's, and out of its powers of two
+      // each warp's own factors: from its maximum to the set's and divided by the sum, and out of its powers of two
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         if (g == 0) {
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(Q4Ring<NB, NT, kAttend>::WARPS * 32, 1) scan_k
           float acc = 0.f;
           for (int w = 0; w < per_set; ++w) {
             const Q4Unit<NB>& f = s_units[hs * per_set + w][i / D];
-            acc = fmaf(rows[w * (4 * NT * D) + i] * f.sc[i % D / 64], f.m, acc);
+            acc = fmaf(rows[w * (4 * NT * D) + i] * f.m, f.sc[i % D / 64], acc);
           }
           po[i] = acc;
         }
@@ -486,11 +490,11 @@ __device__ __forceinline__ void scan_slots(const Q4Args& a, int b, int lane, Pag
 }
 
 // Joins the parts of (head, sequence) in slot order. splits > 0: the gather's parts, splits per
-// sequence; otherwise the scan's. A chain of two dependent loads; eight parts per thread are under way at
-// once (7 us for 38 parts of 32 heads in four sequences, begun while the scan ends).
+// sequence; otherwise the scan's. Bound by the latency of its loads, all of which a thread has under way at
+// once up to eight parts (7 us for 38 parts of 32 heads in four sequences, begun while the scan ends).
 constexpr int kMaxParts = 512;   // of one sequence
 template <int D>
-__global__ void __launch_bounds__(1024) q4_merge_kernel(const __grid_constant__ Q4Args a, int splits, float* out,
+__global__ void __launch_bounds__(1024, 1) q4_merge_kernel(const __grid_constant__ Q4Args a, int splits, float* out,
                                                         float* lse) {
   constexpr int ROWS = 1024 / D;   // parts added at once
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, e = tid % D, row = tid / D;
@@ -505,30 +509,43 @@ __global__ void __launch_bounds__(1024) q4_merge_kernel(const __grid_constant__ 
     scan_slots(a, b, tid & 31, [&](int i) { return seq_pages(a, i); }, first, count);
   }
   wait_for_primary();
-  for (int i = tid; i < count; i += blockDim.x) s_ml[i] = __ldcg(a.part_ml + h * a.slots + first + i);
-  __syncthreads();
-  float M = -INFINITY;
-  for (int i = 0; i < count; ++i) M = fmaxf(M, s_ml[i].x);
-  float o = 0.f;
+  // the outputs of a thread's first parts are on their way while the sums are joined
+  constexpr int BATCH = 8;
   const float* po = a.part_o + (first * a.H + h) * D + e;
-  for (int i0 = row; i0 < count; i0 += 8 * ROWS) {                 // eight loads under way at once
-    float x[8];
+  float x[BATCH];
+  auto load = [&](int i0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = i0 + k * ROWS < count ? __ldcg(po + (size_t)(i0 + k * ROWS) * a.H * D) : 0.f;
+    for (int k = 0; k < BATCH; ++k) x[k] = i0 + k * ROWS < count ? __ldcg(po + (size_t)(i0 + k * ROWS) * a.H * D) : 0.f;
+  };
+  for (int i = tid; i < count; i += blockDim.x) s_ml[i] = __ldcg(a.part_ml + h * a.slots + first + i);
+  load(row);
+  __syncthreads();
+  // every warp the same maximum and sum
+  float M = -INFINITY, L = 0.f;
+  for (int i = tid & 31; i < count; i += 32) M = fmaxf(M, s_ml[i].x);
+  M = warp_max(M);
+  for (int i = tid & 31; i < count; i += 32) L = fmaf(part_weight(s_ml[i].x, M), s_ml[i].y, L);
+  L = warp_sum(L);
+  const float inv = reciprocal(L);
+  float o = 0.f;
+  for (int i0 = row; i0 < count; i0 += BATCH * ROWS) {
+    if (i0 != row) load(i0);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + k * ROWS < count) o = fmaf(part_weight(s_ml[i0 + k * ROWS].x, M), x[k], o);
+    for (int k = 0; k < BATCH; ++k)
+      if (i0 + k * ROWS < count) {
+        const float2 ml = s_ml[i0 + k * ROWS];
+        o = fmaf(part_weight(ml.x, M) * ml.y * inv, x[k], o);
+      }
   }
   s_o[row][e] = o;
   __syncthreads();
   if (row != 0) return;
-  float O = 0.f, L = 0.f;
+  float O = 0.f;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) O += s_o[i][e];
-  for (int i = 0; i < count; ++i) L = fmaf(part_weight(s_ml[i].x, M), s_ml[i].y, L);
-  const bool some = L != 0.f;   // true for NaN: a NaN among the rows is not an empty sequence
-  out[((size_t)b * a.H + h) * D + e] = some ? O / L : 0.f;
-  if (lse && e == 0) lse[(size_t)b * a.H + h] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  out[((size_t)b * a.H + h) * D + e] = O;
+  // (a sum of NaN, of a NaN among the rows, is not an empty sequence)
+  if (lse && e == 0) lse[(size_t)b * a.H + h] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 // The head soft vote from the scan's base-2 logits and parts: v_i = sum_h 2^(l_hi - M_h) / Z_h. Like the
@@ -730,19 +747,25 @@ __global__ void __launch_bounds__(kGatherWarps * 32, kGatherCtas) gather_kernel(
   st.flush(&merge[warp][0][0], s_units[warp], !flushed, lane);
   __syncthreads();
   const int64_t slot = (int64_t)b * ga.splits + split;
+  // a thread to each (warp, head): the warp's factor in the head's part
+  if (tid < kGatherWarps * 4 * NT) {
+    const int w = tid / (4 * NT), hg = tid % (4 * NT);
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kGatherWarps; ++i) M = fmaxf(M, s_ml[i][hg].x);
+#pragma unroll
+    for (int i = 0; i < kGatherWarps; ++i) L = fmaf(part_weight(s_ml[i][hg].x, M), s_ml[i][hg].y, L);
+    s_units[w][hg].m = part_weight(s_ml[w][hg].x, M) * reciprocal(L);
+    if (w == 0 && hg < nh) a.part_ml[(head0 + hg) * a.slots + slot] = make_float2(M, L);
+  }
+  __syncthreads();
   for (int i = tid; i < nh * D; i += kGatherWarps * 32) {
     const int hg = i / D;
-    float M = -INFINITY, L = 0.f, O = 0.f;
+    float O = 0.f;
 #pragma unroll
-    for (int w = 0; w < kGatherWarps; ++w) M = fmaxf(M, s_ml[w][hg].x);
-#pragma unroll
-    for (int w = 0; w < kGatherWarps; ++w) {
-      const float wt = part_weight(s_ml[w][hg].x, M);
-      L = fmaf(wt, s_ml[w][hg].y, L);
-      O = fmaf(wt, merge[w][hg][i % D] * __uint_as_float((254u << 23) - __float_as_uint(s_units[w][hg].sc[i % D / 64])), O);
-    }
+    for (int w = 0; w < kGatherWarps; ++w)
+      O = fmaf(merge[w][hg][i % D] * s_units[w][hg].m, __uint_as_float((254u << 23) - __float_as_uint(s_units[w][hg].sc[i % D / 64])), O);
     a.part_o[(slot * a.H + head0) * D + i] = O;
-    if (i % D == 0) a.part_ml[(head0 + hg) * a.slots + slot] = make_float2(M, L);
   }
 }
 
