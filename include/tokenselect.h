@@ -209,12 +209,11 @@ ts_status ts_attend(ts_ctx* ctx, const float* q, const void* k_pool, const void*
  * as they are. Scores, sums and outputs accumulate in fp32; the softmax weights
  * are rounded to bf16 for their product with v, the outputs once at the end (a
  * row's weights sum to 2^37 at most before they are divided, so values below 2^90
- * never pass fp32). No
- * cache is read or written: the context gives the head geometry (d 64 or 128,
- * G <= 16, bf16 or 4-bit pools, else TS_ERR_UNSUPPORTED), B <= max_batch, and a
- * prompt may be longer than its max tokens. Boundaries that are not as above
- * record TS_ERR_SEQ_LEN: nothing is written for a sequence that descends or
- * ends beyond `total`. A row's result depends on no later row, on no other
+ * never pass fp32). No cache is read or written: the context gives the head
+ * geometry (d 64 or 128, G <= 16, bf16 or 4-bit pools, else TS_ERR_UNSUPPORTED),
+ * B <= max_batch, and a prompt may be longer than its max tokens. Boundaries that
+ * are not as above record TS_ERR_SEQ_LEN: nothing is written for a sequence that
+ * descends or ends beyond `total`. A row's result depends on no later row, on no other
  * sequence and on no row past the last one, whatever those hold (NaN and
  * infinities too). An infinite value that a row does see gives it an infinity, or
  * NaN where its weight is below fp32's range. Repeated calls give the same bits. */
