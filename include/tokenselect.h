@@ -57,6 +57,7 @@ extern "C" {
 
 typedef struct ts_ctx ts_ctx;     /* opaque; library-owned */
 typedef struct ts_cache ts_cache; /* opaque; library-owned */
+typedef struct ts_rope ts_rope;   /* opaque; library-owned, host memory only */
 
 typedef enum {
   TS_OK = 0,
@@ -312,6 +313,113 @@ ts_status ts_append_prompt(ts_ctx* ctx, const void* k, int64_t k_stride, const v
 ts_status ts_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* starts, int B, int total,
                      const int32_t* page_table, const void* k_pool, const void* v_pool, float* k_out,
                      float* v_out, void* stream);
+
+/* Rotary positions. A head's first rot_dim elements are turned in pairs, (i, i + rot_dim/2) or, interleaved, (2i,
+ * 2i + 1):  y1 = a (x1 cos t - x2 sin t), y2 = a (x2 cos t + x1 sin t), t = position * f_i; the others pass as they
+ * are. f_i = base^(-2i/rot_dim) radians per position, then by `scaling` (with n = original, lengths in positions):
+ *  PLAIN   f_i;
+ *  LINEAR  f_i / factor;
+ *  BASE    base * factor^(rot_dim/(rot_dim - 2)) in place of base;
+ *  BANDS   t f_i + (1 - t) f_i / factor, t = (n f_i / 2pi - low) / (high - low) held to [0, 1]: pairs that turn more
+ *          than `high` times within n positions keep their frequency, those below `low` turns are scaled;
+ *  YARN    t f_i / factor + (1 - t) f_i, t = (i - i_high) / (i_low - i_high) held to [0, 1], where i_x is the pair
+ *          that turns x times within n positions, i_high rounded down and at least 0, i_low rounded up and at most
+ *          rot_dim - 1 (their difference at least 0.001); a = 0.1 ln(factor) + 1 for a factor above 1;
+ *  GIVEN   freqs[rot_dim/2] (host memory, read by ts_rope_create).
+ * a = attention where that is not 0, else 1 unless the rule names one. Angles are exact modulo a turn to 2^-32 of
+ * it plus what `position` makes of the last bit of f_i / 2pi in fp64, for every int32 position, negative ones too. */
+enum { TS_ROPE_PLAIN = 0, TS_ROPE_LINEAR = 1, TS_ROPE_BASE = 2, TS_ROPE_BANDS = 3, TS_ROPE_YARN = 4, TS_ROPE_GIVEN = 5 };
+typedef struct {
+  int rot_dim;            /* even, 2 to 128, at most the context's head_dim      */
+  int interleaved;        /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1)  */
+  int scaling;            /* TS_ROPE_*                                          */
+  double base;            /* > 0                                                */
+  double factor;          /* > 0; not read for PLAIN and GIVEN                  */
+  int original;           /* context that the model was made for: BANDS, YARN   */
+  double low, high;       /* turns within it, 0 < low < high: BANDS, YARN       */
+  double attention;       /* factor of what is turned; 0: by the rule           */
+  const double* freqs;    /* GIVEN, else NULL                                   */
+} ts_rope_config;
+/* Works out the frequencies on the host (no device memory: a handle serves every context and device). */
+ts_status ts_rope_create(ts_rope** out, const ts_rope_config* cfg);
+ts_status ts_rope_destroy(ts_rope* rope);
+/* The handle's frequencies (rot_dim/2 of them, radians per position) and its factor a. */
+ts_status ts_rope_read(const ts_rope* rope, double* freqs, double* attention);
+
+/* Turns rows of heads by their positions: x and out [total][heads][d] (d the context's head_dim), dense inside a row,
+ * x_stride and out_stride elements from row to row, each of type TS_KV_F32 or TS_KV_BF16; positions int32 [total] on
+ * the device. Rows 16-byte aligned. Computed in fp32 and rounded once. out may be x where type and stride are the
+ * same; otherwise they must not share memory. With the positions negated the call is its own transpose: the gradient
+ * of x from that of out (and, where a is 1, the inverse). The context gives d and the device. */
+ts_status ts_rotate(ts_ctx* ctx, const ts_rope* rope, const void* x, int64_t x_stride, int dtype, int heads,
+                    const int32_t* positions, int total, void* out, int64_t out_stride, int out_dtype, void* stream);
+
+/* ts_append_prompt with K rows turned on their way, exactly as ts_rotate (rounded to the rows' type, then quantised
+ * for a 4-bit pool) and then ts_append_prompt would write them. Row r is turned by positions[r], which need not be
+ * its place in the cache (drafts of one depth share a position). q and q_out NULL, or: the queries of the same rows,
+ * q [total][H][d] of the rows' type with q_stride, are turned too, into q_out [total][H][d] of type q_out_dtype
+ * (TS_KV_F32 for ts_decode_step and its kin, TS_KV_BF16 for ts_tree_attend) with q_out_stride; q_out may be q as in
+ * ts_rotate. All `total` rows of q are turned, whether their K and V rows have a place or not. */
+ts_status ts_append_rotated(ts_ctx* ctx, const ts_rope* rope, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, const int32_t* positions, const int32_t* cu_rows, const int32_t* starts,
+                            int B, int total, const int32_t* page_table, void* k_pool, void* v_pool, const void* q,
+                            int64_t q_stride, void* q_out, int64_t q_out_stride, int q_out_dtype, void* stream);
+
+/* Attention of drafted tokens over the whole cache. Packed rows cu_rows[b] .. cu_rows[b + 1] - 1 (cu_rows as in
+ * ts_prompt_attend) are the queries of the last T_b = cu_rows[b + 1] - cu_rows[b] cached tokens of sequence b, which
+ * are appended already: seq_lens[b] counts them. Row i of a sequence sees all tokens before seq_lens[b] - T_b, and of
+ * the T_b drafts those j whose bit is set in its mask: mask int32 [total][mask_words] on the device, bit j % 32 of
+ * word j / 32 (a tree: a row's own bit and its ancestors'; any set of bits is served, the row's own not implied).
+ * mask NULL: the drafts j <= i, a chain. q bf16 [total][H][d] with q_stride, out bf16 [total][H][d] with out_stride,
+ * lse fp32 [total][H] or NULL, alignment as in ts_prompt_attend. A row that sees nothing gives out = 0 and
+ * lse = -inf. T_b may be 0; T_b above 1024, above 32 mask_words or above seq_lens[b], a length above the maximum, or
+ * boundaries that are not ascending record TS_ERR_SEQ_LEN, and nothing is written for that sequence; the tokens of a
+ * page outside the pool are left out and TS_ERR_PAGE_OOB is recorded. bf16 pools with d 64 or 128 and at most 16
+ * query heads per KV head, else TS_ERR_UNSUPPORTED. Scores, sums and outputs accumulate in fp32; softmax weights are
+ * rounded to bf16 for their product with v, outputs once at the end. A row's result depends on no draft that it does
+ * not see and on nothing behind its sequence, whatever those hold (NaN and infinities too); rows of out and lse from
+ * cu_rows[B] on are left as they are. Repeated calls give the same bits. */
+ts_status ts_tree_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
+                         const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_rows, const int32_t* mask,
+                         int mask_words, int B, int total, float scale, void* out, int64_t out_stride, float* lse,
+                         void* stream);
+
+/* Which drafted tokens the target keeps, and the token behind them. Node 0 of a sequence's rows is the root, the last
+ * token that is certain (its entries of tokens, parents and u are not read); node i > 0 holds the drafted token
+ * tokens[r] behind node parents[r] < i (numbers within the sequence). target fp32 [total][vocab], target_stride
+ * elements from row to row: the target's probabilities behind each node; draft likewise: those that the node's
+ * children were drawn from, or NULL for drafts without probabilities. u fp32 [total] and u_next fp32 [B]: numbers
+ * from [0, 1). From the root on, the children of the current node are tried in ascending order:
+ *   with p and q the node's rows, c = 0, Z = 1, W = 1:  child x is taken iff u q(x) Z < max(p(x) - c q(x), 0) W;
+ *   otherwise c += Z / W (where W > 0), Z = sum_i max(p(i) - c q(i), 0), and W -= q(x) if `distinct`
+ * (distinct != 0: siblings were drawn without replacement, each from what its elder siblings left of q; 0: each
+ * from q). draft NULL: x is taken iff u Z < p(x), otherwise Z -= p(x) and p(x) = 0. A child that is taken becomes the
+ * current node; with none left next_token[b] is drawn from the residual r = max(p - c q, 0): the smallest i with
+ * sum_{j <= i} r(j) > u_next[b] sum r (the last i with r(i) > 0 where rounding leaves none), from p where r is zero
+ * throughout, -1 where p is too. Tokens so drawn are distributed as the target's. Entries that are NaN or negative
+ * count as 0. Sums and tests carry 2^-45 and better.
+ * path int32 [B][path_stride] receives the taken nodes in order, node 0 first, then -1; count int32 [B] how many.
+ * More than path_stride record TS_ERR_CAPACITY (the first ones are written, count is the whole number). At most 1024
+ * nodes per sequence; more, or boundaries that are not ascending, record TS_ERR_SEQ_LEN, count 0 and -1 (so does a
+ * sequence without rows, without an error). A token outside [0, vocab) or a parent outside [0, i) records
+ * TS_ERR_INVALID_ARG, and that node is passed over. vocab <= 2^20. The outputs must not share memory with the
+ * inputs. The context gives max_batch, the device and the status word. */
+ts_status ts_verify_tree(ts_ctx* ctx, const int32_t* tokens, const int32_t* parents, const int32_t* cu_rows, int B,
+                         int total, int vocab, const float* target, int64_t target_stride, const float* draft,
+                         int64_t draft_stride, const float* u, const float* u_next, int distinct, int32_t* path,
+                         int64_t path_stride, int32_t* count, int32_t* next_token, void* stream);
+
+/* Keeps the K and V rows of a path of drafts: of the last T_b = cu_rows[b + 1] - cu_rows[b] cached tokens (seq_lens[b]
+ * counts them), row path[b][j] moves to row j for j < count[b], so that the path follows the certain tokens without a
+ * gap. path and count as ts_verify_tree writes them: ascending within [0, T_b), count[b] in [0, min(T_b, path_stride)].
+ * new_lens int32 [B] or NULL receives seq_lens[b] - T_b + count[b]; it must not share memory with seq_lens. Every
+ * pool type, values move as they are. n_layers pools each, layer_bytes from one to the next (a multiple of 16, at
+ * least a pool; not read for one). A path that is not as above records TS_ERR_INVALID_ARG, a count above path_stride
+ * TS_ERR_CAPACITY, boundaries or lengths that are not as in ts_tree_attend TS_ERR_SEQ_LEN: nothing moves for that
+ * sequence and its length stays. A row with a page outside the pool records TS_ERR_PAGE_OOB and does not move. */
+ts_status ts_keep_rows(ts_ctx* ctx, const int32_t* path, int64_t path_stride, const int32_t* count, const int32_t* cu_rows,
+                       const int32_t* seq_lens, int B, int total, const int32_t* page_table, void* k_pool, void* v_pool,
+                       int n_layers, int64_t layer_bytes, int32_t* new_lens, void* stream);
 
 /* Block-level selection, the granularity the method argues against
  * (TokenSelect review, figure 2(b): InfLLM-style methods keep or drop whole

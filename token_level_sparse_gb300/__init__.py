@@ -20,7 +20,8 @@ __all__ = [
     "TS_KV_F32", "TS_KV_BF16", "TS_KV_Q4", "TS_SELECT_TOPK", "TS_SELECT_TOPP", "STATUS",
     "TS_SCORE_HEAD_SOFT_VOTE", "TS_SCORE_LOGIT_SUM", "TS_SCORE_HEAD_HARD_VOTE", "ts_score_fn",
     "ts_prefill_chunk", "ts_select_blocks", "ts_append_kv", "ts_append_prompt", "ts_read_kv", "ts_attend",
-    "ts_prompt_attend", "ts_page_bytes",
+    "ts_prompt_attend", "ts_page_bytes", "RopeConfig", "Rope", "ROPE_SCALING", "ts_rope_create", "ts_rope_destroy",
+    "ts_rope_read", "ts_rotate", "ts_append_rotated", "ts_tree_attend", "ts_verify_tree", "ts_keep_rows",
     "ts_create", "ts_destroy", "ts_cache_create", "ts_cache_destroy", "ts_cache_reset",
     "ts_cache_check", "ts_score", "ts_select", "ts_sparse_attend", "ts_decode_step",
     "ts_get_status", "ts_status_str", "ts_version", "ts_profile_enable", "ts_profile_read",
@@ -51,6 +52,15 @@ class Config(ctypes.Structure):
     _fields_ = [("n_q_heads", c_int), ("n_kv_heads", c_int), ("head_dim", c_int),
                 ("page_size", c_int), ("kv_dtype", c_int), ("max_batch", c_int),
                 ("max_pages_per_seq", c_int), ("num_pages", c_int64)]
+
+
+ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "yarn": 4, "given": 5}
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", c_int), ("interleaved", c_int), ("scaling", c_int), ("base", c_double), ("factor", c_double),
+                ("original", c_int), ("low", c_double), ("high", c_double), ("attention", c_double),
+                ("freqs", POINTER(c_double))]
 
 
 class Profile(ctypes.Structure):
@@ -103,6 +113,20 @@ _SIGS = {
     "ts_prompt_attend": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int,
                                  c_int, c_float, c_void_p, c_int64, c_void_p, c_void_p]),
     "ts_page_bytes": (c_int64, [POINTER(Config)]),
+    "ts_rope_create": (c_int, [POINTER(c_void_p), POINTER(RopeConfig)]),
+    "ts_rope_destroy": (c_int, [c_void_p]),
+    "ts_rope_read": (c_int, [c_void_p, POINTER(c_double), POINTER(c_double)]),
+    "ts_rotate": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_void_p, c_int, c_void_p, c_int64, c_int,
+                          c_void_p]),
+    "ts_append_rotated": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                                  c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_int,
+                                  c_void_p]),
+    "ts_tree_attend": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                               c_int, c_int, c_int, c_float, c_void_p, c_int64, c_void_p, c_void_p]),
+    "ts_verify_tree": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_int64, c_void_p,
+                               c_int64, c_void_p, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_void_p, c_void_p]),
+    "ts_keep_rows": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p,
+                             c_void_p, c_int, c_int64, c_void_p, c_void_p]),
     "ts_set_wait_limit": (c_int, [c_void_p, ctypes.c_uint64]),
     "ts_inject_barrier_skip": (c_int, [c_void_p, c_int, c_int]),
     "ts_profile_enable": (c_int, [c_void_p, c_int]),
@@ -370,6 +394,56 @@ def ts_prompt_attend(ctx, q, q_stride, k, k_stride, v, v_stride, cu_rows, B, tot
                                       scale, _p(out), out_stride, _p(lse), _s(stream)), "ts_prompt_attend")
 
 
+def ts_rope_create(cfg: RopeConfig) -> int:
+    h = c_void_p()
+    _check(library().ts_rope_create(ctypes.byref(h), ctypes.byref(cfg)), "ts_rope_create")
+    return h.value
+
+
+def ts_rope_destroy(rope: int) -> None:
+    _check(library().ts_rope_destroy(rope), "ts_rope_destroy")
+
+
+def ts_rope_read(rope: int, pairs: int):
+    """(frequencies of the pairs in radians per position, factor of what is turned)."""
+    f, a = (c_double * pairs)(), c_double()
+    _check(library().ts_rope_read(rope, f, ctypes.byref(a)), "ts_rope_read")
+    return list(f), a.value
+
+
+def ts_rotate(ctx, rope, x, x_stride, dtype, heads, positions, total, out, out_stride, out_dtype, stream=None) -> None:
+    _check(library().ts_rotate(ctx, rope, _p(x), x_stride, dtype, heads, _p(positions), total, _p(out), out_stride,
+                               out_dtype, _s(stream)), "ts_rotate")
+
+
+def ts_append_rotated(ctx, rope, k, k_stride, v, v_stride, positions, cu_rows, starts, B, total, page_table, k_pool,
+                      v_pool, q=None, q_stride=0, q_out=None, q_out_stride=0, q_out_dtype=0, stream=None) -> None:
+    _check(library().ts_append_rotated(ctx, rope, _p(k), k_stride, _p(v), v_stride, _p(positions), _p(cu_rows), _p(starts),
+                                       B, total, _p(page_table), _p(k_pool), _p(v_pool), _p(q), q_stride, _p(q_out),
+                                       q_out_stride, q_out_dtype, _s(stream)), "ts_append_rotated")
+
+
+def ts_tree_attend(ctx, q, q_stride, k_pool, v_pool, page_table, seq_lens, cu_rows, mask, mask_words, B, total, scale, out,
+                   out_stride, lse=None, stream=None) -> None:
+    _check(library().ts_tree_attend(ctx, _p(q), q_stride, _p(k_pool), _p(v_pool), _p(page_table), _p(seq_lens), _p(cu_rows),
+                                    _p(mask), mask_words, B, total, scale, _p(out), out_stride, _p(lse), _s(stream)),
+           "ts_tree_attend")
+
+
+def ts_verify_tree(ctx, tokens, parents, cu_rows, B, total, vocab, target, target_stride, draft, draft_stride, u, u_next,
+                   distinct, path, path_stride, count, next_token, stream=None) -> None:
+    _check(library().ts_verify_tree(ctx, _p(tokens), _p(parents), _p(cu_rows), B, total, vocab, _p(target), target_stride,
+                                    _p(draft), draft_stride, _p(u), _p(u_next), distinct, _p(path), path_stride, _p(count),
+                                    _p(next_token), _s(stream)), "ts_verify_tree")
+
+
+def ts_keep_rows(ctx, path, path_stride, count, cu_rows, seq_lens, B, total, page_table, k_pool, v_pool, n_layers=1,
+                 layer_bytes=0, new_lens=None, stream=None) -> None:
+    _check(library().ts_keep_rows(ctx, _p(path), path_stride, _p(count), _p(cu_rows), _p(seq_lens), B, total,
+                                  _p(page_table), _p(k_pool), _p(v_pool), n_layers, layer_bytes, _p(new_lens),
+                                  _s(stream)), "ts_keep_rows")
+
+
 def ts_page_bytes(cfg: Config) -> int:
     """Bytes of one page of a K pool (or a V pool), all KV heads."""
     return library().ts_page_bytes(ctypes.byref(cfg))
@@ -595,12 +669,168 @@ class Context:
                          _row_stride(v, total, row), cu_rows, cu_rows.shape[0] - 1, total, scale, out,
                          _row_stride(out, total, self._q_row), lse, stream)
 
+    def rope(self, rot_dim=None, **kw):
+        """A Rope for this context's heads (all of each head turned where rot_dim is not given)."""
+        return Rope(self.cfg.head_dim if rot_dim is None else rot_dim, **kw)
+
+    def _heads(self, where, x, heads, total, here):
+        """Refuses a packed [total][heads][d] tensor of another shape, type or device; its row stride and type."""
+        if x.dim() != 3 or x.shape[2] != self.cfg.head_dim or (heads and x.shape[1] != heads) or x.shape[0] != total:
+            _refuse(where, "TS_ERR_SHAPE", f"{tuple(x.shape)} instead of {(total, heads or 'heads', self.cfg.head_dim)}")
+        kind = x.dtype
+        if kind is not _bfloat16 and kind is not _float32:
+            _refuse(where, "TS_ERR_INVALID_ARG", f"{kind} instead of bfloat16 or float32")
+        if x.get_device() != here:
+            _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not on the current device")
+        return _row_stride(x, total, x.shape[1:]), TS_KV_F32 if kind is _float32 else TS_KV_BF16
+
+    @staticmethod
+    def _counted(where, here, *specs):
+        """Refuses every (tensor, shape, type) that is not dense, of exactly this shape and type, on the current device."""
+        for t, shape, dtype in specs:
+            if t is None:
+                continue
+            if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == here:
+                continue
+            if t.shape != shape:
+                _refuse(where, "TS_ERR_SHAPE", f"{tuple(t.shape)} instead of {tuple(shape)}")
+            if t.dtype is not dtype:
+                _refuse(where, "TS_ERR_INVALID_ARG", f"{t.dtype} instead of {dtype}")
+            _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not dense or not on the current device")
+
+    def rotate(self, rope, x, positions, out, stream=None):
+        """x / out [total][heads][d] (bf16 or fp32 each): rows turned by positions int32 [total]. out may be x."""
+        if _device is None:
+            _torch()
+        here, total = _device(), x.shape[0]
+        xs, kind = self._heads("rotate", x, 0, total, here)
+        os_, out_kind = self._heads("rotate", out, x.shape[1], total, here)
+        self._counted("rotate", here, (positions, (total,), _int32))
+        ts_rotate(self.handle, rope.handle, x, xs, kind, x.shape[1], positions, total, out, os_, out_kind, stream)
+
+    def append_rotated(self, rope, k, v, positions, cu_rows, page_table, k_pool, v_pool, starts=None, q=None, q_out=None,
+                       stream=None):
+        """append_prompt with K turned by positions int32 [total]; q [total][H][d] of the rows' type into q_out too."""
+        if _device is None:
+            _torch()
+        here, B, total, kind = _device(), cu_rows.shape[0] - 1, k.shape[0], self._rows_dtype()
+        ks, _ = self._heads("append_rotated", k, self._kv_row[0], total, here)
+        vs, _ = self._heads("append_rotated", v, self._kv_row[0], total, here)
+        qs = os_ = out_kind = 0
+        if (q is None) != (q_out is None):
+            _refuse("append_rotated", "TS_ERR_INVALID_ARG", "q and q_out come together")
+        if q is not None:
+            qs, _ = self._heads("append_rotated", q, self._q_row[0], total, here)
+            os_, out_kind = self._heads("append_rotated", q_out, self._q_row[0], total, here)
+        for t in (k, v) if q is None else (k, v, q):
+            if t.dtype is not kind:
+                _refuse("append_rotated", "TS_ERR_INVALID_ARG", f"{t.dtype} instead of {kind}")
+        self._counted("append_rotated", here, (positions, (total,), _int32), (cu_rows, (B + 1,), _int32), (starts, (B,), _int32))
+        self._paged("append_rotated", B, page_table, k_pool, v_pool)
+        ts_append_rotated(self.handle, rope.handle, k, ks, v, vs, positions, cu_rows, starts, B, total, page_table, k_pool,
+                          v_pool, q, qs, q_out, os_, out_kind, stream)
+
+    def tree_attend(self, q, k_pool, v_pool, page_table, seq_lens, cu_rows, mask, out, lse=None, scale=0.0, stream=None):
+        """q / out [total][H][d] (bf16): the last cached tokens of each sequence, a tree of drafts, over its whole cache.
+        mask int32 [total][words]: bit j of a row is set where it sees draft j; None: the drafts up to its own."""
+        if _device is None:
+            _torch()
+        here, B, total, heads = _device(), cu_rows.shape[0] - 1, q.shape[0], self._q_row[0]
+        qs, kind = self._heads("tree_attend", q, heads, total, here)
+        os_, out_kind = self._heads("tree_attend", out, heads, total, here)
+        if kind != TS_KV_BF16 or out_kind != TS_KV_BF16:
+            _refuse("tree_attend", "TS_ERR_INVALID_ARG", "bfloat16 rows are wanted")
+        self._counted("tree_attend", here, (seq_lens, (B,), _int32), (cu_rows, (B + 1,), _int32), (lse, (total, heads), _float32))
+        words = 0
+        if mask is not None:
+            if mask.dim() != 2:
+                _refuse("tree_attend", "TS_ERR_SHAPE", f"{tuple(mask.shape)} instead of {(total, 'words')}")
+            words = mask.shape[1]
+            self._counted("tree_attend", here, (mask, (total, words), _int32))
+        self._paged("tree_attend", B, page_table, k_pool, v_pool)
+        ts_tree_attend(self.handle, q, qs, k_pool, v_pool, page_table, seq_lens, cu_rows, mask, words, B, total, scale, out,
+                       os_, lse, stream)
+
+    def verify_tree(self, tokens, parents, cu_rows, target, draft, u, u_next, path, count, next_token, distinct=False,
+                    stream=None):
+        """target / draft fp32 [total][vocab] (draft None: drafts without probabilities): path int32 [B][most], count and
+        next_token int32 [B] receive the nodes that the target keeps and the token behind them."""
+        if _device is None:
+            _torch()
+        here, B, total = _device(), cu_rows.shape[0] - 1, tokens.shape[0]
+        if target.dim() != 2 or target.shape[0] != total or (draft is not None and draft.shape != target.shape):
+            _refuse("verify_tree", "TS_ERR_SHAPE", f"{tuple(target.shape)} instead of {(total, 'vocab')}, for both")
+        _rows_of("verify_tree", total, (target, _float32), (draft, _float32))
+        if path.dim() != 2 or path.shape[0] != B:
+            _refuse("verify_tree", "TS_ERR_SHAPE", f"{tuple(path.shape)} instead of {(B, 'most')}")
+        self._counted("verify_tree", here, (tokens, (total,), _int32), (parents, (total,), _int32), (cu_rows, (B + 1,), _int32),
+                      (u, (total,), _float32), (u_next, (B,), _float32), (path, path.shape, _int32), (count, (B,), _int32),
+                      (next_token, (B,), _int32))
+        vocab = target.shape[1]
+        ts_verify_tree(self.handle, tokens, parents, cu_rows, B, total, vocab, target, target.stride(0) if total > 1 else vocab,
+                       draft, 0 if draft is None else (draft.stride(0) if total > 1 else vocab), u, u_next,
+                       1 if distinct else 0, path, path.shape[1], count, next_token, stream)
+
+    def keep_rows(self, path, count, cu_rows, seq_lens, page_table, k_pool, v_pool, new_lens=None, total=None, stream=None):
+        """The K and V rows of path's nodes to the front of the drafts'. Pools of one layer, or [layers][...] with a pool
+        each, dense in itself. total: rows that cu_rows may end at (any, where it is not given)."""
+        if _device is None:
+            _torch()
+        here, B = _device(), cu_rows.shape[0] - 1
+        if path.dim() != 2 or path.shape[0] != B:
+            _refuse("keep_rows", "TS_ERR_SHAPE", f"{tuple(path.shape)} instead of {(B, 'most')}")
+        self._counted("keep_rows", here, (path, path.shape, _int32), (count, (B,), _int32), (cu_rows, (B + 1,), _int32),
+                      (seq_lens, (B,), _int32), (new_lens, (B,), _int32))
+        layers, step, one = 1, 0, (k_pool, v_pool)
+        if k_pool.dim() == 5 or (self._q4 and k_pool.dim() == 4):
+            if k_pool.shape != v_pool.shape or k_pool.stride(0) != v_pool.stride(0):
+                _refuse("keep_rows", "TS_ERR_SHAPE", "the pools of K and V differ")
+            layers, step = k_pool.shape[0], k_pool.stride(0) * k_pool.element_size()
+            if layers == 0:
+                return
+            one = (k_pool[0], v_pool[0])
+        self._paged("keep_rows", B, page_table, *one)
+        ts_keep_rows(self.handle, path, path.shape[1], count, cu_rows, seq_lens, B, (1 << 30) if total is None else total,
+                     page_table, k_pool, v_pool, layers, step, new_lens, stream)
+
     def select_blocks(self, vote, seq_lens, block, budget, idx, count, stream=None):
         ts_select_blocks(self.handle, vote, vote.stride(0), seq_lens, seq_lens.shape[0], block, budget, idx,
                          idx.stride(0), count, stream)
 
     def status(self, stream=None) -> int:
         return ts_get_status(self.handle, stream)
+
+
+class Rope:
+    """Owns a ts_rope: the frequencies of rotary positions. scaling is one of ROPE_SCALING; freqs: radians per position of
+    each pair, for "given"."""
+
+    def __init__(self, rot_dim, base=10000.0, interleaved=False, scaling="plain", factor=1.0, original=0, low=0.0, high=0.0,
+                 attention=0.0, freqs=None):
+        self.handle = None
+        if scaling not in ROPE_SCALING:
+            _refuse("rope", "TS_ERR_INVALID_ARG", f"{scaling} is none of {', '.join(ROPE_SCALING)}")
+        if freqs is not None and len(freqs) != rot_dim // 2:
+            _refuse("rope", "TS_ERR_SHAPE", f"{len(freqs)} frequencies instead of {rot_dim // 2}")
+        self.rot_dim = rot_dim
+        given = None if freqs is None else (c_double * len(freqs))(*[float(f) for f in freqs])
+        self.handle = ts_rope_create(RopeConfig(rot_dim, 1 if interleaved else 0, ROPE_SCALING[scaling], base, factor, original,
+                                                low, high, attention, given))
+
+    def read(self):
+        """(frequencies of the pairs in radians per position, factor of what is turned)."""
+        return ts_rope_read(self.handle, self.rot_dim // 2)
+
+    def close(self):
+        if self.handle:
+            ts_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class Cache:

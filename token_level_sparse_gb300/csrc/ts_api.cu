@@ -5,6 +5,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 
 #include "ts_internal.h"
@@ -44,6 +45,9 @@ void free_ctx_buffers(ts_ctx* c) {
   cudaFree(c->sel_rows);
   cudaFree(c->q4_part_o);
   cudaFree(c->q4_part_ml);
+  cudaFree(c->tree_part_o);
+  cudaFree(c->tree_part_ml);
+  cudaFree(c->tree_base);
   cudaFree(c->step_partials);
   cudaFree(c->step_hist);
   cudaFree(c->step_mass);
@@ -76,6 +80,8 @@ bool valid_params(const ts_select_params* p) {
 
 constexpr int kMaxRows = 1 << 30;                     // rows of one packed call
 constexpr int64_t kMaxRowStride = (int64_t)1 << 31;   // elements from one packed row to the next
+constexpr double kInv2Pi = 0x1.45f306dc9c883p-3, kInv2PiLow = -0x1.6b01ec5417056p-57;   // 1 / 2pi
+constexpr int kMaxVocab = 1 << 20;                    // tokens of a vocabulary
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
@@ -83,6 +89,16 @@ cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 bool elsewhere(const ts_ctx* ctx) {
   int device = -1;
   return cudaGetDevice(&device) != cudaSuccess || device != ctx->device;
+}
+bool aligned16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
+  return true;
+}
+// n elements of 4 bytes from p on, and m from q on, share memory
+bool overlap4(const void* p, int64_t n, const void* q, int64_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + 4 * (uintptr_t)m && b < a + 4 * (uintptr_t)n;
 }
 bool q4_elsewhere(const ts_ctx* ctx) { return ctx->cfg.kv_dtype == TS_KV_Q4 && elsewhere(ctx); }
 
@@ -189,6 +205,12 @@ ts_status ts_create(ts_ctx** out, const ts_config* cfg) {
     const size_t slots = (size_t)q4_part_slots(c, ctx->num_sms);
     chk(alloc(&ctx->q4_part_o, slots * H * D));
     chk(alloc(&ctx->q4_part_ml, slots * H));
+  }
+  if (tree_supported(c)) {
+    const size_t slots = (size_t)tree_part_slots(ctx->num_sms);
+    chk(alloc(&ctx->tree_part_o, slots * 256 * D));
+    chk(alloc(&ctx->tree_part_ml, slots * 256));
+    chk(alloc(&ctx->tree_base, B + 1));
   }
   chk(alloc(&ctx->gsync, 4));
   if (e == cudaSuccess) chk(cudaMemset(ctx->gsync, 0, 4 * sizeof(unsigned)));   // then kept zero by each launch
@@ -549,6 +571,172 @@ ts_status ts_prompt_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const v
   if (!prompt_supported(c)) return TS_ERR_UNSUPPORTED;
   PromptCall a{q, q_stride, k, k_stride, v, v_stride, cu_rows, B, total, resolve_scale(ctx, scale), out, out_stride, lse};
   return launch_prompt_attend(ctx, a, as_stream(stream));
+}
+
+// Frequencies of every pair in radians per position, by the configuration's rule.
+ts_status ts_rope_create(ts_rope** out, const ts_rope_config* cfg) {
+  if (!out || !cfg) return TS_ERR_INVALID_ARG;
+  *out = nullptr;
+  const ts_rope_config& c = *cfg;
+  if (c.rot_dim < 2 || c.rot_dim > 128 || c.rot_dim % 2 != 0) return TS_ERR_SHAPE;
+  if (c.interleaved != 0 && c.interleaved != 1) return TS_ERR_INVALID_ARG;
+  if (c.scaling < TS_ROPE_PLAIN || c.scaling > TS_ROPE_GIVEN) return TS_ERR_INVALID_ARG;
+  if ((c.scaling == TS_ROPE_GIVEN) != (c.freqs != nullptr)) return TS_ERR_INVALID_ARG;
+  const double pi = 3.14159265358979323846;
+  if (c.scaling != TS_ROPE_GIVEN && !(std::isfinite(c.base) && c.base > 0.)) return TS_ERR_INVALID_ARG;
+  if (c.scaling != TS_ROPE_GIVEN && c.scaling != TS_ROPE_PLAIN && !(std::isfinite(c.factor) && c.factor > 0.))
+    return TS_ERR_INVALID_ARG;
+  const bool ranged = c.scaling == TS_ROPE_BANDS || c.scaling == TS_ROPE_YARN;
+  if (ranged && !(c.original > 0 && std::isfinite(c.low) && std::isfinite(c.high) && c.low > 0. && c.high > c.low))
+    return TS_ERR_INVALID_ARG;
+  if (c.scaling == TS_ROPE_YARN && c.base == 1.) return TS_ERR_INVALID_ARG;
+  if (!std::isfinite(c.attention) || c.attention < 0.) return TS_ERR_INVALID_ARG;
+  ts_rope* r = new (std::nothrow) ts_rope();
+  if (!r) return TS_ERR_CUDA;
+  r->rot_dim = c.rot_dim;
+  r->interleaved = c.interleaved;
+  const int n = c.rot_dim / 2;
+  double base = c.base, first = 0., last = 0.;
+  if (c.scaling == TS_ROPE_BASE && c.rot_dim > 2) base *= std::pow(c.factor, (double)c.rot_dim / (c.rot_dim - 2));
+  if (c.scaling == TS_ROPE_YARN) {
+    // the pairs that turn `high` and `low` times within the original context
+    auto pair = [&](double turns) { return c.rot_dim * std::log(c.original / (2. * pi * turns)) / (2. * std::log(c.base)); };
+    first = std::max(0., std::floor(pair(c.high)));
+    last = std::min((double)c.rot_dim - 1., std::ceil(pair(c.low)));
+  }
+  for (int i = 0; i < n; ++i) {
+    double f = c.scaling == TS_ROPE_GIVEN ? c.freqs[i] : std::pow(base, -2. * i / c.rot_dim);
+    if (c.scaling == TS_ROPE_LINEAR) f /= c.factor;
+    if (c.scaling == TS_ROPE_BANDS) {
+      const double t = std::min(1., std::max(0., (c.original * f / (2. * pi) - c.low) / (c.high - c.low)));
+      f = (1. - t) * f / c.factor + t * f;
+    }
+    if (c.scaling == TS_ROPE_YARN) {
+      const double t = std::min(1., std::max(0., (i - first) / std::max(last - first, 0.001)));
+      f = t * f / c.factor + (1. - t) * f;
+    }
+    if (!std::isfinite(f)) {
+      delete r;
+      return TS_ERR_INVALID_ARG;
+    }
+    r->freqs[i] = f;
+    // f / 2pi modulo 1 in units of 2^-64: the product with 1 / 2pi (to 107 bits) in two parts, both exact modulo 1
+    const double whole = std::fabs(f) * kInv2Pi, rest = std::fma(std::fabs(f), kInv2Pi, -whole) + std::fabs(f) * kInv2PiLow;
+    const double turn = std::fmod(whole, 1.), more = std::fmod(rest, 1.);
+    const uint64_t low = (uint64_t)std::ldexp(std::fabs(more), 64);
+    const uint64_t u = (uint64_t)std::ldexp(turn, 64) + (more < 0. ? 0 - low : low);
+    r->turns[i] = f < 0. ? 0 - u : u;
+  }
+  const double by_rule = c.scaling == TS_ROPE_YARN && c.factor > 1. ? 0.1 * std::log(c.factor) + 1. : 1.;
+  r->factor = (float)(c.attention > 0. ? c.attention : by_rule);
+  *out = r;
+  return TS_OK;
+}
+
+ts_status ts_rope_destroy(ts_rope* rope) {
+  if (!rope) return TS_ERR_INVALID_ARG;
+  delete rope;
+  return TS_OK;
+}
+
+ts_status ts_rope_read(const ts_rope* rope, double* freqs, double* attention) {
+  if (!rope || !freqs || !attention) return TS_ERR_INVALID_ARG;
+  for (int i = 0; i < rope->rot_dim / 2; ++i) freqs[i] = rope->freqs[i];
+  *attention = rope->factor;
+  return TS_OK;
+}
+
+ts_status ts_rotate(ts_ctx* ctx, const ts_rope* rope, const void* x, int64_t x_stride, int dtype, int heads,
+                    const int32_t* positions, int total, void* out, int64_t out_stride, int out_dtype, void* stream) {
+  if (!ctx || !rope || (total > 0 && (!x || !positions || !out))) return TS_ERR_INVALID_ARG;
+  if (elsewhere(ctx)) return TS_ERR_INVALID_ARG;
+  if ((dtype != TS_KV_F32 && dtype != TS_KV_BF16) || (out_dtype != TS_KV_F32 && out_dtype != TS_KV_BF16))
+    return TS_ERR_INVALID_ARG;
+  const ts_config& c = ctx->cfg;
+  if (heads < 1 || heads > 4096 || total < 0 || total > kMaxRows || rope->rot_dim > c.head_dim) return TS_ERR_SHAPE;
+  const int64_t row = (int64_t)heads * c.head_dim;
+  if (x_stride < row || out_stride < row || x_stride > kMaxRowStride || out_stride > kMaxRowStride) return TS_ERR_SHAPE;
+  if (x_stride % (dtype == TS_KV_F32 ? 4 : 8) != 0 || out_stride % (out_dtype == TS_KV_F32 ? 4 : 8) != 0)
+    return TS_ERR_INVALID_ARG;
+  if (!aligned16({x, out})) return TS_ERR_INVALID_ARG;
+  RotateCall a{x, x_stride, dtype, heads, positions, total, out, out_stride, out_dtype};
+  return launch_rotate(ctx, rope, a, as_stream(stream));
+}
+
+ts_status ts_append_rotated(ts_ctx* ctx, const ts_rope* rope, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, const int32_t* positions, const int32_t* cu_rows, const int32_t* starts,
+                            int B, int total, const int32_t* page_table, void* k_pool, void* v_pool, const void* q,
+                            int64_t q_stride, void* q_out, int64_t q_out_stride, int q_out_dtype, void* stream) {
+  if (!ctx || !rope || !cu_rows || !page_table || !k_pool || !v_pool) return TS_ERR_INVALID_ARG;
+  if (total > 0 && (!k || !v || !positions)) return TS_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return TS_ERR_INVALID_ARG;
+  if (elsewhere(ctx)) return TS_ERR_INVALID_ARG;
+  const ts_config& c = ctx->cfg;
+  const int64_t row = (int64_t)c.n_kv_heads * c.head_dim, qrow = (int64_t)c.n_q_heads * c.head_dim;
+  const int64_t per16 = c.kv_dtype == TS_KV_F32 ? 4 : 8;
+  if (B < 1 || B > c.max_batch || total < 0 || total > kMaxRows || rope->rot_dim > c.head_dim) return TS_ERR_SHAPE;
+  if (k_stride < row || v_stride < row || k_stride > kMaxRowStride || v_stride > kMaxRowStride) return TS_ERR_SHAPE;
+  if (k_stride % per16 != 0 || v_stride % per16 != 0) return TS_ERR_INVALID_ARG;
+  if (q) {
+    if (q_out_dtype != TS_KV_F32 && q_out_dtype != TS_KV_BF16) return TS_ERR_INVALID_ARG;
+    if (q_stride < qrow || q_out_stride < qrow || q_stride > kMaxRowStride || q_out_stride > kMaxRowStride) return TS_ERR_SHAPE;
+    if (q_stride % per16 != 0 || q_out_stride % (q_out_dtype == TS_KV_F32 ? 4 : 8) != 0) return TS_ERR_INVALID_ARG;
+  }
+  if (!aligned16({k, v, k_pool, v_pool, q, q_out})) return TS_ERR_INVALID_ARG;
+  AppendPromptCall a{k, k_stride, v, v_stride, cu_rows, starts, B, total, page_table, k_pool, v_pool};
+  RotateCall r{q, q_stride, c.kv_dtype == TS_KV_F32 ? TS_KV_F32 : TS_KV_BF16, c.n_q_heads, positions, total, q_out, q_out_stride,
+               q_out_dtype};
+  return launch_append_rotated(ctx, rope, a, r, as_stream(stream));
+}
+
+ts_status ts_tree_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
+                         const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_rows, const int32_t* mask,
+                         int mask_words, int B, int total, float scale, void* out, int64_t out_stride, float* lse,
+                         void* stream) {
+  if (!ctx || !k_pool || !v_pool || !page_table || !seq_lens || !cu_rows) return TS_ERR_INVALID_ARG;
+  if (total > 0 && (!q || !out)) return TS_ERR_INVALID_ARG;
+  if (elsewhere(ctx)) return TS_ERR_INVALID_ARG;
+  const ts_config& c = ctx->cfg;
+  const int64_t row = (int64_t)c.n_q_heads * c.head_dim;
+  if (B < 1 || B > c.max_batch || total < 0 || total > kMaxRows) return TS_ERR_SHAPE;
+  if (mask && (mask_words < 1 || mask_words > kMaxTree / 32)) return TS_ERR_SHAPE;
+  if (q_stride < row || out_stride < row || q_stride > kMaxRowStride || out_stride > kMaxRowStride) return TS_ERR_SHAPE;
+  if (q_stride % 8 != 0 || out_stride % 8 != 0 || !aligned16({q, k_pool, v_pool, out})) return TS_ERR_INVALID_ARG;
+  if (std::isnan(scale)) return TS_ERR_INVALID_ARG;
+  if (!tree_supported(c)) return TS_ERR_UNSUPPORTED;
+  TreeCall a{q, q_stride, k_pool, v_pool, page_table, seq_lens, cu_rows, mask, mask_words, B, total,
+             resolve_scale(ctx, scale), out, out_stride, lse};
+  return launch_tree_attend(ctx, a, as_stream(stream));
+}
+
+ts_status ts_verify_tree(ts_ctx* ctx, const int32_t* tokens, const int32_t* parents, const int32_t* cu_rows, int B,
+                         int total, int vocab, const float* target, int64_t target_stride, const float* draft,
+                         int64_t draft_stride, const float* u, const float* u_next, int distinct, int32_t* path,
+                         int64_t path_stride, int32_t* count, int32_t* next_token, void* stream) {
+  if (!ctx || !cu_rows || !u_next || !path || !count || !next_token) return TS_ERR_INVALID_ARG;
+  if (total > 0 && (!tokens || !parents || !target || !u)) return TS_ERR_INVALID_ARG;
+  if (elsewhere(ctx)) return TS_ERR_INVALID_ARG;
+  if (B < 1 || B > ctx->cfg.max_batch || total < 0 || total > kMaxRows) return TS_ERR_SHAPE;
+  if (vocab < 1 || vocab > kMaxVocab || path_stride < 1 || path_stride > kMaxRowStride) return TS_ERR_SHAPE;
+  if (target_stride < vocab || (draft && draft_stride < vocab)) return TS_ERR_SHAPE;
+  VerifyCall a{tokens, parents, cu_rows, B, total, vocab, target, target_stride, draft, draft_stride, u, u_next,
+               distinct != 0, path, path_stride, count, next_token};
+  return launch_verify(ctx, a, as_stream(stream));
+}
+
+ts_status ts_keep_rows(ts_ctx* ctx, const int32_t* path, int64_t path_stride, const int32_t* count, const int32_t* cu_rows,
+                       const int32_t* seq_lens, int B, int total, const int32_t* page_table, void* k_pool, void* v_pool,
+                       int n_layers, int64_t layer_bytes, int32_t* new_lens, void* stream) {
+  if (!ctx || !path || !count || !cu_rows || !seq_lens || !page_table || !k_pool || !v_pool) return TS_ERR_INVALID_ARG;
+  if (elsewhere(ctx)) return TS_ERR_INVALID_ARG;
+  if (B < 1 || B > ctx->cfg.max_batch || total < 0 || total > kMaxRows) return TS_ERR_SHAPE;
+  if (path_stride < 1 || path_stride > kMaxRowStride || n_layers < 1 || n_layers > 65535) return TS_ERR_SHAPE;
+  if (n_layers > 1 && layer_bytes < ctx->cfg.num_pages * ts_page_bytes(&ctx->cfg)) return TS_ERR_SHAPE;
+  if ((n_layers > 1 && layer_bytes % 16 != 0) || !aligned16({k_pool, v_pool})) return TS_ERR_INVALID_ARG;
+  // (each of many CTAs reads the lengths, one writes the new ones)
+  if (new_lens && overlap4(new_lens, B, seq_lens, B)) return TS_ERR_INVALID_ARG;
+  KeepCall a{path, path_stride, count, cu_rows, seq_lens, B, total, page_table, k_pool, v_pool, n_layers, layer_bytes, new_lens};
+  return launch_keep_rows(ctx, a, as_stream(stream));
 }
 
 ts_status ts_select_blocks(ts_ctx* ctx, const float* vote, int64_t vote_stride, const int32_t* seq_lens, int B,

@@ -264,6 +264,13 @@ __device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
+// Two fp32 values as bf16, rounded to nearest, the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Compensated (Kahan) accumulation in fp32.
 struct KahanF {
   float s = 0.f, c = 0.f;

@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <utility>
 
 #include "../../include/tokenselect.h"
 
@@ -71,6 +72,9 @@ struct ts_ctx {
   int32_t* sel_rows = nullptr;           // persistent kernel: per CTA, its selected tokens [kStepFlagCap]
   float* q4_part_o = nullptr;            // 4-bit pools: attention parts [slots][H][d], q4_part_slots
   float2* q4_part_ml = nullptr;          // ... and their (max, sum), also the score's [H][slots]
+  float* tree_part_o = nullptr;          // tree attention: parts [2 num_sms][d / 4][256 rows][4]
+  float2* tree_part_ml = nullptr;        // ... and their (max, sum) [2 num_sms][256]
+  int64_t* tree_base = nullptr;          // [max_batch + 1] key tiles before each sequence's
   int64_t kernels = 0;           // kernel launches issued
   // persistent decode-step kernel
   int step_grid = 0;                     // CTAs of the cooperative launch (0: not yet sized)
@@ -119,7 +123,17 @@ struct ts_cache {
   uint8_t* filled = nullptr;     // [n_layers][max_batch]
 };
 
+struct ts_rope {
+  int rot_dim = 0;
+  int interleaved = 0;
+  float factor = 1.f;            // of what is turned
+  double freqs[64] = {};         // radians per position
+  uint64_t turns[64] = {};       // the same as a fraction of a turn, in units of 2^-64
+};
+
 namespace ts {
+
+constexpr int kMaxTree = 1024;   // drafted tokens of one sequence
 
 // Counter slots per sequence: [0] score, [1] select, [2 .. 2+H_kv) attention.
 constexpr int kCounterSlots = 2 + 64;
@@ -239,6 +253,68 @@ struct PromptCall {        // causal attention of packed prompts
   float* lse;
 };
 
+struct RotateCall {        // rows of heads turned by their positions
+  const void* x;           // null: none (beside an append)
+  int64_t stride;          // elements
+  int dtype;               // TS_KV_F32 or TS_KV_BF16
+  int heads;
+  const int32_t* positions;
+  int total;
+  void* out;
+  int64_t out_stride;
+  int out_dtype;
+};
+
+struct TreeCall {          // drafted tokens over the whole cache
+  const void* q;
+  int64_t q_stride;
+  const void* k_pool;
+  const void* v_pool;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_rows;
+  const int32_t* mask;     // or null: causal
+  int mask_words;
+  int B, total;
+  float scale;
+  void* out;
+  int64_t out_stride;
+  float* lse;
+};
+
+struct VerifyCall {
+  const int32_t* tokens;
+  const int32_t* parents;
+  const int32_t* cu_rows;
+  int B, total, vocab;
+  const float* target;
+  int64_t target_stride;
+  const float* draft;      // or null
+  int64_t draft_stride;
+  const float* u;
+  const float* u_next;
+  int distinct;
+  int32_t* path;
+  int64_t path_stride;
+  int32_t* count;
+  int32_t* next;
+};
+
+struct KeepCall {
+  const int32_t* path;
+  int64_t path_stride;
+  const int32_t* count;
+  const int32_t* cu_rows;
+  const int32_t* seq_lens;
+  int B, total;
+  const int32_t* page_table;
+  void* k_pool;
+  void* v_pool;
+  int layers;
+  int64_t layer_bytes;
+  int32_t* new_lens;
+};
+
 // Head geometries with a compiled kernel: (kv type flag, element type, d, H_kv, G).
 #define TS_STEP_GEOMETRIES(X)             \
   X(TS_KV_F32, float, 64, 4, 1)           \
@@ -270,6 +346,14 @@ ts_status launch_append_prompt(ts_ctx* ctx, const AppendPromptCall& c, cudaStrea
 ts_status launch_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* starts, int B, int total,
                          const int32_t* page_table, const void* k_pool, const void* v_pool, float* k_out,
                          float* v_out, cudaStream_t s);
+ts_status launch_rotate(ts_ctx* ctx, const ts_rope* rope, const RotateCall& c, cudaStream_t s);
+ts_status launch_append_rotated(ts_ctx* ctx, const ts_rope* rope, const AppendPromptCall& c, const RotateCall& q,
+                                cudaStream_t s);
+bool tree_supported(const ts_config& c);
+int64_t tree_part_slots(int num_sms);
+ts_status launch_tree_attend(ts_ctx* ctx, const TreeCall& c, cudaStream_t s);
+ts_status launch_verify(ts_ctx* ctx, const VerifyCall& c, cudaStream_t s);
+ts_status launch_keep_rows(ts_ctx* ctx, const KeepCall& c, cudaStream_t s);
 bool prompt_supported(const ts_config& c);
 ts_status launch_prompt_attend(ts_ctx* ctx, const PromptCall& c, cudaStream_t s);
 ts_status launch_select_blocks(ts_ctx* ctx, const float* vote, int64_t vote_stride, const int32_t* seq_lens, int B,
@@ -297,6 +381,21 @@ inline bool ensure_smem(size_t bytes, int device) {
     return false;
   done.fetch_or(bit, std::memory_order_acq_rel);
   return true;
+}
+
+// Launches `kernel` as a dependent of the kernel before it in the stream (programmatic dependent launch).
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, Args&&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads);
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, std::forward<Args>(args)...);
 }
 
 // Brackets the launches made during its lifetime with a pair of timing events

@@ -799,21 +799,6 @@ Q4Args make_args(ts_ctx* ctx, const float* q, const void* k_pool, const void* v_
   return a;
 }
 
-// Launches `kernel` as a dependent of the kernel before it in the stream (see launch_dependents).
-template <typename... Params, typename... Args>
-cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, Args&&... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = grid;
-  lc.blockDim = dim3(threads);
-  lc.stream = s;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, kernel, std::forward<Args>(args)...);
-}
-
 template <int NB, int NT>
 ts_status run_attend(ts_ctx* ctx, const Q4Args& a, float* out, float* lse, cudaStream_t s) {
   constexpr size_t smem = Q4Ring<NB, NT, true>::SMEM;

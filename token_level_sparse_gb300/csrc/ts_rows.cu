@@ -7,89 +7,10 @@
 // then its threads move 16 bytes (or, into and out of 4-bit blocks, 8 elements) each. Every byte is
 // read and written once, so the copies are bound by memory; eight lanes share one 4-bit group
 // of 64 elements, whose 32 code bytes of neighbouring tokens are contiguous in the block.
-#include "ts_q4.cuh"
+#include "ts_rows.cuh"
 
 namespace ts {
 namespace {
-
-// Rows of a CTA: four, whose codes are 128 contiguous bytes, or one where there are few rows, so that a decode
-// step's rows do not queue behind one another. 33,122 rows written and read back: 89.5 us with four rows
-// and 128 threads, 92.5 with 64 threads, 94.7 with 16 rows and 256 threads, 120 with two rows. Eight rows, one to a
-// CTA, written and read back: 4.6 us with 256 threads, 4.8 with 128.
-constexpr int kRowsPerCta = 4;
-__host__ __device__ constexpr int rows_threads(int rows) { return rows == 1 ? 256 : 128; }
-
-struct RowsArgs {
-  const int32_t* cu;           // [B + 1]; null: one row per sequence, at position seq_lens[b] - 1
-  const int32_t* starts;       // [B] or null (0)
-  const int32_t* seq_lens;     // with cu == null
-  int B, total, rows_per_cta;
-  const int32_t* page_table;
-  int pt_stride, page_shift;
-  int64_t num_pages;
-  int max_tokens;
-  int HKV, D;
-  const unsigned char* src[2]; // K and V rows, bytes
-  int64_t src_stride[2];       // bytes between rows
-  unsigned char* pool[2];
-  float* dst[2];               // ts_read_kv: [total][H_kv][d]
-  int* status;
-};
-
-// Place of the CTA's rows: page * page size + slot, or -1 (no such position; recorded).
-__device__ __forceinline__ void place_rows(const RowsArgs& a, int64_t* place) {
-  // the boundaries of up to 256 sequences in shared memory: one read instead of one per step of the search
-  __shared__ int32_t s_cu[257];
-  const int32_t* cu = a.cu;
-  if (a.cu && a.B <= 256) {
-    for (int b = threadIdx.x; b <= a.B; b += blockDim.x) s_cu[b] = a.cu[b];
-    __syncthreads();
-    cu = s_cu;
-  }
-  if (a.cu && blockIdx.x == 0) {
-    // the boundaries: ascending, from 0, within the rows that there are
-    for (int b = threadIdx.x; b <= a.B; b += blockDim.x) {
-      const int v = cu[b];
-      if (v > a.total || (b == 0 ? v != 0 : v < cu[b - 1])) set_error(a.status, TS_ERR_SEQ_LEN);
-    }
-  }
-  if ((int)threadIdx.x < a.rows_per_cta) {
-    const int64_t r = (int64_t)blockIdx.x * a.rows_per_cta + threadIdx.x;
-    int64_t at = -1;
-    if (r < a.total) {
-      int b = (int)r;
-      int64_t pos = -1;
-      bool inside = true;
-      if (a.cu) {
-        int lo = 0, hi = a.B;              // the last b with cu[b] <= r
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (cu[mid] <= r) lo = mid; else hi = mid;
-        }
-        b = lo;
-        // rows behind the last sequence stay as they are, so do those of one that ends beyond the rows
-        inside = cu[b] >= 0 && r >= cu[b] && r < cu[b + 1] && cu[b + 1] <= a.total;
-        const int start = a.starts ? a.starts[b] : 0;
-        pos = start < 0 ? -1 : start + (r - cu[b]);
-      } else {
-        pos = (int64_t)a.seq_lens[b] - 1;
-      }
-      if (inside) {
-        if (pos < 0 || pos >= a.max_tokens) {
-          set_error(a.status, TS_ERR_SEQ_LEN);
-        } else {
-          const int page = a.page_table[(size_t)b * a.pt_stride + (pos >> a.page_shift)];
-          if (page < 0 || (int64_t)page >= a.num_pages)
-            set_error(a.status, TS_ERR_PAGE_OOB);
-          else
-            at = ((int64_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-        }
-      }
-    }
-    place[threadIdx.x] = at;
-  }
-  __syncthreads();
-}
 
 // bf16 and fp32 pools: rows copied as they are, 16 bytes per thread, four under way. Bound by memory: 33,122 rows
 // of 8 KV heads of 128, K and V: 50 us, 5.5 TB/s read and written in bf16 (16- and one-token pages alike), 91 us and
@@ -112,18 +33,7 @@ __global__ void __launch_bounds__(rows_threads(1)) append_rows_kernel(const __gr
   }
 }
 
-// 4-bit pools. Eight lanes quantise one group of 64 elements: scale = bf16(max|x| / 7), code =
-// 8 + round(x / scale), ties to even. A scale of zero gives zeros; a group with a NaN or an infinity
-// reads back as NaN: its scale is not finite and its codes stand for zero.
-//
-// The bits are those of exact arithmetic, without a division: x and the scale s have 8 significant bits
-// each, so a quotient that is not halfway between two codes is at least 2^-9 away from it (numerator
-// and denominator of the difference are whole numbers below 2^9 of one unit), and likewise max|x| / 7
-// lies 2^-12 away from any midpoint of bf16. A product with 1/7 that is right to 2^-22 therefore rounds
-// to the right scale. A quotient x r, r near 1/s, is off by less than 2^-19, and is rounded twice: to a
-// multiple of 2^-10 (by a sum with 1.5 2^13), which makes a quotient halfway between codes exact and leaves
-// every other one on its side of halfway, then to a whole number, ties to even (by a sum with 1.5 2^23).
-// Scales near or below the smallest normal number have fewer bits and take the divisions instead.
+// 4-bit pools (q4_quantise8).
 //
 // Measured: 33,122 rows of 8 KV heads of 128, K and V: 43 us, 4.0 TB/s, bound by issue (with the divisions
 // throughout 104 us; eight loads under way in place of four 2 us more).
@@ -158,45 +68,8 @@ __global__ void __launch_bounds__(rows_threads(ROWS)) append_q4_kernel(const __g
     for (int k = 0; k < BATCH; ++k) {
       const int i = i0 + k * COLS, isv = i >= groups, c = isv ? i - groups : i, g = c / NB, nb = c % NB;
       if (i >= 2 * groups) break;        // (the same in all eight lanes)
-      const uint32_t in[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-      // the largest magnitude by its bits, two at a time: ordered like the values, with infinities and NaN on top
-      uint32_t mb = 0u;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mb = __vmaxu2(mb, in[e] & 0x7fff7fffu);
-#pragma unroll
-      for (int d = 4; d >= 1; d >>= 1) mb = __vmaxu2(mb, __shfl_xor_sync(peers, mb, d));
-      const float top = bf16_bits_f(max(mb & 0xffffu, mb >> 16));
       __nv_bfloat16 sb;
-      uint32_t w;
-      if (top >= 0x1p-100f && top < INFINITY) {
-        sb = __float2bfloat16_rn(top * (1.f / 7.f));
-        const float s = __bfloat162float(sb);
-        float rs;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(s));
-        const uint64_t r2 = pack_f2(rs, rs), fine = pack_f2(12288.f, 12288.f),
-                       whole = pack_f2(12582920.f - 12288.f, 12582920.f - 12288.f), one = pack_f2(1.f, 1.f);
-        uint32_t u[4];                   // two codes in the low byte
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint64_t x = pack_f2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u));
-          // 1.5 2^23 + 8 + the rounded quotient: the code in the low byte, since |q| < 7.1 (s >= top / 7 (1 - 2^-8))
-          float lo, hi;
-          unpack_f2(fma_f2(fma_f2(x, r2, fine), one, whole), lo, hi);
-          u[e] = __float_as_uint(hi) * 16u + __float_as_uint(lo);
-        }
-        w = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
-      } else {
-        sb = __float2bfloat16_rn(__fdiv_rn(top, 7.f));
-        const float s = __bfloat162float(sb);
-        const bool live = s > 0.f && s < INFINITY;
-        w = 0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = __uint_as_float(e & 1 ? in[e >> 1] & 0xffff0000u : in[e >> 1] << 16);
-          const int q = live ? max(-7, min(7, __float2int_rn(__fdiv_rn(x, s)))) : 0;
-          w |= (uint32_t)(q + 8) << (4 * e);
-        }
-      }
+      const uint32_t w = q4_quantise8(raw[k], peers, sb);
       if (at >= 0) {
         unsigned char* base = a.pool[isv] + ((at >> 4) * a.HKV + g) * BLK;
         *reinterpret_cast<uint32_t*>(base + nb * 512 + slot * 32 + lane8 * 4) = w;
@@ -287,23 +160,123 @@ __global__ void __launch_bounds__(rows_threads(ROWS)) read_rows_kernel(const __g
   }
 }
 
-RowsArgs base_args(ts_ctx* ctx, int B, int total, const int32_t* page_table, void* k_pool, void* v_pool) {
-  const ts_config& c = ctx->cfg;
-  RowsArgs a{};
-  a.B = B;
-  a.total = total;
-  a.rows_per_cta = total >= 2 * ctx->num_sms ? kRowsPerCta : 1;
-  a.page_table = page_table;
-  a.pt_stride = c.max_pages_per_seq;
-  a.page_shift = ctx->page_shift;
-  a.num_pages = c.num_pages;
-  a.max_tokens = ctx->max_tokens;
-  a.HKV = c.n_kv_heads;
-  a.D = c.head_dim;
-  a.pool[0] = static_cast<unsigned char*>(k_pool);
-  a.pool[1] = static_cast<unsigned char*>(v_pool);
-  a.status = ctx->status;
-  return a;
+// Rows of kept drafts to the front of their draft (ts_keep_rows): row path[j] of the last T rows goes to row j, for
+// every layer. Places ascend and path[j] >= j, so row j is never the source of a later row: a thread moves its 16 bytes
+// (of one head, K or V) of the rows one after another, eight loads under way before their stores, and needs nobody
+// else. Bytes move as they are, whatever the pool's type (4-bit scales are two bytes of a token: a thread each). Bound by
+// latency: page, row in, row out.
+constexpr int kKeepThreads = 128, kKeepRows = 128, kKeepBatch = 8;
+
+struct KeepArgs {
+  const int32_t* path;
+  int64_t path_stride;
+  const int32_t* count;
+  const int32_t* cu;
+  int B, total;
+  const int32_t* seq_lens;
+  const int32_t* page_table;
+  int pt_stride, page_shift;
+  int64_t num_pages;
+  int max_tokens, HKV, D;
+  unsigned char* pool[2];
+  int64_t layer_bytes;
+  int32_t* new_lens;           // or null
+  int* status;
+};
+
+template <int kType>
+__global__ void __launch_bounds__(kKeepThreads) keep_rows_kernel(const __grid_constant__ KeepArgs a) {
+  __shared__ int64_t s_src[kKeepRows], s_dst[kKeepRows];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const bool lead = blockIdx.y == 0 && blockIdx.z == 0;          // the CTA that reports for its sequence
+  const int32_t* path = a.path + b * a.path_stride;
+  const int c0 = a.cu[b], T = a.cu[b + 1] - c0, n = a.seq_lens[b], count = a.count[b];
+  int err = 0;
+  if (c0 < 0 || T < 0 || c0 + (int64_t)T > a.total || (b == 0 && c0 != 0) || n < T || n > a.max_tokens)
+    err = TS_ERR_SEQ_LEN;
+  else if (count > a.path_stride)
+    err = TS_ERR_CAPACITY;
+  else if (count < 0 || count > T)
+    err = TS_ERR_INVALID_ARG;
+  if (!err) {
+    bool bad = false;
+    for (int j = tid; j < count; j += kKeepThreads) {
+      const int at = path[j];
+      bad |= at < j || at >= T || (j > 0 && at <= path[j - 1]);
+    }
+    if (__syncthreads_or(bad)) err = TS_ERR_INVALID_ARG;
+  }
+  if (lead && tid == 0) {
+    if (err) set_error(a.status, err);
+    if (a.new_lens) a.new_lens[b] = err ? n : n - T + count;
+  }
+  if (err) return;
+  const int first = n - T, ps = 1 << a.page_shift;
+  // this thread's piece of a row: K or V, head, 16 bytes of it (4-bit pools: then the scales, 2 bytes each)
+  constexpr int ES = kType == TS_KV_F32 ? 4 : 2;
+  const int pieces = kType == TS_KV_Q4 ? a.D / 32 + a.D / 64 : a.D * ES / 16;
+  const int i = blockIdx.y * kKeepThreads + tid;
+  const bool mine = i < 2 * a.HKV * pieces;
+  const int isv = i / (a.HKV * pieces), g = i / pieces % a.HKV, piece = i % pieces;
+  unsigned char* pool = a.pool[isv & 1] + blockIdx.z * a.layer_bytes;
+  int64_t head;                                                  // bytes of a head in its page, of a token in it
+  int token, off;
+  if (kType == TS_KV_Q4) {
+    head = q4_block_bytes(a.D);
+    if (piece < a.D / 32) {
+      token = 32;
+      off = piece / 2 * 512 + piece % 2 * 16;
+    } else {
+      token = 2;
+      off = q4_code_bytes(a.D) + (piece - a.D / 32) * 32;
+    }
+  } else {
+    token = a.D * ES;
+    head = (int64_t)ps * token;
+    off = piece * 16;
+  }
+  const bool whole = kType != TS_KV_Q4 || token == 32;           // 16 bytes, else 2
+  auto address = [&](int64_t place) {
+    return pool + ((place >> a.page_shift) * a.HKV + g) * head + (place & (ps - 1)) * token + off;
+  };
+  for (int j0 = 0; j0 < count; j0 += kKeepRows) {
+    const int rows = min(kKeepRows, count - j0);
+    __syncthreads();
+    for (int j = tid; j < rows; j += kKeepThreads) {
+      int64_t place[2];
+      for (int e = 0; e < 2; ++e) {
+        const int pos = first + (e ? j0 + j : path[j0 + j]);
+        const int page = a.page_table[(int64_t)b * a.pt_stride + (pos >> a.page_shift)];
+        place[e] = page < 0 || page >= a.num_pages ? -1 : ((int64_t)page << a.page_shift) + (pos & (ps - 1));
+      }
+      const bool bad = place[0] < 0 || place[1] < 0;
+      if (bad && lead) set_error(a.status, TS_ERR_PAGE_OOB);
+      s_src[j] = bad || path[j0 + j] == j0 + j ? -1 : place[0];  // (a row that stays where it is)
+      s_dst[j] = place[1];
+    }
+    __syncthreads();
+    if (!mine) continue;
+    for (int j = 0; j < rows; j += kKeepBatch) {
+      uint4 v[kKeepBatch];
+#pragma unroll
+      for (int k = 0; k < kKeepBatch; ++k) {
+        const int64_t src = j + k < rows ? s_src[j + k] : -1;
+        if (src < 0) continue;
+        if (whole)
+          v[k] = *reinterpret_cast<const uint4*>(address(src));
+        else
+          v[k].x = *reinterpret_cast<const uint16_t*>(address(src));
+      }
+#pragma unroll
+      for (int k = 0; k < kKeepBatch; ++k) {
+        if (j + k >= rows || s_src[j + k] < 0) continue;
+        if (whole)
+          *reinterpret_cast<uint4*>(address(s_dst[j + k])) = v[k];
+        else
+          *reinterpret_cast<uint16_t*>(address(s_dst[j + k])) = (uint16_t)v[k].x;
+      }
+    }
+  }
 }
 
 ts_status run_append(ts_ctx* ctx, const RowsArgs& a, cudaStream_t s) {
@@ -323,7 +296,7 @@ ts_status run_append(ts_ctx* ctx, const RowsArgs& a, cudaStream_t s) {
 
 ts_status launch_append_q4(ts_ctx* ctx, const void* k_new, const void* v_new, const int32_t* page_table,
                            const int32_t* seq_lens, int B, void* k_pool, void* v_pool, cudaStream_t s) {
-  RowsArgs a = base_args(ctx, B, B, page_table, k_pool, v_pool);
+  RowsArgs a = rows_args(ctx, B, B, page_table, k_pool, v_pool);
   a.seq_lens = seq_lens;
   a.src[0] = static_cast<const unsigned char*>(k_new);
   a.src[1] = static_cast<const unsigned char*>(v_new);
@@ -333,7 +306,7 @@ ts_status launch_append_q4(ts_ctx* ctx, const void* k_new, const void* v_new, co
 
 ts_status launch_append_prompt(ts_ctx* ctx, const AppendPromptCall& c, cudaStream_t s) {
   if (c.total == 0) return TS_OK;
-  RowsArgs a = base_args(ctx, c.B, c.total, c.page_table, c.k_pool, c.v_pool);
+  RowsArgs a = rows_args(ctx, c.B, c.total, c.page_table, c.k_pool, c.v_pool);
   const int64_t es = ctx->cfg.kv_dtype == TS_KV_F32 ? 4 : 2;
   a.cu = c.cu_rows;
   a.starts = c.starts;
@@ -348,7 +321,7 @@ ts_status launch_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* sta
                          const int32_t* page_table, const void* k_pool, const void* v_pool, float* k_out, float* v_out,
                          cudaStream_t s) {
   if (total == 0) return TS_OK;
-  RowsArgs a = base_args(ctx, B, total, page_table, const_cast<void*>(k_pool), const_cast<void*>(v_pool));
+  RowsArgs a = rows_args(ctx, B, total, page_table, const_cast<void*>(k_pool), const_cast<void*>(v_pool));
   a.cu = cu_rows;
   a.starts = starts;
   a.dst[0] = k_out;
@@ -362,6 +335,24 @@ ts_status launch_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* sta
   TS_READ_ROWS(TS_KV_BF16, 1) TS_READ_ROWS(TS_KV_BF16, kRowsPerCta)
   TS_READ_ROWS(TS_KV_F32, 1) TS_READ_ROWS(TS_KV_F32, kRowsPerCta)
 #undef TS_READ_ROWS
+  return cuda_status(cudaGetLastError());
+}
+
+ts_status launch_keep_rows(ts_ctx* ctx, const KeepCall& c, cudaStream_t s) {
+  const ts_config& cfg = ctx->cfg;
+  KeepArgs a{c.path, c.path_stride, c.count, c.cu_rows, c.B, c.total, c.seq_lens, c.page_table, cfg.max_pages_per_seq,
+             ctx->page_shift, cfg.num_pages, ctx->max_tokens, cfg.n_kv_heads, cfg.head_dim,
+             {static_cast<unsigned char*>(c.k_pool), static_cast<unsigned char*>(c.v_pool)}, c.layer_bytes, c.new_lens,
+             ctx->status};
+  const int d = cfg.head_dim;
+  const int pieces = 2 * cfg.n_kv_heads * (cfg.kv_dtype == TS_KV_Q4 ? d / 32 + d / 64 : d * (cfg.kv_dtype == TS_KV_F32 ? 4 : 2) / 16);
+  const dim3 grid(c.B, (pieces + kKeepThreads - 1) / kKeepThreads, c.layers);
+  ctx->kernels += 1;
+  switch (cfg.kv_dtype) {
+    case TS_KV_F32: keep_rows_kernel<TS_KV_F32><<<grid, kKeepThreads, 0, s>>>(a); break;
+    case TS_KV_BF16: keep_rows_kernel<TS_KV_BF16><<<grid, kKeepThreads, 0, s>>>(a); break;
+    default: keep_rows_kernel<TS_KV_Q4><<<grid, kKeepThreads, 0, s>>>(a);
+  }
   return cuda_status(cudaGetLastError());
 }
 

@@ -1,0 +1,955 @@
+// Attention of drafted tokens over a paged cache: the last T cached tokens of a sequence are the nodes of a tree of drafts
+// (or the newest tokens of a sequence); each sees the whole prefix and those of the T that its mask names, or
+// that come before it.
+//
+//   s[r][j] = scale <q_r, k_j>      out_r = sum_j 2^(s' - m) v_j / sum_j 2^(s' - m)      (seen j; s' = s log2(e))
+//
+// Every K and V row is needed once per KV head, 4 d bytes, for 4 d G T operations: bound by memory up to G T of
+// about 256 rows, by the tensor cores from there on. Both products run on tcgen05 with their accumulators in tensor
+// memory, as for whole prompts (the softmax with its running maximum is the same), and K and V come page by page.
+//
+// A tile is 128 query rows of one KV head: 128 / G tokens with all G query heads of the group; a block is two
+// neighbouring tiles, which share every key and value tile of 128 tokens. The key tiles of all blocks of all KV heads and
+// sequences, one behind another, are dealt to one CTA per SM in equal, contiguous shares, whatever the lengths are. A
+// share that begins or ends inside a block leaves its sums in fp32 (unnormalised, with maximum and sum), and a second kernel
+// joins them, in order: the same bits every time. Roles of a CTA:
+//   warp 8      loads: the query tiles of an item, then K and V pages (TMA, 128-byte swizzle, slots of 128 tokens)
+//   warp 9      products: S = Q K^T, O += P V
+//   warp 10     finds the items of the share
+//   warp 11     looks through the value tiles that hold drafts or end the sequence (below)
+//   warps 0-3   softmax of tile 0, a thread per row; outputs
+//   warps 4-7   the same of tile 1. Where a block has one tile they have nothing to do, and tile 0 uses both score
+//               buffers in turn, so that the next scores are there when a softmax ends.
+//
+// Masked places hold what they hold: a score that is not seen is replaced before it is used. A value that is not
+// finite would reach other rows through a weight of zero, so among the drafts (and behind the sequence's end, where a page may
+// never have been written) such values come out of the tile in shared memory, their tokens are noted, and the rows that see
+// them get them back in the outputs, read from the pool.
+#include <cmath>
+
+#include "ts_flash.cuh"
+
+namespace ts {
+namespace {
+
+constexpr int kTrRows = 128;     // query rows of a tile
+constexpr int kTrKeys = 128;     // tokens of a key tile
+constexpr int kTrSoftmaxWarps = 8;
+constexpr int kTrThreads = (kTrSoftmaxWarps + 4) * 32;
+// Registers a thread: 168 at launch (65536 / 384), shared out as in the prompt attention.
+constexpr int kTrSoftmaxRegs = 208, kTrOtherRegs = 88;
+static_assert(2 * kTrSoftmaxRegs + kTrOtherRegs <= 3 * 168, "register shares");
+constexpr float kTrMaxSum = 16384.f;   // of a tile's weights against a maximum taken earlier
+
+struct TreeArgs {
+  CUtensorMap q, k, v;           // q [rows][heads][d]; k, v [pages][heads * page size][d]
+  const int32_t* cu;
+  const int32_t* seq_lens;
+  const int32_t* page_table;
+  int pt_stride, page_shift;
+  int64_t num_pages;
+  int max_tokens;
+  const uint32_t* mask;          // or null: causal
+  int mask_words;
+  const __nv_bfloat16* v_pool;
+  int B, total;
+  int H, HKV, G;
+  int tokens;                    // tokens of a tile: 128 / G
+  float scale2;                  // |scale| log2(e)
+  int negate;                    // scale < 0: the products are taken with -Q
+  __nv_bfloat16* out;
+  int64_t out_stride;
+  float* lse;
+  float* part_o;                 // [2 slots per CTA][d / 4][256 rows][4]
+  float2* part_ml;               // [2 slots per CTA][256 rows]: maximum (unscaled), sum
+  int64_t* seq_base;             // [B + 1] key tiles before each sequence's
+  int* status;
+  uint64_t wait_ns;
+};
+
+template <int D>
+struct TrShape {
+  static constexpr int HALVES = D / 64;
+  static constexpr int QT = kTrRows * D * 2;    // bytes of a query tile
+  static constexpr int KT = kTrKeys * D * 2;    // bytes of a key or value tile
+  static constexpr int STAGE = 32 * 128;        // bytes of a softmax warp's output staging: 32 rows of 64 columns
+  static constexpr int SMEM = 2 * QT + 4 * KT + kTrSoftmaxWarps * STAGE + 1024;
+  static_assert(SMEM + 2048 <= 227 * 1024, "shared memory of an SM");
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t S_COL = 0, O_COL = 256;   // buffer i: S at 128 i (weights over its first 64); tile i: O at 256 + 128 i
+};
+
+// A sequence's share of the work.
+struct TreeSeq {
+  int row0, T, n;                // first packed row, drafts, cached tokens (drafts among them)
+  int blocks, tiles;             // blocks of drafts, key tiles of a block
+  int err;
+  __device__ __forceinline__ int64_t work(int HKV) const { return (int64_t)HKV * blocks * tiles; }
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
+  TreeSeq s;
+  s.row0 = a.cu[b];
+  const int end = a.cu[b + 1];
+  s.T = end - s.row0;
+  s.n = a.seq_lens[b];
+  const bool rows_ok = s.row0 >= 0 && end >= s.row0 && end <= a.total && (b != 0 || s.row0 == 0);
+  const bool ok = rows_ok && s.T <= kMaxTree && (!a.mask || s.T <= 32 * a.mask_words) && s.n >= s.T && s.n <= a.max_tokens;
+  s.err = ok ? 0 : TS_ERR_SEQ_LEN;
+  s.blocks = ok ? (s.T + 2 * a.tokens - 1) / (2 * a.tokens) : 0;
+  s.tiles = (s.n + kTrKeys - 1) / kTrKeys;
+  return s;
+}
+
+// Running sums over the lanes.
+__device__ __forceinline__ int64_t warp_scan_ll(int64_t x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(kFull, x, d);
+    if (lane >= d) x += o;
+  }
+  return x;
+}
+
+// First tile of CTA c's share of `work` tiles among `ctas`, and the CTA that has tile t.
+__device__ __forceinline__ int64_t share_begin(int64_t work, int ctas, int c) { return work * c / ctas; }
+__device__ __forceinline__ int share_of(int64_t work, int ctas, int64_t t) { return (int)(((t + 1) * ctas - 1) / work); }
+
+struct TreeItem {
+  int found, row0, T, n, i0;     // sequence; first token (among the drafts) of the block
+  int b, kv, j0, j1;             // key tiles [j0, j1) of the block
+  int slot;                      // where the sums go; -1: the whole block, outputs
+};
+
+// Exponent from reference (ma, a2) to (mb, b2), maxima unscaled and scaled: by the numbers that the weights were taken
+// against where fp32 holds those, else from the exact product.
+__device__ __forceinline__ float from_to(float ma, float a2, float mb, float b2, float scale2) {
+  return far(a2) ? (far(b2) ? (ma - mb) * scale2 : fmaf(ma, scale2, -b2)) : (far(b2) ? -fmaf(mb, scale2, -a2) : a2 - b2);
+}
+
+// The 128 bits of keys [key0, key0 + 128) that draft `tok` (packed row `row`) sees, the drafts beginning at key `d0`.
+__device__ __forceinline__ void seen_bits(const TreeArgs& a, int row, int tok, int T, int d0, int key0, uint32_t (&bits)[4]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int k = key0 + 32 * w - d0;          // first key of the word, counted from the drafts' first
+    uint32_t m;
+    if (a.mask) {
+      const uint32_t* words = a.mask + (int64_t)row * a.mask_words;
+      // arithmetic shift: k may lie before the drafts
+      const int at = k >> 5, sh = k & 31, last = (T + 31) >> 5;
+      const uint32_t lo = at >= 0 && at < last ? words[at] : (at < 0 ? 0xffffffffu : 0u);
+      const uint32_t hi = at + 1 >= 0 && at + 1 < last ? words[at + 1] : (at + 1 < 0 ? 0xffffffffu : 0u);
+      m = __funnelshift_r(lo, hi, sh);
+    } else {
+      const int lim = tok - k;                 // the last seen bit
+      m = lim < 0 ? 0u : (lim >= 31 ? 0xffffffffu : (2u << lim) - 1u);
+    }
+    const int left = T - k;                    // bits before the sequence's end
+    if (left < 32) m = left <= 0 ? 0u : m & ((1u << left) - 1u);
+    bits[w] = m;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
+  using S = TrShape<D>;
+  extern __shared__ unsigned char dsm_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* sQ = base;                // two query tiles
+  unsigned char* sK = sQ + 2 * S::QT;      // two key slots
+  unsigned char* sV = sK + 2 * S::KT;      // two value slots
+  unsigned char* sO = sV + 2 * S::KT;      // output staging, one area per softmax warp
+  __shared__ __align__(8) uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], s_full[2],
+      p_ready[2], o_done[2], item_full[2], item_empty[2], item_clean[2], drained;
+  __shared__ uint32_t s_tmem;
+  __shared__ TreeItem s_item[2];
+  __shared__ uint32_t s_odd[2][kMaxTree / 32];   // drafts whose values are not all finite, per item slot
+  __shared__ int s_any_odd[2];
+  // keys of a tile whose page lies outside the pool, per key tile (of the last four), and whether there are any: the
+  // loads run at most three tiles ahead of the softmax
+  __shared__ uint32_t s_bad[4][4];
+  __shared__ uint32_t s_any_bad[4];
+
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
+  const uint64_t settle = a.wait_ns > kWaitLimitNs ? a.wait_ns : kWaitLimitNs;   // for what is in flight at the end
+
+  if (warp == kTrSoftmaxWarps + 1) {
+    tmem_alloc(&s_tmem, S::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&drained, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 2);           // the products and the look through
+      mbar_init(&v_clean[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_ready[i], kTrSoftmaxWarps / 2);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], kTrSoftmaxWarps + 3);
+      mbar_init(&item_clean[i], 1);
+      s_any_odd[i] = 0;
+    }
+    mbar_fence_init();
+  }
+  if (tid < 2 * (kMaxTree / 32)) (&s_odd[0][0])[tid] = 0u;
+  tc_fence_before();
+  if (warp == kTrSoftmaxWarps && lane == 0) {
+    prefetch_tmap(&a.q);
+    prefetch_tmap(&a.k);
+    prefetch_tmap(&a.v);
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may set itself up where there is room
+
+  // Item k of this CTA is in slot k % 2. From it every role derives the same: whether the block has a second tile, the
+  // first key tile that holds drafts (or what is behind the sequence).
+  auto read_item = [&](int k, TreeItem& it, bool& two, int& drafts_from) -> bool {
+    if (!mbar_wait(&item_full[k & 1], (k >> 1) & 1, a.wait_ns)) return false;
+    it = s_item[k & 1];
+    two = it.i0 + a.tokens < it.T;
+    drafts_from = (it.n - it.T) / kTrKeys;
+    return true;
+  };
+  TreeItem it;
+  bool two;
+  int drafts_from;
+
+  if (warp >= kTrSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTrOtherRegs));
+    if (warp == kTrSoftmaxWarps) {
+      // ---------------------------------------------------------------- loads
+      bool ok = true;
+      int items = 0, g = 0;                                       // loaded so far: items' queries, key tiles
+      int kn = 0, vn = 0;
+      const int ps = 1 << a.page_shift, per_tile = kTrKeys >> a.page_shift;
+      auto all = [&](bool x) -> bool { return __all_sync(kFull, x); };
+      for (;;) {
+        ok = all(read_item(items, it, two, drafts_from));
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[items & 1]);
+        if (!it.found) break;
+        if (items > 0) ok = all(mbar_wait(&q_empty, (items - 1) & 1, a.wait_ns));
+        if (!ok) break;
+        const int tiles_q = two ? 2 : 1;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full, (uint32_t)(tiles_q * S::HALVES * a.G * a.tokens * 128));
+          for (int i = 0; i < tiles_q; ++i)
+            for (int h = 0; h < S::HALVES; ++h)
+              tma_load_3d(sQ + i * S::QT + h * (kTrRows * 128), &a.q, h * 64, it.kv * a.G, it.row0 + it.i0 + i * a.tokens,
+                          &q_full);
+        }
+        ++items;
+        const int32_t* pages = a.page_table + (int64_t)it.b * a.pt_stride;
+        const int n_pages = (it.n + ps - 1) >> a.page_shift;
+        // this lane's pages of a tile; -1 (the copy is filled with zeros) behind the sequence and for no page of the pool
+        auto page_of = [&](int j, int k) -> int {
+          const int p = j * per_tile + lane + 32 * k;
+          return lane + 32 * k < per_tile && p < n_pages ? pages[p] : -1;
+        };
+        int next[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) next[k] = page_of(it.j0, k);
+        for (int j = it.j0; j < it.j1; ++j, ++g) {
+          int cur[4];
+          uint32_t bad[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            cur[k] = next[k];
+            const bool there = lane + 32 * k < per_tile && j * per_tile + lane + 32 * k < n_pages;
+            const bool out = there && (cur[k] < 0 || (int64_t)cur[k] >= a.num_pages);
+            if (out) cur[k] = -1;
+            const unsigned m = __ballot_sync(kFull, out);
+            if (m) {
+              if (lane == 0) set_error(a.status, TS_ERR_PAGE_OOB);
+              if (ps == 1) {
+                bad[k] = m;
+              } else {                                            // (k is 0: eight pages, two to a word)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                  bad[w] |= (m >> (2 * w) & 1u ? 0xffffu : 0u) | (m >> (2 * w + 1) & 1u ? 0xffff0000u : 0u);
+              }
+            }
+          }
+          if (j + 1 < it.j1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) next[k] = page_of(j + 1, k);
+          }
+          const int s = g & 1;
+          if (g >= 2) ok = all(mbar_wait(&k_empty[s], ((g >> 1) - 1) & 1, a.wait_ns));
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t any = bad[0] | bad[1] | bad[2] | bad[3];
+            s_any_bad[g & 3] = any;
+            if (any) {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) s_bad[g & 3][w] = bad[w];
+            }
+            mbar_arrive_expect_tx(&k_full[s], S::KT);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (lane + 32 * k < per_tile)
+              for (int h = 0; h < S::HALVES; ++h)
+                tma_load_3d(sK + s * S::KT + h * (kTrKeys * 128) + (lane + 32 * k) * ps * 128, &a.k, h * 64, it.kv * ps, cur[k],
+                            &k_full[s]);
+          ++kn;
+          if (g >= 2) ok = all(mbar_wait(&v_empty[s], ((g >> 1) - 1) & 1, a.wait_ns));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&v_full[s], S::KT);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (lane + 32 * k < per_tile)
+              for (int h = 0; h < S::HALVES; ++h)
+                tma_load_3d(sV + s * S::KT + h * (kTrKeys * 128) + (lane + 32 * k) * ps * 128, &a.v, h * 64, it.kv * ps, cur[k],
+                            &v_full[s]);
+          ++vn;
+        }
+        if (!ok) break;
+      }
+      if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
+      // nothing may still be landing when the CTA exits, however short the limit was that a role gave up at
+      if (items > 0) mbar_wait(&q_full, (items - 1) & 1, settle);
+      for (int j = max(0, kn - 2); j < kn; ++j) mbar_wait(&k_full[j & 1], (j >> 1) & 1, settle);
+      for (int j = max(0, vn - 2); j < vn; ++j) mbar_wait(&v_full[j & 1], (j >> 1) & 1, settle);
+      __syncwarp();
+    } else if (warp == kTrSoftmaxWarps + 1) {
+      // ------------------------------------------------------------- products
+      // (the whole warp goes through the loop and one lane issues, with descriptors in uniform registers)
+      const uint32_t idesc_s = idesc_bf16_f32(kTrRows, kTrKeys) | (a.negate ? 1u << 13 : 0u);   // bit 13: -A
+      constexpr uint32_t idesc_o = idesc_bf16_f32_bmn(kTrRows, D);
+      const uint64_t dq = sdesc_sw128(smem_addr(sQ)), dk = sdesc_sw128(smem_addr(sK));
+      const uint64_t dv = sdesc_sw128_mn(smem_addr(sV), kTrKeys * 128, 1024);
+      const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
+      const uint32_t qk_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32);
+      // scores of query tile i and the key slot into buffer x
+      auto scores = [&](int i, int slot, int x) {
+        const uint32_t ql = q_lo + i * (S::QT >> 4), kl = k_lo + slot * (S::KT >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int h = 0; h < S::HALVES; ++h)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16(tmem + S::S_COL + 128 * x, sdesc_from(ql + ((h * (kTrRows * 128) + ks * 32) >> 4), qk_hi),
+                        sdesc_from(kl + ((h * (kTrKeys * 128) + ks * 32) >> 4), qk_hi), idesc_s, (h | ks) != 0);
+          umma_commit(&s_full[x]);
+        }
+        __syncwarp();
+      };
+      // the outputs of tile i take the weights of buffer x
+      auto outputs = [&](int i, int slot, int x, bool more) {
+        const uint32_t vl = v_lo + slot * (S::KT >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < kTrKeys / 16; ++ks)
+            umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * x + 8 * ks, sdesc_from(vl + ((ks * 2048) >> 4), v_hi),
+                         idesc_o, more || ks != 0);
+          umma_commit(&o_done[x]);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(kFull, mbar_wait(bar, parity, a.wait_ns)); };
+      bool ok = true;
+      int kt = 0;                                                 // key tiles of the items before
+      uint32_t clean_par = 0u, p_par = 0u;                        // parities of the next waits, by slot and by buffer
+      for (int k = 0;; ++k) {
+        ok = __all_sync(kFull, read_item(k, it, two, drafts_from));
+        if (!ok) break;
+        const bool found = __shfl_sync(kFull, it.found, 0) != 0, pair = __shfl_sync(kFull, two ? 1 : 0, 0) != 0;
+        const int nt = __shfl_sync(kFull, it.j1 - it.j0, 0), look = __shfl_sync(kFull, drafts_from - it.j0, 0);
+        if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+        __syncwarp();
+        if (!found) break;
+        ok = wait(&q_full, k & 1) && wait(&k_full[kt & 1], (kt >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const int ahead = pair ? 1 : 2;                           // key tiles whose scores are taken before the first outputs
+        scores(0, kt & 1, 0);
+        if (pair) scores(1, kt & 1, 1);
+        commit(&k_empty[kt & 1]);
+        if (!pair && nt > 1) {
+          ok = wait(&k_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          scores(0, (kt + 1) & 1, 1);
+          commit(&k_empty[(kt + 1) & 1]);
+        }
+        if (nt <= ahead) commit(&q_empty);
+        for (int j = 0; j < nt && ok; ++j) {
+          const int g = kt + j, s = g & 1;
+          ok = wait(&v_full[s], (g >> 1) & 1);
+          if (ok && j >= look) {
+            ok = wait(&v_clean[s], (clean_par >> s) & 1u);
+            clean_par ^= 1u << s;
+          }
+          if (!ok) break;
+          const int n1 = j + ahead, s1 = (kt + n1) & 1;           // the key tile whose scores come next
+          const bool next = n1 < nt;
+          for (int i = 0; i < (pair ? 2 : 1) && ok; ++i) {
+            const int x = pair ? i : j & 1;
+            ok = wait(&p_ready[x], (p_par >> x) & 1u);
+            p_par ^= 1u << x;
+            if (ok && next && i == 0) ok = wait(&k_full[s1], ((kt + n1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            outputs(i, s, x, j != 0);
+            if (next) scores(i, s1, x);
+          }
+          if (!ok) break;
+          commit(&v_empty[s]);
+          if (next) commit(&k_empty[s1]);
+          if (n1 + 1 == nt) commit(&q_empty);
+        }
+        if (!ok) break;
+        kt += nt;
+      }
+      if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
+      // no product may be under way when tensor memory is given back
+      commit(&drained);
+      mbar_wait(&drained, 0, settle);
+      __syncwarp();
+    } else if (warp == kTrSoftmaxWarps + 2) {
+      // ---------------------------------------------------------------- items
+      int64_t work = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        TreeSeq s{};
+        if (b < a.B) s = tree_seq(a, b);
+        const int64_t w = b < a.B ? s.work(a.HKV) : 0;
+        const int64_t run = work + warp_scan_ll(w, lane);
+        if (blockIdx.x == 0 && b < a.B) {
+          if (s.err) set_error(a.status, s.err);
+          a.seq_base[b + 1] = run;
+          if (b == 0) a.seq_base[0] = 0;
+        }
+        work = __shfl_sync(kFull, run, 31);
+      }
+      const int ctas = (int)min((int64_t)gridDim.x, work);
+      int64_t t = 0, e = 0;
+      if ((int)blockIdx.x < ctas) {
+        t = share_begin(work, ctas, blockIdx.x);
+        e = share_begin(work, ctas, blockIdx.x + 1);
+      }
+      const int64_t begin = t;
+      int b0 = 0;                                                 // the sequences looked at: 32 from b0 on
+      int64_t before = 0;                                         // tiles of the sequences before them
+      bool found = true;
+      for (int k = 0; found; ++k) {
+        found = t < e;
+        TreeItem item{};
+        if (found) {
+          for (;;) {                                              // the sequence of tile t
+            const int b = b0 + lane;
+            TreeSeq s{};
+            if (b < a.B) s = tree_seq(a, b);
+            const int64_t w = b < a.B ? s.work(a.HKV) : 0;
+            const int64_t run = warp_scan_ll(w, lane);
+            const unsigned m = __ballot_sync(kFull, before + run > t);
+            if (m || b0 + 32 >= a.B) {
+              const int src = m ? __ffs(m) - 1 : 31;
+              const int64_t start = before + __shfl_sync(kFull, run - w, src);
+              item.row0 = __shfl_sync(kFull, s.row0, src);
+              item.T = __shfl_sync(kFull, s.T, src);
+              item.n = __shfl_sync(kFull, s.n, src);
+              const int tiles = __shfl_sync(kFull, s.tiles, src), blocks = __shfl_sync(kFull, s.blocks, src);
+              if (!m) {                                           // (not reached: t lies below the work)
+                found = false;
+                break;
+              }
+              const int64_t u = (t - start) / tiles;
+              item.b = b0 + src;
+              item.kv = (int)(u / blocks);
+              item.i0 = (int)(u % blocks) * 2 * a.tokens;
+              item.j0 = (int)((t - start) % tiles);
+              item.j1 = (int)min((int64_t)tiles, item.j0 + (e - t));
+              item.slot = item.j0 == 0 && item.j1 == tiles ? -1 : 2 * (int)blockIdx.x + (t == begin ? 0 : 1);
+              t += item.j1 - item.j0;
+              break;
+            }
+            before += __shfl_sync(kFull, run, 31);
+            b0 += 32;
+          }
+        }
+        item.found = found;
+        if (k >= 2 && !__all_sync(kFull, mbar_wait(&item_empty[k & 1], ((k >> 1) - 1) & 1, a.wait_ns))) {
+          if (lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
+          break;
+        }
+        if (s_any_odd[k & 1]) {
+          if (lane < kMaxTree / 32) s_odd[k & 1][lane] = 0u;
+          __syncwarp();
+          if (lane == 0) s_any_odd[k & 1] = 0;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          s_item[k & 1] = item;
+          mbar_arrive(&item_full[k & 1]);
+        }
+        __syncwarp();
+      }
+    } else {
+      // ----------------------------------- values that are not finite among the drafts and behind them
+      bool ok = true;
+      int kt = 0;
+      for (int k = 0;; ++k) {
+        ok = __all_sync(kFull, read_item(k, it, two, drafts_from));
+        if (!ok || !it.found) break;
+        for (int j = it.j0; j < it.j1 && ok; ++j, ++kt) {
+          const int vs = kt & 1;
+          ok = __all_sync(kFull, mbar_wait(&v_full[vs], (kt >> 1) & 1, a.wait_ns));
+          if (!ok) break;
+          if (j >= drafts_from) {
+            unsigned char* vt = sV + vs * S::KT;
+            uint32_t odd = 0u;
+#pragma unroll 8
+            for (int c = 0; c < S::KT / 512; ++c) {
+              const uint4 w = lds128(vt + c * 512 + lane * 16);
+              odd |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                     ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+            }
+            if (odd & 0x80008000u) {
+              for (int off = lane * 16; off < S::KT; off += 512) {               // byte in the tile
+                const int r = (off % (kTrKeys * 128)) / 128, at = j * kTrKeys + r - (it.n - it.T);
+                if (at < 0) continue;                             // every row sees it
+                uint16_t* e16 = reinterpret_cast<uint16_t*>(vt + off);
+                for (int e = 0; e < 8; ++e) {
+                  if ((e16[e] & 0x7f80u) != 0x7f80u) continue;
+                  e16[e] = 0;
+                  if (at < it.T) {
+                    atomicOr(&s_odd[k & 1][at >> 5], 1u << (at & 31));
+                    s_any_odd[k & 1] = 1;
+                  }
+                }
+              }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_clean[vs]);
+          }
+          // (also for the tiles not looked at: so this warp never falls a round behind the value slots)
+          if (lane == 0) mbar_arrive(&v_empty[vs]);
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive(&item_clean[k & 1]);
+          mbar_arrive(&item_empty[k & 1]);
+        }
+        __syncwarp();
+      }
+      if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTrSoftmaxRegs));
+    const int i = warp >> 2;                                      // tile
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t inv_g = 65536u / (uint32_t)a.G + 1u;           // r / G = (r inv_g) >> 16 for r < 128, G <= 16
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tO = tmem + S::O_COL + 128 * i + lane_off;
+    bool ok = true;
+    // parities of the next score tile and of the last outputs, by buffer (a block with one tile uses both)
+    uint32_t s_par = 0u, o_par = 0u;
+    int kt = 0;                                                   // key tiles of the items before
+    for (int k = 0; ok; ++k) {
+      ok = __all_sync(kFull, read_item(k, it, two, drafts_from));
+      if (!ok || !it.found) break;
+      const int slot = k & 1, nt = __shfl_sync(kFull, it.j1 - it.j0, 0);
+      const bool pair = __shfl_sync(kFull, two ? 1 : 0, 0) != 0;
+      if (i == 0 || pair) {
+        const int first = it.i0 + i * a.tokens;                   // first draft of the tile
+        const int row_tok = (int)((uint32_t)row * inv_g >> 16), tok = first + row_tok;
+        const bool real = row_tok < a.tokens && tok < it.T;
+        const bool idle = !__any_sync(kFull, real);               // no row of this warp is a query: it only keeps step
+        const int d0 = it.n - it.T;                               // first draft's position
+        const int packed = it.row0 + (real ? tok : 0);
+        float mx = -INFINITY, la = 0.f, lb = 0.f;                 // running maximum (unscaled) and two halves of the sum
+        int x_last = 0;
+        for (int j = 0; j < nt; ++j) {
+          const int x = pair ? i : j & 1, key0 = (it.j0 + j) * kTrKeys;
+          const uint32_t tS = tmem + S::S_COL + 128 * x + lane_off;
+          ok = __all_sync(kFull, mbar_wait(&s_full[x], (s_par >> x) & 1u, a.wait_ns));
+          if (!ok) break;
+          tc_fence_after();
+          s_par ^= 1u << x;
+          if (!idle) {
+            // what is not seen in this tile: drafts, what is behind the sequence, pages outside the pool
+            const int ring = (kt + j) & 3;
+            const bool any_bad = s_any_bad[ring] != 0u;
+            const bool cut = key0 + kTrKeys > d0 || any_bad;
+            uint32_t bits[4];
+            if (cut) {
+              seen_bits(a, packed, tok, it.T, d0, key0, bits);
+              if (any_bad) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) bits[w] &= ~s_bad[ring][w];
+              }
+            }
+            // Weights against the maximum that the row has, which covers most tiles. Where their sum says that
+            // it does not (and in the first tile, which has none), the scores, still in tensor memory, are read
+            // again and the maximum is taken first.
+            uint32_t p[64];
+            float ta, tb, m2 = mx * a.scale2;
+            bool over = real;                                     // this row needs its maximum (in a pass that takes it)
+            for (bool raise = j == 0;; raise = true) {
+              uint32_t u[128];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) tmem_ld_x32(tS + 32 * c, u + 32 * c);
+              tmem_wait_ld();
+              float* y = reinterpret_cast<float*>(u);
+              if (cut) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) y[c] = bits[c >> 5] >> (c & 31) & 1u ? y[c] : -INFINITY;
+              }
+              if (raise) {
+                float ma = y[0], mb = y[1];
+#pragma unroll
+                for (int c = 2; c < 128; c += 2) {
+                  ma = fmaxf(ma, y[c]);
+                  mb = fmaxf(mb, y[c + 1]);
+                }
+                // each row by itself, so that no row's bits depend on another's: rows that do not need it keep their
+                // maximum, as do rows that are no query of the sequence (their operands may be anything)
+                const float mn = over ? fmaxf(mx, fmaxf(ma, mb)) : mx, n2 = mn * a.scale2;
+                const float f = mn == mx ? 1.f : pr_ex2(from_to(mx, m2, mn, n2, a.scale2));
+                mx = mn;
+                m2 = n2;
+                la *= f;
+                lb *= f;
+                if (j > 0) {
+                  // the last product must be in before its accumulators are rescaled
+                  ok = __all_sync(kFull, mbar_wait(&o_done[x_last], (o_par >> x_last & 1u) ^ 1u, a.wait_ns));
+                  if (!ok) break;
+                  tc_fence_after();
+                  // (rare, and the scores hold most registers: eight columns at a time)
+#pragma unroll 1
+                  for (int c = 0; c < D; c += 8) {
+                    float o[8];
+                    tmem_ld_x8(tO + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] *= f;
+                    tmem_st_x8(tO + c, o);
+                  }
+                }
+              }
+              float ms = m2 == -INFINITY ? 0.f : -m2;             // nothing seen yet: every weight is zero
+              if (raise && __any_sync(kFull, far(m2) && m2 != -INFINITY)) {
+                const bool shift = far(m2) && m2 != -INFINITY;
+                const float off = shift ? mx : 0.f;
+                ms = shift ? 0.f : ms;
+#pragma unroll
+                for (int c = 0; c < 128; c += 2) add2(y[c], y[c + 1], -off, -off);
+              }
+              const uint64_t sc = pack_f2(a.scale2, a.scale2), mm = pack_f2(ms, ms);
+              ta = tb = 0.f;
+#pragma unroll
+              for (int c = 0; c < 64; ++c) {
+                float y0, y1;
+                unpack_f2(fma_f2(pack_f2(y[2 * c], y[2 * c + 1]), sc, mm), y0, y1);
+                y0 = pr_ex2(y0);
+                y1 = pr_ex2(y1);
+                add2(ta, tb, y0, y1);
+                p[c] = pack_bf16(y0, y1);
+              }
+              if (raise) break;
+              over = real && (!(ta + tb <= kTrMaxSum) || far(m2));
+              if (!__any_sync(kFull, over)) break;
+            }
+            if (!ok) break;
+            la += ta;
+            lb += tb;
+            tmem_st_x32(tS, p);
+            tmem_st_x32(tS + 32, p + 32);
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[x]);
+          o_par ^= 1u << x;
+          x_last = x;
+        }
+        // ---- outputs
+        if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[x_last], (o_par >> x_last & 1u) ^ 1u, a.wait_ns));
+        if (ok) ok = __all_sync(kFull, mbar_wait(&item_clean[slot], (k >> 1) & 1, a.wait_ns));
+        if (ok && !idle) {
+          tc_fence_after();
+          const float l = la + lb;
+          const int head = it.kv * a.G + row - row_tok * a.G;
+          // values that are not finite, of the drafts that the row sees, for columns [col, col + 32)
+          const bool odd = s_any_odd[slot] != 0;
+          auto put_back = [&](int col, uint32_t (&o)[32]) {
+            for (int t = it.j0 * kTrKeys > d0 ? it.j0 * kTrKeys - d0 : 0; t < min(it.T, it.j1 * kTrKeys - d0); ++t) {
+              if (!(s_odd[slot][t >> 5] >> (t & 31) & 1u)) continue;
+              uint32_t one[4];
+              seen_bits(a, packed, tok, it.T, d0, d0 + t, one);
+              if (!real || !(one[0] & 1u)) continue;
+              const int pos = d0 + t, ps = 1 << a.page_shift;
+              const int page = a.page_table[(int64_t)it.b * a.pt_stride + (pos >> a.page_shift)];
+              const __nv_bfloat16* v = a.v_pool + ((((int64_t)page * a.HKV + it.kv) << a.page_shift) + (pos & (ps - 1))) * D + col;
+              for (int e = 0; e < 32; ++e) {
+                const float y = __bfloat162float(v[e]);
+                if (!isfinite(y)) {
+#pragma unroll
+                  for (int z = 0; z < 32; ++z)
+                    if (z == e) o[z] = __float_as_uint(__uint_as_float(o[z]) + y);
+                }
+              }
+            }
+          };
+          if (it.slot >= 0) {
+            // sums of a part of the block: 16 bytes of 32 neighbouring rows side by side
+            const int at = 128 * i + row;
+            if (real) a.part_ml[(int64_t)it.slot * 256 + at] = make_float2(mx, l);
+            float4* dst = reinterpret_cast<float4*>(a.part_o) + (int64_t)it.slot * (D / 4) * 256 + at;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld_x32(tO + 32 * c, o);
+              tmem_wait_ld();
+              if (odd) put_back(32 * c, o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (real)
+                  dst[(int64_t)(8 * c + e) * 256] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                                __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            }
+          } else {
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (a row that sees nothing: zeros)
+            if (real && a.lse)
+              a.lse[(int64_t)packed * a.H + head] = l == 0.f ? -INFINITY : (mx * a.scale2 + log2f(l)) * 0.6931471805599453f;
+            // this lane's output row; a null pointer where it is none
+            const uint64_t dst = real ? reinterpret_cast<uint64_t>(a.out + (int64_t)packed * a.out_stride + (int64_t)head * D) : 0u;
+            unsigned char* stage = sO + warp * S::STAGE;
+#pragma unroll 1
+            for (int h = 0; h < S::HALVES; ++h) {
+              // 64 columns of 32 rows through this warp's staging area (swizzled like the operands), so that a
+              // store covers whole 128-byte pieces of four rows instead of 16 bytes of 32
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint32_t o[32];
+                tmem_ld_x32(tO + 64 * h + 32 * c, o);
+                tmem_wait_ld();
+                if (odd) put_back(64 * h + 32 * c, o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int z = 0; z < 4; ++z)
+                    w[z] = pack_bf16(__uint_as_float(o[8 * e + 2 * z]) * inv, __uint_as_float(o[8 * e + 2 * z + 1]) * inv);
+                  *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + e) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+              __syncwarp();
+#pragma unroll
+              for (int r4 = 0; r4 < 8; ++r4) {
+                const int rl = 4 * r4 + (lane >> 3), c16 = lane & 7;
+                const uint64_t to = __shfl_sync(kFull, dst, rl);
+                const uint4 v = lds128(stage + rl * 128 + ((c16 ^ (rl & 7)) << 4));
+                if (to) *reinterpret_cast<uint4*>(to + 128 * h + c16 * 16) = v;
+              }
+              __syncwarp();
+            }
+          }
+          // the accumulators have been read before the next item's weights let a product write them
+          tc_fence_before();
+        }
+      }
+      if (i == 1 && !pair) {
+        // Tile 0 goes through both buffers. These warps follow it, phase by phase: a parity tells a phase only from its
+        // neighbours, so one who ran ahead would take a phase of this item for one of the next.
+        for (int j = 0; j < nt && ok; ++j) {
+          ok = __all_sync(kFull, mbar_wait(&s_full[j & 1], (s_par >> (j & 1)) & 1u, a.wait_ns));
+          s_par ^= 1u << (j & 1);
+          o_par ^= 1u << (j & 1);
+        }
+      } else if (pair) {
+        // the other tile's buffer took nt phases (what this tile waits for next was issued behind all of them)
+        const uint32_t flip = (uint32_t)(nt & 1) << (i ^ 1);
+        s_par ^= flip;
+        o_par ^= flip;
+      }
+      kt += nt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
+    }
+    if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kTrSoftmaxWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::TMEM_COLS);
+  }
+}
+
+// Joins the sums of blocks that several CTAs had parts of. Eight rows of one KV head to a CTA (neighbouring rows of a block:
+// heads, then tokens), a thread per row and four columns. Bound by the parts read (from L2).
+constexpr int kJoinRows = 8;
+constexpr int kJoinParts = 256;  // CTAs of a call, at most
+
+template <int D>
+__global__ void __launch_bounds__(kJoinRows * D / 4) join_kernel(const __grid_constant__ TreeArgs a, int grid) {
+  constexpr int COLS = D / 4;
+  __shared__ int s_first[kJoinRows], s_parts[kJoinRows], s_at[kJoinRows], s_slot0[kJoinRows];
+  __shared__ float s_f[kJoinRows][kJoinParts];
+  const int tid = threadIdx.x;
+  const int64_t per_kv = (int64_t)a.total * a.G;
+  const int row = tid / COLS, col = tid % COLS;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t idx = (int64_t)blockIdx.x * kJoinRows + row;
+  const int kv = (int)(idx / per_kv);
+  const int packed = (int)(idx % per_kv / a.G), head = (int)(idx % a.G);
+  if (col == 0) {
+    s_parts[row] = 0;
+    if (kv < a.HKV) {
+      int lo = 0, hi = a.B;                                       // the last sequence that begins at or before the row
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu[mid] <= packed) lo = mid; else hi = mid;
+      }
+      const TreeSeq s = tree_seq(a, lo);
+      const int64_t work = a.seq_base[a.B];
+      if (s.blocks > 0 && packed >= s.row0 && packed < s.row0 + s.T) {
+        const int ctas = (int)min((int64_t)grid, work);
+        const int tok = packed - s.row0, block = tok / (2 * a.tokens), in = tok - block * 2 * a.tokens;
+        const int64_t t0 = a.seq_base[lo] + ((int64_t)kv * s.blocks + block) * s.tiles;
+        const int c0 = share_of(work, ctas, t0), c1 = share_of(work, ctas, t0 + s.tiles - 1);
+        s_first[row] = c0;
+        s_parts[row] = c1 > c0 ? c1 - c0 + 1 : 0;                 // (else the block's outputs are there)
+        s_slot0[row] = 2 * c0 + (share_begin(work, ctas, c0) < t0 ? 1 : 0);
+        s_at[row] = (in / a.tokens) * 128 + in % a.tokens * a.G + head;
+      }
+    }
+  }
+  __syncthreads();
+  const int parts = s_parts[row];
+  auto slot_of = [&](int k) { return k == 0 ? s_slot0[row] : 2 * (s_first[row] + k); };
+  // every part's factor: the row's columns share the parts out
+  float M = -INFINITY, total = 0.f;
+  for (int k = col; k < parts; k += COLS) {
+    const float2 ml = a.part_ml[(int64_t)slot_of(k) * 256 + s_at[row]];
+    M = fmaxf(M, ml.y > 0.f || ml.y != ml.y ? ml.x : -INFINITY);
+  }
+  // (COLS is 16 or 32: a row's columns lie in one warp)
+#pragma unroll
+  for (int d = COLS / 2; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, d));
+  const float M2 = M * a.scale2;
+  for (int k = col; k < parts; k += COLS) {
+    const float2 ml = a.part_ml[(int64_t)slot_of(k) * 256 + s_at[row]];
+    const float f = ml.y == 0.f ? 0.f : (ml.x == M ? 1.f : pr_ex2(from_to(ml.x, ml.x * a.scale2, M, M2, a.scale2)));
+    s_f[row][k] = f;
+  }
+  __syncthreads();
+  if (parts == 0) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* src = reinterpret_cast<const float4*>(a.part_o) + (int64_t)col * 256 + s_at[row];
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) {
+    const float f = s_f[row][k];
+    const int slot = slot_of(k);
+    const float4 o = src[(int64_t)slot * COLS * 256];
+    const float l = a.part_ml[(int64_t)slot * 256 + s_at[row]].y;
+    if (f != 0.f) {                                               // (a part whose weight vanishes may hold anything)
+      total = fmaf(f, l, total);
+      acc.x = fmaf(f, o.x, acc.x);
+      acc.y = fmaf(f, o.y, acc.y);
+      acc.z = fmaf(f, o.z, acc.z);
+      acc.w = fmaf(f, o.w, acc.w);
+    }
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  __nv_bfloat16* out = a.out + (int64_t)packed * a.out_stride + (int64_t)(kv * a.G + head) * D + col * 4;
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (a.lse && col == 0)
+    a.lse[(int64_t)packed * a.H + kv * a.G + head] =
+        total == 0.f ? -INFINITY : (M2 + log2f(total)) * 0.6931471805599453f;
+}
+
+// bf16 [pages][heads * page size][d] in boxes of 64 elements x one page of one head.
+bool pages_map(CUtensorMap* map, const void* pool, int64_t pages, int rows, int d, int page_size) {
+  const auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)rows * d * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)page_size, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+ts_status run_tree(ts_ctx* ctx, const TreeArgs& a, cudaStream_t s) {
+  if (!ensure_smem<tree_kernel<D>>((size_t)TrShape<D>::SMEM, ctx->device)) return TS_ERR_CUDA;
+  ProfScope ps(ctx, TS_PROF_ATTEND, s);
+  ctx->kernels += 2;
+  const int grid = ctx->num_sms < kJoinParts ? ctx->num_sms : kJoinParts;
+  tree_kernel<D><<<grid, kTrThreads, TrShape<D>::SMEM, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_status(e);
+  const int64_t rows = (int64_t)a.total * a.H;
+  return cuda_status(launch_behind(join_kernel<D>, dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows)), kJoinRows * D / 4, s, a, grid));
+}
+
+}  // namespace
+
+bool tree_supported(const ts_config& c) {
+  return c.kv_dtype == TS_KV_BF16 && (c.head_dim == 64 || c.head_dim == 128) && c.n_q_heads / c.n_kv_heads <= 16;
+}
+
+int64_t tree_part_slots(int num_sms) { return 2 * (int64_t)num_sms; }
+
+ts_status launch_tree_attend(ts_ctx* ctx, const TreeCall& c, cudaStream_t s) {
+  if (c.total == 0) return TS_OK;
+  const ts_config& cfg = ctx->cfg;
+  TreeArgs a{};
+  a.cu = c.cu_rows;
+  a.seq_lens = c.seq_lens;
+  a.page_table = c.page_table;
+  a.pt_stride = cfg.max_pages_per_seq;
+  a.page_shift = ctx->page_shift;
+  a.num_pages = cfg.num_pages;
+  a.max_tokens = ctx->max_tokens;
+  a.mask = reinterpret_cast<const uint32_t*>(c.mask);
+  a.mask_words = c.mask_words;
+  a.v_pool = static_cast<const __nv_bfloat16*>(c.v_pool);
+  a.B = c.B;
+  a.total = c.total;
+  a.H = cfg.n_q_heads;
+  a.HKV = cfg.n_kv_heads;
+  a.G = a.H / a.HKV;
+  a.tokens = kTrRows / a.G;
+  a.scale2 = std::fabs(c.scale) * 1.4426950408889634f;
+  a.negate = c.scale < 0.f;
+  a.out = static_cast<__nv_bfloat16*>(c.out);
+  a.out_stride = c.out_stride;
+  a.lse = c.lse;
+  a.part_o = ctx->tree_part_o;
+  a.part_ml = ctx->tree_part_ml;
+  a.seq_base = ctx->tree_base;
+  a.status = ctx->status;
+  a.wait_ns = ctx->wait_ns;
+  const int ps = 1 << ctx->page_shift, rows = a.HKV * ps;
+  if (!rows_map(&a.q, c.q, c.total, a.H, cfg.head_dim, c.q_stride, a.G, a.tokens) ||
+      !pages_map(&a.k, c.k_pool, cfg.num_pages, rows, cfg.head_dim, ps) ||
+      !pages_map(&a.v, c.v_pool, cfg.num_pages, rows, cfg.head_dim, ps))
+    return TS_ERR_CUDA;
+  return cfg.head_dim == 64 ? run_tree<64>(ctx, a, s) : run_tree<128>(ctx, a, s);
+}
+
+}  // namespace ts

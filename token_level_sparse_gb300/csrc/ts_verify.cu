@@ -1,0 +1,348 @@
+// Which drafted tokens of a tree the target keeps, and the token behind them (ts_verify_tree).
+//
+// At a node with target distribution p and draft distribution q the children are tried in order. A child x is taken
+// where u q(x) Z < r(x) W; else, r being the residual, its mass moves on:
+//
+//   r_0 = p, Z_0 = 1, W_0 = 1      r_k = max(r_(k-1) - Z_(k-1) q / W_(k-1), 0),  Z_k = sum r_k
+//
+// (W: what is left of the draft's mass, 1 throughout where siblings are drawn independently). Z_k is not divided out, so
+// the residual is r_k = max(p - c_k q, 0) with c_k = c_(k-1) + Z_(k-1) / W_(k-1): one number per node, and every
+// element is formed from p and q alone. With no child left a token is drawn from r: the first whose running sum passes
+// u Z. Drafts without probabilities stand for a q of 1 at each child: refused ones are taken out of p.
+//
+// What it reads is small (the last node's rows of p and q, and once more for every refused child that has a sibling behind it),
+// and a chain of dependent steps, so it is bound by latency. A cluster of CTAs takes a sequence, a slice of the
+// vocabulary each. The first warp of the first CTA walks: p(x) and q(x) of all nodes are fetched beforehand, side by side, so
+// its steps run in shared memory, and tells the others what to sum (a message in their shared memory, a cluster
+// barrier on either side). Nobody else decides anything, so all of them always agree on the next barrier.
+//
+// Sums decide whole numbers, so they are held to 2^-45 and better: p - c q exactly in two floats (c in two floats), sums of
+// pairs with TwoSum, warps and CTAs in fp64 and in a fixed order. FP64 throughout would be the slower pipe by
+// far. Entries that are NaN or negative count as zero.
+#include <cooperative_groups.h>
+
+#include "ts_common.cuh"
+
+namespace ts {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kVfThreads = 512;
+constexpr int kVfWarps = kVfThreads / 32;
+constexpr int kVfCluster = 8;          // CTAs of a sequence, at most (the portable size)
+constexpr int kVfSlice = 1 << 17;      // vocabulary of a CTA, at most
+
+struct VerifyArgs {
+  const int32_t* tokens;
+  const int32_t* parents;
+  const int32_t* cu;
+  int B, total, V;
+  const float* target;
+  int64_t target_stride;
+  const float* draft;                  // or null
+  int64_t draft_stride;
+  const float* u;
+  const float* u_next;
+  int distinct;
+  int32_t* path;
+  int64_t path_stride;
+  int32_t* count;
+  int32_t* next;
+  int* status;
+};
+
+enum { kVfSum = 0, kVfDraw = 1, kVfEnd = 2 };
+
+struct Order {                         // what the walk asks of every CTA
+  int what;
+  int node;                            // the node whose rows are meant (in its sequence)
+  int masked;                          // drafts without probabilities: its children are taken out
+  double c;
+};
+
+// max(p - c q, 0) as a pair of floats; entries that are NaN or negative count as zero
+__device__ __forceinline__ void residual(float p, float q, float ch, float cl, float& hi, float& lo) {
+  q = fmaxf(q, 0.f);
+  const float h = ch * q, e = fmaf(ch, q, -h);      // c_hi q exactly
+  float s, t;
+  two_sum(p, -h, s, t);
+  const float l = t - e - cl * q;
+  const bool some = s + l > 0.f;
+  hi = some ? s : 0.f;
+  lo = some ? l : 0.f;
+}
+
+__global__ void __launch_bounds__(kVfThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int b = blockIdx.x / ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  extern __shared__ unsigned s_gone[];                          // bit per token of the slice (drafts without probabilities)
+  __shared__ int s_parent[kMaxTree], s_token[kMaxTree];
+  __shared__ float s_u[kMaxTree], s_p[kMaxTree], s_q[kMaxTree];
+  __shared__ Order s_order;
+  __shared__ double s_part[kVfCluster * kVfWarps];              // (of the first CTA) sums by CTA and warp
+  __shared__ int s_found;
+
+  const int first = a.cu[b], end = a.cu[b + 1];
+  const bool fine = first >= 0 && end >= first && end <= a.total && end - first <= kMaxTree && (b != 0 || first == 0);
+  const int T = fine ? end - first : 0;
+  if (rank == 0 && tid == 0 && !fine) set_error(a.status, TS_ERR_SEQ_LEN);
+
+  // the slice, and this warp's part of it
+  const int slice = (a.V + ctas - 1) / ctas, v0 = min(a.V, rank * slice), v1 = min(a.V, v0 + slice);
+  const int part = (slice + kVfWarps - 1) / kVfWarps, w0 = min(v1, v0 + warp * part), w1 = min(v1, w0 + part);
+
+  if (rank == 0) {
+    for (int i = tid; i < T; i += kVfThreads) {
+      const int par = i ? a.parents[first + i] : -1, tok = i ? a.tokens[first + i] : -1;
+      const bool ok = i == 0 || (par >= 0 && par < i && tok >= 0 && tok < a.V);
+      if (!ok) set_error(a.status, TS_ERR_INVALID_ARG);
+      const bool use = ok && i > 0;
+      s_parent[i] = use ? par : -2;
+      s_token[i] = use ? tok : -1;
+      s_u[i] = use ? a.u[first + i] : 0.f;
+      s_p[i] = use ? a.target[(int64_t)(first + par) * a.target_stride + tok] : 0.f;
+      s_q[i] = use && a.draft ? a.draft[(int64_t)(first + par) * a.draft_stride + tok] : 0.f;
+    }
+    __syncthreads();
+  }
+
+  // state of the walk (first warp of the first CTA; the same in every lane)
+  int cur = 0, at = 1, kept = T > 0 ? 1 : 0;
+  double c = 0., Z = 1., W = 1.;
+  bool stale = false;                  // Z is that of an earlier c
+  int draws = 0;
+  if (rank == 0 && warp == 0 && lane == 0 && T > 0) {
+    if (a.path_stride > 0) a.path[(int64_t)b * a.path_stride] = 0;
+  }
+  bool drawn = false;
+  int token = -1;
+
+  for (;;) {
+    if (rank == 0 && warp == 0) {
+      Order o{kVfEnd, cur, 0, 0.};
+      if (T > 0 && !drawn) {
+        o.what = kVfDraw;
+        // children of cur from node `at` on
+        while (at < T) {
+          const int i = at + lane;
+          const unsigned m = __ballot_sync(kFull, i < T && s_parent[i] == cur);
+          if (!m) {
+            at += 32;
+            continue;
+          }
+          const int x = at + __ffs(m) - 1;
+          if (a.draft && stale) {      // its test needs the sum of the residual
+            o.what = kVfSum;
+            at = x;
+            break;
+          }
+          at = x + 1;
+          const double u = s_u[x];
+          bool yes;
+          double px = fmaxf(s_p[x], 0.f);
+          if (a.draft) {
+            const double qx = fmaxf(s_q[x], 0.f);
+            const double r = fmax(px - c * qx, 0.);
+            yes = W > 0. && u * qx * Z < r * W;
+            if (!yes) {
+              if (W > 0.) c += Z / W;
+              if (a.distinct) W -= qx;
+              stale = true;
+            }
+          } else {
+            // a token that an earlier child had is gone
+            bool dup = false;
+            for (int j = cur + 1 + lane; j < x; j += 32) dup |= s_parent[j] == cur && s_token[j] == s_token[x];
+            if (__any_sync(kFull, dup)) px = 0.;
+            yes = u * Z < px;
+            if (!yes) Z -= px;
+          }
+          if (yes) {
+            if (lane == 0 && kept < a.path_stride) a.path[(int64_t)b * a.path_stride + kept] = x;
+            ++kept;
+            cur = x;
+            c = 0.;
+            Z = W = 1.;
+            stale = false;
+          }
+        }
+        o.node = cur;
+        o.masked = a.draft == nullptr && draws == 0;
+        o.c = draws == 0 ? c : 0.;     // nothing left of the residual: the second draw is from p itself
+      }
+      if (lane < ctas) *cluster.map_shared_rank(&s_order, lane) = o;
+    }
+    cluster.sync();
+    const Order o = s_order;
+    if (o.what == kVfEnd) break;
+    // ---- sums of this warp's part
+    const float* p = a.target + (int64_t)(first + o.node) * a.target_stride;
+    const bool with_q = a.draft != nullptr && o.c != 0.;
+    const float* q = with_q ? a.draft + (int64_t)(first + o.node) * a.draft_stride : p;
+    const float ch = with_q ? (float)o.c : 0.f, cl = with_q ? (float)(o.c - (double)ch) : 0.f;
+    if (o.masked) {
+      for (int i = tid; i < (slice + 31) / 32; i += kVfThreads) s_gone[i] = 0u;
+      __syncthreads();
+      for (int i = o.node + 1 + tid; i < T; i += kVfThreads) {
+        const int tok = a.tokens[first + i];
+        if (a.parents[first + i] == o.node && tok >= v0 && tok < v1) atomicOr(&s_gone[(tok - v0) >> 5], 1u << ((tok - v0) & 31));
+      }
+      __syncthreads();
+    }
+    auto entry = [&](int i, float pv, float qv, float& hi, float& lo) {
+      residual(pv, qv, ch, cl, hi, lo);
+      if (o.masked && (s_gone[(i - v0) >> 5] >> ((i - v0) & 31) & 1u)) hi = lo = 0.f;
+    };
+    float hi = 0.f, lo = 0.f;
+    constexpr int UN = 8;
+    for (int i0 = w0 + lane; i0 < w1; i0 += 32 * UN) {
+      float pv[UN], qv[UN];
+#pragma unroll
+      for (int k = 0; k < UN; ++k) {
+        const int i = i0 + 32 * k;
+        pv[k] = i < w1 ? __ldg(p + i) : 0.f;
+        qv[k] = i < w1 && with_q ? __ldg(q + i) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < UN; ++k) {
+        const int i = i0 + 32 * k;
+        float x, y, s, e;
+        entry(min(i, w1 - 1), pv[k], qv[k], x, y);
+        two_sum(hi, x, s, e);
+        hi = s;
+        lo += e + y;
+      }
+    }
+    double mine = (double)hi + (double)lo;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) mine += __shfl_xor_sync(kFull, mine, d);
+    if (lane == 0) *cluster.map_shared_rank(&s_part[rank * kVfWarps + warp], 0) = mine;
+    if (tid == 0) s_found = -1;
+    cluster.sync();
+    if (o.what == kVfSum) {
+      if (rank == 0 && warp == 0) {
+        double s = 0.;
+        for (int k = lane; k < ctas * kVfWarps; k += 32) s += s_part[k];
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+        Z = s;
+        stale = false;
+      }
+      continue;
+    }
+    // ---- the draw: every warp finds from all sums whether its part holds the token
+    const double* parts = cluster.map_shared_rank(&s_part[0], 0);
+    const int n = ctas * kVfWarps;
+    // running sums over the parts, the same in every warp
+    constexpr int PL = kVfCluster * kVfWarps / 32;
+    double all = 0., held[PL], run_to[PL], before = 0.;
+#pragma unroll
+    for (int k = 0; k < PL; ++k) {
+      held[k] = 32 * k + lane < n ? parts[32 * k + lane] : 0.;
+      double run = held[k];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const double o2 = __shfl_up_sync(kFull, run, d);
+        if (lane >= d) run += o2;
+      }
+      run_to[k] = run + all;
+      all = __shfl_sync(kFull, run_to[k], 31);
+    }
+    const double t = (double)a.u_next[b] * all;
+    // the first part that holds something and whose running sum passes t; where rounding leaves none, the last that does
+    int from = -1;
+    bool passed = false;
+#pragma unroll
+    for (int k = 0; k < PL; ++k) {
+      const unsigned some = __ballot_sync(kFull, held[k] > 0.);
+      const unsigned over = __ballot_sync(kFull, held[k] > 0. && run_to[k] > t);
+      if (passed || !some) continue;
+      passed = over != 0u;
+      from = 32 * k + (over ? __ffs(over) - 1 : 31 - __clz(some));
+      before = __shfl_sync(kFull, run_to[k] - held[k], from & 31);
+    }
+    if (from == rank * kVfWarps + warp) {
+      // a lane takes neighbouring elements: its sum, the sums of the lanes before it, then its elements one by one
+      const int len = (w1 - w0 + 31) / 32, e0 = min(w1, w0 + lane * len), e1 = min(w1, e0 + len);
+      float shi = 0.f, slo = 0.f;
+      int last = -1;
+      for (int i = e0; i < e1; ++i) {
+        float x, y, s, e;
+        entry(i, p[i], with_q ? q[i] : 0.f, x, y);
+        two_sum(shi, x, s, e);
+        shi = s;
+        slo += e + y;
+        if (x + y > 0.f) last = i;
+      }
+      const double sum = (double)shi + (double)slo;
+      double run = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const double o2 = __shfl_up_sync(kFull, run, d);
+        if (lane >= d) run += o2;
+      }
+      const double base = before + (run - sum);
+      const unsigned over = __ballot_sync(kFull, sum > 0. && before + run > t);
+      const unsigned some = __ballot_sync(kFull, last >= 0);
+      const int owner = over ? __ffs(over) - 1 : 31 - __clz(some);
+      if (some && lane == owner) {
+        int pick = last;
+        double acc = base;
+        for (int i = e0; i < e1; ++i) {
+          float x, y;
+          entry(i, p[i], with_q ? q[i] : 0.f, x, y);
+          acc += (double)x + (double)y;
+          if (acc > t && x + y > 0.f) {
+            pick = i;
+            break;
+          }
+        }
+        *cluster.map_shared_rank(&s_found, 0) = pick;
+      }
+    }
+    cluster.sync();
+    if (rank == 0 && warp == 0) {
+      ++draws;
+      token = s_found;
+      drawn = token >= 0 || draws == 2;
+    }
+  }
+  if (rank == 0) {
+    if (warp == 0 && lane == 0) {
+      a.count[b] = kept;
+      a.next[b] = token;
+      if (kept > a.path_stride) set_error(a.status, TS_ERR_CAPACITY);
+      s_found = kept;
+    }
+    __syncthreads();
+    for (int64_t i = s_found + tid; i < a.path_stride; i += kVfThreads) a.path[(int64_t)b * a.path_stride + i] = -1;
+  }
+  cluster.sync();                      // no CTA leaves while its shared memory may still be written to
+}
+
+}  // namespace
+
+ts_status launch_verify(ts_ctx* ctx, const VerifyCall& c, cudaStream_t s) {
+  VerifyArgs a{c.tokens, c.parents, c.cu_rows, c.B, c.total, c.vocab, c.target, c.target_stride, c.draft, c.draft_stride,
+               c.u, c.u_next, c.distinct, c.path, c.path_stride, c.count, c.next, ctx->status};
+  int ctas = 1;
+  while (ctas < kVfCluster && (c.vocab > kVfSlice * ctas || c.vocab >= 2048 * ctas)) ctas *= 2;
+  const size_t smem = c.draft ? 0 : (size_t)((c.vocab + ctas - 1) / ctas + 31) / 32 * 4;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(c.B * ctas));
+  lc.blockDim = dim3(kVfThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  ctx->kernels += 1;
+  return cuda_status(cudaLaunchKernelEx(&lc, verify_kernel, a));
+}
+
+}  // namespace ts
