@@ -13,7 +13,7 @@
 // sequences, one behind another, are dealt to one CTA per SM in equal, contiguous shares, whatever the lengths are. A
 // share that begins or ends inside a block leaves its sums in fp32 (unnormalised, with maximum and sum), and a second kernel
 // joins them, in order: the same bits every time. Roles of a CTA:
-//   warp 8      loads: the query tiles of an item, then K and V pages (TMA, 128-byte swizzle, slots of 128 tokens)
+//   warp 8      loads: the query tiles of an item, then K and V pages (TMA, 128-byte swizzle) into a ring of tiles
 //   warp 9      products: S = Q K^T, O += P V
 //   warp 10     finds the items of the share
 //   warp 11     looks through the value tiles that hold drafts or end the sequence (below)
@@ -39,6 +39,9 @@ constexpr int kTrThreads = (kTrSoftmaxWarps + 4) * 32;
 // Registers a thread: 168 at launch (65536 / 384), shared out as in the prompt attention.
 constexpr int kTrSoftmaxRegs = 208, kTrOtherRegs = 88;
 static_assert(2 * kTrSoftmaxRegs + kTrOtherRegs <= 3 * 168, "register shares");
+// Per key tile, eight of which are told apart: the ring holds a value tile that is in use and SLOTS - 1 tiles behind it,
+// half of them keys, so nothing is more than seven key tiles ahead of anything.
+constexpr int kTrRing = 8;
 constexpr float kTrMaxSum = 16384.f;   // of a tile's weights against a maximum taken earlier
 
 struct TreeArgs {
@@ -72,9 +75,9 @@ struct TrShape {
   static constexpr int HALVES = D / 64;
   static constexpr int QT = kTrRows * D * 2;    // bytes of a query tile
   static constexpr int KT = kTrKeys * D * 2;    // bytes of a key or value tile
-  static constexpr int STAGE = 32 * 128;        // bytes of a softmax warp's output staging: 32 rows of 64 columns
-  static constexpr int SMEM = 2 * QT + 4 * KT + kTrSoftmaxWarps * STAGE + 1024;
-  static_assert(SMEM + 2048 <= 227 * 1024, "shared memory of an SM");
+  static constexpr int SLOTS = D == 128 ? 5 : 10;   // key and value tiles under way or in use
+  static constexpr int SMEM = 2 * QT + SLOTS * KT + 1024;
+  static_assert(SMEM + 1536 <= 227 * 1024, "shared memory of an SM");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t S_COL = 0, O_COL = 256;   // buffer i: S at 128 i (weights over its first 64); tile i: O at 256 + 128 i
 };
@@ -114,6 +117,10 @@ __device__ __forceinline__ int64_t warp_scan_ll(int64_t x, int lane) {
 // First tile of CTA c's share of `work` tiles among `ctas`, and the CTA that has tile t.
 __device__ __forceinline__ int64_t share_begin(int64_t work, int ctas, int c) { return work * c / ctas; }
 __device__ __forceinline__ int share_of(int64_t work, int ctas, int64_t t) { return (int)(((t + 1) * ctas - 1) / work); }
+
+// Places in the ring of an item's key tile j and value tile j, counted from its first: K(0), K(1), V(0), K(2), V(1), ...
+__device__ __forceinline__ uint32_t key_load(int j) { return j == 0 ? 0u : 2u * (uint32_t)j - 1u; }
+__device__ __forceinline__ uint32_t value_load(int j, int nt) { return (uint32_t)min(2 * j + 2, 2 * nt - 1); }
 
 struct TreeItem {
   int found, row0, T, n, i0;     // sequence; first token (among the drafts) of the block
@@ -156,19 +163,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   extern __shared__ unsigned char dsm_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* sQ = base;                // two query tiles
-  unsigned char* sK = sQ + 2 * S::QT;      // two key slots
-  unsigned char* sV = sK + 2 * S::KT;      // two value slots
-  unsigned char* sO = sV + 2 * S::KT;      // output staging, one area per softmax warp
-  __shared__ __align__(8) uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], s_full[2],
-      p_ready[2], o_done[2], item_full[2], item_empty[2], item_clean[2], drained;
+  unsigned char* sKV = sQ + 2 * S::QT;     // key and value tiles, a ring in the order of their use
+  __shared__ __align__(8) uint64_t q_full, q_empty, full[S::SLOTS], empty[S::SLOTS], v_clean[kTrRing], s_full[2], p_ready[2],
+      o_done[2], item_full[2], item_empty[2], item_clean[2], drained;
   __shared__ uint32_t s_tmem;
   __shared__ TreeItem s_item[2];
   __shared__ uint32_t s_odd[2][kMaxTree / 32];   // drafts whose values are not all finite, per item slot
   __shared__ int s_any_odd[2];
-  // keys of a tile whose page lies outside the pool, per key tile (of the last four), and whether there are any: the
-  // loads run at most three tiles ahead of the softmax
-  __shared__ uint32_t s_bad[4][4];
-  __shared__ uint32_t s_any_bad[4];
+  // keys of a tile whose page lies outside the pool, and whether there are any, for the last eight key tiles
+  __shared__ uint32_t s_bad[kTrRing][4];
+  __shared__ uint32_t s_any_bad[kTrRing];
 
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const uint64_t settle = a.wait_ns > kWaitLimitNs ? a.wait_ns : kWaitLimitNs;   // for what is in flight at the end
@@ -182,11 +186,6 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     mbar_init(&q_empty, 1);
     mbar_init(&drained, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 2);           // the products and the look through
-      mbar_init(&v_clean[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], kTrSoftmaxWarps / 2);
       mbar_init(&o_done[i], 1);
@@ -195,6 +194,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       mbar_init(&item_clean[i], 1);
       s_any_odd[i] = 0;
     }
+    for (int i = 0; i < S::SLOTS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 2);             // the products and the look through
+    }
+    for (int i = 0; i < kTrRing; ++i) mbar_init(&v_clean[i], 1);
     mbar_fence_init();
   }
   if (tid < 2 * (kMaxTree / 32)) (&s_odd[0][0])[tid] = 0u;
@@ -227,8 +231,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     if (warp == kTrSoftmaxWarps) {
       // ---------------------------------------------------------------- loads
       bool ok = true;
-      int items = 0, g = 0;                                       // loaded so far: items' queries, key tiles
-      int kn = 0, vn = 0;
+      int items = 0, kt = 0;                                      // loaded so far: items' queries, key tiles
+      uint32_t loads = 0;                                         // ... tiles of the ring
       const int ps = 1 << a.page_shift, per_tile = kTrKeys >> a.page_shift;
       auto all = [&](bool x) -> bool { return __all_sync(kFull, x); };
       for (;;) {
@@ -237,36 +241,24 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[items & 1]);
         if (!it.found) break;
-        if (items > 0) ok = all(mbar_wait(&q_empty, (items - 1) & 1, a.wait_ns));
-        if (!ok) break;
-        const int tiles_q = two ? 2 : 1;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full, (uint32_t)(tiles_q * S::HALVES * a.G * a.tokens * 128));
-          for (int i = 0; i < tiles_q; ++i)
-            for (int h = 0; h < S::HALVES; ++h)
-              tma_load_3d(sQ + i * S::QT + h * (kTrRows * 128), &a.q, h * 64, it.kv * a.G, it.row0 + it.i0 + i * a.tokens,
-                          &q_full);
-        }
-        ++items;
         const int32_t* pages = a.page_table + (int64_t)it.b * a.pt_stride;
         const int n_pages = (it.n + ps - 1) >> a.page_shift;
-        // this lane's pages of a tile; -1 (the copy is filled with zeros) behind the sequence and for no page of the pool
-        auto page_of = [&](int j, int k) -> int {
-          const int p = j * per_tile + lane + 32 * k;
-          return lane + 32 * k < per_tile && p < n_pages ? pages[p] : -1;
-        };
-        int next[4];
+        // this lane's pages of a tile (four where a page holds one token); -1 behind the sequence
+        auto fetch = [&](int j, int (&p)[4]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) next[k] = page_of(it.j0, k);
-        for (int j = it.j0; j < it.j1; ++j, ++g) {
-          int cur[4];
+          for (int k = 0; k < 4; ++k) {
+            const int at = j * per_tile + lane + 32 * k;
+            p[k] = lane + 32 * k < per_tile && at < n_pages ? pages[at] : -1;
+          }
+        };
+        // -1 (the copy is filled with zeros) for what is no page of the pool either; which keys that leaves out
+        auto vet = [&](int j, int (&p)[4]) {
           uint32_t bad[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            cur[k] = next[k];
             const bool there = lane + 32 * k < per_tile && j * per_tile + lane + 32 * k < n_pages;
-            const bool out = there && (cur[k] < 0 || (int64_t)cur[k] >= a.num_pages);
-            if (out) cur[k] = -1;
+            const bool out = there && (p[k] < 0 || (int64_t)p[k] >= a.num_pages);
+            if (out) p[k] = -1;
             const unsigned m = __ballot_sync(kFull, out);
             if (m) {
               if (lane == 0) set_error(a.status, TS_ERR_PAGE_OOB);
@@ -279,57 +271,76 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
               }
             }
           }
-          if (j + 1 < it.j1) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) next[k] = page_of(j + 1, k);
-          }
-          const int s = g & 1;
-          if (g >= 2) ok = all(mbar_wait(&k_empty[s], ((g >> 1) - 1) & 1, a.wait_ns));
-          if (!ok) break;
           if (lane == 0) {
             const uint32_t any = bad[0] | bad[1] | bad[2] | bad[3];
-            s_any_bad[g & 3] = any;
+            s_any_bad[kt & (kTrRing - 1)] = any;
             if (any) {
 #pragma unroll
-              for (int w = 0; w < 4; ++w) s_bad[g & 3][w] = bad[w];
+              for (int w = 0; w < 4; ++w) s_bad[kt & (kTrRing - 1)][w] = bad[w];
             }
-            mbar_arrive_expect_tx(&k_full[s], S::KT);
           }
+          ++kt;
+        };
+        auto load = [&](const CUtensorMap* map, const int (&p)[4]) -> bool {
+          const uint32_t s = loads % S::SLOTS, round = loads / S::SLOTS;
+          if (round > 0 && !all(mbar_wait(&empty[s], (round - 1) & 1, a.wait_ns))) return false;
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], S::KT);
           __syncwarp();
+          ++loads;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (lane + 32 * k < per_tile)
               for (int h = 0; h < S::HALVES; ++h)
-                tma_load_3d(sK + s * S::KT + h * (kTrKeys * 128) + (lane + 32 * k) * ps * 128, &a.k, h * 64, it.kv * ps, cur[k],
-                            &k_full[s]);
-          ++kn;
-          if (g >= 2) ok = all(mbar_wait(&v_empty[s], ((g >> 1) - 1) & 1, a.wait_ns));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&v_full[s], S::KT);
-          __syncwarp();
+                tma_load_3d(sKV + s * S::KT + h * (kTrKeys * 128) + (lane + 32 * k) * ps * 128, map, h * 64, it.kv * ps, p[k],
+                            &full[s]);
+          return true;
+        };
+        int cur[4], next[4] = {-1, -1, -1, -1};
+        fetch(it.j0, cur);
+        if (it.j0 + 1 < it.j1) fetch(it.j0 + 1, next);
+        if (items > 0) ok = all(mbar_wait(&q_empty, (items - 1) & 1, a.wait_ns));
+        if (!ok) break;
+        const int tiles_q = two ? 2 : 1;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full, (uint32_t)(tiles_q * S::HALVES * a.G * a.tokens * 128));
+          for (int i = 0; i < tiles_q; ++i)
+            for (int h = 0; h < S::HALVES; ++h)
+              tma_load_3d(sQ + i * S::QT + h * (kTrRows * 128), &a.q, h * 64, it.kv * a.G, it.row0 + it.i0 + i * a.tokens,
+                          &q_full);
+        }
+        ++items;
+        vet(it.j0, cur);
+        ok = load(&a.k, cur);
+        for (int j = it.j0; j < it.j1 && ok; ++j) {               // K(j + 1), V(j)
+          int after[4] = {-1, -1, -1, -1};
+          if (j + 1 < it.j1) {
+            if (j + 2 < it.j1) fetch(j + 2, after);
+            vet(j + 1, next);
+            ok = load(&a.k, next);
+            if (!ok) break;
+          }
+          ok = load(&a.v, cur);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (lane + 32 * k < per_tile)
-              for (int h = 0; h < S::HALVES; ++h)
-                tma_load_3d(sV + s * S::KT + h * (kTrKeys * 128) + (lane + 32 * k) * ps * 128, &a.v, h * 64, it.kv * ps, cur[k],
-                            &v_full[s]);
-          ++vn;
+          for (int k = 0; k < 4; ++k) {
+            cur[k] = next[k];
+            next[k] = after[k];
+          }
         }
         if (!ok) break;
       }
       if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
       // nothing may still be landing when the CTA exits, however short the limit was that a role gave up at
       if (items > 0) mbar_wait(&q_full, (items - 1) & 1, settle);
-      for (int j = max(0, kn - 2); j < kn; ++j) mbar_wait(&k_full[j & 1], (j >> 1) & 1, settle);
-      for (int j = max(0, vn - 2); j < vn; ++j) mbar_wait(&v_full[j & 1], (j >> 1) & 1, settle);
+      for (uint32_t l = loads > S::SLOTS ? loads - S::SLOTS : 0u; l < loads; ++l)
+        mbar_wait(&full[l % S::SLOTS], (l / S::SLOTS) & 1, settle);
       __syncwarp();
     } else if (warp == kTrSoftmaxWarps + 1) {
       // ------------------------------------------------------------- products
       // (the whole warp goes through the loop and one lane issues, with descriptors in uniform registers)
       const uint32_t idesc_s = idesc_bf16_f32(kTrRows, kTrKeys) | (a.negate ? 1u << 13 : 0u);   // bit 13: -A
       constexpr uint32_t idesc_o = idesc_bf16_f32_bmn(kTrRows, D);
-      const uint64_t dq = sdesc_sw128(smem_addr(sQ)), dk = sdesc_sw128(smem_addr(sK));
-      const uint64_t dv = sdesc_sw128_mn(smem_addr(sV), kTrKeys * 128, 1024);
+      const uint64_t dq = sdesc_sw128(smem_addr(sQ)), dk = sdesc_sw128(smem_addr(sKV));
+      const uint64_t dv = sdesc_sw128_mn(smem_addr(sKV), kTrKeys * 128, 1024);
       const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
       const uint32_t qk_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32);
       // scores of query tile i and the key slot into buffer x
@@ -365,7 +376,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(kFull, mbar_wait(bar, parity, a.wait_ns)); };
       bool ok = true;
       int kt = 0;                                                 // key tiles of the items before
-      uint32_t clean_par = 0u, p_par = 0u;                        // parities of the next waits, by slot and by buffer
+      uint32_t clean_par = 0u, p_par = 0u;                        // parities of the next waits, by key tile and by buffer
+      auto full_tile = [&](uint32_t l) -> bool { return wait(&full[l % S::SLOTS], (l / S::SLOTS) & 1); };
       for (int k = 0;; ++k) {
         ok = __all_sync(kFull, read_item(k, it, two, drafts_from));
         if (!ok) break;
@@ -374,45 +386,49 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(&item_empty[k & 1]);
         __syncwarp();
         if (!found) break;
-        ok = wait(&q_full, k & 1) && wait(&k_full[kt & 1], (kt >> 1) & 1);
+        const uint32_t l0 = 2u * (uint32_t)kt;                    // the item's first tile of the ring
+        // scores of the item's key tile j, for one tile of queries into buffer x or for both
+        auto score_tile = [&](int j, int i, int x, bool last) {
+          const uint32_t s = (l0 + key_load(j)) % S::SLOTS;
+          scores(i, s, x);
+          if (last) {
+            commit(&empty[s]);
+            if (j + 1 == nt) commit(&q_empty);
+          }
+        };
+        ok = wait(&q_full, k & 1) && full_tile(l0);
         if (!ok) break;
         tc_fence_after();
         const int ahead = pair ? 1 : 2;                           // key tiles whose scores are taken before the first outputs
-        scores(0, kt & 1, 0);
-        if (pair) scores(1, kt & 1, 1);
-        commit(&k_empty[kt & 1]);
+        score_tile(0, 0, 0, !pair);
+        if (pair) score_tile(0, 1, 1, true);
         if (!pair && nt > 1) {
-          ok = wait(&k_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1);
+          ok = full_tile(l0 + key_load(1));
           if (!ok) break;
           tc_fence_after();
-          scores(0, (kt + 1) & 1, 1);
-          commit(&k_empty[(kt + 1) & 1]);
+          score_tile(1, 0, 1, true);
         }
-        if (nt <= ahead) commit(&q_empty);
         for (int j = 0; j < nt && ok; ++j) {
-          const int g = kt + j, s = g & 1;
-          ok = wait(&v_full[s], (g >> 1) & 1);
+          const uint32_t l = l0 + value_load(j, nt);
+          const int g = (kt + j) & (kTrRing - 1);
+          ok = full_tile(l);
           if (ok && j >= look) {
-            ok = wait(&v_clean[s], (clean_par >> s) & 1u);
-            clean_par ^= 1u << s;
+            ok = wait(&v_clean[g], (clean_par >> g) & 1u);
+            clean_par ^= 1u << g;
           }
           if (!ok) break;
-          const int n1 = j + ahead, s1 = (kt + n1) & 1;           // the key tile whose scores come next
-          const bool next = n1 < nt;
+          const int n1 = j + ahead;                               // the key tile whose scores come next
           for (int i = 0; i < (pair ? 2 : 1) && ok; ++i) {
             const int x = pair ? i : j & 1;
             ok = wait(&p_ready[x], (p_par >> x) & 1u);
             p_par ^= 1u << x;
-            if (ok && next && i == 0) ok = wait(&k_full[s1], ((kt + n1) >> 1) & 1);
+            if (ok && n1 < nt && i == 0) ok = full_tile(l0 + key_load(n1));
             if (!ok) break;
             tc_fence_after();
-            outputs(i, s, x, j != 0);
-            if (next) scores(i, s1, x);
+            outputs(i, l % S::SLOTS, x, j != 0);
+            if (n1 < nt) score_tile(n1, i, x, !pair || i == 1);
           }
-          if (!ok) break;
-          commit(&v_empty[s]);
-          if (next) commit(&k_empty[s1]);
-          if (n1 + 1 == nt) commit(&q_empty);
+          if (ok) commit(&empty[l % S::SLOTS]);
         }
         if (!ok) break;
         kt += nt;
@@ -504,16 +520,19 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     } else {
       // ----------------------------------- values that are not finite among the drafts and behind them
       bool ok = true;
-      int kt = 0;
+      uint32_t l = 0;                                             // tiles of the ring so far
       for (int k = 0;; ++k) {
         ok = __all_sync(kFull, read_item(k, it, two, drafts_from));
         if (!ok || !it.found) break;
-        for (int j = it.j0; j < it.j1 && ok; ++j, ++kt) {
-          const int vs = kt & 1;
-          ok = __all_sync(kFull, mbar_wait(&v_full[vs], (kt >> 1) & 1, a.wait_ns));
+        // every tile of the ring in turn, keys too: a parity tells a phase only from its neighbours
+        const int nt = it.j1 - it.j0;
+        for (int i = 0; i < 2 * nt && ok; ++i, ++l) {
+          ok = __all_sync(kFull, mbar_wait(&full[l % S::SLOTS], (l / S::SLOTS) & 1, a.wait_ns));
           if (!ok) break;
-          if (j >= drafts_from) {
-            unsigned char* vt = sV + vs * S::KT;
+          const bool value = i == 2 * nt - 1 || (i >= 2 && i % 2 == 0);
+          const int j = it.j0 + (i == 2 * nt - 1 ? nt - 1 : i / 2 - 1);
+          if (value && j >= drafts_from) {
+            unsigned char* vt = sKV + l % S::SLOTS * S::KT;
             uint32_t odd = 0u;
 #pragma unroll 8
             for (int c = 0; c < S::KT / 512; ++c) {
@@ -538,10 +557,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&v_clean[vs]);
+            if (lane == 0) mbar_arrive(&v_clean[((l - i) / 2 + j - it.j0) & (kTrRing - 1)]);
           }
-          // (also for the tiles not looked at: so this warp never falls a round behind the value slots)
-          if (lane == 0) mbar_arrive(&v_empty[vs]);
+          if (lane == 0) mbar_arrive(&empty[l % S::SLOTS]);
           __syncwarp();
         }
         if (!ok) break;
@@ -588,7 +606,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
           s_par ^= 1u << x;
           if (!idle) {
             // what is not seen in this tile: drafts, what is behind the sequence, pages outside the pool
-            const int ring = (kt + j) & 3;
+            const int ring = (kt + j) & (kTrRing - 1);
             const bool any_bad = s_any_bad[ring] != 0u;
             const bool cut = key0 + kTrKeys > d0 || any_bad;
             uint32_t bits[4];
@@ -732,37 +750,21 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (a row that sees nothing: zeros)
             if (real && a.lse)
               a.lse[(int64_t)packed * a.H + head] = l == 0.f ? -INFINITY : (mx * a.scale2 + log2f(l)) * 0.6931471805599453f;
-            // this lane's output row; a null pointer where it is none
-            const uint64_t dst = real ? reinterpret_cast<uint64_t>(a.out + (int64_t)packed * a.out_stride + (int64_t)head * D) : 0u;
-            unsigned char* stage = sO + warp * S::STAGE;
+            unsigned char* dst = reinterpret_cast<unsigned char*>(a.out + (int64_t)packed * a.out_stride + (int64_t)head * D);
 #pragma unroll 1
-            for (int h = 0; h < S::HALVES; ++h) {
-              // 64 columns of 32 rows through this warp's staging area (swizzled like the operands), so that a
-              // store covers whole 128-byte pieces of four rows instead of 16 bytes of 32
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld_x32(tO + 32 * c, o);
+              tmem_wait_ld();
+              if (odd) put_back(32 * c, o);
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t o[32];
-                tmem_ld_x32(tO + 64 * h + 32 * c, o);
-                tmem_wait_ld();
-                if (odd) put_back(64 * h + 32 * c, o);
+              for (int e = 0; e < 4; ++e) {
+                uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  uint32_t w[4];
-#pragma unroll
-                  for (int z = 0; z < 4; ++z)
-                    w[z] = pack_bf16(__uint_as_float(o[8 * e + 2 * z]) * inv, __uint_as_float(o[8 * e + 2 * z + 1]) * inv);
-                  *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + e) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                for (int z = 0; z < 4; ++z)
+                  w[z] = pack_bf16(__uint_as_float(o[8 * e + 2 * z]) * inv, __uint_as_float(o[8 * e + 2 * z + 1]) * inv);
+                if (real) *reinterpret_cast<uint4*>(dst + 64 * c + 16 * e) = make_uint4(w[0], w[1], w[2], w[3]);
               }
-              __syncwarp();
-#pragma unroll
-              for (int r4 = 0; r4 < 8; ++r4) {
-                const int rl = 4 * r4 + (lane >> 3), c16 = lane & 7;
-                const uint64_t to = __shfl_sync(kFull, dst, rl);
-                const uint4 v = lds128(stage + rl * 128 + ((c16 ^ (rl & 7)) << 4));
-                if (to) *reinterpret_cast<uint4*>(to + 128 * h + c16 * 16) = v;
-              }
-              __syncwarp();
             }
           }
           // the accumulators have been read before the next item's weights let a product write them
@@ -798,86 +800,112 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
 }
 
 // Joins the sums of blocks that several CTAs had parts of. Eight rows of one KV head to a CTA (neighbouring rows of a block:
-// heads, then tokens), a thread per row and four columns. Bound by the parts read (from L2).
-constexpr int kJoinRows = 8;
+// heads, then tokens), whose sums lie side by side; a thread per row, four columns and every fourth part, so that all of
+// a row's parts are on their way at once. Bound by latency: shares, factors, parts (from L2).
+constexpr int kJoinRows = 8, kJoinGroups = 4;
 constexpr int kJoinParts = 256;  // CTAs of a call, at most
 
 template <int D>
-__global__ void __launch_bounds__(kJoinRows * D / 4) join_kernel(const __grid_constant__ TreeArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(const __grid_constant__ TreeArgs a, int grid) {
   constexpr int COLS = D / 4;
   __shared__ int s_first[kJoinRows], s_parts[kJoinRows], s_at[kJoinRows], s_slot0[kJoinRows];
   __shared__ float s_f[kJoinRows][kJoinParts];
-  const int tid = threadIdx.x;
+  __shared__ float s_inv[kJoinRows];
+  __shared__ float4 s_acc[kJoinGroups - 1][kJoinRows * COLS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t per_kv = (int64_t)a.total * a.G;
-  const int row = tid / COLS, col = tid % COLS;
+  const int row = tid % kJoinRows, col = tid / kJoinRows % COLS, grp = tid / (kJoinRows * COLS);
+  auto place = [&](int r, int& kv, int& packed, int& head) {
+    const int64_t idx = (int64_t)blockIdx.x * kJoinRows + r;
+    kv = (int)(idx / per_kv);
+    packed = (int)(idx % per_kv / a.G);
+    head = (int)(idx % a.G);
+  };
+  int kv, packed, head;
+  place(row, kv, packed, head);
+  int lo = 0;
+  TreeSeq s{};
+  if (tid < kJoinRows && kv < a.HKV) {
+    int hi = a.B;                                                 // the last sequence that begins at or before the row
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.cu[mid] <= packed) lo = mid; else hi = mid;
+    }
+    s = tree_seq(a, lo);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t idx = (int64_t)blockIdx.x * kJoinRows + row;
-  const int kv = (int)(idx / per_kv);
-  const int packed = (int)(idx % per_kv / a.G), head = (int)(idx % a.G);
-  if (col == 0) {
+  if (tid < kJoinRows) {
     s_parts[row] = 0;
-    if (kv < a.HKV) {
-      int lo = 0, hi = a.B;                                       // the last sequence that begins at or before the row
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= packed) lo = mid; else hi = mid;
-      }
-      const TreeSeq s = tree_seq(a, lo);
+    if (s.blocks > 0 && packed >= s.row0 && packed < s.row0 + s.T) {
       const int64_t work = a.seq_base[a.B];
-      if (s.blocks > 0 && packed >= s.row0 && packed < s.row0 + s.T) {
-        const int ctas = (int)min((int64_t)grid, work);
-        const int tok = packed - s.row0, block = tok / (2 * a.tokens), in = tok - block * 2 * a.tokens;
-        const int64_t t0 = a.seq_base[lo] + ((int64_t)kv * s.blocks + block) * s.tiles;
-        const int c0 = share_of(work, ctas, t0), c1 = share_of(work, ctas, t0 + s.tiles - 1);
-        s_first[row] = c0;
-        s_parts[row] = c1 > c0 ? c1 - c0 + 1 : 0;                 // (else the block's outputs are there)
-        s_slot0[row] = 2 * c0 + (share_begin(work, ctas, c0) < t0 ? 1 : 0);
-        s_at[row] = (in / a.tokens) * 128 + in % a.tokens * a.G + head;
-      }
+      const int ctas = (int)min((int64_t)grid, work);
+      const int tok = packed - s.row0, block = tok / (2 * a.tokens), in = tok - block * 2 * a.tokens;
+      const int64_t t0 = a.seq_base[lo] + ((int64_t)kv * s.blocks + block) * s.tiles;
+      const int c0 = share_of(work, ctas, t0), c1 = share_of(work, ctas, t0 + s.tiles - 1);
+      s_first[row] = c0;
+      s_parts[row] = c1 > c0 ? c1 - c0 + 1 : 0;                   // (else the block's outputs are there)
+      s_slot0[row] = 2 * c0 + (share_begin(work, ctas, c0) < t0 ? 1 : 0);
+      s_at[row] = (in / a.tokens) * 128 + in % a.tokens * a.G + head;
+    }
+  }
+  __syncthreads();
+  auto slot_of = [&](int r, int k) { return k == 0 ? s_slot0[r] : 2 * (s_first[r] + k); };
+  if (warp < kJoinRows && s_parts[warp] > 0) {
+    // every part's factor, and the row's sum: a warp per row, a lane per part
+    const int parts = s_parts[warp];
+    const float2* ml = a.part_ml + s_at[warp];
+    float M = -INFINITY, total = 0.f;
+    for (int k = lane; k < parts; k += 32) {
+      const float2 x = ml[(int64_t)slot_of(warp, k) * 256];
+      M = fmaxf(M, x.y == 0.f ? -INFINITY : x.x);
+    }
+    M = warp_max(M);
+    const float M2 = M * a.scale2;
+    for (int k = lane; k < parts; k += 32) {
+      const float2 x = ml[(int64_t)slot_of(warp, k) * 256];
+      const float f = x.y == 0.f ? 0.f : (x.x == M ? 1.f : pr_ex2(from_to(x.x, x.x * a.scale2, M, M2, a.scale2)));
+      s_f[warp][k] = f;
+      if (f != 0.f) total = fmaf(f, x.y, total);
+    }
+    total = warp_sum(total);
+    if (lane == 0) {
+      s_inv[warp] = total == 0.f ? 0.f : 1.f / total;
+      int kv1, packed1, head1;
+      place(warp, kv1, packed1, head1);
+      if (a.lse)
+        a.lse[(int64_t)packed1 * a.H + kv1 * a.G + head1] =
+            total == 0.f ? -INFINITY : (M2 + log2f(total)) * 0.6931471805599453f;
     }
   }
   __syncthreads();
   const int parts = s_parts[row];
-  auto slot_of = [&](int k) { return k == 0 ? s_slot0[row] : 2 * (s_first[row] + k); };
-  // every part's factor: the row's columns share the parts out
-  float M = -INFINITY, total = 0.f;
-  for (int k = col; k < parts; k += COLS) {
-    const float2 ml = a.part_ml[(int64_t)slot_of(k) * 256 + s_at[row]];
-    M = fmaxf(M, ml.y > 0.f || ml.y != ml.y ? ml.x : -INFINITY);
-  }
-  // (COLS is 16 or 32: a row's columns lie in one warp)
-#pragma unroll
-  for (int d = COLS / 2; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, d));
-  const float M2 = M * a.scale2;
-  for (int k = col; k < parts; k += COLS) {
-    const float2 ml = a.part_ml[(int64_t)slot_of(k) * 256 + s_at[row]];
-    const float f = ml.y == 0.f ? 0.f : (ml.x == M ? 1.f : pr_ex2(from_to(ml.x, ml.x * a.scale2, M, M2, a.scale2)));
-    s_f[row][k] = f;
-  }
-  __syncthreads();
-  if (parts == 0) return;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4* src = reinterpret_cast<const float4*>(a.part_o) + (int64_t)col * 256 + s_at[row];
-#pragma unroll 4
-  for (int k = 0; k < parts; ++k) {
+#pragma unroll 8
+  for (int k = grp; k < parts; k += kJoinGroups) {
     const float f = s_f[row][k];
-    const int slot = slot_of(k);
-    const float4 o = src[(int64_t)slot * COLS * 256];
-    const float l = a.part_ml[(int64_t)slot * 256 + s_at[row]].y;
+    const float4 o = src[(int64_t)slot_of(row, k) * COLS * 256];
     if (f != 0.f) {                                               // (a part whose weight vanishes may hold anything)
-      total = fmaf(f, l, total);
       acc.x = fmaf(f, o.x, acc.x);
       acc.y = fmaf(f, o.y, acc.y);
       acc.z = fmaf(f, o.z, acc.z);
       acc.w = fmaf(f, o.w, acc.w);
     }
   }
-  const float inv = total == 0.f ? 0.f : 1.f / total;
+  if (grp > 0) s_acc[grp - 1][tid % (kJoinRows * COLS)] = acc;
+  __syncthreads();
+  if (grp > 0 || parts == 0) return;
+#pragma unroll
+  for (int g = 0; g < kJoinGroups - 1; ++g) {
+    const float4 o = s_acc[g][tid];
+    acc.x += o.x;
+    acc.y += o.y;
+    acc.z += o.z;
+    acc.w += o.w;
+  }
+  const float inv = s_inv[row];
   __nv_bfloat16* out = a.out + (int64_t)packed * a.out_stride + (int64_t)(kv * a.G + head) * D + col * 4;
   *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (a.lse && col == 0)
-    a.lse[(int64_t)packed * a.H + kv * a.G + head] =
-        total == 0.f ? -INFINITY : (M2 + log2f(total)) * 0.6931471805599453f;
 }
 
 // bf16 [pages][heads * page size][d] in boxes of 64 elements x one page of one head.
@@ -903,7 +931,7 @@ ts_status run_tree(ts_ctx* ctx, const TreeArgs& a, cudaStream_t s) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
   const int64_t rows = (int64_t)a.total * a.H;
-  return cuda_status(launch_behind(join_kernel<D>, dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows)), kJoinRows * D / 4, s, a, grid));
+  return cuda_status(launch_behind(join_kernel<D>, dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows)), kJoinRows * D / 4 * kJoinGroups, s, a, grid));
 }
 
 }  // namespace
