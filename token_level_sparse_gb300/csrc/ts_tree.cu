@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kTrRows = 128;     // query rows of a tile
 constexpr int kTrKeys = 128;     // tokens of a key tile
+constexpr int kTrHalf = 64;      // keys of a score buffer: half a tile
 constexpr int kTrSoftmaxWarps = 8;
 constexpr int kTrThreads = (kTrSoftmaxWarps + 4) * 32;
 // Registers a thread: 168 at launch (65536 / 384), shared out as in the prompt attention.
@@ -79,7 +80,8 @@ struct TrShape {
   static constexpr int SMEM = 2 * QT + SLOTS * KT + 1024;
   static_assert(SMEM + 1536 <= 227 * 1024, "shared memory of an SM");
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t S_COL = 0, O_COL = 256;   // buffer i: S at 128 i (weights over its first 64); tile i: O at 256 + 128 i
+  // tile i: scores of half tile h at 128 i + 64 h (weights over the first 32 columns), outputs at 256 + 128 i
+  static constexpr uint32_t S_COL = 0, O_COL = 256;
 };
 
 // A sequence's share of the work.
@@ -134,27 +136,21 @@ __device__ __forceinline__ float from_to(float ma, float a2, float mb, float b2,
   return far(a2) ? (far(b2) ? (ma - mb) * scale2 : fmaf(ma, scale2, -b2)) : (far(b2) ? -fmaf(mb, scale2, -a2) : a2 - b2);
 }
 
-// The 128 bits of keys [key0, key0 + 128) that draft `tok` (packed row `row`) sees, the drafts beginning at key `d0`.
-__device__ __forceinline__ void seen_bits(const TreeArgs& a, int row, int tok, int T, int d0, int key0, uint32_t (&bits)[4]) {
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const int k = key0 + 32 * w - d0;          // first key of the word, counted from the drafts' first
-    uint32_t m;
-    if (a.mask) {
-      const uint32_t* words = a.mask + (int64_t)row * a.mask_words;
-      // arithmetic shift: k may lie before the drafts
-      const int at = k >> 5, sh = k & 31, last = (T + 31) >> 5;
-      const uint32_t lo = at >= 0 && at < last ? words[at] : (at < 0 ? 0xffffffffu : 0u);
-      const uint32_t hi = at + 1 >= 0 && at + 1 < last ? words[at + 1] : (at + 1 < 0 ? 0xffffffffu : 0u);
-      m = __funnelshift_r(lo, hi, sh);
-    } else {
-      const int lim = tok - k;                 // the last seen bit
-      m = lim < 0 ? 0u : (lim >= 31 ? 0xffffffffu : (2u << lim) - 1u);
-    }
-    const int left = T - k;                    // bits before the sequence's end
-    if (left < 32) m = left <= 0 ? 0u : m & ((1u << left) - 1u);
-    bits[w] = m;
+// Which of the 32 tokens from draft k on (k may lie before the first) draft `tok`, packed row `row`, sees.
+__device__ __forceinline__ uint32_t seen_bits(const TreeArgs& a, int row, int tok, int T, int k) {
+  uint32_t m;
+  if (a.mask) {
+    const uint32_t* words = a.mask + (int64_t)row * a.mask_words;
+    const int at = k >> 5, last = (T + 31) >> 5;                  // (an arithmetic shift)
+    const uint32_t lo = at >= 0 && at < last ? words[at] : (at < 0 ? 0xffffffffu : 0u);
+    const uint32_t hi = at + 1 >= 0 && at + 1 < last ? words[at + 1] : (at + 1 < 0 ? 0xffffffffu : 0u);
+    m = __funnelshift_r(lo, hi, k & 31);
+  } else {
+    const int lim = tok - k;                   // the last seen bit
+    m = lim < 0 ? 0u : (lim >= 31 ? 0xffffffffu : (2u << lim) - 1u);
   }
+  const int left = T - k;                      // bits before the sequence's end
+  return left >= 32 ? m : left <= 0 ? 0u : m & ((1u << left) - 1u);
 }
 
 template <int D>
@@ -164,8 +160,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* sQ = base;                // two query tiles
   unsigned char* sKV = sQ + 2 * S::QT;     // key and value tiles, a ring in the order of their use
-  __shared__ __align__(8) uint64_t q_full, q_empty, full[S::SLOTS], empty[S::SLOTS], v_clean[kTrRing], s_full[2], p_ready[2],
-      o_done[2], item_full[2], item_empty[2], item_clean[2], drained;
+  __shared__ __align__(8) uint64_t q_full, q_empty, full[S::SLOTS], empty[S::SLOTS], v_clean[kTrRing], s_full[2][2], p_ready[2][2],
+      o_done[2][2], item_full[2], item_empty[2], item_clean[2], drained;
   __shared__ uint32_t s_tmem;
   __shared__ TreeItem s_item[2];
   __shared__ uint32_t s_odd[2][kMaxTree / 32];   // drafts whose values are not all finite, per item slot
@@ -186,9 +182,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     mbar_init(&q_empty, 1);
     mbar_init(&drained, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_ready[i], kTrSoftmaxWarps / 2);
-      mbar_init(&o_done[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s_full[i][h], 1);
+        mbar_init(&o_done[i][h], 1);
+        mbar_init(&p_ready[i][h], kTrSoftmaxWarps / 2);
+      }
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], kTrSoftmaxWarps + 3);
       mbar_init(&item_clean[i], 1);
@@ -337,35 +335,35 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     } else if (warp == kTrSoftmaxWarps + 1) {
       // ------------------------------------------------------------- products
       // (the whole warp goes through the loop and one lane issues, with descriptors in uniform registers)
-      const uint32_t idesc_s = idesc_bf16_f32(kTrRows, kTrKeys) | (a.negate ? 1u << 13 : 0u);   // bit 13: -A
+      const uint32_t idesc_s = idesc_bf16_f32(kTrRows, kTrHalf) | (a.negate ? 1u << 13 : 0u);   // bit 13: -A
       constexpr uint32_t idesc_o = idesc_bf16_f32_bmn(kTrRows, D);
       const uint64_t dq = sdesc_sw128(smem_addr(sQ)), dk = sdesc_sw128(smem_addr(sKV));
       const uint64_t dv = sdesc_sw128_mn(smem_addr(sKV), kTrKeys * 128, 1024);
       const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
       const uint32_t qk_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32);
-      // scores of query tile i and the key slot into buffer x
-      auto scores = [&](int i, int slot, int x) {
-        const uint32_t ql = q_lo + i * (S::QT >> 4), kl = k_lo + slot * (S::KT >> 4);
+      // scores of query tile i and half a tile of keys
+      auto scores = [&](int i, int slot, int half) {
+        const uint32_t ql = q_lo + i * (S::QT >> 4), kl = k_lo + ((slot * S::KT + half * (kTrHalf * 128)) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < S::HALVES; ++h)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + S::S_COL + 128 * x, sdesc_from(ql + ((h * (kTrRows * 128) + ks * 32) >> 4), qk_hi),
+              umma_bf16(tmem + S::S_COL + 128 * i + 64 * half, sdesc_from(ql + ((h * (kTrRows * 128) + ks * 32) >> 4), qk_hi),
                         sdesc_from(kl + ((h * (kTrKeys * 128) + ks * 32) >> 4), qk_hi), idesc_s, (h | ks) != 0);
-          umma_commit(&s_full[x]);
+          umma_commit(&s_full[i][half]);
         }
         __syncwarp();
       };
-      // the outputs of tile i take the weights of buffer x
-      auto outputs = [&](int i, int slot, int x, bool more) {
-        const uint32_t vl = v_lo + slot * (S::KT >> 4);
+      // the outputs of tile i take the weights of half a tile
+      auto outputs = [&](int i, int slot, int half, bool more) {
+        const uint32_t vl = v_lo + ((slot * S::KT + half * (kTrHalf * 128)) >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < kTrKeys / 16; ++ks)
-            umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * x + 8 * ks, sdesc_from(vl + ((ks * 2048) >> 4), v_hi),
-                         idesc_o, more || ks != 0);
-          umma_commit(&o_done[x]);
+          for (int ks = 0; ks < kTrHalf / 16; ++ks)
+            umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 64 * half + 8 * ks,
+                         sdesc_from(vl + ((ks * 2048) >> 4), v_hi), idesc_o, more || ks != 0);
+          umma_commit(&o_done[i][half]);
         }
         __syncwarp();
       };
@@ -387,48 +385,43 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         __syncwarp();
         if (!found) break;
         const uint32_t l0 = 2u * (uint32_t)kt;                    // the item's first tile of the ring
-        // scores of the item's key tile j, for one tile of queries into buffer x or for both
-        auto score_tile = [&](int j, int i, int x, bool last) {
-          const uint32_t s = (l0 + key_load(j)) % S::SLOTS;
-          scores(i, s, x);
-          if (last) {
-            commit(&empty[s]);
-            if (j + 1 == nt) commit(&q_empty);
-          }
-        };
+        const int tiles = pair ? 2 : 1, halves = 2 * nt;
         ok = wait(&q_full, k & 1) && full_tile(l0);
         if (!ok) break;
         tc_fence_after();
-        const int ahead = pair ? 1 : 2;                           // key tiles whose scores are taken before the first outputs
-        score_tile(0, 0, 0, !pair);
-        if (pair) score_tile(0, 1, 1, true);
-        if (!pair && nt > 1) {
-          ok = full_tile(l0 + key_load(1));
-          if (!ok) break;
-          tc_fence_after();
-          score_tile(1, 0, 1, true);
-        }
-        for (int j = 0; j < nt && ok; ++j) {
-          const uint32_t l = l0 + value_load(j, nt);
-          const int g = (kt + j) & (kTrRing - 1);
-          ok = full_tile(l);
-          if (ok && j >= look) {
-            ok = wait(&v_clean[g], (clean_par >> g) & 1u);
-            clean_par ^= 1u << g;
+        for (int t = 0; t < 2; ++t)
+          for (int i = 0; i < tiles; ++i) scores(i, l0 % S::SLOTS, t);
+        commit(&empty[l0 % S::SLOTS]);
+        if (nt == 1) commit(&q_empty);
+        for (int t = 0; t < halves && ok; ++t) {                  // half tile t: outputs, and the scores of half tile t + 2
+          const int j = t >> 1, h = t & 1, g = (kt + j) & (kTrRing - 1);
+          const uint32_t vs = (l0 + value_load(j, nt)) % S::SLOTS, ks = (l0 + key_load(j + 1)) % S::SLOTS;
+          const bool next = t + 2 < halves;
+          if (h == 0) {
+            ok = full_tile(l0 + value_load(j, nt));
+            if (ok && j >= look) {
+              ok = wait(&v_clean[g], (clean_par >> g) & 1u);
+              clean_par ^= 1u << g;
+            }
           }
-          if (!ok) break;
-          const int n1 = j + ahead;                               // the key tile whose scores come next
-          for (int i = 0; i < (pair ? 2 : 1) && ok; ++i) {
-            const int x = pair ? i : j & 1;
-            ok = wait(&p_ready[x], (p_par >> x) & 1u);
-            p_par ^= 1u << x;
-            if (ok && n1 < nt && i == 0) ok = full_tile(l0 + key_load(n1));
+          for (int i = 0; i < tiles && ok; ++i) {
+            ok = wait(&p_ready[i][h], (p_par >> (2 * i + h)) & 1u);
             if (!ok) break;
+            p_par ^= 1u << (2 * i + h);
             tc_fence_after();
-            outputs(i, l % S::SLOTS, x, j != 0);
-            if (n1 < nt) score_tile(n1, i, x, !pair || i == 1);
+            outputs(i, vs, h, t != 0);
+            if (!next) continue;
+            if (h == 0 && i == 0) {
+              ok = full_tile(l0 + key_load(j + 1));
+              if (!ok) break;
+              tc_fence_after();
+            }
+            scores(i, ks, h);
           }
-          if (ok) commit(&empty[l % S::SLOTS]);
+          if (!ok || h == 0) continue;
+          commit(&empty[vs]);
+          if (next) commit(&empty[ks]);
+          if (j + 2 == nt) commit(&q_empty);
         }
         if (!ok) break;
         kt += nt;
@@ -580,7 +573,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + S::O_COL + 128 * i + lane_off;
     bool ok = true;
-    // parities of the next score tile and of the last outputs, by buffer (a block with one tile uses both)
+    // Parities of the next scores and outputs, by half. A parity tells a phase only from its neighbours: with a barrier for
+    // each half, the outputs before the last ones of a barrier are behind scores that this warp has seen.
     uint32_t s_par = 0u, o_par = 0u;
     int kt = 0;                                                   // key tiles of the items before
     for (int k = 0; ok; ++k) {
@@ -596,47 +590,48 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         const int d0 = it.n - it.T;                               // first draft's position
         const int packed = it.row0 + (real ? tok : 0);
         float mx = -INFINITY, la = 0.f, lb = 0.f;                 // running maximum (unscaled) and two halves of the sum
-        int x_last = 0;
-        for (int j = 0; j < nt; ++j) {
-          const int x = pair ? i : j & 1, key0 = (it.j0 + j) * kTrKeys;
-          const uint32_t tS = tmem + S::S_COL + 128 * x + lane_off;
-          ok = __all_sync(kFull, mbar_wait(&s_full[x], (s_par >> x) & 1u, a.wait_ns));
+        for (int t = 0; t < 2 * nt; ++t) {
+          const int h = t & 1, key0 = it.j0 * kTrKeys + t * kTrHalf;
+          const uint32_t tS = tmem + S::S_COL + 128 * i + 64 * h + lane_off;
+          ok = __all_sync(kFull, mbar_wait(&s_full[i][h], (s_par >> h) & 1u, a.wait_ns));
           if (!ok) break;
           tc_fence_after();
-          s_par ^= 1u << x;
+          s_par ^= 1u << h;
           if (!idle) {
             // what is not seen in this tile: drafts, what is behind the sequence, pages outside the pool
-            const int ring = (kt + j) & (kTrRing - 1);
+            const int ring = (kt + (t >> 1)) & (kTrRing - 1);
             const bool any_bad = s_any_bad[ring] != 0u;
-            const bool cut = key0 + kTrKeys > d0 || any_bad;
-            uint32_t bits[4];
-            if (cut) {
-              seen_bits(a, packed, tok, it.T, d0, key0, bits);
-              if (any_bad) {
+            if (key0 + kTrHalf > d0 || any_bad) {
+              // (rare: such scores are replaced in tensor memory, before and apart from what most tiles go through)
+#pragma unroll 1
+              for (int w = 0; w < 2; ++w) {
+                const uint32_t m = seen_bits(a, packed, tok, it.T, key0 + 32 * w - d0) & ~(any_bad ? s_bad[ring][2 * h + w] : 0u);
+                if (!__any_sync(kFull, m != 0xffffffffu)) continue;
+                uint32_t u[32];
+                tmem_ld_x32(tS + 32 * w, u);
+                tmem_wait_ld();
 #pragma unroll
-                for (int w = 0; w < 4; ++w) bits[w] &= ~s_bad[ring][w];
+                for (int c = 0; c < 32; ++c) u[c] = m >> c & 1u ? u[c] : 0xff800000u;
+                tmem_st_x32(tS + 32 * w, u);
               }
+              tmem_wait_st();
             }
             // Weights against the maximum that the row has, which covers most tiles. Where their sum says that
             // it does not (and in the first tile, which has none), the scores, still in tensor memory, are read
             // again and the maximum is taken first.
-            uint32_t p[64];
+            uint32_t p[kTrHalf / 2];
             float ta, tb, m2 = mx * a.scale2;
             bool over = real;                                     // this row needs its maximum (in a pass that takes it)
-            for (bool raise = j == 0;; raise = true) {
-              uint32_t u[128];
+            for (bool raise = t == 0;; raise = true) {
+              uint32_t u[kTrHalf];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) tmem_ld_x32(tS + 32 * c, u + 32 * c);
+              for (int c = 0; c < kTrHalf / 32; ++c) tmem_ld_x32(tS + 32 * c, u + 32 * c);
               tmem_wait_ld();
               float* y = reinterpret_cast<float*>(u);
-              if (cut) {
-#pragma unroll
-                for (int c = 0; c < 128; ++c) y[c] = bits[c >> 5] >> (c & 31) & 1u ? y[c] : -INFINITY;
-              }
               if (raise) {
                 float ma = y[0], mb = y[1];
 #pragma unroll
-                for (int c = 2; c < 128; c += 2) {
+                for (int c = 2; c < kTrHalf; c += 2) {
                   ma = fmaxf(ma, y[c]);
                   mb = fmaxf(mb, y[c + 1]);
                 }
@@ -648,9 +643,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
                 m2 = n2;
                 la *= f;
                 lb *= f;
-                if (j > 0) {
+                if (t > 0) {
                   // the last product must be in before its accumulators are rescaled
-                  ok = __all_sync(kFull, mbar_wait(&o_done[x_last], (o_par >> x_last & 1u) ^ 1u, a.wait_ns));
+                  ok = __all_sync(kFull, mbar_wait(&o_done[i][h ^ 1], (o_par >> (h ^ 1) & 1u) ^ 1u, a.wait_ns));
                   if (!ok) break;
                   tc_fence_after();
                   // (rare, and the scores hold most registers: eight columns at a time)
@@ -671,12 +666,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
                 const float off = shift ? mx : 0.f;
                 ms = shift ? 0.f : ms;
 #pragma unroll
-                for (int c = 0; c < 128; c += 2) add2(y[c], y[c + 1], -off, -off);
+                for (int c = 0; c < kTrHalf; c += 2) add2(y[c], y[c + 1], -off, -off);
               }
               const uint64_t sc = pack_f2(a.scale2, a.scale2), mm = pack_f2(ms, ms);
               ta = tb = 0.f;
 #pragma unroll
-              for (int c = 0; c < 64; ++c) {
+              for (int c = 0; c < kTrHalf / 2; ++c) {
                 float y0, y1;
                 unpack_f2(fma_f2(pack_f2(y[2 * c], y[2 * c + 1]), sc, mm), y0, y1);
                 y0 = pr_ex2(y0);
@@ -692,17 +687,15 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             la += ta;
             lb += tb;
             tmem_st_x32(tS, p);
-            tmem_st_x32(tS + 32, p + 32);
             tmem_wait_st();
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[x]);
-          o_par ^= 1u << x;
-          x_last = x;
+          if (lane == 0) mbar_arrive(&p_ready[i][h]);
+          o_par ^= 1u << h;
         }
         // ---- outputs
-        if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[x_last], (o_par >> x_last & 1u) ^ 1u, a.wait_ns));
+        if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[i][1], (o_par >> 1 & 1u) ^ 1u, a.wait_ns));   // (an even number of halves)
         if (ok) ok = __all_sync(kFull, mbar_wait(&item_clean[slot], (k >> 1) & 1, a.wait_ns));
         if (ok && !idle) {
           tc_fence_after();
@@ -713,9 +706,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
           auto put_back = [&](int col, uint32_t (&o)[32]) {
             for (int t = it.j0 * kTrKeys > d0 ? it.j0 * kTrKeys - d0 : 0; t < min(it.T, it.j1 * kTrKeys - d0); ++t) {
               if (!(s_odd[slot][t >> 5] >> (t & 31) & 1u)) continue;
-              uint32_t one[4];
-              seen_bits(a, packed, tok, it.T, d0, d0 + t, one);
-              if (!real || !(one[0] & 1u)) continue;
+              if (!real || !(seen_bits(a, packed, tok, it.T, t) & 1u)) continue;
               const int pos = d0 + t, ps = 1 << a.page_shift;
               const int page = a.page_table[(int64_t)it.b * a.pt_stride + (pos >> a.page_shift)];
               const __nv_bfloat16* v = a.v_pool + ((((int64_t)page * a.HKV + it.kv) << a.page_shift) + (pos & (ps - 1))) * D + col;
@@ -770,20 +761,6 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
           // the accumulators have been read before the next item's weights let a product write them
           tc_fence_before();
         }
-      }
-      if (i == 1 && !pair) {
-        // Tile 0 goes through both buffers. These warps follow it, phase by phase: a parity tells a phase only from its
-        // neighbours, so one who ran ahead would take a phase of this item for one of the next.
-        for (int j = 0; j < nt && ok; ++j) {
-          ok = __all_sync(kFull, mbar_wait(&s_full[j & 1], (s_par >> (j & 1)) & 1u, a.wait_ns));
-          s_par ^= 1u << (j & 1);
-          o_par ^= 1u << (j & 1);
-        }
-      } else if (pair) {
-        // the other tile's buffer took nt phases (what this tile waits for next was issued behind all of them)
-        const uint32_t flip = (uint32_t)(nt & 1) << (i ^ 1);
-        s_par ^= flip;
-        o_par ^= flip;
       }
       kt += nt;
       __syncwarp();
