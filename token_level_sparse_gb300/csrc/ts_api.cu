@@ -47,7 +47,6 @@ void free_ctx_buffers(ts_ctx* c) {
   cudaFree(c->q4_part_ml);
   cudaFree(c->tree_part_o);
   cudaFree(c->tree_part_ml);
-  cudaFree(c->tree_base);
   cudaFree(c->step_partials);
   cudaFree(c->step_hist);
   cudaFree(c->step_mass);
@@ -210,7 +209,6 @@ ts_status ts_create(ts_ctx** out, const ts_config* cfg) {
     const size_t slots = (size_t)tree_part_slots(ctx->num_sms);
     chk(alloc(&ctx->tree_part_o, slots * 256 * D));
     chk(alloc(&ctx->tree_part_ml, slots * 256));
-    chk(alloc(&ctx->tree_base, B + 1));
   }
   chk(alloc(&ctx->gsync, 4));
   if (e == cudaSuccess) chk(cudaMemset(ctx->gsync, 0, 4 * sizeof(unsigned)));   // then kept zero by each launch

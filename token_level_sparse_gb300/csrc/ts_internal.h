@@ -74,7 +74,6 @@ struct ts_ctx {
   float2* q4_part_ml = nullptr;          // ... and their (max, sum), also the score's [H][slots]
   float* tree_part_o = nullptr;          // tree attention: parts [2 num_sms][d / 4][256 rows][4]
   float2* tree_part_ml = nullptr;        // ... and their (max, sum) [2 num_sms][256]
-  int64_t* tree_base = nullptr;          // [max_batch + 1] key tiles before each sequence's
   int64_t kernels = 0;           // kernel launches issued
   // persistent decode-step kernel
   int step_grid = 0;                     // CTAs of the cooperative launch (0: not yet sized)

@@ -66,7 +66,6 @@ struct TreeArgs {
   float* lse;
   float* part_o;                 // [2 slots per CTA][d / 4][256 rows][4]
   float2* part_ml;               // [2 slots per CTA][256 rows]: maximum (unscaled), sum
-  int64_t* seq_base;             // [B + 1] key tiles before each sequence's
   int* status;
   uint64_t wait_ns;
 };
@@ -440,11 +439,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         if (b < a.B) s = tree_seq(a, b);
         const int64_t w = b < a.B ? s.work(a.HKV) : 0;
         const int64_t run = work + warp_scan_ll(w, lane);
-        if (blockIdx.x == 0 && b < a.B) {
-          if (s.err) set_error(a.status, s.err);
-          a.seq_base[b + 1] = run;
-          if (b == 0) a.seq_base[0] = 0;
-        }
+        if (blockIdx.x == 0 && s.err) set_error(a.status, s.err);
         work = __shfl_sync(kFull, run, 31);
       }
       const int ctas = (int)min((int64_t)gridDim.x, work);
@@ -777,9 +772,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
 }
 
 // Joins the sums of blocks that several CTAs had parts of. Eight rows of one KV head to a CTA (neighbouring rows of a block:
-// heads, then tokens), whose sums lie side by side; a thread per row, four columns and every fourth part, so that all of
-// a row's parts are on their way at once. Bound by latency: shares, factors, parts (from L2).
-constexpr int kJoinRows = 8, kJoinGroups = 4;
+// heads, then tokens), whose sums lie side by side; a thread per row, four columns and every second part. Bound by latency:
+// the shares are worked out while the kernel before it still runs, and sums and factors are on their way together.
+constexpr int kJoinRows = 8, kJoinGroups = 2, kJoinBatch = 8;
 constexpr int kJoinParts = 256;  // CTAs of a call, at most
 
 template <int D>
@@ -800,45 +795,69 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(c
   };
   int kv, packed, head;
   place(row, kv, packed, head);
-  int lo = 0;
-  TreeSeq s{};
-  if (tid < kJoinRows && kv < a.HKV) {
-    int hi = a.B;                                                 // the last sequence that begins at or before the row
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu[mid] <= packed) lo = mid; else hi = mid;
+  if (warp == 0) {
+    // lane r < 8: the first key tile of row r's block (-1: no row of a sequence), its key tiles, the row's place
+    int64_t work = 0, t0 = -1;
+    int tiles = 0, at = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      TreeSeq s{};
+      if (b0 + lane < a.B) s = tree_seq(a, b0 + lane);
+      const int64_t w = s.work(a.HKV), run = work + warp_scan_ll(w, lane);
+      for (int r = 0; r < kJoinRows; ++r) {
+        const int p = __shfl_sync(kFull, packed, r);
+        const unsigned m = __ballot_sync(kFull, s.blocks > 0 && p >= s.row0 && p < s.row0 + s.T);
+        if (!m) continue;
+        const int src = __ffs(m) - 1, row0 = __shfl_sync(kFull, s.row0, src), blocks = __shfl_sync(kFull, s.blocks, src);
+        const int n = __shfl_sync(kFull, s.tiles, src);
+        const int64_t before = __shfl_sync(kFull, run - w, src);
+        if (lane == r && kv < a.HKV) {
+          const int tok = p - row0, block = tok / (2 * a.tokens), in = tok - block * 2 * a.tokens;
+          tiles = n;
+          t0 = before + ((int64_t)kv * blocks + block) * n;
+          at = (in / a.tokens) * 128 + in % a.tokens * a.G + head;
+        }
+      }
+      work = __shfl_sync(kFull, run, 31);
     }
-    s = tree_seq(a, lo);
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tid < kJoinRows) {
-    s_parts[row] = 0;
-    if (s.blocks > 0 && packed >= s.row0 && packed < s.row0 + s.T) {
-      const int64_t work = a.seq_base[a.B];
-      const int ctas = (int)min((int64_t)grid, work);
-      const int tok = packed - s.row0, block = tok / (2 * a.tokens), in = tok - block * 2 * a.tokens;
-      const int64_t t0 = a.seq_base[lo] + ((int64_t)kv * s.blocks + block) * s.tiles;
-      const int c0 = share_of(work, ctas, t0), c1 = share_of(work, ctas, t0 + s.tiles - 1);
-      s_first[row] = c0;
-      s_parts[row] = c1 > c0 ? c1 - c0 + 1 : 0;                   // (else the block's outputs are there)
-      s_slot0[row] = 2 * c0 + (share_begin(work, ctas, c0) < t0 ? 1 : 0);
-      s_at[row] = (in / a.tokens) * 128 + in % a.tokens * a.G + head;
+    if (lane < kJoinRows) {
+      int parts = 0;
+      if (t0 >= 0) {
+        const int ctas = (int)min((int64_t)grid, work);
+        const int c0 = share_of(work, ctas, t0), c1 = share_of(work, ctas, t0 + tiles - 1);
+        parts = c1 > c0 ? c1 - c0 + 1 : 0;                        // (else the block's outputs are there)
+        s_first[lane] = c0;
+        s_slot0[lane] = 2 * c0 + (share_begin(work, ctas, c0) < t0 ? 1 : 0);
+        s_at[lane] = at;
+      }
+      s_parts[lane] = parts;
     }
   }
   __syncthreads();
   auto slot_of = [&](int r, int k) { return k == 0 ? s_slot0[r] : 2 * (s_first[r] + k); };
+  const int parts = s_parts[row];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float4* src = reinterpret_cast<const float4*>(a.part_o) + (int64_t)col * 256 + (parts ? s_at[row] : 0);
+  float4 o[kJoinBatch];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int e = 0; e < kJoinBatch; ++e) {
+      const int k = k0 + e * kJoinGroups;
+      if (k < parts) o[e] = src[(int64_t)slot_of(row, k) * COLS * 256];
+    }
+  };
+  load(grp);
   if (warp < kJoinRows && s_parts[warp] > 0) {
     // every part's factor, and the row's sum: a warp per row, a lane per part
-    const int parts = s_parts[warp];
+    const int n = s_parts[warp];
     const float2* ml = a.part_ml + s_at[warp];
     float M = -INFINITY, total = 0.f;
-    for (int k = lane; k < parts; k += 32) {
+    for (int k = lane; k < n; k += 32) {
       const float2 x = ml[(int64_t)slot_of(warp, k) * 256];
       M = fmaxf(M, x.y == 0.f ? -INFINITY : x.x);
     }
     M = warp_max(M);
     const float M2 = M * a.scale2;
-    for (int k = lane; k < parts; k += 32) {
+    for (int k = lane; k < n; k += 32) {
       const float2 x = ml[(int64_t)slot_of(warp, k) * 256];
       const float f = x.y == 0.f ? 0.f : (x.x == M ? 1.f : pr_ex2(from_to(x.x, x.x * a.scale2, M, M2, a.scale2)));
       s_f[warp][k] = f;
@@ -855,18 +874,19 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(c
     }
   }
   __syncthreads();
-  const int parts = s_parts[row];
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* src = reinterpret_cast<const float4*>(a.part_o) + (int64_t)col * 256 + s_at[row];
-#pragma unroll 8
-  for (int k = grp; k < parts; k += kJoinGroups) {
-    const float f = s_f[row][k];
-    const float4 o = src[(int64_t)slot_of(row, k) * COLS * 256];
-    if (f != 0.f) {                                               // (a part whose weight vanishes may hold anything)
-      acc.x = fmaf(f, o.x, acc.x);
-      acc.y = fmaf(f, o.y, acc.y);
-      acc.z = fmaf(f, o.z, acc.z);
-      acc.w = fmaf(f, o.w, acc.w);
+  for (int k0 = grp; k0 < parts; k0 += kJoinBatch * kJoinGroups) {
+    if (k0 != grp) load(k0);
+#pragma unroll
+    for (int e = 0; e < kJoinBatch; ++e) {
+      const int k = k0 + e * kJoinGroups;
+      const float f = k < parts ? s_f[row][k] : 0.f;
+      if (f != 0.f) {                                             // (a part whose weight vanishes may hold anything)
+        acc.x = fmaf(f, o[e].x, acc.x);
+        acc.y = fmaf(f, o[e].y, acc.y);
+        acc.z = fmaf(f, o[e].z, acc.z);
+        acc.w = fmaf(f, o[e].w, acc.w);
+      }
     }
   }
   if (grp > 0) s_acc[grp - 1][tid % (kJoinRows * COLS)] = acc;
@@ -874,11 +894,11 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(c
   if (grp > 0 || parts == 0) return;
 #pragma unroll
   for (int g = 0; g < kJoinGroups - 1; ++g) {
-    const float4 o = s_acc[g][tid];
-    acc.x += o.x;
-    acc.y += o.y;
-    acc.z += o.z;
-    acc.w += o.w;
+    const float4 x = s_acc[g][tid];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
   }
   const float inv = s_inv[row];
   __nv_bfloat16* out = a.out + (int64_t)packed * a.out_stride + (int64_t)(kv * a.G + head) * D + col * 4;
@@ -946,7 +966,6 @@ ts_status launch_tree_attend(ts_ctx* ctx, const TreeCall& c, cudaStream_t s) {
   a.lse = c.lse;
   a.part_o = ctx->tree_part_o;
   a.part_ml = ctx->tree_part_ml;
-  a.seq_base = ctx->tree_base;
   a.status = ctx->status;
   a.wait_ns = ctx->wait_ns;
   const int ps = 1 << ctx->page_shift, rows = a.HKV * ps;
