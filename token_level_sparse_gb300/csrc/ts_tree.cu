@@ -9,7 +9,7 @@
 // memory, as for whole prompts (the softmax with its running maximum is the same), and K and V come page by page.
 //
 // A tile is 128 query rows of one KV head: 128 / G tokens with all G query heads of the group; a block is two
-// neighbouring tiles, which share every key and value tile of 128 tokens. The key tiles of all blocks of all KV heads and
+// neighbouring tiles, which share every key and value tile of 64 tokens. The key tiles of all blocks of all KV heads and
 // sequences, one behind another, are dealt to one CTA per SM in equal, contiguous shares, whatever the lengths are. A
 // share that begins or ends inside a block leaves its sums in fp32 (unnormalised, with maximum and sum), and a second kernel
 // joins them, in order: the same bits every time. Roles of a CTA:
@@ -33,16 +33,15 @@ namespace ts {
 namespace {
 
 constexpr int kTrRows = 128;     // query rows of a tile
-constexpr int kTrKeys = 128;     // tokens of a key tile
-constexpr int kTrHalf = 64;      // keys of a score buffer: half a tile
+constexpr int kTrKeys = 64;      // tokens of a key tile
 constexpr int kTrSoftmaxWarps = 8;
 constexpr int kTrThreads = (kTrSoftmaxWarps + 4) * 32;
 // Registers a thread: 168 at launch (65536 / 384), shared out as in the prompt attention.
 constexpr int kTrSoftmaxRegs = 208, kTrOtherRegs = 88;
 static_assert(2 * kTrSoftmaxRegs + kTrOtherRegs <= 3 * 168, "register shares");
-// Per key tile, eight of which are told apart: the ring holds a value tile that is in use and SLOTS - 1 tiles behind it,
-// half of them keys, so nothing is more than seven key tiles ahead of anything.
-constexpr int kTrRing = 8;
+// What is kept per key tile, for the last sixteen: the ring holds a value tile that is in use and at most 19 tiles behind it,
+// so nothing is more than eleven key tiles ahead of anything.
+constexpr int kTrRing = 16;
 constexpr float kTrMaxSum = 16384.f;   // of a tile's weights against a maximum taken earlier
 
 struct TreeArgs {
@@ -75,11 +74,11 @@ struct TrShape {
   static constexpr int HALVES = D / 64;
   static constexpr int QT = kTrRows * D * 2;    // bytes of a query tile
   static constexpr int KT = kTrKeys * D * 2;    // bytes of a key or value tile
-  static constexpr int SLOTS = D == 128 ? 5 : 10;   // key and value tiles under way or in use
+  static constexpr int SLOTS = D == 128 ? 10 : 20;  // key and value tiles under way or in use
   static constexpr int SMEM = 2 * QT + SLOTS * KT + 1024;
   static_assert(SMEM + 1536 <= 227 * 1024, "shared memory of an SM");
   static constexpr uint32_t TMEM_COLS = 512;
-  // tile i: scores of half tile h at 128 i + 64 h (weights over the first 32 columns), outputs at 256 + 128 i
+  // tile i: scores of key tile t at 128 i + 64 (t % 2) (weights over the first 32 columns), outputs at 256 + 128 i
   static constexpr uint32_t S_COL = 0, O_COL = 256;
 };
 
@@ -165,8 +164,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   __shared__ TreeItem s_item[2];
   __shared__ uint32_t s_odd[2][kMaxTree / 32];   // drafts whose values are not all finite, per item slot
   __shared__ int s_any_odd[2];
-  // keys of a tile whose page lies outside the pool, and whether there are any, for the last eight key tiles
-  __shared__ uint32_t s_bad[kTrRing][4];
+  // keys of a tile whose page lies outside the pool, and whether there are any
+  __shared__ uint32_t s_bad[kTrRing][2];
   __shared__ uint32_t s_any_bad[kTrRing];
 
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
@@ -230,7 +229,10 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       bool ok = true;
       int items = 0, kt = 0;                                      // loaded so far: items' queries, key tiles
       uint32_t loads = 0;                                         // ... tiles of the ring
-      const int ps = 1 << a.page_shift, per_tile = kTrKeys >> a.page_shift;
+      uint32_t slot = 0, phase = 0;                               // where the next one goes
+      const int ps = 1 << a.page_shift;
+      const int tile_shift = ps == 1 ? 6 : 2;                     // log2 of a tile's pages
+      const int per = ps == 1 ? 1 : 8, words = ps == 1 ? 2 : 1;
       auto all = [&](bool x) -> bool { return __all_sync(kFull, x); };
       for (;;) {
         ok = all(read_item(items, it, two, drafts_from));
@@ -240,61 +242,83 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         if (!it.found) break;
         const int32_t* pages = a.page_table + (int64_t)it.b * a.pt_stride;
         const int n_pages = (it.n + ps - 1) >> a.page_shift;
-        // this lane's pages of a tile (four where a page holds one token); -1 behind the sequence
-        auto fetch = [&](int j, int (&p)[4]) {
+        // The pages of `per` tiles at a time, one to a lane (two where a page holds one token, for a single tile); -1, whose
+        // copy is filled with zeros, behind the sequence and for what is no page of the pool (`out`: those).
+        int page[2], ahead[2];
+        unsigned out[2] = {0u, 0u};
+        auto fetch = [&](int j, int (&p)[2]) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int at = j * per_tile + lane + 32 * k;
-            p[k] = lane + 32 * k < per_tile && at < n_pages ? pages[at] : -1;
+          for (int k = 0; k < 2; ++k) {
+            const int at = (j << tile_shift) + lane + 32 * k;
+            p[k] = k < words && at < n_pages ? pages[at] : -1;
           }
         };
-        // -1 (the copy is filled with zeros) for what is no page of the pool either; which keys that leaves out
-        auto vet = [&](int j, int (&p)[4]) {
-          uint32_t bad[4] = {0u, 0u, 0u, 0u};
+        auto vet = [&](int j) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const bool there = lane + 32 * k < per_tile && j * per_tile + lane + 32 * k < n_pages;
-            const bool out = there && (p[k] < 0 || (int64_t)p[k] >= a.num_pages);
-            if (out) p[k] = -1;
-            const unsigned m = __ballot_sync(kFull, out);
-            if (m) {
-              if (lane == 0) set_error(a.status, TS_ERR_PAGE_OOB);
-              if (ps == 1) {
-                bad[k] = m;
-              } else {                                            // (k is 0: eight pages, two to a word)
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                  bad[w] |= (m >> (2 * w) & 1u ? 0xffffu : 0u) | (m >> (2 * w + 1) & 1u ? 0xffff0000u : 0u);
-              }
-            }
+          for (int k = 0; k < 2; ++k) {
+            const bool there = k < words && (j << tile_shift) + lane + 32 * k < n_pages;
+            const bool bad = there && (page[k] < 0 || (int64_t)page[k] >= a.num_pages);
+            if (bad) page[k] = -1;
+            out[k] = __ballot_sync(kFull, bad);
           }
+          if ((out[0] | out[1]) && lane == 0) set_error(a.status, TS_ERR_PAGE_OOB);
+        };
+        // which keys of tile j (one of those at hand) its pages leave out
+        auto note = [&](int in) {
           if (lane == 0) {
-            const uint32_t any = bad[0] | bad[1] | bad[2] | bad[3];
-            s_any_bad[kt & (kTrRing - 1)] = any;
-            if (any) {
-#pragma unroll
-              for (int w = 0; w < 4; ++w) s_bad[kt & (kTrRing - 1)][w] = bad[w];
+            uint32_t bad[2] = {out[0], out[1]};
+            if (ps != 1) {                                        // four pages, two to a word
+              const unsigned m = out[0] >> (4 * in);
+              bad[0] = (m & 1u ? 0xffffu : 0u) | (m & 2u ? 0xffff0000u : 0u);
+              bad[1] = (m & 4u ? 0xffffu : 0u) | (m & 8u ? 0xffff0000u : 0u);
             }
+            const int r = kt & (kTrRing - 1);
+            s_any_bad[r] = bad[0] | bad[1];
+            s_bad[r][0] = bad[0];
+            s_bad[r][1] = bad[1];
           }
           ++kt;
         };
-        auto load = [&](const CUtensorMap* map, const int (&p)[4]) -> bool {
-          const uint32_t s = loads % S::SLOTS, round = loads / S::SLOTS;
-          if (round > 0 && !all(mbar_wait(&empty[s], (round - 1) & 1, a.wait_ns))) return false;
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], S::KT);
-          __syncwarp();
-          ++loads;
+        // a tile's pages, a copy for each and 64 columns: the same in every lane, or a lane's own
+        auto pick = [&](int in, int (&p)[4]) {
+          if (ps != 1) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (lane + 32 * k < per_tile)
+            for (int k = 0; k < 4; ++k) p[k] = __shfl_sync(kFull, page[0], 4 * in + k);
+          } else {
+            p[0] = p[2] = page[0];
+            p[1] = p[3] = page[1];
+          }
+        };
+        auto load = [&](const CUtensorMap* map, const int (&p)[4]) -> bool {
+          if (loads >= S::SLOTS && !all(mbar_wait(&empty[slot], phase ^ 1u, a.wait_ns))) return false;
+          unsigned char* dst = sKV + slot * S::KT;
+          if (ps != 1) {
+            // (one lane of a converged warp, operands the same in all of them)
+            if (elect_one()) {
+              mbar_arrive_expect_tx(&full[slot], S::KT);
+#pragma unroll
               for (int h = 0; h < S::HALVES; ++h)
-                tma_load_3d(sKV + s * S::KT + h * (kTrKeys * 128) + (lane + 32 * k) * ps * 128, map, h * 64, it.kv * ps, p[k],
-                            &full[s]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  tma_load_3d(dst + h * (kTrKeys * 128) + k * 2048, map, h * 64, it.kv * kPage, p[k], &full[slot]);
+            }
+            __syncwarp();
+          } else {
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::KT);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2 * S::HALVES; ++k)
+              tma_load_3d(dst + (lane + 32 * k) * 128, map, (k >> 1) * 64, it.kv, p[k], &full[slot]);
+          }
+          ++loads;
+          if (++slot == S::SLOTS) {
+            slot = 0;
+            phase ^= 1u;
+          }
           return true;
         };
-        int cur[4], next[4] = {-1, -1, -1, -1};
-        fetch(it.j0, cur);
-        if (it.j0 + 1 < it.j1) fetch(it.j0 + 1, next);
+        fetch(it.j0, page);
+        if (it.j0 + per < it.j1) fetch(it.j0 + per, ahead);
         if (items > 0) ok = all(mbar_wait(&q_empty, (items - 1) & 1, a.wait_ns));
         if (!ok) break;
         const int tiles_q = two ? 2 : 1;
@@ -306,22 +330,29 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
                           &q_full);
         }
         ++items;
-        vet(it.j0, cur);
+        vet(it.j0);
+        note(0);
+        int cur[4], next[4];
+        pick(0, cur);
         ok = load(&a.k, cur);
+        int in = 0;                                               // place of tile j + 1 among the pages at hand
         for (int j = it.j0; j < it.j1 && ok; ++j) {               // K(j + 1), V(j)
-          int after[4] = {-1, -1, -1, -1};
           if (j + 1 < it.j1) {
-            if (j + 2 < it.j1) fetch(j + 2, after);
-            vet(j + 1, next);
+            if (++in == per) {
+              in = 0;
+              page[0] = ahead[0];
+              page[1] = ahead[1];
+              if (j + 1 + per < it.j1) fetch(j + 1 + per, ahead);
+              vet(j + 1);
+            }
+            note(in);
+            pick(in, next);
             ok = load(&a.k, next);
             if (!ok) break;
           }
           ok = load(&a.v, cur);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            cur[k] = next[k];
-            next[k] = after[k];
-          }
+          for (int k = 0; k < 4; ++k) cur[k] = next[k];
         }
         if (!ok) break;
       }
@@ -334,35 +365,35 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     } else if (warp == kTrSoftmaxWarps + 1) {
       // ------------------------------------------------------------- products
       // (the whole warp goes through the loop and one lane issues, with descriptors in uniform registers)
-      const uint32_t idesc_s = idesc_bf16_f32(kTrRows, kTrHalf) | (a.negate ? 1u << 13 : 0u);   // bit 13: -A
+      const uint32_t idesc_s = idesc_bf16_f32(kTrRows, kTrKeys) | (a.negate ? 1u << 13 : 0u);   // bit 13: -A
       constexpr uint32_t idesc_o = idesc_bf16_f32_bmn(kTrRows, D);
       const uint64_t dq = sdesc_sw128(smem_addr(sQ)), dk = sdesc_sw128(smem_addr(sKV));
       const uint64_t dv = sdesc_sw128_mn(smem_addr(sKV), kTrKeys * 128, 1024);
       const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
       const uint32_t qk_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32);
-      // scores of query tile i and half a tile of keys
-      auto scores = [&](int i, int slot, int half) {
-        const uint32_t ql = q_lo + i * (S::QT >> 4), kl = k_lo + ((slot * S::KT + half * (kTrHalf * 128)) >> 4);
+      // scores of query tile i and the key tile in a slot, into buffer x
+      auto scores = [&](int i, int slot, int x) {
+        const uint32_t ql = q_lo + i * (S::QT >> 4), kl = k_lo + slot * (S::KT >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < S::HALVES; ++h)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + S::S_COL + 128 * i + 64 * half, sdesc_from(ql + ((h * (kTrRows * 128) + ks * 32) >> 4), qk_hi),
+              umma_bf16(tmem + S::S_COL + 128 * i + 64 * x, sdesc_from(ql + ((h * (kTrRows * 128) + ks * 32) >> 4), qk_hi),
                         sdesc_from(kl + ((h * (kTrKeys * 128) + ks * 32) >> 4), qk_hi), idesc_s, (h | ks) != 0);
-          umma_commit(&s_full[i][half]);
+          umma_commit(&s_full[i][x]);
         }
         __syncwarp();
       };
-      // the outputs of tile i take the weights of half a tile
-      auto outputs = [&](int i, int slot, int half, bool more) {
-        const uint32_t vl = v_lo + ((slot * S::KT + half * (kTrHalf * 128)) >> 4);
+      // the outputs of tile i take the weights of buffer x
+      auto outputs = [&](int i, int slot, int x, bool more) {
+        const uint32_t vl = v_lo + slot * (S::KT >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < kTrHalf / 16; ++ks)
-            umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 64 * half + 8 * ks,
+          for (int ks = 0; ks < kTrKeys / 16; ++ks)
+            umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 64 * x + 8 * ks,
                          sdesc_from(vl + ((ks * 2048) >> 4), v_hi), idesc_o, more || ks != 0);
-          umma_commit(&o_done[i][half]);
+          umma_commit(&o_done[i][x]);
         }
         __syncwarp();
       };
@@ -384,43 +415,44 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         __syncwarp();
         if (!found) break;
         const uint32_t l0 = 2u * (uint32_t)kt;                    // the item's first tile of the ring
-        const int tiles = pair ? 2 : 1, halves = 2 * nt;
-        ok = wait(&q_full, k & 1) && full_tile(l0);
+        const int tiles = pair ? 2 : 1;
+        ok = wait(&q_full, k & 1);
+        for (int t = 0; t < min(2, nt) && ok; ++t) {
+          ok = full_tile(l0 + key_load(t));
+          if (!ok) break;
+          tc_fence_after();
+          for (int i = 0; i < tiles; ++i) scores(i, (l0 + key_load(t)) % S::SLOTS, t);
+          commit(&empty[(l0 + key_load(t)) % S::SLOTS]);
+        }
         if (!ok) break;
-        tc_fence_after();
-        for (int t = 0; t < 2; ++t)
-          for (int i = 0; i < tiles; ++i) scores(i, l0 % S::SLOTS, t);
-        commit(&empty[l0 % S::SLOTS]);
-        if (nt == 1) commit(&q_empty);
-        for (int t = 0; t < halves && ok; ++t) {                  // half tile t: outputs, and the scores of half tile t + 2
-          const int j = t >> 1, h = t & 1, g = (kt + j) & (kTrRing - 1);
-          const uint32_t vs = (l0 + value_load(j, nt)) % S::SLOTS, ks = (l0 + key_load(j + 1)) % S::SLOTS;
-          const bool next = t + 2 < halves;
-          if (h == 0) {
-            ok = full_tile(l0 + value_load(j, nt));
-            if (ok && j >= look) {
-              ok = wait(&v_clean[g], (clean_par >> g) & 1u);
-              clean_par ^= 1u << g;
-            }
+        if (nt <= 2) commit(&q_empty);
+        for (int t = 0; t < nt && ok; ++t) {                      // outputs of key tile t, scores of key tile t + 2
+          const int x = t & 1, g = (kt + t) & (kTrRing - 1);
+          const uint32_t vl = l0 + value_load(t, nt), kl = l0 + key_load(t + 2);
+          const bool next = t + 2 < nt;
+          ok = full_tile(vl);
+          if (ok && t >= look) {
+            ok = wait(&v_clean[g], (clean_par >> g) & 1u);
+            clean_par ^= 1u << g;
           }
           for (int i = 0; i < tiles && ok; ++i) {
-            ok = wait(&p_ready[i][h], (p_par >> (2 * i + h)) & 1u);
+            ok = wait(&p_ready[i][x], (p_par >> (2 * i + x)) & 1u);
             if (!ok) break;
-            p_par ^= 1u << (2 * i + h);
+            p_par ^= 1u << (2 * i + x);
             tc_fence_after();
-            outputs(i, vs, h, t != 0);
+            outputs(i, vl % S::SLOTS, x, t != 0);
             if (!next) continue;
-            if (h == 0 && i == 0) {
-              ok = full_tile(l0 + key_load(j + 1));
+            if (i == 0) {
+              ok = full_tile(kl);
               if (!ok) break;
               tc_fence_after();
             }
-            scores(i, ks, h);
+            scores(i, kl % S::SLOTS, x);
           }
-          if (!ok || h == 0) continue;
-          commit(&empty[vs]);
-          if (next) commit(&empty[ks]);
-          if (j + 2 == nt) commit(&q_empty);
+          if (!ok) break;
+          commit(&empty[vl % S::SLOTS]);
+          if (next) commit(&empty[kl % S::SLOTS]);
+          if (t + 3 == nt) commit(&q_empty);
         }
         if (!ok) break;
         kt += nt;
@@ -568,8 +600,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + S::O_COL + 128 * i + lane_off;
     bool ok = true;
-    // Parities of the next scores and outputs, by half. A parity tells a phase only from its neighbours: with a barrier for
-    // each half, the outputs before the last ones of a barrier are behind scores that this warp has seen.
+    // Parities of the next scores and outputs, by buffer. A parity tells a phase only from its neighbours: with a barrier for
+    // each buffer, the outputs before the last ones of a barrier are behind scores that this warp has seen.
     uint32_t s_par = 0u, o_par = 0u;
     int kt = 0;                                                   // key tiles of the items before
     for (int k = 0; ok; ++k) {
@@ -585,22 +617,22 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         const int d0 = it.n - it.T;                               // first draft's position
         const int packed = it.row0 + (real ? tok : 0);
         float mx = -INFINITY, la = 0.f, lb = 0.f;                 // running maximum (unscaled) and two halves of the sum
-        for (int t = 0; t < 2 * nt; ++t) {
-          const int h = t & 1, key0 = it.j0 * kTrKeys + t * kTrHalf;
-          const uint32_t tS = tmem + S::S_COL + 128 * i + 64 * h + lane_off;
-          ok = __all_sync(kFull, mbar_wait(&s_full[i][h], (s_par >> h) & 1u, a.wait_ns));
+        for (int t = 0; t < nt; ++t) {
+          const int x = t & 1, key0 = (it.j0 + t) * kTrKeys;
+          const uint32_t tS = tmem + S::S_COL + 128 * i + 64 * x + lane_off;
+          ok = __all_sync(kFull, mbar_wait(&s_full[i][x], (s_par >> x) & 1u, a.wait_ns));
           if (!ok) break;
           tc_fence_after();
-          s_par ^= 1u << h;
+          s_par ^= 1u << x;
           if (!idle) {
             // what is not seen in this tile: drafts, what is behind the sequence, pages outside the pool
-            const int ring = (kt + (t >> 1)) & (kTrRing - 1);
+            const int ring = (kt + t) & (kTrRing - 1);
             const bool any_bad = s_any_bad[ring] != 0u;
-            if (key0 + kTrHalf > d0 || any_bad) {
+            if (key0 + kTrKeys > d0 || any_bad) {
               // (rare: such scores are replaced in tensor memory, before and apart from what most tiles go through)
 #pragma unroll 1
               for (int w = 0; w < 2; ++w) {
-                const uint32_t m = seen_bits(a, packed, tok, it.T, key0 + 32 * w - d0) & ~(any_bad ? s_bad[ring][2 * h + w] : 0u);
+                const uint32_t m = seen_bits(a, packed, tok, it.T, key0 + 32 * w - d0) & ~(any_bad ? s_bad[ring][w] : 0u);
                 if (!__any_sync(kFull, m != 0xffffffffu)) continue;
                 uint32_t u[32];
                 tmem_ld_x32(tS + 32 * w, u);
@@ -614,19 +646,19 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             // Weights against the maximum that the row has, which covers most tiles. Where their sum says that
             // it does not (and in the first tile, which has none), the scores, still in tensor memory, are read
             // again and the maximum is taken first.
-            uint32_t p[kTrHalf / 2];
+            uint32_t p[kTrKeys / 2];
             float ta, tb, m2 = mx * a.scale2;
             bool over = real;                                     // this row needs its maximum (in a pass that takes it)
             for (bool raise = t == 0;; raise = true) {
-              uint32_t u[kTrHalf];
+              uint32_t u[kTrKeys];
 #pragma unroll
-              for (int c = 0; c < kTrHalf / 32; ++c) tmem_ld_x32(tS + 32 * c, u + 32 * c);
+              for (int c = 0; c < kTrKeys / 32; ++c) tmem_ld_x32(tS + 32 * c, u + 32 * c);
               tmem_wait_ld();
               float* y = reinterpret_cast<float*>(u);
               if (raise) {
                 float ma = y[0], mb = y[1];
 #pragma unroll
-                for (int c = 2; c < kTrHalf; c += 2) {
+                for (int c = 2; c < kTrKeys; c += 2) {
                   ma = fmaxf(ma, y[c]);
                   mb = fmaxf(mb, y[c + 1]);
                 }
@@ -640,7 +672,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
                 lb *= f;
                 if (t > 0) {
                   // the last product must be in before its accumulators are rescaled
-                  ok = __all_sync(kFull, mbar_wait(&o_done[i][h ^ 1], (o_par >> (h ^ 1) & 1u) ^ 1u, a.wait_ns));
+                  ok = __all_sync(kFull, mbar_wait(&o_done[i][x ^ 1], (o_par >> (x ^ 1) & 1u) ^ 1u, a.wait_ns));
                   if (!ok) break;
                   tc_fence_after();
                   // (rare, and the scores hold most registers: eight columns at a time)
@@ -661,12 +693,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
                 const float off = shift ? mx : 0.f;
                 ms = shift ? 0.f : ms;
 #pragma unroll
-                for (int c = 0; c < kTrHalf; c += 2) add2(y[c], y[c + 1], -off, -off);
+                for (int c = 0; c < kTrKeys; c += 2) add2(y[c], y[c + 1], -off, -off);
               }
               const uint64_t sc = pack_f2(a.scale2, a.scale2), mm = pack_f2(ms, ms);
               ta = tb = 0.f;
 #pragma unroll
-              for (int c = 0; c < kTrHalf / 2; ++c) {
+              for (int c = 0; c < kTrKeys / 2; ++c) {
                 float y0, y1;
                 unpack_f2(fma_f2(pack_f2(y[2 * c], y[2 * c + 1]), sc, mm), y0, y1);
                 y0 = pr_ex2(y0);
@@ -686,11 +718,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[i][h]);
-          o_par ^= 1u << h;
+          if (lane == 0) mbar_arrive(&p_ready[i][x]);
+          o_par ^= 1u << x;
         }
         // ---- outputs
-        if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[i][1], (o_par >> 1 & 1u) ^ 1u, a.wait_ns));   // (an even number of halves)
+        const int x1 = (nt - 1) & 1;                              // the last outputs
+        if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[i][x1], (o_par >> x1 & 1u) ^ 1u, a.wait_ns));
         if (ok) ok = __all_sync(kFull, mbar_wait(&item_clean[slot], (k >> 1) & 1, a.wait_ns));
         if (ok && !idle) {
           tc_fence_after();
