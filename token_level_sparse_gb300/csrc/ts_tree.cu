@@ -39,8 +39,8 @@ constexpr int kTrThreads = (kTrSoftmaxWarps + 4) * 32;
 // Registers a thread: 168 at launch (65536 / 384), shared out as in the prompt attention.
 constexpr int kTrSoftmaxRegs = 208, kTrOtherRegs = 88;
 static_assert(2 * kTrSoftmaxRegs + kTrOtherRegs <= 3 * 168, "register shares");
-// What is kept per key tile, for the last sixteen: the ring holds a value tile that is in use and at most 19 tiles behind it,
-// so nothing is more than eleven key tiles ahead of anything.
+// What is kept per key tile, for the last sixteen: the ring holds a value tile that is in use and at most 10 keys behind it, so
+// nothing is more than eleven key tiles ahead of anything.
 constexpr int kTrRing = 16;
 constexpr float kTrMaxSum = 16384.f;   // of a tile's weights against a maximum taken earlier
 
@@ -74,8 +74,8 @@ struct TrShape {
   static constexpr int HALVES = D / 64;
   static constexpr int QT = kTrRows * D * 2;    // bytes of a query tile
   static constexpr int KT = kTrKeys * D * 2;    // bytes of a key or value tile
-  static constexpr int SLOTS = D == 128 ? 10 : 20;  // key and value tiles under way or in use
-  static constexpr int SMEM = 2 * QT + SLOTS * KT + 1024;
+  static constexpr int SLOTS = D == 128 ? 5 : 10;   // pairs of key and value tiles under way or in use
+  static constexpr int SMEM = 2 * QT + SLOTS * 2 * KT + 1024;
   static_assert(SMEM + 1536 <= 227 * 1024, "shared memory of an SM");
   static constexpr uint32_t TMEM_COLS = 512;
   // tile i: scores of key tile t at 128 i + 64 (t % 2) (weights over the first 32 columns), outputs at 256 + 128 i
@@ -118,10 +118,6 @@ __device__ __forceinline__ int64_t warp_scan_ll(int64_t x, int lane) {
 __device__ __forceinline__ int64_t share_begin(int64_t work, int ctas, int c) { return work * c / ctas; }
 __device__ __forceinline__ int share_of(int64_t work, int ctas, int64_t t) { return (int)(((t + 1) * ctas - 1) / work); }
 
-// Places in the ring of an item's key tile j and value tile j, counted from its first: K(0), K(1), V(0), K(2), V(1), ...
-__device__ __forceinline__ uint32_t key_load(int j) { return j == 0 ? 0u : 2u * (uint32_t)j - 1u; }
-__device__ __forceinline__ uint32_t value_load(int j, int nt) { return (uint32_t)min(2 * j + 2, 2 * nt - 1); }
-
 struct TreeItem {
   int found, row0, T, n, i0;     // sequence; first token (among the drafts) of the block
   int b, kv, j0, j1;             // key tiles [j0, j1) of the block
@@ -157,8 +153,10 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   extern __shared__ unsigned char dsm_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* sQ = base;                // two query tiles
-  unsigned char* sKV = sQ + 2 * S::QT;     // key and value tiles, a ring in the order of their use
-  __shared__ __align__(8) uint64_t q_full, q_empty, full[S::SLOTS], empty[S::SLOTS], v_clean[kTrRing], s_full[2][2], p_ready[2][2],
+  // The ring: pairs of tiles that are needed and given back together, an item's key tiles being 0 .. nt - 1:
+  // (K0, K1), then (V(t), K(t + 2)) for each t up to nt - 3, then (V(nt - 2), V(nt - 1)); or (K0, V0) where there is one
+  unsigned char* sKV = sQ + 2 * S::QT;
+  __shared__ __align__(8) uint64_t q_full, q_empty, full[S::SLOTS], empty[S::SLOTS], v_clean[S::SLOTS], s_full[2][2], p_ready[2][2],
       o_done[2][2], item_full[2], item_empty[2], item_clean[2], drained;
   __shared__ uint32_t s_tmem;
   __shared__ TreeItem s_item[2];
@@ -193,8 +191,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     for (int i = 0; i < S::SLOTS; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 2);             // the products and the look through
+      mbar_init(&v_clean[i], 1);
     }
-    for (int i = 0; i < kTrRing; ++i) mbar_init(&v_clean[i], 1);
     mbar_fence_init();
   }
   if (tid < 2 * (kMaxTree / 32)) (&s_odd[0][0])[tid] = 0u;
@@ -289,27 +287,36 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             p[1] = p[3] = page[1];
           }
         };
-        auto load = [&](const CUtensorMap* map, const int (&p)[4]) -> bool {
-          if (loads >= S::SLOTS && !all(mbar_wait(&empty[slot], phase ^ 1u, a.wait_ns))) return false;
-          unsigned char* dst = sKV + slot * S::KT;
+        auto copy = [&](unsigned char* dst, const CUtensorMap* map, const int (&p)[4]) {
           if (ps != 1) {
-            // (one lane of a converged warp, operands the same in all of them)
-            if (elect_one()) {
-              mbar_arrive_expect_tx(&full[slot], S::KT);
 #pragma unroll
-              for (int h = 0; h < S::HALVES; ++h)
+            for (int h = 0; h < S::HALVES; ++h)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  tma_load_3d(dst + h * (kTrKeys * 128) + k * 2048, map, h * 64, it.kv * kPage, p[k], &full[slot]);
-            }
-            __syncwarp();
+              for (int k = 0; k < 4; ++k)
+                tma_load_3d(dst + h * (kTrKeys * 128) + k * 2048, map, h * 64, it.kv * kPage, p[k], &full[slot]);
           } else {
-            if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::KT);
-            __syncwarp();
 #pragma unroll
             for (int k = 0; k < 2 * S::HALVES; ++k)
               tma_load_3d(dst + (lane + 32 * k) * 128, map, (k >> 1) * 64, it.kv, p[k], &full[slot]);
           }
+        };
+        auto load = [&](const CUtensorMap* m0, const int (&p0)[4], const CUtensorMap* m1, const int (&p1)[4]) -> bool {
+          if (loads >= S::SLOTS && !all(mbar_wait(&empty[slot], phase ^ 1u, a.wait_ns))) return false;
+          unsigned char* dst = sKV + slot * 2 * S::KT;
+          if (ps != 1) {
+            // (one lane of a converged warp, operands the same in all of them)
+            if (elect_one()) {
+              mbar_arrive_expect_tx(&full[slot], 2 * S::KT);
+              copy(dst, m0, p0);
+              copy(dst + S::KT, m1, p1);
+            }
+          } else {
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2 * S::KT);
+            __syncwarp();
+            copy(dst, m0, p0);
+            copy(dst + S::KT, m1, p1);
+          }
+          __syncwarp();
           ++loads;
           if (++slot == S::SLOTS) {
             slot = 0;
@@ -331,28 +338,37 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         }
         ++items;
         vet(it.j0);
-        note(0);
-        int cur[4], next[4];
-        pick(0, cur);
-        ok = load(&a.k, cur);
-        int in = 0;                                               // place of tile j + 1 among the pages at hand
-        for (int j = it.j0; j < it.j1 && ok; ++j) {               // K(j + 1), V(j)
-          if (j + 1 < it.j1) {
-            if (++in == per) {
-              in = 0;
-              page[0] = ahead[0];
-              page[1] = ahead[1];
-              if (j + 1 + per < it.j1) fetch(j + 1 + per, ahead);
-              vet(j + 1);
-            }
-            note(in);
-            pick(in, next);
-            ok = load(&a.k, next);
-            if (!ok) break;
+        int in = 0, at = it.j0;                                   // the next tile and its place among the pages at hand
+        auto get = [&](int (&p)[4]) {
+          if (in == per) {
+            in = 0;
+            page[0] = ahead[0];
+            page[1] = ahead[1];
+            if (at + per < it.j1) fetch(at + per, ahead);
+            vet(at);
           }
-          ok = load(&a.v, cur);
+          note(in);
+          pick(in, p);
+          ++in;
+          ++at;
+        };
+        int p0[4], p1[4], p2[4];
+        get(p0);
+        if (it.j1 - it.j0 == 1) {
+          ok = load(&a.k, p0, &a.v, p0);
+        } else {
+          get(p1);
+          ok = load(&a.k, p0, &a.k, p1);
+          for (int j = it.j0 + 2; j < it.j1 && ok; ++j) {
+            get(p2);
+            ok = load(&a.v, p0, &a.k, p2);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) cur[k] = next[k];
+            for (int k = 0; k < 4; ++k) {
+              p0[k] = p1[k];
+              p1[k] = p2[k];
+            }
+          }
+          if (ok) ok = load(&a.v, p0, &a.v, p1);
         }
         if (!ok) break;
       }
@@ -371,31 +387,24 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       const uint64_t dv = sdesc_sw128_mn(smem_addr(sKV), kTrKeys * 128, 1024);
       const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
       const uint32_t qk_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32);
-      // scores of query tile i and the key tile in a slot, into buffer x
-      auto scores = [&](int i, int slot, int x) {
-        const uint32_t ql = q_lo + i * (S::QT >> 4), kl = k_lo + slot * (S::KT >> 4);
-        if (elect_one()) {
+      // (by one lane) scores of query tile i and the key tile in half `e` of a slot, into buffer x
+      auto scores = [&](int i, uint32_t slot, uint32_t e, int x) {
+        const uint32_t ql = q_lo + i * (S::QT >> 4), kl = k_lo + (2 * slot + e) * (S::KT >> 4);
 #pragma unroll
-          for (int h = 0; h < S::HALVES; ++h)
+        for (int h = 0; h < S::HALVES; ++h)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + S::S_COL + 128 * i + 64 * x, sdesc_from(ql + ((h * (kTrRows * 128) + ks * 32) >> 4), qk_hi),
-                        sdesc_from(kl + ((h * (kTrKeys * 128) + ks * 32) >> 4), qk_hi), idesc_s, (h | ks) != 0);
-          umma_commit(&s_full[i][x]);
-        }
-        __syncwarp();
+          for (int ks = 0; ks < 4; ++ks)
+            umma_bf16(tmem + S::S_COL + 128 * i + 64 * x, sdesc_from(ql + ((h * (kTrRows * 128) + ks * 32) >> 4), qk_hi),
+                      sdesc_from(kl + ((h * (kTrKeys * 128) + ks * 32) >> 4), qk_hi), idesc_s, (h | ks) != 0);
+        umma_commit(&s_full[i][x]);
       };
-      // the outputs of tile i take the weights of buffer x
-      auto outputs = [&](int i, int slot, int x, bool more) {
-        const uint32_t vl = v_lo + slot * (S::KT >> 4);
-        if (elect_one()) {
+      // (by one lane) the outputs of tile i take the weights of buffer x and the value tile in half `e` of a slot
+      auto outputs = [&](int i, uint32_t slot, uint32_t e, int x, bool more) {
+        const uint32_t vl = v_lo + (2 * slot + e) * (S::KT >> 4);
 #pragma unroll
-          for (int ks = 0; ks < kTrKeys / 16; ++ks)
-            umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 64 * x + 8 * ks,
-                         sdesc_from(vl + ((ks * 2048) >> 4), v_hi), idesc_o, more || ks != 0);
-          umma_commit(&o_done[i][x]);
-        }
-        __syncwarp();
+        for (int ks = 0; ks < kTrKeys / 16; ++ks)
+          umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 64 * x + 8 * ks,
+                       sdesc_from(vl + ((ks * 2048) >> 4), v_hi), idesc_o, more || ks != 0);
       };
       auto commit = [&](uint64_t* bar) {
         if (elect_one()) umma_commit(bar);
@@ -403,9 +412,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(kFull, mbar_wait(bar, parity, a.wait_ns)); };
       bool ok = true;
-      int kt = 0;                                                 // key tiles of the items before
-      uint32_t clean_par = 0u, p_par = 0u;                        // parities of the next waits, by key tile and by buffer
-      auto full_tile = [&](uint32_t l) -> bool { return wait(&full[l % S::SLOTS], (l / S::SLOTS) & 1); };
+      uint32_t slot = 0, phase = 0;                               // the next pair
+      uint32_t clean_par = 0u, p_par = 0u;                        // parities of the next waits, by slot and by buffer
       for (int k = 0;; ++k) {
         ok = __all_sync(kFull, read_item(k, it, two, drafts_from));
         if (!ok) break;
@@ -414,48 +422,68 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(&item_empty[k & 1]);
         __syncwarp();
         if (!found) break;
-        const uint32_t l0 = 2u * (uint32_t)kt;                    // the item's first tile of the ring
         const int tiles = pair ? 2 : 1;
-        ok = wait(&q_full, k & 1);
-        for (int t = 0; t < min(2, nt) && ok; ++t) {
-          ok = full_tile(l0 + key_load(t));
-          if (!ok) break;
-          tc_fence_after();
-          for (int i = 0; i < tiles; ++i) scores(i, (l0 + key_load(t)) % S::SLOTS, t);
-          commit(&empty[(l0 + key_load(t)) % S::SLOTS]);
-        }
-        if (!ok) break;
-        if (nt <= 2) commit(&q_empty);
-        for (int t = 0; t < nt && ok; ++t) {                      // outputs of key tile t, scores of key tile t + 2
-          const int x = t & 1, g = (kt + t) & (kTrRing - 1);
-          const uint32_t vl = l0 + value_load(t, nt), kl = l0 + key_load(t + 2);
-          const bool next = t + 2 < nt;
-          ok = full_tile(vl);
-          if (ok && t >= look) {
-            ok = wait(&v_clean[g], (clean_par >> g) & 1u);
-            clean_par ^= 1u << g;
+        // waits for the next pair, and where values of it (`looked`) are looked through, for that
+        auto arrived = [&](bool looked) -> bool {
+          bool here = mbar_wait(&full[slot], phase, a.wait_ns);
+          if (looked) {
+            here = here && mbar_wait(&v_clean[slot], (clean_par >> slot) & 1u, a.wait_ns);
+            clean_par ^= 1u << slot;
           }
-          for (int i = 0; i < tiles && ok; ++i) {
-            ok = wait(&p_ready[i][x], (p_par >> (2 * i + x)) & 1u);
-            if (!ok) break;
+          return here;
+        };
+        auto advance = [&]() {
+          if (++slot == S::SLOTS) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        };
+        ok = wait(&q_full, k & 1) && __all_sync(kFull, arrived(nt == 1 && look <= 0));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          for (int i = 0; i < tiles; ++i) scores(i, slot, 0, 0);
+          if (nt > 1) {
+            for (int i = 0; i < tiles; ++i) scores(i, slot, 1, 1);
+            umma_commit(&empty[slot]);
+          }
+          if (nt <= 2) umma_commit(&q_empty);
+        }
+        __syncwarp();
+        uint32_t vs = slot, ve = 1;                               // where the values are: slot and half
+        for (int t = 0; t < nt; ++t) {                            // outputs of key tile t, scores of key tile t + 2
+          const int x = t & 1;
+          const bool next = t + 2 < nt, last = t + 1 == nt;
+          bool here = true;
+          if (!last) {
+            advance();
+            here = arrived(look <= (next ? t : nt - 1));
+            vs = slot;
+          }
+          ve = last ? 1u : 0u;
+          for (int i = 0; i < tiles; ++i) {
+            here = mbar_wait(&p_ready[i][x], (p_par >> (2 * i + x)) & 1u, a.wait_ns) && here;
             p_par ^= 1u << (2 * i + x);
+            ok = __all_sync(kFull, here);
+            if (!ok) break;
             tc_fence_after();
-            outputs(i, vl % S::SLOTS, x, t != 0);
-            if (!next) continue;
-            if (i == 0) {
-              ok = full_tile(kl);
-              if (!ok) break;
-              tc_fence_after();
+            if (elect_one()) {
+              outputs(i, vs, ve, x, t != 0);
+              if (next)
+                scores(i, vs, 1, x);
+              else
+                umma_commit(&o_done[i][x]);
+              if (i + 1 == tiles) {
+                if (next || last) umma_commit(&empty[vs]);
+                if (t + 3 == nt) umma_commit(&q_empty);
+              }
             }
-            scores(i, kl % S::SLOTS, x);
+            __syncwarp();
           }
           if (!ok) break;
-          commit(&empty[vl % S::SLOTS]);
-          if (next) commit(&empty[kl % S::SLOTS]);
-          if (t + 3 == nt) commit(&q_empty);
         }
         if (!ok) break;
-        kt += nt;
+        advance();
       }
       if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
       // no product may be under way when tensor memory is given back
@@ -540,19 +568,22 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     } else {
       // ----------------------------------- values that are not finite among the drafts and behind them
       bool ok = true;
-      uint32_t l = 0;                                             // tiles of the ring so far
+      uint32_t slot = 0, phase = 0;                               // the next pair
       for (int k = 0;; ++k) {
         ok = __all_sync(kFull, read_item(k, it, two, drafts_from));
         if (!ok || !it.found) break;
-        // every tile of the ring in turn, keys too: a parity tells a phase only from its neighbours
+        // every pair of the ring in turn, keys too: a parity tells a phase only from its neighbours
         const int nt = it.j1 - it.j0;
-        for (int i = 0; i < 2 * nt && ok; ++i, ++l) {
-          ok = __all_sync(kFull, mbar_wait(&full[l % S::SLOTS], (l / S::SLOTS) & 1, a.wait_ns));
+        for (int m = 0; m < nt && ok; ++m) {
+          ok = __all_sync(kFull, mbar_wait(&full[slot], phase, a.wait_ns));
           if (!ok) break;
-          const bool value = i == 2 * nt - 1 || (i >= 2 && i % 2 == 0);
-          const int j = it.j0 + (i == 2 * nt - 1 ? nt - 1 : i / 2 - 1);
-          if (value && j >= drafts_from) {
-            unsigned char* vt = sKV + l % S::SLOTS * S::KT;
+          const bool end = m + 1 == nt;
+          bool looked = false;
+          for (int e = nt == 1 ? 1 : 0; e < (end ? 2 : 1); ++e) {
+            const int j = it.j0 + m - 1 + e;                      // the value tile in half e
+            if (m + e == 0 || j < drafts_from) continue;
+            looked = true;
+            unsigned char* vt = sKV + (2 * slot + e) * S::KT;
             uint32_t odd = 0u;
 #pragma unroll 8
             for (int c = 0; c < S::KT / 512; ++c) {
@@ -575,12 +606,18 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
                 }
               }
             }
+          }
+          if (looked) {
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&v_clean[((l - i) / 2 + j - it.j0) & (kTrRing - 1)]);
+            if (lane == 0) mbar_arrive(&v_clean[slot]);
           }
-          if (lane == 0) mbar_arrive(&empty[l % S::SLOTS]);
+          if (lane == 0) mbar_arrive(&empty[slot]);
           __syncwarp();
+          if (++slot == S::SLOTS) {
+            slot = 0;
+            phase ^= 1u;
+          }
         }
         if (!ok) break;
         if (lane == 0) {
@@ -600,8 +637,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + S::O_COL + 128 * i + lane_off;
     bool ok = true;
-    // Parities of the next scores and outputs, by buffer. A parity tells a phase only from its neighbours: with a barrier for
-    // each buffer, the outputs before the last ones of a barrier are behind scores that this warp has seen.
+    // Parities of the next scores by buffer, and of an item's last outputs (the last two tiles').
     uint32_t s_par = 0u, o_par = 0u;
     int kt = 0;                                                   // key tiles of the items before
     for (int k = 0; ok; ++k) {
@@ -672,7 +708,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
                 lb *= f;
                 if (t > 0) {
                   // the last product must be in before its accumulators are rescaled
-                  ok = __all_sync(kFull, mbar_wait(&o_done[i][x ^ 1], (o_par >> (x ^ 1) & 1u) ^ 1u, a.wait_ns));
+                  // (the next tile's scores are behind it; the last tile has none)
+                  ok = __all_sync(kFull, t + 1 < nt ? mbar_wait(&s_full[i][x ^ 1], (s_par >> (x ^ 1)) & 1u, a.wait_ns)
+                                                    : mbar_wait(&o_done[i][x ^ 1], (o_par >> (x ^ 1)) & 1u, a.wait_ns));
                   if (!ok) break;
                   tc_fence_after();
                   // (rare, and the scores hold most registers: eight columns at a time)
@@ -719,11 +757,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_ready[i][x]);
-          o_par ^= 1u << x;
         }
         // ---- outputs
-        const int x1 = (nt - 1) & 1;                              // the last outputs
-        if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[i][x1], (o_par >> x1 & 1u) ^ 1u, a.wait_ns));
+        const int x1 = (nt - 1) & 1;
+        if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[i][x1], (o_par >> x1) & 1u, a.wait_ns));
+        o_par ^= nt > 1 ? 3u : 1u;
         if (ok) ok = __all_sync(kFull, mbar_wait(&item_clean[slot], (k >> 1) & 1, a.wait_ns));
         if (ok && !idle) {
           tc_fence_after();
