@@ -9,7 +9,7 @@
 // memory, as for whole prompts (the softmax with its running maximum is the same), and K and V come page by page.
 //
 // A tile is 128 query rows of one KV head: 128 / G tokens with all G query heads of the group; a block is two
-// neighbouring tiles, which share every key and value tile of 64 tokens. The key tiles of all blocks of all KV heads and
+// neighbouring tiles, which share every key and value tile of 128 tokens. The key tiles of all blocks of all KV heads and
 // sequences, one behind another, are dealt to one CTA per SM in equal, contiguous shares, whatever the lengths are. A
 // share that begins or ends inside a block leaves its sums in fp32 (unnormalised, with maximum and sum), and a second kernel
 // joins them, in order: the same bits every time. Roles of a CTA:
@@ -33,15 +33,15 @@ namespace ts {
 namespace {
 
 constexpr int kTrRows = 128;     // query rows of a tile
-constexpr int kTrKeys = 64;      // tokens of a key tile
+constexpr int kTrKeys = 128;     // tokens of a key tile
 constexpr int kTrSoftmaxWarps = 8;
 constexpr int kTrThreads = (kTrSoftmaxWarps + 4) * 32;
 // Registers a thread: 168 at launch (65536 / 384), shared out as in the prompt attention.
 constexpr int kTrSoftmaxRegs = 208, kTrOtherRegs = 88;
 static_assert(2 * kTrSoftmaxRegs + kTrOtherRegs <= 3 * 168, "register shares");
-// What is kept per key tile, for the last sixteen: the ring holds a value tile that is in use and at most 10 keys behind it, so
-// nothing is more than eleven key tiles ahead of anything.
-constexpr int kTrRing = 16;
+// What is kept per key tile, for the last eight: the ring holds a value tile that is in use and SLOTS - 1 tiles behind it, every
+// second one keys, so nothing is more than six key tiles ahead of anything.
+constexpr int kTrRing = 8;
 constexpr float kTrMaxSum = 16384.f;   // of a tile's weights against a maximum taken earlier
 
 struct TreeArgs {
@@ -74,11 +74,12 @@ struct TrShape {
   static constexpr int HALVES = D / 64;
   static constexpr int QT = kTrRows * D * 2;    // bytes of a query tile
   static constexpr int KT = kTrKeys * D * 2;    // bytes of a key or value tile
-  static constexpr int SLOTS = D == 128 ? 5 : 10;   // pairs of key and value tiles under way or in use
-  static constexpr int SMEM = 2 * QT + SLOTS * 2 * KT + 1024;
+  static constexpr int SLOTS = D == 128 ? 5 : 10;   // key and value tiles under way or in use
+  static constexpr int SMEM = 2 * QT + SLOTS * KT + 1024;
   static_assert(SMEM + 1536 <= 227 * 1024, "shared memory of an SM");
   static constexpr uint32_t TMEM_COLS = 512;
-  // tile i: scores of key tile t at 128 i + 64 (t % 2) (weights over the first 32 columns), outputs at 256 + 128 i
+  // score buffer x at 128 x (weights over its first 64 columns): tile x's, or in a block with one tile the one of every
+  // second key tile; outputs of tile i at 256 + 128 i
   static constexpr uint32_t S_COL = 0, O_COL = 256;
 };
 
@@ -118,6 +119,10 @@ __device__ __forceinline__ int64_t warp_scan_ll(int64_t x, int lane) {
 __device__ __forceinline__ int64_t share_begin(int64_t work, int ctas, int c) { return work * c / ctas; }
 __device__ __forceinline__ int share_of(int64_t work, int ctas, int64_t t) { return (int)(((t + 1) * ctas - 1) / work); }
 
+// Places in the ring of an item's key tile j and value tile j, counted from its first: K(0), K(1), V(0), K(2), V(1), ...
+__device__ __forceinline__ uint32_t key_load(int j) { return j == 0 ? 0u : 2u * (uint32_t)j - 1u; }
+__device__ __forceinline__ uint32_t value_load(int j, int nt) { return (uint32_t)min(2 * j + 2, 2 * nt - 1); }
+
 struct TreeItem {
   int found, row0, T, n, i0;     // sequence; first token (among the drafts) of the block
   int b, kv, j0, j1;             // key tiles [j0, j1) of the block
@@ -153,17 +158,15 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   extern __shared__ unsigned char dsm_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* sQ = base;                // two query tiles
-  // The ring: pairs of tiles that are needed and given back together, an item's key tiles being 0 .. nt - 1:
-  // (K0, K1), then (V(t), K(t + 2)) for each t up to nt - 3, then (V(nt - 2), V(nt - 1)); or (K0, V0) where there is one
-  unsigned char* sKV = sQ + 2 * S::QT;
-  __shared__ __align__(8) uint64_t q_full, q_empty, full[S::SLOTS], empty[S::SLOTS], v_clean[S::SLOTS], s_full[2][2], p_ready[2][2],
-      o_done[2][2], item_full[2], item_empty[2], item_clean[2], drained;
+  unsigned char* sKV = sQ + 2 * S::QT;     // key and value tiles, a ring in the order of their use
+  __shared__ __align__(8) uint64_t q_full, q_empty, full[S::SLOTS], empty[S::SLOTS], v_clean[kTrRing], s_full[3], p_ready[3],
+      o_done[3], item_full[2], item_empty[2], item_clean[2], drained;
   __shared__ uint32_t s_tmem;
   __shared__ TreeItem s_item[2];
   __shared__ uint32_t s_odd[2][kMaxTree / 32];   // drafts whose values are not all finite, per item slot
   __shared__ int s_any_odd[2];
   // keys of a tile whose page lies outside the pool, and whether there are any
-  __shared__ uint32_t s_bad[kTrRing][2];
+  __shared__ uint32_t s_bad[kTrRing][4];
   __shared__ uint32_t s_any_bad[kTrRing];
 
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
@@ -178,11 +181,6 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     mbar_init(&q_empty, 1);
     mbar_init(&drained, 1);
     for (int i = 0; i < 2; ++i) {
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(&s_full[i][h], 1);
-        mbar_init(&o_done[i][h], 1);
-        mbar_init(&p_ready[i][h], kTrSoftmaxWarps / 2);
-      }
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], kTrSoftmaxWarps + 3);
       mbar_init(&item_clean[i], 1);
@@ -191,7 +189,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     for (int i = 0; i < S::SLOTS; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 2);             // the products and the look through
-      mbar_init(&v_clean[i], 1);
+    }
+    for (int i = 0; i < kTrRing; ++i) mbar_init(&v_clean[i], 1);
+    for (int i = 0; i < 3; ++i) {          // tile 0, tile 1, and every second key tile of a block with one tile
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_ready[i], kTrSoftmaxWarps / 2);
+      mbar_init(&o_done[i], 1);
     }
     mbar_fence_init();
   }
@@ -229,8 +232,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       uint32_t loads = 0;                                         // ... tiles of the ring
       uint32_t slot = 0, phase = 0;                               // where the next one goes
       const int ps = 1 << a.page_shift;
-      const int tile_shift = ps == 1 ? 6 : 2;                     // log2 of a tile's pages
-      const int per = ps == 1 ? 1 : 8, words = ps == 1 ? 2 : 1;
+      const int tile_shift = ps == 1 ? 7 : 3;                     // log2 of a tile's pages
+      const int per = ps == 1 ? 1 : 4, words = ps == 1 ? 4 : 1;
       auto all = [&](bool x) -> bool { return __all_sync(kFull, x); };
       for (;;) {
         ok = all(read_item(items, it, two, drafts_from));
@@ -240,81 +243,70 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         if (!it.found) break;
         const int32_t* pages = a.page_table + (int64_t)it.b * a.pt_stride;
         const int n_pages = (it.n + ps - 1) >> a.page_shift;
-        // The pages of `per` tiles at a time, one to a lane (two where a page holds one token, for a single tile); -1, whose
+        // The pages of `per` tiles at a time, one to a lane (four where a page holds one token, for a single tile); -1, whose
         // copy is filled with zeros, behind the sequence and for what is no page of the pool (`out`: those).
-        int page[2], ahead[2];
-        unsigned out[2] = {0u, 0u};
-        auto fetch = [&](int j, int (&p)[2]) {
+        int page[4], ahead[4];
+        unsigned out[4] = {0u, 0u, 0u, 0u};
+        auto fetch = [&](int j, int (&p)[4]) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < 4; ++k) {
             const int at = (j << tile_shift) + lane + 32 * k;
             p[k] = k < words && at < n_pages ? pages[at] : -1;
           }
         };
         auto vet = [&](int j) {
+          unsigned any = 0u;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < 4; ++k) {
             const bool there = k < words && (j << tile_shift) + lane + 32 * k < n_pages;
             const bool bad = there && (page[k] < 0 || (int64_t)page[k] >= a.num_pages);
             if (bad) page[k] = -1;
             out[k] = __ballot_sync(kFull, bad);
+            any |= out[k];
           }
-          if ((out[0] | out[1]) && lane == 0) set_error(a.status, TS_ERR_PAGE_OOB);
+          if (any && lane == 0) set_error(a.status, TS_ERR_PAGE_OOB);
         };
-        // which keys of tile j (one of those at hand) its pages leave out
+        // which keys of tile `in` of those at hand its pages leave out
         auto note = [&](int in) {
           if (lane == 0) {
-            uint32_t bad[2] = {out[0], out[1]};
-            if (ps != 1) {                                        // four pages, two to a word
-              const unsigned m = out[0] >> (4 * in);
-              bad[0] = (m & 1u ? 0xffffu : 0u) | (m & 2u ? 0xffff0000u : 0u);
-              bad[1] = (m & 4u ? 0xffffu : 0u) | (m & 8u ? 0xffff0000u : 0u);
-            }
             const int r = kt & (kTrRing - 1);
-            s_any_bad[r] = bad[0] | bad[1];
-            s_bad[r][0] = bad[0];
-            s_bad[r][1] = bad[1];
+            const unsigned m = out[0] >> (8 * in);                // eight pages, two to a word
+            uint32_t any = 0u;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t bad = ps == 1 ? out[w] : (m >> (2 * w) & 1u ? 0xffffu : 0u) | (m >> (2 * w + 1) & 1u ? 0xffff0000u : 0u);
+              s_bad[r][w] = bad;
+              any |= bad;
+            }
+            s_any_bad[r] = any;
           }
           ++kt;
         };
-        // a tile's pages, a copy for each and 64 columns: the same in every lane, or a lane's own
-        auto pick = [&](int in, int (&p)[4]) {
-          if (ps != 1) {
+        // a tile's pages: the same in every lane, or (pages of one token) a lane's own four
+        auto pick = [&](int in, int (&p)[8]) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = __shfl_sync(kFull, page[0], 4 * in + k);
-          } else {
-            p[0] = p[2] = page[0];
-            p[1] = p[3] = page[1];
-          }
+          for (int k = 0; k < 8; ++k) p[k] = ps == 1 ? page[k & 3] : __shfl_sync(kFull, page[0], 8 * in + k);
         };
-        auto copy = [&](unsigned char* dst, const CUtensorMap* map, const int (&p)[4]) {
-          if (ps != 1) {
-#pragma unroll
-            for (int h = 0; h < S::HALVES; ++h)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tma_load_3d(dst + h * (kTrKeys * 128) + k * 2048, map, h * 64, it.kv * kPage, p[k], &full[slot]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 2 * S::HALVES; ++k)
-              tma_load_3d(dst + (lane + 32 * k) * 128, map, (k >> 1) * 64, it.kv, p[k], &full[slot]);
-          }
-        };
-        auto load = [&](const CUtensorMap* m0, const int (&p0)[4], const CUtensorMap* m1, const int (&p1)[4]) -> bool {
+        auto load = [&](const CUtensorMap* map, const int (&p)[8]) -> bool {
           if (loads >= S::SLOTS && !all(mbar_wait(&empty[slot], phase ^ 1u, a.wait_ns))) return false;
-          unsigned char* dst = sKV + slot * 2 * S::KT;
+          unsigned char* dst = sKV + slot * S::KT;
           if (ps != 1) {
             // (one lane of a converged warp, operands the same in all of them)
             if (elect_one()) {
-              mbar_arrive_expect_tx(&full[slot], 2 * S::KT);
-              copy(dst, m0, p0);
-              copy(dst + S::KT, m1, p1);
+              mbar_arrive_expect_tx(&full[slot], S::KT);
+#pragma unroll
+              for (int h = 0; h < S::HALVES; ++h)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  tma_load_3d(dst + h * (kTrKeys * 128) + k * 2048, map, h * 64, it.kv * kPage, p[k], &full[slot]);
             }
           } else {
-            if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2 * S::KT);
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::KT);
             __syncwarp();
-            copy(dst, m0, p0);
-            copy(dst + S::KT, m1, p1);
+#pragma unroll
+            for (int k = 0; k < 4 * S::HALVES; ++k)
+              tma_load_3d(dst + (k >> 2) * (kTrKeys * 128) + (lane + 32 * (k & 3)) * 128, map, (k >> 2) * 64, it.kv, p[k & 3],
+                          &full[slot]);
           }
           __syncwarp();
           ++loads;
@@ -339,11 +331,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         ++items;
         vet(it.j0);
         int in = 0, at = it.j0;                                   // the next tile and its place among the pages at hand
-        auto get = [&](int (&p)[4]) {
+        auto get = [&](int (&p)[8]) {
           if (in == per) {
             in = 0;
-            page[0] = ahead[0];
-            page[1] = ahead[1];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) page[k] = ahead[k];
             if (at + per < it.j1) fetch(at + per, ahead);
             vet(at);
           }
@@ -352,23 +344,18 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
           ++in;
           ++at;
         };
-        int p0[4], p1[4], p2[4];
+        int p0[8], p1[8];
         get(p0);
-        if (it.j1 - it.j0 == 1) {
-          ok = load(&a.k, p0, &a.v, p0);
-        } else {
-          get(p1);
-          ok = load(&a.k, p0, &a.k, p1);
-          for (int j = it.j0 + 2; j < it.j1 && ok; ++j) {
-            get(p2);
-            ok = load(&a.v, p0, &a.k, p2);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              p0[k] = p1[k];
-              p1[k] = p2[k];
-            }
+        ok = load(&a.k, p0);
+        for (int j = it.j0; j < it.j1 && ok; ++j) {               // K(j + 1), V(j)
+          if (j + 1 < it.j1) {
+            get(p1);
+            ok = load(&a.k, p1);
+            if (!ok) break;
           }
-          if (ok) ok = load(&a.v, p0, &a.v, p1);
+          ok = load(&a.v, p0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) p0[k] = p1[k];
         }
         if (!ok) break;
       }
@@ -387,24 +374,25 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       const uint64_t dv = sdesc_sw128_mn(smem_addr(sKV), kTrKeys * 128, 1024);
       const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
       const uint32_t qk_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32);
-      // (by one lane) scores of query tile i and the key tile in half `e` of a slot, into buffer x
-      auto scores = [&](int i, uint32_t slot, uint32_t e, int x) {
-        const uint32_t ql = q_lo + i * (S::QT >> 4), kl = k_lo + (2 * slot + e) * (S::KT >> 4);
+      // (by one lane) scores of query tile i and the key tile in a slot, into the buffer of barrier x
+      auto scores = [&](int i, uint32_t slot, int x) {
+        const uint32_t ql = q_lo + i * (S::QT >> 4), kl = k_lo + slot * (S::KT >> 4);
 #pragma unroll
         for (int h = 0; h < S::HALVES; ++h)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            umma_bf16(tmem + S::S_COL + 128 * i + 64 * x, sdesc_from(ql + ((h * (kTrRows * 128) + ks * 32) >> 4), qk_hi),
+            umma_bf16(tmem + S::S_COL + (x ? 128 : 0), sdesc_from(ql + ((h * (kTrRows * 128) + ks * 32) >> 4), qk_hi),
                       sdesc_from(kl + ((h * (kTrKeys * 128) + ks * 32) >> 4), qk_hi), idesc_s, (h | ks) != 0);
-        umma_commit(&s_full[i][x]);
+        umma_commit(&s_full[x]);
       };
-      // (by one lane) the outputs of tile i take the weights of buffer x and the value tile in half `e` of a slot
-      auto outputs = [&](int i, uint32_t slot, uint32_t e, int x, bool more) {
-        const uint32_t vl = v_lo + (2 * slot + e) * (S::KT >> 4);
+      // (by one lane) the outputs of tile i take the weights of the buffer of barrier x
+      auto outputs = [&](int i, uint32_t slot, int x, bool more) {
+        const uint32_t vl = v_lo + slot * (S::KT >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTrKeys / 16; ++ks)
-          umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + 128 * i + 64 * x + 8 * ks,
-                       sdesc_from(vl + ((ks * 2048) >> 4), v_hi), idesc_o, more || ks != 0);
+          umma_bf16_ts(tmem + S::O_COL + 128 * i, tmem + S::S_COL + (x ? 128 : 0) + 8 * ks, sdesc_from(vl + ((ks * 2048) >> 4), v_hi),
+                       idesc_o, more || ks != 0);
+        umma_commit(&o_done[x]);
       };
       auto commit = [&](uint64_t* bar) {
         if (elect_one()) umma_commit(bar);
@@ -412,8 +400,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(kFull, mbar_wait(bar, parity, a.wait_ns)); };
       bool ok = true;
-      uint32_t slot = 0, phase = 0;                               // the next pair
-      uint32_t clean_par = 0u, p_par = 0u;                        // parities of the next waits, by slot and by buffer
+      int kt = 0;                                                 // key tiles of the items before
+      uint32_t clean_par = 0u, p_par = 0u;                        // parities of the next waits, by key tile and by barrier
+      auto come = [&](uint32_t l) -> bool { return mbar_wait(&full[l % S::SLOTS], (l / S::SLOTS) & 1, a.wait_ns); };
       for (int k = 0;; ++k) {
         ok = __all_sync(kFull, read_item(k, it, two, drafts_from));
         if (!ok) break;
@@ -422,68 +411,62 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(&item_empty[k & 1]);
         __syncwarp();
         if (!found) break;
+        const uint32_t l0 = 2u * (uint32_t)kt;                    // the item's first tile of the ring
         const int tiles = pair ? 2 : 1;
-        // waits for the next pair, and where values of it (`looked`) are looked through, for that
-        auto arrived = [&](bool looked) -> bool {
-          bool here = mbar_wait(&full[slot], phase, a.wait_ns);
-          if (looked) {
-            here = here && mbar_wait(&v_clean[slot], (clean_par >> slot) & 1u, a.wait_ns);
-            clean_par ^= 1u << slot;
+        const int ahead = pair ? 1 : 2;                           // key tiles whose scores are taken before the first outputs
+        ok = wait(&q_full, k & 1);
+        for (int j = 0; j < min(ahead, nt) && ok; ++j) {
+          const uint32_t l = l0 + key_load(j);
+          ok = __all_sync(kFull, come(l));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            for (int i = 0; i < tiles; ++i) scores(i, l % S::SLOTS, pair ? i : 2 * j);
+            umma_commit(&empty[l % S::SLOTS]);
+            if (j + 1 == nt) umma_commit(&q_empty);
           }
-          return here;
-        };
-        auto advance = [&]() {
-          if (++slot == S::SLOTS) {
-            slot = 0;
-            phase ^= 1u;
-          }
-        };
-        ok = wait(&q_full, k & 1) && __all_sync(kFull, arrived(nt == 1 && look <= 0));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          for (int i = 0; i < tiles; ++i) scores(i, slot, 0, 0);
-          if (nt > 1) {
-            for (int i = 0; i < tiles; ++i) scores(i, slot, 1, 1);
-            umma_commit(&empty[slot]);
-          }
-          if (nt <= 2) umma_commit(&q_empty);
+          __syncwarp();
         }
-        __syncwarp();
-        uint32_t vs = slot, ve = 1;                               // where the values are: slot and half
-        for (int t = 0; t < nt; ++t) {                            // outputs of key tile t, scores of key tile t + 2
-          const int x = t & 1;
-          const bool next = t + 2 < nt, last = t + 1 == nt;
-          bool here = true;
-          if (!last) {
-            advance();
-            here = arrived(look <= (next ? t : nt - 1));
-            vs = slot;
+        if (!ok) break;
+        for (int j = 0; j < nt && ok; ++j) {                      // outputs of key tile j, scores of the one that is ahead
+          const uint32_t vl = l0 + value_load(j, nt), kl = l0 + key_load(j + ahead);
+          const int g = (kt + j) & (kTrRing - 1);
+          const bool next = j + ahead < nt;
+          bool here = come(vl);
+          if (j >= look) {
+            here = here && mbar_wait(&v_clean[g], (clean_par >> g) & 1u, a.wait_ns);
+            clean_par ^= 1u << g;
           }
-          ve = last ? 1u : 0u;
-          for (int i = 0; i < tiles; ++i) {
-            here = mbar_wait(&p_ready[i][x], (p_par >> (2 * i + x)) & 1u, a.wait_ns) && here;
-            p_par ^= 1u << (2 * i + x);
+          for (int i = 0; i < tiles && ok; ++i) {
+            const int x = pair ? i : 2 * (j & 1);
+            here = mbar_wait(&p_ready[x], (p_par >> x) & 1u, a.wait_ns) && here;
+            p_par ^= 1u << x;
             ok = __all_sync(kFull, here);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              outputs(i, vs, ve, x, t != 0);
-              if (next)
-                scores(i, vs, 1, x);
-              else
-                umma_commit(&o_done[i][x]);
+              outputs(i, vl % S::SLOTS, x, j != 0);
+              if (i + 1 == tiles) umma_commit(&empty[vl % S::SLOTS]);
+            }
+            __syncwarp();
+            if (!next) continue;
+            if (i == 0) {
+              ok = __all_sync(kFull, come(kl));
+              if (!ok) break;
+              tc_fence_after();
+            }
+            if (elect_one()) {
+              scores(i, kl % S::SLOTS, x);
               if (i + 1 == tiles) {
-                if (next || last) umma_commit(&empty[vs]);
-                if (t + 3 == nt) umma_commit(&q_empty);
+                umma_commit(&empty[kl % S::SLOTS]);
+                if (j + ahead + 1 == nt) umma_commit(&q_empty);
               }
             }
             __syncwarp();
           }
-          if (!ok) break;
         }
         if (!ok) break;
-        advance();
+        kt += nt;
       }
       if (!ok && lane == 0) set_error(a.status, TS_ERR_TIMEOUT);
       // no product may be under way when tensor memory is given back
@@ -568,22 +551,20 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     } else {
       // ----------------------------------- values that are not finite among the drafts and behind them
       bool ok = true;
-      uint32_t slot = 0, phase = 0;                               // the next pair
+      int kt = 0;                                                 // key tiles of the items before
+      uint32_t slot = 0, phase = 0;                               // the next tile of the ring
       for (int k = 0;; ++k) {
         ok = __all_sync(kFull, read_item(k, it, two, drafts_from));
         if (!ok || !it.found) break;
-        // every pair of the ring in turn, keys too: a parity tells a phase only from its neighbours
+        // every tile of the ring in turn, keys too: a parity tells a phase only from its neighbours
         const int nt = it.j1 - it.j0;
-        for (int m = 0; m < nt && ok; ++m) {
+        for (int m = 0; m < 2 * nt && ok; ++m) {
           ok = __all_sync(kFull, mbar_wait(&full[slot], phase, a.wait_ns));
           if (!ok) break;
-          const bool end = m + 1 == nt;
-          bool looked = false;
-          for (int e = nt == 1 ? 1 : 0; e < (end ? 2 : 1); ++e) {
-            const int j = it.j0 + m - 1 + e;                      // the value tile in half e
-            if (m + e == 0 || j < drafts_from) continue;
-            looked = true;
-            unsigned char* vt = sKV + (2 * slot + e) * S::KT;
+          const bool value = m == 2 * nt - 1 || (m >= 2 && m % 2 == 0);
+          const int j = it.j0 + (m == 2 * nt - 1 ? nt - 1 : m / 2 - 1);
+          if (value && j >= drafts_from) {
+            unsigned char* vt = sKV + slot * S::KT;
             uint32_t odd = 0u;
 #pragma unroll 8
             for (int c = 0; c < S::KT / 512; ++c) {
@@ -606,11 +587,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
                 }
               }
             }
-          }
-          if (looked) {
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&v_clean[slot]);
+            if (lane == 0) mbar_arrive(&v_clean[(kt + j - it.j0) & (kTrRing - 1)]);
           }
           if (lane == 0) mbar_arrive(&empty[slot]);
           __syncwarp();
@@ -620,6 +599,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
           }
         }
         if (!ok) break;
+        kt += nt;
         if (lane == 0) {
           mbar_arrive(&item_clean[k & 1]);
           mbar_arrive(&item_empty[k & 1]);
@@ -637,8 +617,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + S::O_COL + 128 * i + lane_off;
     bool ok = true;
-    // Parities of the next scores by buffer, and of an item's last outputs (the last two tiles').
-    uint32_t s_par = 0u, o_par = 0u;
+    uint32_t s_par = 0u, o_par = 0u;                              // parities of the next scores and outputs, by barrier
     int kt = 0;                                                   // key tiles of the items before
     for (int k = 0; ok; ++k) {
       ok = __all_sync(kFull, read_item(k, it, two, drafts_from));
@@ -653,21 +632,24 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         const int d0 = it.n - it.T;                               // first draft's position
         const int packed = it.row0 + (real ? tok : 0);
         float mx = -INFINITY, la = 0.f, lb = 0.f;                 // running maximum (unscaled) and two halves of the sum
-        for (int t = 0; t < nt; ++t) {
-          const int x = t & 1, key0 = (it.j0 + t) * kTrKeys;
-          const uint32_t tS = tmem + S::S_COL + 128 * i + 64 * x + lane_off;
-          ok = __all_sync(kFull, mbar_wait(&s_full[i][x], (s_par >> x) & 1u, a.wait_ns));
+        int x = i;
+        for (int j = 0; j < nt; ++j) {
+          // the outputs before these went to the same barrier where the block has two tiles, else to the other one
+          const int before = x, key0 = (it.j0 + j) * kTrKeys;
+          x = pair ? i : 2 * (j & 1);
+          const uint32_t tS = tmem + S::S_COL + (x ? 128 : 0) + lane_off;
+          ok = __all_sync(kFull, mbar_wait(&s_full[x], (s_par >> x) & 1u, a.wait_ns));
           if (!ok) break;
           tc_fence_after();
           s_par ^= 1u << x;
           if (!idle) {
             // what is not seen in this tile: drafts, what is behind the sequence, pages outside the pool
-            const int ring = (kt + t) & (kTrRing - 1);
+            const int ring = (kt + j) & (kTrRing - 1);
             const bool any_bad = s_any_bad[ring] != 0u;
             if (key0 + kTrKeys > d0 || any_bad) {
               // (rare: such scores are replaced in tensor memory, before and apart from what most tiles go through)
 #pragma unroll 1
-              for (int w = 0; w < 2; ++w) {
+              for (int w = 0; w < 4; ++w) {
                 const uint32_t m = seen_bits(a, packed, tok, it.T, key0 + 32 * w - d0) & ~(any_bad ? s_bad[ring][w] : 0u);
                 if (!__any_sync(kFull, m != 0xffffffffu)) continue;
                 uint32_t u[32];
@@ -685,18 +667,19 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             uint32_t p[kTrKeys / 2];
             float ta, tb, m2 = mx * a.scale2;
             bool over = real;                                     // this row needs its maximum (in a pass that takes it)
-            for (bool raise = t == 0;; raise = true) {
-              uint32_t u[kTrKeys];
-#pragma unroll
-              for (int c = 0; c < kTrKeys / 32; ++c) tmem_ld_x32(tS + 32 * c, u + 32 * c);
-              tmem_wait_ld();
-              float* y = reinterpret_cast<float*>(u);
+            for (bool raise = j == 0;; raise = true) {
               if (raise) {
-                float ma = y[0], mb = y[1];
+                float ma = -INFINITY, mb = -INFINITY;
+#pragma unroll 1
+                for (int c0 = 0; c0 < kTrKeys; c0 += 32) {
+                  uint32_t u[32];
+                  tmem_ld_x32(tS + c0, u);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int c = 2; c < kTrKeys; c += 2) {
-                  ma = fmaxf(ma, y[c]);
-                  mb = fmaxf(mb, y[c + 1]);
+                  for (int c = 0; c < 32; c += 2) {
+                    ma = fmaxf(ma, __uint_as_float(u[c]));
+                    mb = fmaxf(mb, __uint_as_float(u[c + 1]));
+                  }
                 }
                 // each row by itself, so that no row's bits depend on another's: rows that do not need it keep their
                 // maximum, as do rows that are no query of the sequence (their operands may be anything)
@@ -706,14 +689,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
                 m2 = n2;
                 la *= f;
                 lb *= f;
-                if (t > 0) {
+                if (j > 0) {
                   // the last product must be in before its accumulators are rescaled
-                  // (the next tile's scores are behind it; the last tile has none)
-                  ok = __all_sync(kFull, t + 1 < nt ? mbar_wait(&s_full[i][x ^ 1], (s_par >> (x ^ 1)) & 1u, a.wait_ns)
-                                                    : mbar_wait(&o_done[i][x ^ 1], (o_par >> (x ^ 1)) & 1u, a.wait_ns));
+                  ok = __all_sync(kFull, mbar_wait(&o_done[before], (o_par >> before & 1u) ^ 1u, a.wait_ns));
                   if (!ok) break;
                   tc_fence_after();
-                  // (rare, and the scores hold most registers: eight columns at a time)
+                  // (rare: eight columns at a time)
 #pragma unroll 1
                   for (int c = 0; c < D; c += 8) {
                     float o[8];
@@ -726,23 +707,33 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
                 }
               }
               float ms = m2 == -INFINITY ? 0.f : -m2;             // nothing seen yet: every weight is zero
-              if (raise && __any_sync(kFull, far(m2) && m2 != -INFINITY)) {
-                const bool shift = far(m2) && m2 != -INFINITY;
-                const float off = shift ? mx : 0.f;
-                ms = shift ? 0.f : ms;
-#pragma unroll
-                for (int c = 0; c < kTrKeys; c += 2) add2(y[c], y[c + 1], -off, -off);
-              }
+              const bool shift = far(m2) && m2 != -INFINITY;
+              const bool shifts = raise && __any_sync(kFull, shift);
+              if (shifts && shift) ms = 0.f;
+              const float off = shifts && shift ? mx : 0.f;
               const uint64_t sc = pack_f2(a.scale2, a.scale2), mm = pack_f2(ms, ms);
               ta = tb = 0.f;
+              // 64 scores at a time, so that they and the weights fit the registers
 #pragma unroll
-              for (int c = 0; c < kTrKeys / 2; ++c) {
-                float y0, y1;
-                unpack_f2(fma_f2(pack_f2(y[2 * c], y[2 * c + 1]), sc, mm), y0, y1);
-                y0 = pr_ex2(y0);
-                y1 = pr_ex2(y1);
-                add2(ta, tb, y0, y1);
-                p[c] = pack_bf16(y0, y1);
+              for (int c0 = 0; c0 < kTrKeys; c0 += 64) {
+                uint32_t u[64];
+                tmem_ld_x32(tS + c0, u);
+                tmem_ld_x32(tS + c0 + 32, u + 32);
+                tmem_wait_ld();
+                float* y = reinterpret_cast<float*>(u);
+                if (shifts) {
+#pragma unroll
+                  for (int c = 0; c < 64; c += 2) add2(y[c], y[c + 1], -off, -off);
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                  float y0, y1;
+                  unpack_f2(fma_f2(pack_f2(y[2 * c], y[2 * c + 1]), sc, mm), y0, y1);
+                  y0 = pr_ex2(y0);
+                  y1 = pr_ex2(y1);
+                  add2(ta, tb, y0, y1);
+                  p[c0 / 2 + c] = pack_bf16(y0, y1);
+                }
               }
               if (raise) break;
               over = real && (!(ta + tb <= kTrMaxSum) || far(m2));
@@ -752,16 +743,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             la += ta;
             lb += tb;
             tmem_st_x32(tS, p);
+            tmem_st_x32(tS + 32, p + 32);
             tmem_wait_st();
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[i][x]);
+          if (lane == 0) mbar_arrive(&p_ready[x]);
+          o_par ^= 1u << x;
         }
         // ---- outputs
-        const int x1 = (nt - 1) & 1;
-        if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[i][x1], (o_par >> x1) & 1u, a.wait_ns));
-        o_par ^= nt > 1 ? 3u : 1u;
+        if (ok) ok = __all_sync(kFull, mbar_wait(&o_done[x], (o_par >> x & 1u) ^ 1u, a.wait_ns));
         if (ok) ok = __all_sync(kFull, mbar_wait(&item_clean[slot], (k >> 1) & 1, a.wait_ns));
         if (ok && !idle) {
           tc_fence_after();
