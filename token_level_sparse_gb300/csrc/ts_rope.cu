@@ -23,8 +23,11 @@
 namespace ts {
 namespace {
 
-constexpr int kRopeThreads = 128;
-constexpr int kRopeBatch = 4;      // heads under way per thread
+// Threads of a CTA, for four rows or (few rows) one. 33,122 rows of 32 heads of 128, bf16 in and out: 92.7 us with 64 threads,
+// 12 CTAs to an SM and the next heads loaded before these are turned; 96 with 128 threads and 6 CTAs, 121 with 256; 156 without the
+// loads ahead.
+__host__ __device__ constexpr int rope_threads(int rows) { return rows == 1 ? 256 : 64; }
+__host__ __device__ constexpr int rope_ctas(int rows) { return rows == 1 ? 2 : 12; }
 
 struct RopeArgs {
   RowsArgs rows;                   // places of the rows, pools (src and dst: K and V rows); total
@@ -39,6 +42,11 @@ struct RopeArgs {
   uint64_t turns[64];              // f_i / 2pi as a fraction of 2^64
 };
 
+__device__ __forceinline__ uint4 shfl4(const uint4& v, int from) {
+  return make_uint4(__shfl_sync(kFull, v.x, from), __shfl_sync(kFull, v.y, from), __shfl_sync(kFull, v.z, from),
+                    __shfl_sync(kFull, v.w, from));
+}
+
 // 8 elements of a row, as they are
 template <typename T>
 struct Raw8;
@@ -47,6 +55,12 @@ struct Raw8<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const unsigned char* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void get(float (&x)[8]) const { KV<__nv_bfloat16>::unpack(a, x); }
+  // those of lane `from`
+  __device__ __forceinline__ Raw8 of(int from) const {
+    Raw8 o;
+    o.a = shfl4(a, from);
+    return o;
+  }
 };
 template <>
 struct Raw8<float> {
@@ -58,6 +72,12 @@ struct Raw8<float> {
   __device__ __forceinline__ void get(float (&x)[8]) const {
     KV<float>::unpack(a, x);
     KV<float>::unpack(b, x + 4);
+  }
+  __device__ __forceinline__ Raw8 of(int from) const {
+    Raw8 o;
+    o.a = shfl4(a, from);
+    o.b = shfl4(b, from);
+    return o;
   }
 };
 
@@ -72,12 +92,14 @@ __device__ __forceinline__ void store_f32(unsigned char* p, const float (&x)[8])
 
 // kPairs 0: neighbours; 1: r/2 apart, a multiple of 8; 2: r/2 apart, any
 template <typename T, int D, int ROWS, int kPairs, bool kQ4>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int ES = (int)sizeof(T), CPR = D / 8, GROUPS = kRopeThreads / CPR;   // lanes of a head; heads at once
+__global__ void __launch_bounds__(rope_threads(ROWS), rope_ctas(ROWS)) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int ES = (int)sizeof(T), THREADS = rope_threads(ROWS);
+  constexpr int CPR = D / 8, GROUPS = THREADS / CPR;              // lanes of a head; heads at once
+  constexpr int BATCH = ES == 4 || kQ4 ? 2 : 4;                   // heads under way, and as many ahead (more spills)
   static_assert(GROUPS % ROWS == 0 && 32 % CPR == 0, "a head in a warp, a row to a thread");
   __shared__ int64_t s_place[kRowsPerCta];
   __shared__ float s_cos[ROWS][64], s_sin[ROWS][64];
-  __shared__ float s_x[kPairs == 2 ? kRopeThreads * 8 : 1];
+  __shared__ float s_x[kPairs == 2 ? THREADS * 8 : 1];
   const int tid = threadIdx.x, c = tid % CPR, grp = tid / CPR, row = grp % ROWS, half = a.r / 2;
   const int64_t r = (int64_t)blockIdx.x * ROWS + row;
   const bool live = r < a.rows.total;
@@ -91,15 +113,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int isv = h >= n_kv;
     return a.rows.src[isv] + r * a.rows.src_stride[isv] + ((int64_t)(h - isv * n_kv) * D + c * 8) * ES;
   };
-  Raw8<T> raw[kRopeBatch];
-  auto load = [&](int h0) {
+  Raw8<T> raw[BATCH], next[BATCH];
+  auto load = [&](int h0, Raw8<T> (&to)[BATCH]) {
 #pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k)
-      if (live && h0 + k * STEP < n) raw[k].load(source(h0 + k * STEP));
+    for (int k = 0; k < BATCH; ++k)
+      if (live && h0 + k * STEP < n) to[k].load(source(h0 + k * STEP));
   };
-  load(grp / ROWS);                // on their way while angles and places are found
+  load(grp / ROWS, raw);           // on their way while angles and places are found
 
-  for (int i = tid; i < ROWS * half; i += kRopeThreads) {
+  for (int i = tid; i < ROWS * half; i += THREADS) {
     const int rr = i / half, p = i - rr * half;
     const int64_t at = (int64_t)blockIdx.x * ROWS + rr;
     if (at < a.rows.total) {
@@ -133,10 +155,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
   const int64_t page = place >> a.rows.page_shift;
   const int ps = 1 << a.rows.page_shift, slot = (int)(place & (ps - 1));
-  for (int h0 = grp / ROWS; h0 - grp / ROWS < n; h0 += kRopeBatch * STEP) {     // (the same count in every thread)
-    if (h0 != grp / ROWS) load(h0);
+  for (int h0 = grp / ROWS; h0 - grp / ROWS < n; h0 += BATCH * STEP) {     // (the same count in every thread)
+    load(h0 + BATCH * STEP, next);
 #pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k) {
+    for (int k = 0; k < BATCH; ++k) {
       const int h = h0 + k * STEP;
       const bool have = live && h < n;
       const bool is_q = h < n_q;
@@ -147,13 +169,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = fmaf(x[e ^ 1], sn[e], x[e] * cs[e]);
       } else if (kPairs == 1) {
-        // lanes behind r have sn 0 and take their own
-        const int to = c * 8 < half ? half / 8 : (c * 8 < a.r ? -half / 8 : 0);
+        // (what lanes behind r make of this is not used)
+        float other[8];
+        raw[k].of((tid & 31) + (c * 8 < half ? half / 8 : (c * 8 < a.r ? -half / 8 : 0))).get(other);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other = __shfl_sync(kFull, x[e], (tid & 31) + to);
-          y[e] = fmaf(to ? other : 0.f, sn[e], x[e] * cs[e]);
-        }
+        for (int e = 0; e < 8; ++e) y[e] = fmaf(other[e], sn[e], x[e] * cs[e]);
       } else {
         float* mine = s_x + tid * 8;
         __syncwarp();
@@ -197,17 +217,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
           *reinterpret_cast<uint4*>(out) = isv ? raw[k].a : to_bf16(y);
       }
     }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) raw[k] = next[k];
   }
 }
 
 template <typename T, int D, int ROWS, bool kQ4>
 void pick(const RopeArgs& a, int grid, cudaStream_t s) {
   if (a.pairs)
-    rope_kernel<T, D, ROWS, 0, kQ4><<<grid, kRopeThreads, 0, s>>>(a);
+    rope_kernel<T, D, ROWS, 0, kQ4><<<grid, rope_threads(ROWS), 0, s>>>(a);
   else if (a.r % 16 == 0)
-    rope_kernel<T, D, ROWS, 1, kQ4><<<grid, kRopeThreads, 0, s>>>(a);
+    rope_kernel<T, D, ROWS, 1, kQ4><<<grid, rope_threads(ROWS), 0, s>>>(a);
   else
-    rope_kernel<T, D, ROWS, 2, kQ4><<<grid, kRopeThreads, 0, s>>>(a);
+    rope_kernel<T, D, ROWS, 2, kQ4><<<grid, rope_threads(ROWS), 0, s>>>(a);
 }
 
 template <typename T, bool kQ4>

@@ -73,7 +73,13 @@ __device__ __forceinline__ void residual(float p, float q, float ch, float cl, f
   lo = some ? l : 0.f;
 }
 
-__global__ void __launch_bounds__(kVfThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
+// Vocabulary of a warp: whole 512-byte pieces, so that aligned rows are read 16 bytes a lane.
+__host__ __device__ inline int warp_part(int V, int ctas) {
+  const int warps = ctas * kVfWarps;
+  return ((V + warps - 1) / warps + 127) / 128 * 128;
+}
+
+__global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
   const int b = blockIdx.x / ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -90,8 +96,8 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const __grid_constan
   if (rank == 0 && tid == 0 && !fine) set_error(a.status, TS_ERR_SEQ_LEN);
 
   // the slice, and this warp's part of it
-  const int slice = (a.V + ctas - 1) / ctas, v0 = min(a.V, rank * slice), v1 = min(a.V, v0 + slice);
-  const int part = (slice + kVfWarps - 1) / kVfWarps, w0 = min(v1, v0 + warp * part), w1 = min(v1, w0 + part);
+  const int part = warp_part(a.V, ctas), slice = kVfWarps * part, v0 = min(a.V, rank * slice), v1 = min(a.V, v0 + slice);
+  const int w0 = min(v1, v0 + warp * part), w1 = min(v1, w0 + part);
 
   if (rank == 0) {
     for (int i = tid; i < T; i += kVfThreads) {
@@ -196,23 +202,52 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const __grid_constan
       if (o.masked && (s_gone[(i - v0) >> 5] >> ((i - v0) & 31) & 1u)) hi = lo = 0.f;
     };
     float hi = 0.f, lo = 0.f;
-    constexpr int UN = 8;
-    for (int i0 = w0 + lane; i0 < w1; i0 += 32 * UN) {
-      float pv[UN], qv[UN];
+    auto add = [&](int i, float pv, float qv) {
+      float x, y, s, e;
+      entry(i, pv, qv, x, y);
+      two_sum(hi, x, s, e);
+      hi = s;
+      lo += e + y;
+    };
+    if (((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15) == 0) {
+      constexpr int UN = 4;            // 16-byte loads of either row under way
+      for (int i0 = w0 + 4 * lane; i0 < w1; i0 += 128 * UN) {
+        float4 pv[UN], qv[UN];
 #pragma unroll
-      for (int k = 0; k < UN; ++k) {
-        const int i = i0 + 32 * k;
-        pv[k] = i < w1 ? __ldg(p + i) : 0.f;
-        qv[k] = i < w1 && with_q ? __ldg(q + i) : 0.f;
+        for (int k = 0; k < UN; ++k) {
+          const int i = i0 + 128 * k;
+          pv[k] = qv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i + 3 < w1) {
+            pv[k] = __ldg(reinterpret_cast<const float4*>(p + i));
+            if (with_q) qv[k] = __ldg(reinterpret_cast<const float4*>(q + i));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+          const int i = i0 + 128 * k;
+          if (i + 3 < w1) {
+            add(i, pv[k].x, qv[k].x);
+            add(i + 1, pv[k].y, qv[k].y);
+            add(i + 2, pv[k].z, qv[k].z);
+            add(i + 3, pv[k].w, qv[k].w);
+          } else {
+            for (int l = i; l < w1; ++l) add(l, p[l], with_q ? q[l] : 0.f);   // (the vocabulary's last elements)
+          }
+        }
       }
+    } else {
+      constexpr int UN = 8;
+      for (int i0 = w0 + lane; i0 < w1; i0 += 32 * UN) {
+        float pv[UN], qv[UN];
 #pragma unroll
-      for (int k = 0; k < UN; ++k) {
-        const int i = i0 + 32 * k;
-        float x, y, s, e;
-        entry(min(i, w1 - 1), pv[k], qv[k], x, y);
-        two_sum(hi, x, s, e);
-        hi = s;
-        lo += e + y;
+        for (int k = 0; k < UN; ++k) {
+          const int i = i0 + 32 * k;
+          pv[k] = i < w1 ? __ldg(p + i) : 0.f;
+          qv[k] = i < w1 && with_q ? __ldg(q + i) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < UN; ++k)
+          if (i0 + 32 * k < w1) add(i0 + 32 * k, pv[k], qv[k]);
       }
     }
     double mine = (double)hi + (double)lo;
@@ -264,42 +299,61 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const __grid_constan
       before = __shfl_sync(kFull, run_to[k] - held[k], from & 31);
     }
     if (from == rank * kVfWarps + warp) {
-      // a lane takes neighbouring elements: its sum, the sums of the lanes before it, then its elements one by one
+      // a lane takes neighbouring elements: its sum, the sums of the lanes before it
       const int len = (w1 - w0 + 31) / 32, e0 = min(w1, w0 + lane * len), e1 = min(w1, e0 + len);
-      float shi = 0.f, slo = 0.f;
-      int last = -1;
-      for (int i = e0; i < e1; ++i) {
-        float x, y, s, e;
-        entry(i, p[i], with_q ? q[i] : 0.f, x, y);
-        two_sum(shi, x, s, e);
-        shi = s;
-        slo += e + y;
-        if (x + y > 0.f) last = i;
+      hi = lo = 0.f;
+      bool any = false;
+      constexpr int UN = 8;
+      for (int i0 = e0; i0 < e1; i0 += UN) {
+        float pv[UN], qv[UN];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+          pv[k] = i0 + k < e1 ? p[i0 + k] : 0.f;
+          qv[k] = i0 + k < e1 && with_q ? q[i0 + k] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+          if (i0 + k >= e1) continue;
+          float x, y, s, e;
+          entry(i0 + k, pv[k], qv[k], x, y);
+          two_sum(hi, x, s, e);
+          hi = s;
+          lo += e + y;
+          any |= x + y > 0.f;
+        }
       }
-      const double sum = (double)shi + (double)slo;
+      const double sum = (double)hi + (double)lo;
       double run = sum;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const double o2 = __shfl_up_sync(kFull, run, d);
         if (lane >= d) run += o2;
       }
-      const double base = before + (run - sum);
-      const unsigned over = __ballot_sync(kFull, sum > 0. && before + run > t);
-      const unsigned some = __ballot_sync(kFull, last >= 0);
-      const int owner = over ? __ffs(over) - 1 : 31 - __clz(some);
-      if (some && lane == owner) {
-        int pick = last;
-        double acc = base;
-        for (int i = e0; i < e1; ++i) {
-          float x, y;
-          entry(i, p[i], with_q ? q[i] : 0.f, x, y);
-          acc += (double)x + (double)y;
-          if (acc > t && x + y > 0.f) {
-            pick = i;
-            break;
+      const unsigned over = __ballot_sync(kFull, any && before + run > t);
+      const unsigned some = __ballot_sync(kFull, any);
+      if (some) {
+        // then the whole warp goes through the elements of one of them, 32 at a time
+        const int owner = over ? __ffs(over) - 1 : 31 - __clz(some);
+        const int f0 = __shfl_sync(kFull, e0, owner), f1 = __shfl_sync(kFull, e1, owner);
+        double acc = __shfl_sync(kFull, before + (run - sum), owner);
+        int pick = -1;
+        for (int i0 = f0; i0 < f1; i0 += 32) {
+          const int i = i0 + lane;
+          float x = 0.f, y = 0.f;
+          if (i < f1) entry(i, p[i], with_q ? q[i] : 0.f, x, y);
+          const double v = (double)x + (double)y;
+          double upto = v;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const double o2 = __shfl_up_sync(kFull, upto, d);
+            if (lane >= d) upto += o2;
           }
+          const unsigned held = __ballot_sync(kFull, v > 0.), passed1 = __ballot_sync(kFull, v > 0. && acc + upto > t);
+          if (held) pick = i0 + (passed1 ? __ffs(passed1) - 1 : 31 - __clz(held));
+          if (passed1) break;
+          acc += __shfl_sync(kFull, upto, 31);
         }
-        *cluster.map_shared_rank(&s_found, 0) = pick;
+        if (lane == 0) *cluster.map_shared_rank(&s_found, 0) = pick;
       }
     }
     cluster.sync();
@@ -329,7 +383,7 @@ ts_status launch_verify(ts_ctx* ctx, const VerifyCall& c, cudaStream_t s) {
                c.u, c.u_next, c.distinct, c.path, c.path_stride, c.count, c.next, ctx->status};
   int ctas = 1;
   while (ctas < kVfCluster && (c.vocab > kVfSlice * ctas || c.vocab >= 2048 * ctas)) ctas *= 2;
-  const size_t smem = c.draft ? 0 : (size_t)((c.vocab + ctas - 1) / ctas + 31) / 32 * 4;
+  const size_t smem = c.draft ? 0 : (size_t)kVfWarps * warp_part(c.vocab, ctas) / 8;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ctas;
