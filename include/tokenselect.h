@@ -397,7 +397,7 @@ ts_status ts_tree_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const voi
  * current node; with none left next_token[b] is drawn from the residual r = max(p - c q, 0): the smallest i with
  * sum_{j <= i} r(j) > u_next[b] sum r (the last i with r(i) > 0 where rounding leaves none), from p where r is zero
  * throughout, -1 where p is too. Tokens so drawn are distributed as the target's. Entries that are NaN or negative
- * count as 0. Sums and tests carry 2^-45 and better.
+ * count as 0. Sums are off by less than 2^-32 of them.
  * path int32 [B][path_stride] receives the taken nodes in order, node 0 first, then -1; count int32 [B] how many.
  * More than path_stride record TS_ERR_CAPACITY (the first ones are written, count is the whole number). At most 1024
  * nodes per sequence; more, or boundaries that are not ascending, record TS_ERR_SEQ_LEN, count 0 and -1 (so does a

@@ -492,6 +492,7 @@ class Context:
                           max_pages_per_seq, num_pages)
         self.handle = ts_create(self.cfg)
         self.max_tokens = max_pages_per_seq * page_size
+        self.cfg_d = head_dim
         # what the packed calls compare their tensors with
         self._q_row, self._kv_row = (n_q_heads, head_dim), (n_kv_heads, head_dim)
         self._q4, self._f32 = kv_dtype == TS_KV_Q4, kv_dtype == TS_KV_F32
@@ -675,22 +676,26 @@ class Context:
 
     def _heads(self, where, x, heads, total, here):
         """Refuses a packed [total][heads][d] tensor of another shape, type or device; its row stride and type."""
-        if x.dim() != 3 or x.shape[2] != self.cfg.head_dim or (heads and x.shape[1] != heads) or x.shape[0] != total:
-            _refuse(where, "TS_ERR_SHAPE", f"{tuple(x.shape)} instead of {(total, heads or 'heads', self.cfg.head_dim)}")
-        kind = x.dtype
-        if kind is not _bfloat16 and kind is not _float32:
+        kind, shape = x.dtype, x.shape
+        f32 = kind is _float32
+        if len(shape) == 3 and (f32 or kind is _bfloat16) and x.get_device() == here:
+            rows, h, d = shape
+            if rows == total and h == heads and d == self.cfg_d:
+                step, head, one = x.stride()                       # (the test that most calls pass)
+                if one == 1 and head == d:
+                    return (step if rows > 1 else h * d), TS_KV_F32 if f32 else TS_KV_BF16
+                return _row_stride(x, total, (h, d)), TS_KV_F32 if f32 else TS_KV_BF16
+        if len(shape) != 3 or tuple(shape) != (total, heads, self.cfg_d):
+            _refuse(where, "TS_ERR_SHAPE", f"{tuple(shape)} instead of {(total, heads, self.cfg_d)}")
+        if not f32 and kind is not _bfloat16:
             _refuse(where, "TS_ERR_INVALID_ARG", f"{kind} instead of bfloat16 or float32")
-        if x.get_device() != here:
-            _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not on the current device")
-        return _row_stride(x, total, x.shape[1:]), TS_KV_F32 if kind is _float32 else TS_KV_BF16
+        _refuse(where, "TS_ERR_INVALID_ARG", "a tensor is not on the current device")
 
     @staticmethod
     def _counted(where, here, *specs):
         """Refuses every (tensor, shape, type) that is not dense, of exactly this shape and type, on the current device."""
         for t, shape, dtype in specs:
-            if t is None:
-                continue
-            if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == here:
+            if t is None or (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == here):
                 continue
             if t.shape != shape:
                 _refuse(where, "TS_ERR_SHAPE", f"{tuple(t.shape)} instead of {tuple(shape)}")
@@ -702,11 +707,13 @@ class Context:
         """x / out [total][heads][d] (bf16 or fp32 each): rows turned by positions int32 [total]. out may be x."""
         if _device is None:
             _torch()
-        here, total = _device(), x.shape[0]
-        xs, kind = self._heads("rotate", x, 0, total, here)
-        os_, out_kind = self._heads("rotate", out, x.shape[1], total, here)
+        if x.dim() != 3:
+            _refuse("rotate", "TS_ERR_SHAPE", f"{tuple(x.shape)} instead of (rows, heads, {self.cfg_d})")
+        here, (total, heads, _) = _device(), x.shape
+        xs, kind = self._heads("rotate", x, heads, total, here)
+        os_, out_kind = self._heads("rotate", out, heads, total, here)
         self._counted("rotate", here, (positions, (total,), _int32))
-        ts_rotate(self.handle, rope.handle, x, xs, kind, x.shape[1], positions, total, out, os_, out_kind, stream)
+        ts_rotate(self.handle, rope.handle, x, xs, kind, heads, positions, total, out, os_, out_kind, stream)
 
     def append_rotated(self, rope, k, v, positions, cu_rows, page_table, k_pool, v_pool, starts=None, q=None, q_out=None,
                        stream=None):
@@ -773,7 +780,7 @@ class Context:
 
     def keep_rows(self, path, count, cu_rows, seq_lens, page_table, k_pool, v_pool, new_lens=None, total=None, stream=None):
         """The K and V rows of path's nodes to the front of the drafts'. Pools of one layer, or [layers][...] with a pool
-        each, dense in itself. total: rows that cu_rows may end at (any, where it is not given)."""
+        each. total: rows that cu_rows may end at (any, where it is not given)."""
         if _device is None:
             _torch()
         here, B = _device(), cu_rows.shape[0] - 1
@@ -781,15 +788,15 @@ class Context:
             _refuse("keep_rows", "TS_ERR_SHAPE", f"{tuple(path.shape)} instead of {(B, 'most')}")
         self._counted("keep_rows", here, (path, path.shape, _int32), (count, (B,), _int32), (cu_rows, (B + 1,), _int32),
                       (seq_lens, (B,), _int32), (new_lens, (B,), _int32))
-        layers, step, one = 1, 0, (k_pool, v_pool)
-        if k_pool.dim() == 5 or (self._q4 and k_pool.dim() == 4):
-            if k_pool.shape != v_pool.shape or k_pool.stride(0) != v_pool.stride(0):
-                _refuse("keep_rows", "TS_ERR_SHAPE", "the pools of K and V differ")
-            layers, step = k_pool.shape[0], k_pool.stride(0) * k_pool.element_size()
+        layers, step = 1, 0
+        if k_pool.dim() == (4 if self._q4 else 5):                 # [layers][...], dense throughout
+            layers = k_pool.shape[0]
             if layers == 0:
                 return
-            one = (k_pool[0], v_pool[0])
-        self._paged("keep_rows", B, page_table, *one)
+            if k_pool.shape != v_pool.shape or k_pool.dtype is not v_pool.dtype or k_pool.nbytes < layers * self._pool_bytes:
+                _refuse("keep_rows", "TS_ERR_SHAPE", f"pools of {layers} layers that differ, or of less than {self._pool_bytes} bytes each")
+            step = k_pool.nbytes // layers
+        self._paged("keep_rows", B, page_table, k_pool, v_pool)
         ts_keep_rows(self.handle, path, path.shape[1], count, cu_rows, seq_lens, B, (1 << 30) if total is None else total,
                      page_table, k_pool, v_pool, layers, step, new_lens, stream)
 

@@ -16,9 +16,9 @@
 // its steps run in shared memory, and tells the others what to sum (a message in their shared memory, a cluster
 // barrier on either side). Nobody else decides anything, so all of them always agree on the next barrier.
 //
-// Sums decide whole numbers, so they are held to 2^-45 and better: p - c q exactly in two floats (c in two floats), sums of
-// pairs with TwoSum, warps and CTAs in fp64 and in a fixed order. FP64 throughout would be the slower pipe by
-// far. Entries that are NaN or negative count as zero.
+// Sums decide whole numbers, so they are held in pairs of floats (p - c q exactly, c in two floats), warps and CTAs in fp64,
+// all in a fixed order: off by 2^-44 of the sum as a rule, by n^2 2^-49 < 2^-33 at most, n <= 256 elements to a lane. FP64
+// throughout would be the slower pipe by far. Entries that are NaN or negative count as zero.
 #include <cooperative_groups.h>
 
 #include "ts_common.cuh"
@@ -65,13 +65,24 @@ struct Order {                         // what the walk asks of every CTA
 __device__ __forceinline__ void residual(float p, float q, float ch, float cl, float& hi, float& lo) {
   q = fmaxf(q, 0.f);
   const float h = ch * q, e = fmaf(ch, q, -h);      // c_hi q exactly
-  float s, t;
-  two_sum(p, -h, s, t);
-  const float l = t - e - cl * q;
+  const float s = p - h, t = (p - s) - h;           // p - h exactly, where it is not negative (so p is the larger)
+  const float l = fmaf(-cl, q, t - e);
   const bool some = s + l > 0.f;
   hi = some ? s : 0.f;
   lo = some ? l : 0.f;
 }
+
+// A sum as a pair of floats, s + c, to which pairs are added (the part of an addition that s does not hold goes to c).
+struct PairSum {
+  float s = 0.f, c = 0.f;
+  __device__ __forceinline__ void add(float hi, float lo) {
+    float t, e;
+    two_sum(s, hi, t, e);              // (one addition on the way from one s to the next)
+    s = t;
+    c += e + lo;
+  }
+  __device__ __forceinline__ double value() const { return (double)s + (double)c; }
+};
 
 // Vocabulary of a warp: whole 512-byte pieces, so that aligned rows are read 16 bytes a lane.
 __host__ __device__ inline int warp_part(int V, int ctas) {
@@ -87,7 +98,9 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
   __shared__ int s_parent[kMaxTree], s_token[kMaxTree];
   __shared__ float s_u[kMaxTree], s_p[kMaxTree], s_q[kMaxTree];
   __shared__ Order s_order;
-  __shared__ double s_part[kVfCluster * kVfWarps];              // (of the first CTA) sums by CTA and warp
+  __shared__ float2 s_part[kVfCluster * kVfWarps];              // (of the first CTA) sums by CTA and warp, as pairs
+  __shared__ double s_before, s_t;                              // the draw: what lies before the part that holds the token,
+  __shared__ int s_from;                                        // the number that is passed, and the part
   __shared__ int s_found;
 
   const int first = a.cu[b], end = a.cu[b + 1];
@@ -122,13 +135,12 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
   if (rank == 0 && warp == 0 && lane == 0 && T > 0) {
     if (a.path_stride > 0) a.path[(int64_t)b * a.path_stride] = 0;
   }
-  bool drawn = false;
   int token = -1;
 
   for (;;) {
     if (rank == 0 && warp == 0) {
       Order o{kVfEnd, cur, 0, 0.};
-      if (T > 0 && !drawn) {
+      if (T > 0) {
         o.what = kVfDraw;
         // children of cur from node `at` on
         while (at < T) {
@@ -201,15 +213,14 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
       residual(pv, qv, ch, cl, hi, lo);
       if (o.masked && (s_gone[(i - v0) >> 5] >> ((i - v0) & 31) & 1u)) hi = lo = 0.f;
     };
-    float hi = 0.f, lo = 0.f;
+    PairSum held_here;
     auto add = [&](int i, float pv, float qv) {
-      float x, y, s, e;
+      float x, y;
       entry(i, pv, qv, x, y);
-      two_sum(hi, x, s, e);
-      hi = s;
-      lo += e + y;
+      held_here.add(x, y);
     };
-    if (((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15) == 0) {
+    const bool aligned = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+    if (aligned) {
       constexpr int UN = 4;            // 16-byte loads of either row under way
       for (int i0 = w0 + 4 * lane; i0 < w1; i0 += 128 * UN) {
         float4 pv[UN], qv[UN];
@@ -250,16 +261,17 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
           if (i0 + 32 * k < w1) add(i0 + 32 * k, pv[k], qv[k]);
       }
     }
-    double mine = (double)hi + (double)lo;
+    // (pairs of floats down to one per warp: sixteen warps' sums in fp64 would queue for its pipe for microseconds)
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) mine += __shfl_xor_sync(kFull, mine, d);
-    if (lane == 0) *cluster.map_shared_rank(&s_part[rank * kVfWarps + warp], 0) = mine;
+    for (int d = 16; d >= 1; d >>= 1)
+      held_here.add(__shfl_xor_sync(kFull, held_here.s, d), __shfl_xor_sync(kFull, held_here.c, d));
+    if (lane == 0) *cluster.map_shared_rank(&s_part[rank * kVfWarps + warp], 0) = make_float2(held_here.s, held_here.c);
     if (tid == 0) s_found = -1;
     cluster.sync();
     if (o.what == kVfSum) {
       if (rank == 0 && warp == 0) {
         double s = 0.;
-        for (int k = lane; k < ctas * kVfWarps; k += 32) s += s_part[k];
+        for (int k = lane; k < ctas * kVfWarps; k += 32) s += (double)s_part[k].x + (double)s_part[k].y;
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
         Z = s;
@@ -267,62 +279,82 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
       }
       continue;
     }
-    // ---- the draw: every warp finds from all sums whether its part holds the token
-    const double* parts = cluster.map_shared_rank(&s_part[0], 0);
-    const int n = ctas * kVfWarps;
-    // running sums over the parts, the same in every warp
-    constexpr int PL = kVfCluster * kVfWarps / 32;
-    double all = 0., held[PL], run_to[PL], before = 0.;
+    // ---- the draw: a warp of every CTA finds from all sums the part that holds the token
+    if (warp == 0) {
+      const float2* parts = cluster.map_shared_rank(&s_part[0], 0);
+      const int n = ctas * kVfWarps;
+      // running sums over the parts: a lane takes PL neighbours
+      constexpr int PL = kVfCluster * kVfWarps / 32;
+      float2 pair[PL];
 #pragma unroll
-    for (int k = 0; k < PL; ++k) {
-      held[k] = 32 * k + lane < n ? parts[32 * k + lane] : 0.;
-      double run = held[k];
+      for (int k = 0; k < PL; ++k) pair[k] = PL * lane + k < n ? parts[PL * lane + k] : make_float2(0.f, 0.f);
+      double held[PL], lane_sum = 0.;
+#pragma unroll
+      for (int k = 0; k < PL; ++k) {
+        held[k] = (double)pair[k].x + (double)pair[k].y;
+        lane_sum += held[k];
+      }
+      double run = lane_sum;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const double o2 = __shfl_up_sync(kFull, run, d);
         if (lane >= d) run += o2;
       }
-      run_to[k] = run + all;
-      all = __shfl_sync(kFull, run_to[k], 31);
-    }
-    const double t = (double)a.u_next[b] * all;
-    // the first part that holds something and whose running sum passes t; where rounding leaves none, the last that does
-    int from = -1;
-    bool passed = false;
+      const double all = __shfl_sync(kFull, run, 31), t = (double)a.u_next[b] * all;
+      // the first part that holds something and whose running sum passes t; where rounding leaves none, the last that does
+      double at_part = run - lane_sum;
+      int mine_over = -1, mine_some = -1;
 #pragma unroll
-    for (int k = 0; k < PL; ++k) {
-      const unsigned some = __ballot_sync(kFull, held[k] > 0.);
-      const unsigned over = __ballot_sync(kFull, held[k] > 0. && run_to[k] > t);
-      if (passed || !some) continue;
-      passed = over != 0u;
-      from = 32 * k + (over ? __ffs(over) - 1 : 31 - __clz(some));
-      before = __shfl_sync(kFull, run_to[k] - held[k], from & 31);
+      for (int k = 0; k < PL; ++k) {
+        if (held[k] > 0.) {
+          mine_some = k;
+          if (mine_over < 0 && at_part + held[k] > t) mine_over = k;
+        }
+        if (mine_over < 0 && k + 1 < PL) at_part += held[k];
+      }
+      const unsigned over = __ballot_sync(kFull, mine_over >= 0), some = __ballot_sync(kFull, mine_some >= 0);
+      const int l = over ? __ffs(over) - 1 : 31 - __clz(some);
+      if (some && lane == l) {
+        s_from = PL * l + (over ? mine_over : mine_some);
+        s_before = over ? at_part : all;                          // (past all: the part's last element is taken)
+        s_t = t;
+      }
+      if (!some && lane == 0) s_from = -1;
     }
-    if (from == rank * kVfWarps + warp) {
+    __syncthreads();
+    if (s_from == rank * kVfWarps + warp) {
+      const double before = s_before, t = s_t;
       // a lane takes neighbouring elements: its sum, the sums of the lanes before it
-      const int len = (w1 - w0 + 31) / 32, e0 = min(w1, w0 + lane * len), e1 = min(w1, e0 + len);
-      hi = lo = 0.f;
+      const int len = part / 32, e0 = min(w1, w0 + lane * len), e1 = min(w1, e0 + len);   // (a multiple of 4)
+      PairSum piece;
       bool any = false;
       constexpr int UN = 8;
       for (int i0 = e0; i0 < e1; i0 += UN) {
-        float pv[UN], qv[UN];
+        __align__(16) float pv[UN], qv[UN];
 #pragma unroll
-        for (int k = 0; k < UN; ++k) {
-          pv[k] = i0 + k < e1 ? p[i0 + k] : 0.f;
-          qv[k] = i0 + k < e1 && with_q ? q[i0 + k] : 0.f;
+        for (int k = 0; k < UN; k += 4) {
+          if (aligned && i0 + k + 3 < e1) {
+            *reinterpret_cast<float4*>(pv + k) = *reinterpret_cast<const float4*>(p + i0 + k);
+            if (with_q) *reinterpret_cast<float4*>(qv + k) = *reinterpret_cast<const float4*>(q + i0 + k);
+          } else {
+#pragma unroll
+            for (int l = k; l < k + 4; ++l) {
+              pv[l] = i0 + l < e1 ? p[i0 + l] : 0.f;
+              qv[l] = i0 + l < e1 && with_q ? q[i0 + l] : 0.f;
+            }
+          }
         }
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
+          if (!with_q) qv[k] = 0.f;
           if (i0 + k >= e1) continue;
-          float x, y, s, e;
+          float x, y;
           entry(i0 + k, pv[k], qv[k], x, y);
-          two_sum(hi, x, s, e);
-          hi = s;
-          lo += e + y;
+          piece.add(x, y);
           any |= x + y > 0.f;
         }
       }
-      const double sum = (double)hi + (double)lo;
+      const double sum = piece.value();
       double run = sum;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -353,15 +385,13 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
           if (passed1) break;
           acc += __shfl_sync(kFull, upto, 31);
         }
-        if (lane == 0) *cluster.map_shared_rank(&s_found, 0) = pick;
+        if (lane < ctas) *cluster.map_shared_rank(&s_found, lane) = pick;
       }
     }
     cluster.sync();
-    if (rank == 0 && warp == 0) {
-      ++draws;
-      token = s_found;
-      drawn = token >= 0 || draws == 2;
-    }
+    ++draws;
+    token = s_found;
+    if (token >= 0 || draws == 2) break;
   }
   if (rank == 0) {
     if (warp == 0 && lane == 0) {
@@ -373,7 +403,6 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
     __syncthreads();
     for (int64_t i = s_found + tid; i < a.path_stride; i += kVfThreads) a.path[(int64_t)b * a.path_stride + i] = -1;
   }
-  cluster.sync();                      // no CTA leaves while its shared memory may still be written to
 }
 
 }  // namespace
