@@ -10,7 +10,7 @@
 //
 // A tile is 128 query rows of one KV head: 128 / G tokens with all G query heads of the group; a block is two
 // neighbouring tiles, which share every key and value tile of 128 tokens. The key tiles of all blocks of all KV heads and
-// sequences, one behind another, are dealt to one CTA per SM in equal, contiguous shares, whatever the lengths are. A
+// sequences, one behind another, are dealt to one CTA per SM in contiguous shares of equal work, whatever the lengths are. A
 // share that begins or ends inside a block leaves its sums in fp32 (unnormalised, with maximum and sum), and a second kernel
 // joins them, in order: the same bits every time. Roles of a CTA:
 //   warp 8      loads: the query tiles of an item, then K and V pages (TMA, 128-byte swizzle) into a ring of tiles
@@ -83,12 +83,17 @@ struct TrShape {
   static constexpr uint32_t S_COL = 0, O_COL = 256;
 };
 
-// A sequence's share of the work.
+// Work is counted per key tile: one of a block with two tiles takes longer, 262,144 tokens of 8 KV heads with G 4 202 to 215 us
+// (33 to 64 drafts) where a block with one tile takes 168 (up to 32).
+constexpr int kTrPair = 5, kTrSingle = 4;
+
+// A sequence's work: its KV heads one behind another, of each the blocks, of each the key tiles.
 struct TreeSeq {
   int row0, T, n;                // first packed row, drafts, cached tokens (drafts among them)
   int blocks, tiles;             // blocks of drafts, key tiles of a block
+  int last;                      // work of a key tile of the last block (of the others: kTrPair)
   int err;
-  __device__ __forceinline__ int64_t work(int HKV) const { return (int64_t)HKV * blocks * tiles; }
+  __device__ __forceinline__ int64_t head() const { return (int64_t)tiles * (blocks > 0 ? kTrPair * (blocks - 1) + last : 0); }
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
@@ -101,7 +106,8 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
   const bool ok = rows_ok && s.T <= kMaxTree && (!a.mask || s.T <= 32 * a.mask_words) && s.n >= s.T && s.n <= a.max_tokens;
   s.err = ok ? 0 : TS_ERR_SEQ_LEN;
   s.blocks = ok ? (s.T + 2 * a.tokens - 1) / (2 * a.tokens) : 0;
-  s.tiles = (s.n + kTrKeys - 1) / kTrKeys;
+  s.tiles = ok ? (s.n + kTrKeys - 1) / kTrKeys : 0;
+  s.last = s.T - (s.blocks - 1) * 2 * a.tokens > a.tokens ? kTrPair : kTrSingle;
   return s;
 }
 
@@ -115,9 +121,11 @@ __device__ __forceinline__ int64_t warp_scan_ll(int64_t x, int lane) {
   return x;
 }
 
-// First tile of CTA c's share of `work` tiles among `ctas`, and the CTA that has tile t.
+// CTAs that share the work (each has a key tile at least), where the share of CTA c begins, and whose share a place is in. A
+// key tile belongs to the share that its beginning lies in.
+__device__ __forceinline__ int share_ctas(int64_t work, int grid) { return (int)max((int64_t)1, min((int64_t)grid, work / kTrPair)); }
 __device__ __forceinline__ int64_t share_begin(int64_t work, int ctas, int c) { return work * c / ctas; }
-__device__ __forceinline__ int share_of(int64_t work, int ctas, int64_t t) { return (int)(((t + 1) * ctas - 1) / work); }
+__device__ __forceinline__ int share_of(int64_t work, int ctas, int64_t at) { return (int)(((at + 1) * ctas - 1) / work); }
 
 // Places in the ring of an item's key tile j and value tile j, counted from its first: K(0), K(1), V(0), K(2), V(1), ...
 __device__ __forceinline__ uint32_t key_load(int j) { return j == 0 ? 0u : 2u * (uint32_t)j - 1u; }
@@ -480,18 +488,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         const int b = b0 + lane;
         TreeSeq s{};
         if (b < a.B) s = tree_seq(a, b);
-        const int64_t w = b < a.B ? s.work(a.HKV) : 0;
-        const int64_t run = work + warp_scan_ll(w, lane);
+        const int64_t run = work + warp_scan_ll(s.head() * a.HKV, lane);
         if (blockIdx.x == 0 && s.err) set_error(a.status, s.err);
         work = __shfl_sync(kFull, run, 31);
       }
-      const int ctas = (int)min((int64_t)gridDim.x, work);
+      const int ctas = share_ctas(work, gridDim.x);
       int64_t t = 0, e = 0;
-      if ((int)blockIdx.x < ctas) {
+      if (work > 0 && (int)blockIdx.x < ctas) {
         t = share_begin(work, ctas, blockIdx.x);
         e = share_begin(work, ctas, blockIdx.x + 1);
       }
-      const int64_t begin = t;
       int b0 = 0;                                                 // the sequences looked at: 32 from b0 on
       int64_t before = 0;                                         // tiles of the sequences before them
       bool found = true;
@@ -499,36 +505,45 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         found = t < e;
         TreeItem item{};
         if (found) {
-          for (;;) {                                              // the sequence of tile t
+          for (;;) {                                              // the sequence and the block that place t is in
             const int b = b0 + lane;
             TreeSeq s{};
             if (b < a.B) s = tree_seq(a, b);
-            const int64_t w = b < a.B ? s.work(a.HKV) : 0;
-            const int64_t run = warp_scan_ll(w, lane);
+            const int64_t w = s.head() * a.HKV, run = warp_scan_ll(w, lane);
             const unsigned m = __ballot_sync(kFull, before + run > t);
-            if (m || b0 + 32 >= a.B) {
-              const int src = m ? __ffs(m) - 1 : 31;
-              const int64_t start = before + __shfl_sync(kFull, run - w, src);
-              item.row0 = __shfl_sync(kFull, s.row0, src);
-              item.T = __shfl_sync(kFull, s.T, src);
-              item.n = __shfl_sync(kFull, s.n, src);
-              const int tiles = __shfl_sync(kFull, s.tiles, src), blocks = __shfl_sync(kFull, s.blocks, src);
-              if (!m) {                                           // (not reached: t lies below the work)
-                found = false;
-                break;
-              }
-              const int64_t u = (t - start) / tiles;
-              item.b = b0 + src;
-              item.kv = (int)(u / blocks);
-              item.i0 = (int)(u % blocks) * 2 * a.tokens;
-              item.j0 = (int)((t - start) % tiles);
-              item.j1 = (int)min((int64_t)tiles, item.j0 + (e - t));
-              item.slot = item.j0 == 0 && item.j1 == tiles ? -1 : 2 * (int)blockIdx.x + (t == begin ? 0 : 1);
-              t += item.j1 - item.j0;
+            if (!m) {
+              before += __shfl_sync(kFull, run, 31);
+              b0 += 32;
+              if (b0 < a.B) continue;
+              found = false;                                      // (not reached: t lies below the work)
               break;
             }
-            before += __shfl_sync(kFull, run, 31);
-            b0 += 32;
+            const int src = __ffs(m) - 1;
+            const int64_t start = before + __shfl_sync(kFull, run - w, src), head = __shfl_sync(kFull, s.head(), src);
+            const int tiles = __shfl_sync(kFull, s.tiles, src), blocks = __shfl_sync(kFull, s.blocks, src);
+            const int last = __shfl_sync(kFull, s.last, src);
+            const int64_t in = (t - start) % head;
+            const int kv = (int)((t - start) / head), block = (int)min(in / (kTrPair * tiles), (int64_t)blocks - 1);
+            const int per = block + 1 < blocks ? kTrPair : last;  // work of a key tile
+            const int64_t at = t - in + (int64_t)block * kTrPair * tiles;        // where the block begins
+            const int j0 = (int)((t - at + per - 1) / per), j1 = (int)min((int64_t)tiles, (e - at + per - 1) / per);
+            t = at + (int64_t)per * tiles;                        // the next block
+            if (j0 >= j1) {                                       // (no key tile of this one begins in the share)
+              if (t < e) continue;
+              found = false;
+              break;
+            }
+            item.row0 = __shfl_sync(kFull, s.row0, src);
+            item.T = __shfl_sync(kFull, s.T, src);
+            item.n = __shfl_sync(kFull, s.n, src);
+            item.b = b0 + src;
+            item.kv = kv;
+            item.i0 = block * 2 * a.tokens;
+            item.j0 = j0;
+            item.j1 = j1;
+            // (one block at most comes from an earlier share, one at most goes on in a later one)
+            item.slot = j0 == 0 && j1 == tiles ? -1 : 2 * (int)blockIdx.x + (j0 == 0 ? 1 : 0);
+            break;
           }
         }
         item.found = found;
@@ -842,7 +857,7 @@ constexpr int kJoinParts = 256;  // CTAs of a call, at most
 template <int D>
 __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(const __grid_constant__ TreeArgs a, int grid) {
   constexpr int COLS = D / 4;
-  __shared__ int s_first[kJoinRows], s_parts[kJoinRows], s_at[kJoinRows], s_slot0[kJoinRows];
+  __shared__ int s_first[kJoinRows], s_parts[kJoinRows], s_at[kJoinRows];
   __shared__ float s_f[kJoinRows][kJoinParts];
   __shared__ float s_inv[kJoinRows];
   __shared__ float4 s_acc[kJoinGroups - 1][kJoinRows * COLS];
@@ -858,24 +873,24 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(c
   int kv, packed, head;
   place(row, kv, packed, head);
   if (warp == 0) {
-    // lane r < 8: the first key tile of row r's block (-1: no row of a sequence), its key tiles, the row's place
-    int64_t work = 0, t0 = -1;
-    int tiles = 0, at = 0;
+    // lane r < 8: where the first and last key tile of row r's block begin (-1: no row of a sequence), and the row's place
+    int64_t work = 0, t0 = -1, t1 = -1;
+    int at = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       TreeSeq s{};
       if (b0 + lane < a.B) s = tree_seq(a, b0 + lane);
-      const int64_t w = s.work(a.HKV), run = work + warp_scan_ll(w, lane);
+      const int64_t w = s.head() * a.HKV, run = work + warp_scan_ll(w, lane);
       for (int r = 0; r < kJoinRows; ++r) {
         const int p = __shfl_sync(kFull, packed, r);
         const unsigned m = __ballot_sync(kFull, s.blocks > 0 && p >= s.row0 && p < s.row0 + s.T);
         if (!m) continue;
         const int src = __ffs(m) - 1, row0 = __shfl_sync(kFull, s.row0, src), blocks = __shfl_sync(kFull, s.blocks, src);
-        const int n = __shfl_sync(kFull, s.tiles, src);
-        const int64_t before = __shfl_sync(kFull, run - w, src);
+        const int n = __shfl_sync(kFull, s.tiles, src), last = __shfl_sync(kFull, s.last, src);
+        const int64_t before = __shfl_sync(kFull, run - w, src), one = __shfl_sync(kFull, s.head(), src);
         if (lane == r && kv < a.HKV) {
           const int tok = p - row0, block = tok / (2 * a.tokens), in = tok - block * 2 * a.tokens;
-          tiles = n;
-          t0 = before + ((int64_t)kv * blocks + block) * n;
+          t0 = before + kv * one + (int64_t)block * kTrPair * n;
+          t1 = t0 + (int64_t)(n - 1) * (block + 1 < blocks ? kTrPair : last);
           at = (in / a.tokens) * 128 + in % a.tokens * a.G + head;
         }
       }
@@ -884,18 +899,17 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(c
     if (lane < kJoinRows) {
       int parts = 0;
       if (t0 >= 0) {
-        const int ctas = (int)min((int64_t)grid, work);
-        const int c0 = share_of(work, ctas, t0), c1 = share_of(work, ctas, t0 + tiles - 1);
+        const int ctas = share_ctas(work, grid);
+        const int c0 = share_of(work, ctas, t0), c1 = share_of(work, ctas, t1);
         parts = c1 > c0 ? c1 - c0 + 1 : 0;                        // (else the block's outputs are there)
         s_first[lane] = c0;
-        s_slot0[lane] = 2 * c0 + (share_begin(work, ctas, c0) < t0 ? 1 : 0);
         s_at[lane] = at;
       }
       s_parts[lane] = parts;
     }
   }
   __syncthreads();
-  auto slot_of = [&](int r, int k) { return k == 0 ? s_slot0[r] : 2 * (s_first[r] + k); };
+  auto slot_of = [&](int r, int k) { return 2 * (s_first[r] + k) + (k == 0 ? 1 : 0); };
   const int parts = s_parts[row];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float4* src = reinterpret_cast<const float4*>(a.part_o) + (int64_t)col * 256 + (parts ? s_at[row] : 0);
