@@ -85,7 +85,7 @@ struct TrShape {
 
 // Work is counted per key tile: one of a block with two tiles takes longer, 262,144 tokens of 8 KV heads with G 4 202 to 215 us
 // (33 to 64 drafts) where a block with one tile takes 168 (up to 32).
-constexpr int kTrPair = 5, kTrSingle = 4;
+constexpr int kTrPair = 3, kTrSingle = 2;
 
 // A sequence's work: its KV heads one behind another, of each the blocks, of each the key tiles.
 struct TreeSeq {
