@@ -349,7 +349,7 @@ ts_status ts_rope_read(const ts_rope* rope, double* freqs, double* attention);
 /* Turns rows of heads by their positions: x and out [total][heads][d] (d the context's head_dim), dense inside a row,
  * x_stride and out_stride elements from row to row, each of type TS_KV_F32 or TS_KV_BF16; positions int32 [total] on
  * the device. Rows 16-byte aligned. Computed in fp32 and rounded once. out may be x where type and stride are the
- * same; otherwise they must not share memory. With the positions negated the call is its own transpose: the gradient
+ * same (another combination at one address is refused); otherwise they must not share memory. With the positions negated the call is its own transpose: the gradient
  * of x from that of out (and, where a is 1, the inverse). The context gives d and the device. */
 ts_status ts_rotate(ts_ctx* ctx, const ts_rope* rope, const void* x, int64_t x_stride, int dtype, int heads,
                     const int32_t* positions, int total, void* out, int64_t out_stride, int out_dtype, void* stream);
@@ -373,7 +373,8 @@ ts_status ts_append_rotated(ts_ctx* ctx, const ts_rope* rope, const void* k, int
  * mask NULL: the drafts j <= i, a chain. q bf16 [total][H][d] with q_stride, out bf16 [total][H][d] with out_stride,
  * lse fp32 [total][H] or NULL, alignment as in ts_prompt_attend. A row that sees nothing gives out = 0 and
  * lse = -inf. T_b may be 0; T_b above 1024, above 32 mask_words or above seq_lens[b], a length above the maximum, or
- * boundaries that are not ascending record TS_ERR_SEQ_LEN, and nothing is written for that sequence; the tokens of a
+ * boundaries that are not ascending record TS_ERR_SEQ_LEN, and nothing is written for that sequence; total is at most
+ * 2^24. The tokens of a
  * page outside the pool are left out and TS_ERR_PAGE_OOB is recorded. bf16 pools with d 64 or 128 and at most 16
  * query heads per KV head, else TS_ERR_UNSUPPORTED. Scores, sums and outputs accumulate in fp32; softmax weights are
  * rounded to bf16 for their product with v, outputs once at the end. A row's result depends on no draft that it does
@@ -412,7 +413,8 @@ ts_status ts_verify_tree(ts_ctx* ctx, const int32_t* tokens, const int32_t* pare
 /* Keeps the K and V rows of a path of drafts: of the last T_b = cu_rows[b + 1] - cu_rows[b] cached tokens (seq_lens[b]
  * counts them), row path[b][j] moves to row j for j < count[b], so that the path follows the certain tokens without a
  * gap. path and count as ts_verify_tree writes them: ascending within [0, T_b), count[b] in [0, min(T_b, path_stride)].
- * new_lens int32 [B] or NULL receives seq_lens[b] - T_b + count[b]; it must not share memory with seq_lens. Every
+ * new_lens int32 [B] or NULL receives seq_lens[b] - T_b + count[b]; it must not share memory with the other
+ * arrays. Every
  * pool type, values move as they are. n_layers pools each, layer_bytes from one to the next (a multiple of 16, at
  * least a pool; not read for one). A path that is not as above records TS_ERR_INVALID_ARG, a count above path_stride
  * TS_ERR_CAPACITY, boundaries or lengths that are not as in ts_tree_attend TS_ERR_SEQ_LEN: nothing moves for that

@@ -80,6 +80,7 @@ bool valid_params(const ts_select_params* p) {
 constexpr int kMaxRows = 1 << 30;                     // rows of one packed call
 constexpr int64_t kMaxRowStride = (int64_t)1 << 31;   // elements from one packed row to the next
 constexpr double kInv2Pi = 0x1.45f306dc9c883p-3, kInv2PiLow = -0x1.6b01ec5417056p-57;   // 1 / 2pi
+constexpr int kMaxTreeRows = 1 << 24;                  // rows of one call for drafted tokens
 constexpr int kMaxVocab = 1 << 20;                    // tokens of a vocabulary
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
@@ -657,6 +658,7 @@ ts_status ts_rotate(ts_ctx* ctx, const ts_rope* rope, const void* x, int64_t x_s
   if (x_stride % (dtype == TS_KV_F32 ? 4 : 8) != 0 || out_stride % (out_dtype == TS_KV_F32 ? 4 : 8) != 0)
     return TS_ERR_INVALID_ARG;
   if (!aligned16({x, out})) return TS_ERR_INVALID_ARG;
+  if (x == out && (x_stride != out_stride || dtype != out_dtype) && total > 0) return TS_ERR_INVALID_ARG;
   RotateCall a{x, x_stride, dtype, heads, positions, total, out, out_stride, out_dtype};
   return launch_rotate(ctx, rope, a, as_stream(stream));
 }
@@ -679,6 +681,8 @@ ts_status ts_append_rotated(ts_ctx* ctx, const ts_rope* rope, const void* k, int
     if (q_out_dtype != TS_KV_F32 && q_out_dtype != TS_KV_BF16) return TS_ERR_INVALID_ARG;
     if (q_stride < qrow || q_out_stride < qrow || q_stride > kMaxRowStride || q_out_stride > kMaxRowStride) return TS_ERR_SHAPE;
     if (q_stride % per16 != 0 || q_out_stride % (q_out_dtype == TS_KV_F32 ? 4 : 8) != 0) return TS_ERR_INVALID_ARG;
+    if (q == q_out && (q_stride != q_out_stride || (q_out_dtype == TS_KV_F32) != (c.kv_dtype == TS_KV_F32)))
+      return TS_ERR_INVALID_ARG;
   }
   if (!aligned16({k, v, k_pool, v_pool, q, q_out})) return TS_ERR_INVALID_ARG;
   AppendPromptCall a{k, k_stride, v, v_stride, cu_rows, starts, B, total, page_table, k_pool, v_pool};
@@ -697,6 +701,7 @@ ts_status ts_tree_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const voi
   const ts_config& c = ctx->cfg;
   const int64_t row = (int64_t)c.n_q_heads * c.head_dim;
   if (B < 1 || B > c.max_batch || total < 0 || total > kMaxRows) return TS_ERR_SHAPE;
+  if (total > kMaxTreeRows) return TS_ERR_SHAPE;
   if (mask && (mask_words < 1 || mask_words > kMaxTree / 32)) return TS_ERR_SHAPE;
   if (q_stride < row || out_stride < row || q_stride > kMaxRowStride || out_stride > kMaxRowStride) return TS_ERR_SHAPE;
   if (q_stride % 8 != 0 || out_stride % 8 != 0 || !aligned16({q, k_pool, v_pool, out})) return TS_ERR_INVALID_ARG;
@@ -731,8 +736,10 @@ ts_status ts_keep_rows(ts_ctx* ctx, const int32_t* path, int64_t path_stride, co
   if (path_stride < 1 || path_stride > kMaxRowStride || n_layers < 1 || n_layers > 65535) return TS_ERR_SHAPE;
   if (n_layers > 1 && layer_bytes < ctx->cfg.num_pages * ts_page_bytes(&ctx->cfg)) return TS_ERR_SHAPE;
   if ((n_layers > 1 && layer_bytes % 16 != 0) || !aligned16({k_pool, v_pool})) return TS_ERR_INVALID_ARG;
-  // (each of many CTAs reads the lengths, one writes the new ones)
-  if (new_lens && overlap4(new_lens, B, seq_lens, B)) return TS_ERR_INVALID_ARG;
+  // (each of many CTAs reads these, one writes the new lengths)
+  if (new_lens && (overlap4(new_lens, B, seq_lens, B) || overlap4(new_lens, B, count, B) || overlap4(new_lens, B, cu_rows, B + 1) ||
+                   overlap4(new_lens, B, path, B * path_stride)))
+    return TS_ERR_INVALID_ARG;
   KeepCall a{path, path_stride, count, cu_rows, seq_lens, B, total, page_table, k_pool, v_pool, n_layers, layer_bytes, new_lens};
   return launch_keep_rows(ctx, a, as_stream(stream));
 }
