@@ -40,7 +40,7 @@
  *    does not fit, a wait that ran out) are recorded in the context's status
  *    word and read back with ts_get_status. Nothing aborts or traps.
  *  - A context is bound to the device current at ts_create (the packed calls,
- *    ts_attend and every call over a 4-bit pool return TS_ERR_INVALID_ARG where
+ *    those for drafted tokens, ts_attend and every call over a 4-bit pool return TS_ERR_INVALID_ARG where
  *    another one is current) and is not thread safe: calls on one context must
  *    be serialised by the caller, and calls that share a context's scratch must
  *    go to one stream (or be ordered).
@@ -461,9 +461,9 @@ ts_status ts_prefill_chunk(ts_ctx* ctx, const float* q, int c, const void* k_poo
  * nanoseconds (default 1 s): the kernel then records TS_ERR_TIMEOUT, raises an
  * abort word that the other CTAs see at their next barrier, waits (bounded)
  * for its own copies in flight, frees its tensor memory and returns, so the
- * context stays usable. The waits of ts_prefill_chunk and ts_prompt_attend have
+ * context stays usable. The waits of ts_prefill_chunk, ts_prompt_attend and ts_tree_attend have
  * the same bound (each by itself; one of the longest lasts as long as 128 rows of
- * a prompt take), but what ts_prompt_attend has in flight when one runs out is
+ * a prompt take), but what the last two have in flight when one runs out is
  * waited for as long as 1 s even where ns is less. The waits of the separate calls
  * (ts_score, ts_attend, ts_sparse_attend) keep the 1 s bound. ns == 0 is
  * TS_ERR_INVALID_ARG. */

