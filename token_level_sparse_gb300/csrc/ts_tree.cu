@@ -92,8 +92,9 @@ struct TrShape {
 };
 
 // Work is counted per key tile: one of a block with two tiles takes longer, 262,144 tokens of 8 KV heads with G 4 202 to 215 us
-// (33 to 64 drafts) where a block with one tile takes 168 (up to 32).
-constexpr int kTrPair = 3, kTrSingle = 2;
+// (33 to 64 drafts) where a block with one tile takes 168 (up to 32); more in one batch, where those wait less for memory. A block of
+// its own costs about three key tiles: its queries, first softmax and outputs.
+constexpr int kTrPair = 3, kTrSingle = 2, kTrBlock = 4;
 
 // A sequence's work: its KV heads one behind another, of each the blocks, of each the key tiles.
 struct TreeSeq {
@@ -101,7 +102,9 @@ struct TreeSeq {
   int blocks, tiles;             // blocks of drafts, key tiles of a block
   int last;                      // work of a key tile of the last block (of the others: kTrPair)
   int err;
-  __device__ __forceinline__ int64_t head() const { return (int64_t)tiles * (blocks > 0 ? kTrPair * (blocks - 1) + last : 0); }
+  // of a block that is not the last one, and of a KV head
+  __device__ __forceinline__ int64_t block() const { return kTrBlock + (int64_t)kTrPair * tiles; }
+  __device__ __forceinline__ int64_t head() const { return blocks > 0 ? block() * (blocks - 1) + kTrBlock + (int64_t)last * tiles : 0; }
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
@@ -129,11 +132,14 @@ __device__ __forceinline__ int64_t warp_scan_ll(int64_t x, int lane) {
   return x;
 }
 
-// CTAs that share the work (each has a key tile at least), where the share of CTA c begins, and whose share a place is in. A
-// key tile belongs to the share that its beginning lies in.
-__device__ __forceinline__ int share_ctas(int64_t work, int grid) { return (int)max((int64_t)1, min((int64_t)grid, work / kTrPair)); }
+// Where the share of CTA c begins, and whose share a place is in. A key tile belongs to the share that its beginning lies
+// in (a share may have none).
 __device__ __forceinline__ int64_t share_begin(int64_t work, int ctas, int c) { return work * c / ctas; }
 __device__ __forceinline__ int share_of(int64_t work, int ctas, int64_t at) { return (int)(((at + 1) * ctas - 1) / work); }
+// The first of `tiles` key tiles, beginning at `at` and every `per` from there on, that begins at a place or behind it.
+__device__ __forceinline__ int first_tile(int64_t at, int per, int tiles, int64_t place) {
+  return place <= at ? 0 : (int)min((int64_t)tiles, (place - at + per - 1) / per);
+}
 
 // Places in the ring of an item's key tile j and value tile j, counted from its first: K(0), K(1), V(0), K(2), V(1), ...
 __device__ __forceinline__ uint32_t key_load(int j) { return j == 0 ? 0u : 2u * (uint32_t)j - 1u; }
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       __syncwarp();
     } else if (warp == kTrSoftmaxWarps + 2) {
       // ---------------------------------------------------------------- items
-      int64_t work = 0;
+      int64_t work = 0, tiles_all = 0;
       for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int b = b0 + lane;
         TreeSeq s{};
@@ -499,8 +505,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         const int64_t run = work + warp_scan_ll(s.head() * a.HKV, lane);
         if (blockIdx.x == 0 && s.err) set_error(a.status, s.err);
         work = __shfl_sync(kFull, run, 31);
+        tiles_all += __shfl_sync(kFull, warp_scan_ll((int64_t)s.blocks * s.tiles, lane), 31) * a.HKV;
       }
-      const int ctas = share_ctas(work, gridDim.x);
+      const int ctas = (int)min((int64_t)gridDim.x, tiles_all);
       int64_t t = 0, e = 0;
       if (work > 0 && (int)blockIdx.x < ctas) {
         t = share_begin(work, ctas, blockIdx.x);
@@ -530,11 +537,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             const int64_t start = before + __shfl_sync(kFull, run - w, src), head = __shfl_sync(kFull, s.head(), src);
             const int tiles = __shfl_sync(kFull, s.tiles, src), blocks = __shfl_sync(kFull, s.blocks, src);
             const int last = __shfl_sync(kFull, s.last, src);
-            const int64_t in = (t - start) % head;
-            const int kv = (int)((t - start) / head), block = (int)min(in / (kTrPair * tiles), (int64_t)blocks - 1);
+            const int64_t in = (t - start) % head, one = kTrBlock + (int64_t)kTrPair * tiles;
+            const int kv = (int)((t - start) / head), block = (int)min(in / one, (int64_t)blocks - 1);
             const int per = block + 1 < blocks ? kTrPair : last;  // work of a key tile
-            const int64_t at = t - in + (int64_t)block * kTrPair * tiles;        // where the block begins
-            const int j0 = (int)((t - at + per - 1) / per), j1 = (int)min((int64_t)tiles, (e - at + per - 1) / per);
+            const int64_t at = t - in + block * one + kTrBlock;   // where the block's key tiles begin
+            const int j0 = first_tile(at, per, tiles, t), j1 = first_tile(at, per, tiles, e);
             t = at + (int64_t)per * tiles;                        // the next block
             if (j0 >= j1) {                                       // (no key tile of this one begins in the share)
               if (t < e) continue;
@@ -865,7 +872,8 @@ constexpr int kJoinParts = 256;  // CTAs of a call, at most
 template <int D>
 __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(const __grid_constant__ TreeArgs a, int grid) {
   constexpr int COLS = D / 4;
-  __shared__ int s_first[kJoinRows], s_parts[kJoinRows], s_at[kJoinRows];
+  __shared__ int s_first[kJoinRows], s_parts[kJoinRows], s_at[kJoinRows], s_per[kJoinRows], s_tiles[kJoinRows], s_ctas;
+  __shared__ int64_t s_begin[kJoinRows], s_work;
   __shared__ float s_f[kJoinRows][kJoinParts];
   __shared__ float s_inv[kJoinRows];
   __shared__ float4 s_acc[kJoinGroups - 1][kJoinRows * COLS];
@@ -881,9 +889,9 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(c
   int kv, packed, head;
   place(row, kv, packed, head);
   if (warp == 0) {
-    // lane r < 8: where the first and last key tile of row r's block begin (-1: no row of a sequence), and the row's place
-    int64_t work = 0, t0 = -1, t1 = -1;
-    int at = 0;
+    // lane r < 8: where row r's block has its key tiles (-1: no row of a sequence), and the row's place
+    int64_t work = 0, tiles_all = 0, t0 = -1;
+    int at = 0, per = 0, tiles = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       TreeSeq s{};
       if (b0 + lane < a.B) s = tree_seq(a, b0 + lane);
@@ -897,21 +905,30 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(c
         const int64_t before = __shfl_sync(kFull, run - w, src), one = __shfl_sync(kFull, s.head(), src);
         if (lane == r && kv < a.HKV) {
           const int tok = p - row0, block = tok / (2 * a.tokens), in = tok - block * 2 * a.tokens;
-          t0 = before + kv * one + (int64_t)block * kTrPair * n;
-          t1 = t0 + (int64_t)(n - 1) * (block + 1 < blocks ? kTrPair : last);
+          tiles = n;
+          per = block + 1 < blocks ? kTrPair : last;
+          t0 = before + kv * one + block * (kTrBlock + (int64_t)kTrPair * n) + kTrBlock;
           at = (in / a.tokens) * 128 + in % a.tokens * a.G + head;
         }
       }
       work = __shfl_sync(kFull, run, 31);
+      tiles_all += __shfl_sync(kFull, warp_scan_ll((int64_t)s.blocks * s.tiles, lane), 31) * a.HKV;
+    }
+    const int ctas = (int)min((int64_t)grid, tiles_all);
+    if (lane == 0) {
+      s_work = work;
+      s_ctas = ctas;
     }
     if (lane < kJoinRows) {
       int parts = 0;
       if (t0 >= 0) {
-        const int ctas = share_ctas(work, grid);
-        const int c0 = share_of(work, ctas, t0), c1 = share_of(work, ctas, t1);
+        const int c0 = share_of(work, ctas, t0), c1 = share_of(work, ctas, t0 + (int64_t)per * (tiles - 1));
         parts = c1 > c0 ? c1 - c0 + 1 : 0;                        // (else the block's outputs are there)
         s_first[lane] = c0;
         s_at[lane] = at;
+        s_begin[lane] = t0;
+        s_per[lane] = per;
+        s_tiles[lane] = tiles;
       }
       s_parts[lane] = parts;
     }
@@ -919,6 +936,15 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(c
   __syncthreads();
   auto slot_of = [&](int r, int k) { return 2 * (s_first[r] + k) + (k == 0 ? 1 : 0); };
   const int parts = s_parts[row];
+  if (warp < kJoinRows) {
+    // which of the CTAs in between have a key tile of the block (a lane looks at those that it takes below)
+    for (int k = lane; k < s_parts[warp]; k += 32) {
+      const int c = s_first[warp] + k;
+      const int j0 = first_tile(s_begin[warp], s_per[warp], s_tiles[warp], share_begin(s_work, s_ctas, c));
+      const int j1 = first_tile(s_begin[warp], s_per[warp], s_tiles[warp], share_begin(s_work, s_ctas, c + 1));
+      s_f[warp][k] = j0 < j1 ? 1.f : 0.f;
+    }
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float4* src = reinterpret_cast<const float4*>(a.part_o) + (int64_t)col * 256 + (parts ? s_at[row] : 0);
   float4 o[kJoinBatch];
@@ -936,13 +962,13 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(c
     const float2* ml = a.part_ml + s_at[warp];
     float M = -INFINITY, total = 0.f;
     for (int k = lane; k < n; k += 32) {
-      const float2 x = ml[(int64_t)slot_of(warp, k) * 256];
+      const float2 x = s_f[warp][k] != 0.f ? ml[(int64_t)slot_of(warp, k) * 256] : make_float2(-INFINITY, 0.f);
       M = fmaxf(M, x.y == 0.f ? -INFINITY : x.x);
     }
     M = warp_max(M);
     const float M2 = M * a.scale2;
     for (int k = lane; k < n; k += 32) {
-      const float2 x = ml[(int64_t)slot_of(warp, k) * 256];
+      const float2 x = s_f[warp][k] != 0.f ? ml[(int64_t)slot_of(warp, k) * 256] : make_float2(-INFINITY, 0.f);
       const float f = x.y == 0.f ? 0.f : (x.x == M ? 1.f : pr_ex2(from_to(x.x, x.x * a.scale2, M, M2, a.scale2)));
       s_f[warp][k] = f;
       if (f != 0.f) total = fmaf(f, x.y, total);
