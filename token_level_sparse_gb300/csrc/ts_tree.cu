@@ -52,6 +52,8 @@ static_assert(2 * kTrSoftmaxRegs + kTrOtherRegs <= 3 * 168, "register shares");
 constexpr int kTrRing = 8;
 constexpr float kTrMaxSum = 16384.f;   // of a tile's weights against a maximum taken earlier
 
+constexpr int kJoinParts = 256;  // CTAs of a call, at most
+
 struct TreeArgs {
   CUtensorMap q, k, v;           // q [rows][heads][d]; k, v [pages][heads * page size][d]
   const int32_t* cu;
@@ -863,156 +865,184 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   }
 }
 
-// Joins the sums of blocks that several CTAs had parts of. Eight rows of one KV head to a CTA (neighbouring rows of a block:
-// heads, then tokens), whose sums lie side by side; a thread per row, four columns and every second part. Bound by latency:
-// the shares are worked out while the kernel before it still runs, and sums and factors are on their way together.
-constexpr int kJoinRows = 8, kJoinGroups = 2, kJoinBatch = 8;
-constexpr int kJoinParts = 256;  // CTAs of a call, at most
+// Joins the sums of blocks that several CTAs had parts of: eight rows of one to a CTA at a time (neighbouring rows of a block:
+// heads, then drafts), whose sums lie side by side; a thread per row, four columns and every second part. Bound by
+// latency (which blocks, factors and parts together, sums), then by the parts read from L2.
+constexpr int kJoinRows = 8, kJoinGroups = 2, kJoinBatch = 6;
+
+// A block that several CTAs have parts of, by the CTA that its first key tile lies with.
+struct TreeJoin {
+  int64_t at;                    // where its key tiles begin
+  int row0, drafts, kv;          // its rows
+  int parts;                     // CTAs from this one to the one that its last key tile lies with; 0: no such block
+  int per, tiles;                // work of a key tile, key tiles
+};
 
 template <int D>
-__global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups) join_kernel(const __grid_constant__ TreeArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups, 256 / D) join_kernel(const __grid_constant__ TreeArgs a, int grid) {
   constexpr int COLS = D / 4;
-  __shared__ int s_first[kJoinRows], s_parts[kJoinRows], s_at[kJoinRows], s_per[kJoinRows], s_tiles[kJoinRows], s_ctas;
-  __shared__ int64_t s_begin[kJoinRows], s_work;
+  __shared__ int s_upto[kJoinParts];                              // pieces of the blocks up to that of each CTA
+  __shared__ TreeJoin s_join[kJoinParts];
+  __shared__ TreeSeq s_seq[32];
+  __shared__ int64_t s_end[32];                                   // work up to a sequence's end
+  __shared__ int64_t s_work;
+  __shared__ int s_ctas;
   __shared__ float s_f[kJoinRows][kJoinParts];
   __shared__ float s_inv[kJoinRows];
   __shared__ float4 s_acc[kJoinGroups - 1][kJoinRows * COLS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t per_kv = (int64_t)a.total * a.G;
   const int row = tid % kJoinRows, col = tid / kJoinRows % COLS, grp = tid / (kJoinRows * COLS);
-  auto place = [&](int r, int& kv, int& packed, int& head) {
-    const int64_t idx = (int64_t)blockIdx.x * kJoinRows + r;
-    kv = (int)(idx / per_kv);
-    packed = (int)(idx % per_kv / a.G);
-    head = (int)(idx % a.G);
-  };
-  int kv, packed, head;
-  place(row, kv, packed, head);
+  // ---- which blocks: a thread per CTA (256 of each), all from lengths and boundaries, while the other kernel runs
   if (warp == 0) {
-    // lane r < 8: where row r's block has its key tiles (-1: no row of a sequence), and the row's place
-    int64_t work = 0, tiles_all = 0, t0 = -1;
-    int at = 0, per = 0, tiles = 0;
+    int64_t work = 0, tiles_all = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       TreeSeq s{};
       if (b0 + lane < a.B) s = tree_seq(a, b0 + lane);
-      const int64_t w = s.head() * a.HKV, run = work + warp_scan_ll(w, lane);
-      for (int r = 0; r < kJoinRows; ++r) {
-        const int p = __shfl_sync(kFull, packed, r);
-        const unsigned m = __ballot_sync(kFull, s.blocks > 0 && p >= s.row0 && p < s.row0 + s.T);
-        if (!m) continue;
-        const int src = __ffs(m) - 1, row0 = __shfl_sync(kFull, s.row0, src), blocks = __shfl_sync(kFull, s.blocks, src);
-        const int n = __shfl_sync(kFull, s.tiles, src), last = __shfl_sync(kFull, s.last, src);
-        const int64_t before = __shfl_sync(kFull, run - w, src), one = __shfl_sync(kFull, s.head(), src);
-        if (lane == r && kv < a.HKV) {
-          const int tok = p - row0, block = tok / (2 * a.tokens), in = tok - block * 2 * a.tokens;
-          tiles = n;
-          per = block + 1 < blocks ? kTrPair : last;
-          t0 = before + kv * one + block * (kTrBlock + (int64_t)kTrPair * n) + kTrBlock;
-          at = (in / a.tokens) * 128 + in % a.tokens * a.G + head;
-        }
-      }
-      work = __shfl_sync(kFull, run, 31);
+      work = __shfl_sync(kFull, work + warp_scan_ll(s.head() * a.HKV, lane), 31);
       tiles_all += __shfl_sync(kFull, warp_scan_ll((int64_t)s.blocks * s.tiles, lane), 31) * a.HKV;
     }
-    const int ctas = (int)min((int64_t)grid, tiles_all);
     if (lane == 0) {
       s_work = work;
-      s_ctas = ctas;
-    }
-    if (lane < kJoinRows) {
-      int parts = 0;
-      if (t0 >= 0) {
-        const int c0 = share_of(work, ctas, t0), c1 = share_of(work, ctas, t0 + (int64_t)per * (tiles - 1));
-        parts = c1 > c0 ? c1 - c0 + 1 : 0;                        // (else the block's outputs are there)
-        s_first[lane] = c0;
-        s_at[lane] = at;
-        s_begin[lane] = t0;
-        s_per[lane] = per;
-        s_tiles[lane] = tiles;
-      }
-      s_parts[lane] = parts;
+      s_ctas = (int)min((int64_t)grid, tiles_all);
     }
   }
   __syncthreads();
-  auto slot_of = [&](int r, int k) { return 2 * (s_first[r] + k) + (k == 0 ? 1 : 0); };
-  const int parts = s_parts[row];
-  if (warp < kJoinRows) {
-    // which of the CTAs in between have a key tile of the block (a lane looks at those that it takes below)
-    for (int k = lane; k < s_parts[warp]; k += 32) {
-      const int c = s_first[warp] + k;
-      const int j0 = first_tile(s_begin[warp], s_per[warp], s_tiles[warp], share_begin(s_work, s_ctas, c));
-      const int j1 = first_tile(s_begin[warp], s_per[warp], s_tiles[warp], share_begin(s_work, s_ctas, c + 1));
-      s_f[warp][k] = j0 < j1 ? 1.f : 0.f;
+  const int64_t work = s_work;
+  const int ctas = s_ctas;
+  TreeJoin mine{};
+  const int64_t begin = tid < ctas ? share_begin(work, ctas, tid) : 0, end = tid < ctas ? share_begin(work, ctas, tid + 1) : 0;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    if (warp == 0) {
+      TreeSeq s{};
+      if (b0 + lane < a.B) s = tree_seq(a, b0 + lane);
+      s_seq[lane] = s;
+      s_end[lane] = before + warp_scan_ll(s.head() * a.HKV, lane);
+    }
+    __syncthreads();
+    const int64_t last = end - 1;                                 // the block that the share's last place is in
+    if (tid < ctas && last >= before && last < s_end[31]) {
+      int b = 0;
+      while (s_end[b] <= last) ++b;
+      const TreeSeq s = s_seq[b];
+      const int64_t start = b ? s_end[b - 1] : before, in = (last - start) % s.head();
+      const int block = (int)min(in / s.block(), (int64_t)s.blocks - 1);
+      mine.kv = (int)((last - start) / s.head());
+      mine.per = block + 1 < s.blocks ? kTrPair : s.last;
+      mine.tiles = s.tiles;
+      mine.at = last - in + block * s.block() + kTrBlock;
+      mine.row0 = s.row0 + block * 2 * a.tokens;
+      mine.drafts = min(s.T - block * 2 * a.tokens, 2 * a.tokens);
+      const int64_t final = mine.at + (int64_t)mine.per * (s.tiles - 1);
+      mine.parts = mine.at >= begin && mine.at < end && final >= end ? share_of(work, ctas, final) - tid + 1 : 0;
+    }
+    before = s_end[31];
+    __syncthreads();
+  }
+  if (tid < kJoinParts) {
+    s_join[tid] = mine;
+    s_upto[tid] = mine.parts ? (mine.drafts * a.G + kJoinRows - 1) / kJoinRows : 0;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int sum = 0;
+    for (int c = lane; c < kJoinParts; c += 32) {
+      int run = s_upto[c];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(kFull, run, d);
+        if (lane >= d) run += x;
+      }
+      s_upto[c] = sum + run;
+      sum += __shfl_sync(kFull, run, 31);
     }
   }
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float4* src = reinterpret_cast<const float4*>(a.part_o) + (int64_t)col * 256 + (parts ? s_at[row] : 0);
-  float4 o[kJoinBatch];
-  auto load = [&](int k0) {
+  for (int piece = blockIdx.x; piece < s_upto[kJoinParts - 1]; piece += gridDim.x) {
+    int c = 0;
+    for (int hi = kJoinParts - 1; c < hi;) {                            // the first CTA with more pieces up to it
+      const int mid = (c + hi) >> 1;
+      if (s_upto[mid] > piece) hi = mid; else c = mid + 1;
+    }
+    const TreeJoin& jn = s_join[c];
+    const int rows = jn.drafts * a.G, r0 = (piece - (c ? s_upto[c - 1] : 0)) * kJoinRows, parts = jn.parts;
+    auto slot_of = [&](int k) { return 2 * (c + k) + (k == 0 ? 1 : 0); };
+    auto place = [&](int r) { return r / a.G / a.tokens * 128 + r / a.G % a.tokens * a.G + r % a.G; };
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + (int64_t)col * 256 + place(min(r0 + row, rows - 1));
+    float4 o[kJoinBatch];
+    auto load = [&](int k0) {
 #pragma unroll
-    for (int e = 0; e < kJoinBatch; ++e) {
-      const int k = k0 + e * kJoinGroups;
-      if (k < parts) o[e] = src[(int64_t)slot_of(row, k) * COLS * 256];
-    }
-  };
-  load(grp);
-  if (warp < kJoinRows && s_parts[warp] > 0) {
-    // every part's factor, and the row's sum: a warp per row, a lane per part
-    const int n = s_parts[warp];
-    const float2* ml = a.part_ml + s_at[warp];
-    float M = -INFINITY, total = 0.f;
-    for (int k = lane; k < n; k += 32) {
-      const float2 x = s_f[warp][k] != 0.f ? ml[(int64_t)slot_of(warp, k) * 256] : make_float2(-INFINITY, 0.f);
-      M = fmaxf(M, x.y == 0.f ? -INFINITY : x.x);
-    }
-    M = warp_max(M);
-    const float M2 = M * a.scale2;
-    for (int k = lane; k < n; k += 32) {
-      const float2 x = s_f[warp][k] != 0.f ? ml[(int64_t)slot_of(warp, k) * 256] : make_float2(-INFINITY, 0.f);
-      const float f = x.y == 0.f ? 0.f : (x.x == M ? 1.f : pr_ex2(from_to(x.x, x.x * a.scale2, M, M2, a.scale2)));
-      s_f[warp][k] = f;
-      if (f != 0.f) total = fmaf(f, x.y, total);
-    }
-    total = warp_sum(total);
-    if (lane == 0) {
-      s_inv[warp] = total == 0.f ? 0.f : 1.f / total;
-      int kv1, packed1, head1;
-      place(warp, kv1, packed1, head1);
-      if (a.lse)
-        a.lse[(int64_t)packed1 * a.H + kv1 * a.G + head1] =
-            total == 0.f ? -INFINITY : (M2 + log2f(total)) * 0.6931471805599453f;
-    }
-  }
-  __syncthreads();
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = grp; k0 < parts; k0 += kJoinBatch * kJoinGroups) {
-    if (k0 != grp) load(k0);
-#pragma unroll
-    for (int e = 0; e < kJoinBatch; ++e) {
-      const int k = k0 + e * kJoinGroups;
-      const float f = k < parts ? s_f[row][k] : 0.f;
-      if (f != 0.f) {                                             // (a part whose weight vanishes may hold anything)
-        acc.x = fmaf(f, o[e].x, acc.x);
-        acc.y = fmaf(f, o[e].y, acc.y);
-        acc.z = fmaf(f, o[e].z, acc.z);
-        acc.w = fmaf(f, o[e].w, acc.w);
+      for (int e = 0; e < kJoinBatch; ++e) {
+        const int k = k0 + e * kJoinGroups;
+        if (k < parts) o[e] = src[(int64_t)slot_of(k) * COLS * 256];
+      }
+    };
+    load(grp);
+    if (warp < kJoinRows && r0 + warp < rows) {
+      // every part's factor, and the row's sum: a warp per row, a lane per part (0: a CTA in between that had no key tile)
+      const int r = r0 + warp;
+      const float2* ml = a.part_ml + place(r);
+      float M = -INFINITY, total = 0.f;
+      auto part = [&](int k) {
+        const int j0 = first_tile(jn.at, jn.per, jn.tiles, share_begin(work, ctas, c + k));
+        const int j1 = first_tile(jn.at, jn.per, jn.tiles, share_begin(work, ctas, c + k + 1));
+        return j0 < j1 ? ml[(int64_t)slot_of(k) * 256] : make_float2(-INFINITY, 0.f);
+      };
+      for (int k = lane; k < parts; k += 32) {
+        const float2 x = part(k);
+        M = fmaxf(M, x.y == 0.f ? -INFINITY : x.x);
+      }
+      M = warp_max(M);
+      const float M2 = M * a.scale2;
+      for (int k = lane; k < parts; k += 32) {
+        const float2 x = part(k);
+        const float f = x.y == 0.f ? 0.f : (x.x == M ? 1.f : pr_ex2(from_to(x.x, x.x * a.scale2, M, M2, a.scale2)));
+        s_f[warp][k] = f;
+        if (f != 0.f) total = fmaf(f, x.y, total);
+      }
+      total = warp_sum(total);
+      if (lane == 0) {
+        s_inv[warp] = total == 0.f ? 0.f : 1.f / total;
+        if (a.lse)
+          a.lse[(int64_t)(jn.row0 + r / a.G) * a.H + jn.kv * a.G + r % a.G] =
+              total == 0.f ? -INFINITY : (M2 + log2f(total)) * 0.6931471805599453f;
       }
     }
-  }
-  if (grp > 0) s_acc[grp - 1][tid % (kJoinRows * COLS)] = acc;
-  __syncthreads();
-  if (grp > 0 || parts == 0) return;
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = grp; k0 < parts; k0 += kJoinBatch * kJoinGroups) {
+      if (k0 != grp) load(k0);
 #pragma unroll
-  for (int g = 0; g < kJoinGroups - 1; ++g) {
-    const float4 x = s_acc[g][tid];
-    acc.x += x.x;
-    acc.y += x.y;
-    acc.z += x.z;
-    acc.w += x.w;
+      for (int e = 0; e < kJoinBatch; ++e) {
+        const int k = k0 + e * kJoinGroups;
+        const float f = k < parts && r0 + row < rows ? s_f[row][k] : 0.f;
+        if (f != 0.f) {                                           // (a part whose weight vanishes may hold anything)
+          acc.x = fmaf(f, o[e].x, acc.x);
+          acc.y = fmaf(f, o[e].y, acc.y);
+          acc.z = fmaf(f, o[e].z, acc.z);
+          acc.w = fmaf(f, o[e].w, acc.w);
+        }
+      }
+    }
+    if (grp > 0) s_acc[grp - 1][tid % (kJoinRows * COLS)] = acc;
+    __syncthreads();
+    if (grp == 0 && r0 + row < rows) {
+#pragma unroll
+      for (int g = 0; g < kJoinGroups - 1; ++g) {
+        const float4 x = s_acc[g][tid];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+      }
+      const float inv = s_inv[row];
+      const int r = r0 + row;
+      __nv_bfloat16* out = a.out + (int64_t)(jn.row0 + r / a.G) * a.out_stride + (int64_t)(jn.kv * a.G + r % a.G) * D + col * 4;
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    }
+    __syncthreads();
   }
-  const float inv = s_inv[row];
-  __nv_bfloat16* out = a.out + (int64_t)packed * a.out_stride + (int64_t)(kv * a.G + head) * D + col * 4;
-  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 // bf16 [pages][heads * page size][d] in boxes of 64 elements x one page of one head.
@@ -1037,8 +1067,7 @@ ts_status run_tree(ts_ctx* ctx, const TreeArgs& a, cudaStream_t s) {
   tree_kernel<D><<<grid, kTrThreads, TrShape<D>::SMEM, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
-  const int64_t rows = (int64_t)a.total * a.H;
-  return cuda_status(launch_behind(join_kernel<D>, dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows)), kJoinRows * D / 4 * kJoinGroups, s, a, grid));
+  return cuda_status(launch_behind(join_kernel<D>, dim3((unsigned)(2 * grid)), kJoinRows * D / 4 * kJoinGroups, s, a, grid));
 }
 
 }  // namespace
