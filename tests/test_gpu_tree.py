@@ -170,6 +170,16 @@ def test_many_sequences():
     Case(4, 2, 64, lens=lens, trees=trees, seed=6).run().check(heads=[0, 3, 7])
 
 
+def test_hundreds_of_sequences():
+    """More sequences than the look-ups take at a time; most blocks whole, some split."""
+    rng = np.random.default_rng(1)
+    trees = [int(x) for x in rng.integers(0, 5, 230)]
+    trees[200] = 100
+    lens = [t + int(rng.integers(0, 60)) for t in trees]
+    lens[35], lens[200], lens[229] = trees[35] + 5000, 3000, trees[229] + 2000
+    Case(4, 2, 64, lens=lens, trees=trees, seed=20).run().check(rows=[0, 3, 99], heads=[0, 7])
+
+
 def test_one_token_pages():
     Case(8, 1, 128, lens=[1, 260, 129], trees=[1, 6, 3], page=1, seed=7).run().check()
     Case(8, 4, 128, lens=[700], trees=[40], page=1, seed=8, spare=5).run().check(heads=[0, 31])
