@@ -134,6 +134,21 @@ def test_what_is_not_turned_and_not_finite():
         assert torch.equal(bad, want)
 
 
+def test_given_frequencies_and_a_factor():
+    """Any frequencies: more than a turn per position, backwards, tiny, zero."""
+    T = tsl()
+    ctx = T.Context(4, 4, 64, T.TS_KV_Q4, 1, 1, 1)
+    rope = ctx.rope(12, scaling="given", freqs=[1.0, -0.25, 7.5, 1234.5678, 3e-9, 0.0], attention=0.75)
+    for pairs in (False, True):
+        rope = ctx.rope(12, interleaved=pairs, scaling="given", freqs=[1.0, -0.25, 7.5, 1234.5678, 3e-9, 0.0], attention=0.75)
+        x = _rows(9, 2, 64, F32, 8)
+        pos = np.array([0, 1, 5, 77, 131071, 10 ** 6, 2 ** 31 - 1, -1, -2 ** 31])
+        out = torch.empty(9, 2, 64, device=DEV)
+        ctx.rotate(rope, x, torch.from_numpy(pos.astype(np.int32)).to(DEV), out)
+        assert ctx.status() == 0
+        _check(out, x, pos, rope, 12, pairs)
+
+
 def test_no_rows_is_nothing_to_do():
     T = tsl()
     ctx = T.Context(4, 4, 64, T.TS_KV_Q4, 1, 1, 1)
