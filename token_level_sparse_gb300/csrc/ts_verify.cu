@@ -97,6 +97,7 @@ __host__ __device__ inline int warp_part(int V, int ctas) {
 __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  cluster.barrier_arrive();            // shared memory of another CTA may be written once that CTA runs (waited for below)
   const int b = blockIdx.x / ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   extern __shared__ unsigned s_gone[];                          // bit per token of the slice (drafts without probabilities)
   __shared__ int s_parent[kMaxTree], s_token[kMaxTree];
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
   }
   int token = -1;
 
+  cluster.barrier_wait(cg::cluster_group::arrival_token());       // (the nodes were fetched meanwhile)
   for (;;) {
     if (rank == 0 && warp == 0) {
       Order o{kVfEnd, cur, 0, 0.};
