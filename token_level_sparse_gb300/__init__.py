@@ -754,6 +754,8 @@ class Context:
                 _refuse("tree_attend", "TS_ERR_SHAPE", f"{tuple(mask.shape)} instead of {(total, 'words')}")
             words = mask.shape[1]
             self._counted("tree_attend", here, (mask, (total, words), _int32))
+            if words == 0 and total > 0:                           # (its address is NULL, which stands for no mask)
+                _refuse("tree_attend", "TS_ERR_SHAPE", "a mask without words")
         self._paged("tree_attend", B, page_table, k_pool, v_pool)
         ts_tree_attend(self.handle, q, qs, k_pool, v_pool, page_table, seq_lens, cu_rows, mask, words, B, total, scale, out,
                        os_, lse, stream)
