@@ -869,6 +869,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
 // heads, then drafts), whose sums lie side by side; a thread per row, four columns and every second part. Bound by
 // latency (which blocks, factors and parts together, sums), then by the parts read from L2.
 constexpr int kJoinRows = 8, kJoinGroups = 2, kJoinBatch = 6;
+constexpr float kNoPart = -1.f;  // in place of a sum or a factor, which are not negative
 
 // A block that several CTAs have parts of, by the CTA that its first key tile lies with.
 struct TreeJoin {
@@ -980,26 +981,29 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups, 256 / D) join
     };
     load(grp);
     if (warp < kJoinRows && r0 + warp < rows) {
-      // every part's factor, and the row's sum: a warp per row, a lane per part (0: a CTA in between that had no key tile)
+      // every part's factor, and the row's sum: a warp per row, a lane per part. A part that saw a number that is none has a
+      // sum that is none (its maximum passes it over), which is its factor too; kNoPart: a CTA in between that had no key tile.
       const int r = r0 + warp;
       const float2* ml = a.part_ml + place(r);
       float M = -INFINITY, total = 0.f;
       auto part = [&](int k) {
         const int j0 = first_tile(jn.at, jn.per, jn.tiles, share_begin(work, ctas, c + k));
         const int j1 = first_tile(jn.at, jn.per, jn.tiles, share_begin(work, ctas, c + k + 1));
-        return j0 < j1 ? ml[(int64_t)slot_of(k) * 256] : make_float2(-INFINITY, 0.f);
+        return j0 < j1 ? ml[(int64_t)slot_of(k) * 256] : make_float2(-INFINITY, kNoPart);
       };
       for (int k = lane; k < parts; k += 32) {
         const float2 x = part(k);
-        M = fmaxf(M, x.y == 0.f ? -INFINITY : x.x);
+        M = fmaxf(M, x.y == 0.f || x.y == kNoPart ? -INFINITY : x.x);
       }
       M = warp_max(M);
       const float M2 = M * a.scale2;
       for (int k = lane; k < parts; k += 32) {
         const float2 x = part(k);
-        const float f = x.y == 0.f ? 0.f : (x.x == M ? 1.f : pr_ex2(from_to(x.x, x.x * a.scale2, M, M2, a.scale2)));
+        const float f = x.y == 0.f || x.y == kNoPart || x.y != x.y
+                            ? x.y
+                            : (x.x == M ? 1.f : pr_ex2(from_to(x.x, x.x * a.scale2, M, M2, a.scale2)));
         s_f[warp][k] = f;
-        if (f != 0.f) total = fmaf(f, x.y, total);
+        if (f != kNoPart) total = fmaf(f, x.y, total);
       }
       total = warp_sum(total);
       if (lane == 0) {
@@ -1016,8 +1020,8 @@ __global__ void __launch_bounds__(kJoinRows * D / 4 * kJoinGroups, 256 / D) join
 #pragma unroll
       for (int e = 0; e < kJoinBatch; ++e) {
         const int k = k0 + e * kJoinGroups;
-        const float f = k < parts && r0 + row < rows ? s_f[row][k] : 0.f;
-        if (f != 0.f) {                                           // (a part whose weight vanishes may hold anything)
+        const float f = k < parts && r0 + row < rows ? s_f[row][k] : kNoPart;
+        if (f != kNoPart) {                                       // (a value that is not finite shows however little it weighs)
           acc.x = fmaf(f, o[e].x, acc.x);
           acc.y = fmaf(f, o[e].y, acc.y);
           acc.z = fmaf(f, o[e].z, acc.z);
