@@ -24,6 +24,7 @@
 // token, cluster barriers of 0.5); 32 trees of up to 64 nodes over 128,256 tokens 57 us, as long as the one with most
 // refusals takes, 6 us for each sweep of its rows.
 #include <cooperative_groups.h>
+#include <math_constants.h>
 
 #include "ts_common.cuh"
 
@@ -322,8 +323,8 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
       const int l = over ? __ffs(over) - 1 : 31 - __clz(some);
       if (some && lane == l) {
         s_from = PL * l + (over ? mine_over : mine_some);
-        s_before = over ? at_part : all;                          // (past all: the part's last element is taken)
-        s_t = t;
+        s_before = at_part;
+        s_t = over ? t : CUDART_INF;                              // (not passed: the part's last element that holds something)
       }
       if (!some && lane == 0) s_from = -1;
     }
