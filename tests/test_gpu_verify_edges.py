@@ -1,7 +1,10 @@
 """ts_verify_tree on the GPU where a walk ends at once, and at the edges of its arithmetic."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
+from oracle import draft_oracle as D
 from parity import tsl
 from test_gpu_verify import Batch
 
@@ -31,6 +34,62 @@ def test_walks_that_end_at_once(V):
     assert set(nxt) == {-1} and set(count) == {0} and b.ctx.status() == tsl().STATUS_CODE["TS_ERR_SEQ_LEN"]
     b.cu = cu
     assert b.run(False, False)[2] == want and b.ctx.status() == 0
+
+
+def _border(seed, V):
+    """A node with three children whose third is decided by a small sum of small residuals: half of the draft's mass lies
+    on tokens that the target gives a little less, the other half on ones that it gives a little more. The first two
+    children are of the former (refused at u just below 1), and c = 1 + Z of the second test has 24 bits and more.
+    Returns p, q, the tokens and the smallest u at which the third child is refused, by exact arithmetic."""
+    rng = np.random.default_rng(seed)
+    few = np.arange(V // 2)
+    q = np.concatenate([rng.uniform(0.5, 1, V // 2), rng.uniform(0.5, 1, V - V // 2)])
+    q[few] *= 0.5 / q[few].sum()
+    q[V // 2:] *= 0.5 / q[V // 2:].sum()
+    eps = 2.0 ** -9
+    p = q.copy()
+    p[few] *= 1 - 2 * eps
+    p[V // 2:] *= 1 + 2 * eps * rng.uniform(0.6, 1.4, V - V // 2)
+    p, q = p.astype(np.float32), q.astype(np.float32)
+    P, Q = [Fraction(float(x)) for x in p], [Fraction(float(x)) for x in q]
+    c = 1 + sum(max(a - b, 0) for a, b in zip(P, Q))
+    Z = sum(max(a - c * b, 0) for a, b in zip(P, Q))
+    for x in range(V // 2, V):
+        u = max(P[x] - c * Q[x], 0) / (Q[x] * Z)
+        if Fraction(1, 8) < u < Fraction(15, 16):
+            break
+    else:
+        return None
+    lo = np.float32(float(u))
+    if Fraction(float(lo)) >= u:
+        lo = np.nextafter(lo, np.float32(0))
+    hi = np.nextafter(lo, np.float32(1))
+    # (the kernel's sum is right to 2^-40 of it: borders that near to a number that u can take are left to others)
+    if min(u - Fraction(float(lo)), Fraction(float(hi)) - u) < u / 2 ** 38:
+        return None
+    return p, q, [0, 0, 1, x], lo, hi
+
+
+@pytest.mark.parametrize("V", [8, 62])
+def test_small_residuals_are_summed_as_exact_arithmetic_does(V):
+    """u just below and at the border of a test against a sum of p - c q that is a thousandth of p and q: products that were
+    rounded once in one place and not in another would be 2^-15 off, u is told apart by 2^-24."""
+    cases = [c for c in (_border(seed, V) for seed in range(60)) if c is not None]
+    assert len(cases) >= 20
+    B = 2 * len(cases)
+    b = Batch([4] * B, V, make=lambda rng, rows, V: (np.zeros((rows, V), dtype=np.float32), np.ones((rows, V), dtype=np.float32)))
+    for s in range(B):
+        p, q, tokens, lo, hi = cases[s // 2]
+        rows = slice(4 * s, 4 * s + 4)
+        b.par[s], b.p[rows], b.q[rows], b.tok[rows] = [-1, 0, 0, 0], p, q, tokens
+        b.u[rows] = [0, 1 - 2.0 ** -24, 1 - 2.0 ** -24, hi if s % 2 else lo]
+    path, count, nxt = b.run(False, False)
+    assert b.ctx.status() == 0
+    for s in range(B):
+        want, _ = D.verify(list(b.tok[4 * s:4 * s + 4]), b.par[s], b.p[4 * s:4 * s + 4], b.q[4 * s:4 * s + 4], b.u[4 * s:4 * s + 4],
+                           b.un[s], False, Fraction)
+        assert want == ([0] if s % 2 else [0, 3])
+        assert path[s][:count[s]] == want, s
 
 
 @pytest.mark.parametrize("V", [7, 40, 2047, 9000, 32001, 128256])

@@ -66,11 +66,12 @@ struct Order {                         // what the walk asks of every CTA
   double c;
 };
 
-// max(p - c q, 0) as a pair of floats; entries that are NaN or negative count as zero
+// max(p - c q, 0) as a pair of floats; entries that are NaN or negative count as zero. The product and the differences are
+// rounded each by itself: a multiply-add in the place of one would leave e out or in twice, up to 2^-24 of c q.
 __device__ __forceinline__ void residual(float p, float q, float ch, float cl, float& hi, float& lo) {
   q = fmaxf(q, 0.f);
-  const float h = ch * q, e = fmaf(ch, q, -h);      // c_hi q exactly
-  const float s = p - h, t = (p - s) - h;           // p - h exactly, where it is not negative (so p is the larger)
+  const float h = __fmul_rn(ch, q), e = fmaf(ch, q, -h);             // c_hi q exactly
+  const float s = __fsub_rn(p, h), t = __fsub_rn(__fsub_rn(p, s), h);   // p - h exactly, where it is not negative (so p is the larger)
   const float l = fmaf(-cl, q, t - e);
   const bool some = s + l > 0.f;
   hi = some ? s : 0.f;
