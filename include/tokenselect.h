@@ -115,7 +115,7 @@ typedef struct {
 
 /* Context: validates and records cfg, allocates the device scratch for
  * max_batch sequences of max_pages_per_seq * page_size tokens on the current
- * device. Returns TS_ERR_UNSUPPORTED for a head geometry with no kernel. */
+ * device (that of ts_tree_attend is allocated by its first call). Returns TS_ERR_UNSUPPORTED for a head geometry with no kernel. */
 ts_status ts_create(ts_ctx** out, const ts_config* cfg);
 ts_status ts_destroy(ts_ctx* ctx);
 
@@ -379,7 +379,9 @@ ts_status ts_append_rotated(ts_ctx* ctx, const ts_rope* rope, const void* k, int
  * query heads per KV head, else TS_ERR_UNSUPPORTED. Scores, sums and outputs accumulate in fp32; softmax weights are
  * rounded to bf16 for their product with v, outputs once at the end. A row's result depends on no draft that it does
  * not see and on nothing behind its sequence, whatever those hold (NaN and infinities too); rows of out and lse from
- * cu_rows[B] on are left as they are. Repeated calls give the same bits. */
+ * cu_rows[B] on are left as they are. Repeated calls give the same bits. A context's first call allocates its scratch
+ * (512 (d + 2) fp32 for each SM: 40 MB at d 128; TS_ERR_CUDA, with nothing enqueued, where there is no room), also
+ * one with total 0 and one whose stream is being captured; later calls allocate nothing. */
 ts_status ts_tree_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
                          const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_rows, const int32_t* mask,
                          int mask_words, int B, int total, float scale, void* out, int64_t out_stride, float* lse,

@@ -59,6 +59,25 @@ void free_ctx_buffers(ts_ctx* c) {
   cudaFree(c->phase_ns);
 }
 
+// Room for the parts of the tree attention (40 MB at d 128), made by a context's first call: most contexts see no drafts.
+// The allocation is no part of a graph that the call is captured into.
+ts_status tree_room(ts_ctx* c) {
+  if (c->tree_part_ml) return TS_OK;
+  const size_t slots = (size_t)tree_part_slots(c->num_sms);
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return cuda_status(e);
+  e = alloc(&c->tree_part_o, slots * 256 * (size_t)c->cfg.head_dim);
+  if (e == cudaSuccess) e = alloc(&c->tree_part_ml, slots * 256);
+  if (e != cudaSuccess) {
+    cudaFree(c->tree_part_o);
+    c->tree_part_o = nullptr;
+    cudaGetLastError();   // (the next launch asks for it)
+  }
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return cuda_status(e);
+}
+
 float resolve_scale(const ts_ctx* ctx, float scale) {
   return scale == 0.f ? 1.f / std::sqrt((float)ctx->cfg.head_dim) : scale;
 }
@@ -205,11 +224,6 @@ ts_status ts_create(ts_ctx** out, const ts_config* cfg) {
     const size_t slots = (size_t)q4_part_slots(c, ctx->num_sms);
     chk(alloc(&ctx->q4_part_o, slots * H * D));
     chk(alloc(&ctx->q4_part_ml, slots * H));
-  }
-  if (tree_supported(c)) {
-    const size_t slots = (size_t)tree_part_slots(ctx->num_sms);
-    chk(alloc(&ctx->tree_part_o, slots * 256 * D));
-    chk(alloc(&ctx->tree_part_ml, slots * 256));
   }
   chk(alloc(&ctx->gsync, 4));
   if (e == cudaSuccess) chk(cudaMemset(ctx->gsync, 0, 4 * sizeof(unsigned)));   // then kept zero by each launch
@@ -707,6 +721,7 @@ ts_status ts_tree_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const voi
   if (q_stride % 8 != 0 || out_stride % 8 != 0 || !aligned16({q, k_pool, v_pool, out})) return TS_ERR_INVALID_ARG;
   if (std::isnan(scale)) return TS_ERR_INVALID_ARG;
   if (!tree_supported(c)) return TS_ERR_UNSUPPORTED;
+  if (const ts_status st = tree_room(ctx); st != TS_OK) return st;
   TreeCall a{q, q_stride, k_pool, v_pool, page_table, seq_lens, cu_rows, mask, mask_words, B, total,
              resolve_scale(ctx, scale), out, out_stride, lse};
   return launch_tree_attend(ctx, a, as_stream(stream));

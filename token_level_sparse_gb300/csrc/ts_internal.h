@@ -72,7 +72,7 @@ struct ts_ctx {
   int32_t* sel_rows = nullptr;           // persistent kernel: per CTA, its selected tokens [kStepFlagCap]
   float* q4_part_o = nullptr;            // 4-bit pools: attention parts [slots][H][d], q4_part_slots
   float2* q4_part_ml = nullptr;          // ... and their (max, sum), also the score's [H][slots]
-  float* tree_part_o = nullptr;          // tree attention: parts [2 num_sms][d / 4][256 rows][4]
+  float* tree_part_o = nullptr;          // tree attention (from its first call on): parts [2 num_sms][d / 4][256 rows][4]
   float2* tree_part_ml = nullptr;        // ... and their (max, sum) [2 num_sms][256]
   int64_t kernels = 0;           // kernel launches issued
   // persistent decode-step kernel
