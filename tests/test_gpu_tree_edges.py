@@ -1,8 +1,10 @@
-"""ts_tree_attend on the GPU: places that hold no number in parts of their own."""
+"""ts_tree_attend on the GPU: places that hold no number in parts of their own, rows by themselves and among others, long
+sequences, and waits that run out."""
 import pytest
 import torch
 
-from test_gpu_tree import Case
+from parity import tsl
+from test_gpu_tree import BF, DEV, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +56,52 @@ def test_a_value_that_is_not_finite_reaches_the_rows_that_see_it_whatever_its_we
         for i in range(4):
             want[i, 8:12, 11] = not hidden or i % 2 == 1
         assert torch.equal(bad, want) and bool(torch.isfinite(c.lse).all()) and c.ctx.status() == 0
+
+
+def _alone(c, b, drafts):
+    """The first drafts of sequence b by themselves: outputs and sums."""
+    T, r0 = tsl(), int(c.cu[b])
+    ctx = T.Context(c.H, c.HKV, c.d, T.TS_KV_BF16, 1, c.table.shape[1], c.pages, c.page)
+    rows = slice(r0, r0 + drafts)
+    out, lse = torch.full((drafts, c.H, c.d), 7.0, dtype=BF, device=DEV), torch.full((drafts, c.H), 7.0, device=DEV)
+    n = c.lens[b] - c.trees[b] + drafts
+    ctx.tree_attend(c.q[rows], c.k_pool, c.v_pool, c.dev(c.table[b:b + 1]), c.dev([n]), c.dev([0, drafts]),
+                    c.mask_tensor()[rows].contiguous(), out, lse)
+    assert ctx.status() == 0
+    return out, lse
+
+
+def test_a_tree_alone_and_without_its_last_rows():
+    """The same bits alone and among others, and for a tree's first drafts without its last, where every block has one key
+    tile (the shares of the key tiles fall alike)."""
+    c = Case(8, 4, 128, lens=[100, 90, 80, 128], trees=[30, 17, 64, 90], seed=23)
+    c.run()
+    for b, t in enumerate(c.trees):
+        for drafts in (t, t - 1, t // 2, 1):
+            out, lse = _alone(c, b, drafts)
+            rows = slice(int(c.cu[b]), int(c.cu[b]) + drafts)
+            assert torch.equal(out, c.out[rows]) and torch.equal(lse, c.lse[rows]), (b, drafts)
+
+
+@pytest.mark.parametrize("HKV,G,d,t,page", [(8, 4, 128, 64, 16), (4, 2, 64, 20, 16), (2, 8, 128, 9, 1)])
+def test_long_sequences(HKV, G, d, t, page):
+    """131,057 tokens: key tiles of a KV head over a dozen CTAs and more."""
+    c = Case(HKV, G, d, lens=[131057], trees=[t], page=page, seed=24)
+    c.run().check(rows=[0, t // 2, t - 1], heads=[0, HKV * G - 1])
+
+
+def test_waits_that_run_out_are_reported():
+    """A limit that the first products cannot keep: the status says so, what follows is right."""
+    T = tsl()
+    c = Case(8, 4, 128, lens=[131057, 300, 64], trees=[20, 33, 5], seed=25)
+    c.run()
+    assert c.ctx.status() == 0
+    want, wl = c.out.clone(), c.lse.clone()
+    for _ in range(3):
+        T.ts_set_wait_limit(c.ctx.handle, 1)
+        c.run()
+        assert c.ctx.status() == T.STATUS_CODE["TS_ERR_TIMEOUT"]
+        T.ts_set_wait_limit(c.ctx.handle, 1000000000)
+        c.out.fill_(0)
+        c.run()
+        assert c.ctx.status() == 0 and torch.equal(c.out, want) and torch.equal(c.lse, wl)
