@@ -326,8 +326,9 @@ ts_status ts_read_kv(ts_ctx* ctx, const int32_t* cu_rows, const int32_t* starts,
  *          that turns x times within n positions, i_high rounded down and at least 0, i_low rounded up and at most
  *          rot_dim - 1 (their difference at least 0.001); a = 0.1 ln(factor) + 1 for a factor above 1;
  *  GIVEN   freqs[rot_dim/2] (host memory, read by ts_rope_create).
- * a = attention where that is not 0, else 1 unless the rule names one. Angles are exact modulo a turn to 2^-32 of
- * it plus what `position` makes of the last bit of f_i / 2pi in fp64, for every int32 position, negative ones too. */
+ * a = attention where that is not 0, else 1 unless the rule names one. Angles, modulo a turn, are exact to 2^-32 of
+ * it plus what `position` makes of the last bit of f_i / 2pi in fp64, for every int32 position, negative ones too; then they
+ * are rounded to fp32, by up to 2^-26 of a turn (9.4e-8 radians, for those near half a turn). */
 enum { TS_ROPE_PLAIN = 0, TS_ROPE_LINEAR = 1, TS_ROPE_BASE = 2, TS_ROPE_BANDS = 3, TS_ROPE_YARN = 4, TS_ROPE_GIVEN = 5 };
 typedef struct {
   int rot_dim;            /* even, 2 to 128, at most the context's head_dim      */
@@ -378,7 +379,9 @@ ts_status ts_append_rotated(ts_ctx* ctx, const ts_rope* rope, const void* k, int
  * page outside the pool are left out and TS_ERR_PAGE_OOB is recorded. bf16 pools with d 64 or 128 and at most 16
  * query heads per KV head, else TS_ERR_UNSUPPORTED. Scores, sums and outputs accumulate in fp32; softmax weights are
  * rounded to bf16 for their product with v, outputs once at the end. A row's result depends on no draft that it does
- * not see and on nothing behind its sequence, whatever those hold (NaN and infinities too); rows of out and lse from
+ * not see and on nothing behind its sequence, whatever those hold (NaN and infinities too). A NaN score that a row sees makes
+ * its outputs and lse NaN, a value that it sees and that is not finite makes that element not finite, however little it
+ * weighs; rows of out and lse from
  * cu_rows[B] on are left as they are. Repeated calls give the same bits. A context's first call allocates its scratch
  * (512 (d + 2) fp32 for each SM: 40 MB at d 128; TS_ERR_CUDA, with nothing enqueued, where there is no room), also
  * one with total 0 and one whose stream is being captured; later calls allocate nothing. */
@@ -399,8 +402,12 @@ ts_status ts_tree_attend(ts_ctx* ctx, const void* q, int64_t q_stride, const voi
  * from q). draft NULL: x is taken iff u Z < p(x), otherwise Z -= p(x) and p(x) = 0. A child that is taken becomes the
  * current node; with none left next_token[b] is drawn from the residual r = max(p - c q, 0): the smallest i with
  * sum_{j <= i} r(j) > u_next[b] sum r (the last i with r(i) > 0 where rounding leaves none), from p where r is zero
- * throughout, -1 where p is too. Tokens so drawn are distributed as the target's. Entries that are NaN or negative
- * count as 0. Sums are off by less than 2^-32 of them.
+ * throughout, -1 where p is too. Entries that are NaN or negative
+ * count as 0. Sums are off by less than 2^-32 of them and 2^-45 of the sums of p and c q.
+ * Tokens so drawn are distributed as the target's, where the rows of target and draft add up to 1: Z and W start at 1, not
+ * at the rows' sums, and what a row misses of 1 (an fp32 softmax: about 1e-6) is carried along undivided. With
+ * `distinct` it is off W, the mass that the elder siblings leave of q, so it shows where they leave little (a tenth of
+ * W = 1e-5): a row whose first tokens hold nearly all of its mass wants few children, or rows that add up better.
  * path int32 [B][path_stride] receives the taken nodes in order, node 0 first, then -1; count int32 [B] how many.
  * More than path_stride record TS_ERR_CAPACITY (the first ones are written, count is the whole number). At most 1024
  * nodes per sequence; more, or boundaries that are not ascending, record TS_ERR_SEQ_LEN, count 0 and -1 (so does a

@@ -7,7 +7,8 @@
 //
 // Angles: f_i / 2pi is held as a 64-bit fraction of a turn, and pos times it, modulo 2^64, is the angle modulo a turn,
 // exactly: far positions cost nothing and lose nothing (fp32 products of a position near 10^6 are off by up to 0.03
-// radians), and negative positions turn back. The top 32 bits go to sincospif; the fraction cut off is 2^-32 of a turn.
+// radians), and negative positions turn back. The top 32 bits (2^-32 of a turn is
+// cut off) go to sincospif as one fp32 number, whose rounding is what is left: up to 2^-26 of a turn, near half a turn.
 //
 // Every byte is read and written once, so this is bound by memory. A thread holds 8 elements of a head (16 bytes of
 // bf16), the same 8 of one row for all the heads that it goes through, so that their cosines and sines stay in

@@ -31,8 +31,10 @@
 //
 // Measured, 32 heads over 8 of 128: up to 32 drafts over 262,144 tokens 168 us, 6.4 TB/s (memory); 64 drafts 211 us, 1.3
 // PFLOP/s (a key tile's chain of scores, softmax, outputs, 3200 cycles, of which the tensor cores work 2050); 64 over 131,057
-// 121 us, of which the join is 12. Key tiles of 64 tokens with two score buffers to a query tile let those overlap better, but each
-// change from one kind of product to the other costs the tensor cores about 150 cycles, and twice as many cost more (128).
+// 121 us, of which the join is 12. One-token pages: 826 us, as each of a tile's 256 copies moves 128 bytes (822 with one draft); d 64,
+// 8 heads over 4, 262,144 tokens: 76 us with 64 drafts, 101 with 128. Key tiles of 64 tokens with two score buffers to a query
+// tile let those overlap better, but each change from one kind of product to the other costs the tensor cores about 150 cycles,
+// and twice as many cost more (128).
 #include <cmath>
 
 #include "ts_flash.cuh"
@@ -93,9 +95,11 @@ struct TrShape {
   static constexpr uint32_t S_COL = 0, O_COL = 256;
 };
 
-// Work is counted per key tile: one of a block with two tiles takes longer, 262,144 tokens of 8 KV heads with G 4 202 to 215 us
-// (33 to 64 drafts) where a block with one tile takes 168 (up to 32); more in one batch, where those wait less for memory. A block of
-// its own costs about three key tiles: its queries, first softmax and outputs.
+// Work is counted per key tile: one of a block with two tiles takes longer, 262,144 tokens of 8 KV heads with G 4 201 to 211 us
+// (33 to 64 drafts) where a block with one tile takes 168 (up to 32); more in one batch, where those wait less for memory. A block
+// (its queries, first softmax and outputs) counts as four units beside its tiles, what two key tiles of a block with one
+// tile count or one and a third of a block with two. Set by timings of 16-token pages with d 128 and G 4 and 7; the same for
+// the others, where only how even the shares are hangs on it.
 constexpr int kTrPair = 3, kTrSingle = 2, kTrBlock = 4;
 
 // A sequence's work: its KV heads one behind another, of each the blocks, of each the key tiles.

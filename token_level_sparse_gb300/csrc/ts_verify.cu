@@ -17,11 +17,12 @@
 // barrier on either side). Nobody else decides anything, so all of them always agree on the next barrier.
 //
 // Sums decide whole numbers, so they are held in pairs of floats (p - c q exactly, c in two floats), warps and CTAs in fp64,
-// all in a fixed order: off by 2^-44 of the sum as a rule, by n^2 2^-49 < 2^-33 at most, n <= 256 elements to a lane. FP64
-// throughout would be the slower pipe by far (sixteen warps that scanned 128 sums in fp64 took 8 us). Entries that are NaN or negative count as zero.
+// all in a fixed order: off by 2^-44 of the sum as a rule, by n^2 2^-49 < 2^-33 at most, n <= 256 elements to a lane, and by 2^-45
+// of the sums of p and c q, which may nearly cancel. FP64 throughout would be the slower pipe by far (sixteen warps that
+// scanned 128 sums in fp64 took 8 us). Entries that are NaN or negative count as zero.
 //
 // Measured: a chain of 6 over 32,001 tokens 13 us (1 for the nodes, 2 for the walk, 1.7 for a sweep, 2 to find the part and 2 the
-// token, cluster barriers of 0.5); 32 trees of up to 64 nodes over 128,256 tokens 57 us, as long as the one with most
+// token, cluster barriers of 0.5); 32 trees of up to 64 nodes over 128,256 tokens 53 us, as long as the one with most
 // refusals takes, 6 us for each sweep of its rows.
 #include <cooperative_groups.h>
 #include <math_constants.h>
